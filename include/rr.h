@@ -527,6 +527,181 @@ rr_status_t rr_workspace_preset(uint64_t value, rr_stream_t stream);
    RR_ERR_INVALID, RR_ERR_HIP. */
 rr_status_t rr_hbm_copy(void *dst, const void *src, size_t bytes, rr_stream_t stream);
 
+/* ------------------------------- a block's operators between two collectives */
+
+/* What a rank of a model computes between two collectives: the tokens sorted to
+   experts for the AlltoAll and summed back after it, the norms around a block,
+   and a block's matrix products.  All of them enqueue work on `stream`, allocate
+   nothing, keep nothing from one call to the next and may be captured into a
+   graph from the first call on; a call that needs scratch memory takes it from
+   the caller (the *_workspace queries say how much, and any contents will do).
+   No entry of a tensor is read or written outside the sizes given, whatever
+   index tensors (slots, sources, offsets) hold.  No atomics on results: the same
+   inputs give the same bits.  Element types RR_FP32, RR_BF16 and RR_FP16; sums
+   and statistics are held in 32 bits and rounded once, when stored.  Outputs may
+   not overlap inputs or each other, unless said otherwise.  Errors:
+   RR_ERR_INVALID (a size, pointer, alignment, type or option that is not as
+   described; nothing is enqueued), RR_ERR_UNSUPPORTED (a size beyond a stated
+   limit), RR_ERR_HIP. */
+
+/* Rows of a matrix: row t starts at element t * ld of `data`, ld >= the row's
+   length.  `data` aligned to its element, any ld.  data == NULL: absent. */
+typedef struct {
+    void *data;
+    size_t ld;
+} rr_rows_t;
+
+typedef enum {
+    RR_ACT_NONE = 0,
+    RR_ACT_RELU = 1,
+    RR_ACT_GELU = 2,    /* z/2 (1 + erf(z / sqrt 2)) */
+    RR_ACT_SILU = 3,    /* z / (1 + exp(-z)) */
+    RR_ACT_SIGMOID = 4  /* gates only */
+} rr_act_t;
+
+/* --- tokens sorted by expert, and back --- */
+
+#define RR_MAX_EXPERTS 1024
+
+/* Orders the pairs (token t, choice j) by the expert ids[t * id_ld + j] names.
+   Pair p = t * k + j; a pair whose id is outside [0, experts) is masked out.
+   counts[e] is the number of pairs of expert e.  A pair's rank is the number of
+   lower-numbered pairs of its expert (the order is stable).
+     capacity == 0 (packed): rows = tokens * k; pair p has slot offsets[e] + rank,
+       offsets[e] = counts[0] + ... + counts[e - 1]; offsets[experts] rows are used.
+     capacity > 0: rows = experts * capacity, offsets[e] = e * capacity; slot
+       e * capacity + rank, or none if rank >= capacity (dropped).  Equal blocks,
+       as alltoall wants them.
+   slots[p] is the pair's slot or -1; sources[row] the pair in that row or -1.
+   ids are int32 or int64 (id_bytes 4 or 8); slots: tokens * k, sources: rows,
+   counts: experts, offsets: experts + 1 int32 words.  Limits: experts <=
+   RR_MAX_EXPERTS, tokens * k and rows < 2^31. */
+rr_status_t expert_sort(const void *ids, int id_bytes, size_t id_ld, size_t tokens, int k,
+                        int experts, size_t capacity, int32_t *slots, int32_t *sources,
+                        int32_t *counts, int32_t *offsets, void *workspace,
+                        size_t workspace_bytes, rr_stream_t stream);
+rr_status_t expert_sort_workspace(size_t tokens, int k, int experts, size_t *bytes);
+
+/* rows[slots[t * k + j]] = x[t] bit for bit; rows whose source is -1 (or not a
+   pair) become zero.  `slots` and `sources` as expert_sort gives them for `rows`
+   rows: a row is written by its pair or, without one, with zeros. */
+rr_status_t expert_dispatch(rr_rows_t x, size_t tokens, size_t hidden, int k, rr_dtype_t dt,
+                            const int32_t *slots, const int32_t *sources, size_t rows,
+                            rr_rows_t out, rr_stream_t stream);
+
+/* out[t] = sum over j of weights[t * k + j] * rows[slots[t * k + j]], in the order
+   of j; pairs without a slot are left out (a token without any gets zeros).
+   weights are fp32; NULL: all 1, which is the gradient of expert_dispatch. */
+rr_status_t expert_combine(rr_rows_t in, size_t rows, size_t hidden, rr_dtype_t dt,
+                           const int32_t *slots, const float *weights, size_t tokens, int k,
+                           rr_rows_t out, rr_stream_t stream);
+
+/* Gradients of expert_combine: drows[slots[p]] = weights[p] * dout[t] (zeros in rows
+   whose source is -1) and dweights[p] = <dout[t], rows[slots[p]]> in fp32 (0
+   without a slot).  weights NULL: all 1; drows.data NULL: not wanted;
+   dweights NULL: not wanted (`in` is then not read and may be absent). */
+rr_status_t expert_combine_backward(rr_rows_t dout, rr_rows_t in, size_t rows, size_t hidden,
+                                    rr_dtype_t dt, const int32_t *slots, const int32_t *sources,
+                                    const float *weights, size_t tokens, int k, rr_rows_t drows,
+                                    float *dweights, rr_stream_t stream);
+
+/* --- the norms around a block --- */
+
+typedef enum { RR_GATE_NONE = 0, RR_GATE_CHANNEL = 1, RR_GATE_ELEMENT = 2 } rr_gate_t;
+
+/* N(v) = v / sqrt(mean(v^2) + eps), over the row's `hidden` elements.
+     n = post_norm ? N(branch) * post_weight : branch
+     h = residual_scale * x + branch_scale * gate_act(gate) * n
+     y = N(h) * pre_weight                                    (pre_norm)
+   `branch` is a block's output, h the stream after it and y the next block's
+   input.  Without a branch h = residual_scale * x.  y is computed from h before
+   h is rounded to its type.  Weights NULL: all 1.  hidden <= 32768. */
+typedef struct {
+    size_t tokens, hidden;
+    int32_t dt;         /* rr_dtype_t of the rows */
+    int32_t weight_dt;  /* of the weights and the channel gate: dt or RR_FP32 */
+    int32_t post_norm, pre_norm;  /* 0 or 1 */
+    int32_t gate_kind;  /* rr_gate_t: none, `hidden` values, or rows like the branch */
+    int32_t gate_act;   /* RR_ACT_NONE, RR_ACT_SIGMOID or RR_ACT_SILU */
+    float residual_scale, branch_scale, eps;
+    int32_t reserved;   /* 0 */
+    rr_rows_t x;        /* not read by the backward call */
+    rr_rows_t branch;   /* absent: the first norm of a model */
+    rr_rows_t gate;     /* RR_GATE_CHANNEL: one row, ld not read */
+    const void *post_weight, *pre_weight;
+    rr_rows_t h;        /* out (absent: not stored); the backward call reads it if
+                           pre_norm */
+    rr_rows_t y;        /* out, if pre_norm; not used by the backward call */
+} rr_norm_t;
+
+/* dh and dy in (dh absent: zero; dy present exactly if pre_norm), the rest out, each
+   absent or NULL if not wanted: dx, dbranch, and dgate for RR_GATE_ELEMENT in dt;
+   dgate_channel, dpost_weight, dpre_weight in fp32, `hidden` values each. */
+typedef struct {
+    rr_rows_t dh, dy;
+    rr_rows_t dx, dbranch, dgate;
+    float *dgate_channel, *dpost_weight, *dpre_weight;
+} rr_norm_grad_t;
+
+/* h may be x itself, and y may be the branch (in place). */
+rr_status_t block_norm(const rr_norm_t *a, rr_stream_t stream);
+/* All gradients at (h, branch, gate) as given: h is the stored stream, which is what the
+   next block read.  dx may be dh and dbranch may be dy (in place). */
+rr_status_t block_norm_backward(const rr_norm_t *a, const rr_norm_grad_t *g, void *workspace,
+                                size_t workspace_bytes, rr_stream_t stream);
+rr_status_t block_norm_backward_workspace(const rr_norm_t *a, const rr_norm_grad_t *g,
+                                          size_t *bytes);
+
+/* --- a block's matrix products --- */
+
+/* z = x w_e^T + bias_e, out = act(z) + residual for the rows of each group e: w_e
+   is n x k at w + e * w_stride, row i at element i * w_ld; bias_e at bias + e * n.
+   Rows of group e: offsets[e] <= row < offsets[e + 1] (device memory, groups + 1
+   words, not descending, as expert_sort gives them); rows before offsets[0] or
+   from offsets[groups] on belong to no group and become zero in out and z.
+   offsets NULL: groups of rows / groups rows each.  Types RR_BF16 and RR_FP16; act
+   and residual work on the 32-bit z, before it is rounded.  Limits: rows, n, k <
+   2^31, ld and w_ld <= 2^22, groups <= RR_MAX_EXPERTS. */
+typedef struct {
+    size_t rows, n, k;
+    int32_t groups;
+    int32_t dt;
+    int32_t act;        /* RR_ACT_NONE, RR_ACT_RELU, RR_ACT_GELU, RR_ACT_SILU */
+    int32_t reserved;   /* 0 */
+    const int32_t *offsets;
+    rr_rows_t x;
+    const void *w;
+    size_t w_ld, w_stride;
+    const void *bias;   /* groups * n, or NULL */
+    rr_rows_t residual; /* or absent */
+    rr_rows_t z;        /* out (or absent); read by the backward call if act is set */
+    rr_rows_t out;      /* not used by the backward call */
+} rr_linear_t;
+
+/* dz = dout * act'(z); dx = dz w_e (rows of no group: zero), dw_e = dz_e^T x_e, db_e =
+   sum of dz's rows in e.  dz is rounded to dt between the passes when act is set,
+   as an operand of the matrix instructions has to be; db is summed from the
+   unrounded dz.  dw: groups x n x k, contiguous, in dt or fp32 (dw_dt); db: fp32,
+   groups * n.  The gradient by the residual is dout itself.  Each output NULL or
+   absent if not wanted. */
+typedef struct {
+    rr_rows_t dout;
+    rr_rows_t dx;
+    void *dw;
+    float *db;
+    int32_t dw_dt;
+    int32_t reserved;   /* 0 */
+} rr_linear_grad_t;
+
+/* residual may be out itself (in place). */
+rr_status_t block_linear(const rr_linear_t *a, void *workspace, size_t workspace_bytes,
+                         rr_stream_t stream);
+rr_status_t block_linear_workspace(const rr_linear_t *a, size_t *bytes);
+rr_status_t block_linear_backward(const rr_linear_t *a, const rr_linear_grad_t *g,
+                                  void *workspace, size_t workspace_bytes, rr_stream_t stream);
+rr_status_t block_linear_backward_workspace(const rr_linear_t *a, const rr_linear_grad_t *g,
+                                            size_t *bytes);
+
 /* Human-readable name of a status. */
 const char *rr_status_string(rr_status_t s);
 

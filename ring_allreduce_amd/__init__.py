@@ -17,6 +17,12 @@ from dataclasses import dataclass
 
 import torch  # noqa: F401  (loads the HIP runtime librr.so must share)
 
+from . import block
+from .block import (ExpertOrder, LinearGrads, NormGrads, block_linear,  # noqa: F401
+                    block_linear_backward, block_norm, block_norm_backward, expert_combine,
+                    expert_combine_backward, expert_dispatch, expert_dispatch_backward,
+                    expert_sort)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librr.so")
 
@@ -145,6 +151,8 @@ _status_string = _sig("rr_status_string", ctypes.c_char_p, _i)
 _abi_version = _sig("rr_abi_version", _i)
 _finalize = _sig("rr_finalize", None)
 
+block._bind(_sig)
+
 # Every symbol include/rr.h declares, for the export check.
 EXPORTED = ["allreduce_ring", "reduce_scatter_ring", "all_gather_ring", "allreduce_ring_ex",
             "reduce_scatter_ring_ex", "all_gather_ring_ex", "allreduce_ring_staged",
@@ -154,7 +162,7 @@ EXPORTED = ["allreduce_ring", "reduce_scatter_ring", "all_gather_ring", "allredu
             "counting_barrier_preset", "counting_barrier_read", "counting_barrier_read_peer",
             "counting_barrier_early_passes", "counting_barrier_run", "counting_barrier_run_timed",
             "rr_last_kernel_error", "rr_init", "rr_workspace_preset", "rr_hbm_copy",
-            "rr_status_string", "rr_abi_version", "rr_finalize"]
+            "rr_status_string", "rr_abi_version", "rr_finalize"] + block.EXPORTED
 
 
 class RRError(RuntimeError):

@@ -10,14 +10,17 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
+BLOCK = os.path.join(HERE, "csrc_block")  # a block's operators between two collectives
 LIB = os.path.join(HERE, "librr.so")
 # one translation unit per kernel family (the in-place ring: one per element
 # type), and the host side with the C ABI
 SOURCES = [os.path.join(CSRC, f) for f in
            ("rr_ring_i32.hip", "rr_ring_f32.hip", "rr_ring_bf16.hip", "rr_ring_f16.hip",
             "rr_staged_kernel.hip", "rr_aux_kernels.hip", "rr_api.hip")]
+SOURCES += [os.path.join(BLOCK, f) for f in ("blk_expert.hip", "blk_norm.hip", "blk_linear.hip")]
 HEADERS = [os.path.join(CSRC, "rr_device.hpp"), os.path.join(CSRC, "rr_kernels.hpp"),
-           os.path.join(CSRC, "rr_ring_kernel.hpp"), os.path.join(ROOT, "include", "rr.h")]
+           os.path.join(CSRC, "rr_ring_kernel.hpp"), os.path.join(BLOCK, "blk_common.hpp"),
+           os.path.join(ROOT, "include", "rr.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -54,7 +57,7 @@ def build(force: bool = True, verbose: bool = False) -> str:
     newest = max(os.path.getmtime(p) for p in SOURCES + HEADERS)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
         return LIB
-    include = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
+    include = ["-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", BLOCK]
     with tempfile.TemporaryDirectory(prefix="rr_build_") as tmpdir:
         objects = [os.path.join(tmpdir, os.path.basename(src) + ".o") for src in SOURCES]
 

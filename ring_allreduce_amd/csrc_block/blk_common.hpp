@@ -1,0 +1,125 @@
+// blk_common.hpp -- what the kernels of a block's operators share: element types,
+// 16-byte row accesses of any alignment, activations, sums over a workgroup, and
+// the host side's argument checks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "rr.h"
+
+namespace blk {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16;
+typedef _Float16 f16;
+
+// ------------------------------------------------------------------ vectors --
+// A Vec<T> is 16 bytes of a row: 4 fp32 or 8 bf16 / fp16 elements.  Rows may start
+// at any element (odd lengths, views of wider tensors): the 16-byte access is
+// declared with the element's alignment only, which gfx950 serves in one
+// instruction; the last, partial vector of a row goes element by element.
+template <typename T> struct Vec {
+    static constexpr int N = 16 / (int)sizeof(T);
+    T e[N];
+};
+
+template <typename T> struct __attribute__((packed, aligned(sizeof(T)))) Loose {
+    u32x4 v;
+};
+
+template <typename T>
+__device__ __forceinline__ Vec<T> load_vec(const T* row, int at, int len) {
+    Vec<T> r;
+    if (at + Vec<T>::N <= len) {
+        r = __builtin_bit_cast(Vec<T>, reinterpret_cast<const Loose<T>*>(row + at)->v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Vec<T>::N; ++i) r.e[i] = at + i < len ? row[at + i] : (T)0.0f;
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_vec(T* row, int at, int len, const Vec<T>& r) {
+    if (at + Vec<T>::N <= len) {
+        reinterpret_cast<Loose<T>*>(row + at)->v = __builtin_bit_cast(u32x4, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Vec<T>::N; ++i)
+            if (at + i < len) row[at + i] = r.e[i];
+    }
+}
+
+// -------------------------------------------------------------- activations --
+// In 32 bits.  exp(-z) overflows to infinity for z below -88, where the logistic
+// function is 0 to 32 bits: 1 / (1 + inf) = 0, and z * 0 is the right limit for
+// every finite z.
+__device__ __forceinline__ float logistic(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+__device__ __forceinline__ float act_value(int act, float z) {
+    switch (act) {
+        case RR_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
+        case RR_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        case RR_ACT_SILU: return z * logistic(z);
+        case RR_ACT_SIGMOID: return logistic(z);
+        default: return z;
+    }
+}
+
+// d act / d z; 0 at the corner of relu.
+__device__ __forceinline__ float act_slope(int act, float z) {
+    switch (act) {
+        case RR_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+        case RR_ACT_GELU:
+            return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
+                   z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+        case RR_ACT_SILU: {
+            const float q = logistic(z);
+            return q * (1.0f + z * (1.0f - q));
+        }
+        case RR_ACT_SIGMOID: {
+            const float q = logistic(z);
+            return q * (1.0f - q);
+        }
+        default: return 1.0f;
+    }
+}
+
+// --------------------------------------------------------------------- sums --
+// Sum over WIDTH neighbouring lanes (a power of two up to 64), to all of them.
+template <int WIDTH> __device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+    for (int d = WIDTH / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+// ----------------------------------------------------------------- the host --
+inline uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+inline bool is_float_type(int dt) { return dt == RR_FP32 || dt == RR_BF16 || dt == RR_FP16; }
+inline uint64_t type_bytes(int dt) { return dt == RR_BF16 || dt == RR_FP16 ? 2 : 4; }
+inline bool aligned_to(const void* p, uint64_t n) { return (uintptr_t)p % n == 0; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+    if (!a || !b || !na || !nb) return false;
+    return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
+
+// Bytes that `rows` rows of `width` elements, `ld` elements apart, reach over.
+inline uint64_t extent(uint64_t rows, uint64_t ld, uint64_t width, uint64_t bytes) {
+    return rows ? ((rows - 1) * ld + width) * bytes : 0;
+}
+
+inline rr_status_t launched() { return hipGetLastError() == hipSuccess ? RR_OK : RR_ERR_HIP; }
+
+// Compute units of the current device (0: the runtime gave no answer).
+inline int compute_units() {
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 0;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+        return 0;
+    return n;
+}
+
+}  // namespace blk

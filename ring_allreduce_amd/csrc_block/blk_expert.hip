@@ -1,0 +1,670 @@
+// blk_expert.hip -- tokens sorted by expert, moved to their experts' rows and summed
+// back, with the gradients (expert_sort, expert_dispatch, expert_combine and its
+// backward call).
+#include "blk_common.hpp"
+
+namespace blk {
+
+// ------------------------------------------------------------------- sort --
+//
+// A counting sort.  With P pairs cut into pieces of kPiece consecutive pairs, one
+// wave each:  hist[c][e] = pairs of expert e in piece c;  its exclusive sum over c
+// plus the rank within the piece is the pair's rank.  Within 64 pairs a lane finds
+// the lanes of its own key with one ballot per key bit, so ranks need no atomics
+// between waves and the order is stable.  Three launches (count, sum over pieces,
+// place), or one workgroup for everything while P is small.
+
+constexpr int kItems = 8;              // pairs per lane
+constexpr int kPiece = 64 * kItems;    // pairs per wave
+constexpr int kSortWaves = 4;          // waves per workgroup of the three-launch form
+constexpr int kOneWaves = 16;          // waves of the one-workgroup form
+
+struct SortArgs {
+    const void* ids;
+    uint64_t id_ld;
+    int32_t pairs, k, experts, bits;
+    int32_t capacity;
+    int32_t rows, pieces;
+    int32_t* slots;
+    int32_t* sources;
+    int32_t* counts;
+    int32_t* offsets;
+    int32_t* hist;      // [pieces][experts]
+};
+
+template <typename I>
+__device__ __forceinline__ int key_of(const SortArgs& a, int p) {
+    if (p >= a.pairs) return a.experts;
+    uint64_t at = (uint64_t)p;
+    if (a.id_ld != (uint64_t)a.k) {
+        const uint32_t t = (uint32_t)p / (uint32_t)a.k;
+        at = (uint64_t)t * a.id_ld + ((uint32_t)p - t * (uint32_t)a.k);
+    }
+    const I id = ((const I*)a.ids)[at];
+    return id >= 0 && id < (I)a.experts ? (int)id : a.experts;
+}
+
+// The lanes whose key equals this lane's.
+__device__ __forceinline__ uint64_t lanes_of_key(int key, int bits) {
+    uint64_t same = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (key >> b) & 1;
+        const uint64_t ones = __ballot(one);
+        same &= one ? ones : ~ones;
+    }
+    return same;
+}
+
+// Places the wave's kItems x 64 pairs; base[e] is the rank of expert e's next pair.
+__device__ __forceinline__ void place_piece(const SortArgs& a, const int* key, int first,
+                                            int* base, const int* start) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int p = first + i * 64 + lane;
+        const uint64_t same = lanes_of_key(key[i], a.bits);
+        const int leader = __ffsll((unsigned long long)same) - 1;
+        int rank = 0;
+        if (lane == leader && key[i] < a.experts)
+            rank = atomicAdd(&base[key[i]], __popcll(same));
+        rank = __shfl(rank, leader) + __popcll(same & ((1ull << lane) - 1));
+        int slot = -1;
+        if (key[i] < a.experts) {
+            if (a.capacity == 0)
+                slot = start[key[i]] + rank;
+            else if (rank < a.capacity)
+                slot = key[i] * a.capacity + rank;
+        }
+        if (p < a.pairs) {
+            a.slots[p] = slot;
+            if (slot >= 0) a.sources[slot] = p;
+        }
+    }
+}
+
+// start[e] = counts[0] + .. + counts[e - 1] in LDS, by the whole workgroup.
+__device__ __forceinline__ void prefix_counts(const int* counts, int* start, int experts) {
+    if (threadIdx.x < 64) {
+        int before = 0;
+        for (int e0 = 0; e0 < experts; e0 += 64) {
+            const int e = e0 + (int)threadIdx.x;
+            const int n = e < experts ? counts[e] : 0;
+            int sum = n;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int up = __shfl_up(sum, d);
+                if ((int)threadIdx.x >= d) sum += up;
+            }
+            if (e < experts) start[e] = before + sum - n;
+            before += __shfl(sum, 63);
+        }
+        if (threadIdx.x == 0) start[experts] = before;
+    }
+    __syncthreads();
+}
+
+// offsets, and -1 in the rows no pair has.
+__device__ __forceinline__ void fill_unused(const SortArgs& a, const int* counts, const int* start,
+                                            int thread, int threads) {
+    for (int e = thread; e <= a.experts; e += threads)
+        a.offsets[e] = a.capacity ? e * a.capacity : start[e];
+    if (a.capacity == 0) {
+        for (int r = start[a.experts] + thread; r < a.rows; r += threads) a.sources[r] = -1;
+        return;
+    }
+    for (int r = thread; r < a.rows; r += threads) {
+        const int e = (int)((uint32_t)r / (uint32_t)a.capacity);
+        if (r - e * a.capacity >= counts[e]) a.sources[r] = -1;
+    }
+}
+
+template <typename I>
+__global__ void __launch_bounds__(64 * kSortWaves) sort_count_kernel(const SortArgs a) {
+    extern __shared__ int lds[];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int* mine = lds + wave * a.experts;
+    for (int e = lane; e < a.experts; e += 64) mine[e] = 0;
+    __syncthreads();
+    const int piece = blockIdx.x * kSortWaves + wave;
+    int key[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) key[i] = key_of<I>(a, piece * kPiece + i * 64 + lane);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+        if (key[i] < a.experts) atomicAdd(&mine[key[i]], 1);
+    __syncthreads();
+    if (piece < a.pieces)
+        for (int e = lane; e < a.experts; e += 64)
+            a.hist[(uint64_t)piece * a.experts + e] = mine[e];
+}
+
+// Exclusive sum of hist over the pieces: a workgroup takes 16 experts, 64 threads each.
+__global__ void __launch_bounds__(1024) sort_sum_kernel(const SortArgs a) {
+    __shared__ int part[64][17];
+    const int e = blockIdx.x * 16 + (threadIdx.x & 15), s = threadIdx.x >> 4;
+    const int per = (a.pieces + 63) / 64;
+    const int lo = s * per, hi = min(lo + per, a.pieces);
+    int sum = 0;
+    if (e < a.experts)
+        for (int c = lo; c < hi; ++c) sum += a.hist[(uint64_t)c * a.experts + e];
+    part[s][threadIdx.x & 15] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int q = 0; q < s; ++q) before += part[q][threadIdx.x & 15];
+    if (e < a.experts) {
+        for (int c = lo; c < hi; ++c) {
+            const uint64_t at = (uint64_t)c * a.experts + e;
+            const int n = a.hist[at];
+            a.hist[at] = before;
+            before += n;
+        }
+        if (s == 63) a.counts[e] = before;
+    }
+}
+
+template <typename I>
+__global__ void __launch_bounds__(64 * kSortWaves) sort_place_kernel(const SortArgs a) {
+    extern __shared__ int lds[];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int* start = lds;                                  // experts + 1
+    int* base = lds + a.experts + 1 + wave * a.experts;
+    const int piece = blockIdx.x * kSortWaves + wave;
+    int key[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) key[i] = key_of<I>(a, piece * kPiece + i * 64 + lane);
+    if (piece < a.pieces)
+        for (int e = lane; e < a.experts; e += 64)
+            base[e] = a.hist[(uint64_t)piece * a.experts + e];
+    prefix_counts(a.counts, start, a.experts);
+    if (piece < a.pieces) place_piece(a, key, piece * kPiece, base, start);
+    fill_unused(a, a.counts, start, blockIdx.x * blockDim.x + threadIdx.x,
+                gridDim.x * blockDim.x);
+}
+
+// Everything in one workgroup: wave w takes piece w.
+template <typename I>
+__global__ void __launch_bounds__(64 * kOneWaves) sort_one_kernel(const SortArgs a) {
+    extern __shared__ int lds[];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int* counts = lds;                                 // experts
+    int* start = lds + a.experts;                      // experts + 1
+    int* base = lds + 2 * a.experts + 1;               // [kOneWaves][experts]
+    for (int i = threadIdx.x; i < kOneWaves * a.experts; i += blockDim.x) base[i] = 0;
+    int key[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) key[i] = key_of<I>(a, wave * kPiece + i * 64 + lane);
+    __syncthreads();
+    int* mine = base + wave * a.experts;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+        if (key[i] < a.experts) atomicAdd(&mine[key[i]], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+        int before = 0;
+        for (int w = 0; w < kOneWaves; ++w) {
+            const int n = base[w * a.experts + e];
+            base[w * a.experts + e] = before;
+            before += n;
+        }
+        counts[e] = before;
+        a.counts[e] = before;
+    }
+    __syncthreads();
+    prefix_counts(counts, start, a.experts);
+    place_piece(a, key, wave * kPiece, mine, start);
+    fill_unused(a, counts, start, threadIdx.x, blockDim.x);
+}
+
+// --------------------------------------------------------------- row moves --
+//
+// All bound by HBM: a row is a few KiB, so the copies are made of 16-byte accesses
+// by a group of threads per token (a wave for short rows, a workgroup for long
+// ones), which reads a token's row once and writes all its copies, or reads all its
+// copies and writes the sum once.
+
+struct MoveArgs {
+    const void* in;      // x, rows or dout
+    const void* in2;     // combine backward: rows
+    void* out;
+    uint64_t in_ld, in2_ld, out_ld;
+    const int32_t* slots;
+    const int32_t* sources;
+    const float* weights;
+    float* dweights;
+    int32_t tokens, k, rows, hidden;
+    int32_t token_blocks;  // workgroups that take tokens; later ones clear unused rows
+};
+
+constexpr int kMoveBlock = 256;
+constexpr int kClearRows = kMoveBlock;   // rows whose source a clearing workgroup looks at
+
+__device__ __forceinline__ int slot_of(const MoveArgs& a, int t, int j) {
+    const int s = a.slots[(uint64_t)t * a.k + j];
+    return s >= 0 && s < a.rows ? s : -1;
+}
+
+// Zeros in the rows without a pair, of kClearRows rows from `first`.
+template <typename T>
+__device__ __forceinline__ void clear_rows(const MoveArgs& a, int64_t first) {
+    __shared__ uint64_t unused[kClearRows / 64];
+    const int64_t r = first + threadIdx.x;
+    bool clear = false;
+    if (r < a.rows) {
+        const int p = a.sources[r];
+        clear = p < 0 || (int64_t)p >= (int64_t)a.tokens * a.k;
+    }
+    const uint64_t m = __ballot(clear);
+    if ((threadIdx.x & 63) == 0) unused[threadIdx.x >> 6] = m;
+    __syncthreads();
+    Vec<T> zero;
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) zero.e[i] = (T)0.0f;
+    for (int w = 0; w < kClearRows / 64; ++w) {
+        uint64_t left = unused[w];
+        while (left) {
+            const int b = __ffsll((unsigned long long)left) - 1;
+            left &= left - 1;
+            T* row = (T*)a.out + (uint64_t)(first + w * 64 + b) * a.out_ld;
+            for (int c = threadIdx.x * Vec<T>::N; c < a.hidden; c += kMoveBlock * Vec<T>::N)
+                store_vec(row, c, a.hidden, zero);
+        }
+    }
+}
+
+// G threads per token (a power of two, 8 .. 256).
+template <typename T, int G>
+__global__ void __launch_bounds__(kMoveBlock) dispatch_kernel(const MoveArgs a) {
+    constexpr int N = Vec<T>::N;
+    if ((int)blockIdx.x >= a.token_blocks) {
+        clear_rows<T>(a, (int64_t)((int)blockIdx.x - a.token_blocks) * kClearRows);
+        return;
+    }
+    const int t = (int)blockIdx.x * (kMoveBlock / G) + (int)threadIdx.x / G;
+    if (t >= a.tokens) return;
+    const int g = threadIdx.x % G;
+    const T* x = (const T*)a.in + (uint64_t)t * a.in_ld;
+    for (int c = g * N; c < a.hidden; c += G * N) {
+        const Vec<T> v = load_vec(x, c, a.hidden);
+        for (int j = 0; j < a.k; ++j) {
+            const int s = slot_of(a, t, j);
+            if (s >= 0) store_vec((T*)a.out + (uint64_t)s * a.out_ld, c, a.hidden, v);
+        }
+    }
+}
+
+constexpr int kTogether = 4;  // rows of a token in flight
+
+template <typename T, int G>
+__global__ void __launch_bounds__(kMoveBlock) combine_kernel(const MoveArgs a) {
+    constexpr int N = Vec<T>::N;
+    const int t = (int)blockIdx.x * (kMoveBlock / G) + (int)threadIdx.x / G;
+    if (t >= a.tokens) return;
+    const int g = threadIdx.x % G;
+    T* out = (T*)a.out + (uint64_t)t * a.out_ld;
+    for (int c = g * N; c < a.hidden; c += G * N) {
+        float sum[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum[i] = 0.0f;
+        for (int j0 = 0; j0 < a.k; j0 += kTogether) {
+            Vec<T> v[kTogether];
+            float w[kTogether];
+            int s[kTogether];
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) {
+                s[j] = j0 + j < a.k ? slot_of(a, t, j0 + j) : -1;
+                if (s[j] >= 0) {
+                    v[j] = load_vec((const T*)a.in + (uint64_t)s[j] * a.in_ld, c, a.hidden);
+                    w[j] = a.weights ? a.weights[(uint64_t)t * a.k + j0 + j] : 1.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j)
+                if (s[j] >= 0)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) sum[i] = fmaf(w[j], (float)v[j].e[i], sum[i]);
+        }
+        Vec<T> r;
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.e[i] = (T)sum[i];
+        store_vec(out, c, a.hidden, r);
+    }
+}
+
+// G = 64 or 256 threads per token.  The dot products are summed per thread in column
+// order, then over the lanes of a wave, then over the waves.
+template <typename T, int G>
+__global__ void __launch_bounds__(kMoveBlock) combine_backward_kernel(const MoveArgs a) {
+    constexpr int N = Vec<T>::N;
+    constexpr int W = G / 64;
+    __shared__ float part[W][kTogether];
+    if ((int)blockIdx.x >= a.token_blocks) {
+        clear_rows<T>(a, (int64_t)((int)blockIdx.x - a.token_blocks) * kClearRows);
+        return;
+    }
+    const int t = (int)blockIdx.x * (kMoveBlock / G) + (int)threadIdx.x / G;
+    if (t >= a.tokens) return;        // whole waves, and with G = 256 the whole workgroup
+    const int g = threadIdx.x % G;
+    const T* d = (const T*)a.in + (uint64_t)t * a.in_ld;
+    for (int j0 = 0; j0 < a.k; j0 += kTogether) {
+        int s[kTogether];
+        float w[kTogether], dot[kTogether];
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) {
+            s[j] = j0 + j < a.k ? slot_of(a, t, j0 + j) : -1;
+            w[j] = s[j] >= 0 && a.weights ? a.weights[(uint64_t)t * a.k + j0 + j] : 1.0f;
+            dot[j] = 0.0f;
+        }
+        for (int c = g * N; c < a.hidden; c += G * N) {
+            const Vec<T> dv = load_vec(d, c, a.hidden);
+            Vec<T> v[kTogether];
+            if (a.dweights) {
+#pragma unroll
+                for (int j = 0; j < kTogether; ++j)
+                    if (s[j] >= 0)
+                        v[j] = load_vec((const T*)a.in2 + (uint64_t)s[j] * a.in2_ld, c, a.hidden);
+            }
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) {
+                if (s[j] < 0) continue;
+                if (a.out) {
+                    Vec<T> r;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) r.e[i] = (T)(w[j] * (float)dv.e[i]);
+                    store_vec((T*)a.out + (uint64_t)s[j] * a.out_ld, c, a.hidden, r);
+                }
+                if (a.dweights)
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        dot[j] = fmaf((float)dv.e[i], (float)v[j].e[i], dot[j]);
+            }
+        }
+        if (!a.dweights) continue;
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) dot[j] = lane_sum<64>(dot[j]);
+        if constexpr (W > 1) {
+            __syncthreads();          // the previous round's sums have been read
+            if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                for (int j = 0; j < kTogether; ++j) part[threadIdx.x >> 6][j] = dot[j];
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) {
+                dot[j] = 0.0f;
+#pragma unroll
+                for (int q = 0; q < W; ++q) dot[j] += part[q][j];
+            }
+        }
+        if (g == 0)
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j)
+                if (j0 + j < a.k) a.dweights[(uint64_t)t * a.k + j0 + j] = s[j] >= 0 ? dot[j] : 0.0f;
+    }
+}
+
+// ------------------------------------------------------------------ host side --
+
+constexpr uint64_t kMaxInt = 0x7FFFFFFFull;
+
+static rr_status_t check_sort(size_t tokens, int k, int experts, size_t capacity) {
+    if (k < 1 || experts < 1) return RR_ERR_INVALID;
+    if (experts > RR_MAX_EXPERTS || tokens > kMaxInt / (uint64_t)k) return RR_ERR_UNSUPPORTED;
+    // the last workgroup's pieces may reach past the pairs, and must still count in 32 bits
+    if ((uint64_t)tokens * k > kMaxInt - kPiece * kSortWaves) return RR_ERR_UNSUPPORTED;
+    if (capacity > kMaxInt / (uint64_t)experts) return RR_ERR_UNSUPPORTED;
+    return RR_OK;
+}
+
+static uint64_t sort_pieces(uint64_t pairs) { return ceil_div(pairs, kPiece); }
+// base, counts and start of every expert in the LDS of one workgroup
+static bool one_workgroup(uint64_t pairs, int experts) {
+    return pairs <= (uint64_t)kPiece * kOneWaves && experts <= 512;
+}
+
+template <typename I> static rr_status_t run_sort(const SortArgs& a, hipStream_t s) {
+    const size_t word = sizeof(int32_t);
+    if (one_workgroup((uint64_t)a.pairs, a.experts)) {
+        const size_t lds = ((kOneWaves + 2) * (size_t)a.experts + 1) * word;
+        sort_one_kernel<I><<<1, 64 * kOneWaves, lds, s>>>(a);
+        return launched();
+    }
+    const unsigned grid = (unsigned)ceil_div(a.pieces, kSortWaves);
+    sort_count_kernel<I><<<grid, 64 * kSortWaves, kSortWaves * a.experts * word, s>>>(a);
+    sort_sum_kernel<<<(unsigned)ceil_div(a.experts, 16), 1024, 0, s>>>(a);
+    const size_t lds = ((kSortWaves + 1) * (size_t)a.experts + 1) * word;
+    sort_place_kernel<I><<<grid, 64 * kSortWaves, lds, s>>>(a);
+    return launched();
+}
+
+// Shared by the row moves: sizes, index tensors and the matrices that are present.
+static rr_status_t check_move(size_t tokens, size_t hidden, int k, size_t rows, int dt) {
+    if (!is_float_type(dt) || k < 1 || hidden < 1) return RR_ERR_INVALID;
+    if (hidden > kMaxInt - 4096 || rows > kMaxInt || tokens > (kMaxInt - kMoveBlock) / (uint64_t)k)
+        return RR_ERR_UNSUPPORTED;
+    return RR_OK;
+}
+static bool good_rows(const rr_rows_t& r, size_t count, size_t hidden, int dt) {
+    if (count == 0) return true;
+    return r.data && aligned_to(r.data, type_bytes(dt)) && r.ld >= hidden && r.ld <= (1ull << 40);
+}
+static uint64_t reach(const rr_rows_t& r, size_t count, size_t hidden, int dt) {
+    return extent(count, r.ld, hidden, type_bytes(dt));
+}
+
+// Threads per token: enough for one 16-byte vector each, so that short rows do not
+// leave most of a workgroup idle.
+static int group_for(size_t hidden, int dt) {
+    const uint64_t vecs = ceil_div(hidden * type_bytes(dt), 16);
+    int g = 8;
+    while (g < kMoveBlock && (uint64_t)g < vecs) g *= 2;
+    return g;
+}
+
+// A launch holds fewer than 2^32 threads.
+static bool grid_fits(uint64_t blocks) { return blocks < (1ull << 32) / kMoveBlock; }
+
+#define BLK_BY_TYPE(dt, CALL)                 \
+    switch (dt) {                             \
+        case RR_FP32: { CALL(float); break; } \
+        case RR_BF16: { CALL(bf16); break; }  \
+        default: { CALL(f16); break; }        \
+    }
+
+#define BLK_BY_GROUP(g, T, KERNEL, grid, s, a)                            \
+    switch (g) {                                                         \
+        case 8: KERNEL<T, 8><<<grid, kMoveBlock, 0, s>>>(a); break;      \
+        case 16: KERNEL<T, 16><<<grid, kMoveBlock, 0, s>>>(a); break;    \
+        case 32: KERNEL<T, 32><<<grid, kMoveBlock, 0, s>>>(a); break;    \
+        case 64: KERNEL<T, 64><<<grid, kMoveBlock, 0, s>>>(a); break;    \
+        case 128: KERNEL<T, 128><<<grid, kMoveBlock, 0, s>>>(a); break;  \
+        default: KERNEL<T, 256><<<grid, kMoveBlock, 0, s>>>(a); break;   \
+    }
+
+}  // namespace blk
+
+using namespace blk;
+
+extern "C" {
+
+rr_status_t expert_sort_workspace(size_t tokens, int k, int experts, size_t* bytes) {
+    if (!bytes) return RR_ERR_INVALID;
+    const rr_status_t st = check_sort(tokens, k, experts, 0);
+    if (st != RR_OK) return st;
+    const uint64_t pairs = (uint64_t)tokens * k;
+    *bytes = one_workgroup(pairs, experts) ? 0 : sort_pieces(pairs) * experts * sizeof(int32_t);
+    return RR_OK;
+}
+
+rr_status_t expert_sort(const void* ids, int id_bytes, size_t id_ld, size_t tokens, int k,
+                        int experts, size_t capacity, int32_t* slots, int32_t* sources,
+                        int32_t* counts, int32_t* offsets, void* workspace,
+                        size_t workspace_bytes, rr_stream_t stream) {
+    rr_status_t st = check_sort(tokens, k, experts, capacity);
+    if (st != RR_OK) return st;
+    const uint64_t pairs = (uint64_t)tokens * k;
+    const uint64_t rows = capacity ? (uint64_t)experts * capacity : pairs;
+    if (id_bytes != 4 && id_bytes != 8) return RR_ERR_INVALID;
+    if (!counts || !offsets || !aligned_to(counts, 4) || !aligned_to(offsets, 4))
+        return RR_ERR_INVALID;
+    if (pairs && (!ids || !slots || !aligned_to(ids, (uint64_t)id_bytes) ||
+                  !aligned_to(slots, 4) || id_ld < (size_t)k || id_ld > (1ull << 40)))
+        return RR_ERR_INVALID;
+    if (rows && (!sources || !aligned_to(sources, 4))) return RR_ERR_INVALID;
+    size_t need = 0;
+    if ((st = expert_sort_workspace(tokens, k, experts, &need)) != RR_OK) return st;
+    if (need && (!workspace || !aligned_to(workspace, 4) || workspace_bytes < need))
+        return RR_ERR_INVALID;
+    const struct { const void* p; uint64_t n; } b[] = {
+        {ids, extent(tokens, id_ld, k, id_bytes)}, {slots, pairs * 4}, {sources, rows * 4},
+        {counts, (uint64_t)experts * 4}, {offsets, (uint64_t)experts * 4 + 4}, {workspace, need}};
+    for (int i = 0; i < 6; ++i)
+        for (int j = i + 1; j < 6; ++j)
+            if (overlap(b[i].p, b[i].n, b[j].p, b[j].n)) return RR_ERR_INVALID;
+    SortArgs a = {};
+    a.ids = ids;
+    a.id_ld = id_ld;
+    a.pairs = (int32_t)pairs;
+    a.k = k;
+    a.experts = experts;
+    while ((1 << a.bits) <= experts) ++a.bits;      // keys 0 .. experts
+    a.capacity = (int32_t)capacity;
+    a.rows = (int32_t)rows;
+    a.pieces = (int32_t)sort_pieces(pairs);
+    a.slots = slots;
+    a.sources = sources;
+    a.counts = counts;
+    a.offsets = offsets;
+    a.hist = (int32_t*)workspace;
+    return id_bytes == 4 ? run_sort<int32_t>(a, (hipStream_t)stream)
+                         : run_sort<int64_t>(a, (hipStream_t)stream);
+}
+
+rr_status_t expert_dispatch(rr_rows_t x, size_t tokens, size_t hidden, int k, rr_dtype_t dt,
+                            const int32_t* slots, const int32_t* sources, size_t rows,
+                            rr_rows_t out, rr_stream_t stream) {
+    const rr_status_t st = check_move(tokens, hidden, k, rows, dt);
+    if (st != RR_OK) return st;
+    if (!good_rows(x, tokens, hidden, dt) || !good_rows(out, rows, hidden, dt))
+        return RR_ERR_INVALID;
+    const uint64_t pairs = (uint64_t)tokens * k;
+    if ((tokens && (!slots || !aligned_to(slots, 4))) || (rows && (!sources || !aligned_to(sources, 4))))
+        return RR_ERR_INVALID;
+    const uint64_t n_out = reach(out, rows, hidden, dt);
+    if (overlap(x.data, reach(x, tokens, hidden, dt), out.data, n_out) ||
+        overlap(slots, pairs * 4, out.data, n_out) || overlap(sources, rows * 4, out.data, n_out))
+        return RR_ERR_INVALID;
+    if (rows == 0) return RR_OK;
+    MoveArgs a = {};
+    a.in = x.data;
+    a.in_ld = x.ld;
+    a.out = out.data;
+    a.out_ld = out.ld;
+    a.slots = slots;
+    a.sources = sources;
+    a.tokens = (int32_t)tokens;
+    a.k = k;
+    a.rows = (int32_t)rows;
+    a.hidden = (int32_t)hidden;
+    const int g = group_for(hidden, dt);
+    if (!grid_fits(ceil_div(tokens, kMoveBlock / g) + ceil_div(rows, kClearRows)))
+        return RR_ERR_UNSUPPORTED;
+    a.token_blocks = (int32_t)ceil_div(tokens, kMoveBlock / g);
+    const unsigned grid = (unsigned)(a.token_blocks + ceil_div(rows, kClearRows));
+    hipStream_t s = (hipStream_t)stream;
+#define CALL(T) BLK_BY_GROUP(g, T, dispatch_kernel, grid, s, a)
+    BLK_BY_TYPE(dt, CALL)
+#undef CALL
+    return launched();
+}
+
+rr_status_t expert_combine(rr_rows_t in, size_t rows, size_t hidden, rr_dtype_t dt,
+                           const int32_t* slots, const float* weights, size_t tokens, int k,
+                           rr_rows_t out, rr_stream_t stream) {
+    const rr_status_t st = check_move(tokens, hidden, k, rows, dt);
+    if (st != RR_OK) return st;
+    if (!good_rows(in, rows, hidden, dt) || !good_rows(out, tokens, hidden, dt))
+        return RR_ERR_INVALID;
+    const uint64_t pairs = (uint64_t)tokens * k;
+    if (tokens && (!slots || !aligned_to(slots, 4) || !aligned_to(weights, 4)))
+        return RR_ERR_INVALID;
+    const uint64_t n_out = reach(out, tokens, hidden, dt);
+    if (overlap(in.data, reach(in, rows, hidden, dt), out.data, n_out) ||
+        overlap(slots, pairs * 4, out.data, n_out) || overlap(weights, pairs * 4, out.data, n_out))
+        return RR_ERR_INVALID;
+    if (tokens == 0) return RR_OK;
+    MoveArgs a = {};
+    a.in = in.data;
+    a.in_ld = in.ld;
+    a.out = out.data;
+    a.out_ld = out.ld;
+    a.slots = slots;
+    a.weights = weights;
+    a.tokens = (int32_t)tokens;
+    a.k = k;
+    a.rows = (int32_t)rows;
+    a.hidden = (int32_t)hidden;
+    const int g = group_for(hidden, dt);
+    if (!grid_fits(ceil_div(tokens, kMoveBlock / g))) return RR_ERR_UNSUPPORTED;
+    const unsigned grid = (unsigned)ceil_div(tokens, kMoveBlock / g);
+    hipStream_t s = (hipStream_t)stream;
+#define CALL(T) BLK_BY_GROUP(g, T, combine_kernel, grid, s, a)
+    BLK_BY_TYPE(dt, CALL)
+#undef CALL
+    return launched();
+}
+
+rr_status_t expert_combine_backward(rr_rows_t dout, rr_rows_t in, size_t rows, size_t hidden,
+                                    rr_dtype_t dt, const int32_t* slots, const int32_t* sources,
+                                    const float* weights, size_t tokens, int k, rr_rows_t drows,
+                                    float* dweights, rr_stream_t stream) {
+    const rr_status_t st = check_move(tokens, hidden, k, rows, dt);
+    if (st != RR_OK) return st;
+    if (!good_rows(dout, tokens, hidden, dt)) return RR_ERR_INVALID;
+    if (dweights && !good_rows(in, rows, hidden, dt)) return RR_ERR_INVALID;
+    if (drows.data && !good_rows(drows, rows, hidden, dt)) return RR_ERR_INVALID;
+    const uint64_t pairs = (uint64_t)tokens * k;
+    if (tokens && (!slots || !aligned_to(slots, 4) || !aligned_to(weights, 4) ||
+                   !aligned_to(dweights, 4)))
+        return RR_ERR_INVALID;
+    if (drows.data && rows && (!sources || !aligned_to(sources, 4))) return RR_ERR_INVALID;
+    const struct { const void* p; uint64_t n; } read[] = {
+        {dout.data, reach(dout, tokens, hidden, dt)},
+        {dweights ? in.data : nullptr, reach(in, rows, hidden, dt)},
+        {slots, pairs * 4}, {sources, rows * 4}, {weights, pairs * 4}};
+    const uint64_t n_rows = drows.data ? reach(drows, rows, hidden, dt) : 0;
+    for (const auto& r : read)
+        if (overlap(r.p, r.n, drows.data, n_rows) || overlap(r.p, r.n, dweights, pairs * 4))
+            return RR_ERR_INVALID;
+    if (overlap(drows.data, n_rows, dweights, pairs * 4)) return RR_ERR_INVALID;
+    MoveArgs a = {};
+    a.in = dout.data;
+    a.in_ld = dout.ld;
+    a.in2 = in.data;
+    a.in2_ld = in.ld;
+    a.out = rows ? drows.data : nullptr;
+    a.out_ld = drows.ld;
+    a.slots = slots;
+    a.sources = sources;
+    a.weights = weights;
+    a.dweights = dweights;
+    a.tokens = (int32_t)tokens;
+    a.k = k;
+    a.rows = (int32_t)rows;
+    a.hidden = (int32_t)hidden;
+    if (!a.out && !a.dweights) return RR_OK;
+    const bool wide = group_for(hidden, dt) > 64;
+    if (!grid_fits(tokens + ceil_div(rows, kClearRows))) return RR_ERR_UNSUPPORTED;
+    a.token_blocks = (int32_t)(wide ? tokens : ceil_div(tokens, kMoveBlock / 64));
+    const unsigned grid = (unsigned)(a.token_blocks + (a.out ? ceil_div(rows, kClearRows) : 0));
+    if (grid == 0) return RR_OK;
+    hipStream_t s = (hipStream_t)stream;
+#define CALL(T)                                                          \
+    if (wide)                                                            \
+        combine_backward_kernel<T, 256><<<grid, kMoveBlock, 0, s>>>(a);  \
+    else                                                                 \
+        combine_backward_kernel<T, 64><<<grid, kMoveBlock, 0, s>>>(a);
+    BLK_BY_TYPE(dt, CALL)
+#undef CALL
+    return launched();
+}
+
+}  // extern "C"
