@@ -1,0 +1,701 @@
+// blk_gemm.hpp -- the matrix products behind block_linear and its gradients.
+//
+// Three forms, all out[i][j] = sum over c of P(i, c) Q(j, c):
+//   forward  i = row, j = n, c = k:    P = x,  Q = w_e         both contiguous along c
+//   dx       i = row, j = k, c = n:    P = dz, Q = w_e         Q contiguous along j
+//   dw       i = n,   j = k, c = row:  P = dz, Q = x           both contiguous along i, j
+#pragma once
+
+#include "blk_common.hpp"
+
+namespace blk {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+#define BLK_LDS __attribute__((address_space(3)))
+
+enum GemmForm { kForward = 0, kByX = 1, kByW = 2 };
+enum GemmTile { kTile256 = 0, kTile128 = 1, kTile64 = 2, kStream16 = 3, kStream32 = 4, kStream64 = 5 };
+constexpr int tile_rows(int tile) {
+    return tile == kTile256 ? 256 : tile == kTile128 ? 128 : tile == kTile64 || tile == kStream64 ? 64
+           : tile == kStream32 ? 32 : 16;
+}
+constexpr int kStreamCols = 32;
+constexpr int tile_cols(int tile) { return tile >= kStream16 ? kStreamCols : tile_rows(tile); }
+
+struct GemmArgs {
+    const void *p, *q;
+    uint64_t p_ld, q_ld, q_group;    // q_group: elements from one group's Q to the next
+    int32_t rows;                    // rows of all groups (P and out, or the contraction)
+    int32_t i, j, c;                 // sizes; the grouped one of i and c is not read
+    int32_t groups;
+    const int32_t* offsets;          // or null: rows / groups rows each
+    // epilogue
+    const void *bias, *residual;
+    void *z, *out;
+    uint64_t residual_ld, z_ld, out_ld, out_group;
+    int32_t act;
+    int32_t wide_out;                // out in fp32
+    int32_t quads;                   // four columns at a time in the epilogue
+    int32_t tiles_i, tiles_j;        // tiles_i: an upper bound over all groups
+    int32_t splits;                  // parts of the contraction
+    float* part;                     // [splits][rows of out][j], if splits > 1
+    uint64_t part_stride;            // elements of one part
+};
+
+// What the host chose for one product; see blk_linear.hip.
+struct GemmPlan {
+    int32_t form, tile;
+    int32_t direct;                  // operands straight from memory into LDS
+};
+
+rr_status_t launch_gemm_bf16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
+rr_status_t launch_gemm_f16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
+
+// ------------------------------------------------------------------- groups --
+
+struct Range {
+    int32_t group;   // -1: rows of no group
+    int32_t lo, hi;
+};
+
+// Range r of rows: 0 is what lies before the first group, groups + 1 what lies after
+// the last one.  Whatever the offsets hold, 0 <= lo <= hi <= rows.
+__device__ __forceinline__ Range range_of(const GemmArgs& a, int r) {
+    Range g = {-1, 0, 0};
+    if (r > a.groups + 1) return g;
+    if (!a.offsets) {
+        if (r < 1 || r > a.groups) return g;
+        const int32_t each = a.rows / a.groups;
+        return {r - 1, (r - 1) * each, r * each};
+    }
+    const auto edge = [&](int k) { return min(max(a.offsets[k], 0), a.rows); };
+    g.lo = r == 0 ? 0 : edge(r - 1);
+    g.hi = r > a.groups ? a.rows : edge(r);
+    if (g.hi < g.lo) g.hi = g.lo;
+    if (r >= 1 && r <= a.groups) g.group = r - 1;
+    return g;
+}
+
+// The range and the first row of row tile `tile` (tiles of `height` rows, counted
+// through the ranges one after another).  Called by whole waves; false past the end.
+__device__ __forceinline__ bool find_tile(const GemmArgs& a, int tile, int height, Range& g) {
+    if (a.groups == 1 && !a.offsets) {
+        g = {0, tile * height, a.rows};
+        return g.lo < a.rows;
+    }
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int r0 = 0; r0 < a.groups + 2; r0 += 64) {
+        const Range r = range_of(a, r0 + lane);
+        const int n = (r.hi - r.lo + height - 1) / height;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(sum, d);
+            if (lane >= d) sum += up;
+        }
+        const uint64_t past = __ballot(tile < before + sum);
+        if (past) {
+            const int at = __ffsll((unsigned long long)past) - 1;
+            g.group = __shfl(r.group, at);
+            g.lo = __shfl(r.lo, at) + (tile - before - (__shfl(sum, at) - __shfl(n, at))) * height;
+            g.hi = __shfl(r.hi, at);
+            return true;
+        }
+        before += __shfl(sum, 63);
+    }
+    return false;
+}
+
+// ----------------------------------------------------------------- the tiles --
+//
+// A tile of an operand in LDS is 64 deep along c, in one of two layouts:
+//   contiguous along c:  [row][64], the eight 16-byte pieces of a row permuted by the
+//     row number, so that the 16 rows a fragment read touches lie in different banks;
+//   contiguous along the rows:  [64][rows], the 32-byte pieces (16 rows) of a line
+//     permuted by the line number, for the transposing read, in which 16 lanes
+//     read four lines of 16 rows and each gets four values of one row.
+constexpr int kDepth = 64;
+
+template <bool ACROSS, int ROWS> struct Tile {
+    static constexpr int kBytes = ROWS * kDepth * 2;
+    __device__ static int mix(int line) {
+        return ((line & 3) | ((line >> 1) & 4)) & (ROWS / 16 - 1);
+    }
+    // (row, c) of the first of the 8 elements in 16-byte piece `id` of the tile
+    __device__ static void place(int id, int& row, int& c) {
+        if constexpr (!ACROSS) {
+            row = id >> 3;
+            c = ((id & 7) ^ (row & 7)) << 3;
+        } else {
+            c = id / (ROWS / 8);
+            const int at = id % (ROWS / 8);
+            row = (((at >> 1) ^ mix(c)) << 4) + ((at & 1) << 3);
+        }
+    }
+    // this lane's part of the fragment of 16 rows from `row`, 32 deep from c: row
+    // row + lane % 16, c + (lane / 16) * 8 .. + 7
+    template <typename V>
+    __device__ static V fragment(const BLK_LDS char* tile, int row, int c) {
+        const int lane = threadIdx.x & 63;
+        if constexpr (!ACROSS) {
+            const int r = row + (lane & 15), piece = (c >> 3) + (lane >> 4);
+            return __builtin_bit_cast(
+                V, *(const BLK_LDS u32x4*)(tile + r * (kDepth * 2) + ((piece ^ (r & 7)) << 4)));
+        } else {
+            s16x4 half[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int line = c + (lane >> 4) * 8 + h * 4 + ((lane & 15) >> 2);
+                half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (BLK_LDS s16x4*)(tile + line * (ROWS * 2) + (((row >> 4) ^ mix(line)) << 5) +
+                                     (lane & 3) * 8));
+            }
+            return __builtin_bit_cast(V, half);
+        }
+    }
+};
+
+template <typename T> struct Mma;
+template <> struct Mma<bf16> {
+    typedef bf16x8 V;
+    __device__ static f32x4 run(V a, V b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <> struct Mma<f16> {
+    typedef f16x8 V;
+    __device__ static f32x4 run(V a, V b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+__device__ __forceinline__ const char* uniform(const char* p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return (const char*)((uint64_t)hi << 32 | lo);
+}
+
+// Loads of one operand's tile through registers: any alignment, any size; what lies
+// outside [row, row_end) x [c, c_end) is zero.
+template <typename T, bool ACROSS, int ROWS, int THREADS> struct Staged {
+    static constexpr int kPieces = ROWS * kDepth / 8 / THREADS;
+    const T* base;
+    uint64_t ld;
+    int row, row_end, c_end;
+    u32x4 r[kPieces];
+    __device__ void start(const T* b, uint64_t stride, int r0, int r_end, int, int end) {
+        base = b;
+        ld = stride;
+        row = r0;
+        row_end = r_end;
+        c_end = end;
+    }
+    __device__ void load(int c0) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            int y, x;
+            Tile<ACROSS, ROWS>::place(k * THREADS + (int)threadIdx.x, y, x);
+            y += row;
+            x += c0;
+            Vec<T> v;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v.e[e] = (T)0.0f;
+            if (y < row_end && x < c_end)
+                v = ACROSS ? load_vec(base + (uint64_t)x * ld, y, row_end)
+                           : load_vec(base + (uint64_t)y * ld, x, c_end);
+            r[k] = __builtin_bit_cast(u32x4, v);
+        }
+    }
+    __device__ void store(BLK_LDS char* tile) const {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k)
+            *(BLK_LDS u32x4*)(tile + (k * THREADS + (int)threadIdx.x) * 16) = r[k];
+    }
+};
+
+// Loads straight from memory into LDS, 16 bytes a lane, a wave 1 KiB of the tile at a
+// time; the permutation is on the side of the addresses read.  A piece outside the
+// operand gets an offset outside the buffer descriptor's range, for which the hardware
+// gives zeros.  The instruction has no register result; the caller waits for it
+// (arrived()) before the barrier behind which the tile is read.
+constexpr uint32_t kReach = 0x80000000u;   // rows of a tile span at most 256 * 2^22 * 2 bytes
+
+template <typename T, bool ACROSS, int ROWS, int THREADS> struct Direct {
+    static constexpr int kPieces = ROWS * kDepth / 8 / THREADS;
+    const char* base;
+    uint64_t step;
+    uint32_t at[kPieces];
+    int depth[kPieces];
+    int c_end;
+    __device__ void start(const T* b, uint64_t ld, int r0, int r_end, int c0, int end) {
+        base = uniform((const char*)(b + (ACROSS ? (uint64_t)c0 * ld + r0 : (uint64_t)r0 * ld + c0)));
+        step = (ACROSS ? ld : 1) * kDepth * sizeof(T);
+        c_end = end;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            int y, x;
+            Tile<ACROSS, ROWS>::place(k * THREADS + (int)threadIdx.x, y, x);
+            const uint64_t off = (ACROSS ? (uint64_t)x * ld + y : (uint64_t)y * ld + x) * sizeof(T);
+            at[k] = r0 + y < r_end ? (uint32_t)off : kReach;
+            depth[k] = x;
+        }
+    }
+    // the tile at c into LDS; tiles are asked for in order
+    __device__ void load(BLK_LDS char* tile, int c) {
+        const uint64_t p = (uint64_t)uniform(base);
+        const u32x4 rsrc = {(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFF, kReach, 0x00027000};
+        const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane(
+            (int)((uint32_t)(uintptr_t)tile + (threadIdx.x >> 6) * 1024));
+        if (c + kDepth <= c_end) {
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) issue(rsrc, at[k], to + k * THREADS * 16);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+                issue(rsrc, c + depth[k] < c_end ? at[k] : kReach, to + k * THREADS * 16);
+        }
+        base += step;
+    }
+    __device__ static void issue(u32x4 rsrc, uint32_t offset, uint32_t to) {
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %0, 0 offen lds"
+                     :
+                     : "s"(rsrc), "v"(offset), "s"(to)
+                     : "memory");
+    }
+};
+
+// This wave's loads into LDS and its reads of LDS are done; then every wave's.
+__device__ __forceinline__ void arrived() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// ---------------------------------------------------------------- the epilogue --
+
+// Four neighbouring columns of one output row, element by element.
+template <typename T>
+__device__ __forceinline__ void finish_each(const GemmArgs& a, int group, bool none, int i, int j,
+                                            f32x4 v) {
+    const int n = min(4, a.j - j);
+    for (int e = 0; e < n; ++e) {
+        float z = v[e];
+        if (a.bias && !none) z += (float)((const T*)a.bias)[(uint64_t)group * a.j + j + e];
+        if (a.z) ((T*)a.z)[(uint64_t)i * a.z_ld + j + e] = (T)z;
+        if (!none) {
+            z = act_value(a.act, z);
+            if (a.residual) z += (float)((const T*)a.residual)[(uint64_t)i * a.residual_ld + j + e];
+        }
+        const uint64_t at = (a.out_group ? (uint64_t)group * a.out_group : 0) +
+                            (uint64_t)i * a.out_ld + j + e;
+        if (a.wide_out)
+            ((float*)a.out)[at] = z;
+        else
+            ((T*)a.out)[at] = (T)z;
+    }
+}
+
+template <typename T> struct Quad {
+    T e[4];
+};
+template <typename T> __device__ __forceinline__ Quad<T> load_quad(const void* p, uint64_t at) {
+    return __builtin_bit_cast(Quad<T>, *(const uint2*)((const T*)p + at));
+}
+template <typename T> __device__ __forceinline__ void store_quad(void* p, uint64_t at, f32x4 v) {
+    const Quad<T> q = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+    *(uint2*)((T*)p + at) = __builtin_bit_cast(uint2, q);
+}
+
+// The same, as 8-byte accesses where the host found every matrix apt for them.
+template <typename T>
+__device__ __forceinline__ void finish(const GemmArgs& a, int group, bool none, int i, int j,
+                                       f32x4 v) {
+    if (j >= a.j) return;
+    if (none) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (!a.quads) return finish_each<T>(a, group, none, i, j, v);
+    if (a.bias && !none) {
+        const Quad<T> b = load_quad<T>(a.bias, (uint64_t)group * a.j + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += (float)b.e[e];
+    }
+    if (a.z) store_quad<T>(a.z, (uint64_t)i * a.z_ld + j, v);
+    if (!none) {
+        if (a.act != RR_ACT_NONE)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = act_value(a.act, v[e]);
+        if (a.residual) {
+            const Quad<T> r = load_quad<T>(a.residual, (uint64_t)i * a.residual_ld + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += (float)r.e[e];
+        }
+    }
+    const uint64_t at = (a.out_group ? (uint64_t)group * a.out_group : 0) + (uint64_t)i * a.out_ld + j;
+    if (a.wide_out)
+        *(f32x4*)((float*)a.out + at) = v;
+    else
+        store_quad<T>(a.out, at, v);
+}
+
+// A part of the contraction's sums, for join_kernel; `i` counts the rows of all groups' outputs.
+__device__ __forceinline__ void keep_part(const GemmArgs& a, int split, uint64_t i, int j, f32x4 v) {
+    if (j >= a.j) return;
+    float* to = a.part + (uint64_t)split * a.part_stride + i * a.j + j;
+    if (a.j % 4 == 0) {
+        *(f32x4*)to = v;
+        return;
+    }
+    for (int e = 0; e < min(4, a.j - j); ++e) to[e] = v[e];
+}
+
+// ------------------------------------------------------------- where a tile is --
+
+struct Spot {
+    Range g;
+    int i0, i_end, c0, c_end, j0, split;
+};
+
+// Workgroup id -> tile.  Workgroups go to the 8 XCDs in turn, each with an L2 of its
+// own: every XCD takes one stretch of the tiles, and a stretch goes through 8 rows of
+// tiles column by column, so that the tiles in flight on an XCD share operands.
+template <bool BY_ROWS, int TI, int TJ>
+__device__ __forceinline__ bool find_spot(const GemmArgs& a, Spot& s) {
+    const unsigned total = (unsigned)a.tiles_i * (unsigned)a.tiles_j;
+    const unsigned id = blockIdx.x, xcd = id & 7, each = total >> 3, more = total & 7;
+    const unsigned at = xcd * each + min(xcd, more) + (id >> 3);
+    const unsigned tall = 8u * (unsigned)a.tiles_j, first = at / tall * 8u;
+    const unsigned high = min(8u, (unsigned)a.tiles_i - first), in = at % tall;
+    const int ti = (int)(first + in % high);
+    s.j0 = (int)(in / high) * TJ;
+    int c_lo, c_hi;
+    if constexpr (BY_ROWS) {
+        if (!find_tile(a, ti, TI, s.g)) return false;
+        s.split = (int)blockIdx.y;
+        s.i0 = s.g.lo;
+        s.i_end = s.g.hi;
+        c_lo = 0;
+        c_hi = s.g.group < 0 ? 0 : a.c;
+    } else {
+        s.split = (int)blockIdx.z;
+        s.g = range_of(a, (int)blockIdx.y + 1);
+        s.i0 = ti * TI;
+        s.i_end = a.i;
+        c_lo = s.g.lo;
+        c_hi = s.g.hi;
+    }
+    s.g.group = __builtin_amdgcn_readfirstlane(s.g.group);
+    s.i0 = __builtin_amdgcn_readfirstlane(s.i0);
+    s.i_end = __builtin_amdgcn_readfirstlane(s.i_end);
+    c_lo = __builtin_amdgcn_readfirstlane(c_lo);
+    c_hi = __builtin_amdgcn_readfirstlane(c_hi);
+    s.c0 = c_lo;
+    s.c_end = c_hi;
+    if (a.splits > 1) {
+        const int each_c = ((c_hi - c_lo + kDepth - 1) / kDepth + a.splits - 1) / a.splits;
+        const int64_t lo = c_lo + (int64_t)s.split * each_c * kDepth;
+        s.c0 = (int)min(lo, (int64_t)c_hi);
+        s.c_end = (int)min(lo + (int64_t)each_c * kDepth, (int64_t)c_hi);
+    }
+    return true;
+}
+
+// The results of a wave: FI x FJ blocks of 16 x 16.  The matrix instruction takes Q as its
+// first operand, so that a lane's four results are neighbours in a row of the output.
+template <typename T, bool BY_ROWS, int FI, int FJ>
+__device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, int i0, int j0,
+                                          const f32x4 (&acc)[FI][FJ]) {
+    const int lane = threadIdx.x & 63;
+    const bool none = s.g.group < 0;
+    if (a.splits > 1 && none) return;        // join_kernel knows
+#pragma unroll
+    for (int x = 0; x < FI; ++x) {
+        const int i = i0 + x * 16 + (lane & 15);
+        if (i >= s.i_end) continue;
+#pragma unroll
+        for (int y = 0; y < FJ; ++y) {
+            const int j = j0 + y * 16 + (lane >> 4) * 4;
+            if (a.splits > 1)
+                keep_part(a, s.split, BY_ROWS ? (uint64_t)i : (uint64_t)s.g.group * a.i + i, j, acc[x][y]);
+            else
+                finish<T>(a, s.g.group, none, i, j, acc[x][y]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the product --
+
+template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ, bool DIRECT>
+__global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a) {
+    typedef typename Mma<T>::V V;
+    constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16;
+    constexpr int PB = Tile<PA, TI>::kBytes, QB = Tile<QA, TJ>::kBytes;
+    __shared__ __align__(1024) char lds[2 * (PB + QB)];
+    BLK_LDS char* const room = (BLK_LDS char*)lds;
+    Spot s;
+    if (!find_spot<BY_ROWS, TI, TJ>(a, s)) return;
+    const T* p = (const T*)a.p;
+    const T* q = (const T*)a.q + (BY_ROWS && s.g.group > 0 ? (uint64_t)s.g.group * a.q_group : 0);
+    const int wave = threadIdx.x >> 6, wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int x = 0; x < FI; ++x)
+#pragma unroll
+        for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const auto multiply = [&](const BLK_LDS char* tile) {
+#pragma unroll
+        for (int k = 0; k < kDepth; k += 32) {
+            V fp[FI], fq[FJ];
+#pragma unroll
+            for (int y = 0; y < FJ; ++y)
+                fq[y] = Tile<QA, TJ>::template fragment<V>(tile + PB, wj + y * 16, k);
+#pragma unroll
+            for (int x = 0; x < FI; ++x)
+                fp[x] = Tile<PA, TI>::template fragment<V>(tile, wi + x * 16, k);
+#pragma unroll
+            for (int x = 0; x < FI; ++x)
+#pragma unroll
+                for (int y = 0; y < FJ; ++y) acc[x][y] = Mma<T>::run(fq[y], fp[x], acc[x][y]);
+        }
+    };
+    if constexpr (DIRECT) {
+        Direct<T, PA, TI, THREADS> lp;
+        Direct<T, QA, TJ, THREADS> lq;
+        lp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
+        lq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
+        if (s.c0 < s.c_end) {
+            lp.load(room, s.c0);
+            lq.load(room + PB, s.c0);
+        }
+        int stage = 0;
+        for (int c = s.c0; c < s.c_end; c += kDepth, stage ^= 1) {
+            arrived();       // this tile is there, and nobody reads the other one any more
+            if (c + kDepth < s.c_end) {
+                BLK_LDS char* next = room + (stage ^ 1) * (PB + QB);
+                lp.load(next, c + kDepth);
+                lq.load(next + PB, c + kDepth);
+            }
+            multiply(room + stage * (PB + QB));
+        }
+    } else {
+        Staged<T, PA, TI, THREADS> lp;
+        Staged<T, QA, TJ, THREADS> lq;
+        lp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
+        lq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
+        lp.load(s.c0);
+        lq.load(s.c0);
+        int stage = 0;
+        for (int c = s.c0; c < s.c_end; c += kDepth, stage ^= 1) {
+            BLK_LDS char* tile = room + stage * (PB + QB);
+            lp.store(tile);
+            lq.store(tile + PB);
+            __syncthreads();
+            if (c + kDepth < s.c_end) {
+                lp.load(c + kDepth);
+                lq.load(c + kDepth);
+            }
+            multiply(tile);
+        }
+    }
+    write_out<T, BY_ROWS, FI, FJ>(a, s, s.i0 + wi, s.j0 + wj, acc);
+}
+
+// ------------------------------------------------------------ few rows: one pass --
+//
+// The forward product of a few rows is the read of the weights.  A workgroup takes
+// 16 FI rows x 32 columns, its waves parts of the contraction, 128 deep each in turn;
+// operands go from memory to registers in the fragments' own layout (a lane's 16 bytes
+// are 8 values of one row, four lanes make 64 neighbouring bytes), and the waves' sums
+// meet in LDS, added in the order of the waves.
+constexpr int kStreamWaves = 8, kStreamDepth = 128;
+
+template <typename T, int R, bool DIRECT> struct Strip {
+    const T* base;
+    uint64_t ld;
+    int row, row_end, c_end;
+    uint32_t at[R];
+    __device__ void start(const T* b, uint64_t stride, int r0, int r_end, int end) {
+        const int lane = threadIdx.x & 63;
+        row = r0;
+        row_end = r_end;
+        c_end = end;
+        ld = stride;
+        base = DIRECT ? (const T*)uniform((const char*)(b + (uint64_t)r0 * stride)) : b;
+        if constexpr (DIRECT)
+#pragma unroll
+            for (int f = 0; f < R; ++f) {
+                const int y = f * 16 + (lane & 15);
+                at[f] = r0 + y < r_end ? (uint32_t)((uint64_t)y * stride * sizeof(T)) : kReach;
+            }
+    }
+    __device__ void load(u32x4 (&v)[4][R], int c0) const {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int c = c0 + s * 32 + (lane >> 4) * 8;
+#pragma unroll
+            for (int f = 0; f < R; ++f) {
+                if constexpr (DIRECT) {
+                    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, kReach, 0x00027000);
+                    v[s][f] = __builtin_amdgcn_raw_buffer_load_b128(
+                        rsrc, c < c_end ? at[f] + (uint32_t)c * (uint32_t)sizeof(T) : kReach, 0, 0);
+                } else {
+                    Vec<T> t;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) t.e[e] = (T)0.0f;
+                    const int y = row + f * 16 + (lane & 15);
+                    if (y < row_end && c < c_end) t = load_vec(base + (uint64_t)y * ld, c, c_end);
+                    v[s][f] = __builtin_bit_cast(u32x4, t);
+                }
+            }
+        }
+    }
+};
+
+template <typename T, int FI, bool DIRECT>
+__global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArgs a) {
+    typedef typename Mma<T>::V V;
+    constexpr int FJ = kStreamCols / 16;
+    __shared__ f32x4 sums[kStreamWaves][FI * FJ][64];
+    Range g;
+    if (!find_tile(a, (int)blockIdx.y, 16 * FI, g)) return;
+    g.group = __builtin_amdgcn_readfirstlane(g.group);
+    const int i0 = __builtin_amdgcn_readfirstlane(g.lo), i_end = __builtin_amdgcn_readfirstlane(g.hi);
+    const int j0 = (int)blockIdx.x * kStreamCols, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int c_end = g.group < 0 ? 0 : a.c;
+    Strip<T, FI, DIRECT> sp;
+    Strip<T, FJ, DIRECT> sq;
+    sp.start((const T*)a.p, a.p_ld, i0, i_end, c_end);
+    sq.start((const T*)a.q + (g.group > 0 ? (uint64_t)g.group * a.q_group : 0), a.q_ld, j0, a.j, c_end);
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int x = 0; x < FI; ++x)
+#pragma unroll
+        for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 vp[4][FI], vq[4][FJ];
+    int c = wave * kStreamDepth;
+    if (c < c_end) {
+        sq.load(vq, c);
+        sp.load(vp, c);
+    }
+    while (c < c_end) {
+        c += kStreamWaves * kStreamDepth;
+        u32x4 np[4][FI], nq[4][FJ];
+        if (c < c_end) {
+            sq.load(nq, c);
+            sp.load(np, c);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int x = 0; x < FI; ++x)
+#pragma unroll
+                for (int y = 0; y < FJ; ++y)
+                    acc[x][y] = Mma<T>::run(__builtin_bit_cast(V, vq[s][y]),
+                                            __builtin_bit_cast(V, vp[s][x]), acc[x][y]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+#pragma unroll
+            for (int x = 0; x < FI; ++x) vp[s][x] = np[s][x];
+#pragma unroll
+            for (int y = 0; y < FJ; ++y) vq[s][y] = nq[s][y];
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < FI; ++x)
+#pragma unroll
+        for (int y = 0; y < FJ; ++y) sums[wave][x * FJ + y][lane] = acc[x][y];
+    __syncthreads();
+    for (int f = wave; f < FI * FJ; f += kStreamWaves) {
+        f32x4 v = sums[0][f][lane];
+#pragma unroll
+        for (int w = 1; w < kStreamWaves; ++w) v += sums[w][f][lane];
+        const int i = i0 + f / FJ * 16 + (lane & 15);
+        if (i < i_end) finish<T>(a, g.group, g.group < 0, i, j0 + f % FJ * 16 + (lane >> 4) * 4, v);
+    }
+}
+
+// ----------------------------------------------------- parts of the contraction --
+
+// Adds the parts in their order and finishes the rows: 256 groups of four columns a workgroup.
+template <typename T> __global__ void __launch_bounds__(256) join_kernel(const GemmArgs a, int by_rows) {
+    const unsigned wide = (unsigned)(a.j + 3) / 4;
+    const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint64_t row = id / wide;
+    const int j = (int)(id % wide) * 4;
+    const uint64_t rows = by_rows ? (uint64_t)a.rows : (uint64_t)a.groups * a.i;
+    if (row >= rows) return;
+    int group = 0;
+    if (!by_rows) {
+        group = (int)(row / a.i);
+    } else if (a.offsets) {
+        int lo = 0, hi = a.groups + 1;       // the first of the offsets beyond the row
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (a.offsets[mid] <= (int)row) lo = mid + 1;
+            else hi = mid;
+        }
+        group = lo > a.groups ? -1 : lo - 1;
+    } else if (a.groups > 1) {
+        group = (int)row / (a.rows / a.groups);
+    }
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (group >= 0)
+        for (int s = 0; s < a.splits; ++s) {
+            const float* from = a.part + (uint64_t)s * a.part_stride + row * a.j + j;
+            if (a.j % 4 == 0)
+                v += *(const f32x4*)from;
+            else
+                for (int e = 0; e < min(4, a.j - j); ++e) v[e] += from[e];
+        }
+    finish<T>(a, group, group < 0, by_rows ? (int)row : (int)(row % a.i), j, v);
+}
+
+// -------------------------------------------------------------------- launching --
+
+template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int WI, int WJ, bool DIRECT>
+static void launch_tile(const GemmArgs& a, hipStream_t s) {
+    const unsigned tiles = (unsigned)a.tiles_i * (unsigned)a.tiles_j;
+    const dim3 grid = BY_ROWS ? dim3(tiles, (unsigned)a.splits) : dim3(tiles, (unsigned)a.groups, (unsigned)a.splits);
+    gemm_kernel<T, PA, QA, BY_ROWS, TI, TI, WI, WJ, DIRECT><<<grid, 64 * WI * WJ, 0, s>>>(a);
+}
+
+template <typename T, bool PA, bool QA, bool BY_ROWS>
+static void launch_form(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
+    if (p.tile == kTile256) launch_tile<T, PA, QA, BY_ROWS, 256, 2, 4, true>(a, s);
+    else if (p.tile == kTile128 && p.direct) launch_tile<T, PA, QA, BY_ROWS, 128, 2, 2, true>(a, s);
+    else if (p.tile == kTile128) launch_tile<T, PA, QA, BY_ROWS, 128, 2, 2, false>(a, s);
+    else if (p.direct) launch_tile<T, PA, QA, BY_ROWS, 64, 2, 2, true>(a, s);
+    else launch_tile<T, PA, QA, BY_ROWS, 64, 2, 2, false>(a, s);
+}
+
+template <typename T> static rr_status_t launch_gemm(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
+    if (p.tile >= kStream16) {
+        const dim3 grid((unsigned)a.tiles_j, (unsigned)a.tiles_i);
+        const int threads = 64 * kStreamWaves;
+        if (p.direct) {
+            if (p.tile == kStream16) stream_kernel<T, 1, true><<<grid, threads, 0, s>>>(a);
+            else if (p.tile == kStream32) stream_kernel<T, 2, true><<<grid, threads, 0, s>>>(a);
+            else stream_kernel<T, 4, true><<<grid, threads, 0, s>>>(a);
+        } else {
+            if (p.tile == kStream16) stream_kernel<T, 1, false><<<grid, threads, 0, s>>>(a);
+            else if (p.tile == kStream32) stream_kernel<T, 2, false><<<grid, threads, 0, s>>>(a);
+            else stream_kernel<T, 4, false><<<grid, threads, 0, s>>>(a);
+        }
+        return launched();
+    }
+    if (p.form == kForward) launch_form<T, false, false, true>(a, p, s);
+    else if (p.form == kByX) launch_form<T, false, true, true>(a, p, s);
+    else launch_form<T, true, true, false>(a, p, s);
+    const rr_status_t st = launched();
+    if (st != RR_OK || a.splits == 1) return st;
+    const bool by_rows = p.form != kByW;
+    const uint64_t rows = by_rows ? (uint64_t)a.rows : (uint64_t)a.groups * a.i;
+    const uint64_t blocks = ceil_div(rows * ceil_div(a.j, 4), 256);
+    join_kernel<T><<<(unsigned)blocks, 256, 0, s>>>(a, by_rows);
+    return launched();
+}
+
+}  // namespace blk

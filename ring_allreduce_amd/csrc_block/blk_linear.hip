@@ -1,280 +1,9 @@
-// blk_linear.hip -- a block's matrix products with bias, activation and residual in
-// the epilogue, dense or over the sorted rows of experts, and their gradients
-// (block_linear, block_linear_backward).
-//
-// Three products, all out[i][j] = sum over c of P(i, c) Q(j, c):
-//   forward  i = row, j = n, c = k:    P = x,  Q = w_e         both contiguous along c
-//   dx       i = row, j = k, c = n:    P = dz, Q = w_e         Q contiguous along j
-//   dw       i = n,   j = k, c = row:  P = dz, Q = x           both contiguous along i, j
-#include "blk_common.hpp"
+// blk_linear.hip -- the entry points of a block's matrix products (block_linear,
+// block_linear_backward): the choice of kernel for each product, the gradient of the
+// activation, and the checks.  The products themselves: blk_gemm.hpp.
+#include "blk_gemm.hpp"
 
 namespace blk {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-#define BLK_LDS __attribute__((address_space(3)))
-
-struct GemmArgs {
-    const void *p, *q;
-    uint64_t p_ld, q_ld, q_group;    // q_group: elements from one group's Q to the next
-    int32_t rows;                    // rows of all groups (P and out, or the contraction)
-    int32_t i, j, c;                 // sizes; the grouped one of i and c is not read
-    int32_t groups;
-    const int32_t* offsets;          // or null: rows / groups rows each
-    // epilogue
-    const void *bias, *residual;
-    void *z, *out;
-    uint64_t residual_ld, z_ld, out_ld, out_group;
-    int32_t act;
-    int32_t wide_out;                // out in fp32
-    int32_t tiles_i, tiles_j;        // tiles_i: an upper bound over all groups
-};
-
-// ------------------------------------------------------------------- groups --
-
-struct Range {
-    int32_t group;   // -1: rows of no group
-    int32_t lo, hi;
-};
-
-// Range r of rows: 0 is what lies before the first group, groups + 1 what lies after
-// the last one.  Whatever the offsets hold, 0 <= lo <= hi <= rows.
-__device__ __forceinline__ Range range_of(const GemmArgs& a, int r) {
-    Range g = {-1, 0, 0};
-    if (r > a.groups + 1) return g;
-    if (!a.offsets) {
-        if (r < 1 || r > a.groups) return g;
-        const int32_t each = a.rows / a.groups;
-        return {r - 1, (r - 1) * each, r * each};
-    }
-    const auto edge = [&](int k) { return min(max(a.offsets[k], 0), a.rows); };
-    g.lo = r == 0 ? 0 : edge(r - 1);
-    g.hi = r > a.groups ? a.rows : edge(r);
-    if (g.hi < g.lo) g.hi = g.lo;
-    if (r >= 1 && r <= a.groups) g.group = r - 1;
-    return g;
-}
-
-// The range and the first row of row tile `tile` (tiles of `height` rows, counted
-// through the ranges one after another).  Called by whole waves; false past the end.
-__device__ __forceinline__ bool find_tile(const GemmArgs& a, int tile, int height, Range& g) {
-    if (a.groups == 1 && !a.offsets) {
-        g = {0, tile * height, a.rows};
-        return g.lo < a.rows;
-    }
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int r0 = 0; r0 < a.groups + 2; r0 += 64) {
-        const Range r = range_of(a, r0 + lane);
-        const int n = (r.hi - r.lo + height - 1) / height;
-        int sum = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
-        }
-        const uint64_t past = __ballot(tile < before + sum);
-        if (past) {
-            const int at = __ffsll((unsigned long long)past) - 1;
-            g.group = __shfl(r.group, at);
-            g.lo = __shfl(r.lo, at) + (tile - before - (__shfl(sum, at) - __shfl(n, at))) * height;
-            g.hi = __shfl(r.hi, at);
-            return true;
-        }
-        before += __shfl(sum, 63);
-    }
-    return false;
-}
-
-// ----------------------------------------------------------------- the tiles --
-//
-// A tile of an operand in LDS is 64 deep along c, in one of two layouts:
-//   contiguous along c:  [row][64], the eight 16-byte pieces of a row permuted by the
-//     row number, so that the 16 rows a fragment read touches lie in different banks;
-//   contiguous along the rows:  [64][rows], the 32-byte pieces (16 rows) of a line
-//     permuted by the line number, for the transposing read, in which 16 lanes
-//     read four lines of 16 rows and each gets four values of one row.
-constexpr int kDepth = 64;
-
-__device__ __forceinline__ int line_mix(int c) { return (c & 3) | ((c >> 1) & 4); }
-
-template <bool ACROSS, int ROWS> struct Tile {
-    // byte address of the 16-byte piece that holds elements (row, c .. c + 7), or
-    // ACROSS: (row .. row + 7, c)
-    __device__ static int piece(int row, int c) {
-        if constexpr (!ACROSS) return row * (kDepth * 2) + (((c >> 3) ^ (row & 7)) << 4);
-        else return c * (ROWS * 2) + (((row >> 4) ^ line_mix(c)) << 5) + ((row & 8) << 1);
-    }
-    // this lane's part of the fragment of 16 rows from `row`, 32 deep from c: row
-    // row + lane % 16, c + (lane / 16) * 8 .. + 7
-    template <typename V>
-    __device__ static V fragment(const BLK_LDS char* tile, int row, int c) {
-        const int lane = threadIdx.x & 63;
-        if constexpr (!ACROSS) {
-            return __builtin_bit_cast(
-                V, *(const BLK_LDS u32x4*)(tile + piece(row + (lane & 15), c + (lane >> 4) * 8)));
-        } else {
-            s16x4 half[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int line = c + (lane >> 4) * 8 + h * 4 + ((lane & 15) >> 2);
-                half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (BLK_LDS s16x4*)(tile + line * (ROWS * 2) + (((row >> 4) ^ line_mix(line)) << 5) +
-                                     (lane & 3) * 8));
-            }
-            return __builtin_bit_cast(V, half);
-        }
-    }
-};
-
-template <typename T> struct Mma;
-template <> struct Mma<bf16> {
-    typedef bf16x8 V;
-    __device__ static f32x4 run(V a, V b, f32x4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-    }
-};
-template <> struct Mma<f16> {
-    typedef f16x8 V;
-    __device__ static f32x4 run(V a, V b, f32x4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-    }
-};
-
-// Loads of one operand's tile through registers: any alignment, any size; what lies
-// outside [row, row_end) x [c, c_end) is zero.
-template <typename T, bool ACROSS, int ROWS, int THREADS> struct Loader {
-    static constexpr int kPieces = ROWS * kDepth / 8 / THREADS;
-    u32x4 r[kPieces];
-    __device__ void load(const T* base, uint64_t ld, int row, int row_end, int c, int c_end) {
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            const int id = k * THREADS + (int)threadIdx.x;
-            Vec<T> v;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v.e[e] = (T)0.0f;
-            if constexpr (!ACROSS) {
-                const int y = row + id / 8, x = c + id % 8 * 8;
-                if (y < row_end && x < c_end) v = load_vec(base + (uint64_t)y * ld, x, c_end);
-            } else {
-                const int y = c + id / (ROWS / 8), x = row + id % (ROWS / 8) * 8;
-                if (y < c_end && x < row_end) v = load_vec(base + (uint64_t)y * ld, x, row_end);
-            }
-            r[k] = __builtin_bit_cast(u32x4, v);
-        }
-    }
-    __device__ void store(BLK_LDS char* tile) const {
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            const int id = k * THREADS + (int)threadIdx.x;
-            const int at = ACROSS ? Tile<ACROSS, ROWS>::piece(id % (ROWS / 8) * 8, id / (ROWS / 8))
-                                  : Tile<ACROSS, ROWS>::piece(id / 8, id % 8 * 8);
-            *(BLK_LDS u32x4*)(tile + at) = r[k];
-        }
-    }
-};
-
-// Four neighbouring columns of one output row.
-template <typename T>
-__device__ __forceinline__ void finish(const GemmArgs& a, const Range& g, bool by_rows, int i, int j,
-                                       f32x4 v) {
-    if (j >= a.j) return;
-    const int n = min(4, a.j - j);
-    const bool none = by_rows && g.group < 0;   // a row of no group: zeros
-    T* out = (T*)a.out + (by_rows ? 0 : (uint64_t)g.group * a.out_group);
-    for (int e = 0; e < n; ++e) {
-        float z = v[e];
-        if (a.bias && !none) z += (float)((const T*)a.bias)[(uint64_t)g.group * a.j + j + e];
-        if (none) z = 0.0f;
-        if (a.z) ((T*)a.z)[(uint64_t)i * a.z_ld + j + e] = (T)z;
-        if (!none) {
-            z = act_value(a.act, z);
-            if (a.residual) z += (float)((const T*)a.residual)[(uint64_t)i * a.residual_ld + j + e];
-        }
-        if (a.wide_out)
-            ((float*)a.out)[(uint64_t)g.group * a.out_group + (uint64_t)i * a.out_ld + j + e] = z;
-        else
-            out[(uint64_t)i * a.out_ld + j + e] = (T)z;
-    }
-}
-
-// 128 x 128 outputs a workgroup, 64 x 64 a wave.  The matrix instruction takes Q as its
-// first operand, so that a lane's four results are neighbours in a row of the output.
-constexpr int kTile = 128;
-
-template <typename T, bool PA, bool QA, bool BY_ROWS>
-__global__ void __launch_bounds__(256) gemm_kernel(const GemmArgs a) {
-    typedef typename Mma<T>::V V;
-    __shared__ __align__(16) char lds[2 * kTile * kDepth * 2];
-    BLK_LDS char* tp = (BLK_LDS char*)lds;
-    BLK_LDS char* tq = tp + kTile * kDepth * 2;
-    const int tj = (int)(blockIdx.x % (unsigned)a.tiles_j);
-    const int ti = (int)(blockIdx.x / (unsigned)a.tiles_j);
-    Range g;
-    int i0, i_end, c0, c_end;
-    if constexpr (BY_ROWS) {
-        if (!find_tile(a, ti, kTile, g)) return;
-        i0 = g.lo;
-        i_end = g.hi;
-        c0 = 0;
-        c_end = g.group < 0 ? 0 : a.c;
-    } else {
-        g = range_of(a, (int)blockIdx.y + 1);
-        i0 = ti * kTile;
-        i_end = a.i;
-        c0 = g.lo;
-        c_end = g.hi;
-    }
-    const int j0 = tj * kTile;
-    const T* p = (const T*)a.p;
-    const T* q = (const T*)a.q + (BY_ROWS && g.group > 0 ? (uint64_t)g.group * a.q_group : 0);
-    const int wave = threadIdx.x >> 6, wi = (wave >> 1) * 64, wj = (wave & 1) * 64;
-    f32x4 acc[4][4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    Loader<T, PA, kTile, 256> lp;
-    Loader<T, QA, kTile, 256> lq;
-    if (c0 < c_end) {
-        lp.load(p, a.p_ld, i0, i_end, c0, c_end);
-        lq.load(q, a.q_ld, j0, a.j, c0, c_end);
-    }
-    for (int c = c0; c < c_end; c += kDepth) {
-        lp.store(tp);
-        lq.store(tq);
-        __syncthreads();
-        if (c + kDepth < c_end) {
-            lp.load(p, a.p_ld, i0, i_end, c + kDepth, c_end);
-            lq.load(q, a.q_ld, j0, a.j, c + kDepth, c_end);
-        }
-#pragma unroll
-        for (int k = 0; k < kDepth; k += 32) {
-            V fp[4], fq[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                fp[x] = Tile<PA, kTile>::template fragment<V>(tp, wi + x * 16, k);
-                fq[x] = Tile<QA, kTile>::template fragment<V>(tq, wj + x * 16, k);
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) acc[x][y] = Mma<T>::run(fq[y], fp[x], acc[x][y]);
-        }
-        __syncthreads();
-    }
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        const int i = i0 + wi + x * 16 + (lane & 15);
-        if (i >= i_end) continue;
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-            finish<T>(a, g, BY_ROWS, i, j0 + wj + y * 16 + (lane >> 4) * 4, acc[x][y]);
-    }
-}
 
 // ------------------------------------------------------- activation's gradient --
 //
@@ -393,17 +122,81 @@ static uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
     return a->rows / height + a->groups + 2;
 }
 
-template <bool PA, bool QA, bool BY_ROWS>
-static rr_status_t run_gemm(const GemmArgs& k, int dt, int groups, hipStream_t s) {
-    const uint64_t blocks = (uint64_t)k.tiles_i * k.tiles_j;
-    if (blocks == 0) return RR_OK;
-    if (blocks > (1u << 24) - 1) return RR_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)blocks, BY_ROWS ? 1u : (unsigned)groups);
-    if (dt == RR_BF16)
-        gemm_kernel<bf16, PA, QA, BY_ROWS><<<grid, 256, 0, s>>>(k);
-    else
-        gemm_kernel<f16, PA, QA, BY_ROWS><<<grid, 256, 0, s>>>(k);
-    return launched();
+static bool good_operand(const void* p, uint64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
+
+// The kernel for one product: i x j outputs (i rows in all, or per group for dw), c deep.
+static GemmPlan choose(const rr_linear_t* a, int form, bool direct, int* splits) {
+    const uint64_t groups = (uint64_t)a->groups, mean = ceil_div(a->rows, groups);
+    const uint64_t i = form == kByW ? a->n : a->rows, j = form == kForward ? a->n : a->k;
+    const uint64_t c = form == kForward ? a->k : form == kByX ? a->n : mean;
+    GemmPlan p = {form, kTile64, direct};
+    *splits = 1;
+    if (form == kForward && mean <= 64) {
+        p.tile = mean <= 16 ? kStream16 : mean <= 32 ? kStream32 : kStream64;
+        return p;
+    }
+    const auto tiles = [&](uint64_t t) {
+        const uint64_t rows = form == kByW ? groups * ceil_div(i, t) : i / t + ceil_div(groups, 2) + (i % t != 0 && groups == 1);
+        return rows * ceil_div(j, t);
+    };
+    const uint64_t n64 = tiles(64), n128 = tiles(128), n256 = tiles(256);
+    double best = (double)ceil_div(n64, 1024) * 0.25 * 2.2;
+    const double by128 = (double)ceil_div(n128, 512) * 0.5 * 1.35, by256 = (double)ceil_div(n256, 256);
+    if (by128 <= best) {
+        best = by128;
+        p.tile = kTile128;
+    }
+    if (direct && by256 <= best) p.tile = kTile256;
+    const uint64_t n = p.tile == kTile64 ? n64 : p.tile == kTile128 ? n128 : n256;
+    if (n < 256 && p.tile != kTile256) {
+        const uint64_t want = 512 / (n ? n : 1), most = c / (4 * kDepth);
+        const uint64_t s = want < most ? want : most;
+        *splits = s < 2 ? 1 : s > 64 ? 64 : (int)s;
+    }
+    return p;
+}
+
+// Bytes of a product's parts, whatever the operands' alignment turns out to be.
+static uint64_t part_bytes(const rr_linear_t* a, int form) {
+    uint64_t most = 0;
+    for (int direct = 0; direct < 2; ++direct) {
+        int splits;
+        choose(a, form, direct != 0, &splits);
+        const uint64_t rows = form == kByW ? (uint64_t)a->groups * a->n : a->rows;
+        const uint64_t j = form == kForward ? a->n : a->k;
+        const uint64_t bytes = splits > 1 ? (uint64_t)splits * rows * j * sizeof(float) : 0;
+        if (bytes > most) most = bytes;
+    }
+    return ceil_div(most, 256) * 256;
+}
+
+static bool quads_ok(const void* p, uint64_t ld, uint64_t bytes) {
+    return !p || (aligned_to(p, 4 * bytes) && ld % 4 == 0);
+}
+
+// `a`: operands, sizes and epilogue are set; the rest follows from the plan.
+static rr_status_t run_gemm(GemmArgs k, const rr_linear_t* a, int form, void* workspace, hipStream_t s) {
+    bool direct = good_operand(k.p, k.p_ld) && good_operand(k.q, k.q_ld) && k.q_group % 8 == 0;
+    // the sizes along which 16 bytes are read
+    if (form == kForward) direct = direct && k.c % 8 == 0;
+    else if (form == kByX) direct = direct && k.c % 8 == 0 && k.j % 8 == 0;
+    else direct = direct && k.i % 8 == 0 && k.j % 8 == 0;
+    int splits;
+    const GemmPlan p = choose(a, form, direct, &splits);
+    const uint64_t ti = form == kByW ? ceil_div(k.i, tile_rows(p.tile)) : row_tiles(a, tile_rows(p.tile));
+    const uint64_t tj = ceil_div(k.j, tile_cols(p.tile));
+    if (ti * tj == 0) return RR_OK;
+    if (ti * tj > (1u << 22)) return RR_ERR_UNSUPPORTED;
+    k.tiles_i = (int32_t)ti;
+    k.tiles_j = (int32_t)tj;
+    k.splits = splits;
+    k.part = (float*)workspace;
+    k.part_stride = (form == kByW ? (uint64_t)k.groups * k.i : (uint64_t)k.rows) * k.j;
+    if (splits > 1 && ceil_div((k.part_stride / k.j) * ceil_div(k.j, 4), 256) > (1u << 24) - 1)
+        return RR_ERR_UNSUPPORTED;
+    k.quads = k.j % 4 == 0 && quads_ok(k.out, k.out_ld, k.wide_out ? 4 : 2) && quads_ok(k.z, k.z_ld, 2) &&
+              quads_ok(k.residual, k.residual_ld, 2) && quads_ok(k.bias, 0, 2);
+    return a->dt == RR_BF16 ? launch_gemm_bf16(k, p, s) : launch_gemm_f16(k, p, s);
 }
 
 // Parts of a group's rows in the sums over rows: enough workgroups to fill the device.
@@ -416,13 +209,15 @@ static uint64_t splits_of(const rr_linear_t* a) {
 }
 
 struct BackwardPlan {
-    uint64_t dz, part;  // bytes of scratch
+    uint64_t dz, part, split;  // bytes of scratch
 };
 static BackwardPlan plan_of(const rr_linear_t* a, const rr_linear_grad_t* g) {
-    BackwardPlan p = {0, 0};
+    BackwardPlan p = {0, 0, 0};
     if (a->act != RR_ACT_NONE && (g->dx.data || g->dw))
         p.dz = ceil_div(a->rows * ceil_div(a->n, 8) * 8 * 2, 256) * 256;
-    if (g->db) p.part = (uint64_t)a->groups * splits_of(a) * a->n * sizeof(float);
+    if (g->db) p.part = ceil_div((uint64_t)a->groups * splits_of(a) * a->n * sizeof(float), 256) * 256;
+    if (g->dx.data) p.split = part_bytes(a, kByX);
+    if (g->dw && part_bytes(a, kByW) > p.split) p.split = part_bytes(a, kByW);
     return p;
 }
 
@@ -436,16 +231,17 @@ rr_status_t block_linear_workspace(const rr_linear_t* a, size_t* bytes) {
     if (!bytes) return RR_ERR_INVALID;
     const rr_status_t st = check_linear(a);
     if (st != RR_OK) return st;
-    *bytes = 0;
+    *bytes = part_bytes(a, kForward);
     return RR_OK;
 }
 
 rr_status_t block_linear(const rr_linear_t* a, void* workspace, size_t workspace_bytes,
                          rr_stream_t stream) {
-    (void)workspace;
-    (void)workspace_bytes;
     const rr_status_t st = check_linear(a);
     if (st != RR_OK) return st;
+    const uint64_t need = part_bytes(a, kForward);
+    if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need))
+        return RR_ERR_INVALID;
     if (!rows_ok(a->out, a->rows, a->n, 2) || !rows_ok_if(a->residual, a->rows, a->n, 2) ||
         !aligned_to(a->bias, 2))
         return RR_ERR_INVALID;
@@ -457,8 +253,12 @@ rr_status_t block_linear(const rr_linear_t* a, void* workspace, size_t workspace
         {a->bias, (uint64_t)a->groups * a->n * 2},
         {a->offsets, (uint64_t)(a->groups + 1) * 4}};
     for (const auto& i : in)
-        if (overlap(i.p, i.n, a->out.data, n_out) || overlap(i.p, i.n, a->z.data, n_z))
+        if (overlap(i.p, i.n, a->out.data, n_out) || overlap(i.p, i.n, a->z.data, n_z) ||
+            overlap(i.p, i.n, workspace, need))
             return RR_ERR_INVALID;
+    if (overlap(a->out.data, n_out, workspace, need) || overlap(a->z.data, n_z, workspace, need) ||
+        overlap(a->residual.data, n_res, workspace, need))
+        return RR_ERR_INVALID;
     if (overlap(a->out.data, n_out, a->z.data, n_z) ||
         overlap(a->residual.data, n_res, a->z.data, n_z))
         return RR_ERR_INVALID;
@@ -483,11 +283,7 @@ rr_status_t block_linear(const rr_linear_t* a, void* workspace, size_t workspace
     k.out = a->out.data;
     k.out_ld = a->out.ld;
     k.act = a->act;
-    const uint64_t ti = row_tiles(a, kTile), tj = ceil_div(a->n, kTile);
-    if (ti > kMaxSize || tj > kMaxSize) return RR_ERR_UNSUPPORTED;
-    k.tiles_i = (int32_t)ti;
-    k.tiles_j = (int32_t)tj;
-    return run_gemm<false, false, true>(k, a->dt, a->groups, (hipStream_t)stream);
+    return run_gemm(k, a, kForward, workspace, (hipStream_t)stream);
 }
 
 rr_status_t block_linear_backward_workspace(const rr_linear_t* a, const rr_linear_grad_t* g,
@@ -496,7 +292,7 @@ rr_status_t block_linear_backward_workspace(const rr_linear_t* a, const rr_linea
     const rr_status_t st = check_grad(a, g);
     if (st != RR_OK) return st;
     const BackwardPlan p = plan_of(a, g);
-    *bytes = p.dz + p.part;
+    *bytes = p.dz + p.part + p.split;
     return RR_OK;
 }
 
@@ -505,7 +301,7 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
     rr_status_t st = check_grad(a, g);
     if (st != RR_OK) return st;
     const BackwardPlan plan = plan_of(a, g);
-    const uint64_t need = plan.dz + plan.part;
+    const uint64_t need = plan.dz + plan.part + plan.split;
     if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need))
         return RR_ERR_INVALID;
     const uint64_t w_bytes = extent(a->groups, a->w_stride, extent(a->n, a->w_ld, a->k, 1), 2);
@@ -526,9 +322,7 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
     }
     hipStream_t s = (hipStream_t)stream;
     rr_rows_t dz = g->dout;
-    const uint64_t tj = ceil_div(a->k, kTile);
-    const uint64_t ti_x = row_tiles(a, kTile), ti_w = ceil_div(a->n, kTile);
-    if (ti_x * tj > (1u << 24) - 1 || ti_w * tj > (1u << 24) - 1) return RR_ERR_UNSUPPORTED;
+    void* const split = (char*)workspace + plan.dz + plan.part;
     if (plan.dz || plan.part) {
         SlopeArgs k = {};
         k.g = groups_of(a);
@@ -571,9 +365,7 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
         k.c = (int32_t)a->n;
         k.out = g->dx.data;
         k.out_ld = g->dx.ld;
-        k.tiles_i = (int32_t)ti_x;
-        k.tiles_j = (int32_t)tj;
-        if ((st = run_gemm<false, true, true>(k, a->dt, a->groups, s)) != RR_OK) return st;
+        if ((st = run_gemm(k, a, kByX, split, s)) != RR_OK) return st;
     }
     if (g->dw) {
         GemmArgs k = groups_of(a);
@@ -587,9 +379,7 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
         k.out_ld = a->k;
         k.out_group = (uint64_t)a->n * a->k;
         k.wide_out = g->dw_dt == RR_FP32;
-        k.tiles_i = (int32_t)ti_w;
-        k.tiles_j = (int32_t)tj;
-        if ((st = run_gemm<true, true, false>(k, a->dt, a->groups, s)) != RR_OK) return st;
+        if ((st = run_gemm(k, a, kByW, split, s)) != RR_OK) return st;
     }
     return RR_OK;
 }
