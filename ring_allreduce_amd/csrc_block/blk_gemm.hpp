@@ -38,7 +38,6 @@ struct GemmArgs {
     uint64_t residual_ld, z_ld, out_ld, out_group;
     int32_t act;
     int32_t wide_out;                // out in fp32
-    int32_t quads;                   // four columns at a time in the epilogue
     int32_t tiles_i, tiles_j;        // tiles_i: an upper bound over all groups
     int32_t splits;                  // parts of the contraction
     float* part;                     // [splits][rows of out][j], if splits > 1
@@ -122,11 +121,11 @@ constexpr int kDepth = 64;
 
 template <bool ACROSS, int ROWS> struct Tile {
     static constexpr int kBytes = ROWS * kDepth * 2;
-    __device__ static int mix(int line) {
+    __device__ __forceinline__ static int mix(int line) {
         return ((line & 3) | ((line >> 1) & 4)) & (ROWS / 16 - 1);
     }
     // (row, c) of the first of the 8 elements in 16-byte piece `id` of the tile
-    __device__ static void place(int id, int& row, int& c) {
+    __device__ __forceinline__ static void place(int id, int& row, int& c) {
         if constexpr (!ACROSS) {
             row = id >> 3;
             c = ((id & 7) ^ (row & 7)) << 3;
@@ -139,7 +138,7 @@ template <bool ACROSS, int ROWS> struct Tile {
     // this lane's part of the fragment of 16 rows from `row`, 32 deep from c: row
     // row + lane % 16, c + (lane / 16) * 8 .. + 7
     template <typename V>
-    __device__ static V fragment(const BLK_LDS char* tile, int row, int c) {
+    __device__ __forceinline__ static V fragment(const BLK_LDS char* tile, int row, int c) {
         const int lane = threadIdx.x & 63;
         if constexpr (!ACROSS) {
             const int r = row + (lane & 15), piece = (c >> 3) + (lane >> 4);
@@ -162,13 +161,13 @@ template <bool ACROSS, int ROWS> struct Tile {
 template <typename T> struct Mma;
 template <> struct Mma<bf16> {
     typedef bf16x8 V;
-    __device__ static f32x4 run(V a, V b, f32x4 c) {
+    __device__ __forceinline__ static f32x4 run(V a, V b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
 };
 template <> struct Mma<f16> {
     typedef f16x8 V;
-    __device__ static f32x4 run(V a, V b, f32x4 c) {
+    __device__ __forceinline__ static f32x4 run(V a, V b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
 };
@@ -188,14 +187,14 @@ template <typename T, bool ACROSS, int ROWS, int THREADS> struct Staged {
     uint64_t ld;
     int row, row_end, c_end;
     u32x4 r[kPieces];
-    __device__ void start(const T* b, uint64_t stride, int r0, int r_end, int, int end) {
+    __device__ __forceinline__ void start(const T* b, uint64_t stride, int r0, int r_end, int, int end) {
         base = b;
         ld = stride;
         row = r0;
         row_end = r_end;
         c_end = end;
     }
-    __device__ void load(int c0) {
+    __device__ __forceinline__ void load(int c0) {
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {
             int y, x;
@@ -211,7 +210,7 @@ template <typename T, bool ACROSS, int ROWS, int THREADS> struct Staged {
             r[k] = __builtin_bit_cast(u32x4, v);
         }
     }
-    __device__ void store(BLK_LDS char* tile) const {
+    __device__ __forceinline__ void store(BLK_LDS char* tile) const {
 #pragma unroll
         for (int k = 0; k < kPieces; ++k)
             *(BLK_LDS u32x4*)(tile + (k * THREADS + (int)threadIdx.x) * 16) = r[k];
@@ -232,7 +231,7 @@ template <typename T, bool ACROSS, int ROWS, int THREADS> struct Direct {
     uint32_t at[kPieces];
     int depth[kPieces];
     int c_end;
-    __device__ void start(const T* b, uint64_t ld, int r0, int r_end, int c0, int end) {
+    __device__ __forceinline__ void start(const T* b, uint64_t ld, int r0, int r_end, int c0, int end) {
         base = uniform((const char*)(b + (ACROSS ? (uint64_t)c0 * ld + r0 : (uint64_t)r0 * ld + c0)));
         step = (ACROSS ? ld : 1) * kDepth * sizeof(T);
         c_end = end;
@@ -245,23 +244,22 @@ template <typename T, bool ACROSS, int ROWS, int THREADS> struct Direct {
             depth[k] = x;
         }
     }
-    // the tile at c into LDS; tiles are asked for in order
-    __device__ void load(BLK_LDS char* tile, int c) {
+    // The tile at c into LDS: aim(), then every piece once.  Tiles are asked for in order.
+    u32x4 rsrc;
+    uint32_t to;
+    int left;
+    __device__ __forceinline__ void aim(BLK_LDS char* tile, int c) {
         const uint64_t p = (uint64_t)uniform(base);
-        const u32x4 rsrc = {(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFF, kReach, 0x00027000};
-        const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane(
+        rsrc = u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFF, kReach, 0x00027000};
+        to = (uint32_t)__builtin_amdgcn_readfirstlane(
             (int)((uint32_t)(uintptr_t)tile + (threadIdx.x >> 6) * 1024));
-        if (c + kDepth <= c_end) {
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k) issue(rsrc, at[k], to + k * THREADS * 16);
-        } else {
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k)
-                issue(rsrc, c + depth[k] < c_end ? at[k] : kReach, to + k * THREADS * 16);
-        }
+        left = c_end - c;
         base += step;
     }
-    __device__ static void issue(u32x4 rsrc, uint32_t offset, uint32_t to) {
+    __device__ __forceinline__ void piece(int k) const {
+        issue(rsrc, depth[k] < left ? at[k] : kReach, to + k * THREADS * 16);
+    }
+    __device__ __forceinline__ static void issue(u32x4 rsrc, uint32_t offset, uint32_t to) {
         asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %0, 0 offen lds"
                      :
                      : "s"(rsrc), "v"(offset), "s"(to)
@@ -276,78 +274,77 @@ __device__ __forceinline__ void arrived() {
 
 // ---------------------------------------------------------------- the epilogue --
 
-// Four neighbouring columns of one output row, element by element.
-template <typename T>
-__device__ __forceinline__ void finish_each(const GemmArgs& a, int group, bool none, int i, int j,
-                                            f32x4 v) {
-    const int n = min(4, a.j - j);
-    for (int e = 0; e < n; ++e) {
-        float z = v[e];
-        if (a.bias && !none) z += (float)((const T*)a.bias)[(uint64_t)group * a.j + j + e];
-        if (a.z) ((T*)a.z)[(uint64_t)i * a.z_ld + j + e] = (T)z;
-        if (!none) {
-            z = act_value(a.act, z);
-            if (a.residual) z += (float)((const T*)a.residual)[(uint64_t)i * a.residual_ld + j + e];
-        }
-        const uint64_t at = (a.out_group ? (uint64_t)group * a.out_group : 0) +
-                            (uint64_t)i * a.out_ld + j + e;
-        if (a.wide_out)
-            ((float*)a.out)[at] = z;
-        else
-            ((T*)a.out)[at] = (T)z;
-    }
-}
-
-template <typename T> struct Quad {
-    T e[4];
+// N (4 or 8) neighbouring columns of one output row, in one access a matrix; any
+// alignment, and element by element past the last column (load_some, store_some).
+template <typename T, int N> struct Some {
+    T e[N];
 };
-template <typename T> __device__ __forceinline__ Quad<T> load_quad(const void* p, uint64_t at) {
-    return __builtin_bit_cast(Quad<T>, *(const uint2*)((const T*)p + at));
+template <int BYTES> struct Words;
+template <> struct Words<8> { typedef uint32_t V __attribute__((ext_vector_type(2))); };
+template <> struct Words<16> { typedef u32x4 V; };
+template <typename T, int BYTES> struct __attribute__((packed, aligned(sizeof(T)))) LooseWords {
+    typename Words<BYTES>::V v;
+};
+
+template <typename T, int N> __device__ __forceinline__ Some<T, N> load_some(const T* p, int n) {
+    Some<T, N> r;
+    if (n >= N) {
+        r = __builtin_bit_cast(Some<T, N>, ((const LooseWords<T, N * sizeof(T)>*)p)->v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) r.e[e] = e < n ? p[e] : (T)0.0f;
+    }
+    return r;
 }
-template <typename T> __device__ __forceinline__ void store_quad(void* p, uint64_t at, f32x4 v) {
-    const Quad<T> q = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
-    *(uint2*)((T*)p + at) = __builtin_bit_cast(uint2, q);
+template <typename T, int N> __device__ __forceinline__ void store_some(T* p, int n, const float (&v)[N]) {
+    Some<T, N> r;
+#pragma unroll
+    for (int e = 0; e < N; ++e) r.e[e] = (T)v[e];
+    if (n >= N) {
+        ((LooseWords<T, N * sizeof(T)>*)p)->v = __builtin_bit_cast(typename Words<N * sizeof(T)>::V, r);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e < n) p[e] = r.e[e];
+    }
+}
+template <int N> __device__ __forceinline__ void store_wide(float* p, int n, const float (&v)[N]) {
+#pragma unroll
+    for (int h = 0; h < N; h += 4) {
+        const float w[4] = {v[h], v[h + 1], v[h + 2], v[h + 3]};
+        if (n > h) store_some<float, 4>(p + h, n - h, w);
+    }
 }
 
-// The same, as 8-byte accesses where the host found every matrix apt for them.
-template <typename T>
-__device__ __forceinline__ void finish(const GemmArgs& a, int group, bool none, int i, int j,
-                                       f32x4 v) {
-    if (j >= a.j) return;
-    if (none) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (!a.quads) return finish_each<T>(a, group, none, i, j, v);
-    if (a.bias && !none) {
-        const Quad<T> b = load_quad<T>(a.bias, (uint64_t)group * a.j + j);
+// z = sum + bias, out = act(z) + residual; zeros for a row of no group.
+template <typename T, int N>
+__device__ __forceinline__ void finish(const GemmArgs& a, int group, int i, int j, float (&v)[N]) {
+    const int n = a.j - j;
+    if (n <= 0) return;
+    if (group < 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += (float)b.e[e];
+        for (int e = 0; e < N; ++e) v[e] = 0.0f;
+    } else if (a.bias) {
+        const Some<T, N> b = load_some<T, N>((const T*)a.bias + (uint64_t)group * a.j + j, n);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] += (float)b.e[e];
     }
-    if (a.z) store_quad<T>(a.z, (uint64_t)i * a.z_ld + j, v);
-    if (!none) {
+    if (a.z) store_some<T, N>((T*)a.z + (uint64_t)i * a.z_ld + j, n, v);
+    if (group >= 0) {
         if (a.act != RR_ACT_NONE)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = act_value(a.act, v[e]);
+            for (int e = 0; e < N; ++e) v[e] = act_value(a.act, v[e]);
         if (a.residual) {
-            const Quad<T> r = load_quad<T>(a.residual, (uint64_t)i * a.residual_ld + j);
+            const Some<T, N> r = load_some<T, N>((const T*)a.residual + (uint64_t)i * a.residual_ld + j, n);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += (float)r.e[e];
+            for (int e = 0; e < N; ++e) v[e] += (float)r.e[e];
         }
     }
     const uint64_t at = (a.out_group ? (uint64_t)group * a.out_group : 0) + (uint64_t)i * a.out_ld + j;
     if (a.wide_out)
-        *(f32x4*)((float*)a.out + at) = v;
+        store_wide<N>((float*)a.out + at, n, v);
     else
-        store_quad<T>(a.out, at, v);
-}
-
-// A part of the contraction's sums, for join_kernel; `i` counts the rows of all groups' outputs.
-__device__ __forceinline__ void keep_part(const GemmArgs& a, int split, uint64_t i, int j, f32x4 v) {
-    if (j >= a.j) return;
-    float* to = a.part + (uint64_t)split * a.part_stride + i * a.j + j;
-    if (a.j % 4 == 0) {
-        *(f32x4*)to = v;
-        return;
-    }
-    for (int e = 0; e < min(4, a.j - j); ++e) to[e] = v[e];
+        store_some<T, N>((T*)a.out + at, n, v);
 }
 
 // ------------------------------------------------------------- where a tile is --
@@ -401,28 +398,48 @@ __device__ __forceinline__ bool find_spot(const GemmArgs& a, Spot& s) {
     return true;
 }
 
-// The results of a wave: FI x FJ blocks of 16 x 16.  The matrix instruction takes Q as its
-// first operand, so that a lane's four results are neighbours in a row of the output.
-template <typename T, bool BY_ROWS, int FI, int FJ>
-__device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, int i0, int j0,
+// The results of the workgroup: FI x FJ blocks of 16 x 16 a wave.  The matrix instruction
+// takes Q as its first operand, so that a lane's four results are neighbours in a row.
+// Written from there, an access would touch 16 rows at 32 bytes each, all on one channel
+// of the L2 where the rows are a power of two apart (1.6 us instead of 0.2 for 16 rows of
+// a 256 x 256 tile); instead 16 rows of every wave at a time go through LDS in 32 bits
+// and leave as whole rows of the tile, 8 columns a thread.
+template <typename T, bool BY_ROWS, int TI, int TJ, int WI, int WJ, int FI, int FJ>
+__device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, BLK_LDS char* room,
                                           const f32x4 (&acc)[FI][FJ]) {
-    const int lane = threadIdx.x & 63;
-    const bool none = s.g.group < 0;
-    if (a.splits > 1 && none) return;        // join_kernel knows
+    constexpr int THREADS = 64 * WI * WJ, LINE = TJ + 4, ROWS = 16 * WI, GROUPS = TJ / 8;
+    constexpr int BUFFER = ROWS * LINE;
+    BLK_LDS float* const store = (BLK_LDS float*)room;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (a.splits > 1 && s.g.group < 0) return;        // join_kernel knows
+    __syncthreads();                                  // the operands' tiles are not read any more
 #pragma unroll
     for (int x = 0; x < FI; ++x) {
-        const int i = i0 + x * 16 + (lane & 15);
-        if (i >= s.i_end) continue;
+        BLK_LDS float* const buf = store + (x & 1) * BUFFER;
+        BLK_LDS float* const mine = buf + (wave / WJ * 16 + (lane & 15)) * LINE + wave % WJ * (TJ / WJ) + (lane >> 4) * 4;
 #pragma unroll
-        for (int y = 0; y < FJ; ++y) {
-            const int j = j0 + y * 16 + (lane >> 4) * 4;
-            if (a.splits > 1)
-                keep_part(a, s.split, BY_ROWS ? (uint64_t)i : (uint64_t)s.g.group * a.i + i, j, acc[x][y]);
-            else
-                finish<T>(a, s.g.group, none, i, j, acc[x][y]);
+        for (int y = 0; y < FJ; ++y) *(BLK_LDS f32x4*)(mine + y * 16) = acc[x][y];
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < ROWS * GROUPS / THREADS; ++t) {
+            const int id = t * THREADS + (int)threadIdx.x, r = id / GROUPS, col = id % GROUPS * 8;
+            const int i = s.i0 + r / 16 * (TI / WI) + x * 16 + r % 16, j = s.j0 + col;
+            const f32x4 lo = *(BLK_LDS f32x4*)(buf + r * LINE + col), hi = *(BLK_LDS f32x4*)(buf + r * LINE + col + 4);
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            if (i >= s.i_end || j >= a.j) continue;
+            if (a.splits > 1) {
+                const uint64_t row = BY_ROWS ? (uint64_t)i : (uint64_t)s.g.group * a.i + i;
+                store_wide<8>(a.part + (uint64_t)s.split * a.part_stride + row * a.j + j, a.j - j, v);
+            } else {
+                finish<T, 8>(a, s.g.group, i, j, v);
+            }
         }
     }
 }
+
+template <int N> struct Int {
+    static constexpr int value = N;
+};
 
 // ------------------------------------------------------------------ the product --
 
@@ -443,7 +460,7 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a)
     for (int x = 0; x < FI; ++x)
 #pragma unroll
         for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const auto multiply = [&](const BLK_LDS char* tile) {
+    [[maybe_unused]] const auto multiply = [&](const BLK_LDS char* tile) {
 #pragma unroll
         for (int k = 0; k < kDepth; k += 32) {
             V fp[FI], fq[FJ];
@@ -460,23 +477,62 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a)
         }
     };
     if constexpr (DIRECT) {
-        Direct<T, PA, TI, THREADS> lp;
-        Direct<T, QA, TJ, THREADS> lq;
+        // Half a tile (32 deep) is multiplied from registers while the next half is read into
+        // others, block row by block row; behind the barrier in the middle of a tile the next
+        // tile has arrived and the loads of the one after it follow into the place just read.
+        typedef Direct<T, PA, TI, THREADS> DP;
+        typedef Direct<T, QA, TJ, THREADS> DQ;
+        constexpr int PIECES = DP::kPieces + DQ::kPieces;
+        DP lp;
+        DQ lq;
         lp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
         lq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
-        if (s.c0 < s.c_end) {
-            lp.load(room, s.c0);
-            lq.load(room + PB, s.c0);
-        }
-        int stage = 0;
-        for (int c = s.c0; c < s.c_end; c += kDepth, stage ^= 1) {
-            arrived();       // this tile is there, and nobody reads the other one any more
-            if (c + kDepth < s.c_end) {
-                BLK_LDS char* next = room + (stage ^ 1) * (PB + QB);
-                lp.load(next, c + kDepth);
-                lq.load(next + PB, c + kDepth);
+        const auto load = [&](int from, int to) {
+#pragma unroll
+            for (int k = from; k < to; ++k)
+                if (k < DP::kPieces) lp.piece(k);
+                else lq.piece(k - DP::kPieces);
+        };
+        V fp[2][FI], fq[2][FJ];
+        const auto half = [&](auto now_, const BLK_LDS char* tile, int k, bool more) {
+            constexpr int now = decltype(now_)::value, then = now ^ 1;
+#pragma unroll
+            for (int x = 0; x < FI; ++x) {
+                if (now == 1 && more) load(x * PIECES / FI, (x + 1) * PIECES / FI);
+                if (x < FJ) fq[then][x] = Tile<QA, TJ>::template fragment<V>(tile + PB, wj + x * 16, k);
+                fp[then][x] = Tile<PA, TI>::template fragment<V>(tile, wi + x * 16, k);
+#pragma unroll
+                for (int y = 0; y < FJ; ++y) acc[x][y] = Mma<T>::run(fq[now][y], fp[now][x], acc[x][y]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            multiply(room + stage * (PB + QB));
+        };
+        const int tiles = (s.c_end - s.c0 + kDepth - 1) / kDepth;
+        if (tiles > 0) {
+            lp.aim(room, s.c0);
+            lq.aim(room + PB, s.c0);
+            load(0, PIECES);
+            arrived();
+            if (tiles > 1) {
+                lp.aim(room + PB + QB, s.c0 + kDepth);
+                lq.aim(room + PB + QB + PB, s.c0 + kDepth);
+                load(0, PIECES);
+            }
+#pragma unroll
+            for (int y = 0; y < FJ; ++y) fq[0][y] = Tile<QA, TJ>::template fragment<V>(room + PB, wj + y * 16, 0);
+#pragma unroll
+            for (int x = 0; x < FI; ++x) fp[0][x] = Tile<PA, TI>::template fragment<V>(room, wi + x * 16, 0);
+        }
+        for (int t = 0; t < tiles; ++t) {
+            BLK_LDS char* const tile = room + (t & 1) * (PB + QB);
+            BLK_LDS char* const next = room + (~t & 1) * (PB + QB);
+            half(Int<0>(), tile, 32, false);
+            arrived();
+            const bool more = t + 2 < tiles;
+            if (more) {
+                lp.aim(tile, s.c0 + (t + 2) * kDepth);
+                lq.aim(tile + PB, s.c0 + (t + 2) * kDepth);
+            }
+            half(Int<1>(), next, 0, more);
         }
     } else {
         Staged<T, PA, TI, THREADS> lp;
@@ -498,7 +554,7 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a)
             multiply(tile);
         }
     }
-    write_out<T, BY_ROWS, FI, FJ>(a, s, s.i0 + wi, s.j0 + wj, acc);
+    write_out<T, BY_ROWS, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
 }
 
 // ------------------------------------------------------------ few rows: one pass --
@@ -515,7 +571,7 @@ template <typename T, int R, bool DIRECT> struct Strip {
     uint64_t ld;
     int row, row_end, c_end;
     uint32_t at[R];
-    __device__ void start(const T* b, uint64_t stride, int r0, int r_end, int end) {
+    __device__ __forceinline__ void start(const T* b, uint64_t stride, int r0, int r_end, int end) {
         const int lane = threadIdx.x & 63;
         row = r0;
         row_end = r_end;
@@ -529,7 +585,7 @@ template <typename T, int R, bool DIRECT> struct Strip {
                 at[f] = r0 + y < r_end ? (uint32_t)((uint64_t)y * stride * sizeof(T)) : kReach;
             }
     }
-    __device__ void load(u32x4 (&v)[4][R], int c0) const {
+    __device__ __forceinline__ void load(u32x4 (&v)[4][R], int c0) const {
         const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -613,13 +669,14 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArg
 #pragma unroll
         for (int w = 1; w < kStreamWaves; ++w) v += sums[w][f][lane];
         const int i = i0 + f / FJ * 16 + (lane & 15);
-        if (i < i_end) finish<T>(a, g.group, g.group < 0, i, j0 + f % FJ * 16 + (lane >> 4) * 4, v);
+        float o[4] = {v[0], v[1], v[2], v[3]};
+        if (i < i_end) finish<T, 4>(a, g.group, i, j0 + f % FJ * 16 + (lane >> 4) * 4, o);
     }
 }
 
 // ----------------------------------------------------- parts of the contraction --
 
-// Adds the parts in their order and finishes the rows: 256 groups of four columns a workgroup.
+// Adds the parts in their order and finishes the rows: four columns a thread.
 template <typename T> __global__ void __launch_bounds__(256) join_kernel(const GemmArgs a, int by_rows) {
     const unsigned wide = (unsigned)(a.j + 3) / 4;
     const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
@@ -641,16 +698,15 @@ template <typename T> __global__ void __launch_bounds__(256) join_kernel(const G
     } else if (a.groups > 1) {
         group = (int)row / (a.rows / a.groups);
     }
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (group >= 0)
         for (int s = 0; s < a.splits; ++s) {
             const float* from = a.part + (uint64_t)s * a.part_stride + row * a.j + j;
-            if (a.j % 4 == 0)
-                v += *(const f32x4*)from;
-            else
-                for (int e = 0; e < min(4, a.j - j); ++e) v[e] += from[e];
+            const Some<float, 4> p = load_some<float, 4>(from, a.j - j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += p.e[e];
         }
-    finish<T>(a, group, group < 0, by_rows ? (int)row : (int)(row % a.i), j, v);
+    finish<T, 4>(a, group, by_rows ? (int)row : (int)(row % a.i), j, v);
 }
 
 // -------------------------------------------------------------------- launching --

@@ -170,10 +170,6 @@ static uint64_t part_bytes(const rr_linear_t* a, int form) {
     return ceil_div(most, 256) * 256;
 }
 
-static bool quads_ok(const void* p, uint64_t ld, uint64_t bytes) {
-    return !p || (aligned_to(p, 4 * bytes) && ld % 4 == 0);
-}
-
 // `a`: operands, sizes and epilogue are set; the rest follows from the plan.
 static rr_status_t run_gemm(GemmArgs k, const rr_linear_t* a, int form, void* workspace, hipStream_t s) {
     bool direct = good_operand(k.p, k.p_ld) && good_operand(k.q, k.q_ld) && k.q_group % 8 == 0;
@@ -194,8 +190,6 @@ static rr_status_t run_gemm(GemmArgs k, const rr_linear_t* a, int form, void* wo
     k.part_stride = (form == kByW ? (uint64_t)k.groups * k.i : (uint64_t)k.rows) * k.j;
     if (splits > 1 && ceil_div((k.part_stride / k.j) * ceil_div(k.j, 4), 256) > (1u << 24) - 1)
         return RR_ERR_UNSUPPORTED;
-    k.quads = k.j % 4 == 0 && quads_ok(k.out, k.out_ld, k.wide_out ? 4 : 2) && quads_ok(k.z, k.z_ld, 2) &&
-              quads_ok(k.residual, k.residual_ld, 2) && quads_ok(k.bias, 0, 2);
     return a->dt == RR_BF16 ? launch_gemm_bf16(k, p, s) : launch_gemm_f16(k, p, s);
 }
 
