@@ -78,6 +78,19 @@ __device__ __forceinline__ Range range_of(const GemmArgs& a, int r) {
     return g;
 }
 
+// Row tiles of `height` rows in all ranges.  Called by whole waves.
+__device__ __forceinline__ int count_tiles(const GemmArgs& a, int height) {
+    if (a.groups == 1 && !a.offsets) return (a.rows + height - 1) / height;
+    int n = 0;
+    for (int r0 = 0; r0 < a.groups + 2; r0 += 64) {
+        const Range r = range_of(a, r0 + (int)(threadIdx.x & 63));
+        n += (r.hi - r.lo + height - 1) / height;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
 // The range and the first row of row tile `tile` (tiles of `height` rows, counted
 // through the ranges one after another).  Called by whole waves; false past the end.
 __device__ __forceinline__ bool find_tile(const GemmArgs& a, int tile, int height, Range& g) {
@@ -135,25 +148,41 @@ template <bool ACROSS, int ROWS> struct Tile {
             row = (((at >> 1) ^ mix(c)) << 4) + ((at & 1) << 3);
         }
     }
-    // this lane's part of the fragment of 16 rows from `row`, 32 deep from c: row
-    // row + lane % 16, c + (lane / 16) * 8 .. + 7
-    template <typename V>
-    __device__ __forceinline__ static V fragment(const BLK_LDS char* tile, int row, int c) {
+};
+
+// Reads fragments of 16 rows, 32 deep, of the tiles in LDS: a lane gets row lane % 16 of
+// block x, c + (lane / 16) * 8 .. + 7.  Of a block's address only the lane's part takes
+// registers: the block row, the half and the operand's place are constants of the
+// instruction, and going to the other stage is one exclusive or.
+template <bool ACROSS, int ROWS> struct Reader {
+    uint32_t at[2];
+    __device__ __forceinline__ void start(uint32_t tile, int row) {    // row: a wave's first, of the tile
         const int lane = threadIdx.x & 63;
         if constexpr (!ACROSS) {
-            const int r = row + (lane & 15), piece = (c >> 3) + (lane >> 4);
-            return __builtin_bit_cast(
-                V, *(const BLK_LDS u32x4*)(tile + r * (kDepth * 2) + ((piece ^ (r & 7)) << 4)));
-        } else {
-            s16x4 half[2];
+            const int r = row + (lane & 15);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int line = c + (lane >> 4) * 8 + h * 4 + ((lane & 15) >> 2);
-                half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (BLK_LDS s16x4*)(tile + line * (ROWS * 2) + (((row >> 4) ^ mix(line)) << 5) +
-                                     (lane & 3) * 8));
-            }
-            return __builtin_bit_cast(V, half);
+            for (int h = 0; h < 2; ++h)
+                at[h] = tile + r * (kDepth * 2) + ((((lane >> 4) + h * 4) ^ (lane & 7)) << 4);
+        } else {
+            const int line = (lane >> 4) * 8 + ((lane & 15) >> 2);
+            at[0] = tile + line * (ROWS * 2) + (((row >> 4) ^ Tile<ACROSS, ROWS>::mix(line)) << 5) + (lane & 3) * 8;
+        }
+    }
+    __device__ __forceinline__ void other(uint32_t stage) {
+        at[0] ^= stage;
+        if constexpr (!ACROSS) at[1] ^= stage;
+    }
+    template <typename V> __device__ __forceinline__ V fragment(int x, int half) const {
+        if constexpr (!ACROSS) {
+            return __builtin_bit_cast(V, *(const BLK_LDS u32x4*)(uintptr_t)(at[half] + x * 16 * kDepth * 2));
+        } else {
+            s16x4 v[2];
+            const uint32_t from = at[0] ^ (x << 5);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (BLK_LDS s16x4*)(uintptr_t)(from + (half * 32 + h * 4) * (ROWS * 2)));
+            return __builtin_bit_cast(V, v);
         }
     }
 };
@@ -171,6 +200,14 @@ template <> struct Mma<f16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
 };
+
+// The thread's number, as a value of this place in the program: what is made from it is
+// made here again instead of being held in registers through the products before.
+__device__ __forceinline__ int here() {
+    int t = (int)threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
 
 __device__ __forceinline__ const char* uniform(const char* p) {
     const uint64_t v = (uint64_t)p;
@@ -229,36 +266,43 @@ template <typename T, bool ACROSS, int ROWS, int THREADS> struct Direct {
     const char* base;
     uint64_t step;
     uint32_t at[kPieces];
-    int depth[kPieces];
-    int c_end;
+    int left;
+    uint32_t mine;                   // of this wave in the tile
+    u32x4 rsrc;
+    uint32_t to;
     __device__ __forceinline__ void start(const T* b, uint64_t ld, int r0, int r_end, int c0, int end) {
-        base = uniform((const char*)(b + (ACROSS ? (uint64_t)c0 * ld + r0 : (uint64_t)r0 * ld + c0)));
+        base = (const char*)(b + (ACROSS ? (uint64_t)c0 * ld + r0 : (uint64_t)r0 * ld + c0));
         step = (ACROSS ? ld : 1) * kDepth * sizeof(T);
-        c_end = end;
+        left = end - c0;
+        mine = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) * 1024);
+        const int thread = here();
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {
             int y, x;
-            Tile<ACROSS, ROWS>::place(k * THREADS + (int)threadIdx.x, y, x);
+            Tile<ACROSS, ROWS>::place(k * THREADS + thread, y, x);
             const uint64_t off = (ACROSS ? (uint64_t)x * ld + y : (uint64_t)y * ld + x) * sizeof(T);
             at[k] = r0 + y < r_end ? (uint32_t)off : kReach;
-            depth[k] = x;
         }
     }
-    // The tile at c into LDS: aim(), then every piece once.  Tiles are asked for in order.
-    u32x4 rsrc;
-    uint32_t to;
-    int left;
-    __device__ __forceinline__ void aim(BLK_LDS char* tile, int c) {
+    // The next 64 deep tile into LDS at `tile`: aim(), then every piece once.  Tiles past the
+    // end come as zeros.
+    __device__ __forceinline__ void aim(uint32_t tile) {
         const uint64_t p = (uint64_t)uniform(base);
         rsrc = u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFF, kReach, 0x00027000};
-        to = (uint32_t)__builtin_amdgcn_readfirstlane(
-            (int)((uint32_t)(uintptr_t)tile + (threadIdx.x >> 6) * 1024));
-        left = c_end - c;
+        to = tile + mine;
+        if (left < kDepth) {
+            const int thread = here();
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                int y, x;
+                Tile<ACROSS, ROWS>::place(k * THREADS + thread, y, x);
+                if (x >= left) at[k] = kReach;
+            }
+        }
+        left -= kDepth;
         base += step;
     }
-    __device__ __forceinline__ void piece(int k) const {
-        issue(rsrc, depth[k] < left ? at[k] : kReach, to + k * THREADS * 16);
-    }
+    __device__ __forceinline__ void piece(int k) const { issue(rsrc, at[k], to + k * THREADS * 16); }
     __device__ __forceinline__ static void issue(u32x4 rsrc, uint32_t offset, uint32_t to) {
         asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %0, 0 offen lds"
                      :
@@ -267,9 +311,10 @@ template <typename T, bool ACROSS, int ROWS, int THREADS> struct Direct {
     }
 };
 
-// This wave's loads into LDS and its reads of LDS are done; then every wave's.
-__device__ __forceinline__ void arrived() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// This wave's loads into LDS but the last LATER are there and its reads of LDS are done,
+// then every wave's.
+template <int LATER> __device__ __forceinline__ void arrived() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(LATER) : "memory");
 }
 
 // ---------------------------------------------------------------- the epilogue --
@@ -288,7 +333,9 @@ template <typename T, int BYTES> struct __attribute__((packed, aligned(sizeof(T)
 
 template <typename T, int N> __device__ __forceinline__ Some<T, N> load_some(const T* p, int n) {
     Some<T, N> r;
-    if (n >= N) {
+    if constexpr (N == 1) {
+        r.e[0] = *p;
+    } else if (n >= N) {
         r = __builtin_bit_cast(Some<T, N>, ((const LooseWords<T, N * sizeof(T)>*)p)->v);
     } else {
 #pragma unroll
@@ -300,7 +347,9 @@ template <typename T, int N> __device__ __forceinline__ void store_some(T* p, in
     Some<T, N> r;
 #pragma unroll
     for (int e = 0; e < N; ++e) r.e[e] = (T)v[e];
-    if (n >= N) {
+    if constexpr (N == 1) {
+        *p = r.e[0];
+    } else if (n >= N) {
         ((LooseWords<T, N * sizeof(T)>*)p)->v = __builtin_bit_cast(typename Words<N * sizeof(T)>::V, r);
     } else {
 #pragma unroll
@@ -309,42 +358,50 @@ template <typename T, int N> __device__ __forceinline__ void store_some(T* p, in
     }
 }
 template <int N> __device__ __forceinline__ void store_wide(float* p, int n, const float (&v)[N]) {
+    if constexpr (N == 1) {
+        *p = v[0];
+    } else {
 #pragma unroll
-    for (int h = 0; h < N; h += 4) {
-        const float w[4] = {v[h], v[h + 1], v[h + 2], v[h + 3]};
-        if (n > h) store_some<float, 4>(p + h, n - h, w);
+        for (int h = 0; h < N; h += 4) {
+            const float w[4] = {v[h], v[h + 1], v[h + 2], v[h + 3]};
+            if (n > h) store_some<float, 4>(p + h, n - h, w);
+        }
     }
 }
 
 // z = sum + bias, out = act(z) + residual; zeros for a row of no group.
 template <typename T, int N>
-__device__ __forceinline__ void finish(const GemmArgs& a, int group, int i, int j, float (&v)[N]) {
-    const int n = a.j - j;
-    if (n <= 0) return;
-    if (group < 0) {
+__device__ __forceinline__ Some<T, N> bias_of(const GemmArgs& a, int group, int j) {
+    if (!a.bias || group < 0 || j >= a.j) return Some<T, N>{};
+    return load_some<T, N>((const T*)a.bias + (uint64_t)group * a.j + j, a.j - j);
+}
+// z, residual and out: of the first of the N columns; n: how many there are.
+template <typename T, int N>
+__device__ __forceinline__ void finish(const GemmArgs& a, int group, int n, float (&v)[N],
+                                       const Some<T, N>& bias, const Some<T, N>& residual, T* z, void* out) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = 0.0f;
-    } else if (a.bias) {
-        const Some<T, N> b = load_some<T, N>((const T*)a.bias + (uint64_t)group * a.j + j, n);
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] += (float)b.e[e];
-    }
-    if (a.z) store_some<T, N>((T*)a.z + (uint64_t)i * a.z_ld + j, n, v);
+    for (int e = 0; e < N; ++e) v[e] = group < 0 ? 0.0f : v[e] + (float)bias.e[e];
+    if (a.z) store_some<T, N>(z, n, v);
     if (group >= 0) {
-        if (a.act != RR_ACT_NONE)
+        if (a.act != RR_ACT_NONE) act_values(a.act, v);
+        if (a.residual)
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[e] = act_value(a.act, v[e]);
-        if (a.residual) {
-            const Some<T, N> r = load_some<T, N>((const T*)a.residual + (uint64_t)i * a.residual_ld + j, n);
-#pragma unroll
-            for (int e = 0; e < N; ++e) v[e] += (float)r.e[e];
-        }
+            for (int e = 0; e < N; ++e) v[e] += (float)residual.e[e];
     }
-    const uint64_t at = (a.out_group ? (uint64_t)group * a.out_group : 0) + (uint64_t)i * a.out_ld + j;
     if (a.wide_out)
-        store_wide<N>((float*)a.out + at, n, v);
+        store_wide<N>((float*)out, n, v);
     else
-        store_some<T, N>((T*)a.out + at, n, v);
+        store_some<T, N>((T*)out, n, v);
+}
+template <typename T, int N>
+__device__ __forceinline__ void finish(const GemmArgs& a, int group, int i, int j, float (&v)[N]) {
+    if (j >= a.j) return;
+    Some<T, N> r = {};
+    if (a.residual && group >= 0)
+        r = load_some<T, N>((const T*)a.residual + (uint64_t)i * a.residual_ld + j, a.j - j);
+    const uint64_t at = (a.out_group ? (uint64_t)group * a.out_group : 0) + (uint64_t)i * a.out_ld + j;
+    finish<T, N>(a, group, a.j - j, v, bias_of<T, N>(a, group, j), r,
+                 (T*)a.z + (uint64_t)i * a.z_ld + j, (char*)a.out + at * (a.wide_out ? 4 : sizeof(T)));
 }
 
 // ------------------------------------------------------------- where a tile is --
@@ -354,29 +411,29 @@ struct Spot {
     int i0, i_end, c0, c_end, j0, split;
 };
 
-// Workgroup id -> tile.  Workgroups go to the 8 XCDs in turn, each with an L2 of its
-// own: every XCD takes one stretch of the tiles, and a stretch goes through 8 rows of
-// tiles column by column, so that the tiles in flight on an XCD share operands.
+// Workgroup -> tile.  Workgroups go to the 8 XCDs in turn, each with an L2 of its own:
+// every XCD takes one stretch of the tiles, and a stretch goes through 8 rows of tiles column by column, so that the tiles in
+// flight on an XCD share operands.
 template <bool BY_ROWS, int TI, int TJ>
-__device__ __forceinline__ bool find_spot(const GemmArgs& a, Spot& s) {
-    const unsigned total = (unsigned)a.tiles_i * (unsigned)a.tiles_j;
-    const unsigned id = blockIdx.x, xcd = id & 7, each = total >> 3, more = total & 7;
+__device__ __forceinline__ bool find_spot(const GemmArgs& a, unsigned tiles_i, unsigned number, Spot& s) {
+    const unsigned tiles = tiles_i * (unsigned)a.tiles_j, outer = number / tiles, id = number % tiles;
+    const unsigned xcd = id & 7, each = tiles >> 3, more = tiles & 7;
     const unsigned at = xcd * each + min(xcd, more) + (id >> 3);
     const unsigned tall = 8u * (unsigned)a.tiles_j, first = at / tall * 8u;
-    const unsigned high = min(8u, (unsigned)a.tiles_i - first), in = at % tall;
+    const unsigned high = min(8u, tiles_i - first), in = at % tall;
     const int ti = (int)(first + in % high);
     s.j0 = (int)(in / high) * TJ;
     int c_lo, c_hi;
     if constexpr (BY_ROWS) {
+        s.split = (int)outer;
         if (!find_tile(a, ti, TI, s.g)) return false;
-        s.split = (int)blockIdx.y;
         s.i0 = s.g.lo;
         s.i_end = s.g.hi;
         c_lo = 0;
         c_hi = s.g.group < 0 ? 0 : a.c;
     } else {
-        s.split = (int)blockIdx.z;
-        s.g = range_of(a, (int)blockIdx.y + 1);
+        s.split = (int)(outer / (unsigned)a.groups);
+        s.g = range_of(a, (int)(outer % (unsigned)a.groups) + 1);
         s.i0 = ti * TI;
         s.i_end = a.i;
         c_lo = s.g.lo;
@@ -408,32 +465,83 @@ template <typename T, bool BY_ROWS, int TI, int TJ, int WI, int WJ, int FI, int 
 __device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, BLK_LDS char* room,
                                           const f32x4 (&acc)[FI][FJ]) {
     constexpr int THREADS = 64 * WI * WJ, LINE = TJ + 4, ROWS = 16 * WI, GROUPS = TJ / 8;
-    constexpr int BUFFER = ROWS * LINE;
+    constexpr int BUFFER = ROWS * LINE, EACH = ROWS * GROUPS / THREADS;
+    static_assert(THREADS % GROUPS == 0, "a thread keeps its columns");
     BLK_LDS float* const store = (BLK_LDS float*)room;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (a.splits > 1 && s.g.group < 0) return;        // join_kernel knows
-    __syncthreads();                                  // the operands' tiles are not read any more
+    const int thread = here(), lane = thread & 63, wave = thread >> 6;
+    const bool whole = a.splits == 1, add = whole && a.residual && s.g.group >= 0;
+    if (!whole && s.g.group < 0) return;        // join_kernel knows
+    const int col = thread % GROUPS * 8, n = a.j - s.j0 - col;
+    // A matrix's rows: those of block row 0 by 32-bit offsets from the tile's corner, and 16
+    // rows on for each block row (rows are at most 2^22 elements apart).
+    const uint64_t corner_out = (a.out_group && whole ? (uint64_t)s.g.group * a.out_group : 0);
+    const uint32_t wide = whole && !a.wide_out ? sizeof(T) : 4;
+    const uint64_t out_ld = whole ? a.out_ld : (uint64_t)a.j;
+    const uint64_t part_row = BY_ROWS ? (uint64_t)s.i0 : (uint64_t)s.g.group * a.i + s.i0;
+    const char* out = whole ? (const char*)a.out + (corner_out + (uint64_t)s.i0 * out_ld + s.j0) * wide
+                            : (const char*)(a.part + (uint64_t)s.split * a.part_stride + part_row * out_ld + s.j0);
+    const char* z = (const char*)a.z + ((uint64_t)s.i0 * a.z_ld + s.j0) * sizeof(T);
+    const char* res = (const char*)a.residual + ((uint64_t)s.i0 * a.residual_ld + s.j0) * sizeof(T);
+    out = uniform(out);
+    z = uniform(z);
+    res = uniform(res);
+    uint32_t at_out[EACH], at_z[EACH], at_res[EACH];
+    int left[EACH];                                   // rows from this one to the tile's end
 #pragma unroll
+    for (int t = 0; t < EACH; ++t) {
+        const int r = t * (THREADS / GROUPS) + thread / GROUPS;
+        const uint32_t row = r / 16 * (TI / WI) + r % 16;
+        at_out[t] = (row * (uint32_t)out_ld + col) * wide;
+        at_z[t] = (row * (uint32_t)a.z_ld + col) * (uint32_t)sizeof(T);
+        at_res[t] = (row * (uint32_t)a.residual_ld + col) * (uint32_t)sizeof(T);
+        left[t] = n > 0 ? s.i_end - s.i0 - (int)row : 0;
+    }
+    const Some<T, 8> bias = whole && n >= 8 ? bias_of<T, 8>(a, s.g.group, s.j0 + col) : Some<T, 8>{};
+    Some<T, 8> residual[EACH] = {}, later[EACH] = {};
+    const auto fetch = [&](Some<T, 8> (&to)[EACH], int x) {
+        const char* from = res + (uint64_t)(x * 16) * a.residual_ld * sizeof(T);
+#pragma unroll
+        for (int t = 0; t < EACH; ++t)
+            if (x * 16 < left[t] && n >= 8) to[t] = load_some<T, 8>((const T*)(from + at_res[t]), 8);
+    };
+    if (add) fetch(residual, 0);
     for (int x = 0; x < FI; ++x) {
         BLK_LDS float* const buf = store + (x & 1) * BUFFER;
         BLK_LDS float* const mine = buf + (wave / WJ * 16 + (lane & 15)) * LINE + wave % WJ * (TJ / WJ) + (lane >> 4) * 4;
+        if (add && x + 1 < FI) fetch(later, x + 1);
 #pragma unroll
-        for (int y = 0; y < FJ; ++y) *(BLK_LDS f32x4*)(mine + y * 16) = acc[x][y];
+        for (int u = 0; u < FI; ++u)
+            if (u == x)
+#pragma unroll
+                for (int y = 0; y < FJ; ++y) *(BLK_LDS f32x4*)(mine + y * 16) = acc[u][y];
         __syncthreads();
+        char* const to = (char*)out + (uint64_t)(x * 16) * out_ld * wide;
+        const char* const to_z = z + (uint64_t)(x * 16) * a.z_ld * sizeof(T);
 #pragma unroll
-        for (int t = 0; t < ROWS * GROUPS / THREADS; ++t) {
-            const int id = t * THREADS + (int)threadIdx.x, r = id / GROUPS, col = id % GROUPS * 8;
-            const int i = s.i0 + r / 16 * (TI / WI) + x * 16 + r % 16, j = s.j0 + col;
-            const f32x4 lo = *(BLK_LDS f32x4*)(buf + r * LINE + col), hi = *(BLK_LDS f32x4*)(buf + r * LINE + col + 4);
-            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            if (i >= s.i_end || j >= a.j) continue;
-            if (a.splits > 1) {
-                const uint64_t row = BY_ROWS ? (uint64_t)i : (uint64_t)s.g.group * a.i + i;
-                store_wide<8>(a.part + (uint64_t)s.split * a.part_stride + row * a.j + j, a.j - j, v);
+        for (int t = 0; t < EACH; ++t) {
+            const BLK_LDS float* const from = buf + (t * (THREADS / GROUPS) + thread / GROUPS) * LINE + col;
+            if (x * 16 >= left[t]) continue;
+            if (n >= 8) {
+                const f32x4 lo = *(const BLK_LDS f32x4*)from, hi = *(const BLK_LDS f32x4*)(from + 4);
+                float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                if (whole)
+                    finish<T, 8>(a, s.g.group, 8, v, bias, residual[t], (T*)(to_z + at_z[t]), to + at_out[t]);
+                else
+                    store_wide<8>((float*)(to + at_out[t]), 8, v);
             } else {
-                finish<T, 8>(a, s.g.group, i, j, v);
+                const int i = s.i0 + (int)((t * (THREADS / GROUPS) + thread / GROUPS) / 16 * (TI / WI)) + x * 16 +
+                              (t * (THREADS / GROUPS) + thread / GROUPS) % 16;
+                for (int e = 0; e < n; ++e) {
+                    float v[1] = {from[e]};
+                    if (whole)
+                        finish<T, 1>(a, s.g.group, i, s.j0 + col + e, v);
+                    else
+                        ((float*)(to + at_out[t]))[e] = v[0];
+                }
             }
         }
+#pragma unroll
+        for (int t = 0; t < EACH; ++t) residual[t] = later[t];
     }
 }
 
@@ -448,38 +556,32 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a)
     typedef typename Mma<T>::V V;
     constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16;
     constexpr int PB = Tile<PA, TI>::kBytes, QB = Tile<QA, TJ>::kBytes;
-    __shared__ __align__(1024) char lds[2 * (PB + QB)];
+    constexpr uint32_t STAGE = PB + QB;              // a power of two, and of the tiles' places its own bit
+    constexpr uint32_t OUT = 2 * 16 * WI * (TJ + 4) * 4;   // write_out's place
+    __shared__ __align__(2 * STAGE) char lds[OUT > 2 * STAGE ? OUT : 2 * STAGE];
     BLK_LDS char* const room = (BLK_LDS char*)lds;
+    const unsigned tiles_i = BY_ROWS ? (unsigned)count_tiles(a, TI) : (unsigned)a.tiles_i;
+    const unsigned total = tiles_i * (unsigned)a.tiles_j * (unsigned)a.splits * (BY_ROWS ? 1u : (unsigned)a.groups);
     Spot s;
-    if (!find_spot<BY_ROWS, TI, TJ>(a, s)) return;
-    const T* p = (const T*)a.p;
-    const T* q = (const T*)a.q + (BY_ROWS && s.g.group > 0 ? (uint64_t)s.g.group * a.q_group : 0);
+    if (blockIdx.x >= total || !find_spot<BY_ROWS, TI, TJ>(a, tiles_i, blockIdx.x, s)) return;
+    const T* const p = (const T*)a.p;
+    const T* const q = (const T*)a.q + (BY_ROWS && s.g.group > 0 ? (uint64_t)s.g.group * a.q_group : 0);
     const int wave = threadIdx.x >> 6, wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
+    Reader<PA, TI> rp;
+    Reader<QA, TJ> rq;
+    const uint32_t first = (uint32_t)(uintptr_t)room;
+    rp.start(first, wi);
+    rq.start(first + PB, wj);
     f32x4 acc[FI][FJ];
 #pragma unroll
     for (int x = 0; x < FI; ++x)
 #pragma unroll
         for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    [[maybe_unused]] const auto multiply = [&](const BLK_LDS char* tile) {
-#pragma unroll
-        for (int k = 0; k < kDepth; k += 32) {
-            V fp[FI], fq[FJ];
-#pragma unroll
-            for (int y = 0; y < FJ; ++y)
-                fq[y] = Tile<QA, TJ>::template fragment<V>(tile + PB, wj + y * 16, k);
-#pragma unroll
-            for (int x = 0; x < FI; ++x)
-                fp[x] = Tile<PA, TI>::template fragment<V>(tile, wi + x * 16, k);
-#pragma unroll
-            for (int x = 0; x < FI; ++x)
-#pragma unroll
-                for (int y = 0; y < FJ; ++y) acc[x][y] = Mma<T>::run(fq[y], fp[x], acc[x][y]);
-        }
-    };
+    uint32_t stage = 0;
     if constexpr (DIRECT) {
         // Half a tile (32 deep) is multiplied from registers while the next half is read into
-        // others, block row by block row; behind the barrier in the middle of a tile the next
-        // tile has arrived and the loads of the one after it follow into the place just read.
+        // others; behind the barrier in the middle of a tile the next tile has arrived and the
+        // loads of the one after it follow into the place just read.
         typedef Direct<T, PA, TI, THREADS> DP;
         typedef Direct<T, QA, TJ, THREADS> DQ;
         constexpr int PIECES = DP::kPieces + DQ::kPieces;
@@ -494,13 +596,23 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a)
                 else lq.piece(k - DP::kPieces);
         };
         V fp[2][FI], fq[2][FJ];
-        const auto half = [&](auto now_, const BLK_LDS char* tile, int k, bool more) {
-            constexpr int now = decltype(now_)::value, then = now ^ 1;
+        // reads of the other half in the first part of the block rows, so that they are done
+        // when the last ones are
+        constexpr int READS = FI / 2;
+        const auto read = [&](int half, int x) {
+#pragma unroll
+            for (int y = x * FJ / READS; y < (x + 1) * FJ / READS; ++y) fq[half][y] = rq.template fragment<V>(y, half);
+#pragma unroll
+            for (int r = x * FI / READS; r < (x + 1) * FI / READS; ++r) fp[half][r] = rp.template fragment<V>(r, half);
+        };
+        const auto multiply = [&](auto now_) {
+            constexpr int now = decltype(now_)::value;
+            __builtin_amdgcn_s_setprio(now);     // loads and first reads behind the barrier go first
 #pragma unroll
             for (int x = 0; x < FI; ++x) {
-                if (now == 1 && more) load(x * PIECES / FI, (x + 1) * PIECES / FI);
-                if (x < FJ) fq[then][x] = Tile<QA, TJ>::template fragment<V>(tile + PB, wj + x * 16, k);
-                fp[then][x] = Tile<PA, TI>::template fragment<V>(tile, wi + x * 16, k);
+                if (now == 1) load(x * PIECES / FI, (x + 1) * PIECES / FI);
+                if (x < READS) read(now ^ 1, x);
+                if (now == 1 && x == FI / 2) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
                 for (int y = 0; y < FJ; ++y) acc[x][y] = Mma<T>::run(fq[now][y], fp[now][x], acc[x][y]);
                 __builtin_amdgcn_sched_barrier(0);
@@ -508,51 +620,60 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a)
         };
         const int tiles = (s.c_end - s.c0 + kDepth - 1) / kDepth;
         if (tiles > 0) {
-            lp.aim(room, s.c0);
-            lq.aim(room + PB, s.c0);
+            lp.aim(first);
+            lq.aim(first + PB);
             load(0, PIECES);
-            arrived();
-            if (tiles > 1) {
-                lp.aim(room + PB + QB, s.c0 + kDepth);
-                lq.aim(room + PB + QB + PB, s.c0 + kDepth);
-                load(0, PIECES);
-            }
+            lp.aim(first + STAGE);
+            lq.aim(first + STAGE + PB);
+            load(0, PIECES);
+            arrived<PIECES>();
 #pragma unroll
-            for (int y = 0; y < FJ; ++y) fq[0][y] = Tile<QA, TJ>::template fragment<V>(room + PB, wj + y * 16, 0);
-#pragma unroll
-            for (int x = 0; x < FI; ++x) fp[0][x] = Tile<PA, TI>::template fragment<V>(room, wi + x * 16, 0);
+            for (int x = 0; x < READS; ++x) read(0, x);
         }
         for (int t = 0; t < tiles; ++t) {
-            BLK_LDS char* const tile = room + (t & 1) * (PB + QB);
-            BLK_LDS char* const next = room + (~t & 1) * (PB + QB);
-            half(Int<0>(), tile, 32, false);
-            arrived();
-            const bool more = t + 2 < tiles;
-            if (more) {
-                lp.aim(tile, s.c0 + (t + 2) * kDepth);
-                lq.aim(tile + PB, s.c0 + (t + 2) * kDepth);
-            }
-            half(Int<1>(), next, 0, more);
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // the reads of half 0, before new ones
+            multiply(Int<0>());
+            arrived<0>();
+            lp.aim(first + stage);
+            lq.aim(first + stage + PB);
+            stage ^= STAGE;
+            rp.other(STAGE);
+            rq.other(STAGE);
+            multiply(Int<1>());
         }
+        arrived<0>();                            // the zeros past the end as well
     } else {
-        Staged<T, PA, TI, THREADS> lp;
-        Staged<T, QA, TJ, THREADS> lq;
-        lp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
-        lq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
-        lp.load(s.c0);
-        lq.load(s.c0);
-        int stage = 0;
-        for (int c = s.c0; c < s.c_end; c += kDepth, stage ^= 1) {
-            BLK_LDS char* tile = room + stage * (PB + QB);
-            lp.store(tile);
-            lq.store(tile + PB);
+        Staged<T, PA, TI, THREADS> gp;
+        Staged<T, QA, TJ, THREADS> gq;
+        gp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
+        gq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
+        gp.load(s.c0);
+        gq.load(s.c0);
+        for (int c = s.c0; c < s.c_end; c += kDepth) {
+            gp.store(room + stage);
+            gq.store(room + stage + PB);
             __syncthreads();
             if (c + kDepth < s.c_end) {
-                lp.load(c + kDepth);
-                lq.load(c + kDepth);
+                gp.load(c + kDepth);
+                gq.load(c + kDepth);
             }
-            multiply(tile);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                V fp[FI], fq[FJ];
+#pragma unroll
+                for (int y = 0; y < FJ; ++y) fq[y] = rq.template fragment<V>(y, h);
+#pragma unroll
+                for (int x = 0; x < FI; ++x) fp[x] = rp.template fragment<V>(x, h);
+#pragma unroll
+                for (int x = 0; x < FI; ++x)
+#pragma unroll
+                    for (int y = 0; y < FJ; ++y) acc[x][y] = Mma<T>::run(fq[y], fp[x], acc[x][y]);
+            }
+            stage ^= STAGE;
+            rp.other(STAGE);
+            rq.other(STAGE);
         }
+        __syncthreads();
     }
     write_out<T, BY_ROWS, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
 }
@@ -713,8 +834,7 @@ template <typename T> __global__ void __launch_bounds__(256) join_kernel(const G
 
 template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int WI, int WJ, bool DIRECT>
 static void launch_tile(const GemmArgs& a, hipStream_t s) {
-    const unsigned tiles = (unsigned)a.tiles_i * (unsigned)a.tiles_j;
-    const dim3 grid = BY_ROWS ? dim3(tiles, (unsigned)a.splits) : dim3(tiles, (unsigned)a.groups, (unsigned)a.splits);
+    const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits * (BY_ROWS ? 1u : (unsigned)a.groups);
     gemm_kernel<T, PA, QA, BY_ROWS, TI, TI, WI, WJ, DIRECT><<<grid, 64 * WI * WJ, 0, s>>>(a);
 }
 

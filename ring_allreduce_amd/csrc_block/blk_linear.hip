@@ -32,13 +32,17 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a) {
     for (int r = lo; r < hi; ++r) {
         const Vec<T> d = load_vec((const T*)a.dout + (uint64_t)r * a.dout_ld, col, a.n);
         Vec<T> o;
+        float v[8];
         if (a.act != RR_ACT_NONE) {
             const Vec<T> z = load_vec((const T*)a.z + (uint64_t)r * a.z_ld, col, a.n);
 #pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (float)z.e[e];
+            act_slopes(a.act, v);
+#pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float v = (float)d.e[e] * act_slope(a.act, (float)z.e[e]);
-                sum[e] += v;
-                o.e[e] = (T)v;
+                v[e] *= (float)d.e[e];
+                sum[e] += v[e];
+                o.e[e] = (T)v[e];
             }
         } else {
 #pragma unroll
@@ -103,7 +107,7 @@ static rr_status_t check_grad(const rr_linear_t* a, const rr_linear_grad_t* g) {
         return RR_ERR_INVALID;
     if (a->act != RR_ACT_NONE && !rows_ok(a->z, a->rows, a->n, 2)) return RR_ERR_INVALID;
     if (!aligned_to(g->dw, type_bytes(g->dw_dt)) || !aligned_to(g->db, 4)) return RR_ERR_INVALID;
-    if (g->dout.ld > kMaxLd || (a->act != RR_ACT_NONE && a->n > kMaxLd)) return RR_ERR_UNSUPPORTED;
+    if (g->dout.ld > kMaxLd || (g->dx.data && g->dx.ld > kMaxLd) || (a->act != RR_ACT_NONE && a->n > kMaxLd)) return RR_ERR_UNSUPPORTED;
     return RR_OK;
 }
 
@@ -182,7 +186,8 @@ static rr_status_t run_gemm(GemmArgs k, const rr_linear_t* a, int form, void* wo
     const uint64_t ti = form == kByW ? ceil_div(k.i, tile_rows(p.tile)) : row_tiles(a, tile_rows(p.tile));
     const uint64_t tj = ceil_div(k.j, tile_cols(p.tile));
     if (ti * tj == 0) return RR_OK;
-    if (ti * tj > (1u << 22)) return RR_ERR_UNSUPPORTED;
+    if (ti * tj * splits * (form == kByW ? (uint64_t)a->groups : 1) > (1u << 23) - 1)
+        return RR_ERR_UNSUPPORTED;
     k.tiles_i = (int32_t)ti;
     k.tiles_j = (int32_t)tj;
     k.splits = splits;
@@ -239,6 +244,8 @@ rr_status_t block_linear(const rr_linear_t* a, void* workspace, size_t workspace
     if (!rows_ok(a->out, a->rows, a->n, 2) || !rows_ok_if(a->residual, a->rows, a->n, 2) ||
         !aligned_to(a->bias, 2))
         return RR_ERR_INVALID;
+    if (a->out.ld > kMaxLd || (a->residual.data && a->residual.ld > kMaxLd) || (a->z.data && a->z.ld > kMaxLd))
+        return RR_ERR_UNSUPPORTED;
     const uint64_t wide = extent(a->groups, a->w_stride, extent(a->n, a->w_ld, a->k, 1), 2);
     const uint64_t n_out = extent(a->rows, a->out.ld, a->n, 2), n_z = extent(a->rows, a->z.ld, a->n, 2);
     const uint64_t n_res = extent(a->rows, a->residual.ld, a->n, 2);

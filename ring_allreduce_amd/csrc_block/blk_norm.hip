@@ -24,6 +24,13 @@ struct NormArgs {
     int32_t at_pre, at_post, at_gate;  // their places among the sums, or -1
 };
 
+__device__ __forceinline__ float gate_value(int act, float z) {
+    return act == RR_ACT_SIGMOID ? logistic(z) : act == RR_ACT_SILU ? z * logistic(z) : z;
+}
+__device__ __forceinline__ float gate_slope(int act, float z) {
+    return act == RR_ACT_SIGMOID ? slope_of<RR_ACT_SIGMOID>(z) : act == RR_ACT_SILU ? slope_of<RR_ACT_SILU>(z) : 1.0f;
+}
+
 // Where the columns of a row lie: thread g of G holds NV vectors, vector v at column
 // (v * G + g) * N, so that every access of a wave is one stretch of the row.
 template <typename T, int G, int NV> struct Row {
@@ -129,8 +136,8 @@ __global__ void __launch_bounds__(Shape<G>::block) norm_kernel(const NormArgs a)
                 h[v][i] = a.residual_scale * (float)x[v].e[i];
                 if (a.branch) {
                     float n = (float)u[v].e[i] * r * wp[v][i];
-                    if (a.gate_kind == RR_GATE_ELEMENT) n *= act_value(a.gate_act, (float)g[v].e[i]);
-                    if (a.gate_kind == RR_GATE_CHANNEL) n *= act_value(a.gate_act, wg[v][i]);
+                    if (a.gate_kind == RR_GATE_ELEMENT) n *= gate_value(a.gate_act, (float)g[v].e[i]);
+                    if (a.gate_kind == RR_GATE_CHANNEL) n *= gate_value(a.gate_act, wg[v][i]);
                     h[v][i] = fmaf(a.branch_scale, n, h[v][i]);
                 }
                 if (R::column(v) + i >= len) h[v][i] = 0.0f;
@@ -225,10 +232,10 @@ __global__ void __launch_bounds__(Shape<G>::block) norm_backward_kernel(const No
                 const float unit = (float)u[v].e[i] * r;
                 if (a.gate_kind != RR_GATE_NONE) {
                     const float z = a.gate_kind == RR_GATE_ELEMENT ? (float)g[v].e[i] : wg[v][i];
-                    const float dg = e * unit * wp[v][i] * act_slope(a.gate_act, z);
+                    const float dg = e * unit * wp[v][i] * gate_slope(a.gate_act, z);
                     g[v].e[i] = (T)dg;
                     sum_gate[v][i] += dg;
-                    e *= act_value(a.gate_act, z);
+                    e *= gate_value(a.gate_act, z);
                 }
                 sum_post[v][i] = fmaf(e, unit, sum_post[v][i]);
                 m[v][i] = e * wp[v][i];
