@@ -47,7 +47,7 @@ struct GemmArgs {
 // What the host chose for one product; see blk_linear.hip.
 struct GemmPlan {
     int32_t form, tile;
-    int32_t direct;                  // operands straight from memory into LDS
+    int32_t direct;                  // kStream*: rows of both operands at 16-byte boundaries
 };
 
 rr_status_t launch_gemm_bf16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
@@ -215,44 +215,6 @@ __device__ __forceinline__ const char* uniform(const char* p) {
     const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
     return (const char*)((uint64_t)hi << 32 | lo);
 }
-
-// Loads of one operand's tile through registers: any alignment, any size; what lies
-// outside [row, row_end) x [c, c_end) is zero.
-template <typename T, bool ACROSS, int ROWS, int THREADS> struct Staged {
-    static constexpr int kPieces = ROWS * kDepth / 8 / THREADS;
-    const T* base;
-    uint64_t ld;
-    int row, row_end, c_end;
-    u32x4 r[kPieces];
-    __device__ __forceinline__ void start(const T* b, uint64_t stride, int r0, int r_end, int, int end) {
-        base = b;
-        ld = stride;
-        row = r0;
-        row_end = r_end;
-        c_end = end;
-    }
-    __device__ __forceinline__ void load(int c0) {
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            int y, x;
-            Tile<ACROSS, ROWS>::place(k * THREADS + (int)threadIdx.x, y, x);
-            y += row;
-            x += c0;
-            Vec<T> v;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v.e[e] = (T)0.0f;
-            if (y < row_end && x < c_end)
-                v = ACROSS ? load_vec(base + (uint64_t)x * ld, y, row_end)
-                           : load_vec(base + (uint64_t)y * ld, x, c_end);
-            r[k] = __builtin_bit_cast(u32x4, v);
-        }
-    }
-    __device__ __forceinline__ void store(BLK_LDS char* tile) const {
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k)
-            *(BLK_LDS u32x4*)(tile + (k * THREADS + (int)threadIdx.x) * 16) = r[k];
-    }
-};
 
 // Loads straight from memory into LDS, 16 bytes a lane, a wave 1 KiB of the tile at a
 // time; the permutation is on the side of the addresses read.  A piece outside the
@@ -551,7 +513,7 @@ template <int N> struct Int {
 
 // ------------------------------------------------------------------ the product --
 
-template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ, bool DIRECT>
+template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ>
 __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a) {
     typedef typename Mma<T>::V V;
     constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16;
@@ -578,103 +540,69 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a)
 #pragma unroll
         for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     uint32_t stage = 0;
-    if constexpr (DIRECT) {
-        // Half a tile (32 deep) is multiplied from registers while the next half is read into
-        // others; behind the barrier in the middle of a tile the next tile has arrived and the
-        // loads of the one after it follow into the place just read.
-        typedef Direct<T, PA, TI, THREADS> DP;
-        typedef Direct<T, QA, TJ, THREADS> DQ;
-        constexpr int PIECES = DP::kPieces + DQ::kPieces;
-        DP lp;
-        DQ lq;
-        lp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
-        lq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
-        const auto load = [&](int from, int to) {
+    // Half a tile (32 deep) is multiplied from registers while the next half is read into
+    // others; behind the barrier in the middle of a tile the next tile has arrived and the
+    // loads of the one after it follow into the place just read.
+    typedef Direct<T, PA, TI, THREADS> DP;
+    typedef Direct<T, QA, TJ, THREADS> DQ;
+    constexpr int PIECES = DP::kPieces + DQ::kPieces;
+    DP lp;
+    DQ lq;
+    lp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
+    lq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
+    const auto load = [&](int from, int to) {
 #pragma unroll
-            for (int k = from; k < to; ++k)
-                if (k < DP::kPieces) lp.piece(k);
-                else lq.piece(k - DP::kPieces);
-        };
-        V fp[2][FI], fq[2][FJ];
-        // reads of the other half in the first part of the block rows, so that they are done
-        // when the last ones are
-        constexpr int READS = FI / 2;
-        const auto read = [&](int half, int x) {
+        for (int k = from; k < to; ++k)
+            if (k < DP::kPieces) lp.piece(k);
+            else lq.piece(k - DP::kPieces);
+    };
+    V fp[2][FI], fq[2][FJ];
+    // reads of the other half in the first part of the block rows, so that they are done
+    // when the last ones are
+    constexpr int READS = FI / 2;
+    const auto read = [&](int half, int x) {
 #pragma unroll
-            for (int y = x * FJ / READS; y < (x + 1) * FJ / READS; ++y) fq[half][y] = rq.template fragment<V>(y, half);
+        for (int y = x * FJ / READS; y < (x + 1) * FJ / READS; ++y) fq[half][y] = rq.template fragment<V>(y, half);
 #pragma unroll
-            for (int r = x * FI / READS; r < (x + 1) * FI / READS; ++r) fp[half][r] = rp.template fragment<V>(r, half);
-        };
-        const auto multiply = [&](auto now_) {
-            constexpr int now = decltype(now_)::value;
-            __builtin_amdgcn_s_setprio(now);     // loads and first reads behind the barrier go first
+        for (int r = x * FI / READS; r < (x + 1) * FI / READS; ++r) fp[half][r] = rp.template fragment<V>(r, half);
+    };
+    const auto multiply = [&](auto now_) {
+        constexpr int now = decltype(now_)::value;
+        __builtin_amdgcn_s_setprio(now);     // loads and first reads behind the barrier go first
 #pragma unroll
-            for (int x = 0; x < FI; ++x) {
-                if (now == 1) load(x * PIECES / FI, (x + 1) * PIECES / FI);
-                if (x < READS) read(now ^ 1, x);
-                if (now == 1 && x == FI / 2) __builtin_amdgcn_s_setprio(0);
+        for (int x = 0; x < FI; ++x) {
+            if (now == 1) load(x * PIECES / FI, (x + 1) * PIECES / FI);
+            if (x < READS) read(now ^ 1, x);
+            if (now == 1 && x == FI / 2) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
-                for (int y = 0; y < FJ; ++y) acc[x][y] = Mma<T>::run(fq[now][y], fp[now][x], acc[x][y]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        };
-        const int tiles = (s.c_end - s.c0 + kDepth - 1) / kDepth;
-        if (tiles > 0) {
-            lp.aim(first);
-            lq.aim(first + PB);
-            load(0, PIECES);
-            lp.aim(first + STAGE);
-            lq.aim(first + STAGE + PB);
-            load(0, PIECES);
-            arrived<PIECES>();
-#pragma unroll
-            for (int x = 0; x < READS; ++x) read(0, x);
+            for (int y = 0; y < FJ; ++y) acc[x][y] = Mma<T>::run(fq[now][y], fp[now][x], acc[x][y]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        for (int t = 0; t < tiles; ++t) {
-            __builtin_amdgcn_s_waitcnt(0xC07F);  // the reads of half 0, before new ones
-            multiply(Int<0>());
-            arrived<0>();
-            lp.aim(first + stage);
-            lq.aim(first + stage + PB);
-            stage ^= STAGE;
-            rp.other(STAGE);
-            rq.other(STAGE);
-            multiply(Int<1>());
-        }
-        arrived<0>();                            // the zeros past the end as well
-    } else {
-        Staged<T, PA, TI, THREADS> gp;
-        Staged<T, QA, TJ, THREADS> gq;
-        gp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
-        gq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
-        gp.load(s.c0);
-        gq.load(s.c0);
-        for (int c = s.c0; c < s.c_end; c += kDepth) {
-            gp.store(room + stage);
-            gq.store(room + stage + PB);
-            __syncthreads();
-            if (c + kDepth < s.c_end) {
-                gp.load(c + kDepth);
-                gq.load(c + kDepth);
-            }
+    };
+    const int tiles = (s.c_end - s.c0 + kDepth - 1) / kDepth;
+    if (tiles > 0) {
+        lp.aim(first);
+        lq.aim(first + PB);
+        load(0, PIECES);
+        lp.aim(first + STAGE);
+        lq.aim(first + STAGE + PB);
+        load(0, PIECES);
+        arrived<PIECES>();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                V fp[FI], fq[FJ];
-#pragma unroll
-                for (int y = 0; y < FJ; ++y) fq[y] = rq.template fragment<V>(y, h);
-#pragma unroll
-                for (int x = 0; x < FI; ++x) fp[x] = rp.template fragment<V>(x, h);
-#pragma unroll
-                for (int x = 0; x < FI; ++x)
-#pragma unroll
-                    for (int y = 0; y < FJ; ++y) acc[x][y] = Mma<T>::run(fq[y], fp[x], acc[x][y]);
-            }
-            stage ^= STAGE;
-            rp.other(STAGE);
-            rq.other(STAGE);
-        }
-        __syncthreads();
+        for (int x = 0; x < READS; ++x) read(0, x);
     }
+    for (int t = 0; t < tiles; ++t) {
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // the reads of half 0, before new ones
+        multiply(Int<0>());
+        arrived<0>();
+        lp.aim(first + stage);
+        lq.aim(first + stage + PB);
+        stage ^= STAGE;
+        rp.other(STAGE);
+        rq.other(STAGE);
+        multiply(Int<1>());
+    }
+    arrived<0>();                            // the zeros past the end as well
     write_out<T, BY_ROWS, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
 }
 
@@ -741,7 +669,12 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArg
     const int i0 = __builtin_amdgcn_readfirstlane(g.lo), i_end = __builtin_amdgcn_readfirstlane(g.hi);
     const int j0 = (int)blockIdx.x * kStreamCols, lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int c_end = g.group < 0 ? 0 : a.c;
+    int c_lo = 0, c_end = g.group < 0 ? 0 : a.c;
+    if (a.splits > 1) {
+        const int each = ((a.c + kStreamDepth - 1) / kStreamDepth + a.splits - 1) / a.splits * kStreamDepth;
+        c_lo = (int)min((int64_t)blockIdx.z * each, (int64_t)c_end);
+        c_end = (int)min((int64_t)c_lo + each, (int64_t)c_end);
+    }
     Strip<T, FI, DIRECT> sp;
     Strip<T, FJ, DIRECT> sq;
     sp.start((const T*)a.p, a.p_ld, i0, i_end, c_end);
@@ -752,7 +685,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArg
 #pragma unroll
         for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     u32x4 vp[4][FI], vq[4][FJ];
-    int c = wave * kStreamDepth;
+    int c = c_lo + wave * kStreamDepth;
     if (c < c_end) {
         sq.load(vq, c);
         sp.load(vp, c);
@@ -790,8 +723,13 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArg
 #pragma unroll
         for (int w = 1; w < kStreamWaves; ++w) v += sums[w][f][lane];
         const int i = i0 + f / FJ * 16 + (lane & 15);
+        const int j = j0 + f % FJ * 16 + (lane >> 4) * 4;
         float o[4] = {v[0], v[1], v[2], v[3]};
-        if (i < i_end) finish<T, 4>(a, g.group, i, j0 + f % FJ * 16 + (lane >> 4) * 4, o);
+        if (i >= i_end || j >= a.j) continue;
+        if (a.splits == 1)
+            finish<T, 4>(a, g.group, i, j, o);
+        else if (g.group >= 0)
+            store_wide<4>(a.part + (uint64_t)blockIdx.z * a.part_stride + (uint64_t)i * a.j + j, a.j - j, o);
     }
 }
 
@@ -832,24 +770,17 @@ template <typename T> __global__ void __launch_bounds__(256) join_kernel(const G
 
 // -------------------------------------------------------------------- launching --
 
-template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int WI, int WJ, bool DIRECT>
-static void launch_tile(const GemmArgs& a, hipStream_t s) {
-    const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits * (BY_ROWS ? 1u : (unsigned)a.groups);
-    gemm_kernel<T, PA, QA, BY_ROWS, TI, TI, WI, WJ, DIRECT><<<grid, 64 * WI * WJ, 0, s>>>(a);
-}
-
 template <typename T, bool PA, bool QA, bool BY_ROWS>
 static void launch_form(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
-    if (p.tile == kTile256) launch_tile<T, PA, QA, BY_ROWS, 256, 2, 4, true>(a, s);
-    else if (p.tile == kTile128 && p.direct) launch_tile<T, PA, QA, BY_ROWS, 128, 2, 2, true>(a, s);
-    else if (p.tile == kTile128) launch_tile<T, PA, QA, BY_ROWS, 128, 2, 2, false>(a, s);
-    else if (p.direct) launch_tile<T, PA, QA, BY_ROWS, 64, 2, 2, true>(a, s);
-    else launch_tile<T, PA, QA, BY_ROWS, 64, 2, 2, false>(a, s);
+    const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits * (BY_ROWS ? 1u : (unsigned)a.groups);
+    if (p.tile == kTile256) gemm_kernel<T, PA, QA, BY_ROWS, 256, 256, 2, 4><<<grid, 512, 0, s>>>(a);
+    else if (p.tile == kTile128) gemm_kernel<T, PA, QA, BY_ROWS, 128, 128, 2, 2><<<grid, 256, 0, s>>>(a);
+    else gemm_kernel<T, PA, QA, BY_ROWS, 64, 64, 2, 2><<<grid, 256, 0, s>>>(a);
 }
 
 template <typename T> static rr_status_t launch_gemm(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
     if (p.tile >= kStream16) {
-        const dim3 grid((unsigned)a.tiles_j, (unsigned)a.tiles_i);
+        const dim3 grid((unsigned)a.tiles_j, (unsigned)a.tiles_i, (unsigned)a.splits);
         const int threads = 64 * kStreamWaves;
         if (p.direct) {
             if (p.tile == kStream16) stream_kernel<T, 1, true><<<grid, threads, 0, s>>>(a);
@@ -860,11 +791,13 @@ template <typename T> static rr_status_t launch_gemm(const GemmArgs& a, const Ge
             else if (p.tile == kStream32) stream_kernel<T, 2, false><<<grid, threads, 0, s>>>(a);
             else stream_kernel<T, 4, false><<<grid, threads, 0, s>>>(a);
         }
-        return launched();
+    } else if (p.form == kForward) {
+        launch_form<T, false, false, true>(a, p, s);
+    } else if (p.form == kByX) {
+        launch_form<T, false, true, true>(a, p, s);
+    } else {
+        launch_form<T, true, true, false>(a, p, s);
     }
-    if (p.form == kForward) launch_form<T, false, false, true>(a, p, s);
-    else if (p.form == kByX) launch_form<T, false, true, true>(a, p, s);
-    else launch_form<T, true, true, false>(a, p, s);
     const rr_status_t st = launched();
     if (st != RR_OK || a.splits == 1) return st;
     const bool by_rows = p.form != kByW;

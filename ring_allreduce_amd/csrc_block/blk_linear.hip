@@ -7,8 +7,9 @@ namespace blk {
 
 // ------------------------------------------------------- activation's gradient --
 //
-// dz = dout act'(z), rounded to the rows' type as the next products' operand, and the
-// column sums of each group in 32 bits.  A workgroup takes 8 columns a thread and one
+// dz = dout act'(z), rounded to the rows' type as the next products' operand (or dout as
+// it is, where its rows cannot be loaded in 16-byte pieces), and the column sums of each
+// group in 32 bits.  A workgroup takes 8 columns a thread and one
 // of `splits` parts of a group's rows; the parts are added in a fixed order.
 struct SlopeArgs {
     GemmArgs g;            // rows, groups, offsets
@@ -45,10 +46,12 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a) {
                 o.e[e] = (T)v[e];
             }
         } else {
+            o = d;
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] += (float)d.e[e];
         }
-        if (a.dz) store_vec((T*)a.dz + (uint64_t)r * a.dz_ld, col, a.n, o);
+        // to the last whole vector: zeros follow the row
+        if (a.dz) store_vec((T*)a.dz + (uint64_t)r * a.dz_ld, col, (int)a.dz_ld, o);
     }
     if (!a.part) return;
     float* to = a.part + ((uint64_t)blockIdx.z * a.splits + blockIdx.y) * a.n;
@@ -65,6 +68,36 @@ slope_parts_kernel(const float* part, int splits, int n, float* db) {
     float sum = 0.0f;
     for (int s = 0; s < splits; ++s) sum += from[(uint64_t)s * n];
     db[(uint64_t)blockIdx.y * n + col] = sum;
+}
+
+// ------------------------------------------------------------------- alignment --
+//
+// The products load whole 16-byte pieces, so a matrix whose rows are not made of them is
+// copied to one whose rows are, filled up with zeros.  Loading such rows as they are, through
+// registers, took 122 us for 6016 x 1111 x 1777 where the copies and the aligned product
+// take 66.
+struct PackPart {
+    const void* from;
+    void* to;
+    uint64_t ld, group;    // group: elements from one group's first row to the next
+    uint64_t vectors;
+    int32_t rows, width, wide;   // rows of a group; wide: the copy's row length
+};
+struct PackArgs {
+    PackPart part[2];      // both operands in one launch
+};
+
+__global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
+    const PackPart& m = a.part[blockIdx.y];
+    const unsigned each = (unsigned)m.wide / 8;
+    for (uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x; id < m.vectors; id += (uint64_t)gridDim.x * 256) {
+        const uint64_t row = m.vectors >> 32 ? id / each : (uint32_t)id / each;
+        const int at = (int)(id - row * each) * 8;
+        const uint32_t group = (uint32_t)row / (uint32_t)m.rows;
+        const uint16_t* from = (const uint16_t*)m.from + group * m.group + (row - group * (uint64_t)m.rows) * m.ld;
+        const Some<uint16_t, 8> v = load_some<uint16_t, 8>(from + at, m.width - at);
+        *(u32x4*)((uint16_t*)m.to + id * 8) = __builtin_bit_cast(u32x4, v);
+    }
 }
 
 // ------------------------------------------------------------------ host side --
@@ -126,76 +159,154 @@ static uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
     return a->rows / height + a->groups + 2;
 }
 
-static bool good_operand(const void* p, uint64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
-
-// The kernel for one product: i x j outputs (i rows in all, or per group for dw), c deep.
-static GemmPlan choose(const rr_linear_t* a, int form, bool direct, int* splits) {
+// The kernel and the parts of the contraction for one product: the least of the times that
+// these figures give, taken from 290 products of 24 to 6016 rows and 256 to 8192 columns and
+// depths on an MI355X (microseconds; a step is 64 deep).
+//   tile       start   a step, with 1 .. 4 workgroups on each compute unit
+//   256 x 256    8     1.75 (1.4 on an empty device)
+//   128 x 128    6     0.75, 1.15
+//    64 x  64    4.5   0.37, 0.6, 0.7, 0.9
+// A further round costs half a start; parts cost 2.2 for the second launch and their bytes,
+// written and read.  A few rows go through the one-pass form instead, to 64 rows where the
+// contraction is too short for parts to pay (2048 x 1024: 8.6 us against 10.4 for 48 rows;
+// at 8192 deep 40 against 16).
+static GemmPlan choose(const rr_linear_t* a, int form, int* splits) {
     const uint64_t groups = (uint64_t)a->groups, mean = ceil_div(a->rows, groups);
     const uint64_t i = form == kByW ? a->n : a->rows, j = form == kForward ? a->n : a->k;
     const uint64_t c = form == kForward ? a->k : form == kByX ? a->n : mean;
-    GemmPlan p = {form, kTile64, direct};
+    const double outputs = (double)(form == kByW ? groups * i : i) * j;
+    GemmPlan p = {form, kTile64, 0};
     *splits = 1;
-    if (form == kForward && mean <= 64) {
+    if (form == kForward && (mean <= 16 || (mean <= 64 && c <= 1024))) {
         p.tile = mean <= 16 ? kStream16 : mean <= 32 ? kStream32 : kStream64;
+        const uint64_t blocks = ceil_div(j, kStreamCols) * ceil_div(a->rows, 16);
+        const uint64_t want = 256 / blocks, most = c / 1024;
+        const uint64_t n = want < most ? want : most;
+        *splits = n < 2 ? 1 : n > 16 ? 16 : (int)n;
         return p;
     }
-    const auto tiles = [&](uint64_t t) {
-        const uint64_t rows = form == kByW ? groups * ceil_div(i, t) : i / t + ceil_div(groups, 2) + (i % t != 0 && groups == 1);
-        return rows * ceil_div(j, t);
-    };
-    const uint64_t n64 = tiles(64), n128 = tiles(128), n256 = tiles(256);
-    double best = (double)ceil_div(n64, 1024) * 0.25 * 2.2;
-    const double by128 = (double)ceil_div(n128, 512) * 0.5 * 1.35, by256 = (double)ceil_div(n256, 256);
-    if (by128 <= best) {
-        best = by128;
-        p.tile = kTile128;
-    }
-    if (direct && by256 <= best) p.tile = kTile256;
-    const uint64_t n = p.tile == kTile64 ? n64 : p.tile == kTile128 ? n128 : n256;
-    if (n < 256 && p.tile != kTile256) {
-        const uint64_t want = 512 / (n ? n : 1), most = c / (4 * kDepth);
-        const uint64_t s = want < most ? want : most;
-        *splits = s < 2 ? 1 : s > 64 ? 64 : (int)s;
+    double best = 1e30;
+    for (int tile = kTile256; tile <= kTile64; ++tile) {
+        const uint64_t t = tile_rows(tile), slots = tile == kTile256 ? 1 : tile == kTile128 ? 2 : 4;
+        const uint64_t high = form == kByW ? groups * ceil_div(i, t)
+                              : groups == 1 ? ceil_div(i, t) : i / t + ceil_div(groups, 2);
+        const uint64_t tiles = (high ? high : 1) * ceil_div(j, t), steps = ceil_div(c, kDepth);
+        for (uint64_t s = 1; s <= 32 && (s == 1 || (s <= steps / 2 && tiles * s <= 1024)); s *= 2) {
+            const uint64_t blocks = tiles * s, rounds = ceil_div(blocks, 256 * slots);
+            const uint64_t load = rounds > 1 ? slots : ceil_div(blocks, 256);
+            const double fill = blocks < 256 ? blocks / 256.0 : 1.0;
+            const double start = tile == kTile256 ? 8 : tile == kTile128 ? 6 : 4.5;
+            const double step = tile == kTile256   ? 1.4 + 0.35 * fill
+                                : tile == kTile128 ? (load == 1 ? 0.6 + 0.3 * fill : 1.15)
+                                : load == 1 ? 0.36 + 0.05 * fill : load == 2 ? 0.6 : load == 3 ? 0.7 : 0.9;
+            double time = start * (0.5 + 0.5 * rounds) + rounds * step * ceil_div(steps, s);
+            if (s > 1) time += 2.2 + 8.0 * s * outputs / 4.5e6;
+            if (time < best) {
+                best = time;
+                p.tile = tile;
+                *splits = (int)s;
+            }
+        }
     }
     return p;
 }
 
-// Bytes of a product's parts, whatever the operands' alignment turns out to be.
-static uint64_t part_bytes(const rr_linear_t* a, int form) {
-    uint64_t most = 0;
-    for (int direct = 0; direct < 2; ++direct) {
-        int splits;
-        choose(a, form, direct != 0, &splits);
-        const uint64_t rows = form == kByW ? (uint64_t)a->groups * a->n : a->rows;
-        const uint64_t j = form == kForward ? a->n : a->k;
-        const uint64_t bytes = splits > 1 ? (uint64_t)splits * rows * j * sizeof(float) : 0;
-        if (bytes > most) most = bytes;
-    }
-    return ceil_div(most, 256) * 256;
+// An operand of 16-byte pieces: its rows start at them and, where the pieces lie along the
+// contraction, end at them too (past a row's end there may be anything).
+static bool good_rows(const rr_rows_t& r, uint64_t group, uint64_t width) {
+    return aligned_to(r.data, 16) && r.ld % 8 == 0 && group % 8 == 0 && width % 8 == 0;
 }
 
-// `a`: operands, sizes and epilogue are set; the rest follows from the plan.
-static rr_status_t run_gemm(GemmArgs k, const rr_linear_t* a, int form, void* workspace, hipStream_t s) {
-    bool direct = good_operand(k.p, k.p_ld) && good_operand(k.q, k.q_ld) && k.q_group % 8 == 0;
-    // the sizes along which 16 bytes are read
-    if (form == kForward) direct = direct && k.c % 8 == 0;
-    else if (form == kByX) direct = direct && k.c % 8 == 0 && k.j % 8 == 0;
-    else direct = direct && k.i % 8 == 0 && k.j % 8 == 0;
+struct Operand {
+    rr_rows_t rows;
+    uint64_t count, width, groups, group;  // rows of a group, row length, groups and their distance
+    bool good() const { return good_rows(rows, groups > 1 ? group : 0, width); }
+    uint64_t copy_bytes() const {
+        return ceil_div(groups * count * ceil_div(width, 8) * 16, 256) * 256;
+    }
+};
+
+// One product: `k` has the sizes and the epilogue.
+struct Product {
+    int form;
+    Operand p, q;
+    GemmArgs k;
+};
+
+static uint64_t product_bytes(const rr_linear_t* a, int form, const Operand& p, const Operand& q) {
     int splits;
-    const GemmPlan p = choose(a, form, direct, &splits);
-    const uint64_t ti = form == kByW ? ceil_div(k.i, tile_rows(p.tile)) : row_tiles(a, tile_rows(p.tile));
-    const uint64_t tj = ceil_div(k.j, tile_cols(p.tile));
+    const GemmPlan plan = choose(a, form, &splits);
+    uint64_t bytes = 0;
+    if (splits > 1) {
+        const uint64_t rows = form == kByW ? (uint64_t)a->groups * a->n : a->rows;
+        bytes = ceil_div((uint64_t)splits * rows * (form == kForward ? a->n : a->k) * sizeof(float), 256) * 256;
+    }
+    if (plan.tile < kStream16) bytes += (p.good() ? 0 : p.copy_bytes()) + (q.good() ? 0 : q.copy_bytes());
+    return bytes;
+}
+
+// Copies the operands that are not good into the scratch memory at `room`.
+static rr_status_t pack(Operand& p, Operand& q, char* room, hipStream_t s) {
+    PackArgs k = {};
+    int n = 0;
+    uint64_t blocks = 0;
+    for (Operand* o : {&p, &q}) {
+        if (o->good()) continue;
+        PackPart& m = k.part[n];
+        m = {o->rows.data, room, o->rows.ld, o->group, 0, (int32_t)o->count, (int32_t)o->width,
+             (int32_t)(ceil_div(o->width, 8) * 8)};
+        m.vectors = o->groups * o->count * (uint64_t)m.wide / 8;
+        if (o->groups * o->count > 0xFFFFFFFFull) return RR_ERR_UNSUPPORTED;
+        room += o->copy_bytes();
+        o->rows = {m.to, (uint64_t)m.wide};
+        o->width = (uint64_t)m.wide;
+        o->group = o->count * (uint64_t)m.wide;
+        if (m.vectors == 0) continue;
+        const uint64_t b = ceil_div(m.vectors, 256);
+        blocks = b > blocks ? b : blocks;
+        ++n;
+    }
+    if (n == 0) return RR_OK;
+    pack_kernel<<<dim3((unsigned)(blocks < 8192 ? blocks : 8192), (unsigned)n), 256, 0, s>>>(k);
+    return launched();
+}
+
+static rr_status_t run_product(const rr_linear_t* a, Product r, void* workspace, hipStream_t s) {
+    GemmArgs& k = r.k;
+    int splits;
+    GemmPlan plan = choose(a, r.form, &splits);
+    const uint64_t ti = r.form == kByW ? ceil_div(k.i, tile_rows(plan.tile)) : row_tiles(a, tile_rows(plan.tile));
+    const uint64_t tj = ceil_div(k.j, tile_cols(plan.tile));
     if (ti * tj == 0) return RR_OK;
-    if (ti * tj * splits * (form == kByW ? (uint64_t)a->groups : 1) > (1u << 23) - 1)
-        return RR_ERR_UNSUPPORTED;
+    if (ti * tj * splits * (r.form == kByW ? (uint64_t)a->groups : 1) > (1u << 23) - 1) return RR_ERR_UNSUPPORTED;
     k.tiles_i = (int32_t)ti;
     k.tiles_j = (int32_t)tj;
     k.splits = splits;
-    k.part = (float*)workspace;
-    k.part_stride = (form == kByW ? (uint64_t)k.groups * k.i : (uint64_t)k.rows) * k.j;
-    if (splits > 1 && ceil_div((k.part_stride / k.j) * ceil_div(k.j, 4), 256) > (1u << 24) - 1)
-        return RR_ERR_UNSUPPORTED;
-    return a->dt == RR_BF16 ? launch_gemm_bf16(k, p, s) : launch_gemm_f16(k, p, s);
+    k.part_stride = (r.form == kByW ? (uint64_t)k.groups * k.i : (uint64_t)k.rows) * k.j;
+    if (splits > 1) {
+        if (ceil_div((k.part_stride / k.j) * ceil_div(k.j, 4), 256) > (1u << 24) - 1) return RR_ERR_UNSUPPORTED;
+        k.part = (float*)workspace;
+    }
+    char* room = (char*)workspace;
+    if (splits > 1) room += ceil_div((uint64_t)splits * k.part_stride * sizeof(float), 256) * 256;
+    plan.direct = r.p.good() && r.q.good();
+    if (plan.tile < kStream16) {
+        const rr_status_t st = pack(r.p, r.q, room, s);
+        if (st != RR_OK) return st;
+    }
+    k.p = r.p.rows.data;
+    k.p_ld = r.p.rows.ld;
+    k.q = r.q.rows.data;
+    k.q_ld = r.q.rows.ld;
+    k.q_group = r.q.group;
+    return a->dt == RR_BF16 ? launch_gemm_bf16(k, plan, s) : launch_gemm_f16(k, plan, s);
+}
+
+static Operand rows_of(const rr_linear_t* a, const rr_rows_t& r, uint64_t width) {
+    return {r, a->rows, width, 1, 0};
+}
+static Operand weights_of(const rr_linear_t* a) {
+    return {{const_cast<void*>(a->w), a->w_ld}, a->n, a->k, (uint64_t)a->groups, a->w_stride};
 }
 
 // Parts of a group's rows in the sums over rows: enough workgroups to fill the device.
@@ -208,15 +319,21 @@ static uint64_t splits_of(const rr_linear_t* a) {
 }
 
 struct BackwardPlan {
-    uint64_t dz, part, split;  // bytes of scratch
+    uint64_t dz, part, product;  // bytes of scratch
 };
 static BackwardPlan plan_of(const rr_linear_t* a, const rr_linear_grad_t* g) {
     BackwardPlan p = {0, 0, 0};
-    if (a->act != RR_ACT_NONE && (g->dx.data || g->dw))
-        p.dz = ceil_div(a->rows * ceil_div(a->n, 8) * 8 * 2, 256) * 256;
+    const Operand dout = rows_of(a, g->dout, a->n);
+    if ((g->dx.data || g->dw) && (a->act != RR_ACT_NONE || !dout.good())) p.dz = dout.copy_bytes();
     if (g->db) p.part = ceil_div((uint64_t)a->groups * splits_of(a) * a->n * sizeof(float), 256) * 256;
-    if (g->dx.data) p.split = part_bytes(a, kByX);
-    if (g->dw && part_bytes(a, kByW) > p.split) p.split = part_bytes(a, kByW);
+    Operand dz = dout;
+    if (p.dz) dz.rows = {nullptr, ceil_div(a->n, 8) * 8};
+    dz.width = ceil_div(a->n, 8) * 8;       // good rows, or a copy with zeros behind each
+    if (g->dx.data) p.product = product_bytes(a, kByX, dz, weights_of(a));
+    if (g->dw) {
+        const uint64_t bytes = product_bytes(a, kByW, dz, rows_of(a, a->x, a->k));
+        if (bytes > p.product) p.product = bytes;
+    }
     return p;
 }
 
@@ -230,7 +347,7 @@ rr_status_t block_linear_workspace(const rr_linear_t* a, size_t* bytes) {
     if (!bytes) return RR_ERR_INVALID;
     const rr_status_t st = check_linear(a);
     if (st != RR_OK) return st;
-    *bytes = part_bytes(a, kForward);
+    *bytes = product_bytes(a, kForward, rows_of(a, a->x, a->k), weights_of(a));
     return RR_OK;
 }
 
@@ -238,7 +355,7 @@ rr_status_t block_linear(const rr_linear_t* a, void* workspace, size_t workspace
                          rr_stream_t stream) {
     const rr_status_t st = check_linear(a);
     if (st != RR_OK) return st;
-    const uint64_t need = part_bytes(a, kForward);
+    const uint64_t need = product_bytes(a, kForward, rows_of(a, a->x, a->k), weights_of(a));
     if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need))
         return RR_ERR_INVALID;
     if (!rows_ok(a->out, a->rows, a->n, 2) || !rows_ok_if(a->residual, a->rows, a->n, 2) ||
@@ -267,12 +384,8 @@ rr_status_t block_linear(const rr_linear_t* a, void* workspace, size_t workspace
         !(a->residual.data == a->out.data && a->residual.ld == a->out.ld))
         return RR_ERR_INVALID;
     if (a->rows == 0) return RR_OK;
-    GemmArgs k = groups_of(a);
-    k.p = a->x.data;
-    k.p_ld = a->x.ld;
-    k.q = a->w;
-    k.q_ld = a->w_ld;
-    k.q_group = a->w_stride;
+    Product r = {kForward, rows_of(a, a->x, a->k), weights_of(a), groups_of(a)};
+    GemmArgs& k = r.k;
     k.i = (int32_t)a->rows;
     k.j = (int32_t)a->n;
     k.c = (int32_t)a->k;
@@ -284,7 +397,7 @@ rr_status_t block_linear(const rr_linear_t* a, void* workspace, size_t workspace
     k.out = a->out.data;
     k.out_ld = a->out.ld;
     k.act = a->act;
-    return run_gemm(k, a, kForward, workspace, (hipStream_t)stream);
+    return run_product(a, r, workspace, (hipStream_t)stream);
 }
 
 rr_status_t block_linear_backward_workspace(const rr_linear_t* a, const rr_linear_grad_t* g,
@@ -293,7 +406,7 @@ rr_status_t block_linear_backward_workspace(const rr_linear_t* a, const rr_linea
     const rr_status_t st = check_grad(a, g);
     if (st != RR_OK) return st;
     const BackwardPlan p = plan_of(a, g);
-    *bytes = p.dz + p.part + p.split;
+    *bytes = p.dz + p.part + p.product;
     return RR_OK;
 }
 
@@ -302,7 +415,7 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
     rr_status_t st = check_grad(a, g);
     if (st != RR_OK) return st;
     const BackwardPlan plan = plan_of(a, g);
-    const uint64_t need = plan.dz + plan.part + plan.split;
+    const uint64_t need = plan.dz + plan.part + plan.product;
     if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need))
         return RR_ERR_INVALID;
     const uint64_t w_bytes = extent(a->groups, a->w_stride, extent(a->n, a->w_ld, a->k, 1), 2);
@@ -323,7 +436,7 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
     }
     hipStream_t s = (hipStream_t)stream;
     rr_rows_t dz = g->dout;
-    void* const split = (char*)workspace + plan.dz + plan.part;
+    void* const room = (char*)workspace + plan.dz + plan.part;
     if (plan.dz || plan.part) {
         SlopeArgs k = {};
         k.g = groups_of(a);
@@ -354,33 +467,25 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
             if ((st = launched()) != RR_OK) return st;
         }
     }
+    Operand by = rows_of(a, dz, ceil_div(a->n, 8) * 8);     // zeros behind the columns, if any
     if (g->dx.data && a->rows) {
-        GemmArgs k = groups_of(a);
-        k.p = dz.data;
-        k.p_ld = dz.ld;
-        k.q = a->w;
-        k.q_ld = a->w_ld;
-        k.q_group = a->w_stride;
-        k.i = (int32_t)a->rows;
-        k.j = (int32_t)a->k;
-        k.c = (int32_t)a->n;
-        k.out = g->dx.data;
-        k.out_ld = g->dx.ld;
-        if ((st = run_gemm(k, a, kByX, split, s)) != RR_OK) return st;
+        Product r = {kByX, by, weights_of(a), groups_of(a)};
+        r.k.i = (int32_t)a->rows;
+        r.k.j = (int32_t)a->k;
+        r.k.c = (int32_t)a->n;
+        r.k.out = g->dx.data;
+        r.k.out_ld = g->dx.ld;
+        if ((st = run_product(a, r, room, s)) != RR_OK) return st;
     }
     if (g->dw) {
-        GemmArgs k = groups_of(a);
-        k.p = dz.data;
-        k.p_ld = dz.ld;
-        k.q = a->x.data;
-        k.q_ld = a->x.ld;
-        k.i = (int32_t)a->n;
-        k.j = (int32_t)a->k;
-        k.out = g->dw;
-        k.out_ld = a->k;
-        k.out_group = (uint64_t)a->n * a->k;
-        k.wide_out = g->dw_dt == RR_FP32;
-        if ((st = run_gemm(k, a, kByW, split, s)) != RR_OK) return st;
+        Product r = {kByW, by, rows_of(a, a->x, a->k), groups_of(a)};
+        r.k.i = (int32_t)a->n;
+        r.k.j = (int32_t)a->k;
+        r.k.out = g->dw;
+        r.k.out_ld = a->k;
+        r.k.out_group = (uint64_t)a->n * a->k;
+        r.k.wide_out = g->dw_dt == RR_FP32;
+        if ((st = run_product(a, r, room, s)) != RR_OK) return st;
     }
     return RR_OK;
 }
