@@ -17,11 +17,12 @@ LIB = os.path.join(HERE, "librr.so")
 SOURCES = [os.path.join(CSRC, f) for f in
            ("rr_ring_i32.hip", "rr_ring_f32.hip", "rr_ring_bf16.hip", "rr_ring_f16.hip",
             "rr_staged_kernel.hip", "rr_aux_kernels.hip", "rr_api.hip")]
-SOURCES += [os.path.join(BLOCK, f) for f in ("blk_expert.hip", "blk_norm.hip", "blk_linear.hip",
+SOURCES += [os.path.join(BLOCK, f) for f in ("blk_expert.hip", "blk_norm.hip", "blk_norm_f32.hip",
+                                                "blk_norm_bf16.hip", "blk_norm_f16.hip", "blk_linear.hip",
                                                 "blk_gemm_bf16.hip", "blk_gemm_f16.hip")]
 HEADERS = [os.path.join(CSRC, "rr_device.hpp"), os.path.join(CSRC, "rr_kernels.hpp"),
            os.path.join(CSRC, "rr_ring_kernel.hpp"), os.path.join(BLOCK, "blk_common.hpp"),
-           os.path.join(BLOCK, "blk_gemm.hpp"),
+           os.path.join(BLOCK, "blk_gemm.hpp"), os.path.join(BLOCK, "blk_norm.hpp"),
            os.path.join(ROOT, "include", "rr.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -40,14 +40,39 @@ __device__ __forceinline__ Vec<T> load_vec(const T* row, int at, int len) {
     return r;
 }
 
+// A whole vector, and nothing else: behind a branch, a load is waited for before the next is
+// sent (and the compiler takes it apart), which costs bandwidth-bound kernels half their rate.
+template <typename T> __device__ __forceinline__ u32x4 load_raw(const T* p) {
+    return reinterpret_cast<const Loose<T>*>(p)->v;
+}
+template <typename T> __device__ __forceinline__ Vec<T> vec_of(u32x4 v) {
+    return __builtin_bit_cast(Vec<T>, v);
+}
+__device__ __forceinline__ u32x4 zero_unless(bool keep, u32x4 v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = keep ? v[i] : 0u;
+    return v;
+}
+// v without its first `skip` bytes (a multiple of 2, 0 .. 16), zeros behind.
+__device__ __forceinline__ u32x4 drop_first(u32x4 v, int skip) {
+    const uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    const int n = (skip & 7) * 8;
+    const uint64_t low = n ? lo >> n | hi << (64 - n) : lo, high = hi >> n;
+    const uint64_t a = skip >= 16 ? 0 : skip >= 8 ? high : low, b = skip >= 8 ? 0 : high;
+    return u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+}
+
 template <typename T>
 __device__ __forceinline__ void store_vec(T* row, int at, int len, const Vec<T>& r) {
+    u32x4 v = __builtin_bit_cast(u32x4, r);
     if (at + Vec<T>::N <= len) {
-        reinterpret_cast<Loose<T>*>(row + at)->v = __builtin_bit_cast(u32x4, r);
+        reinterpret_cast<Loose<T>*>(row + at)->v = v;
     } else {
-#pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i)
-            if (at + i < len) row[at + i] = r.e[i];
+#pragma unroll 1
+        for (; at < len; ++at) {
+            row[at] = vec_of<T>(v).e[0];
+            v = drop_first(v, (int)sizeof(T));
+        }
     }
 }
 

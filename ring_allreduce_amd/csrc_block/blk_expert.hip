@@ -236,40 +236,38 @@ struct MoveArgs {
 };
 
 constexpr int kMoveBlock = 256;
-constexpr int kClearRows = kMoveBlock;   // rows whose source a clearing workgroup looks at
+constexpr int kClearRows = 32;   // rows whose source a clearing workgroup looks at
 
 __device__ __forceinline__ int slot_of(const MoveArgs& a, int t, int j) {
     const int s = a.slots[(uint64_t)t * a.k + j];
     return s >= 0 && s < a.rows ? s : -1;
 }
 
-// Zeros in the rows without a pair, of kClearRows rows from `first`.
+// Zeros in the rows without a pair, of kClearRows rows from `first`, a wave its share of them.
 template <typename T>
 __device__ __forceinline__ void clear_rows(const MoveArgs& a, int64_t first) {
-    __shared__ uint64_t unused[kClearRows / 64];
-    const int64_t r = first + threadIdx.x;
+    constexpr int EACH = kClearRows / (kMoveBlock / 64);
+    const int lane = threadIdx.x & 63;
+    first += (int64_t)(threadIdx.x >> 6) * EACH;
     bool clear = false;
-    if (r < a.rows) {
-        const int p = a.sources[r];
+    if (lane < EACH && first + lane < a.rows) {
+        const int p = a.sources[first + lane];
         clear = p < 0 || (int64_t)p >= (int64_t)a.tokens * a.k;
     }
-    const uint64_t m = __ballot(clear);
-    if ((threadIdx.x & 63) == 0) unused[threadIdx.x >> 6] = m;
-    __syncthreads();
+    uint64_t left = __ballot(clear);
     Vec<T> zero;
 #pragma unroll
     for (int i = 0; i < Vec<T>::N; ++i) zero.e[i] = (T)0.0f;
-    for (int w = 0; w < kClearRows / 64; ++w) {
-        uint64_t left = unused[w];
-        while (left) {
-            const int b = __ffsll((unsigned long long)left) - 1;
-            left &= left - 1;
-            T* row = (T*)a.out + (uint64_t)(first + w * 64 + b) * a.out_ld;
-            for (int c = threadIdx.x * Vec<T>::N; c < a.hidden; c += kMoveBlock * Vec<T>::N)
-                store_vec(row, c, a.hidden, zero);
-        }
+    while (left) {
+        const int b = __ffsll((unsigned long long)left) - 1;
+        left &= left - 1;
+        T* row = (T*)a.out + (uint64_t)(first + b) * a.out_ld;
+        for (int c = lane * Vec<T>::N; c < a.hidden; c += 64 * Vec<T>::N) store_vec(row, c, a.hidden, zero);
     }
 }
+
+// A loop over the row's whole vectors, whose loads have no branches, and one over the
+// elements left behind them.  Rows that are not there are read as row 0 and not counted.
 
 // G threads per token (a power of two, 8 .. 256).
 template <typename T, int G>
@@ -281,114 +279,142 @@ __global__ void __launch_bounds__(kMoveBlock) dispatch_kernel(const MoveArgs a) 
     }
     const int t = (int)blockIdx.x * (kMoveBlock / G) + (int)threadIdx.x / G;
     if (t >= a.tokens) return;
-    const int g = threadIdx.x % G;
+    const int g = threadIdx.x % G, whole = a.hidden / N * N;
     const T* x = (const T*)a.in + (uint64_t)t * a.in_ld;
-    for (int c = g * N; c < a.hidden; c += G * N) {
-        const Vec<T> v = load_vec(x, c, a.hidden);
+    for (int c = g * N; c < whole; c += G * N) {
+        const u32x4 v = load_raw(x + c);
         for (int j = 0; j < a.k; ++j) {
             const int s = slot_of(a, t, j);
-            if (s >= 0) store_vec((T*)a.out + (uint64_t)s * a.out_ld, c, a.hidden, v);
+            if (s >= 0) reinterpret_cast<Loose<T>*>((T*)a.out + (uint64_t)s * a.out_ld + c)->v = v;
+        }
+    }
+    for (int c = whole + g; c < a.hidden; c += G) {
+        const T v = x[c];
+        for (int j = 0; j < a.k; ++j) {
+            const int s = slot_of(a, t, j);
+            if (s >= 0) ((T*)a.out)[(uint64_t)s * a.out_ld + c] = v;
         }
     }
 }
 
-constexpr int kTogether = 4;  // rows of a token in flight
-
-template <typename T, int G>
+// J rows of a token at a time (the smallest of 1, 2, 4, 8 that takes all k, if one does).
+template <typename T, int G, int J>
 __global__ void __launch_bounds__(kMoveBlock) combine_kernel(const MoveArgs a) {
     constexpr int N = Vec<T>::N;
     const int t = (int)blockIdx.x * (kMoveBlock / G) + (int)threadIdx.x / G;
     if (t >= a.tokens) return;
-    const int g = threadIdx.x % G;
+    const int g = threadIdx.x % G, whole = a.hidden / N * N;
     T* out = (T*)a.out + (uint64_t)t * a.out_ld;
-    for (int c = g * N; c < a.hidden; c += G * N) {
+    int s[J];
+    float w[J];
+    const auto slots = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int at = min(j0 + j, a.k - 1);
+            s[j] = j0 + j < a.k ? slot_of(a, t, at) : -1;
+            w[j] = a.weights ? a.weights[(uint64_t)t * a.k + at] : 1.0f;
+        }
+    };
+    slots(0);
+    for (int c = g * N; c < whole; c += G * N) {
         float sum[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) sum[i] = 0.0f;
-        for (int j0 = 0; j0 < a.k; j0 += kTogether) {
-            Vec<T> v[kTogether];
-            float w[kTogether];
-            int s[kTogether];
+        for (int j0 = 0; j0 < a.k; j0 += J) {
+            if (a.k > J) slots(j0);
+            u32x4 v[J];
 #pragma unroll
-            for (int j = 0; j < kTogether; ++j) {
-                s[j] = j0 + j < a.k ? slot_of(a, t, j0 + j) : -1;
-                if (s[j] >= 0) {
-                    v[j] = load_vec((const T*)a.in + (uint64_t)s[j] * a.in_ld, c, a.hidden);
-                    w[j] = a.weights ? a.weights[(uint64_t)t * a.k + j0 + j] : 1.0f;
-                }
-            }
+            for (int j = 0; j < J; ++j) v[j] = load_raw((const T*)a.in + (uint64_t)max(s[j], 0) * a.in_ld + c);
 #pragma unroll
-            for (int j = 0; j < kTogether; ++j)
+            for (int j = 0; j < J; ++j)
                 if (s[j] >= 0)
 #pragma unroll
-                    for (int i = 0; i < N; ++i) sum[i] = fmaf(w[j], (float)v[j].e[i], sum[i]);
+                    for (int i = 0; i < N; ++i) sum[i] = fmaf(w[j], (float)vec_of<T>(v[j]).e[i], sum[i]);
         }
         Vec<T> r;
 #pragma unroll
         for (int i = 0; i < N; ++i) r.e[i] = (T)sum[i];
-        store_vec(out, c, a.hidden, r);
+        reinterpret_cast<Loose<T>*>(out + c)->v = __builtin_bit_cast(u32x4, r);
+    }
+    for (int c = whole + g; c < a.hidden; c += G) {
+        float sum = 0.0f;
+        for (int j = 0; j < a.k; ++j) {
+            const int at = slot_of(a, t, j);
+            if (at >= 0)
+                sum = fmaf(a.weights ? a.weights[(uint64_t)t * a.k + j] : 1.0f,
+                           (float)((const T*)a.in)[(uint64_t)at * a.in_ld + c], sum);
+        }
+        out[c] = (T)sum;
     }
 }
 
 // G = 64 or 256 threads per token.  The dot products are summed per thread in column
 // order, then over the lanes of a wave, then over the waves.
-template <typename T, int G>
+template <typename T, int G, int J>
 __global__ void __launch_bounds__(kMoveBlock) combine_backward_kernel(const MoveArgs a) {
     constexpr int N = Vec<T>::N;
     constexpr int W = G / 64;
-    __shared__ float part[W][kTogether];
+    __shared__ float part[W][J];
     if ((int)blockIdx.x >= a.token_blocks) {
         clear_rows<T>(a, (int64_t)((int)blockIdx.x - a.token_blocks) * kClearRows);
         return;
     }
     const int t = (int)blockIdx.x * (kMoveBlock / G) + (int)threadIdx.x / G;
     if (t >= a.tokens) return;        // whole waves, and with G = 256 the whole workgroup
-    const int g = threadIdx.x % G;
+    const int g = threadIdx.x % G, whole = a.hidden / N * N;
     const T* d = (const T*)a.in + (uint64_t)t * a.in_ld;
-    for (int j0 = 0; j0 < a.k; j0 += kTogether) {
-        int s[kTogether];
-        float w[kTogether], dot[kTogether];
+    const T* rows = a.dweights ? (const T*)a.in2 : d;    // d: read, and not counted
+    const uint64_t rows_ld = a.dweights ? a.in2_ld : 0;
+    for (int j0 = 0; j0 < a.k; j0 += J) {
+        int s[J];
+        float w[J], dot[J];
 #pragma unroll
-        for (int j = 0; j < kTogether; ++j) {
-            s[j] = j0 + j < a.k ? slot_of(a, t, j0 + j) : -1;
-            w[j] = s[j] >= 0 && a.weights ? a.weights[(uint64_t)t * a.k + j0 + j] : 1.0f;
+        for (int j = 0; j < J; ++j) {
+            const int at = min(j0 + j, a.k - 1);
+            s[j] = j0 + j < a.k ? slot_of(a, t, at) : -1;
+            w[j] = a.weights ? a.weights[(uint64_t)t * a.k + at] : 1.0f;
             dot[j] = 0.0f;
         }
-        for (int c = g * N; c < a.hidden; c += G * N) {
-            const Vec<T> dv = load_vec(d, c, a.hidden);
-            Vec<T> v[kTogether];
-            if (a.dweights) {
+        for (int c = g * N; c < whole; c += G * N) {
+            const u32x4 dv = load_raw(d + c);
+            u32x4 v[J];
 #pragma unroll
-                for (int j = 0; j < kTogether; ++j)
-                    if (s[j] >= 0)
-                        v[j] = load_vec((const T*)a.in2 + (uint64_t)s[j] * a.in2_ld, c, a.hidden);
-            }
+            for (int j = 0; j < J; ++j) v[j] = load_raw(rows + (uint64_t)max(s[j], 0) * rows_ld + c);
 #pragma unroll
-            for (int j = 0; j < kTogether; ++j) {
+            for (int j = 0; j < J; ++j) {
                 if (s[j] < 0) continue;
                 if (a.out) {
                     Vec<T> r;
 #pragma unroll
-                    for (int i = 0; i < N; ++i) r.e[i] = (T)(w[j] * (float)dv.e[i]);
-                    store_vec((T*)a.out + (uint64_t)s[j] * a.out_ld, c, a.hidden, r);
+                    for (int i = 0; i < N; ++i) r.e[i] = (T)(w[j] * (float)vec_of<T>(dv).e[i]);
+                    reinterpret_cast<Loose<T>*>((T*)a.out + (uint64_t)s[j] * a.out_ld + c)->v =
+                        __builtin_bit_cast(u32x4, r);
                 }
-                if (a.dweights)
 #pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        dot[j] = fmaf((float)dv.e[i], (float)v[j].e[i], dot[j]);
+                for (int i = 0; i < N; ++i)
+                    dot[j] = fmaf((float)vec_of<T>(dv).e[i], (float)vec_of<T>(v[j]).e[i], dot[j]);
+            }
+        }
+        for (int c = whole + g; c < a.hidden; c += G) {
+            const float dv = (float)d[c];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (s[j] < 0) continue;
+                if (a.out) ((T*)a.out)[(uint64_t)s[j] * a.out_ld + c] = (T)(w[j] * dv);
+                if (a.dweights) dot[j] = fmaf(dv, (float)rows[(uint64_t)s[j] * rows_ld + c], dot[j]);
             }
         }
         if (!a.dweights) continue;
 #pragma unroll
-        for (int j = 0; j < kTogether; ++j) dot[j] = lane_sum<64>(dot[j]);
+        for (int j = 0; j < J; ++j) dot[j] = lane_sum<64>(dot[j]);
         if constexpr (W > 1) {
             __syncthreads();          // the previous round's sums have been read
             if ((threadIdx.x & 63) == 0)
 #pragma unroll
-                for (int j = 0; j < kTogether; ++j) part[threadIdx.x >> 6][j] = dot[j];
+                for (int j = 0; j < J; ++j) part[threadIdx.x >> 6][j] = dot[j];
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < kTogether; ++j) {
+            for (int j = 0; j < J; ++j) {
                 dot[j] = 0.0f;
 #pragma unroll
                 for (int q = 0; q < W; ++q) dot[j] += part[q][j];
@@ -396,7 +422,7 @@ __global__ void __launch_bounds__(kMoveBlock) combine_backward_kernel(const Move
         }
         if (g == 0)
 #pragma unroll
-            for (int j = 0; j < kTogether; ++j)
+            for (int j = 0; j < J; ++j)
                 if (j0 + j < a.k) a.dweights[(uint64_t)t * a.k + j0 + j] = s[j] >= 0 ? dot[j] : 0.0f;
     }
 }
@@ -461,6 +487,36 @@ static int group_for(size_t hidden, int dt) {
 
 // A launch holds fewer than 2^32 threads.
 static bool grid_fits(uint64_t blocks) { return blocks < (1ull << 32) / kMoveBlock; }
+
+// Rows of a token at a time.
+static int together(int k) { return k <= 1 ? 1 : k <= 2 ? 2 : k <= 4 ? 4 : 8; }
+
+template <typename T, int J> static void launch_combine(const MoveArgs& a, int g, unsigned grid, hipStream_t s) {
+    switch (g) {
+        case 8: combine_kernel<T, 8, J><<<grid, kMoveBlock, 0, s>>>(a); break;
+        case 16: combine_kernel<T, 16, J><<<grid, kMoveBlock, 0, s>>>(a); break;
+        case 32: combine_kernel<T, 32, J><<<grid, kMoveBlock, 0, s>>>(a); break;
+        case 64: combine_kernel<T, 64, J><<<grid, kMoveBlock, 0, s>>>(a); break;
+        case 128: combine_kernel<T, 128, J><<<grid, kMoveBlock, 0, s>>>(a); break;
+        default: combine_kernel<T, 256, J><<<grid, kMoveBlock, 0, s>>>(a); break;
+    }
+}
+template <typename T> static void launch_combine(const MoveArgs& a, int g, unsigned grid, hipStream_t s) {
+    switch (together(a.k)) {
+        case 1: launch_combine<T, 1>(a, g, grid, s); break;
+        case 2: launch_combine<T, 2>(a, g, grid, s); break;
+        case 4: launch_combine<T, 4>(a, g, grid, s); break;
+        default: launch_combine<T, 8>(a, g, grid, s); break;
+    }
+}
+template <typename T, int G> static void launch_backward(const MoveArgs& a, unsigned grid, hipStream_t s) {
+    switch (together(a.k)) {
+        case 1: combine_backward_kernel<T, G, 1><<<grid, kMoveBlock, 0, s>>>(a); break;
+        case 2: combine_backward_kernel<T, G, 2><<<grid, kMoveBlock, 0, s>>>(a); break;
+        case 4: combine_backward_kernel<T, G, 4><<<grid, kMoveBlock, 0, s>>>(a); break;
+        default: combine_backward_kernel<T, G, 8><<<grid, kMoveBlock, 0, s>>>(a); break;
+    }
+}
 
 #define BLK_BY_TYPE(dt, CALL)                 \
     switch (dt) {                             \
@@ -602,11 +658,15 @@ rr_status_t expert_combine(rr_rows_t in, size_t rows, size_t hidden, rr_dtype_t 
     a.k = k;
     a.rows = (int32_t)rows;
     a.hidden = (int32_t)hidden;
+    if (rows == 0) {               // no slot has a row: something to read and not count
+        a.in = out.data;
+        a.in_ld = 0;
+    }
     const int g = group_for(hidden, dt);
     if (!grid_fits(ceil_div(tokens, kMoveBlock / g))) return RR_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)ceil_div(tokens, kMoveBlock / g);
     hipStream_t s = (hipStream_t)stream;
-#define CALL(T) BLK_BY_GROUP(g, T, combine_kernel, grid, s, a)
+#define CALL(T) launch_combine<T>(a, g, grid, s)
     BLK_BY_TYPE(dt, CALL)
 #undef CALL
     return launched();
@@ -638,8 +698,8 @@ rr_status_t expert_combine_backward(rr_rows_t dout, rr_rows_t in, size_t rows, s
     MoveArgs a = {};
     a.in = dout.data;
     a.in_ld = dout.ld;
-    a.in2 = in.data;
-    a.in2_ld = in.ld;
+    a.in2 = rows ? in.data : dout.data;   // without rows: something to read and not count
+    a.in2_ld = rows ? in.ld : 0;
     a.out = rows ? drows.data : nullptr;
     a.out_ld = drows.ld;
     a.slots = slots;
@@ -657,11 +717,11 @@ rr_status_t expert_combine_backward(rr_rows_t dout, rr_rows_t in, size_t rows, s
     const unsigned grid = (unsigned)(a.token_blocks + (a.out ? ceil_div(rows, kClearRows) : 0));
     if (grid == 0) return RR_OK;
     hipStream_t s = (hipStream_t)stream;
-#define CALL(T)                                                          \
-    if (wide)                                                            \
-        combine_backward_kernel<T, 256><<<grid, kMoveBlock, 0, s>>>(a);  \
-    else                                                                 \
-        combine_backward_kernel<T, 64><<<grid, kMoveBlock, 0, s>>>(a);
+#define CALL(T)                                  \
+    if (wide)                                    \
+        launch_backward<T, 256>(a, grid, s);     \
+    else                                         \
+        launch_backward<T, 64>(a, grid, s);
     BLK_BY_TYPE(dt, CALL)
 #undef CALL
     return launched();
