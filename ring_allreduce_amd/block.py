@@ -97,13 +97,29 @@ def _check(status, what):
         raise RRError(status, what)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+
+
+class _Current:
+    """The current stream of the current device: nothing to set, nothing to restore."""
+    __slots__ = ("handle",)
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *_):
+        return False
+
+
 @contextlib.contextmanager
-def _on(device, stream):
-    """The device and stream of a call, for its allocations and its launch; yields
-    the stream's handle."""
+def _switched(device, stream):
     with torch.cuda.device(device):
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
+            yield _raw_stream(device.index)
             return
         s = stream
         if isinstance(s, int):
@@ -113,53 +129,86 @@ def _on(device, stream):
             yield s.cuda_stream
 
 
+def _on(device, stream):
+    """The device and stream of a call, for its allocations and its launch; a context that
+    gives the stream's handle.  A call on the current ones enters nothing: a small call's
+    time is the host's, and torch's contexts are 4 us of it."""
+    if stream is None and device.index == _current_device():
+        return _Current(_raw_stream(device.index))
+    return _switched(device, stream)
+
+
 def _need(cond, what):
     if not cond:
         raise ValueError(what)
 
 
+# Messages are made where a check fails: made beforehand they cost more than the checks.
 def _matrix(t, name, device=None, dtype=None, rows=None, width=None):
     """``t`` as a matrix of neighbouring elements in a row; returns its _Rows."""
-    _need(isinstance(t, torch.Tensor) and t.dim() == 2, f"{name} must be a matrix")
-    _need(t.device.type == "cuda" and (device is None or t.device == device),
-          f"{name} must be on the same GPU")
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be on the same GPU")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    _need(rows is None or t.shape[0] == rows, f"{name} must have {rows} rows, not {t.shape[0]}")
-    _need(width is None or t.shape[1] == width,
-          f"{name} must have {width} columns, not {t.shape[1]}")
-    if t.numel() == 0:
-        return _Rows(t.data_ptr(), max(1, t.shape[1]))
-    _need(t.shape[1] == 1 or t.stride(1) == 1, f"{name}: the elements of a row must be neighbours")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    _need(ld >= t.shape[1], f"{name}: rows overlap")
+    r, w = t.shape
+    if rows is not None and r != rows:
+        raise ValueError(f"{name} must have {rows} rows, not {r}")
+    if width is not None and w != width:
+        raise ValueError(f"{name} must have {width} columns, not {w}")
+    if r == 0 or w == 0:
+        return _Rows(t.data_ptr(), w or 1)
+    ld, step = t.stride()
+    if step != 1 and w != 1:
+        raise ValueError(f"{name}: the elements of a row must be neighbours")
+    if r == 1:
+        ld = w
+    elif ld < w:
+        raise ValueError(f"{name}: rows overlap")
     return _Rows(t.data_ptr(), ld)
 
 
 def _float_type(t, name):
-    if t.dtype not in FLOAT_DTYPES:
+    dt = FLOAT_DTYPES.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}; use float32, bfloat16 or float16")
-    return FLOAT_DTYPES[t.dtype]
+    return dt
+
+
+def _vector(t, name, device, dtype, numel):
+    """The address of a contiguous tensor of ``numel`` elements (None: any number)."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be on the same GPU")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous() or (numel is not None and t.numel() != numel):
+        raise ValueError(f"{name} must be contiguous" +
+                         ("" if numel is None else f", with {numel} elements"))
+    return t.data_ptr()
 
 
 def _ints(t, name, device, numel=None):
-    _need(isinstance(t, torch.Tensor) and t.device == device, f"{name} must be on the same GPU")
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32, not {t.dtype}")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
-    _need(numel is None or t.numel() == numel, f"{name} must have {numel} elements, not {t.numel()}")
-    return t.data_ptr()
+    return _vector(t, name, device, torch.int32, numel)
 
 
 def _row(t, name, device, dtype, numel):
     """A contiguous vector, or None."""
-    if t is None:
-        return None
-    _need(isinstance(t, torch.Tensor) and t.device == device, f"{name} must be on the same GPU")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    _need(t.is_contiguous() and t.numel() == numel, f"{name} must have {numel} neighbouring elements")
-    return t.data_ptr()
+    return None if t is None else _vector(t, name, device, dtype, numel)
+
+
+def _new(rows, width, like):
+    """A new matrix of ``like``'s type on its device, and its _Rows."""
+    t = torch.empty((rows, width), dtype=like.dtype, device=like.device)
+    return t, _Rows(t.data_ptr(), width or 1)
+
+
+def _scratch(size, device):
+    """``size`` bytes of scratch memory: (tensor or None, its address or None)."""
+    if not size:
+        return None, None
+    t = torch.empty(size, dtype=torch.uint8, device=device)
+    return t, t.data_ptr()
 
 
 # ------------------------------------------------ tokens sorted by expert, and back
@@ -185,24 +234,25 @@ def expert_sort(ids, experts: int, capacity: int = 0, *, stream=None) -> ExpertO
     _need(experts >= 1 and capacity >= 0, "experts must be positive and capacity not negative")
     at = _matrix(ids, "ids")
     tokens, k = ids.shape
-    with _on(ids.device, stream) as s:
+    dev = ids.device
+    with _on(dev, stream) as s:
         need = _sz()
-        _check(_expert_sort_workspace(tokens, k, experts, ctypes.byref(need)), "expert_sort")
+        _check(_expert_sort_workspace(tokens, k, experts, need), "expert_sort")
         rows = experts * capacity if capacity else tokens * k
-        word = dict(dtype=torch.int32, device=ids.device)
-        order = ExpertOrder(torch.empty((tokens, k), **word), torch.empty(rows, **word),
-                            torch.empty(experts, **word), torch.empty(experts + 1, **word))
-        work = torch.empty(need.value // 4, **word) if need.value else None
+        slots = torch.empty((tokens, k), dtype=torch.int32, device=dev)
+        sources = torch.empty(rows, dtype=torch.int32, device=dev)
+        counts = torch.empty(experts, dtype=torch.int32, device=dev)
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+        work, wp = _scratch(need.value, dev)
         _check(_expert_sort(at.data, ids.element_size(), at.ld, tokens, k, experts, capacity,
-                            order.slots.data_ptr(), order.sources.data_ptr(),
-                            order.counts.data_ptr(), order.offsets.data_ptr(),
-                            work.data_ptr() if work is not None else None, need.value, s),
-               "expert_sort")
-    return order
+                            slots.data_ptr(), sources.data_ptr(), counts.data_ptr(),
+                            offsets.data_ptr(), wp, need.value, s), "expert_sort")
+    return ExpertOrder(slots, sources, counts, offsets)
 
 
 def _pairs(slots, name="slots"):
-    _need(isinstance(slots, torch.Tensor) and slots.dim() == 2, f"{name} must be [tokens, k]")
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 2:
+        raise ValueError(f"{name} must be [tokens, k]")
     return slots.shape
 
 
@@ -217,8 +267,9 @@ def expert_dispatch(x, slots, sources, *, out=None, stream=None):
     with _on(x.device, stream) as s:
         sp, so = _ints(slots, "slots", x.device), _ints(sources, "sources", x.device)
         if out is None:
-            out = torch.empty((rows, hidden), dtype=x.dtype, device=x.device)
-        o = _matrix(out, "out", x.device, x.dtype, rows, hidden)
+            out, o = _new(rows, hidden, x)
+        else:
+            o = _matrix(out, "out", x.device, x.dtype, rows, hidden)
         _check(_expert_dispatch(xr, tokens, hidden, k, dt, sp, so, rows, o, s), "expert_dispatch")
     return out
 
@@ -234,8 +285,9 @@ def expert_combine(rows, slots, weights=None, *, out=None, stream=None):
         sp = _ints(slots, "slots", rows.device)
         wp = _row(weights, "weights", rows.device, torch.float32, tokens * k)
         if out is None:
-            out = torch.empty((tokens, hidden), dtype=rows.dtype, device=rows.device)
-        o = _matrix(out, "out", rows.device, rows.dtype, tokens, hidden)
+            out, o = _new(tokens, hidden, rows)
+        else:
+            o = _matrix(out, "out", rows.device, rows.dtype, tokens, hidden)
         _check(_expert_combine(r, rows.shape[0], hidden, dt, sp, wp, tokens, k, o, s),
                "expert_combine")
     return out
@@ -262,8 +314,10 @@ def expert_combine_backward(dout, rows, slots, sources, weights=None, *, need_ro
         drows = dweights = None
         o = _Rows()
         if need_rows:
-            drows = torch.empty((n, hidden), dtype=dout.dtype, device=dev) if out is None else out
-            o = _matrix(drows, "out", dev, dout.dtype, n, hidden)
+            if out is None:
+                drows, o = _new(n, hidden, dout)
+            else:
+                drows, o = out, _matrix(out, "out", dev, dout.dtype, n, hidden)
         if need_weights:
             dweights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
         _check(_expert_combine_backward(d, r, n, hidden, dt, sp, so, wp, tokens, k, o,
@@ -326,15 +380,17 @@ def block_norm(x, branch=None, *, post_norm=True, post_weight=None, gate=None, g
     a.x = xr
     with _on(x.device, stream) as s:
         if h is None:
-            h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        a.h = _matrix(h, "h", x.device, x.dtype, *x.shape)
+            h, a.h = _new(*x.shape, x)
+        else:
+            a.h = _matrix(h, "h", x.device, x.dtype, *x.shape)
         if pre_norm:
             if y is None:
-                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            a.y = _matrix(y, "y", x.device, x.dtype, *x.shape)
+                y, a.y = _new(*x.shape, x)
+            else:
+                a.y = _matrix(y, "y", x.device, x.dtype, *x.shape)
         else:
             _need(y is None, "y without pre_norm")
-        _check(_block_norm(ctypes.byref(a), s), "block_norm")
+        _check(_block_norm(a, s), "block_norm")
     return h, y
 
 
@@ -371,9 +427,9 @@ def block_norm_backward(dh, dy, h, branch=None, *, post_norm=True, post_weight=N
         a.h = _matrix(h, "h", dev, dtype, *shape)
     with _on(dev, stream) as s:
         def rows(name):
-            t = torch.empty(shape, dtype=dtype, device=dev)
+            t, r = _new(*shape, like)
             setattr(out, name, t)
-            return _matrix(t, name)
+            return r
 
         def sums(name):
             t = torch.empty(shape[1], dtype=torch.float32, device=dev)
@@ -393,12 +449,9 @@ def block_norm_backward(dh, dy, h, branch=None, *, post_norm=True, post_weight=N
         if "dpre_weight" in need and pre_weight is not None:
             g.dpre_weight = sums("dpre_weight")
         size = _sz()
-        _check(_block_norm_backward_workspace(ctypes.byref(a), ctypes.byref(g), ctypes.byref(size)),
-               "block_norm_backward")
-        work = torch.empty(size.value, dtype=torch.uint8, device=dev) if size.value else None
-        _check(_block_norm_backward(ctypes.byref(a), ctypes.byref(g),
-                                    work.data_ptr() if work is not None else None, size.value, s),
-               "block_norm_backward")
+        _check(_block_norm_backward_workspace(a, g, size), "block_norm_backward")
+        work, wp = _scratch(size.value, dev)
+        _check(_block_norm_backward(a, g, wp, size.value, s), "block_norm_backward")
     return out
 
 
@@ -446,17 +499,16 @@ def block_linear(x, w, bias=None, *, act="none", residual=None, offsets=None, sa
         a.residual = _matrix(residual, "residual", dev, x.dtype, *shape)
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty(shape, dtype=x.dtype, device=dev)
-        a.out = _matrix(out, "out", dev, x.dtype, *shape)
+            out, a.out = _new(*shape, x)
+        else:
+            a.out = _matrix(out, "out", dev, x.dtype, *shape)
         z = None
         if save_preact:
-            z = torch.empty(shape, dtype=x.dtype, device=dev)
-            a.z = _matrix(z, "z")
+            z, a.z = _new(*shape, x)
         size = _sz()
-        _check(_block_linear_workspace(ctypes.byref(a), ctypes.byref(size)), "block_linear")
-        work = torch.empty(size.value, dtype=torch.uint8, device=dev) if size.value else None
-        _check(_block_linear(ctypes.byref(a), work.data_ptr() if work is not None else None,
-                             size.value, s), "block_linear")
+        _check(_block_linear_workspace(a, size), "block_linear")
+        work, wp = _scratch(size.value, dev)
+        _check(_block_linear(a, wp, size.value, s), "block_linear")
     return (out, z) if save_preact else out
 
 
@@ -486,8 +538,7 @@ def block_linear_backward(dout, x, w, z=None, *, act="none", offsets=None, need_
     g.dw_dt = FLOAT_DTYPES[dw_dtype]
     with _on(dev, stream) as s:
         if need_dx:
-            out.dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-            g.dx = _matrix(out.dx, "dx")
+            out.dx, g.dx = _new(*x.shape, x)
         if need_dw:
             out.dw = torch.empty(w.shape, dtype=dw_dtype, device=dev)
             g.dw = out.dw.data_ptr()
@@ -495,10 +546,7 @@ def block_linear_backward(dout, x, w, z=None, *, act="none", offsets=None, need_
             out.db = torch.empty(w.shape[:-1], dtype=torch.float32, device=dev)
             g.db = out.db.data_ptr()
         size = _sz()
-        _check(_block_linear_backward_workspace(ctypes.byref(a), ctypes.byref(g),
-                                                ctypes.byref(size)), "block_linear_backward")
-        work = torch.empty(size.value, dtype=torch.uint8, device=dev) if size.value else None
-        _check(_block_linear_backward(ctypes.byref(a), ctypes.byref(g),
-                                      work.data_ptr() if work is not None else None, size.value,
-                                      s), "block_linear_backward")
+        _check(_block_linear_backward_workspace(a, g, size), "block_linear_backward")
+        work, wp = _scratch(size.value, dev)
+        _check(_block_linear_backward(a, g, wp, size.value, s), "block_linear_backward")
     return out
