@@ -40,8 +40,10 @@ struct GemmArgs {
     int32_t wide_out;                // out in fp32
     int32_t tiles_i, tiles_j;        // tiles_i: an upper bound over all groups
     int32_t splits;                  // parts of the contraction
-    float* part;                     // [splits][rows of out][j], if splits > 1
+    float* part;                     // [splits][rows of out][j], if splits > 1, or whole tiles of
+                                     // the last round
     uint64_t part_stride;            // elements of one part
+    int32_t slots, steps;            // of the last round (slots 0: as it is), see last_round_parts
 };
 
 // What the host chose for one product; see blk_linear.hip.
@@ -78,48 +80,81 @@ __device__ __forceinline__ Range range_of(const GemmArgs& a, int r) {
     return g;
 }
 
-// Row tiles of `height` rows in all ranges.  Called by whole waves.
-__device__ __forceinline__ int count_tiles(const GemmArgs& a, int height) {
-    if (a.groups == 1 && !a.offsets) return (a.rows + height - 1) / height;
-    int n = 0;
-    for (int r0 = 0; r0 < a.groups + 2; r0 += 64) {
-        const Range r = range_of(a, r0 + (int)(threadIdx.x & 63));
-        n += (r.hi - r.lo + height - 1) / height;
-    }
+// Row tiles of `height` rows, counted through the ranges one after another.  A wave looks at
+// 64 ranges at a time, a lane each; of the first 64 it keeps what it found.
+struct RowTiles {
+    Range first;      // of this lane
+    int n, upto;      // its tiles, and those up to and with it
+    int total;        // of all ranges
+};
+
+__device__ __forceinline__ int lanes_upto(int n) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
-    return __builtin_amdgcn_readfirstlane(n);
+    for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(n, d);
+        if (lane >= d) n += up;
+    }
+    return n;
 }
 
-// The range and the first row of row tile `tile` (tiles of `height` rows, counted
-// through the ranges one after another).  Called by whole waves; false past the end.
-__device__ __forceinline__ bool find_tile(const GemmArgs& a, int tile, int height, Range& g) {
+// Called by whole waves.
+__device__ __forceinline__ RowTiles count_tiles(const GemmArgs& a, int height) {
+    RowTiles t = {};
+    if (a.groups == 1 && !a.offsets) {
+        t.total = (a.rows + height - 1) / height;
+        return t;
+    }
+    for (int r0 = 0; r0 < a.groups + 2; r0 += 64) {
+        const Range r = range_of(a, r0 + (int)(threadIdx.x & 63));
+        const int n = (r.hi - r.lo + height - 1) / height, upto = lanes_upto(n);
+        if (r0 == 0) t.first = r, t.n = n, t.upto = upto;
+        t.total += __shfl(upto, 63);
+    }
+    t.total = __builtin_amdgcn_readfirstlane(t.total);
+    return t;
+}
+
+// The range and the first row of row tile `tile`.  Called by whole waves; false past the end.
+__device__ __forceinline__ bool find_tile(const GemmArgs& a, const RowTiles& t, int tile, int height, Range& g) {
+    if (tile >= t.total) return false;
     if (a.groups == 1 && !a.offsets) {
         g = {0, tile * height, a.rows};
-        return g.lo < a.rows;
+        return true;
     }
-    const int lane = threadIdx.x & 63;
     int before = 0;
     for (int r0 = 0; r0 < a.groups + 2; r0 += 64) {
-        const Range r = range_of(a, r0 + lane);
-        const int n = (r.hi - r.lo + height - 1) / height;
-        int sum = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
+        Range r = t.first;
+        int n = t.n, upto = t.upto;
+        if (r0 > 0) {
+            r = range_of(a, r0 + (int)(threadIdx.x & 63));
+            n = (r.hi - r.lo + height - 1) / height;
+            upto = lanes_upto(n);
         }
-        const uint64_t past = __ballot(tile < before + sum);
+        const uint64_t past = __ballot(tile < before + upto);
         if (past) {
             const int at = __ffsll((unsigned long long)past) - 1;
             g.group = __shfl(r.group, at);
-            g.lo = __shfl(r.lo, at) + (tile - before - (__shfl(sum, at) - __shfl(n, at))) * height;
+            g.lo = __shfl(r.lo, at) + (tile - before - (__shfl(upto, at) - __shfl(n, at))) * height;
             g.hi = __shfl(r.hi, at);
             return true;
         }
-        before += __shfl(sum, 63);
+        before += __shfl(upto, 63);
     }
     return false;
+}
+
+// The last, partly filled round of workgroups: `rest` tiles on a device that takes `slots` at
+// once.  Into how many parts of the contraction each of these tiles is cut, so that they fill
+// the device too; 1 where the time saved (1.75 us a step of a 256 x 256 tile) does not pay for
+// the parts' way through memory (0.12 us each) and the launch that adds them (4 us).
+__host__ __device__ inline int last_round_parts(unsigned rest, unsigned slots, int steps) {
+    if (rest == 0) return 1;
+    int s = (int)(slots / rest);
+    s = s > 8 ? 8 : s;
+    s = s > steps / 4 ? steps / 4 : s;
+    if (s < 2 || 14 * steps * (s - 1) <= s * (32 + (int)rest * s)) return 1;
+    return s;
 }
 
 // ----------------------------------------------------------------- the tiles --
@@ -371,14 +406,34 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int group, int i, int 
 struct Spot {
     Range g;
     int i0, i_end, c0, c_end, j0, split;
+    int parts;        // of the contraction, in the last round: 1, or this is part `split` of
+    unsigned tile;    // its tile `tile`
 };
 
 // Workgroup -> tile.  Workgroups go to the 8 XCDs in turn, each with an L2 of its own:
 // every XCD takes one stretch of the tiles, and a stretch goes through 8 rows of tiles column by column, so that the tiles in
 // flight on an XCD share operands.
 template <bool BY_ROWS, int TI, int TJ>
-__device__ __forceinline__ bool find_spot(const GemmArgs& a, unsigned tiles_i, unsigned number, Spot& s) {
-    const unsigned tiles = tiles_i * (unsigned)a.tiles_j, outer = number / tiles, id = number % tiles;
+__device__ __forceinline__ bool find_spot(const GemmArgs& a, const RowTiles& rows, unsigned number, Spot& s) {
+    const unsigned tiles_i = BY_ROWS ? (unsigned)rows.total : (unsigned)a.tiles_i;
+    const unsigned tiles = tiles_i * (unsigned)a.tiles_j;
+    if (tiles == 0) return false;
+    s.parts = 1;
+    s.tile = 0;
+    if (a.slots) {
+        const unsigned whole = tiles / (unsigned)a.slots * (unsigned)a.slots, rest = tiles - whole;
+        const int parts = last_round_parts(rest, (unsigned)a.slots, a.steps);
+        if (number >= whole && parts > 1) {
+            const unsigned i = number - whole;
+            if (i >= rest * (unsigned)parts) return false;
+            s.parts = parts;
+            s.tile = i % rest;
+            s.split = (int)(i / rest);
+            number = whole + s.tile;
+        }
+    }
+    const unsigned outer = number / tiles, id = number % tiles;
+    if (outer >= (unsigned)a.splits * (BY_ROWS ? 1u : (unsigned)a.groups)) return false;
     const unsigned xcd = id & 7, each = tiles >> 3, more = tiles & 7;
     const unsigned at = xcd * each + min(xcd, more) + (id >> 3);
     const unsigned tall = 8u * (unsigned)a.tiles_j, first = at / tall * 8u;
@@ -387,14 +442,14 @@ __device__ __forceinline__ bool find_spot(const GemmArgs& a, unsigned tiles_i, u
     s.j0 = (int)(in / high) * TJ;
     int c_lo, c_hi;
     if constexpr (BY_ROWS) {
-        s.split = (int)outer;
-        if (!find_tile(a, ti, TI, s.g)) return false;
+        if (s.parts == 1) s.split = (int)outer;
+        if (!find_tile(a, rows, ti, TI, s.g)) return false;
         s.i0 = s.g.lo;
         s.i_end = s.g.hi;
         c_lo = 0;
         c_hi = s.g.group < 0 ? 0 : a.c;
     } else {
-        s.split = (int)(outer / (unsigned)a.groups);
+        if (s.parts == 1) s.split = (int)(outer / (unsigned)a.groups);
         s.g = range_of(a, (int)(outer % (unsigned)a.groups) + 1);
         s.i0 = ti * TI;
         s.i_end = a.i;
@@ -408,8 +463,9 @@ __device__ __forceinline__ bool find_spot(const GemmArgs& a, unsigned tiles_i, u
     c_hi = __builtin_amdgcn_readfirstlane(c_hi);
     s.c0 = c_lo;
     s.c_end = c_hi;
-    if (a.splits > 1) {
-        const int each_c = ((c_hi - c_lo + kDepth - 1) / kDepth + a.splits - 1) / a.splits;
+    const int parts = a.splits * s.parts;    // one of them is 1
+    if (parts > 1) {
+        const int each_c = ((c_hi - c_lo + kDepth - 1) / kDepth + parts - 1) / parts;
         const int64_t lo = c_lo + (int64_t)s.split * each_c * kDepth;
         s.c0 = (int)min(lo, (int64_t)c_hi);
         s.c_end = (int)min(lo + (int64_t)each_c * kDepth, (int64_t)c_hi);
@@ -431,17 +487,19 @@ __device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, BLK_
     static_assert(THREADS % GROUPS == 0, "a thread keeps its columns");
     BLK_LDS float* const store = (BLK_LDS float*)room;
     const int thread = here(), lane = thread & 63, wave = thread >> 6;
-    const bool whole = a.splits == 1, add = whole && a.residual && s.g.group >= 0;
+    const bool whole = a.splits == 1 && s.parts == 1, add = whole && a.residual && s.g.group >= 0;
     if (!whole && s.g.group < 0) return;        // join_kernel knows
     const int col = thread % GROUPS * 8, n = a.j - s.j0 - col;
     // A matrix's rows: those of block row 0 by 32-bit offsets from the tile's corner, and 16
     // rows on for each block row (rows are at most 2^22 elements apart).
     const uint64_t corner_out = (a.out_group && whole ? (uint64_t)s.g.group * a.out_group : 0);
     const uint32_t wide = whole && !a.wide_out ? sizeof(T) : 4;
-    const uint64_t out_ld = whole ? a.out_ld : (uint64_t)a.j;
+    const uint64_t out_ld = whole ? a.out_ld : s.parts > 1 ? (uint64_t)TJ : (uint64_t)a.j;
     const uint64_t part_row = BY_ROWS ? (uint64_t)s.i0 : (uint64_t)s.g.group * a.i + s.i0;
     const char* out = whole ? (const char*)a.out + (corner_out + (uint64_t)s.i0 * out_ld + s.j0) * wide
-                            : (const char*)(a.part + (uint64_t)s.split * a.part_stride + part_row * out_ld + s.j0);
+                      : s.parts > 1
+                          ? (const char*)(a.part + ((uint64_t)s.tile * s.parts + s.split) * (TI * TJ))
+                          : (const char*)(a.part + (uint64_t)s.split * a.part_stride + part_row * out_ld + s.j0);
     const char* z = (const char*)a.z + ((uint64_t)s.i0 * a.z_ld + s.j0) * sizeof(T);
     const char* res = (const char*)a.residual + ((uint64_t)s.i0 * a.residual_ld + s.j0) * sizeof(T);
     out = uniform(out);
@@ -522,10 +580,10 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a)
     constexpr uint32_t OUT = 2 * 16 * WI * (TJ + 4) * 4;   // write_out's place
     __shared__ __align__(2 * STAGE) char lds[OUT > 2 * STAGE ? OUT : 2 * STAGE];
     BLK_LDS char* const room = (BLK_LDS char*)lds;
-    const unsigned tiles_i = BY_ROWS ? (unsigned)count_tiles(a, TI) : (unsigned)a.tiles_i;
-    const unsigned total = tiles_i * (unsigned)a.tiles_j * (unsigned)a.splits * (BY_ROWS ? 1u : (unsigned)a.groups);
+    RowTiles rows = {};
+    if constexpr (BY_ROWS) rows = count_tiles(a, TI);
     Spot s;
-    if (blockIdx.x >= total || !find_spot<BY_ROWS, TI, TJ>(a, tiles_i, blockIdx.x, s)) return;
+    if (!find_spot<BY_ROWS, TI, TJ>(a, rows, blockIdx.x, s)) return;
     const T* const p = (const T*)a.p;
     const T* const q = (const T*)a.q + (BY_ROWS && s.g.group > 0 ? (uint64_t)s.g.group * a.q_group : 0);
     const int wave = threadIdx.x >> 6, wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
@@ -664,7 +722,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArg
     constexpr int FJ = kStreamCols / 16;
     __shared__ f32x4 sums[kStreamWaves][FI * FJ][64];
     Range g;
-    if (!find_tile(a, (int)blockIdx.y, 16 * FI, g)) return;
+    if (!find_tile(a, count_tiles(a, 16 * FI), (int)blockIdx.y, 16 * FI, g)) return;
     g.group = __builtin_amdgcn_readfirstlane(g.group);
     const int i0 = __builtin_amdgcn_readfirstlane(g.lo), i_end = __builtin_amdgcn_readfirstlane(g.hi);
     const int j0 = (int)blockIdx.x * kStreamCols, lane = threadIdx.x & 63;
@@ -768,12 +826,52 @@ template <typename T> __global__ void __launch_bounds__(256) join_kernel(const G
     finish<T, 4>(a, group, by_rows ? (int)row : (int)(row % a.i), j, v);
 }
 
+// Adds the parts of the last round's tiles: 32 rows a workgroup.
+template <typename T, bool BY_ROWS, int TI, int TJ>
+__global__ void __launch_bounds__(256) join_last_kernel(const GemmArgs a) {
+    RowTiles rows = {};
+    if constexpr (BY_ROWS) rows = count_tiles(a, TI);
+    const unsigned tiles = (BY_ROWS ? (unsigned)rows.total : (unsigned)a.tiles_i) * (unsigned)a.tiles_j;
+    const unsigned whole = tiles / (unsigned)a.slots * (unsigned)a.slots, rest = tiles - whole;
+    if (blockIdx.x >= rest || last_round_parts(rest, (unsigned)a.slots, a.steps) < 2) return;
+    Spot s;
+    if (!find_spot<BY_ROWS, TI, TJ>(a, rows, whole + blockIdx.x, s)) return;
+    constexpr int GROUPS = TJ / 8;
+    const int col = (int)threadIdx.x % GROUPS * 8, j = s.j0 + col;
+    if (j >= a.j) return;
+    const int n = a.j - j;
+    const Some<T, 8> bias = bias_of<T, 8>(a, s.g.group, j);
+    for (int row = (int)(blockIdx.y * 32 + threadIdx.x / GROUPS), k = 0; k < 32; k += 256 / GROUPS, row += 256 / GROUPS) {
+        const int i = s.i0 + row;
+        if (i >= s.i_end) return;
+        float v[8] = {};
+        if (s.g.group >= 0)
+            for (int p = 0; p < s.parts; ++p) {
+                const float* from = a.part + ((uint64_t)s.tile * s.parts + p) * (TI * TJ) + row * TJ + col;
+                const f32x4 lo = *(const f32x4*)from, hi = *(const f32x4*)(from + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] += lo[e];
+                    v[4 + e] += hi[e];
+                }
+            }
+        Some<T, 8> r = {};
+        if (a.residual && s.g.group >= 0) r = load_some<T, 8>((const T*)a.residual + (uint64_t)i * a.residual_ld + j, n);
+        const uint64_t at = (a.out_group ? (uint64_t)s.g.group * a.out_group : 0) + (uint64_t)i * a.out_ld + j;
+        finish<T, 8>(a, s.g.group, n, v, bias, r, (T*)a.z + (uint64_t)i * a.z_ld + j,
+                     (char*)a.out + at * (a.wide_out ? 4 : sizeof(T)));
+    }
+}
+
 // -------------------------------------------------------------------- launching --
 
 template <typename T, bool PA, bool QA, bool BY_ROWS>
 static void launch_form(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
     const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits * (BY_ROWS ? 1u : (unsigned)a.groups);
-    if (p.tile == kTile256) gemm_kernel<T, PA, QA, BY_ROWS, 256, 256, 2, 4><<<grid, 512, 0, s>>>(a);
+    if (p.tile == kTile256) {
+        gemm_kernel<T, PA, QA, BY_ROWS, 256, 256, 2, 4><<<grid + (unsigned)a.slots, 512, 0, s>>>(a);
+        if (a.slots) join_last_kernel<T, BY_ROWS, 256, 256><<<dim3((unsigned)a.slots / 2, 8), 256, 0, s>>>(a);
+    }
     else if (p.tile == kTile128) gemm_kernel<T, PA, QA, BY_ROWS, 128, 128, 2, 2><<<grid, 256, 0, s>>>(a);
     else gemm_kernel<T, PA, QA, BY_ROWS, 64, 64, 2, 2><<<grid, 256, 0, s>>>(a);
 }

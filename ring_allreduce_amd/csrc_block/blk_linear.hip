@@ -30,28 +30,45 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a) {
     float sum[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-    for (int r = lo; r < hi; ++r) {
-        const Vec<T> d = load_vec((const T*)a.dout + (uint64_t)r * a.dout_ld, col, a.n);
-        Vec<T> o;
+    const T* dout = (const T*)a.dout + col;
+    const T* z = a.act != RR_ACT_NONE ? (const T*)a.z + col : dout;
+    const uint64_t z_ld = a.act != RR_ACT_NONE ? a.z_ld : a.dout_ld;
+    const auto row = [&](int r, u32x4 draw, u32x4 zraw) {
+        const Vec<T> d = vec_of<T>(draw), zv = vec_of<T>(zraw);
+        Vec<T> o = d;
         float v[8];
-        if (a.act != RR_ACT_NONE) {
-            const Vec<T> z = load_vec((const T*)a.z + (uint64_t)r * a.z_ld, col, a.n);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = (float)z.e[e];
+        for (int e = 0; e < 8; ++e) v[e] = (float)zv.e[e];
+        if (a.act != RR_ACT_NONE) {
             act_slopes(a.act, v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 v[e] *= (float)d.e[e];
-                sum[e] += v[e];
                 o.e[e] = (T)v[e];
             }
-        } else {
-            o = d;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += (float)d.e[e];
         }
-        // to the last whole vector: zeros follow the row
-        if (a.dz) store_vec((T*)a.dz + (uint64_t)r * a.dz_ld, col, (int)a.dz_ld, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[e];
+        // whole vectors: zeros follow the row
+        if (a.dz) *(u32x4*)((T*)a.dz + (uint64_t)r * a.dz_ld + col) = __builtin_bit_cast(u32x4, o);
+    };
+    if (col + 8 <= a.n) {
+        int r = lo;
+        for (; r + 4 <= hi; r += 4) {
+            u32x4 dv[4], zv[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                dv[u] = load_raw(dout + (uint64_t)(r + u) * a.dout_ld);
+                zv[u] = load_raw(z + (uint64_t)(r + u) * z_ld);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) row(r + u, dv[u], zv[u]);
+        }
+        for (; r < hi; ++r) row(r, load_raw(dout + (uint64_t)r * a.dout_ld), load_raw(z + (uint64_t)r * z_ld));
+    } else {
+        for (int r = lo; r < hi; ++r)
+            row(r, __builtin_bit_cast(u32x4, load_vec(dout + (uint64_t)r * a.dout_ld, 0, a.n - col)),
+                __builtin_bit_cast(u32x4, load_vec(z + (uint64_t)r * z_ld, 0, a.n - col)));
     }
     if (!a.part) return;
     float* to = a.part + ((uint64_t)blockIdx.z * a.splits + blockIdx.y) * a.n;
@@ -60,14 +77,23 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a) {
         if (col + e < a.n) to[col + e] = sum[e];
 }
 
+// 16 columns a workgroup, 16 threads each.
 __global__ void __launch_bounds__(256)
 slope_parts_kernel(const float* part, int splits, int n, float* db) {
-    const int col = (int)blockIdx.x * 256 + (int)threadIdx.x;
-    if (col >= n) return;
-    const float* from = part + (uint64_t)blockIdx.y * splits * n + col;
+    __shared__ float lds[16][17];
+    const int c = threadIdx.x & 15, s = threadIdx.x >> 4, col = (int)blockIdx.x * 16 + c;
+    const float* from = part + (uint64_t)blockIdx.y * splits * n;
     float sum = 0.0f;
-    for (int s = 0; s < splits; ++s) sum += from[(uint64_t)s * n];
-    db[(uint64_t)blockIdx.y * n + col] = sum;
+    if (col < n)
+#pragma unroll 4
+        for (int p = s; p < splits; p += 16) sum += from[(uint64_t)p * n + col];
+    lds[s][c] = sum;
+    __syncthreads();
+    if (s == 0 && col < n) {
+        float all = 0.0f;
+        for (int q = 0; q < 16; ++q) all += lds[q][c];
+        db[(uint64_t)blockIdx.y * n + col] = all;
+    }
 }
 
 // ------------------------------------------------------------------- alignment --
@@ -170,13 +196,16 @@ static uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
 // written and read.  A few rows go through the one-pass form instead, to 64 rows where the
 // contraction is too short for parts to pay (2048 x 1024: 8.6 us against 10.4 for 48 rows;
 // at 8192 deep 40 against 16).
-static GemmPlan choose(const rr_linear_t* a, int form, int* splits) {
+constexpr unsigned kSlots = 256;      // 256 x 256 tiles that a device takes at once: one a compute unit
+
+static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) {
     const uint64_t groups = (uint64_t)a->groups, mean = ceil_div(a->rows, groups);
     const uint64_t i = form == kByW ? a->n : a->rows, j = form == kForward ? a->n : a->k;
     const uint64_t c = form == kForward ? a->k : form == kByX ? a->n : mean;
     const double outputs = (double)(form == kByW ? groups * i : i) * j;
     GemmPlan p = {form, kTile64, 0};
     *splits = 1;
+    *slots = 0;
     if (form == kForward && (mean <= 16 || (mean <= 64 && c <= 1024))) {
         p.tile = mean <= 16 ? kStream16 : mean <= 32 ? kStream32 : kStream64;
         const uint64_t blocks = ceil_div(j, kStreamCols) * ceil_div(a->rows, 16);
@@ -187,13 +216,13 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits) {
     }
     double best = 1e30;
     for (int tile = kTile256; tile <= kTile64; ++tile) {
-        const uint64_t t = tile_rows(tile), slots = tile == kTile256 ? 1 : tile == kTile128 ? 2 : 4;
+        const uint64_t t = tile_rows(tile), each = tile == kTile256 ? 1 : tile == kTile128 ? 2 : 4;
         const uint64_t high = form == kByW ? groups * ceil_div(i, t)
                               : groups == 1 ? ceil_div(i, t) : i / t + ceil_div(groups, 2);
         const uint64_t tiles = (high ? high : 1) * ceil_div(j, t), steps = ceil_div(c, kDepth);
         for (uint64_t s = 1; s <= 32 && (s == 1 || (s <= steps / 2 && tiles * s <= 1024)); s *= 2) {
-            const uint64_t blocks = tiles * s, rounds = ceil_div(blocks, 256 * slots);
-            const uint64_t load = rounds > 1 ? slots : ceil_div(blocks, 256);
+            const uint64_t blocks = tiles * s, rounds = ceil_div(blocks, 256 * each);
+            const uint64_t load = rounds > 1 ? each : ceil_div(blocks, 256);
             const double fill = blocks < 256 ? blocks / 256.0 : 1.0;
             const double start = tile == kTile256 ? 8 : tile == kTile128 ? 6 : 4.5;
             const double step = tile == kTile256   ? 1.4 + 0.35 * fill
@@ -201,10 +230,19 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits) {
                                 : load == 1 ? 0.36 + 0.05 * fill : load == 2 ? 0.6 : load == 3 ? 0.7 : 0.9;
             double time = start * (0.5 + 0.5 * rounds) + rounds * step * ceil_div(steps, s);
             if (s > 1) time += 2.2 + 8.0 * s * outputs / 4.5e6;
+            int last = 0;
+            if (tile == kTile256 && s == 1 && (form != kByW || (groups == 1 && !a->offsets))) {
+                const unsigned rest = (unsigned)(tiles % kSlots);
+                const int parts = last_round_parts(rest, kSlots, (int)steps);
+                // how many tiles uneven groups make is known on the device only
+                if (parts > 1 || (form != kByW && a->offsets && rounds < 16)) last = kSlots;
+                if (parts > 1) time += 4 + 0.12 * rest * parts - step * (steps - ceil_div(steps, parts));
+            }
             if (time < best) {
                 best = time;
                 p.tile = tile;
                 *splits = (int)s;
+                *slots = last;
             }
         }
     }
@@ -234,9 +272,9 @@ struct Product {
 };
 
 static uint64_t product_bytes(const rr_linear_t* a, int form, const Operand& p, const Operand& q) {
-    int splits;
-    const GemmPlan plan = choose(a, form, &splits);
-    uint64_t bytes = 0;
+    int splits, slots;
+    const GemmPlan plan = choose(a, form, &splits, &slots);
+    uint64_t bytes = (uint64_t)slots * 256 * 256 * sizeof(float);
     if (splits > 1) {
         const uint64_t rows = form == kByW ? (uint64_t)a->groups * a->n : a->rows;
         bytes = ceil_div((uint64_t)splits * rows * (form == kForward ? a->n : a->k) * sizeof(float), 256) * 256;
@@ -273,8 +311,8 @@ static rr_status_t pack(Operand& p, Operand& q, char* room, hipStream_t s) {
 
 static rr_status_t run_product(const rr_linear_t* a, Product r, void* workspace, hipStream_t s) {
     GemmArgs& k = r.k;
-    int splits;
-    GemmPlan plan = choose(a, r.form, &splits);
+    int splits, slots;
+    GemmPlan plan = choose(a, r.form, &splits, &slots);
     const uint64_t ti = r.form == kByW ? ceil_div(k.i, tile_rows(plan.tile)) : row_tiles(a, tile_rows(plan.tile));
     const uint64_t tj = ceil_div(k.j, tile_cols(plan.tile));
     if (ti * tj == 0) return RR_OK;
@@ -289,6 +327,12 @@ static rr_status_t run_product(const rr_linear_t* a, Product r, void* workspace,
     }
     char* room = (char*)workspace;
     if (splits > 1) room += ceil_div((uint64_t)splits * k.part_stride * sizeof(float), 256) * 256;
+    if (slots) {
+        k.slots = slots;
+        k.steps = (int32_t)ceil_div(r.form == kByW ? a->rows : (uint64_t)k.c, kDepth);
+        k.part = (float*)workspace;
+        room += (uint64_t)slots * 256 * 256 * sizeof(float);
+    }
     plan.direct = r.p.good() && r.q.good();
     if (plan.tile < kStream16) {
         const rr_status_t st = pack(r.p, r.q, room, s);
@@ -462,7 +506,7 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
             slope_kernel<f16><<<grid, 256, 0, s>>>(k);
         if ((st = launched()) != RR_OK) return st;
         if (g->db) {
-            const dim3 sums((unsigned)ceil_div(a->n, 256), (unsigned)a->groups);
+            const dim3 sums((unsigned)ceil_div(a->n, 16), (unsigned)a->groups);
             slope_parts_kernel<<<sums, 256, 0, s>>>(k.part, k.splits, k.n, g->db);
             if ((st = launched()) != RR_OK) return st;
         }
