@@ -7,29 +7,31 @@ namespace blk {
 
 // ------------------------------------------------------------------- sort --
 //
-// A counting sort.  With P pairs cut into pieces of kPiece consecutive pairs, one
-// wave each:  hist[c][e] = pairs of expert e in piece c;  its exclusive sum over c
-// plus the rank within the piece is the pair's rank.  Within 64 pairs a lane finds
-// the lanes of its own key with one ballot per key bit, so ranks need no atomics
-// between waves and the order is stable.  Three launches (count, sum over pieces,
-// place), or one workgroup for everything while P is small.
+// A counting sort.  The pairs are cut into pieces of kPiece consecutive ones, one wave
+// each, and kSortWaves pieces make a workgroup's share:  hist[g][e] = pairs of expert e in
+// share g;  its exclusive sum over g, plus the counts of the share's earlier waves, plus the
+// rank within the piece is the pair's rank.  Within 64 pairs a lane finds the lanes of its
+// own key with one ballot per key bit, so ranks need no atomics between waves and the
+// order is stable.  Three launches (count, sum over shares, place), or one workgroup for
+// everything while there are few pairs.  65536 x 8 pairs of 256 experts: 16 us, of which the
+// 12 MB that are read and written are 3; the rest is the three launches' chains of latency.
 
 constexpr int kItems = 8;              // pairs per lane
 constexpr int kPiece = 64 * kItems;    // pairs per wave
 constexpr int kSortWaves = 4;          // waves per workgroup of the three-launch form
-constexpr int kOneWaves = 16;          // waves of the one-workgroup form
+constexpr int kOneWaves = 16;          // waves of the one-workgroup form, at most
 
 struct SortArgs {
     const void* ids;
     uint64_t id_ld;
     int32_t pairs, k, experts, bits;
     int32_t capacity;
-    int32_t rows, pieces;
+    int32_t rows, shares;
     int32_t* slots;
     int32_t* sources;
     int32_t* counts;
     int32_t* offsets;
-    int32_t* hist;      // [pieces][experts]
+    int32_t* hist;      // [shares][experts]
 };
 
 template <typename I>
@@ -82,84 +84,114 @@ __device__ __forceinline__ void place_piece(const SortArgs& a, const int* key, i
     }
 }
 
+__device__ __forceinline__ int lanes_upto(int n) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(n, d);
+        if (lane >= d) n += up;
+    }
+    return n;
+}
+
 // start[e] = counts[0] + .. + counts[e - 1] in LDS, by the whole workgroup.
 __device__ __forceinline__ void prefix_counts(const int* counts, int* start, int experts) {
     if (threadIdx.x < 64) {
-        int before = 0;
-        for (int e0 = 0; e0 < experts; e0 += 64) {
-            const int e = e0 + (int)threadIdx.x;
-            const int n = e < experts ? counts[e] : 0;
-            int sum = n;
+        const int lane = threadIdx.x;
+        int n[RR_MAX_EXPERTS / 64];
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int up = __shfl_up(sum, d);
-                if ((int)threadIdx.x >= d) sum += up;
-            }
-            if (e < experts) start[e] = before + sum - n;
-            before += __shfl(sum, 63);
+        for (int q = 0; q < RR_MAX_EXPERTS / 64; ++q) n[q] = q * 64 + lane < experts ? counts[q * 64 + lane] : 0;
+        int before = 0;
+#pragma unroll
+        for (int q = 0; q < RR_MAX_EXPERTS / 64; ++q) {
+            if (q * 64 >= experts) break;
+            const int upto = lanes_upto(n[q]);
+            if (q * 64 + lane < experts) start[q * 64 + lane] = before + upto - n[q];
+            before += __shfl(upto, 63);
         }
-        if (threadIdx.x == 0) start[experts] = before;
+        if (lane == 0) start[experts] = before;
     }
     __syncthreads();
 }
 
 // offsets, and -1 in the rows no pair has.
-__device__ __forceinline__ void fill_unused(const SortArgs& a, const int* counts, const int* start,
-                                            int thread, int threads) {
-    for (int e = thread; e <= a.experts; e += threads)
-        a.offsets[e] = a.capacity ? e * a.capacity : start[e];
+__device__ __forceinline__ void fill_unused(const SortArgs& a, const int* counts, const int* start) {
+    const int threads = (int)blockDim.x, thread = (int)threadIdx.x;
+    if (blockIdx.x == 0)
+        for (int e = thread; e <= a.experts; e += threads) a.offsets[e] = a.capacity ? e * a.capacity : start[e];
     if (a.capacity == 0) {
-        for (int r = start[a.experts] + thread; r < a.rows; r += threads) a.sources[r] = -1;
+        for (int64_t r = (int64_t)start[a.experts] + (int64_t)blockIdx.x * threads + thread; r < a.rows;
+             r += (int64_t)gridDim.x * threads)
+            a.sources[r] = -1;
         return;
     }
-    for (int r = thread; r < a.rows; r += threads) {
-        const int e = (int)((uint32_t)r / (uint32_t)a.capacity);
-        if (r - e * a.capacity >= counts[e]) a.sources[r] = -1;
-    }
+    for (int e = (int)blockIdx.x; e < a.experts; e += (int)gridDim.x)
+        for (int64_t r = (int64_t)min(counts[e], a.capacity) + thread; r < a.capacity; r += threads)
+            a.sources[(int64_t)e * a.capacity + r] = -1;
+}
+
+// The waves' counts of their keys: mine[e] of each, all zero before.
+__device__ __forceinline__ void count_keys(const SortArgs& a, const int* key, int* mine) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+        if (key[i] < a.experts) atomicAdd(&mine[key[i]], 1);
 }
 
 template <typename I>
 __global__ void __launch_bounds__(64 * kSortWaves) sort_count_kernel(const SortArgs a) {
     extern __shared__ int lds[];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    int* mine = lds + wave * a.experts;
-    for (int e = lane; e < a.experts; e += 64) mine[e] = 0;
-    __syncthreads();
-    const int piece = blockIdx.x * kSortWaves + wave;
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) lds[e] = 0;
+    const int piece = blockIdx.x * kSortWaves + (threadIdx.x >> 6);
     int key[kItems];
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) key[i] = key_of<I>(a, piece * kPiece + i * 64 + lane);
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-        if (key[i] < a.experts) atomicAdd(&mine[key[i]], 1);
+    for (int i = 0; i < kItems; ++i) key[i] = key_of<I>(a, piece * kPiece + i * 64 + (int)(threadIdx.x & 63));
     __syncthreads();
-    if (piece < a.pieces)
-        for (int e = lane; e < a.experts; e += 64)
-            a.hist[(uint64_t)piece * a.experts + e] = mine[e];
+    count_keys(a, key, lds);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
+        a.hist[(uint64_t)blockIdx.x * a.experts + e] = lds[e];
 }
 
-// Exclusive sum of hist over the pieces: a workgroup takes 16 experts, 64 threads each.
-__global__ void __launch_bounds__(1024) sort_sum_kernel(const SortArgs a) {
-    __shared__ int part[64][17];
-    const int e = blockIdx.x * 16 + (threadIdx.x & 15), s = threadIdx.x >> 4;
-    const int per = (a.pieces + 63) / 64;
-    const int lo = s * per, hi = min(lo + per, a.pieces);
-    int sum = 0;
-    if (e < a.experts)
-        for (int c = lo; c < hi; ++c) sum += a.hist[(uint64_t)c * a.experts + e];
-    part[s][threadIdx.x & 15] = sum;
-    __syncthreads();
+// Exclusive sum of hist over the shares: a wave an expert, a lane four shares at a time.
+__global__ void __launch_bounds__(256) sort_sum_kernel(const SortArgs a) {
+    const int e = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (e >= a.experts) return;
     int before = 0;
-    for (int q = 0; q < s; ++q) before += part[q][threadIdx.x & 15];
-    if (e < a.experts) {
-        for (int c = lo; c < hi; ++c) {
-            const uint64_t at = (uint64_t)c * a.experts + e;
-            const int n = a.hist[at];
-            a.hist[at] = before;
-            before += n;
+    for (int64_t c0 = 0; c0 < a.shares; c0 += 256) {
+        int n[4], sum = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t c = c0 + lane * 4 + u;
+            n[u] = c < a.shares ? a.hist[(uint64_t)c * a.experts + e] : 0;
         }
-        if (s == 63) a.counts[e] = before;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sum += n[u];
+        const int upto = lanes_upto(sum);
+        int at = before + upto - sum;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t c = c0 + lane * 4 + u;
+            if (c < a.shares) a.hist[(uint64_t)c * a.experts + e] = at;
+            at += n[u];
+        }
+        before += __shfl(upto, 63);
     }
+    if (lane == 0) a.counts[e] = before;
+}
+
+// base[w][e]: counts of the waves -> rank of wave w's first pair of expert e; the counts of
+// all waves come to `all`, if given.
+__device__ __forceinline__ void ranks_of_waves(int* base, int waves, int experts, const int* before, int* all) {
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) {
+        int at = before ? before[e] : 0;
+        for (int w = 0; w < waves; ++w) {
+            const int n = base[w * experts + e];
+            base[w * experts + e] = at;
+            at += n;
+        }
+        if (all) all[e] = at;
+    }
+    __syncthreads();
 }
 
 template <typename I>
@@ -167,52 +199,41 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_place_kernel(const SortA
     extern __shared__ int lds[];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     int* start = lds;                                  // experts + 1
-    int* base = lds + a.experts + 1 + wave * a.experts;
+    int* base = lds + a.experts + 1;                   // [kSortWaves][experts]
+    for (int i = threadIdx.x; i < kSortWaves * a.experts; i += blockDim.x) base[i] = 0;
     const int piece = blockIdx.x * kSortWaves + wave;
     int key[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) key[i] = key_of<I>(a, piece * kPiece + i * 64 + lane);
-    if (piece < a.pieces)
-        for (int e = lane; e < a.experts; e += 64)
-            base[e] = a.hist[(uint64_t)piece * a.experts + e];
-    prefix_counts(a.counts, start, a.experts);
-    if (piece < a.pieces) place_piece(a, key, piece * kPiece, base, start);
-    fill_unused(a, a.counts, start, blockIdx.x * blockDim.x + threadIdx.x,
-                gridDim.x * blockDim.x);
+    __syncthreads();
+    count_keys(a, key, base + wave * a.experts);
+    if (a.capacity == 0) prefix_counts(a.counts, start, a.experts);
+    else __syncthreads();
+    ranks_of_waves(base, kSortWaves, a.experts, a.hist + (uint64_t)blockIdx.x * a.experts, nullptr);
+    place_piece(a, key, piece * kPiece, base + wave * a.experts, start);
+    fill_unused(a, a.counts, start);
 }
 
 // Everything in one workgroup: wave w takes piece w.
 template <typename I>
 __global__ void __launch_bounds__(64 * kOneWaves) sort_one_kernel(const SortArgs a) {
     extern __shared__ int lds[];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = (int)blockDim.x >> 6;
     int* counts = lds;                                 // experts
     int* start = lds + a.experts;                      // experts + 1
-    int* base = lds + 2 * a.experts + 1;               // [kOneWaves][experts]
-    for (int i = threadIdx.x; i < kOneWaves * a.experts; i += blockDim.x) base[i] = 0;
+    int* base = lds + 2 * a.experts + 1;               // [waves][experts]
+    for (int i = threadIdx.x; i < waves * a.experts; i += blockDim.x) base[i] = 0;
     int key[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) key[i] = key_of<I>(a, wave * kPiece + i * 64 + lane);
     __syncthreads();
-    int* mine = base + wave * a.experts;
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-        if (key[i] < a.experts) atomicAdd(&mine[key[i]], 1);
+    count_keys(a, key, base + wave * a.experts);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
-        int before = 0;
-        for (int w = 0; w < kOneWaves; ++w) {
-            const int n = base[w * a.experts + e];
-            base[w * a.experts + e] = before;
-            before += n;
-        }
-        counts[e] = before;
-        a.counts[e] = before;
-    }
-    __syncthreads();
-    prefix_counts(counts, start, a.experts);
-    place_piece(a, key, wave * kPiece, mine, start);
-    fill_unused(a, counts, start, threadIdx.x, blockDim.x);
+    ranks_of_waves(base, waves, a.experts, nullptr, counts);
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) a.counts[e] = counts[e];
+    if (a.capacity == 0) prefix_counts(counts, start, a.experts);
+    place_piece(a, key, wave * kPiece, base + wave * a.experts, start);
+    fill_unused(a, counts, start);
 }
 
 // --------------------------------------------------------------- row moves --
@@ -440,7 +461,7 @@ static rr_status_t check_sort(size_t tokens, int k, int experts, size_t capacity
     return RR_OK;
 }
 
-static uint64_t sort_pieces(uint64_t pairs) { return ceil_div(pairs, kPiece); }
+static uint64_t sort_shares(uint64_t pairs) { return ceil_div(pairs, kPiece * kSortWaves); }
 // base, counts and start of every expert in the LDS of one workgroup
 static bool one_workgroup(uint64_t pairs, int experts) {
     return pairs <= (uint64_t)kPiece * kOneWaves && experts <= 512;
@@ -449,13 +470,14 @@ static bool one_workgroup(uint64_t pairs, int experts) {
 template <typename I> static rr_status_t run_sort(const SortArgs& a, hipStream_t s) {
     const size_t word = sizeof(int32_t);
     if (one_workgroup((uint64_t)a.pairs, a.experts)) {
-        const size_t lds = ((kOneWaves + 2) * (size_t)a.experts + 1) * word;
-        sort_one_kernel<I><<<1, 64 * kOneWaves, lds, s>>>(a);
+        const unsigned pieces = (unsigned)ceil_div(a.pairs, kPiece), waves = pieces < 4 ? 4 : pieces;
+        const size_t lds = ((waves + 2) * (size_t)a.experts + 1) * word;
+        sort_one_kernel<I><<<1, 64 * waves, lds, s>>>(a);
         return launched();
     }
-    const unsigned grid = (unsigned)ceil_div(a.pieces, kSortWaves);
-    sort_count_kernel<I><<<grid, 64 * kSortWaves, kSortWaves * a.experts * word, s>>>(a);
-    sort_sum_kernel<<<(unsigned)ceil_div(a.experts, 16), 1024, 0, s>>>(a);
+    const unsigned grid = (unsigned)a.shares;
+    sort_count_kernel<I><<<grid, 64 * kSortWaves, a.experts * word, s>>>(a);
+    sort_sum_kernel<<<(unsigned)ceil_div(a.experts, 4), 256, 0, s>>>(a);
     const size_t lds = ((kSortWaves + 1) * (size_t)a.experts + 1) * word;
     sort_place_kernel<I><<<grid, 64 * kSortWaves, lds, s>>>(a);
     return launched();
@@ -546,7 +568,7 @@ rr_status_t expert_sort_workspace(size_t tokens, int k, int experts, size_t* byt
     const rr_status_t st = check_sort(tokens, k, experts, 0);
     if (st != RR_OK) return st;
     const uint64_t pairs = (uint64_t)tokens * k;
-    *bytes = one_workgroup(pairs, experts) ? 0 : sort_pieces(pairs) * experts * sizeof(int32_t);
+    *bytes = one_workgroup(pairs, experts) ? 0 : sort_shares(pairs) * experts * sizeof(int32_t);
     return RR_OK;
 }
 
@@ -584,7 +606,7 @@ rr_status_t expert_sort(const void* ids, int id_bytes, size_t id_ld, size_t toke
     while ((1 << a.bits) <= experts) ++a.bits;      // keys 0 .. experts
     a.capacity = (int32_t)capacity;
     a.rows = (int32_t)rows;
-    a.pieces = (int32_t)sort_pieces(pairs);
+    a.shares = (int32_t)sort_shares(pairs);
     a.slots = slots;
     a.sources = sources;
     a.counts = counts;
