@@ -1,0 +1,168 @@
+"""A block's operators at the sizes where another kernel or another way through it is taken: large
+tiles, the last round of tiles cut along the contraction, operands that have to be copied, rows
+of every register layout, many rows a workgroup, k beyond one batch of rows."""
+import numpy as np
+import pytest
+import torch
+
+from tests.block_util import DTYPES, U, assert_within, store_error, strided
+from tests.test_gpu_block_linear import check_backward, check_forward, make
+from tests.test_gpu_block_norm import EPS, STEPS, backward64, forward64, own_args, wide
+from tests.test_gpu_block_norm import make as make_norm
+from tests.test_gpu_expert import check_order, gathered64, make_ids, order_of, setup, spread64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def rr():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import ring_allreduce_amd
+    return ring_allreduce_amd
+
+
+@pytest.mark.parametrize("rows,n,k,dtype,act", [
+    (4090, 4088, 520, "bf16", "silu"),       # one round of 256 x 256 tiles, edges in both directions
+    (4350, 4090, 2048, "bf16", "none"),      # a second round of few: cut along the contraction
+    (2050, 8200, 1032, "fp16", "relu"), (8200, 2056, 1040, "bf16", "gelu")])
+def test_large_tiles(rr, rows, n, k, dtype, act):
+    d = make(rows, n, k, None, dtype, True, True)
+    check_forward(rr, d, None, act, DTYPES[dtype])
+    check_backward(rr, d, None, act, DTYPES[dtype])
+
+
+@pytest.mark.parametrize("sizes,before,after,n,k", [
+    ([1500, 0, 2300, 700], 3, 90, 4096, 1032), ([5000, 3300], 0, 0, 2048, 2048),
+    ([100] * 80, 1, 0, 1032, 520), ([4000, 4000], 0, 200, 2056, 2056)], ids=lambda v: str(v)[:24])
+def test_large_groups(rr, sizes, before, after, n, k):
+    rows = before + sum(sizes) + after
+    off = torch.from_numpy(before + np.concatenate([[0], np.cumsum(sizes)])).to(torch.int32).cuda()
+    d = make(rows, n, k, len(sizes), "bf16", True, True)
+    check_forward(rr, d, off, "silu", torch.bfloat16)
+    check_backward(rr, d, off, "silu", torch.bfloat16)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_operands_to_copy(rr, act):
+    """Odd widths, rows at odd elements and groups at odd distances, past which there is NaN."""
+    rows, n, k = 700, 391, 453
+    off = torch.tensor([0, 300, 333, 700], dtype=torch.int32, device="cuda")
+    d = make(rows, n, k, 3, "bf16", True, False)
+    want = rr.block_linear(d["x"], d["w"], d["bias"], act=act, offsets=off)
+    grads = rr.block_linear_backward(d["dout"], d["x"], d["w"], d["z"], act=act, offsets=off)
+    store = torch.full((3, n * (k + 4) + 7), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w = store.as_strided((3, n, k), (n * (k + 4) + 7, k + 4, 1), 0)
+    w.copy_(d["w"])
+    d2 = dict(d, x=strided(d["x"], 5, offset=3)[0], w=w, dout=strided(d["dout"], 1, offset=1)[0],
+              z=strided(d["z"], 3)[0])
+    assert torch.equal(rr.block_linear(d2["x"], w, d["bias"], act=act, offsets=off), want)
+    again = rr.block_linear_backward(d2["dout"], d2["x"], w, d2["z"], act=act, offsets=off)
+    for name in ("dx", "dw", "db"):
+        assert torch.equal(getattr(again, name), getattr(grads, name)), name
+    check_forward(rr, d2, off, act, torch.bfloat16)
+    check_backward(rr, d2, off, act, torch.bfloat16)
+
+
+def test_few_rows_long_contraction(rr):
+    """The one-pass form cut along the contraction, and at the rows where it ends."""
+    for rows in (1, 16, 17, 33, 64, 65):
+        for n, k in ((40, 8192), (520, 4104), (33, 2051)):
+            d = make(rows, n, k, None, "bf16", True, True)
+            check_forward(rr, d, None, "silu", torch.bfloat16)
+
+
+NORM = [  # tokens, hidden, gate, act, post, pre, weights
+    (5000, 520, "element", "silu", True, True, "same"), (9000, 72, "channel", "sigmoid", True, True, "fp32"),
+    (3000, 1030, "channel", "silu", True, True, "same"), (1500, 4104, "element", "sigmoid", True, True, "same"),
+    (700, 8200, "channel", "none", True, True, "same"), (600, 12296, "channel", "silu", True, True, "fp32"),
+    (40, 16383, "element", "none", True, True, "same"), (300, 9, "element", "silu", False, True, "none"),
+    (11, 32767, "none", "none", True, False, "none")]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("case", NORM, ids=str)
+def test_norm_layouts(rr, dtype, case):
+    tokens, hidden, gate, act, post, pre, weights = case
+    d = make_norm(tokens, hidden, dtype, gate, weights, 2)
+    c, args = own_args(d, act, post, pre)
+    dt = DTYPES[dtype]
+    h, y = rr.block_norm(c["x"], c["branch"], **args)
+    w = wide(d)
+    rh, sh, ry, sy = forward64(w, act, post, pre)
+    assert_within(h.cpu(), rh, store_error(rh, dt) + STEPS * U * sh, "h")
+    if pre:
+        assert_within(y.cpu(), ry, store_error(ry, dt) + STEPS * U * sy, "y")
+    got = rr.block_norm_backward(c["dh"], c["dy"] if pre else None, c["h"], c["branch"], **args)
+    ref, size = backward64(w, act, post, pre)
+    for name in ("dx", "dbranch", "dgate", "dpost_weight", "dpre_weight"):
+        g = getattr(got, name)
+        if g is None:
+            assert name not in ref or weights == "none" and "weight" in name, name
+            continue
+        bound = (STEPS + tokens) * U * size[name] if g.dim() == 1 else \
+            store_error(ref[name], dt) + STEPS * U * size[name]
+        assert_within(g.cpu(), ref[name], bound, name)
+
+
+def test_norm_without_what_is_optional(rr):
+    """No gradient by the stream, no branch, no norm: what is absent counts as zero."""
+    d = make_norm(50, 1000, "bf16", "none", "same")
+    c, args = own_args(d, "none", True, True)
+    zero = torch.zeros_like(c["dh"])
+    a = rr.block_norm_backward(None, c["dy"], c["h"], c["branch"], **args)
+    b = rr.block_norm_backward(zero, c["dy"], c["h"], c["branch"], **args)
+    for name in ("dx", "dbranch", "dpost_weight", "dpre_weight"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
+    only = rr.block_norm_backward(c["dh"], None, None, None, post_norm=False, pre_norm=False,
+                                  residual_scale=0.5)
+    assert torch.equal(only.dx, (c["dh"].float() * 0.5).bfloat16())
+    h, y = rr.block_norm(c["x"], None, post_norm=False, pre_norm=False, residual_scale=2.0, eps=EPS)
+    assert y is None and torch.equal(h, (c["x"].float() * 2).bfloat16())
+    c["branch"][7] = float("inf")
+    h, _ = rr.block_norm(c["x"], None, post_norm=False, pre_norm=False)
+    assert torch.equal(h, c["x"])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("shape", [(300, 1030, 12, 20, 0, "masked"), (90, 4104, 17, 40, 5, "any"),
+                                   (500, 40, 3, 16, 300, "masked"), (70, 3, 2, 6, 90, "any")], ids=str)
+def test_moves(rr, dtype, shape):
+    """More rows a token than are summed at a time; many unused rows."""
+    tokens, hidden, k = shape[:3]
+    slots, sources, ds, dq, x, rows, weights = setup(rr, *shape, dtype)
+    assert torch.equal(rr.expert_dispatch(x.cuda(), ds, dq).cpu().double(), spread64(x, sources, k))
+    unused = torch.ones(len(rows), dtype=torch.bool)
+    unused[torch.from_numpy(slots[slots >= 0])] = False
+    rows[unused] = float("nan")                     # rows without a pair do not count
+    got = rr.expert_combine(rows.cuda(), ds, weights.cuda()).cpu()
+    terms = gathered64(rows, slots) * weights[..., None].double()
+    assert_within(got, terms.sum(1), store_error(terms.sum(1), DTYPES[dtype]) +
+                  2 * k * U * terms.abs().sum(1), "out")
+    drows, dweights = rr.expert_combine_backward(x.cuda(), rows.cuda(), ds, dq, weights.cuda())
+    ref = spread64(x, sources, k, weights)
+    assert_within(drows.cpu(), ref, store_error(ref, DTYPES[dtype]) + U * ref.abs(), "drows")
+    terms = gathered64(rows, slots) * x[:, None].double()
+    steps = -(-hidden // 64) + 8 + 10
+    assert_within(dweights.cpu(), terms.sum(2), steps * U * terms.abs().sum(2), "dweights")
+
+
+def test_no_rows(rr):
+    """Nothing to move: every pair without a slot, and no rows at all."""
+    x = torch.randn(5, 72, device="cuda").bfloat16()
+    slots = torch.full((5, 3), -1, dtype=torch.int32, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert rr.expert_dispatch(x, slots, none).shape == (0, 72)
+    empty = torch.empty(0, 72, dtype=torch.bfloat16, device="cuda")
+    assert not bool(rr.expert_combine(empty, slots).any())
+    drows, dweights = rr.expert_combine_backward(x, empty, slots, none)
+    assert drows.shape == (0, 72) and not bool(dweights.any())
+
+
+@pytest.mark.parametrize("tokens,k,experts,capacity,kind", [
+    (8193, 1, 1024, 9, "any"), (70000, 4, 256, 1200, "masked"), (300000, 1, 3, 0, "masked"),
+    (40000, 2, 1024, 0, "one"), (2048, 4, 512, 0, "masked"), (2049, 4, 512, 17, "any")])
+def test_sort_sizes(rr, tokens, k, experts, capacity, kind):
+    ids = make_ids(tokens, k, experts, kind, tokens)
+    check_order(rr.expert_sort(torch.from_numpy(ids).cuda(), experts, capacity),
+                order_of(ids, experts, capacity))
