@@ -4,7 +4,9 @@ Tokens sorted by expert and moved to the AlltoAll's blocks and back, the norms
 around a block, and a block's matrix products, with their gradients, as declared
 in ``include/rr.h``.  Like the rest of the binding this only marshals: it checks
 shapes and types, makes output and scratch tensors, and calls the library; there
-is no fallback.
+is no fallback.  Calls in their usual form (on the current device and stream, new
+outputs) are marshalled by the module ``_block``, in C++; what it does not take it
+leaves to the Python here, which also says what is wrong with a call.
 
 Every call runs on ``stream`` (default: torch's current stream of the tensors'
 device); the outputs and scratch it allocates belong to that stream.  Matrices may
@@ -60,9 +62,12 @@ class _LinearGrad(ctypes.Structure):
 
 
 def _bind(sig):
-    """Declares the library's functions with the binding's ``sig``; called once."""
+    """Declares the library's functions with the binding's ``sig``; called once, when
+    librr.so is loaded."""
     p = ctypes.POINTER
     g = globals()
+    from . import _block
+    g["_block"] = _block
     g["_expert_sort"] = sig("expert_sort", _i, _vp, _i, _sz, _sz, _i, _i, _sz, _vp, _vp, _vp, _vp,
                             _vp, _sz, _vp)
     g["_expert_sort_workspace"] = sig("expert_sort_workspace", _i, _sz, _i, _i, p(_sz))
@@ -228,6 +233,10 @@ def expert_sort(ids, experts: int, capacity: int = 0, *, stream=None) -> ExpertO
     stably.  Ids outside [0, experts) are masked out.  ``capacity`` 0 packs the experts'
     rows one after another (tokens * k rows); otherwise every expert has ``capacity``
     rows and later pairs are dropped."""
+    if stream is None:
+        done = _block.sort(ids, experts, capacity)
+        if done is not None:
+            return ExpertOrder(*done)
     _need(isinstance(ids, torch.Tensor) and ids.dim() == 2, "ids must be a matrix")
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"ids must be int32 or int64, not {ids.dtype}")
@@ -259,6 +268,10 @@ def _pairs(slots, name="slots"):
 def expert_dispatch(x, slots, sources, *, out=None, stream=None):
     """Copies each token's row to the rows of its slots: [len(sources), hidden].  Rows
     without a source become zero."""
+    if stream is None and out is None:
+        done = _block.dispatch(x, slots, sources)
+        if done is not None:
+            return done
     dt = _float_type(x, "x")
     xr = _matrix(x, "x")
     tokens, k = _pairs(slots)
@@ -277,6 +290,10 @@ def expert_dispatch(x, slots, sources, *, out=None, stream=None):
 def expert_combine(rows, slots, weights=None, *, out=None, stream=None):
     """Sum of each token's rows, times ``weights`` [tokens, k] (fp32; None: all 1), in the
     order of its choices: [tokens, hidden]."""
+    if stream is None and out is None:
+        done = _block.combine(rows, slots, weights)
+        if done is not None:
+            return done
     dt = _float_type(rows, "rows")
     r = _matrix(rows, "rows")
     tokens, k = _pairs(slots)
@@ -302,6 +319,10 @@ def expert_combine_backward(dout, rows, slots, sources, weights=None, *, need_ro
                             need_weights=True, out=None, stream=None):
     """Gradients of ``expert_combine``: (drows [len(sources), hidden] in the rows' type,
     dweights [tokens, k] in fp32); what is not needed is None."""
+    if stream is None and out is None:
+        done = _block.combine_backward(dout, rows, slots, sources, weights, need_rows, need_weights)
+        if done is not None:
+            return done
     dt = _float_type(dout, "dout")
     tokens, k = _pairs(slots)
     d = _matrix(dout, "dout", None, None, tokens)
@@ -374,6 +395,11 @@ def block_norm(x, branch=None, *, post_norm=True, post_weight=None, gate=None, g
     v / sqrt(mean(v^2) + eps).  ``gate`` is [hidden] or [tokens, hidden].  Returns (h, y);
     y is None without pre_norm.  Without a branch, pass post_norm=False; h is then
     residual_scale * x.  ``h`` may be x itself and ``y`` the branch (in place)."""
+    if stream is None and h is None and y is None:
+        done = _block.norm(x, branch, post_norm, post_weight, gate, ACTS.get(gate_act, -1),
+                           residual_scale, branch_scale, pre_norm, pre_weight, eps)
+        if done is not None:
+            return done
     xr = _matrix(x, "x")
     a = _norm_args(x, branch, post_norm, post_weight, gate, gate_act, residual_scale, branch_scale,
                    pre_norm, pre_weight, eps)
@@ -405,13 +431,22 @@ class NormGrads:
     dpre_weight: torch.Tensor | None = None
 
 
+NORM_GRADS = ("dx", "dbranch", "dgate", "dpost_weight", "dpre_weight")
+
+
 def block_norm_backward(dh, dy, h, branch=None, *, post_norm=True, post_weight=None, gate=None,
                         gate_act="none", residual_scale=1.0, branch_scale=1.0, pre_norm=True,
-                        pre_weight=None, eps=1e-6, need=("dx", "dbranch", "dgate", "dpost_weight",
-                                                         "dpre_weight"), stream=None) -> NormGrads:
+                        pre_weight=None, eps=1e-6, need=NORM_GRADS, stream=None) -> NormGrads:
     """Gradients of ``block_norm`` with the same arguments.  ``dh`` and ``dy`` are the
     gradients by h and y (dh None: zero; dy None without pre_norm); ``h`` is the stream
     that block_norm returned (not read without pre_norm)."""
+    if stream is None:
+        wanted = 31 if need is NORM_GRADS else sum(1 << i for i, n in enumerate(NORM_GRADS) if n in need)
+        done = _block.norm_backward(dh, dy, h, branch, post_norm, post_weight, gate,
+                                    ACTS.get(gate_act, -1), residual_scale, branch_scale, pre_norm,
+                                    pre_weight, eps, wanted)
+        if done is not None:
+            return NormGrads(*done)
     like = next((t for t in (dh, dy, h, branch) if t is not None), None)
     _need(like is not None and like.dim() == 2, "dh, dy or h must be given")
     a = _norm_args(like, branch, post_norm, post_weight, gate, gate_act, residual_scale,
@@ -492,6 +527,10 @@ def block_linear(x, w, bias=None, *, act="none", residual=None, offsets=None, sa
     ``expert_sort`` gives them, or None for equal groups.  Rows of no group become zero.
     Returns out, or (out, z) with the pre-activation z = x w^T + bias that
     ``block_linear_backward`` needs if save_preact.  ``residual`` may be ``out``."""
+    if stream is None and out is None:
+        done = _block.linear(x, w, bias, ACTS.get(act, -1), residual, offsets, save_preact)
+        if done is not None:
+            return done
     a = _linear_args(x, w, offsets, act)
     dev, shape = x.device, (x.shape[0], a.n)
     a.bias = _row(bias, "bias", dev, x.dtype, a.groups * a.n)
@@ -525,6 +564,11 @@ def block_linear_backward(dout, x, w, z=None, *, act="none", offsets=None, need_
     """Gradients of ``block_linear`` by x, w and bias (the residual's is dout itself).
     ``z`` is the saved pre-activation, needed if act is set; ``dw_dtype`` x's dtype
     (default) or float32."""
+    if stream is None and dw_dtype in (None, torch.float32):
+        done = _block.linear_backward(dout, x, w, z, ACTS.get(act, -1), offsets, need_dx, need_dw,
+                                      need_db, dw_dtype is not None)
+        if done is not None:
+            return LinearGrads(*done)
     a = _linear_args(x, w, offsets, act)
     dev = x.device
     g, out = _LinearGrad(), LinearGrads()

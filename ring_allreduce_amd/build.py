@@ -12,6 +12,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BLOCK = os.path.join(HERE, "csrc_block")  # a block's operators between two collectives
 LIB = os.path.join(HERE, "librr.so")
+# the Python module that marshals the usual calls of a block's operators; links librr.so
+BINDING_SOURCE = os.path.join(BLOCK, "blk_binding.cpp")
+BINDING = os.path.join(HERE, "_block.so")
 # one translation unit per kernel family (the in-place ring: one per element
 # type), and the host side with the C ABI
 SOURCES = [os.path.join(CSRC, f) for f in
@@ -57,8 +60,8 @@ def _version_script(path: str) -> str:
 
 def build(force: bool = True, verbose: bool = False) -> str:
     """Compile every HIP source (in parallel) and link ring_allreduce_amd/librr.so."""
-    newest = max(os.path.getmtime(p) for p in SOURCES + HEADERS)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
+    newest = max(os.path.getmtime(p) for p in SOURCES + HEADERS + [BINDING_SOURCE])
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in (LIB, BINDING)):
         return LIB
     include = ["-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", BLOCK]
     with tempfile.TemporaryDirectory(prefix="rr_build_") as tmpdir:
@@ -81,7 +84,32 @@ def build(force: bool = True, verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile and link the module ring_allreduce_amd._block against librr.so and torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = [os.path.join(ROOT, "include"), *cpp_extension.include_paths(),
+                sysconfig.get_paths()["include"],
+                os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include")]
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [HIPCC, "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-DUSE_ROCM=1",
+           "-D__HIP_PLATFORM_AMD__=1",         # host code: what hipcc defines for device code
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           *("-I" + p for p in includes), "-x", "c++", BINDING_SOURCE, "-o", tmp,
+           "-L" + HERE, "-lrr", "-L" + torch_lib, "-lc10", "-lc10_hip", "-ltorch_cpu",
+           "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
