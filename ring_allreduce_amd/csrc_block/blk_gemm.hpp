@@ -817,6 +817,7 @@ template <typename T> __global__ void __launch_bounds__(256) join_kernel(const G
     }
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (group >= 0)
+#pragma unroll 8
         for (int s = 0; s < a.splits; ++s) {
             const float* from = a.part + (uint64_t)s * a.part_stride + row * a.j + j;
             const Some<float, 4> p = load_some<float, 4>(from, a.j - j);

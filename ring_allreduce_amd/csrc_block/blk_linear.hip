@@ -9,22 +9,25 @@ namespace blk {
 //
 // dz = dout act'(z), rounded to the rows' type as the next products' operand (or dout as
 // it is, where its rows cannot be loaded in 16-byte pieces), and the column sums of each
-// group in 32 bits.  A workgroup takes 8 columns a thread and one
-// of `splits` parts of a group's rows; the parts are added in a fixed order.
+// group in 32 bits.  A thread takes 8 columns; a workgroup takes
+// as many threads across as the columns need, the rest along the rows, and one of `splits`
+// parts of a group's rows; the sums are added in a fixed order.
 struct SlopeArgs {
     GemmArgs g;            // rows, groups, offsets
     const void *dout, *z;
     void* dz;              // or null: nothing but the sums
     uint64_t dout_ld, z_ld, dz_ld;
     float* part;           // [groups][splits][n], or null
-    int32_t n, act, splits;
+    int32_t n, act, splits, threads;
 };
 
 template <typename T>
 __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a) {
-    const int col = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 8;
+    __shared__ float lds[8][256];
+    const int wide = a.threads, high = 256 / wide;      // threads across and along the rows
+    const int x = (int)threadIdx.x % wide, y = (int)threadIdx.x / wide;
+    const int col = ((int)blockIdx.x * wide + x) * 8;
     const Range g = range_of(a.g, (int)blockIdx.z + 1);
-    if (col >= a.n) return;
     const int per = (g.hi - g.lo + a.splits - 1) / a.splits;
     const int lo = g.lo + min((int)blockIdx.y * per, g.hi - g.lo), hi = min(lo + per, g.hi);
     float sum[8];
@@ -53,24 +56,34 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a) {
         if (a.dz) *(u32x4*)((T*)a.dz + (uint64_t)r * a.dz_ld + col) = __builtin_bit_cast(u32x4, o);
     };
     if (col + 8 <= a.n) {
-        int r = lo;
-        for (; r + 4 <= hi; r += 4) {
+        int r = lo + y;
+        for (; r + 3 * high < hi; r += 4 * high) {
             u32x4 dv[4], zv[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                dv[u] = load_raw(dout + (uint64_t)(r + u) * a.dout_ld);
-                zv[u] = load_raw(z + (uint64_t)(r + u) * z_ld);
+                dv[u] = load_raw(dout + (uint64_t)(r + u * high) * a.dout_ld);
+                zv[u] = load_raw(z + (uint64_t)(r + u * high) * z_ld);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) row(r + u, dv[u], zv[u]);
+            for (int u = 0; u < 4; ++u) row(r + u * high, dv[u], zv[u]);
         }
-        for (; r < hi; ++r) row(r, load_raw(dout + (uint64_t)r * a.dout_ld), load_raw(z + (uint64_t)r * z_ld));
-    } else {
-        for (int r = lo; r < hi; ++r)
+        for (; r < hi; r += high)
+            row(r, load_raw(dout + (uint64_t)r * a.dout_ld), load_raw(z + (uint64_t)r * z_ld));
+    } else if (col < a.n) {
+        for (int r = lo + y; r < hi; r += high)
             row(r, __builtin_bit_cast(u32x4, load_vec(dout + (uint64_t)r * a.dout_ld, 0, a.n - col)),
                 __builtin_bit_cast(u32x4, load_vec(z + (uint64_t)r * z_ld, 0, a.n - col)));
     }
     if (!a.part) return;
+    if (high > 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) lds[e][threadIdx.x] = sum[e];
+        __syncthreads();
+        if (y > 0) return;
+        for (int q = 1; q < high; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += lds[e][q * wide + x];
+    }
     float* to = a.part + ((uint64_t)blockIdx.z * a.splits + blockIdx.y) * a.n;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -235,7 +248,7 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
                 const unsigned rest = (unsigned)(tiles % kSlots);
                 const int parts = last_round_parts(rest, kSlots, (int)steps);
                 // how many tiles uneven groups make is known on the device only
-                if (parts > 1 || (form != kByW && a->offsets && rounds < 16)) last = kSlots;
+                if (parts > 1 || (form != kByW && a->offsets && rounds < 16 && steps >= 16)) last = kSlots;
                 if (parts > 1) time += 4 + 0.12 * rest * parts - step * (steps - ceil_div(steps, parts));
             }
             if (time < best) {
@@ -353,11 +366,17 @@ static Operand weights_of(const rr_linear_t* a) {
     return {{const_cast<void*>(a->w), a->w_ld}, a->n, a->k, (uint64_t)a->groups, a->w_stride};
 }
 
-// Parts of a group's rows in the sums over rows: enough workgroups to fill the device.
+// Threads of a workgroup across the columns in the gradient of the activation.
+static uint64_t slope_threads(const rr_linear_t* a) {
+    uint64_t t = 1;
+    while (t < 256 && t * 8 < a->n) t *= 2;
+    return t;
+}
+// Parts of a group's rows there: enough workgroups to fill the device, and four rows a thread.
 static uint64_t splits_of(const rr_linear_t* a) {
-    const uint64_t cols = ceil_div(a->n, 256 * 8) * a->groups;
+    const uint64_t t = slope_threads(a), cols = ceil_div(a->n, t * 8) * a->groups;
     const uint64_t each = ceil_div(a->rows, a->groups);
-    const uint64_t want = ceil_div(2048, cols), most = ceil_div(each, 16);
+    const uint64_t want = ceil_div(2048, cols), most = ceil_div(each, 256 / t * 4);
     const uint64_t n = want < most ? want : most;
     return n < 1 ? 1 : n > 1024 ? 1024 : n;
 }
@@ -369,7 +388,7 @@ static BackwardPlan plan_of(const rr_linear_t* a, const rr_linear_grad_t* g) {
     BackwardPlan p = {0, 0, 0};
     const Operand dout = rows_of(a, g->dout, a->n);
     if ((g->dx.data || g->dw) && (a->act != RR_ACT_NONE || !dout.good())) p.dz = dout.copy_bytes();
-    if (g->db) p.part = ceil_div((uint64_t)a->groups * splits_of(a) * a->n * sizeof(float), 256) * 256;
+    if (g->db && splits_of(a) > 1) p.part = ceil_div((uint64_t)a->groups * splits_of(a) * a->n * sizeof(float), 256) * 256;
     Operand dz = dout;
     if (p.dz) dz.rows = {nullptr, ceil_div(a->n, 8) * 8};
     dz.width = ceil_div(a->n, 8) * 8;       // good rows, or a copy with zeros behind each
@@ -481,7 +500,7 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
     hipStream_t s = (hipStream_t)stream;
     rr_rows_t dz = g->dout;
     void* const room = (char*)workspace + plan.dz + plan.part;
-    if (plan.dz || plan.part) {
+    if (plan.dz || g->db) {
         SlopeArgs k = {};
         k.g = groups_of(a);
         k.dout = g->dout.data;
@@ -491,13 +510,14 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
         k.n = (int32_t)a->n;
         k.act = a->act;
         k.splits = (int32_t)splits_of(a);
+        k.threads = (int32_t)slope_threads(a);
         if (plan.dz) {
             dz = {workspace, ceil_div(a->n, 8) * 8};
             k.dz = dz.data;
             k.dz_ld = dz.ld;
         }
-        if (plan.part) k.part = (float*)((char*)workspace + plan.dz);
-        const uint64_t cols = ceil_div(a->n, 256 * 8);
+        k.part = plan.part ? (float*)((char*)workspace + plan.dz) : g->db;
+        const uint64_t cols = ceil_div(a->n, (uint64_t)k.threads * 8);
         if (cols > (1u << 24) - 1) return RR_ERR_UNSUPPORTED;
         const dim3 grid((unsigned)cols, (unsigned)k.splits, (unsigned)a->groups);
         if (a->dt == RR_BF16)
@@ -505,7 +525,7 @@ rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* 
         else
             slope_kernel<f16><<<grid, 256, 0, s>>>(k);
         if ((st = launched()) != RR_OK) return st;
-        if (g->db) {
+        if (plan.part) {
             const dim3 sums((unsigned)ceil_div(a->n, 16), (unsigned)a->groups);
             slope_parts_kernel<<<sums, 256, 0, s>>>(k.part, k.splits, k.n, g->db);
             if ((st = launched()) != RR_OK) return st;

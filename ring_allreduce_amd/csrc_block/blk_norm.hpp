@@ -221,6 +221,8 @@ __global__ void __launch_bounds__(Shape<G>::block) norm_kernel(const NormArgs a)
 //   dgate = e n act'(gate);   m = e act(gate) post_weight
 //   du = r m - u r^3 mean(m u)
 //   dpre_weight = sum_t dy h q;  dpost_weight = sum_t e act(gate) u r.
+// A channel gate is the same for all tokens: with S = sum_t e u r, dpost_weight is act(gate) S
+// and the gate's gradient post_weight act'(gate) S.
 // Two rounds of sums over a row: (h^2, p h, u^2), then (m u).  The statistics are
 // computed again from the rows, which are read anyway, instead of being stored by
 // the forward call.  The sums over tokens stay in registers over all rows that a
@@ -237,12 +239,12 @@ norm_backward_kernel(const NormArgs a) {
     __shared__ float lds[2][4][16];
     __shared__ float held[IN_LDS ? 2 * NV * N : 1][IN_LDS ? G : 1];
     const int len = a.hidden;
-    float sum_pre[NV][N], sum_post[NV][N], sum_gate[NV][N];
+    float sum_pre[NV][N], sum_post[NV][N];
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            sum_pre[v][i] = sum_post[v][i] = sum_gate[v][i] = 0.0f;
+            sum_pre[v][i] = sum_post[v][i] = 0.0f;
             if constexpr (IN_LDS) held[v * N + i][threadIdx.x] = held[(NV + v) * N + i][threadIdx.x] = 0.0f;
         }
     const float inv = 1.0f / (float)len;
@@ -314,14 +316,13 @@ norm_backward_kernel(const NormArgs a) {
                 dx[v].e[i] = (T)(a.residual_scale * d);
                 float e = a.branch_scale * d;
                 const float unit = R::value(in.u, v, i) * r;
-                if constexpr (GATE != RR_GATE_NONE) {
-                    const float at_gate = e * unit * wp[i] * gate_slope(a.gate_act, z[i]);
-                    if constexpr (GATE == RR_GATE_ELEMENT) dg[v].e[i] = (T)at_gate;
-                    else sum_gate[v][i] += at_gate;
+                if constexpr (GATE == RR_GATE_ELEMENT) {
+                    dg[v].e[i] = (T)(e * unit * wp[i] * gate_slope(a.gate_act, z[i]));
                     e *= gate_value(a.gate_act, z[i]);
                 }
                 if constexpr (IN_LDS) held[(NV + v) * N + i][threadIdx.x] = fmaf(e, unit, held[(NV + v) * N + i][threadIdx.x]);
                 else sum_post[v][i] = fmaf(e, unit, sum_post[v][i]);
+                if constexpr (GATE == RR_GATE_CHANNEL) e *= gate_value(a.gate_act, z[i]);
                 m[v][i] = e * wp[i];
                 s2[0] = fmaf(m[v][i], R::value(in.u, v, i), s2[0]);
             }
@@ -380,8 +381,22 @@ norm_backward_kernel(const NormArgs a) {
                 sum_post[v][i] = held[(NV + v) * N + i][threadIdx.x];
             }
     write(sum_pre, a.at_pre);
+    if constexpr (GATE == RR_GATE_CHANNEL) {
+        float sum_gate[NV][N];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float wp[N], z[N];
+            R::weights(wp, a.post_weight, a.wide_weights, v, len);
+            R::weights(z, a.gate, a.wide_weights, v, len);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                sum_gate[v][i] = sum_post[v][i] * wp[i] * gate_slope(a.gate_act, z[i]);
+                sum_post[v][i] *= gate_value(a.gate_act, z[i]);
+            }
+        }
+        write(sum_gate, a.at_gate);
+    }
     write(sum_post, a.at_post);
-    if constexpr (GATE == RR_GATE_CHANNEL) write(sum_gate, a.at_gate);
 }
 
 struct Config {
