@@ -50,6 +50,7 @@ struct GemmArgs {
 struct GemmPlan {
     int32_t form, tile;
     int32_t direct;                  // kStream*: rows of both operands at 16-byte boundaries
+    int32_t deep;                    // kTile128, kTile64: four stages in LDS, else two
 };
 
 rr_status_t launch_gemm_bf16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
@@ -576,14 +577,18 @@ template <int N> struct Int {
 
 // ------------------------------------------------------------------ the product --
 
-template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ>
-__global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a) {
+// STAGES tiles of the operands are in LDS or on their way there.  Where a compute unit has one
+// or two workgroups, the time of a step is the loads' way through memory, and four stages
+// take as many steps to hide it.
+template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ, int STAGES>
+__global__ void __launch_bounds__(64 * WI * WJ, STAGES * (TI + TJ) * kDepth * 2 > 81920 && WI * WJ == 4 ? 1 : 2)
+gemm_kernel(const GemmArgs a) {
     typedef typename Mma<T>::V V;
     constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16;
     constexpr int PB = Tile<PA, TI>::kBytes, QB = Tile<QA, TJ>::kBytes;
     constexpr uint32_t STAGE = PB + QB;              // a power of two, and of the tiles' places its own bit
     constexpr uint32_t OUT = 2 * 16 * WI * (TJ + 4) * 4;   // write_out's place
-    __shared__ __align__(2 * STAGE) char lds[OUT > 2 * STAGE ? OUT : 2 * STAGE];
+    __shared__ __align__(2 * STAGE) char lds[OUT > STAGES * STAGE ? OUT : STAGES * STAGE];
     BLK_LDS char* const room = (BLK_LDS char*)lds;
     RowTiles rows = {};
     if constexpr (BY_ROWS) rows = count_tiles(a, TI);
@@ -644,25 +649,26 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) gemm_kernel(const GemmArgs a)
     };
     const int tiles = (s.c_end - s.c0 + kDepth - 1) / kDepth;
     if (tiles > 0) {
-        lp.aim(first);
-        lq.aim(first + PB);
-        load(0, PIECES);
-        lp.aim(first + STAGE);
-        lq.aim(first + STAGE + PB);
-        load(0, PIECES);
-        arrived<PIECES>();
+#pragma unroll
+        for (int t = 0; t < STAGES; ++t) {
+            lp.aim(first + t * STAGE);
+            lq.aim(first + t * STAGE + PB);
+            load(0, PIECES);
+        }
+        arrived<PIECES * (STAGES - 1)>();
 #pragma unroll
         for (int x = 0; x < READS; ++x) read(0, x);
     }
     for (int t = 0; t < tiles; ++t) {
         __builtin_amdgcn_s_waitcnt(0xC07F);  // the reads of half 0, before new ones
         multiply(Int<0>());
-        arrived<0>();
+        arrived<PIECES * (STAGES - 2)>();        // the next tile
         lp.aim(first + stage);
         lq.aim(first + stage + PB);
-        stage ^= STAGE;
-        rp.other(STAGE);
-        rq.other(STAGE);
+        const uint32_t change = ((t ^ (t + 1)) & (STAGES - 1)) * STAGE;
+        stage ^= change;
+        rp.other(change);
+        rq.other(change);
         multiply(Int<1>());
     }
     arrived<0>();                            // the zeros past the end as well
@@ -875,11 +881,13 @@ template <typename T, bool PA, bool QA, bool BY_ROWS>
 static void launch_form(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
     const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits * (BY_ROWS ? 1u : (unsigned)a.groups);
     if (p.tile == kTile256) {
-        gemm_kernel<T, PA, QA, BY_ROWS, 256, 256, 2, 4><<<grid + (unsigned)a.slots, 512, 0, s>>>(a);
+        gemm_kernel<T, PA, QA, BY_ROWS, 256, 256, 2, 4, 2><<<grid + (unsigned)a.slots, 512, 0, s>>>(a);
         if (a.slots) join_last_kernel<T, BY_ROWS, 256, 256><<<dim3((unsigned)a.slots / 2, 8), 256, 0, s>>>(a);
     }
-    else if (p.tile == kTile128) gemm_kernel<T, PA, QA, BY_ROWS, 128, 128, 2, 2><<<grid, 256, 0, s>>>(a);
-    else gemm_kernel<T, PA, QA, BY_ROWS, 64, 64, 2, 2><<<grid, 256, 0, s>>>(a);
+    else if (p.tile == kTile128 && p.deep) gemm_kernel<T, PA, QA, BY_ROWS, 128, 128, 2, 2, 4><<<grid, 256, 0, s>>>(a);
+    else if (p.tile == kTile128) gemm_kernel<T, PA, QA, BY_ROWS, 128, 128, 2, 2, 2><<<grid, 256, 0, s>>>(a);
+    else if (p.deep) gemm_kernel<T, PA, QA, BY_ROWS, 64, 64, 2, 2, 4><<<grid, 256, 0, s>>>(a);
+    else gemm_kernel<T, PA, QA, BY_ROWS, 64, 64, 2, 2, 2><<<grid, 256, 0, s>>>(a);
 }
 
 template <typename T> static rr_status_t launch_gemm(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {

@@ -216,7 +216,7 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
     const uint64_t i = form == kByW ? a->n : a->rows, j = form == kForward ? a->n : a->k;
     const uint64_t c = form == kForward ? a->k : form == kByX ? a->n : mean;
     const double outputs = (double)(form == kByW ? groups * i : i) * j;
-    GemmPlan p = {form, kTile64, 0};
+    GemmPlan p = {form, kTile64, 0, 0};
     *splits = 1;
     *slots = 0;
     if (form == kForward && (mean <= 16 || (mean <= 64 && c <= 1024))) {
@@ -254,6 +254,7 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
             if (time < best) {
                 best = time;
                 p.tile = tile;
+                p.deep = rounds == 1 && load <= (tile == kTile64 ? 2 : 1);
                 *splits = (int)s;
                 *slots = last;
             }
