@@ -28,14 +28,17 @@ norm_parts_kernel(const float* part, int parts, uint64_t stride, int hidden, flo
 
 // ------------------------------------------------------------------ host side --
 
-// Threads and vectors per row.  A row of few vectors goes to one wave (no barrier); a longer
+// Threads and vectors per row.  A row of few vectors goes to a part of a wave or one wave (no barrier); a longer
 // one to as many threads as keep it in registers.  The backward kernel holds five rows, the
 // next five and the sums over tokens, so it takes twice the threads (16384 x 4096 bf16 with an
 // element gate: 358 us with 256 threads of two vectors).
 static Config pick(int hidden, int dt, bool back) {
     const int n = (int)(16 / type_bytes(dt));
     const int vecs = (int)ceil_div(hidden, n);
-    if (hidden < n) return {64, 1, true};
+    if (hidden < n) return {8, 1, true};
+    if (vecs <= 8) return {8, 1, false};
+    if (vecs <= 16) return {16, 1, false};
+    if (vecs <= 32) return {32, 1, false};
     if (vecs <= 64) return {64, 1, false};
     if (vecs <= 128) return {64, 2, false};
     if (vecs <= 256) return {256, 1, false};
@@ -52,7 +55,8 @@ static int rows_of(const Config& c) { return c.group < 256 ? 256 / c.group : 1; 
 static unsigned grid_of(const Config& c, size_t tokens) {
     const int cus = compute_units();
     const uint64_t want = ceil_div(tokens, rows_of(c));
-    const uint64_t most = (uint64_t)(cus > 0 ? cus : 256) * (c.group == 64 ? (c.vecs == 1 ? 3 : 2) : c.group == 256 ? 4 : c.group == 512 ? 2 : 1);
+    if (want <= 2) return 1;       // a second row costs less than the launch that adds two parts
+    const uint64_t most = (uint64_t)(cus > 0 ? cus : 256) * (c.group <= 64 ? (c.vecs == 1 ? 3 : 2) : c.group == 256 ? 4 : c.group == 512 ? 2 : 1);
     return (unsigned)(want < most ? want : most);
 }
 
@@ -247,6 +251,9 @@ rr_status_t block_norm_backward(const rr_norm_t* a, const rr_norm_grad_t* g, voi
     k.dgate = g->dgate.data;
     k.dgate_ld = g->dgate.ld;
     k.part = (float*)workspace;
+    k.dpre = g->dpre_weight;
+    k.dpost = g->dpost_weight;
+    k.dgate_channel = g->dgate_channel;
     k.at_pre = k.at_post = k.at_gate = -1;
     float* sums[3] = {nullptr, nullptr, nullptr};
     if (g->dpre_weight) sums[k.at_pre = k.sums++] = g->dpre_weight;
@@ -262,9 +269,9 @@ rr_status_t block_norm_backward(const rr_norm_t* a, const rr_norm_grad_t* g, voi
     const unsigned grid = grid_of(c, t);
     hipStream_t s = (hipStream_t)stream;
     if (t && (st = launch_norm(k, a->dt, c, grid, true, s)) != RR_OK) return st;
-    if (k.sums) {
+    if (k.sums && (grid > 1 || t == 0)) {
         const dim3 parts((unsigned)ceil_div(h, 16), (unsigned)k.sums);
-        norm_parts_kernel<<<parts, 256, 0, s>>>(k.part, (int)parts_of(a), (uint64_t)k.sums * h,
+        norm_parts_kernel<<<parts, 256, 0, s>>>(k.part, t ? (int)parts_of(a) : 0, (uint64_t)k.sums * h,
                                                 (int)h, sums[0], sums[1], sums[2]);
         if ((st = launched()) != RR_OK) return st;
     }

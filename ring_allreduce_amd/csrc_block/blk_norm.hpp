@@ -22,6 +22,7 @@ struct NormArgs {
     float* part;           // [workgroups][sums][hidden]
     int32_t sums;          // weight gradients wanted: 0 .. 3
     int32_t at_pre, at_post, at_gate;  // their places among the sums, or -1
+    float *dpre, *dpost, *dgate_channel;
     const void* any;       // a matrix that is there
     uint64_t any_ld;
 };
@@ -68,6 +69,9 @@ template <typename T, int G, int NV, bool TINY> struct Row {
     __device__ __forceinline__ static void zero(u32x4 (&r)[NV]) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) r[v] = u32x4{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ static void store(const Vec<T>& r, int v, void* p, uint64_t ld, int64_t t, int len) {
+        if (column(v) < len) store_vec((T*)p + (uint64_t)t * ld, column(v), len, r);
     }
     __device__ __forceinline__ static void store(const Vec<T> (&r)[NV], void* p, uint64_t ld, int64_t t, int len) {
         T* row = (T*)p + (uint64_t)t * ld;
@@ -119,7 +123,7 @@ template <typename T, int G, int NV, bool TINY> struct Row {
 template <int G, int K>
 __device__ __forceinline__ void row_sums(float (&s)[K], float* lds) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) s[k] = lane_sum<64>(s[k]);
+    for (int k = 0; k < K; ++k) s[k] = lane_sum<(G < 64 ? G : 64)>(s[k]);
     if constexpr (G > 64) {
         constexpr int W = G / 64;
         if ((threadIdx.x & 63) == 0)
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(Shape<G>::block) norm_kernel(const NormArgs a)
 // loads of the next row on their way beside this one took 295 us for 16384 x 4096 bf16
 // with an element gate, with spills, against 250 (1074 MB: 4.3 TB/s) without.
 template <typename T, int G, int NV, int GATE, bool TINY>
-__global__ void __launch_bounds__(Shape<G>::block, G == 64 ? (NV == 1 ? 3 : 2) : 4)
+__global__ void __launch_bounds__(Shape<G>::block, G <= 64 ? (NV == 1 ? 3 : 2) : 4)
 norm_backward_kernel(const NormArgs a) {
     typedef Row<T, G, NV, TINY> R;
     constexpr int N = Vec<T>::N;
@@ -273,7 +277,6 @@ norm_backward_kernel(const NormArgs a) {
         if (!a.pre) R::zero(in.h), R::zero(in.dy);
         if (!a.branch) R::zero(in.u);
         if (!a.dh) R::zero(in.dh);
-        Vec<T> dx[NV], dg[NV], du[NV];
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -296,6 +299,7 @@ norm_backward_kernel(const NormArgs a) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float wn[N], wp[N], z[N];
+            Vec<T> dx, dg;
             R::weights(wn, a.pre_weight, a.wide_weights, v, len);
             R::weights(wp, a.post_weight, a.wide_weights, v, len);
             if constexpr (GATE == RR_GATE_CHANNEL) {
@@ -313,11 +317,11 @@ norm_backward_kernel(const NormArgs a) {
                     if constexpr (IN_LDS) held[v * N + i][threadIdx.x] = fmaf(dyv * q, hv, held[v * N + i][threadIdx.x]);
                     else sum_pre[v][i] = fmaf(dyv * q, hv, sum_pre[v][i]);
                 }
-                dx[v].e[i] = (T)(a.residual_scale * d);
+                dx.e[i] = (T)(a.residual_scale * d);
                 float e = a.branch_scale * d;
                 const float unit = R::value(in.u, v, i) * r;
                 if constexpr (GATE == RR_GATE_ELEMENT) {
-                    dg[v].e[i] = (T)(e * unit * wp[i] * gate_slope(a.gate_act, z[i]));
+                    dg.e[i] = (T)(e * unit * wp[i] * gate_slope(a.gate_act, z[i]));
                     e *= gate_value(a.gate_act, z[i]);
                 }
                 if constexpr (IN_LDS) held[(NV + v) * N + i][threadIdx.x] = fmaf(e, unit, held[(NV + v) * N + i][threadIdx.x]);
@@ -326,10 +330,10 @@ norm_backward_kernel(const NormArgs a) {
                 m[v][i] = e * wp[i];
                 s2[0] = fmaf(m[v][i], R::value(in.u, v, i), s2[0]);
             }
+            if (a.dx) R::store(dx, v, a.dx, a.dx_ld, t, len);
+            if constexpr (GATE == RR_GATE_ELEMENT)
+                if (a.dgate) R::store(dg, v, a.dgate, a.dgate_ld, t, len);
         }
-        if (a.dx) R::store(dx, a.dx, a.dx_ld, t, len);
-        if constexpr (GATE == RR_GATE_ELEMENT)
-            if (a.dgate) R::store(dg, a.dgate, a.dgate_ld, t, len);
         if (a.dbranch) {
             float bu = 0.0f;
             if (a.post) {
@@ -337,37 +341,38 @@ norm_backward_kernel(const NormArgs a) {
                 bu = r * r * r * s2[0] * inv;
             }
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
+            for (int v = 0; v < NV; ++v) {
+                Vec<T> du;
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    du[v].e[i] = (T)fmaf(r, m[v][i], -bu * R::value(in.u, v, i));
-            R::store(du, a.dbranch, a.dbranch_ld, t, len);
+                for (int i = 0; i < N; ++i) du.e[i] = (T)fmaf(r, m[v][i], -bu * R::value(in.u, v, i));
+                R::store(du, v, a.dbranch, a.dbranch_ld, t, len);
+            }
         }
     }
     if (a.sums == 0) return;
-    float* to = a.part + (uint64_t)blockIdx.x * a.sums * len;
-    const auto write = [&](const float (&sum)[NV][N], int at) {
+    // one workgroup writes the gradients themselves
+    const auto write = [&](const float (&sum)[NV][N], int at, float* whole) {
         if (at < 0) return;
+        float* const to = gridDim.x == 1 ? whole : a.part + ((uint64_t)blockIdx.x * a.sums + at) * len;
         if constexpr (G > 64) {
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    if (R::column(v) + i < len) to[(uint64_t)at * len + R::column(v) + i] = sum[v][i];
+                    if (R::column(v) + i < len) to[R::column(v) + i] = sum[v][i];
         } else {                       // the workgroup's rows, added in their order
-            __shared__ float joined[Shape<G>::rows][NV * N][64];
-            const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+            __shared__ float joined[Shape<G>::rows][NV * N * G];
+            const int g = threadIdx.x % G, row = threadIdx.x / G;
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int i = 0; i < N; ++i) joined[wave][v * N + i][lane] = sum[v][i];
+                for (int i = 0; i < N; ++i) joined[row][(v * N + i) * G + g] = sum[v][i];
             __syncthreads();
-            for (int k = wave; k < NV * N; k += Shape<G>::rows) {
+            for (int k = threadIdx.x; k < NV * N * G; k += Shape<G>::block) {
                 float all = 0.0f;
-#pragma unroll
-                for (int w = 0; w < Shape<G>::rows; ++w) all += joined[w][k][lane];
-                const int c = (k / N * G + lane) * N + k % N;
-                if (c < len) to[(uint64_t)at * len + c] = all;
+                for (int w = 0; w < Shape<G>::rows; ++w) all += joined[w][k];
+                const int c = (k / (N * G) * G + k % G) * N + k / G % N;
+                if (c < len) to[c] = all;
             }
             __syncthreads();
         }
@@ -380,7 +385,7 @@ norm_backward_kernel(const NormArgs a) {
                 sum_pre[v][i] = held[v * N + i][threadIdx.x];
                 sum_post[v][i] = held[(NV + v) * N + i][threadIdx.x];
             }
-    write(sum_pre, a.at_pre);
+    write(sum_pre, a.at_pre, a.dpre);
     if constexpr (GATE == RR_GATE_CHANNEL) {
         float sum_gate[NV][N];
 #pragma unroll
@@ -394,9 +399,9 @@ norm_backward_kernel(const NormArgs a) {
                 sum_post[v][i] *= gate_value(a.gate_act, z[i]);
             }
         }
-        write(sum_gate, a.at_gate);
+        write(sum_gate, a.at_gate, a.dgate_channel);
     }
-    write(sum_post, a.at_post);
+    write(sum_post, a.at_post, a.dpost);
 }
 
 struct Config {
@@ -427,7 +432,10 @@ static void launch_rows(const NormArgs& a, const Config& c, unsigned grid, bool 
 #define BLK_ROWS(G, NV, TINY, BACK)                                        \
     if (c.group == G && c.vecs == NV && c.tiny == TINY && back == BACK)    \
         return launch_rows<T, G, NV, TINY, BACK>(a, grid, s)
-    BLK_ROWS(64, 1, true, false);
+    BLK_ROWS(8, 1, true, false);
+    BLK_ROWS(8, 1, false, false);
+    BLK_ROWS(16, 1, false, false);
+    BLK_ROWS(32, 1, false, false);
     BLK_ROWS(64, 1, false, false);
     BLK_ROWS(64, 2, false, false);
     BLK_ROWS(256, 1, false, false);
@@ -435,7 +443,10 @@ static void launch_rows(const NormArgs& a, const Config& c, unsigned grid, bool 
     BLK_ROWS(512, 2, false, false);
     BLK_ROWS(1024, 2, false, false);
     BLK_ROWS(1024, 4, false, false);
-    BLK_ROWS(64, 1, true, true);
+    BLK_ROWS(8, 1, true, true);
+    BLK_ROWS(8, 1, false, true);
+    BLK_ROWS(16, 1, false, true);
+    BLK_ROWS(32, 1, false, true);
     BLK_ROWS(64, 1, false, true);
     BLK_ROWS(64, 2, false, true);
     BLK_ROWS(256, 1, false, true);
