@@ -693,7 +693,9 @@ typedef struct {
     int32_t reserved;   /* 0 */
 } rr_linear_grad_t;
 
-/* residual may be out itself (in place). */
+/* residual may be out itself (in place).  Scratch memory (aligned to 16 bytes) holds parts of
+   long contractions and copies of operands whose rows are not made of 16-byte pieces: ask
+   with the very struct that the call gets. */
 rr_status_t block_linear(const rr_linear_t *a, void *workspace, size_t workspace_bytes,
                          rr_stream_t stream);
 rr_status_t block_linear_workspace(const rr_linear_t *a, size_t *bytes);

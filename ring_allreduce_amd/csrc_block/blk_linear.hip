@@ -207,8 +207,8 @@ static uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
 //    64 x  64    4.5   0.37, 0.6, 0.7, 0.9
 // A further round costs half a start; parts cost 2.2 for the second launch and their bytes,
 // written and read.  A few rows go through the one-pass form instead, to 64 rows where the
-// contraction is too short for parts to pay (2048 x 1024: 8.6 us against 10.4 for 48 rows;
-// at 8192 deep 40 against 16).
+// contraction is too short for parts to pay (48 x 8192 x 1024: 9.4 us against 10.2; 48 x 1024
+// x 8192: 40 against 16).
 constexpr unsigned kSlots = 256;      // 256 x 256 tiles that a device takes at once: one a compute unit
 
 static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) {
