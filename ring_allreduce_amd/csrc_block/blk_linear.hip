@@ -219,6 +219,10 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
     GemmPlan p = {form, kTile64, 0, 0};
     *splits = 1;
     *slots = 0;
+    if (form == kForward && groups == 1 && !a->offsets && a->rows <= 2) {
+        p.tile = kDot;
+        return p;
+    }
     if (form == kForward && (mean <= 16 || (mean <= 64 && c <= 1024))) {
         p.tile = mean <= 16 ? kStream16 : mean <= 32 ? kStream32 : kStream64;
         const uint64_t blocks = ceil_div(j, kStreamCols) * ceil_div(a->rows, 16);
@@ -348,6 +352,10 @@ static rr_status_t run_product(const rr_linear_t* a, Product r, void* workspace,
         room += (uint64_t)slots * 256 * 256 * sizeof(float);
     }
     plan.direct = r.p.good() && r.q.good();
+    if (plan.tile == kStream16 && !plan.direct && a->groups == 1 && !a->offsets && a->rows <= 4) {
+        plan.tile = kDot;
+        k.splits = 1;
+    }
     if (plan.tile < kStream16) {
         const rr_status_t st = pack(r.p, r.q, room, s);
         if (st != RR_OK) return st;

@@ -72,6 +72,50 @@ def test_few_rows_long_contraction(rr):
             check_forward(rr, d, None, "silu", torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5])
+def test_one_to_four_rows(rr, dtype, rows):
+    """Dots: widths of less than a vector, of parts of a wave's stretch, of several; rows at odd
+    elements."""
+    for n, k in ((1, 3), (5, 8), (2051, 519), (2048, 4096), (70, 2055), (9, 6152)):
+        d = make(rows, n, k, None, dtype, True, True)
+        check_forward(rr, d, None, "gelu", DTYPES[dtype])
+        far = dict(d, x=strided(d["x"], 3, offset=1)[0], w=strided(d["w"], 1, offset=5)[0])
+        check_forward(rr, far, None, "silu", DTYPES[dtype])
+
+
+def test_far_rows(rr):
+    """Rows beyond 2^31 elements and 2^32 bytes: the last ones come out as they do alone."""
+    tokens, hidden, last = 280_000, 8192, 279_000
+    x = torch.empty(tokens, hidden, dtype=torch.bfloat16, device="cuda")
+    x[last:].normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    x[:last] = 1.0
+    w = torch.randn(hidden, device="cuda").bfloat16()
+    h, y = rr.block_norm(x, post_norm=False, pre_weight=w)
+    h2, y2 = rr.block_norm(x[last:].contiguous(), post_norm=False, pre_weight=w)
+    assert torch.equal(h[last:], h2) and torch.equal(y[last:], y2)
+    del h, h2, y2
+    d = rr.block_norm_backward(None, y, x, post_norm=False, pre_weight=w, need=("dx",))
+    d2 = rr.block_norm_backward(None, y[last:].contiguous(), x[last:].contiguous(), post_norm=False,
+                                pre_weight=w, need=("dx",))
+    assert torch.equal(d.dx[last:], d2.dx)
+    del d, d2, y
+    slots = torch.arange(tokens, dtype=torch.int32, device="cuda").flip(0).reshape(-1, 1).contiguous()
+    sources = slots.reshape(-1).clone()
+    rows = rr.expert_dispatch(x, slots, sources)
+    assert torch.equal(rows[:tokens - last].flip(0), x[last:])
+    back = rr.expert_combine(rows, slots)
+    assert torch.equal(back[last:], x[last:]) and torch.equal(back[:5], x[:5])
+    del rows, back
+    wide = torch.randn(64, hidden, device="cuda").bfloat16()
+    out = rr.block_linear(x, wide)
+    few = rr.block_linear(x[last:].contiguous(), wide)
+    # another tile or cut of the contraction adds in another order
+    size = x[last:].float().abs() @ wide.float().abs().t()
+    assert bool(((out[last:].double() - few.double()).abs() <= 2 * store_error(few.double(), torch.bfloat16) +
+                 2 * (hidden + 2) * U * size.double()).all())
+
+
 NORM = [  # tokens, hidden, gate, act, post, pre, weights
     (5000, 520, "element", "silu", True, True, "same"), (9000, 72, "channel", "sigmoid", True, True, "fp32"),
     (3000, 1030, "channel", "silu", True, True, "same"), (1500, 4104, "element", "sigmoid", True, True, "same"),
