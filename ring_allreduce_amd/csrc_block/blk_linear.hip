@@ -199,13 +199,14 @@ static uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
 }
 
 // The kernel and the parts of the contraction for one product: the least of the times that
-// these figures give, taken from 290 products of 24 to 6016 rows and 256 to 8192 columns and
-// depths on an MI355X (microseconds; a step is 64 deep).
+// these figures give, fitted on an MI355X to 320 products of 32 to 6400 rows and 128 to 8192
+// columns and depths, each with every tile and 1 to 16 parts (microseconds; a step is 64
+// deep; what they choose is 0.4% slower on average than the best).
 //   tile       start   a step, with 1 .. 4 workgroups on each compute unit
-//   256 x 256    8     1.75 (1.4 on an empty device)
-//   128 x 128    6     0.75, 1.15
-//    64 x  64    4.5   0.37, 0.6, 0.7, 0.9
-// A further round costs half a start; parts cost 2.2 for the second launch and their bytes,
+//   256 x 256   11.3    1.63 (1.1 on an empty device)
+//   128 x 128    6.6    0.73 (0.47), 1.16
+//    64 x  64    3.8    0.28, 0.51, 0.73, 0.83
+// A further round costs 0.6 of a start; parts cost 4.6 for the second launch and their bytes,
 // written and read.  A few rows go through the one-pass form instead, to 64 rows where the
 // contraction is too short for parts to pay (48 x 8192 x 1024: 9.4 us against 10.2; 48 x 1024
 // x 8192: 40 against 16).
@@ -241,12 +242,12 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
             const uint64_t blocks = tiles * s, rounds = ceil_div(blocks, 256 * each);
             const uint64_t load = rounds > 1 ? each : ceil_div(blocks, 256);
             const double fill = blocks < 256 ? blocks / 256.0 : 1.0;
-            const double start = tile == kTile256 ? 8 : tile == kTile128 ? 6 : 4.5;
-            const double step = tile == kTile256   ? 1.4 + 0.35 * fill
-                                : tile == kTile128 ? (load == 1 ? 0.6 + 0.3 * fill : 1.15)
-                                : load == 1 ? 0.36 + 0.05 * fill : load == 2 ? 0.6 : load == 3 ? 0.7 : 0.9;
-            double time = start * (0.5 + 0.5 * rounds) + rounds * step * ceil_div(steps, s);
-            if (s > 1) time += 2.2 + 8.0 * s * outputs / 4.5e6;
+            const double start = tile == kTile256 ? 11.3 : tile == kTile128 ? 6.6 : 3.8;
+            const double step = tile == kTile256   ? 1.11 + 0.52 * fill
+                                : tile == kTile128 ? (load == 1 ? 0.47 + 0.26 * fill : 1.16)
+                                : load == 1 ? 0.28 : load == 2 ? 0.51 : load == 3 ? 0.73 : 0.83;
+            double time = start * (0.4 + 0.6 * rounds) + rounds * step * ceil_div(steps, s);
+            if (s > 1) time += 4.6 + 8.0 * s * outputs / 5.95e6;
             int last = 0;
             if (tile == kTile256 && s == 1 && (form != kByW || (groups == 1 && !a->offsets))) {
                 const unsigned rest = (unsigned)(tiles % kSlots);
