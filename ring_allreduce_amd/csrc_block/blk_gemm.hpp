@@ -548,23 +548,17 @@ __device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, BLK_
         for (int t = 0; t < EACH; ++t) {
             const BLK_LDS float* const from = buf + (t * (THREADS / GROUPS) + thread / GROUPS) * LINE + col;
             if (x * 16 >= left[t]) continue;
-            if (n >= 8) {
-                const f32x4 lo = *(const BLK_LDS f32x4*)from, hi = *(const BLK_LDS f32x4*)(from + 4);
-                float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                if (whole)
-                    finish<T, 8>(a, s.g.group, 8, v, bias, residual[t], (T*)(to_z + at_z[t]), to + at_out[t]);
-                else
-                    store_wide<8>((float*)(to + at_out[t]), 8, v);
-            } else {
-                const int i = s.i0 + (int)((t * (THREADS / GROUPS) + thread / GROUPS) / 16 * (TI / WI)) + x * 16 +
-                              (t * (THREADS / GROUPS) + thread / GROUPS) % 16;
-                for (int e = 0; e < n; ++e) {
-                    float v[1] = {from[e]};
-                    if (whole)
-                        finish<T, 1>(a, s.g.group, i, s.j0 + col + e, v);
-                    else
-                        ((float*)(to + at_out[t]))[e] = v[0];
-                }
+            const f32x4 lo = *(const BLK_LDS f32x4*)from, hi = *(const BLK_LDS f32x4*)(from + 4);
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            if (!whole) {
+                store_wide<8>((float*)(to + at_out[t]), n, v);
+            } else if (n >= 8) {
+                finish<T, 8>(a, s.g.group, 8, v, bias, residual[t], (T*)(to_z + at_z[t]), to + at_out[t]);
+            } else {       // the last columns: their elements' loads together, then their stores
+                Some<T, 8> r = {};
+                if (add) r = load_some<T, 8>((const T*)(res + (uint64_t)(x * 16) * a.residual_ld * sizeof(T) + at_res[t]), n);
+                finish<T, 8>(a, s.g.group, n, v, bias_of<T, 8>(a, s.g.group, s.j0 + col), r,
+                             (T*)(to_z + at_z[t]), to + at_out[t]);
             }
         }
 #pragma unroll
