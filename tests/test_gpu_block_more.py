@@ -210,3 +210,61 @@ def test_sort_sizes(rr, tokens, k, experts, capacity, kind):
     ids = make_ids(tokens, k, experts, kind, tokens)
     check_order(rr.expert_sort(torch.from_numpy(ids).cuda(), experts, capacity),
                 order_of(ids, experts, capacity))
+
+
+def test_binding_refuses(rr):
+    """Wrong shapes, types, layouts and places of GPU tensors, one argument at a time."""
+    x = torch.zeros(6, 16, device="cuda").bfloat16()
+    w, b = torch.zeros(8, 16, device="cuda").bfloat16(), torch.zeros(8, device="cuda").bfloat16()
+    i = torch.zeros(6, 2, dtype=torch.int32, device="cuda")
+    q = torch.zeros(12, dtype=torch.int32, device="cuda")
+    values = [
+        lambda: rr.expert_sort(i, 4, -1), lambda: rr.expert_dispatch(x, i[:5], q),
+        lambda: rr.expert_dispatch(x, i, q.cpu()), lambda: rr.expert_dispatch(x.t(), i, q),
+        lambda: rr.expert_combine(x, i, torch.zeros(6, 3, device="cuda")),
+        lambda: rr.expert_combine_backward(x, x, i, q), lambda: rr.expert_combine(x, i[:, :1].expand(6, 2)),
+        lambda: rr.block_norm(x, x[:5]), lambda: rr.block_norm(x, x, post_weight=x[0, :8].contiguous()),
+        lambda: rr.block_norm(x, x, gate_act="silu"), lambda: rr.block_norm(x, x, gate=x[:3]),
+        lambda: rr.block_norm(x, x, pre_norm=False, pre_weight=x[0].clone()),
+        lambda: rr.block_norm(x), lambda: rr.block_norm(x, x.cpu()),
+        lambda: rr.block_norm_backward(x, None, x, x), lambda: rr.block_norm_backward(x, x, None, x),
+        lambda: rr.block_linear(x, w[:, :8]), lambda: rr.block_linear(x, w, b[:7]),
+        lambda: rr.block_linear(x, w, b.cpu()), lambda: rr.block_linear(x, w, act="sigmoid"),
+        lambda: rr.block_linear(x, w, residual=x), lambda: rr.block_linear(x, w, offsets=q[:3]),
+        lambda: rr.block_linear(x, torch.zeros(4, 8, 16, device="cuda").bfloat16()),
+        lambda: rr.block_linear_backward(x, x, w), lambda: rr.block_linear_backward(x[:, :8], x, w, act="relu")]
+    types = [
+        lambda: rr.expert_sort(i.to(torch.int16), 4), lambda: rr.expert_dispatch(x, i.long(), q),
+        lambda: rr.expert_combine(x, i, torch.zeros(6, 2, device="cuda").bfloat16()),
+        lambda: rr.block_norm(x, x.float()), lambda: rr.block_norm(x, x, post_weight=x[0].half()),
+        lambda: rr.block_linear(x, w.half()), lambda: rr.block_linear(x, w, b.float()),
+        lambda: rr.block_linear(x, w, offsets=q[:2].long()),
+        lambda: rr.block_linear_backward(x[:, :8], x, w, dw_dtype=torch.float16)]
+    for call in values:
+        with pytest.raises((ValueError, rr.RRError)):
+            call()
+    for call in types:
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(rr.RRError):
+        rr.expert_sort(i, 2000)
+    with pytest.raises(rr.RRError):
+        rr.block_norm(x, x, eps=-1.0)
+
+
+def test_unusual_forms_give_the_same(rr):
+    """Given outputs, another stream and strides: the same bits as the usual call."""
+    d = make(90, 136, 72, None, "bf16", True, True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a = rr.block_linear(d["x"], d["w"], d["bias"], act="silu", residual=d["residual"])
+    b = rr.block_linear(d["x"], d["w"], d["bias"], act="silu", residual=d["residual"], stream=side)
+    c = rr.block_linear(d["x"], d["w"], d["bias"], act="silu", residual=d["residual"],
+                        out=torch.empty_like(a))
+    side.synchronize()
+    assert torch.equal(a, b) and torch.equal(a, c)
+    one = rr.block_norm_backward(d["dout"], d["dout"], d["z"], d["residual"], need=("dbranch", "dx"))
+    two = rr.block_norm_backward(d["dout"], d["dout"], d["z"], d["residual"], stream=side)
+    side.synchronize()
+    assert torch.equal(one.dx, two.dx) and torch.equal(one.dbranch, two.dbranch)
+    assert one.dgate is None and two.dpost_weight is None
