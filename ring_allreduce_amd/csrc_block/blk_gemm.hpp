@@ -190,7 +190,7 @@ template <bool ACROSS, int ROWS> struct Tile {
 // Reads fragments of 16 rows, 32 deep, of the tiles in LDS: a lane gets row lane % 16 of
 // block x, c + (lane / 16) * 8 .. + 7.  Of a block's address only the lane's part takes
 // registers: the block row, the half and the operand's place are constants of the
-// instruction, and going to the other stage is one exclusive or.
+// instruction, and going to another place is one addition.
 template <bool ACROSS, int ROWS> struct Reader {
     uint32_t at[2];
     __device__ __forceinline__ void start(uint32_t tile, int row) {    // row: a wave's first, of the tile
@@ -205,9 +205,9 @@ template <bool ACROSS, int ROWS> struct Reader {
             at[0] = tile + line * (ROWS * 2) + (((row >> 4) ^ Tile<ACROSS, ROWS>::mix(line)) << 5) + (lane & 3) * 8;
         }
     }
-    __device__ __forceinline__ void other(uint32_t stage) {
-        at[0] ^= stage;
-        if constexpr (!ACROSS) at[1] ^= stage;
+    __device__ __forceinline__ void move(uint32_t by) {
+        at[0] += by;
+        if constexpr (!ACROSS) at[1] += by;
     }
     template <typename V> __device__ __forceinline__ V fragment(int x, int half) const {
         if constexpr (!ACROSS) {
@@ -574,12 +574,15 @@ template <int N> struct Int {
 
 // Bound, at 256 x 256, by power and the way from the L2s into LDS: with all loads but the
 // first taken out 8192 x 8192 x 8192 takes 646 us (1700 TFLOP/s), with loads that all hit the
-// L2 742, as it is 790 (1390).  A tile of 256 x 256 moves 64 KiB into LDS for 8.4 MFLOP; 128 x
+// L2 742, as it is 770 (1430).  A tile of 256 x 256 moves 64 KiB into LDS for 8.4 MFLOP; 128 x
 // 128 ones move twice that for their work and reach 12 TB/s between L2s and LDS at 700
 // TFLOP/s.  Eight waves of 128 x 64 keep a step's reads of LDS at 192 KiB; four of 128 x 128
 // read 128 KiB but leave a SIMD one wave (the loop 7% faster, start and end 60 us slower).
 //
-// STAGES tiles of the operands are in LDS or on their way there.  Where a compute unit has one
+// STAGES tiles of the operands are in LDS or on their way there, and of Q half a step longer
+// one more: its loads and P's then go out in different halves of a step, where both at once
+// wait for each other (8192 x 8192 x 8192 810 us instead of 772, 1600 x 4096 x 4096 69 instead
+// of 59, small products 2%).  At 256 x 256 these are all 160 KB.  Where a compute unit has one
 // or two workgroups, the time of a step is the loads' way through memory, and four stages
 // take as many steps to hide it.
 template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ, int STAGES>
@@ -588,9 +591,9 @@ gemm_kernel(const GemmArgs a) {
     typedef typename Mma<T>::V V;
     constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16;
     constexpr int PB = Tile<PA, TI>::kBytes, QB = Tile<QA, TJ>::kBytes;
-    constexpr uint32_t STAGE = PB + QB;              // a power of two, and of the tiles' places its own bit
+    constexpr uint32_t PLACES = STAGES * PB + (STAGES + 1) * QB;    // P's, then Q's
     constexpr uint32_t OUT = 2 * 16 * WI * (TJ + 4) * 4;   // write_out's place
-    __shared__ __align__(2 * STAGE) char lds[OUT > STAGES * STAGE ? OUT : STAGES * STAGE];
+    __shared__ __align__(PB) char lds[OUT > PLACES ? OUT : PLACES];
     BLK_LDS char* const room = (BLK_LDS char*)lds;
     RowTiles rows = {};
     if constexpr (BY_ROWS) rows = count_tiles(a, TI);
@@ -601,18 +604,18 @@ gemm_kernel(const GemmArgs a) {
     const int wave = threadIdx.x >> 6, wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
     Reader<PA, TI> rp;
     Reader<QA, TJ> rq;
-    const uint32_t first = (uint32_t)(uintptr_t)room;
-    rp.start(first, wi);
-    rq.start(first + PB, wj);
+    const uint32_t p_at = (uint32_t)(uintptr_t)room, q_at = p_at + STAGES * PB;
+    rp.start(p_at, wi);
+    rq.start(q_at, wj);
     f32x4 acc[FI][FJ];
 #pragma unroll
     for (int x = 0; x < FI; ++x)
 #pragma unroll
         for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t stage = 0;
     // Half a tile (32 deep) is multiplied from registers while the next half is read into
-    // others; behind the barrier in the middle of a tile the next tile has arrived and the
-    // loads of the one after it follow into the place just read.
+    // others.  Behind the barrier in the middle of a tile the next tile has arrived; the loads
+    // of P that are STAGES tiles ahead follow into the place just read, those of Q, which has
+    // one place more, in the next tile's first half.
     typedef Direct<T, PA, TI, THREADS> DP;
     typedef Direct<T, QA, TJ, THREADS> DQ;
     constexpr int PIECES = DP::kPieces + DQ::kPieces;
@@ -620,12 +623,6 @@ gemm_kernel(const GemmArgs a) {
     DQ lq;
     lp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
     lq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
-    const auto load = [&](int from, int to) {
-#pragma unroll
-        for (int k = from; k < to; ++k)
-            if (k < DP::kPieces) lp.piece(k);
-            else lq.piece(k - DP::kPieces);
-    };
     V fp[2][FI], fq[2][FJ];
     // reads of the other half in the first part of the block rows, so that they are done
     // when the last ones are
@@ -641,7 +638,13 @@ gemm_kernel(const GemmArgs a) {
         __builtin_amdgcn_s_setprio(now);     // loads and first reads behind the barrier go first
 #pragma unroll
         for (int x = 0; x < FI; ++x) {
-            if (now == 1) load(x * PIECES / FI, (x + 1) * PIECES / FI);
+            if constexpr (now == 0) {
+#pragma unroll
+                for (int k = x * DQ::kPieces / FI; k < (x + 1) * DQ::kPieces / FI; ++k) lq.piece(k);
+            } else {
+#pragma unroll
+                for (int k = x * DP::kPieces / FI; k < (x + 1) * DP::kPieces / FI; ++k) lp.piece(k);
+            }
             if (x < READS) read(now ^ 1, x);
             if (now == 1 && x == FI / 2) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
@@ -653,24 +656,33 @@ gemm_kernel(const GemmArgs a) {
     if (tiles > 0) {
 #pragma unroll
         for (int t = 0; t < STAGES; ++t) {
-            lp.aim(first + t * STAGE);
-            lq.aim(first + t * STAGE + PB);
-            load(0, PIECES);
+            lp.aim(p_at + t * PB);
+            lq.aim(q_at + t * QB);
+#pragma unroll
+            for (int k = 0; k < DP::kPieces; ++k) lp.piece(k);
+#pragma unroll
+            for (int k = 0; k < DQ::kPieces; ++k) lq.piece(k);
         }
         arrived<PIECES * (STAGES - 1)>();
 #pragma unroll
         for (int x = 0; x < READS; ++x) read(0, x);
     }
+    // the places of the tile that is read, and where Q's loads go
+    uint32_t p_now = 0, q_now = 0, q_new = STAGES * QB;
     for (int t = 0; t < tiles; ++t) {
         __builtin_amdgcn_s_waitcnt(0xC07F);  // the reads of half 0, before new ones
+        lq.aim(q_at + q_new);
+        q_new = q_now;
         multiply(Int<0>());
-        arrived<PIECES * (STAGES - 2)>();        // the next tile
-        lp.aim(first + stage);
-        lq.aim(first + stage + PB);
-        const uint32_t change = ((t ^ (t + 1)) & (STAGES - 1)) * STAGE;
-        stage ^= change;
-        rp.other(change);
-        rq.other(change);
+        // all but the loads behind the next tile's: of Q one tile's more than of P
+        arrived<PIECES * (STAGES - 2) + DQ::kPieces>();
+        lp.aim(p_at + p_now);
+        const uint32_t by_p = p_now == (STAGES - 1) * PB ? -p_now : PB;
+        const uint32_t by_q = q_now == STAGES * QB ? -q_now : QB;
+        p_now += by_p;
+        q_now += by_q;
+        rp.move(by_p);
+        rq.move(by_q);
         multiply(Int<1>());
     }
     arrived<0>();                            // the zeros past the end as well
