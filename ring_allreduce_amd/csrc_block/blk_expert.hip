@@ -7,19 +7,25 @@ namespace blk {
 
 // ------------------------------------------------------------------- sort --
 //
-// A counting sort.  The pairs are cut into pieces of kPiece consecutive ones, one wave
-// each, and kSortWaves pieces make a workgroup's share:  hist[g][e] = pairs of expert e in
-// share g;  its exclusive sum over g, plus the counts of the share's earlier waves, plus the
-// rank within the piece is the pair's rank.  Within 64 pairs a lane finds the lanes of its
-// own key with one ballot per key bit, so ranks need no atomics between waves and the
-// order is stable.  Three launches (count, sum over shares, place), or one workgroup for
-// everything while there are few pairs.  65536 x 8 pairs of 256 experts: 16 us, of which the
-// 12 MB that are read and written are 3; the rest is the three launches' chains of latency.
+// A counting sort.  The pairs are cut into pieces of N x 64 consecutive ones, one wave each,
+// and kSortWaves pieces make a workgroup's share:  hist[g][e] = pairs of expert e in share
+// g;  its exclusive sum over g, plus the counts of the share's earlier waves, plus the rank
+// within the piece is the pair's rank.  Within 64 pairs a lane finds the lanes of its own key
+// with one ballot per key bit, so ranks need no atomics between waves and the order is
+// stable.
+//
+// Bound by latency: one workgroup does everything for up to 4096 pairs, two launches (count,
+// place) sum the counts of up to 32 shares in the second one, and three (count, sum over
+// shares, place) sort the rest.  A lane takes as few of 1, 2, 4 or 8 pairs as that allows,
+// since its pairs go one after another: 64 pairs 4.9 us (3.0 on the GPU), 4096 7.9, 16384
+// 10.0, 65536 11.1; 524288 of 256 experts 16.8, of which the 12 MB that are read and written
+// are 3.
 
-constexpr int kItems = 8;              // pairs per lane
-constexpr int kPiece = 64 * kItems;    // pairs per wave
-constexpr int kSortWaves = 4;          // waves per workgroup of the three-launch form
+constexpr int kItems = 8;              // pairs per lane, at most
+constexpr int kSortWaves = 4;          // waves per workgroup of the forms of several launches
 constexpr int kOneWaves = 16;          // waves of the one-workgroup form, at most
+constexpr int kOneItems = 4;           // its pairs per lane, at most: with 8 the others are faster
+constexpr int kFewShares = 32;         // shares whose sums every workgroup finds by itself
 
 struct SortArgs {
     const void* ids;
@@ -34,52 +40,74 @@ struct SortArgs {
     int32_t* hist;      // [shares][experts]
 };
 
-template <typename I>
-__device__ __forceinline__ int key_of(const SortArgs& a, int p) {
-    if (p >= a.pairs) return a.experts;
-    uint64_t at = (uint64_t)p;
-    if (a.id_ld != (uint64_t)a.k) {
-        const uint32_t t = (uint32_t)p / (uint32_t)a.k;
-        at = (uint64_t)t * a.id_ld + ((uint32_t)p - t * (uint32_t)a.k);
+// The keys of the wave's pairs, first + i * 64 + lane; `experts` where there is none.  The
+// loads go out together, those past the end to the last pair.
+template <typename I, int N>
+__device__ __forceinline__ void load_keys(const SortArgs& a, int first, int (&key)[N]) {
+    const int lane = threadIdx.x & 63;
+    I id[N] = {};
+    if (a.pairs > 0) {
+        uint64_t at[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) at[i] = (uint64_t)min(first + i * 64 + lane, a.pairs - 1);
+        if (a.id_ld != (uint64_t)a.k) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t t = (uint32_t)at[i] / (uint32_t)a.k;
+                at[i] += (uint64_t)t * (a.id_ld - (uint64_t)a.k);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) id[i] = ((const I*)a.ids)[at[i]];
     }
-    const I id = ((const I*)a.ids)[at];
-    return id >= 0 && id < (I)a.experts ? (int)id : a.experts;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        key[i] = first + i * 64 + lane < a.pairs && id[i] >= 0 && id[i] < (I)a.experts ? (int)id[i] : a.experts;
 }
 
-// The lanes whose key equals this lane's.
-__device__ __forceinline__ uint64_t lanes_of_key(int key, int bits) {
-    uint64_t same = ~0ull;
-    for (int b = 0; b < bits; ++b) {
-        const bool one = (key >> b) & 1;
-        const uint64_t ones = __ballot(one);
-        same &= one ? ones : ~ones;
-    }
-    return same;
-}
-
-// Places the wave's kItems x 64 pairs; base[e] is the rank of expert e's next pair.
-__device__ __forceinline__ void place_piece(const SortArgs& a, const int* key, int first,
+// Places the wave's N x 64 pairs; base[e] is the rank of expert e's next pair.  Each
+// step is done for all items before the next, so that a wave, which may have its SIMD to
+// itself, does not wait for one item's chain of ballots, atomic, shuffle and store after
+// another; LDS keeps the atomics of a wave in their order.
+template <int N>
+__device__ __forceinline__ void place_piece(const SortArgs& a, const int (&key)[N], int first,
                                             int* base, const int* start) {
     const int lane = threadIdx.x & 63;
+    uint64_t same[N];     // the lanes whose key equals this lane's
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int p = first + i * 64 + lane;
-        const uint64_t same = lanes_of_key(key[i], a.bits);
-        const int leader = __ffsll((unsigned long long)same) - 1;
-        int rank = 0;
-        if (lane == leader && key[i] < a.experts)
-            rank = atomicAdd(&base[key[i]], __popcll(same));
-        rank = __shfl(rank, leader) + __popcll(same & ((1ull << lane) - 1));
-        int slot = -1;
+    for (int i = 0; i < N; ++i) same[i] = ~0ull;
+    for (int b = 0; b < a.bits; ++b) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool one = (key[i] >> b) & 1;
+            const uint64_t ones = __ballot(one);
+            same[i] &= one ? ones : ~ones;
+        }
+    }
+    int rank[N], slot[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        rank[i] = 0;
+        if (lane == __ffsll((unsigned long long)same[i]) - 1 && key[i] < a.experts)
+            rank[i] = atomicAdd(&base[key[i]], __popcll(same[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        rank[i] = __shfl(rank[i], __ffsll((unsigned long long)same[i]) - 1) + __popcll(same[i] & ((1ull << lane) - 1));
+        slot[i] = -1;
         if (key[i] < a.experts) {
             if (a.capacity == 0)
-                slot = start[key[i]] + rank;
-            else if (rank < a.capacity)
-                slot = key[i] * a.capacity + rank;
+                slot[i] = start[key[i]] + rank[i];
+            else if (rank[i] < a.capacity)
+                slot[i] = key[i] * a.capacity + rank[i];
         }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int p = first + i * 64 + lane;
         if (p < a.pairs) {
-            a.slots[p] = slot;
-            if (slot >= 0) a.sources[slot] = p;
+            a.slots[p] = slot[i];
+            if (slot[i] >= 0) a.sources[slot[i]] = p;
         }
     }
 }
@@ -131,25 +159,32 @@ __device__ __forceinline__ void fill_unused(const SortArgs& a, const int* counts
 }
 
 // The waves' counts of their keys: mine[e] of each, all zero before.
-__device__ __forceinline__ void count_keys(const SortArgs& a, const int* key, int* mine) {
+template <int N>
+__device__ __forceinline__ void count_keys(const SortArgs& a, const int (&key)[N], int* mine) {
 #pragma unroll
-    for (int i = 0; i < kItems; ++i)
+    for (int i = 0; i < N; ++i)
         if (key[i] < a.experts) atomicAdd(&mine[key[i]], 1);
 }
 
-template <typename I>
+// Workgroups go to the 8 XCDs in turn; each XCD gets shares that follow one another, so that
+// an expert's neighbouring rows are written through one L2.
+__device__ __forceinline__ int share_of_block(const SortArgs& a) {
+    const int x = (int)blockIdx.x & 7, each = a.shares >> 3, more = a.shares & 7;
+    return x * each + min(x, more) + ((int)blockIdx.x >> 3);
+}
+
+template <typename I, int N>
 __global__ void __launch_bounds__(64 * kSortWaves) sort_count_kernel(const SortArgs a) {
     extern __shared__ int lds[];
+    const int share = share_of_block(a);
+    int key[N];
+    load_keys<I>(a, (share * kSortWaves + (int)(threadIdx.x >> 6)) * N * 64, key);
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) lds[e] = 0;
-    const int piece = blockIdx.x * kSortWaves + (threadIdx.x >> 6);
-    int key[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) key[i] = key_of<I>(a, piece * kPiece + i * 64 + (int)(threadIdx.x & 63));
     __syncthreads();
     count_keys(a, key, lds);
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
-        a.hist[(uint64_t)blockIdx.x * a.experts + e] = lds[e];
+        a.hist[(uint64_t)share * a.experts + e] = lds[e];
 }
 
 // Exclusive sum of hist over the shares: a wave an expert, a lane four shares at a time.
@@ -179,60 +214,91 @@ __global__ void __launch_bounds__(256) sort_sum_kernel(const SortArgs a) {
     if (lane == 0) a.counts[e] = before;
 }
 
-// base[w][e]: counts of the waves -> rank of wave w's first pair of expert e; the counts of
-// all waves come to `all`, if given.
-__device__ __forceinline__ void ranks_of_waves(int* base, int waves, int experts, const int* before, int* all) {
-    for (int e = threadIdx.x; e < experts; e += blockDim.x) {
-        int at = before ? before[e] : 0;
-        for (int w = 0; w < waves; ++w) {
-            const int n = base[w * experts + e];
-            base[w * experts + e] = at;
-            at += n;
-        }
-        if (all) all[e] = at;
+// base[w][e]: counts of the waves -> rank of wave w's first pair of expert e, from `at`;
+// returns the rank of the first pair behind them.
+__device__ __forceinline__ int ranks_of_waves(int* base, int waves, int experts, int e, int at) {
+    for (int w = 0; w < waves; ++w) {
+        const int n = base[w * experts + e];
+        base[w * experts + e] = at;
+        at += n;
     }
-    __syncthreads();
+    return at;
 }
 
-template <typename I>
+// FEW: hist holds the shares' counts, which are summed here; otherwise sort_sum_kernel has.
+template <typename I, int N, bool FEW>
 __global__ void __launch_bounds__(64 * kSortWaves) sort_place_kernel(const SortArgs a) {
     extern __shared__ int lds[];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    constexpr int THREADS = 64 * kSortWaves, EACH = (RR_MAX_EXPERTS + THREADS - 1) / THREADS;
+    const int wave = threadIdx.x >> 6, share = share_of_block(a);
     int* start = lds;                                  // experts + 1
     int* base = lds + a.experts + 1;                   // [kSortWaves][experts]
-    for (int i = threadIdx.x; i < kSortWaves * a.experts; i += blockDim.x) base[i] = 0;
-    const int piece = blockIdx.x * kSortWaves + wave;
-    int key[kItems];
+    int* sums = base + kSortWaves * a.experts;         // experts, if FEW
+    const int first = (share * kSortWaves + wave) * N * 64;
+    int key[N], before[EACH];
+    load_keys<I>(a, first, key);
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) key[i] = key_of<I>(a, piece * kPiece + i * 64 + lane);
+    for (int u = 0; u < EACH; ++u) {
+        if (u * THREADS >= a.experts) break;
+        const int e = u * THREADS + (int)threadIdx.x;
+        const int* const from = a.hist + min(e, a.experts - 1);
+        if constexpr (!FEW) {
+            before[u] = from[(uint64_t)share * a.experts];
+        } else {
+            int all = 0;
+            before[u] = 0;
+            for (int c0 = 0; c0 < a.shares; c0 += 16) {
+                int n[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) n[c] = from[min(c0 + c, a.shares - 1) * a.experts];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    all += c0 + c < a.shares ? n[c] : 0;
+                    before[u] += c0 + c < share ? n[c] : 0;
+                }
+            }
+            if (e < a.experts) {
+                sums[e] = all;
+                if (blockIdx.x == 0) a.counts[e] = all;
+            }
+        }
+    }
+    for (int i = threadIdx.x; i < kSortWaves * a.experts; i += THREADS) base[i] = 0;
     __syncthreads();
     count_keys(a, key, base + wave * a.experts);
-    if (a.capacity == 0) prefix_counts(a.counts, start, a.experts);
+    const int* const counts = FEW ? sums : a.counts;
+    if (FEW) __syncthreads();
+    if (a.capacity == 0) prefix_counts(counts, start, a.experts);
     else __syncthreads();
-    ranks_of_waves(base, kSortWaves, a.experts, a.hist + (uint64_t)blockIdx.x * a.experts, nullptr);
-    place_piece(a, key, piece * kPiece, base + wave * a.experts, start);
-    fill_unused(a, a.counts, start);
+    fill_unused(a, counts, start);
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
+        const int e = u * THREADS + (int)threadIdx.x;
+        if (e < a.experts) ranks_of_waves(base, kSortWaves, a.experts, e, before[u]);
+    }
+    __syncthreads();
+    place_piece(a, key, first, base + wave * a.experts, start);
 }
 
-// Everything in one workgroup: wave w takes piece w.
-template <typename I>
+// Everything in one workgroup: wave w takes N x 64 pairs.
+template <typename I, int N>
 __global__ void __launch_bounds__(64 * kOneWaves) sort_one_kernel(const SortArgs a) {
     extern __shared__ int lds[];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = (int)blockDim.x >> 6;
+    const int wave = threadIdx.x >> 6, waves = (int)blockDim.x >> 6;
     int* counts = lds;                                 // experts
     int* start = lds + a.experts;                      // experts + 1
     int* base = lds + 2 * a.experts + 1;               // [waves][experts]
+    int key[N];
+    load_keys<I>(a, wave * N * 64, key);
     for (int i = threadIdx.x; i < waves * a.experts; i += blockDim.x) base[i] = 0;
-    int key[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) key[i] = key_of<I>(a, wave * kPiece + i * 64 + lane);
     __syncthreads();
     count_keys(a, key, base + wave * a.experts);
     __syncthreads();
-    ranks_of_waves(base, waves, a.experts, nullptr, counts);
-    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) a.counts[e] = counts[e];
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
+        a.counts[e] = counts[e] = ranks_of_waves(base, waves, a.experts, e, 0);
+    __syncthreads();
     if (a.capacity == 0) prefix_counts(counts, start, a.experts);
-    place_piece(a, key, wave * kPiece, base + wave * a.experts, start);
+    place_piece(a, key, wave * N * 64, base + wave * a.experts, start);
     fill_unused(a, counts, start);
 }
 
@@ -458,30 +524,61 @@ static rr_status_t check_sort(size_t tokens, int k, int experts, size_t capacity
     if (k < 1 || experts < 1) return RR_ERR_INVALID;
     if (experts > RR_MAX_EXPERTS || tokens > kMaxInt / (uint64_t)k) return RR_ERR_UNSUPPORTED;
     // the last workgroup's pieces may reach past the pairs, and must still count in 32 bits
-    if ((uint64_t)tokens * k > kMaxInt - kPiece * kSortWaves) return RR_ERR_UNSUPPORTED;
+    if ((uint64_t)tokens * k > kMaxInt - 64 * kItems * kSortWaves) return RR_ERR_UNSUPPORTED;
     if (capacity > kMaxInt / (uint64_t)experts) return RR_ERR_UNSUPPORTED;
     return RR_OK;
 }
 
-static uint64_t sort_shares(uint64_t pairs) { return ceil_div(pairs, kPiece * kSortWaves); }
+// The fewest pairs a lane of 1, 2, 4 .. at_most with which `waves` waves take all.
+static int items_for(uint64_t pairs, int waves, int at_most) {
+    int n = 1;
+    while (n < at_most && pairs > (uint64_t)64 * n * waves) n *= 2;
+    return n;
+}
+// Few shares while four pairs a lane or fewer allow that (65536 pairs in 64 shares of four:
+// 10.5 us, in 32 of eight 12.1); four too while a compute unit has no second share (131072
+// pairs 12.2 instead of 14.7; 524288 of 256 experts 17.5 instead of 16.9).
+static int sort_items(uint64_t pairs) {
+    const int n = items_for(pairs, kSortWaves * kFewShares, 4);
+    return n == 4 && pairs > (uint64_t)64 * 4 * kSortWaves * 256 ? kItems : n;
+}
+static uint64_t sort_shares(uint64_t pairs) { return ceil_div(pairs, 64 * sort_items(pairs) * kSortWaves); }
 // base, counts and start of every expert in the LDS of one workgroup
 static bool one_workgroup(uint64_t pairs, int experts) {
-    return pairs <= (uint64_t)kPiece * kOneWaves && experts <= 512;
+    return pairs <= (uint64_t)64 * kOneItems * kOneWaves && experts <= 512;
+}
+
+template <typename I, int N> static void run_one(const SortArgs& a, hipStream_t s) {
+    const unsigned pieces = (unsigned)ceil_div(a.pairs, 64 * N), waves = pieces < 4 ? 4 : pieces;
+    const size_t lds = ((waves + 2) * (size_t)a.experts + 1) * sizeof(int32_t);
+    sort_one_kernel<I, N><<<1, 64 * waves, lds, s>>>(a);
+}
+
+template <typename I, int N> static void run_shares(const SortArgs& a, hipStream_t s) {
+    const unsigned grid = (unsigned)a.shares;
+    const size_t word = sizeof(int32_t), lds = ((kSortWaves + 2) * (size_t)a.experts + 1) * word;
+    sort_count_kernel<I, N><<<grid, 64 * kSortWaves, a.experts * word, s>>>(a);
+    if (N < 4 || (N == 4 && a.shares <= kFewShares)) {
+        if constexpr (N <= 4) sort_place_kernel<I, N, true><<<grid, 64 * kSortWaves, lds, s>>>(a);
+    } else if constexpr (N >= 4) {
+        sort_sum_kernel<<<(unsigned)ceil_div(a.experts, 4), 256, 0, s>>>(a);
+        sort_place_kernel<I, N, false><<<grid, 64 * kSortWaves, lds, s>>>(a);
+    }
 }
 
 template <typename I> static rr_status_t run_sort(const SortArgs& a, hipStream_t s) {
-    const size_t word = sizeof(int32_t);
     if (one_workgroup((uint64_t)a.pairs, a.experts)) {
-        const unsigned pieces = (unsigned)ceil_div(a.pairs, kPiece), waves = pieces < 4 ? 4 : pieces;
-        const size_t lds = ((waves + 2) * (size_t)a.experts + 1) * word;
-        sort_one_kernel<I><<<1, 64 * waves, lds, s>>>(a);
-        return launched();
+        const int n = items_for((uint64_t)a.pairs, kOneWaves, kOneItems);
+        if (n == 1) run_one<I, 1>(a, s);
+        else if (n == 2) run_one<I, 2>(a, s);
+        else run_one<I, 4>(a, s);
+    } else {
+        const int n = sort_items((uint64_t)a.pairs);
+        if (n == 1) run_shares<I, 1>(a, s);
+        else if (n == 2) run_shares<I, 2>(a, s);
+        else if (n == 4) run_shares<I, 4>(a, s);
+        else run_shares<I, 8>(a, s);
     }
-    const unsigned grid = (unsigned)a.shares;
-    sort_count_kernel<I><<<grid, 64 * kSortWaves, a.experts * word, s>>>(a);
-    sort_sum_kernel<<<(unsigned)ceil_div(a.experts, 4), 256, 0, s>>>(a);
-    const size_t lds = ((kSortWaves + 1) * (size_t)a.experts + 1) * word;
-    sort_place_kernel<I><<<grid, 64 * kSortWaves, lds, s>>>(a);
     return launched();
 }
 

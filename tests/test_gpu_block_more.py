@@ -268,3 +268,11 @@ def test_unusual_forms_give_the_same(rr):
     side.synchronize()
     assert torch.equal(one.dx, two.dx) and torch.equal(one.dbranch, two.dbranch)
     assert one.dgate is None and two.dpost_weight is None
+
+
+@pytest.mark.parametrize("pairs", [1024, 1025, 2049, 4095, 4097, 8192, 8193, 16385, 32768, 32769, 65537, 262144, 262145])
+@pytest.mark.parametrize("experts,capacity", [(7, 0), (256, 90), (1024, 0)])
+def test_sort_at_the_edges_of_its_forms(rr, pairs, experts, capacity):
+    ids = make_ids(pairs, 1, experts, "masked", pairs + experts)
+    check_order(rr.expert_sort(torch.from_numpy(ids).cuda(), experts, capacity),
+                order_of(ids, experts, capacity))
