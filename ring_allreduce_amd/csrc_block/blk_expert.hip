@@ -558,9 +558,11 @@ template <typename I, int N> static void run_shares(const SortArgs& a, hipStream
     const unsigned grid = (unsigned)a.shares;
     const size_t word = sizeof(int32_t), lds = ((kSortWaves + 2) * (size_t)a.experts + 1) * word;
     sort_count_kernel<I, N><<<grid, 64 * kSortWaves, a.experts * word, s>>>(a);
-    if (N < 4 || (N == 4 && a.shares <= kFewShares)) {
+    // a thread of the place kernel sums the counts of one expert in 256 after another: 32
+    // shares of 1024 experts 18.2 us, with the kernel that sums them 16.0
+    if (N <= 4 && a.shares * ceil_div(a.experts, 64 * kSortWaves) <= kFewShares) {
         if constexpr (N <= 4) sort_place_kernel<I, N, true><<<grid, 64 * kSortWaves, lds, s>>>(a);
-    } else if constexpr (N >= 4) {
+    } else {
         sort_sum_kernel<<<(unsigned)ceil_div(a.experts, 4), 256, 0, s>>>(a);
         sort_place_kernel<I, N, false><<<grid, 64 * kSortWaves, lds, s>>>(a);
     }
