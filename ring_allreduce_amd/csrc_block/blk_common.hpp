@@ -86,9 +86,36 @@ __device__ __forceinline__ float logistic(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
 
+// The normal distribution beyond a >= 0: *tail = 1 - Phi(a), off by 1.4e-6 of itself up to 5,
+// where 1 - erf has lost all but a digit; returns exp(-a^2 / 2).  The tail is that times a
+// polynomial in 1 / (1 + 0.3 a), fitted to the least largest relative error (8.6e-8) over 0
+// .. 20; the rest is the rounding of a^2 / 2.  Without branches: the two ranges of erff, both
+// taken by most waves, cost the GELU of 1001 x 1111 values 6 us behind its product.
+__device__ __forceinline__ float normal_tail(float a, float* tail) {
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3f * a);
+    const float c[9] = {6.19887214e-06f, 0.119510077f, 0.121712074f, 0.0957123935f, 0.139562428f,
+                        -0.0713275298f, 0.223317936f, -0.166166559f, 0.0376729406f};
+    float q = c[8];
+#pragma unroll
+    for (int k = 7; k >= 0; --k) q = q * t + c[k];
+    const float e = __expf(-0.5f * a * a);
+    *tail = e * q;
+    return e;
+}
+// |z|, at most 20, from where on the tail is 0 in 32 bits; NaN stays.
+__device__ __forceinline__ float magnitude(float z) {
+    const float a = fabsf(z);
+    return a > 20.0f ? 20.0f : a;
+}
+
 template <int ACT> __device__ __forceinline__ float act_of(float z) {
     if constexpr (ACT == RR_ACT_RELU) return z > 0.0f || z != z ? z : 0.0f;
-    if constexpr (ACT == RR_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    if constexpr (ACT == RR_ACT_GELU) {        // z Phi(z), for either sign from the tail
+        const float a = magnitude(z);
+        float tail;
+        normal_tail(a, &tail);
+        return fmaxf(z, 0.0f) - a * tail;
+    }
     if constexpr (ACT == RR_ACT_SILU) return z * logistic(z);
     if constexpr (ACT == RR_ACT_SIGMOID) return logistic(z);
     return z;
@@ -97,9 +124,12 @@ template <int ACT> __device__ __forceinline__ float act_of(float z) {
 // d act / d z; 0 at the corner of relu.
 template <int ACT> __device__ __forceinline__ float slope_of(float z) {
     if constexpr (ACT == RR_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if constexpr (ACT == RR_ACT_GELU)
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-               z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+    if constexpr (ACT == RR_ACT_GELU) {
+        const float a = magnitude(z);
+        float tail;
+        const float e = normal_tail(a, &tail);
+        return (z > 0.0f ? 1.0f - tail : tail) + copysignf(a, z) * e * 0.39894228040143268f;
+    }
     if constexpr (ACT == RR_ACT_SILU) {
         const float q = logistic(z);
         return q * (1.0f + z * (1.0f - q));

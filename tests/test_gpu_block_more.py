@@ -276,3 +276,30 @@ def test_sort_at_the_edges_of_its_forms(rr, pairs, experts, capacity):
     ids = make_ids(pairs, 1, experts, "masked", pairs + experts)
     check_order(rr.expert_sort(torch.from_numpy(ids).cuda(), experts, capacity),
                 order_of(ids, experts, capacity))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_gelu_of_single_values(rr, dtype):
+    """x w^T with k = 1 and w = 1 is x itself, so this is the activation and its slope alone.
+    What lies beyond z is off by the rounding of z^2 / 2 (two steps of 2^-24 of at most 18),
+    the exponential's and the fit's, together 4e-6 of it."""
+    dt = DTYPES[dtype]
+    z = torch.cat([torch.linspace(-6, 6, 24001), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 19.0, 21.0, 1e4, 6e4])])
+    x = z.to(dt).cuda()[:, None]
+    one = torch.ones(1, 1, dtype=dt, device="cuda")
+    out, kept = rr.block_linear(x, one, act="gelu", save_preact=True)
+    assert torch.equal(kept, x)
+    v = x.double()
+    tail = 0.5 * torch.special.erfc(v.abs() * 0.5 ** 0.5)
+    want = v.clamp(min=0) - v.abs() * tail
+    half = torch.finfo(dt).eps / 2
+    least = torch.finfo(dt).smallest_normal * half          # half a step of the smallest values
+    assert bool(((out.double() - want).abs() <= 4e-6 * v.abs() * tail + (half + 2.0 ** -23) * want.abs() + least).all())
+    dz = rr.block_linear_backward(torch.ones_like(x), x, one, x, act="gelu", need_dw=False, need_db=False).dx
+    density = torch.exp(-0.5 * v * v) * 0.3989422804014327
+    slope = torch.where(v > 0, 1 - tail, tail) + v * density
+    bound = 4e-6 * (tail + v.abs() * density) + (2 * half + 2.0 ** -22) * slope.abs() + 2 * least
+    assert bool(((dz.double() - slope).abs() <= bound).all())
+    far = torch.tensor([[float("inf")], [float("nan")]], dtype=dt, device="cuda")
+    got = rr.block_linear(far, one, act="gelu")
+    assert float(got[0]) == float("inf") and bool(got[1].isnan())
