@@ -497,6 +497,10 @@ __device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, BLK_
     const bool whole = a.splits == 1 && s.parts == 1, add = whole && a.residual && s.g.group >= 0;
     if (!whole && s.g.group < 0) return;        // join_kernel knows
     const int col = thread % GROUPS * 8, n = a.j - s.j0 - col;
+    // A tile of whole columns knows that of all its threads.  With the last columns, the tile
+    // takes one way for all threads too: two in one wave, for its whole and its cut pieces of
+    // 8 columns, would be two epilogues (3000 x 3001 x 3001 with GELU 102 us instead of 87).
+    const bool inside = s.j0 + TJ <= a.j;
     // A matrix's rows: those of block row 0 by 32-bit offsets from the tile's corner, and 16
     // rows on for each block row (rows are at most 2^22 elements apart).
     const uint64_t corner_out = (a.out_group && whole ? (uint64_t)s.g.group * a.out_group : 0);
@@ -523,19 +527,19 @@ __device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, BLK_
         at_res[t] = (row * (uint32_t)a.residual_ld + col) * (uint32_t)sizeof(T);
         left[t] = n > 0 ? s.i_end - s.i0 - (int)row : 0;
     }
-    const Some<T, 8> bias = whole && n >= 8 ? bias_of<T, 8>(a, s.g.group, s.j0 + col) : Some<T, 8>{};
+    const Some<T, 8> bias = whole ? bias_of<T, 8>(a, s.g.group, s.j0 + col) : Some<T, 8>{};
     Some<T, 8> residual[EACH] = {}, later[EACH] = {};
     const auto fetch = [&](Some<T, 8> (&to)[EACH], int x) {
         const char* from = res + (uint64_t)(x * 16) * a.residual_ld * sizeof(T);
 #pragma unroll
         for (int t = 0; t < EACH; ++t)
-            if (x * 16 < left[t] && n >= 8) to[t] = load_some<T, 8>((const T*)(from + at_res[t]), 8);
+            if (x * 16 < left[t]) to[t] = load_some<T, 8>((const T*)(from + at_res[t]), 8);
     };
-    if (add) fetch(residual, 0);
+    if (add && inside) fetch(residual, 0);
     for (int x = 0; x < FI; ++x) {
         BLK_LDS float* const buf = store + (x & 1) * BUFFER;
         BLK_LDS float* const mine = buf + (wave / WJ * 16 + (lane & 15)) * LINE + wave % WJ * (TJ / WJ) + (lane >> 4) * 4;
-        if (add && x + 1 < FI) fetch(later, x + 1);
+        if (add && inside && x + 1 < FI) fetch(later, x + 1);
 #pragma unroll
         for (int u = 0; u < FI; ++u)
             if (u == x)
@@ -552,13 +556,12 @@ __device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, BLK_
             float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             if (!whole) {
                 store_wide<8>((float*)(to + at_out[t]), n, v);
-            } else if (n >= 8) {
+            } else if (inside) {
                 finish<T, 8>(a, s.g.group, 8, v, bias, residual[t], (T*)(to_z + at_z[t]), to + at_out[t]);
-            } else {       // the last columns: their elements' loads together, then their stores
+            } else {
                 Some<T, 8> r = {};
                 if (add) r = load_some<T, 8>((const T*)(res + (uint64_t)(x * 16) * a.residual_ld * sizeof(T) + at_res[t]), n);
-                finish<T, 8>(a, s.g.group, n, v, bias_of<T, 8>(a, s.g.group, s.j0 + col), r,
-                             (T*)(to_z + at_z[t]), to + at_out[t]);
+                finish<T, 8>(a, s.g.group, n, v, bias, r, (T*)(to_z + at_z[t]), to + at_out[t]);
             }
         }
 #pragma unroll
