@@ -23,8 +23,6 @@ constexpr int tile_rows(int tile) {
     return tile == kTile256 ? 256 : tile == kTile128 ? 128 : tile == kTile64 || tile == kStream64 ? 64
            : tile == kStream32 ? 32 : tile == kDot ? 4 : 16;
 }
-constexpr int kStreamCols = 32;
-constexpr int tile_cols(int tile) { return tile >= kStream16 ? kStreamCols : tile_rows(tile); }
 
 struct GemmArgs {
     const void *p, *q;
@@ -52,6 +50,8 @@ struct GemmPlan {
     int32_t form, tile;
     int32_t direct;                  // kStream*: rows of both operands at 16-byte boundaries
     int32_t deep;                    // kTile128, kTile64: four stages in LDS, else two
+    int32_t narrow;                  // kStream*: 16 columns a workgroup, else 32
+    int cols() const { return tile < kStream16 ? tile_rows(tile) : narrow ? 16 : 32; }
 };
 
 rr_status_t launch_gemm_bf16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
@@ -694,9 +694,9 @@ gemm_kernel(const GemmArgs a) {
 
 // ------------------------------------------------------------ few rows: one pass --
 //
-// The forward product of a few rows is the read of the weights (1 x 8192 x 8192 bf16: 31 us,
-// 4.3 TB/s; weights that the last call left in the caches are no faster).  A workgroup takes
-// 16 FI rows x 32 columns, its waves parts of the contraction, 128 deep each in turn;
+// The forward product of a few rows is the read of the weights (4 x 8192 x 8192 bf16: 27 us,
+// 4.9 TB/s; 4 x 16384 x 8192 55).  A workgroup takes 16 FI rows x 16 FJ columns, its waves
+// parts of the contraction, 128 deep each in turn;
 // operands go from memory to registers in the fragments' own layout (a lane's 16 bytes
 // are 8 values of one row, four lanes make 64 neighbouring bytes), and the waves' sums
 // meet in LDS, added in the order of the waves.
@@ -745,16 +745,15 @@ template <typename T, int R, bool DIRECT> struct Strip {
     }
 };
 
-template <typename T, int FI, bool DIRECT>
+template <typename T, int FI, int FJ, bool DIRECT>
 __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArgs a) {
     typedef typename Mma<T>::V V;
-    constexpr int FJ = kStreamCols / 16;
     __shared__ f32x4 sums[kStreamWaves][FI * FJ][64];
     Range g;
     if (!find_tile(a, count_tiles(a, 16 * FI), (int)blockIdx.y, 16 * FI, g)) return;
     g.group = __builtin_amdgcn_readfirstlane(g.group);
     const int i0 = __builtin_amdgcn_readfirstlane(g.lo), i_end = __builtin_amdgcn_readfirstlane(g.hi);
-    const int j0 = (int)blockIdx.x * kStreamCols, lane = threadIdx.x & 63;
+    const int j0 = (int)blockIdx.x * (16 * FJ), lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int c_lo = 0, c_end = g.group < 0 ? 0 : a.c;
     if (a.splits > 1) {
@@ -824,11 +823,11 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArg
 //
 // Up to four rows of one group: a wave goes along one row of the weights, or two, 1 KiB of
 // each at a time, and adds products in 32 bits on the vector units.  The weights are read in
-// memory's own order and at any alignment: 1 x 8192 x 8192 takes 25.5 us (5.2 TB/s) against 33
-// of the one-pass form above, 1 x 4096 x 4096 8.2 against 13, 3 x 572 x 2366 (rows without
-// whole 16-byte pieces) 6.2 against 16.  Every row of x costs as many loads from the caches as
-// the weights do from memory, so with aligned rows it ends at two (2 x 8192 x 8192: 30 against
-// 33; 4: 46 against 33).
+// memory's own order and at any alignment: 1 x 8192 x 8192 takes 23 us (5.8 TB/s) against 27 of
+// the one-pass form above, 1 x 4096 x 4096 7.3 against 9.9, 3 x 572 x 2366 (rows without whole
+// 16-byte pieces) 6.2 against 16.  Every row of x costs as many loads from the caches as the
+// weights do from memory, so with aligned rows it ends at two (2 x 8192 x 8192: 23 against 27;
+// 4: 46 against 27).
 constexpr int kDotWaves = 4;
 
 template <typename T, int M, int R>
@@ -995,6 +994,15 @@ static void launch_form(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
     else gemm_kernel<T, PA, QA, BY_ROWS, 64, 64, 2, 2, 2><<<grid, 256, 0, s>>>(a);
 }
 
+template <typename T, int FI> static void launch_stream(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
+    const dim3 grid((unsigned)a.tiles_j, (unsigned)a.tiles_i, (unsigned)a.splits);
+    const int threads = 64 * kStreamWaves;
+    if (p.direct && p.narrow) stream_kernel<T, FI, 1, true><<<grid, threads, 0, s>>>(a);
+    else if (p.direct) stream_kernel<T, FI, 2, true><<<grid, threads, 0, s>>>(a);
+    else if (p.narrow) stream_kernel<T, FI, 1, false><<<grid, threads, 0, s>>>(a);
+    else stream_kernel<T, FI, 2, false><<<grid, threads, 0, s>>>(a);
+}
+
 template <typename T> static rr_status_t launch_gemm(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
     if (p.tile == kDot) {
         // two rows of the weights a wave where that leaves no compute unit empty
@@ -1004,17 +1012,9 @@ template <typename T> static rr_status_t launch_gemm(const GemmArgs& a, const Ge
         else if (a.rows == 3) launch_dot<T, 3, 1>(a, s);
         else launch_dot<T, 4, 1>(a, s);
     } else if (p.tile >= kStream16) {
-        const dim3 grid((unsigned)a.tiles_j, (unsigned)a.tiles_i, (unsigned)a.splits);
-        const int threads = 64 * kStreamWaves;
-        if (p.direct) {
-            if (p.tile == kStream16) stream_kernel<T, 1, true><<<grid, threads, 0, s>>>(a);
-            else if (p.tile == kStream32) stream_kernel<T, 2, true><<<grid, threads, 0, s>>>(a);
-            else stream_kernel<T, 4, true><<<grid, threads, 0, s>>>(a);
-        } else {
-            if (p.tile == kStream16) stream_kernel<T, 1, false><<<grid, threads, 0, s>>>(a);
-            else if (p.tile == kStream32) stream_kernel<T, 2, false><<<grid, threads, 0, s>>>(a);
-            else stream_kernel<T, 4, false><<<grid, threads, 0, s>>>(a);
-        }
+        if (p.tile == kStream16) launch_stream<T, 1>(a, p, s);
+        else if (p.tile == kStream32) launch_stream<T, 2>(a, p, s);
+        else launch_stream<T, 4>(a, p, s);
     } else if (p.form == kForward) {
         launch_form<T, false, false, true>(a, p, s);
     } else if (p.form == kByX) {

@@ -217,7 +217,7 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
     const uint64_t i = form == kByW ? a->n : a->rows, j = form == kForward ? a->n : a->k;
     const uint64_t c = form == kForward ? a->k : form == kByX ? a->n : mean;
     const double outputs = (double)(form == kByW ? groups * i : i) * j;
-    GemmPlan p = {form, kTile64, 0, 0};
+    GemmPlan p = {form, kTile64, 0, 0, 0};
     *splits = 1;
     *slots = 0;
     if (form == kForward && groups == 1 && !a->offsets && a->rows <= 2) {
@@ -226,7 +226,14 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
     }
     if (form == kForward && (mean <= 16 || (mean <= 64 && c <= 1024))) {
         p.tile = mean <= 16 ? kStream16 : mean <= 32 ? kStream32 : kStream64;
-        const uint64_t blocks = ceil_div(j, kStreamCols) * ceil_div(a->rows, 16);
+        // 16 columns a workgroup instead of 32 where that gives a compute unit no more than two,
+        // of more rows than 16 one: 4 x 8192 x 8192 27 us against 31, 4 x 4096 x 4096 9.9 (12.2),
+        // 4 x 1024 x 4096 8.7 (9.6), 64 x 4096 x 1024 9.0 (10.0); but 4 x 16384 x 1024 9.8
+        // (9.2), 64 x 8200 x 1000 14.4 (12.1), and with longer rows 4 x 8192 x 16384 54 (44),
+        // 4 x 2048 x 16384 20.8 (18.7)
+        const uint64_t high = ceil_div(a->rows, tile_rows(p.tile));
+        p.narrow = c <= 8192 && ceil_div(j, 16) * high <= (p.tile == kStream16 ? 2 : 1) * kSlots;
+        const uint64_t blocks = ceil_div(j, p.cols()) * high;
         const uint64_t want = 256 / blocks, most = c / 1024;
         const uint64_t n = want < most ? want : most;
         *splits = n < 2 ? 1 : n > 16 ? 16 : (int)n;
@@ -333,7 +340,7 @@ static rr_status_t run_product(const rr_linear_t* a, Product r, void* workspace,
     int splits, slots;
     GemmPlan plan = choose(a, r.form, &splits, &slots);
     const uint64_t ti = r.form == kByW ? ceil_div(k.i, tile_rows(plan.tile)) : row_tiles(a, tile_rows(plan.tile));
-    const uint64_t tj = ceil_div(k.j, tile_cols(plan.tile));
+    const uint64_t tj = ceil_div(k.j, plan.cols());
     if (ti * tj == 0) return RR_OK;
     if (ti * tj * splits * (r.form == kByW ? (uint64_t)a->groups : 1) > (1u << 23) - 1) return RR_ERR_UNSUPPORTED;
     k.tiles_i = (int32_t)ti;

@@ -303,3 +303,11 @@ def test_gelu_of_single_values(rr, dtype):
     far = torch.tensor([[float("inf")], [float("nan")]], dtype=dt, device="cuda")
     got = rr.block_linear(far, one, act="gelu")
     assert float(got[0]) == float("inf") and bool(got[1].isnan())
+
+
+@pytest.mark.parametrize("rows,n,k,groups", [
+    (16, 8192, 264, 1), (5, 8208, 264, 1), (33, 4096, 520, 1), (32, 4112, 520, 1), (7, 1000, 8200, 1),
+    (3, 1000, 8192, 1), (40, 1040, 72, 5), (9, 530, 1001, 1), (64, 530, 1001, 1), (48, 5000, 999, 2)])
+def test_few_rows_at_the_edges_of_the_forms(rr, rows, n, k, groups):
+    d = make(rows, n, k, groups if groups > 1 else None, "bf16", True, True)
+    check_forward(rr, d, None, "silu", torch.bfloat16)
