@@ -17,10 +17,10 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 #define BLK_LDS __attribute__((address_space(3)))
 
 enum GemmForm { kForward = 0, kByX = 1, kByW = 2 };
-enum GemmTile { kTile256 = 0, kTile128 = 1, kTile64 = 2, kStream16 = 3, kStream32 = 4, kStream64 = 5,
-                kDot = 6 };
+enum GemmTile { kTile256 = 0, kTile128 = 1, kTile64 = 2, kInner64 = 3, kStream16 = 4, kStream32 = 5,
+                kStream64 = 6, kDot = 7 };
 constexpr int tile_rows(int tile) {
-    return tile == kTile256 ? 256 : tile == kTile128 ? 128 : tile == kTile64 || tile == kStream64 ? 64
+    return tile == kTile256 ? 256 : tile == kTile128 ? 128 : tile == kTile64 || tile == kInner64 || tile == kStream64 ? 64
            : tile == kStream32 ? 32 : tile == kDot ? 4 : 16;
 }
 
@@ -51,7 +51,7 @@ struct GemmPlan {
     int32_t direct;                  // kStream*: rows of both operands at 16-byte boundaries
     int32_t deep;                    // kTile128, kTile64: four stages in LDS, else two
     int32_t narrow;                  // kStream*: 16 columns a workgroup, else 32
-    int cols() const { return tile < kStream16 ? tile_rows(tile) : narrow ? 16 : 32; }
+    int cols() const { return tile < kInner64 ? tile_rows(tile) : tile >= kStream16 && narrow ? 16 : 32; }
 };
 
 rr_status_t launch_gemm_bf16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
@@ -260,7 +260,8 @@ __device__ __forceinline__ const char* uniform(const char* p) {
 // (arrived()) before the barrier behind which the tile is read.
 constexpr uint32_t kReach = 0x80000000u;   // rows of a tile span at most 256 * 2^22 * 2 bytes
 
-template <typename T, bool ACROSS, int ROWS, int THREADS> struct Direct {
+// THREADS: that load a tile together; PART: of a larger workgroup.
+template <typename T, bool ACROSS, int ROWS, int THREADS, bool PART> struct Direct {
     static constexpr int kPieces = ROWS * kDepth / 8 / THREADS;
     const char* base;
     uint64_t step;
@@ -274,7 +275,8 @@ template <typename T, bool ACROSS, int ROWS, int THREADS> struct Direct {
         step = (ACROSS ? ld : 1) * kDepth * sizeof(T);
         left = end - c0;
         mine = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) * 1024);
-        const int thread = here();
+        if constexpr (PART) mine %= THREADS * 16;
+        const int thread = PART ? here() % THREADS : here();
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {
             int y, x;
@@ -290,7 +292,7 @@ template <typename T, bool ACROSS, int ROWS, int THREADS> struct Direct {
         rsrc = u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFF, kReach, 0x00027000};
         to = tile + mine;
         if (left < kDepth) {
-            const int thread = here();
+            const int thread = PART ? here() % THREADS : here();
 #pragma unroll
             for (int k = 0; k < kPieces; ++k) {
                 int y, x;
@@ -496,6 +498,10 @@ __device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, BLK_
     const int thread = here(), lane = thread & 63, wave = thread >> 6;
     const bool whole = a.splits == 1 && s.parts == 1, add = whole && a.residual && s.g.group >= 0;
     if (!whole && s.g.group < 0) return;        // join_kernel knows
+    if (thread >= THREADS) {                    // of another part: there for the barriers
+        for (int x = 0; x < FI; ++x) __syncthreads();
+        return;
+    }
     const int col = thread % GROUPS * 8, n = a.j - s.j0 - col;
     // A tile of whole columns knows that of all its threads.  With the last columns, the tile
     // takes one way for all threads too: two in one wave, for its whole and its cut pieces of
@@ -588,15 +594,18 @@ template <int N> struct Int {
 // of 59, small products 2%).  At 256 x 256 these are all 160 KB.  Where a compute unit has one
 // or two workgroups, the time of a step is the loads' way through memory, and four stages
 // take as many steps to hide it.
-template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ, int STAGES>
-__global__ void __launch_bounds__(64 * WI * WJ, STAGES * (TI + TJ) * kDepth * 2 > 81920 && WI * WJ == 4 ? 1 : 2)
+//
+// PARTS parts of the contraction are multiplied by as many sets of waves, whose sums meet in
+// LDS, so that few rows fill the device without a second launch that adds them up.
+template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ, int STAGES, int PARTS = 1>
+__global__ void __launch_bounds__(64 * WI * WJ * PARTS, STAGES * (TI + TJ) * kDepth * 2 > 81920 && WI * WJ == 4 ? 1 : 2)
 gemm_kernel(const GemmArgs a) {
     typedef typename Mma<T>::V V;
     constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16;
     constexpr int PB = Tile<PA, TI>::kBytes, QB = Tile<QA, TJ>::kBytes;
     constexpr uint32_t PLACES = STAGES * PB + (STAGES + 1) * QB;    // P's, then Q's
     constexpr uint32_t OUT = 2 * 16 * WI * (TJ + 4) * 4;   // write_out's place
-    __shared__ __align__(PB) char lds[OUT > PLACES ? OUT : PLACES];
+    __shared__ __align__(PB) char lds[OUT > PARTS * PLACES ? OUT : PARTS * PLACES];
     BLK_LDS char* const room = (BLK_LDS char*)lds;
     RowTiles rows = {};
     if constexpr (BY_ROWS) rows = count_tiles(a, TI);
@@ -604,10 +613,19 @@ gemm_kernel(const GemmArgs a) {
     if (!find_spot<BY_ROWS, TI, TJ>(a, rows, blockIdx.x, s)) return;
     const T* const p = (const T*)a.p;
     const T* const q = (const T*)a.q + (BY_ROWS && s.g.group > 0 ? (uint64_t)s.g.group * a.q_group : 0);
-    const int wave = threadIdx.x >> 6, wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
+    int wave = threadIdx.x >> 6, part = 0, tiles = (s.c_end - s.c0 + kDepth - 1) / kDepth;
+    if constexpr (PARTS > 1) {
+        part = __builtin_amdgcn_readfirstlane(wave / (WI * WJ));
+        wave %= WI * WJ;
+        tiles = (tiles + PARTS - 1) / PARTS;       // of each; the last ones may be past the end
+        const int64_t lo = s.c0 + (int64_t)part * tiles * kDepth;
+        s.c0 = (int)min(lo, (int64_t)s.c_end);
+        s.c_end = (int)min(lo + (int64_t)tiles * kDepth, (int64_t)s.c_end);
+    }
+    const int wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
     Reader<PA, TI> rp;
     Reader<QA, TJ> rq;
-    const uint32_t p_at = (uint32_t)(uintptr_t)room, q_at = p_at + STAGES * PB;
+    const uint32_t p_at = (uint32_t)(uintptr_t)room + part * PLACES, q_at = p_at + STAGES * PB;
     rp.start(p_at, wi);
     rq.start(q_at, wj);
     f32x4 acc[FI][FJ];
@@ -619,8 +637,8 @@ gemm_kernel(const GemmArgs a) {
     // others.  Behind the barrier in the middle of a tile the next tile has arrived; the loads
     // of P that are STAGES tiles ahead follow into the place just read, those of Q, which has
     // one place more, in the next tile's first half.
-    typedef Direct<T, PA, TI, THREADS> DP;
-    typedef Direct<T, QA, TJ, THREADS> DQ;
+    typedef Direct<T, PA, TI, THREADS, (PARTS > 1)> DP;
+    typedef Direct<T, QA, TJ, THREADS, (PARTS > 1)> DQ;
     constexpr int PIECES = DP::kPieces + DQ::kPieces;
     DP lp;
     DQ lq;
@@ -655,7 +673,6 @@ gemm_kernel(const GemmArgs a) {
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    const int tiles = (s.c_end - s.c0 + kDepth - 1) / kDepth;
     if (tiles > 0) {
 #pragma unroll
         for (int t = 0; t < STAGES; ++t) {
@@ -689,13 +706,28 @@ gemm_kernel(const GemmArgs a) {
         multiply(Int<1>());
     }
     arrived<0>();                            // the zeros past the end as well
+    if constexpr (PARTS > 1) {
+        BLK_LDS f32x4* const sums = (BLK_LDS f32x4*)room + (wave * FI * FJ * 64 + (threadIdx.x & 63));
+        constexpr int EACH = WI * WJ * FI * FJ * 64;
+        if (part > 0)
+#pragma unroll
+            for (int f = 0; f < FI * FJ; ++f) sums[(part - 1) * EACH + f * 64] = acc[f / FJ][f % FJ];
+        __syncthreads();
+        if (part == 0)
+#pragma unroll
+            for (int f = 0; f < FI * FJ; ++f)
+#pragma unroll
+                for (int m = 0; m < PARTS - 1; ++m) acc[f / FJ][f % FJ] += sums[m * EACH + f * 64];
+        __syncthreads();
+    }
     write_out<T, BY_ROWS, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
 }
 
 // ------------------------------------------------------------ few rows: one pass --
 //
-// The forward product of a few rows is the read of the weights (4 x 8192 x 8192 bf16: 27 us,
-// 4.9 TB/s; 4 x 16384 x 8192 55).  A workgroup takes 16 FI rows x 16 FJ columns, its waves
+// The forward product of a few rows is the read of the weights (4 x 4096 x 4096 bf16: 9.9 us,
+// 4 x 8192 x 4096 15.7; 4 x 8192 x 8192 27, 4.9 TB/s, where the tiles above need 24).  A
+// workgroup takes 16 FI rows x 16 FJ columns, its waves
 // parts of the contraction, 128 deep each in turn;
 // operands go from memory to registers in the fragments' own layout (a lane's 16 bytes
 // are 8 values of one row, four lanes make 64 neighbouring bytes), and the waves' sums
@@ -984,6 +1016,11 @@ __global__ void __launch_bounds__(256) join_last_kernel(const GemmArgs a) {
 template <typename T, bool PA, bool QA, bool BY_ROWS>
 static void launch_form(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
     const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits * (BY_ROWS ? 1u : (unsigned)a.groups);
+    if constexpr (BY_ROWS && !PA && !QA)
+        if (p.tile == kInner64) {
+            gemm_kernel<T, PA, QA, BY_ROWS, 64, 32, 2, 1, 3, 4><<<grid, 512, 0, s>>>(a);
+            return;
+        }
     if (p.tile == kTile256) {
         gemm_kernel<T, PA, QA, BY_ROWS, 256, 256, 2, 4, 2><<<grid + (unsigned)a.slots, 512, 0, s>>>(a);
         if (a.slots) join_last_kernel<T, BY_ROWS, 256, 256><<<dim3((unsigned)a.slots / 2, 8), 256, 0, s>>>(a);

@@ -198,6 +198,12 @@ static uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
     return a->rows / height + a->groups + 2;
 }
 
+// An operand of 16-byte pieces: its rows start at them and, where the pieces lie along the
+// contraction, end at them too (past a row's end there may be anything).
+static bool good_rows(const rr_rows_t& r, uint64_t group, uint64_t width) {
+    return aligned_to(r.data, 16) && r.ld % 8 == 0 && group % 8 == 0 && width % 8 == 0;
+}
+
 // The kernel and the parts of the contraction for one product: the least of the times that
 // these figures give, fitted on an MI355X to 320 products of 32 to 6400 rows and 128 to 8192
 // columns and depths, each with every tile and 1 to 16 parts (microseconds; a step is 64
@@ -207,9 +213,14 @@ static uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
 //   128 x 128    6.6    0.73 (0.47), 1.16
 //    64 x  64    3.8    0.28, 0.51, 0.73, 0.83
 // A further round costs 0.6 of a start; parts cost 4.6 for the second launch and their bytes,
-// written and read.  A few rows go through the one-pass form instead, to 64 rows where the
-// contraction is too short for parts to pay (48 x 8192 x 1024: 9.4 us against 10.2; 48 x 1024
-// x 8192: 40 against 16).
+// written and read.  Up to 64 rows of a long contraction may be cut inside the workgroup
+// instead (kInner64: 64 x 32, four parts; start 7.2, 3.6 for a further round, a step of all
+// parts 0.3 to 0.56): 32 x 8192 x 8192 25.5 us against 29.7, 32 x 4096 x 4096 13.3 against
+// 14.9, but 32 x 16384 x 4096 29.4 against 24.7 and 32 x 1024 x 4096 11.9 against 10.4.  A few
+// rows go through the one-pass form, to 64 rows where the contraction is too short for parts
+// to pay (48 x 8192 x 1024: 9.4 us against 10.2; 48 x 1024 x 8192: 40 against 16), and up to 16
+// where that is the better time (16 x 4096 x 4096 11.8 us against 12.9, 16 x 8192 x 8192 34
+// against 25; the tiles only for whole 16-byte pieces, copies of the weights would cost more).
 constexpr unsigned kSlots = 256;      // 256 x 256 tiles that a device takes at once: one a compute unit
 
 static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) {
@@ -224,28 +235,47 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
         p.tile = kDot;
         return p;
     }
-    if (form == kForward && (mean <= 16 || (mean <= 64 && c <= 1024))) {
+    double best = 1e30;
+    const bool few = form == kForward && mean <= 64;
+    if (few && (mean <= 16 || c <= 1024)) {
         p.tile = mean <= 16 ? kStream16 : mean <= 32 ? kStream32 : kStream64;
         // 16 columns a workgroup instead of 32 where that gives a compute unit no more than two,
         // of more rows than 16 one: 4 x 8192 x 8192 27 us against 31, 4 x 4096 x 4096 9.9 (12.2),
         // 4 x 1024 x 4096 8.7 (9.6), 64 x 4096 x 1024 9.0 (10.0); but 4 x 16384 x 1024 9.8
         // (9.2), 64 x 8200 x 1000 14.4 (12.1), and with longer rows 4 x 8192 x 16384 54 (44),
         // 4 x 2048 x 16384 20.8 (18.7)
-        const uint64_t high = ceil_div(a->rows, tile_rows(p.tile));
+        const uint64_t high = a->rows ? ceil_div(a->rows, tile_rows(p.tile)) : 1;
         p.narrow = c <= 8192 && ceil_div(j, 16) * high <= (p.tile == kStream16 ? 2 : 1) * kSlots;
         const uint64_t blocks = ceil_div(j, p.cols()) * high;
         const uint64_t want = 256 / blocks, most = c / 1024;
         const uint64_t n = want < most ? want : most;
         *splits = n < 2 ? 1 : n > 16 ? 16 : (int)n;
-        return p;
+        if (mean > 16 || groups > 1 || a->offsets || c <= 1024 || c > 8192 || !good_rows(a->x, 0, a->k) ||
+            !good_rows({const_cast<void*>(a->w), a->w_ld}, 0, a->k))
+            return p;
+        const double uneven = blocks > kSlots ? (double)ceil_div(blocks, kSlots) * kSlots / blocks : 1;
+        best = 0.93 * (4 + (*splits > 1 ? 3.5 : 0) + 2.0 * j * c / 5.9e6 * (1 + mean / 64.0) * uneven);
     }
-    double best = 1e30;
+    if (few) {
+        const uint64_t high = groups == 1 ? ceil_div(i, 64) : i / 64 + ceil_div(groups, 2);
+        const uint64_t blocks = (high ? high : 1) * ceil_div(j, 32), more = (blocks - 1) / kSlots;
+        const double fill = (double)(blocks - more * kSlots) / kSlots;
+        const double steps = (double)ceil_div(ceil_div(c, kDepth), 4);
+        const double time = (7.2 + 3.6 * more + steps * (0.56 * more + 0.3 + 0.26 * fill * fill)) * (0.92 + 0.09 * mean / 64);
+        if (time < best) {
+            best = time;
+            p.tile = kInner64;
+            *splits = 1;
+        }
+    }
     for (int tile = kTile256; tile <= kTile64; ++tile) {
         const uint64_t t = tile_rows(tile), each = tile == kTile256 ? 1 : tile == kTile128 ? 2 : 4;
         const uint64_t high = form == kByW ? groups * ceil_div(i, t)
                               : groups == 1 ? ceil_div(i, t) : i / t + ceil_div(groups, 2);
         const uint64_t tiles = (high ? high : 1) * ceil_div(j, t), steps = ceil_div(c, kDepth);
-        for (uint64_t s = 1; s <= 32 && (s == 1 || (s <= steps / 2 && tiles * s <= 1024)); s *= 2) {
+        // of few rows, no more than two tiles on a compute unit: their loads are what takes time
+        // then (16 x 16384 x 8192 50 us with four, 43 with two)
+        for (uint64_t s = 1; s <= 32 && (s == 1 || (s <= steps / 2 && tiles * s <= (few ? 512 : 1024))); s *= 2) {
             const uint64_t blocks = tiles * s, rounds = ceil_div(blocks, 256 * each);
             const uint64_t load = rounds > 1 ? each : ceil_div(blocks, 256);
             const double fill = blocks < 256 ? blocks / 256.0 : 1.0;
@@ -273,12 +303,6 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
         }
     }
     return p;
-}
-
-// An operand of 16-byte pieces: its rows start at them and, where the pieces lie along the
-// contraction, end at them too (past a row's end there may be anything).
-static bool good_rows(const rr_rows_t& r, uint64_t group, uint64_t width) {
-    return aligned_to(r.data, 16) && r.ld % 8 == 0 && group % 8 == 0 && width % 8 == 0;
 }
 
 struct Operand {

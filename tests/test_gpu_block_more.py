@@ -311,3 +311,26 @@ def test_gelu_of_single_values(rr, dtype):
 def test_few_rows_at_the_edges_of_the_forms(rr, rows, n, k, groups):
     d = make(rows, n, k, groups if groups > 1 else None, "bf16", True, True)
     check_forward(rr, d, None, "silu", torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows,n,k,groups,dtype", [
+    (17, 96, 1032, 1, "bf16"), (64, 1111, 4096, 1, "fp16"), (33, 1, 1025, 1, "bf16"), (48, 4096, 8192, 1, "bf16"),
+    (50, 333, 1777, 1, "bf16"), (64, 32, 20000, 1, "bf16"), (96, 264, 2048, 4, "fp16"), (160, 72, 1100, 5, "bf16"),
+    (31, 40, 1280, 1, "bf16")])
+def test_few_rows_of_long_contractions(rr, rows, n, k, groups, dtype):
+    d = make(rows, n, k, groups if groups > 1 else None, dtype, True, True)
+    check_forward(rr, d, None, "gelu", DTYPES[dtype])
+    if groups > 1:                         # uneven, empty ones, rows of no group
+        off = torch.tensor([3, 3] + [rows // 2 + i for i in range(groups - 2)] + [rows - 5], dtype=torch.int32, device="cuda")
+        check_forward(rr, d, off, "silu", DTYPES[dtype])
+
+
+@pytest.mark.parametrize("rows,n,k", [(3, 8192, 2048), (16, 8200, 1032), (9, 16384, 1096), (5, 4096, 8192), (12, 11000, 4096)])
+def test_up_to_sixteen_rows_in_tiles(rr, rows, n, k):
+    d = make(rows, n, k, None, "bf16", True, True)
+    check_forward(rr, d, None, "none", torch.bfloat16)
+    ragged = torch.empty(rows, k + 1, dtype=torch.bfloat16, device="cuda")[:, 1:]
+    ragged.copy_(d["x"])
+    out = rr.block_linear(ragged, d["w"], d["bias"], residual=d["residual"])
+    ref = (d["x"].double() @ d["w"].double().t() + d["bias"].double() + d["residual"].double())
+    assert float((out.double() - ref).norm() / ref.norm()) < 2.0 ** -8
