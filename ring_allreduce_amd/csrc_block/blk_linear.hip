@@ -191,11 +191,12 @@ static GemmArgs groups_of(const rr_linear_t* a) {
     return k;
 }
 
-// Row tiles of all groups: each can add one partly filled, and so can the rows before
-// the first and after the last one.
+// Row tiles of all groups, at most: each that has rows can add one partly filled, and so can
+// the rows before the first and after the last one.
 static uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
     if (a->groups == 1 && !a->offsets) return ceil_div(a->rows, height);
-    return a->rows / height + a->groups + 2;
+    const uint64_t ranges = (uint64_t)a->groups + 2;
+    return a->rows / height + (a->rows < ranges ? a->rows : ranges);
 }
 
 // An operand of 16-byte pieces: its rows start at them and, where the pieces lie along the
@@ -237,8 +238,11 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
     }
     double best = 1e30;
     const bool few = form == kForward && mean <= 64;
+    // of uneven groups, those of more than 16 rows would read their weights twice (32 groups of
+    // 4096 x 2048: 400 rows 128 us with tiles of 16, 142 with 32; 512 rows 159 and 146)
+    const uint64_t some = groups > 1 && a->offsets ? mean * 5 / 4 : mean;
     if (few && (mean <= 16 || c <= 1024)) {
-        p.tile = mean <= 16 ? kStream16 : mean <= 32 ? kStream32 : kStream64;
+        p.tile = some <= 16 ? kStream16 : mean <= 32 ? kStream32 : kStream64;
         // 16 columns a workgroup instead of 32 where that gives a compute unit no more than two,
         // of more rows than 16 one: 4 x 8192 x 8192 27 us against 31, 4 x 4096 x 4096 9.9 (12.2),
         // 4 x 1024 x 4096 8.7 (9.6), 64 x 4096 x 1024 9.0 (10.0); but 4 x 16384 x 1024 9.8

@@ -334,3 +334,12 @@ def test_up_to_sixteen_rows_in_tiles(rr, rows, n, k):
     out = rr.block_linear(ragged, d["w"], d["bias"], residual=d["residual"])
     ref = (d["x"].double() @ d["w"].double().t() + d["bias"].double() + d["residual"].double())
     assert float((out.double() - ref).norm() / ref.norm()) < 2.0 ** -8
+
+
+@pytest.mark.parametrize("rows,n,k,groups", [(1, 72, 264, 64), (5, 520, 1032, 100), (200, 264, 1160, 16), (96, 40, 2048, 6)])
+def test_few_rows_over_many_groups(rr, rows, n, k, groups):
+    d = make(rows, n, k, groups, "bf16", True, True)
+    g = torch.Generator().manual_seed(rows)
+    edges = torch.randint(0, rows + 1, (groups + 1,), generator=g).sort().values.int().cuda()
+    check_forward(rr, d, edges, "silu", torch.bfloat16)
+    check_backward(rr, d, edges, "silu", torch.bfloat16)
