@@ -542,7 +542,10 @@ static int sort_items(uint64_t pairs) {
     const int n = items_for(pairs, kSortWaves * kFewShares, 4);
     return n == 4 && pairs > (uint64_t)64 * 4 * kSortWaves * 256 ? kItems : n;
 }
-static uint64_t sort_shares(uint64_t pairs) { return ceil_div(pairs, 64 * sort_items(pairs) * kSortWaves); }
+// One share at least: no pairs have counts and unused rows too.
+static uint64_t sort_shares(uint64_t pairs) {
+    return pairs ? ceil_div(pairs, 64 * sort_items(pairs) * kSortWaves) : 1;
+}
 // base, counts and start of every expert in the LDS of one workgroup
 static bool one_workgroup(uint64_t pairs, int experts) {
     return pairs <= (uint64_t)64 * kOneItems * kOneWaves && experts <= 512;
