@@ -220,12 +220,14 @@ __global__ void __launch_bounds__(Shape<G>::block) norm_kernel(const NormArgs a)
 }
 
 // The gradients.  With q = (mean(h^2) + eps)^-1/2 and p = dy * pre_weight,
-//   d  = dh + q p - h q^3 mean(p h)                 gradient at the stream
+//   d  = dh + q (p - h q (q mean(p h)))             gradient at the stream
 //   dx = residual_scale d
 // and with r the same of the branch u, n = u r post_weight, e = branch_scale d:
 //   dgate = e n act'(gate);   m = e act(gate) post_weight
-//   du = r m - u r^3 mean(m u)
+//   du = r (m - u r (r mean(m u)))
 //   dpre_weight = sum_t dy h q;  dpost_weight = sum_t e act(gate) u r.
+// d and du in this order: the cubes of q and r leave 32 bits for rows near 1e15, or near 1e-13
+// with eps 0, where everything else is still far from it.
 // A channel gate is the same for all tokens: with S = sum_t e u r, dpost_weight is act(gate) S
 // and the gate's gradient post_weight act'(gate) S.
 // Two rounds of sums over a row: (h^2, p h, u^2), then (m u).  The statistics are
@@ -293,7 +295,7 @@ norm_backward_kernel(const NormArgs a) {
         }
         if (a.pre || a.post) row_sums<G>(s, lds[turn][0]);
         const float q = rsqrtf(fmaf(s[0], inv, a.eps));
-        const float back = q * q * q * s[1] * inv;
+        const float back = q * (q * s[1] * inv);
         const float r = a.post ? rsqrtf(fmaf(s[2], inv, a.eps)) : 1.0f;
         float m[NV][N];
         float s2[1] = {0.0f};
@@ -314,7 +316,7 @@ norm_backward_kernel(const NormArgs a) {
                 float d = R::value(in.dh, v, i);
                 if (a.pre) {
                     const float hv = R::value(in.h, v, i), dyv = R::value(in.dy, v, i);
-                    d += fmaf(q * wn[i], dyv, -back * hv);
+                    d = fmaf(q, fmaf(-back, hv, wn[i] * dyv), d);
                     if constexpr (IN_LDS) held[v * N + i][threadIdx.x] = fmaf(dyv * q, hv, held[v * N + i][threadIdx.x]);
                     else sum_pre[v][i] = fmaf(dyv * q, hv, sum_pre[v][i]);
                 }
@@ -339,13 +341,13 @@ norm_backward_kernel(const NormArgs a) {
             float bu = 0.0f;
             if (a.post) {
                 row_sums<G>(s2, lds[turn][3]);
-                bu = r * r * r * s2[0] * inv;
+                bu = r * (r * s2[0] * inv);
             }
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 Vec<T> du;
 #pragma unroll
-                for (int i = 0; i < N; ++i) du.e[i] = (T)fmaf(r, m[v][i], -bu * R::value(in.u, v, i));
+                for (int i = 0; i < N; ++i) du.e[i] = (T)(r * fmaf(-bu, R::value(in.u, v, i), m[v][i]));
                 R::store(du, v, a.dbranch, a.dbranch_ld, t, len);
             }
         }

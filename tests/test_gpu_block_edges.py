@@ -4,6 +4,8 @@ import numpy as np
 import pytest
 import torch
 
+from tests.block_util import DTYPES, U, assert_within, store_error
+from tests.test_gpu_block_norm import STEPS
 from tests.test_gpu_expert import check_order, make_ids, order_of
 
 pytestmark = pytest.mark.gpu
@@ -25,3 +27,35 @@ def test_sort_of_no_tokens(rr, dtype, tokens, k, experts, capacity):
     ids = make_ids(tokens, k, experts, "any", 1)
     o = rr.expert_sort(torch.from_numpy(ids).to(dtype).cuda(), experts, capacity)
     check_order(o, order_of(ids, experts, capacity))
+
+
+def pullback64(grad, v, w, eps):
+    """Gradient of N(v) * w by v, the magnitude its error is counted in, and by w."""
+    r = (v.square().mean(1, keepdim=True) + eps).rsqrt()
+    u, p = v * r, grad * w
+    d = r * (p - u * (p * u).mean(1, keepdim=True))
+    return d, r * (p.abs() + u.abs() * (p * u).abs().mean(1, keepdim=True)), (grad * u).sum(0)
+
+
+@pytest.mark.parametrize("hidden", [96, 1030, 4099, 12296])
+@pytest.mark.parametrize("dtype,scale,eps", [
+    ("bf16", 1e14, 1e-6), ("bf16", 1e15, 1e-6), ("bf16", 1e16, 1e-6), ("fp32", 1e15, 1e-6),
+    ("fp32", 1e-13, 0.0), ("fp32", 1e-15, 0.0), ("bf16", 1e-13, 0.0)])
+def test_norm_gradients_of_rows_far_from_one(rr, dtype, scale, eps, hidden):
+    """The gradients scale with 1 / size, down to where the squares leave 32 bits: no power of it
+    beyond that may be formed on the way."""
+    g, dt, tokens = torch.Generator().manual_seed(hidden), DTYPES[dtype], 40
+    rnd = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    h, u = ((rnd(tokens, hidden) * scale).to(dt) for _ in range(2))
+    dy, wn, wp = rnd(tokens, hidden).to(dt), (1 + 0.3 * rnd(hidden)).to(dt), (1 + 0.3 * rnd(hidden)).to(dt)
+    got = rr.block_norm_backward(None, dy.cuda(), h.cuda(), u.cuda(), post_weight=wp.cuda(),
+                                 pre_weight=wn.cuda(), eps=eps)
+    dx, size, dpre = pullback64(dy.double(), h.double(), wn.double(), eps)
+    assert_within(got.dx.cpu(), dx, store_error(dx, dt) + STEPS * U * size, "dx")
+    assert_within(got.dpre_weight.cpu(), dpre, (STEPS + tokens) * U *
+                  (dy.double() * h.double() / h.double().square().mean(1, keepdim=True).sqrt()).abs().sum(0), "dpre")
+    du, size_u, dpost = pullback64(dx, u.double(), wp.double(), eps)
+    more = pullback64(size, u.double().abs(), wp.double().abs(), eps)[1]      # dx's own error, carried on
+    assert_within(got.dbranch.cpu(), du, store_error(du, dt) + STEPS * U * (size_u + more), "dbranch")
+    unit_u = (u.double() / u.double().square().mean(1, keepdim=True).sqrt()).abs()
+    assert_within(got.dpost_weight.cpu(), dpost, (STEPS + tokens) * U * (size * unit_u).sum(0), "dpost")
