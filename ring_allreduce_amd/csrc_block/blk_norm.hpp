@@ -347,7 +347,7 @@ norm_backward_kernel(const NormArgs a) {
             for (int v = 0; v < NV; ++v) {
                 Vec<T> du;
 #pragma unroll
-                for (int i = 0; i < N; ++i) du.e[i] = (T)(r * fmaf(-bu, R::value(in.u, v, i), m[v][i]));
+                for (int i = 0; i < N; ++i) du.e[i] = (T)(a.post ? r * fmaf(-bu, R::value(in.u, v, i), m[v][i]) : m[v][i]);
                 R::store(du, v, a.dbranch, a.dbranch_ld, t, len);
             }
         }

@@ -59,3 +59,19 @@ def test_norm_gradients_of_rows_far_from_one(rr, dtype, scale, eps, hidden):
     assert_within(got.dbranch.cpu(), du, store_error(du, dt) + STEPS * U * (size_u + more), "dbranch")
     unit_u = (u.double() / u.double().square().mean(1, keepdim=True).sqrt()).abs()
     assert_within(got.dpost_weight.cpu(), dpost, (STEPS + tokens) * U * (size * unit_u).sum(0), "dpost")
+
+
+@pytest.mark.parametrize("hidden", [72, 1030, 4099])
+@pytest.mark.parametrize("gate", [False, True])
+def test_norm_gradient_by_an_infinite_branch(rr, gate, hidden):
+    """Without a norm of the branch its gradient is the stream's times scale and gate, whatever
+    the branch holds."""
+    g, tokens = torch.Generator().manual_seed(hidden), 20
+    u, dh, z = (torch.randn(tokens, hidden, generator=g).bfloat16() for _ in range(3))
+    u[3, 5], u[7, 0], u[11, hidden - 1] = float("inf"), float("nan"), float("-inf")
+    args = dict(gate=z.cuda(), gate_act="sigmoid") if gate else {}
+    got = rr.block_norm_backward(dh.cuda(), None, None, u.cuda(), post_norm=False, pre_norm=False,
+                                 branch_scale=1.5, **args)
+    want = 1.5 * dh.double() * (torch.sigmoid(z.double()) if gate else 1.0)
+    # the exponential's argument is under 8: its rounding counts as many steps
+    assert_within(got.dbranch.cpu(), want, store_error(want, torch.bfloat16) + 16 * U * want.abs(), "dbranch")
