@@ -93,7 +93,14 @@ struct Args {
         }
         return (float)v;
     }
-    bool flag(int i) { return PyObject_IsTrue(a[i]) == 1; }
+    bool flag(int i) {
+        const int v = PyObject_IsTrue(a[i]);
+        if (v < 0) {
+            PyErr_Clear();
+            good = false;
+        }
+        return v == 1;
+    }
 };
 
 rr_dtype_t type_of(at::ScalarType t) {
@@ -335,21 +342,22 @@ PyObject* linear(Args& a) {
 PyObject* linear_backward(Args& a) {
     const Tensor *dout = a.needed(0), *x = a.needed(1), *w = a.needed(2), *z = a.tensor(3), *offsets = a.tensor(5);
     const long act = a.number(4);
+    const bool need_dx = a.flag(6), need_dw = a.flag(7), need_db = a.flag(8), wide_dw = a.flag(9);
     Call c;
     rr_linear_t l = {};
     rr_linear_grad_t g = {};
     if (!a.good || !c.begin(*x) || !linear_args(c, *x, *w, offsets, act, l)) return none();
-    const auto type = x->scalar_type(), wide = a.flag(9) ? at::kFloat : type;
+    const auto type = x->scalar_type(), wide = wide_dw ? at::kFloat : type;
     const int64_t rows = (int64_t)l.rows, n = (int64_t)l.n;
     if (!c.matrix(*dout, type, rows, n, g.dout)) return none();
     if (act != RR_ACT_NONE && (!z || !c.matrix(*z, type, rows, n, l.z))) return none();
     Tensor dx, dw, db;
-    if (a.flag(6)) dx = c.make_rows(rows, (int64_t)l.k, type, g.dx);
-    if (a.flag(7)) {
+    if (need_dx) dx = c.make_rows(rows, (int64_t)l.k, type, g.dx);
+    if (need_dw) {
         dw = c.make(w->sizes(), wide);
         g.dw = dw.data_ptr();
     }
-    if (a.flag(8)) {
+    if (need_db) {
         db = c.make(w->sizes().slice(0, (size_t)w->dim() - 1), at::kFloat);
         g.db = (float*)db.data_ptr();
     }

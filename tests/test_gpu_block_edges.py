@@ -75,3 +75,22 @@ def test_norm_gradient_by_an_infinite_branch(rr, gate, hidden):
     want = 1.5 * dh.double() * (torch.sigmoid(z.double()) if gate else 1.0)
     # the exponential's argument is under 8: its rounding counts as many steps
     assert_within(got.dbranch.cpu(), want, store_error(want, torch.bfloat16) + 16 * U * want.abs(), "dbranch")
+
+
+def test_options_without_a_truth_value(rr):
+    """They raise what their bool() raises, and the next call is as it was."""
+    x, w = torch.randn(6, 16, device="cuda").bfloat16(), torch.randn(8, 16, device="cuda").bfloat16()
+    i = torch.zeros(6, 1, dtype=torch.int32, device="cuda")
+    q, bad = torch.full((1,), -1, dtype=torch.int32, device="cuda"), torch.zeros(2)
+    want = rr.block_linear(x, w)
+    for call in (lambda: rr.block_norm(x, x, post_norm=bad), lambda: rr.block_norm(x, x, pre_norm=bad),
+                 lambda: rr.block_norm_backward(x, x, x, x, post_norm=bad),
+                 lambda: rr.block_linear(x, w, save_preact=bad),
+                 lambda: rr.block_linear_backward(want, x, w, need_dx=bad),
+                 lambda: rr.block_linear_backward(want, x, w, need_dw=bad),
+                 lambda: rr.block_linear_backward(want, x, w, need_db=bad),
+                 lambda: rr.expert_combine_backward(x, x[:1], i, q, need_rows=bad),
+                 lambda: rr.expert_combine_backward(x, x[:1], i, q, need_weights=bad)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call()
+    assert torch.equal(rr.block_linear(x, w), want)
