@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 from dataclasses import dataclass
 
 import torch
@@ -202,6 +203,16 @@ def _row(t, name, device, dtype, numel):
     return None if t is None else _vector(t, name, device, dtype, numel)
 
 
+def _ordered(t, name, device, dtype, *shape):
+    """A contiguous tensor of ``shape``, but for dimensions of 1, or flat; or None."""
+    if t is None:
+        return None
+    at = _vector(t, name, device, dtype, math.prod(shape))
+    if t.dim() != 1 and [n for n in t.shape if n != 1] != [n for n in shape if n != 1]:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    return at
+
+
 def _new(rows, width, like):
     """A new matrix of ``like``'s type on its device, and its _Rows."""
     t = torch.empty((rows, width), dtype=like.dtype, device=like.device)
@@ -300,7 +311,7 @@ def expert_combine(rows, slots, weights=None, *, out=None, stream=None):
     hidden = rows.shape[1]
     with _on(rows.device, stream) as s:
         sp = _ints(slots, "slots", rows.device)
-        wp = _row(weights, "weights", rows.device, torch.float32, tokens * k)
+        wp = _ordered(weights, "weights", rows.device, torch.float32, tokens, k)
         if out is None:
             out, o = _new(tokens, hidden, rows)
         else:
@@ -331,7 +342,7 @@ def expert_combine_backward(dout, rows, slots, sources, weights=None, *, need_ro
     with _on(dev, stream) as s:
         r = _matrix(rows, "rows", dev, dout.dtype, n, hidden) if need_weights else _Rows()
         sp, so = _ints(slots, "slots", dev), _ints(sources, "sources", dev)
-        wp = _row(weights, "weights", dev, torch.float32, tokens * k)
+        wp = _ordered(weights, "weights", dev, torch.float32, tokens, k)
         drows = dweights = None
         o = _Rows()
         if need_rows:
@@ -533,7 +544,7 @@ def block_linear(x, w, bias=None, *, act="none", residual=None, offsets=None, sa
             return done
     a = _linear_args(x, w, offsets, act)
     dev, shape = x.device, (x.shape[0], a.n)
-    a.bias = _row(bias, "bias", dev, x.dtype, a.groups * a.n)
+    a.bias = _ordered(bias, "bias", dev, x.dtype, a.groups, a.n)
     if residual is not None:
         a.residual = _matrix(residual, "residual", dev, x.dtype, *shape)
     with _on(dev, stream) as s:

@@ -43,6 +43,19 @@ struct Call {
     bool vector(const Tensor& t, at::ScalarType type, int64_t numel) const {
         return here(t) && t.scalar_type() == type && t.numel() == numel && t.is_contiguous();
     }
+    // A vector whose elements are in the order of a tensor of `sizes`: that tensor, but for
+    // dimensions of 1, or a flat one.
+    bool ordered(const Tensor& t, at::ScalarType type, at::IntArrayRef sizes) const {
+        if (!vector(t, type, c10::multiply_integers(sizes))) return false;
+        if (t.dim() == 1) return true;
+        size_t at = 0;
+        for (const int64_t n : t.sizes()) {
+            if (n == 1) continue;
+            while (at < sizes.size() && sizes[at] == 1) ++at;
+            if (at == sizes.size() || sizes[at++] != n) return false;
+        }
+        return true;
+    }
     Tensor make(at::IntArrayRef sizes, at::ScalarType type) const {
         return at::empty(sizes, at::TensorOptions().dtype(type).device(c10::DeviceType::CUDA, (c10::DeviceIndex)device));
     }
@@ -169,7 +182,7 @@ PyObject* combine(Args& a) {
     const int64_t n = rows->size(0), hidden = rows->size(1), tokens = slots->size(0), k = slots->size(1);
     rr_rows_t in, to;
     if (!c.matrix(*rows, rows->scalar_type(), n, hidden, in) || tokens < 1 || k < 1 ||
-        !c.vector(*slots, at::kInt, tokens * k) || (weights && !c.vector(*weights, at::kFloat, tokens * k)))
+        !c.vector(*slots, at::kInt, tokens * k) || (weights && !c.ordered(*weights, at::kFloat, {tokens, k})))
         return none();
     Tensor out = c.make_rows(tokens, hidden, rows->scalar_type(), to);
     if (expert_combine(in, (size_t)n, (size_t)hidden, type_of(rows->scalar_type()), ints(*slots),
@@ -191,7 +204,7 @@ PyObject* combine_backward(Args& a) {
     rr_rows_t d, r = {nullptr, 0}, to = {nullptr, 0};
     if (!c.matrix(*dout, type, tokens, hidden, d) || slots->size(0) != tokens || k < 1 || n < 1 ||
         !c.vector(*slots, at::kInt, tokens * k) || !c.vector(*sources, at::kInt, n) ||
-        (weights && !c.vector(*weights, at::kFloat, tokens * k)))
+        (weights && !c.ordered(*weights, at::kFloat, {tokens, k})))
         return none();
     if (need_weights && (!rows || !c.matrix(*rows, type, n, hidden, r))) return none();
     Tensor drows, dweights;
@@ -325,7 +338,7 @@ PyObject* linear(Args& a) {
     if (!a.good || !c.begin(*x) || !linear_args(c, *x, *w, offsets, act, l)) return none();
     const auto type = x->scalar_type();
     const int64_t rows = (int64_t)l.rows, n = (int64_t)l.n;
-    if (bias && !c.vector(*bias, type, l.groups * n)) return none();
+    if (bias && !c.ordered(*bias, type, {l.groups, n})) return none();
     l.bias = bias ? bias->data_ptr() : nullptr;
     if (residual && !c.matrix(*residual, type, rows, n, l.residual)) return none();
     Tensor out = c.make_rows(rows, n, type, l.out), z;

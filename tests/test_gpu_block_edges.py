@@ -94,3 +94,32 @@ def test_options_without_a_truth_value(rr):
         with pytest.raises(RuntimeError, match="ambiguous"):
             call()
     assert torch.equal(rr.block_linear(x, w), want)
+
+
+def test_weights_and_bias_in_another_order_are_refused(rr):
+    """As many elements are not enough: they are read in the order of [tokens, k] and [groups, n]."""
+    x, i = torch.randn(6, 16, device="cuda"), torch.arange(12, dtype=torch.int32, device="cuda").reshape(6, 2)
+    q, rows = torch.arange(12, dtype=torch.int32, device="cuda"), torch.randn(12, 16, device="cuda")
+    w = torch.rand(6, 2, device="cuda")
+    xs, ws = torch.randn(9, 16, device="cuda").bfloat16(), torch.randn(3, 8, 16, device="cuda").bfloat16()
+    b = torch.randn(3, 8, device="cuda").bfloat16()
+    out = torch.empty(9, 8, dtype=torch.bfloat16, device="cuda")
+    bad_w, bad_b = w.t().contiguous(), b.t().contiguous()
+    for call in (lambda: rr.expert_combine(rows, i, bad_w), lambda: rr.expert_combine(rows, i, bad_w, out=torch.empty_like(x)),
+                 lambda: rr.expert_combine(rows, i, w.reshape(3, 4)),
+                 lambda: rr.expert_combine_backward(x, rows, i, q, bad_w),
+                 lambda: rr.expert_combine_backward(x, rows, i, q, bad_w, out=torch.empty_like(rows)),
+                 lambda: rr.block_linear(xs, ws, bad_b), lambda: rr.block_linear(xs, ws, bad_b, out=out),
+                 lambda: rr.block_linear(xs, ws, b.reshape(2, 12))):
+        with pytest.raises(ValueError, match="must be"):
+            call()
+    want, grads = rr.expert_combine(rows, i, w), rr.expert_combine_backward(x, rows, i, q, w)
+    made = rr.block_linear(xs, ws, b)
+    for same in (lambda t: t.reshape(-1), lambda t: t[..., None], lambda t: t[None]):     # the same order
+        assert torch.equal(rr.expert_combine(rows, i, same(w)), want)
+        assert torch.equal(rr.expert_combine(rows, i, same(w), out=torch.empty_like(x)), want)
+        assert all(torch.equal(*ab) for ab in zip(rr.expert_combine_backward(x, rows, i, q, same(w)), grads))
+        assert torch.equal(rr.block_linear(xs, ws, same(b)), made)
+        assert torch.equal(rr.block_linear(xs, ws, same(b), out=out), made)
+    one = rr.block_linear(xs, ws[0], b[0])
+    assert torch.equal(rr.block_linear(xs, ws[0], b[:1]), one) and torch.equal(rr.block_linear(xs, ws[:1], b[0]), one)
