@@ -5,8 +5,9 @@ around a block, and a block's matrix products, with their gradients, as declared
 in ``include/rr.h``.  Like the rest of the binding this only marshals: it checks
 shapes and types, makes output and scratch tensors, and calls the library; there
 is no fallback.  Calls in their usual form (on the current device and stream, new
-outputs) are marshalled by the module ``_block``, in C++; what it does not take it
-leaves to the Python here, which also says what is wrong with a call.
+outputs) are marshalled by the module ``_block``, in C++, which is bound to the torch it
+was built with; what it does not take it leaves to the Python here, which also says what
+is wrong with a call.
 
 Every call runs on ``stream`` (default: torch's current stream of the tensors'
 device); the outputs and scratch it allocates belong to that stream.  Matrices may
@@ -17,6 +18,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import warnings
 from dataclasses import dataclass
 
 import torch
@@ -62,12 +64,24 @@ class _LinearGrad(ctypes.Structure):
                 ("dw_dt", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class _Absent:
+    """In the place of the module ``_block``: takes no call, so that all are marshalled here."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _bind(sig):
     """Declares the library's functions with the binding's ``sig``; called once, when
     librr.so is loaded."""
     p = ctypes.POINTER
     g = globals()
-    from . import _block
+    try:
+        from . import _block
+    except ImportError as e:
+        warnings.warn(f"{__package__}._block cannot be loaded ({e}); the calls of a block's "
+                      "operators are marshalled in Python", RuntimeWarning, stacklevel=3)
+        _block = _Absent()
     g["_block"] = _block
     g["_expert_sort"] = sig("expert_sort", _i, _vp, _i, _sz, _sz, _i, _i, _sz, _vp, _vp, _vp, _vp,
                             _vp, _sz, _vp)

@@ -1,5 +1,8 @@
 """Unusual calls of a block's operators, where they can be checked without a GPU."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch  # noqa: F401
@@ -29,3 +32,33 @@ def test_marshalling_leaves_no_error_behind(call):
     from ring_allreduce_amd import _block
     x, i = torch.zeros(4, 8).bfloat16(), torch.zeros(4, 2, dtype=torch.int32)
     assert call(_block, x, i, torch.zeros(2)) is None
+
+
+def test_package_without_the_marshalling_module():
+    """The module is a faster way into the library, not the library: without it (not built, or
+    built against another torch) the package is there, says so, and marshals in Python."""
+    program = """
+import sys, warnings
+sys.modules["ring_allreduce_amd._block"] = None          # an import of it fails
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    import ring_allreduce_amd as rr
+assert any("_block" in str(w.message) for w in seen), seen
+import torch
+x, i = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+for call in (lambda: rr.expert_sort(i, 4), lambda: rr.expert_dispatch(x, i, i.reshape(-1)),
+             lambda: rr.expert_combine(x, i), lambda: rr.block_norm(x, x),
+             lambda: rr.expert_combine_backward(x, x, i, i.reshape(-1)),
+             lambda: rr.block_norm_backward(x, x, x, x), lambda: rr.block_linear(x.bfloat16(), x.bfloat16()),
+             lambda: rr.block_linear_backward(x.bfloat16(), x.bfloat16(), x.bfloat16())):
+    try:
+        call()
+    except ValueError as e:
+        assert "GPU" in str(e), e
+    else:
+        raise AssertionError("host tensors were taken")
+assert rr._abi_version() >= 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", program], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr

@@ -123,3 +123,29 @@ def test_weights_and_bias_in_another_order_are_refused(rr):
         assert torch.equal(rr.block_linear(xs, ws, same(b), out=out), made)
     one = rr.block_linear(xs, ws[0], b[0])
     assert torch.equal(rr.block_linear(xs, ws[0], b[:1]), one) and torch.equal(rr.block_linear(xs, ws[:1], b[0]), one)
+
+
+def test_marshalled_in_python(rr, monkeypatch):
+    """The same bits from every call without the C++ marshalling."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, u, dh, dy, gate, w = rnd(70, 96), rnd(70, 96), rnd(70, 96), rnd(70, 96), rnd(70, 96), rnd(96)
+    ws, b, dout, z = rnd(3, 40, 96), rnd(3, 40), rnd(70, 40), rnd(70, 40)
+    ids = torch.from_numpy(make_ids(70, 2, 3, "masked", 3)).cuda()
+    weights, rows = torch.rand(70, 2, generator=g, device="cuda"), rnd(60, 96)
+    off = torch.tensor([0, 30, 31, 68], dtype=torch.int32, device="cuda")
+
+    def step():
+        o = rr.expert_sort(ids, 3, 20)
+        n = rr.block_norm_backward(dh, dy, x, u, post_weight=w, pre_weight=w, gate=gate, gate_act="silu")
+        m = rr.block_linear_backward(dout, x, ws, z, act="gelu", offsets=off)
+        return [o.slots, o.sources, o.counts, o.offsets, rr.expert_dispatch(x, o.slots, o.sources),
+                rr.expert_combine(rows, o.slots, weights),
+                *rr.expert_combine_backward(x, rows, o.slots, o.sources, weights),
+                *rr.block_norm(x, u, post_weight=w, pre_weight=w, gate=gate, gate_act="silu"),
+                n.dx, n.dbranch, n.dgate, n.dpost_weight, n.dpre_weight,
+                *rr.block_linear(x, ws, b, act="gelu", offsets=off, save_preact=True), m.dx, m.dw, m.db]
+
+    want = step()
+    monkeypatch.setattr(rr.block, "_block", rr.block._Absent())
+    assert all(torch.equal(p, q) for p, q in zip(want, step(), strict=True))
