@@ -304,12 +304,17 @@ template <typename T, bool ACROSS, int ROWS, int THREADS, bool PART> struct Dire
         base += step;
     }
     __device__ __forceinline__ void piece(int k) const { issue(rsrc, at[k], to + k * THREADS * 16); }
+    // m0 is one of the registers that the compiler allocates for itself only (which it warns of),
+    // but it does merge its own writes of m0 across instructions that are not known to write it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
     __device__ __forceinline__ static void issue(u32x4 rsrc, uint32_t offset, uint32_t to) {
         asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %0, 0 offen lds"
                      :
                      : "s"(rsrc), "v"(offset), "s"(to)
-                     : "memory");
+                     : "m0", "memory");
     }
+#pragma clang diagnostic pop
 };
 
 // This wave's loads into LDS but the last LATER are there and its reads of LDS are done,

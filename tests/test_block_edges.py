@@ -1,6 +1,7 @@
 """Unusual calls of a block's operators, where they can be checked without a GPU."""
 import ctypes
 import os
+import re
 import subprocess
 import sys
 
@@ -62,3 +63,22 @@ assert rr._abi_version() >= 0
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", program], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_inline_assembly_names_the_registers_it_writes():
+    """A register written by an instruction of an asm block and not an operand of it has to be
+    among what it clobbers: the compiler may keep a value there."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    blocks = 0
+    for folder in ("csrc", "csrc_block"):
+        at = os.path.join(root, "ring_allreduce_amd", folder)
+        for name in sorted(os.listdir(at)):
+            with open(os.path.join(at, name)) as fh:
+                text = fh.read()
+            for block in re.findall(r"\basm\s*(?:volatile)?\s*\(.*?\)\s*;", text, flags=re.S):
+                blocks += 1
+                strings = re.findall(r'"((?:[^"\\]|\\.)*)"', block)
+                code = strings[0].replace("\\n", "\n").replace("\\t", " ")
+                for written in re.findall(r"^\s*\w+\s+(m0|vcc|exec|s\d+|v\d+)\b", code, flags=re.M):
+                    assert written in strings[1:], f"{name}: {written} in {block}"
+    assert blocks >= 3
