@@ -575,7 +575,7 @@ typedef enum {
    slots[p] is the pair's slot or -1; sources[row] the pair in that row or -1.
    ids are int32 or int64 (id_bytes 4 or 8); slots: tokens * k, sources: rows,
    counts: experts, offsets: experts + 1 int32 words.  Limits: experts <=
-   RR_MAX_EXPERTS, tokens * k and rows < 2^31. */
+   RR_MAX_EXPERTS, tokens * k < 2^31 - 2048, rows < 2^31. */
 rr_status_t expert_sort(const void *ids, int id_bytes, size_t id_ld, size_t tokens, int k,
                         int experts, size_t capacity, int32_t *slots, int32_t *sources,
                         int32_t *counts, int32_t *offsets, void *workspace,
@@ -584,7 +584,11 @@ rr_status_t expert_sort_workspace(size_t tokens, int k, int experts, size_t *byt
 
 /* rows[slots[t * k + j]] = x[t] bit for bit; rows whose source is -1 (or not a
    pair) become zero.  `slots` and `sources` as expert_sort gives them for `rows`
-   rows: a row is written by its pair or, without one, with zeros. */
+   rows: a row is written by its pair or, without one, with zeros.  Limits of this
+   and the next two: hidden < 2^31 - 4096, rows < 2^31, tokens * k < 2^31 - 256, and a
+   launch's 2^24 workgroups, which take 256 / G tokens each (G the power of two from 8
+   to 256 that covers a row's 16-byte pieces, of the gradients 64 or 256) or, where rows
+   without a source are cleared, 32 rows. */
 rr_status_t expert_dispatch(rr_rows_t x, size_t tokens, size_t hidden, int k, rr_dtype_t dt,
                             const int32_t *slots, const int32_t *sources, size_t rows,
                             rr_rows_t out, rr_stream_t stream);
@@ -660,8 +664,10 @@ rr_status_t block_norm_backward_workspace(const rr_norm_t *a, const rr_norm_grad
    words, not descending, as expert_sort gives them); rows before offsets[0] or
    from offsets[groups] on belong to no group and become zero in out and z.
    offsets NULL: groups of rows / groups rows each.  Types RR_BF16 and RR_FP16; act
-   and residual work on the 32-bit z, before it is rounded.  Limits: rows, n, k <
-   2^31, ld and w_ld <= 2^22, groups <= RR_MAX_EXPERTS. */
+   and residual work on the 32-bit z, before it is rounded.  Limits: rows < 2^31 - 1024,
+   ld and w_ld (and with them n and k) <= 2^22, groups <= RR_MAX_EXPERTS, and a launch's
+   2^23 tiles of 64 x 64 or more results, with their parts (16 x 16 or more up to 64 rows
+   a group). */
 typedef struct {
     size_t rows, n, k;
     int32_t groups;

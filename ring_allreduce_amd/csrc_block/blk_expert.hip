@@ -838,9 +838,11 @@ rr_status_t expert_combine_backward(rr_rows_t dout, rr_rows_t in, size_t rows, s
     a.hidden = (int32_t)hidden;
     if (!a.out && !a.dweights) return RR_OK;
     const bool wide = group_for(hidden, dt) > 64;
-    if (!grid_fits(tokens + ceil_div(rows, kClearRows))) return RR_ERR_UNSUPPORTED;
-    a.token_blocks = (int32_t)(wide ? tokens : ceil_div(tokens, kMoveBlock / 64));
-    const unsigned grid = (unsigned)(a.token_blocks + (a.out ? ceil_div(rows, kClearRows) : 0));
+    const uint64_t token_blocks = wide ? tokens : ceil_div(tokens, kMoveBlock / 64);
+    const uint64_t blocks = token_blocks + (a.out ? ceil_div(rows, kClearRows) : 0);
+    if (!grid_fits(blocks)) return RR_ERR_UNSUPPORTED;
+    a.token_blocks = (int32_t)token_blocks;
+    const unsigned grid = (unsigned)blocks;
     if (grid == 0) return RR_OK;
     hipStream_t s = (hipStream_t)stream;
 #define CALL(T)                                  \

@@ -149,3 +149,22 @@ def test_marshalled_in_python(rr, monkeypatch):
     want = step()
     monkeypatch.setattr(rr.block, "_block", rr.block._Absent())
     assert all(torch.equal(p, q) for p, q in zip(want, step(), strict=True))
+
+
+def test_combine_backward_of_many_tokens(rr):
+    """More tokens than a launch has workgroups: four short rows share one."""
+    tokens, hidden = (1 << 24) + 9, 8
+    at = torch.tensor([0, 1, 77, 1 << 20, (1 << 24) - 1, 1 << 24, tokens - 1], device="cuda")
+    slots = torch.full((tokens, 1), -1, dtype=torch.int32, device="cuda")
+    slots[at, 0] = torch.arange(len(at), dtype=torch.int32, device="cuda")
+    sources = torch.cat([at.int(), torch.full((3,), -1, dtype=torch.int32, device="cuda")])
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = torch.randint(-4, 5, (len(sources), hidden), generator=g, device="cuda").bfloat16()
+    dout = torch.zeros(tokens, hidden, dtype=torch.bfloat16, device="cuda")
+    dout[at] = torch.randint(-4, 5, (len(at), hidden), generator=g, device="cuda").bfloat16()
+    drows, dweights = rr.expert_combine_backward(dout, rows, slots, sources)
+    assert torch.equal(drows[:len(at)], dout[at]) and not bool(drows[len(at):].any())
+    want = torch.zeros(tokens, 1, device="cuda")            # sums of few small integers: exact
+    want[at, 0] = (dout[at].float() * rows[:len(at)].float()).sum(1)
+    assert torch.equal(dweights, want)
+    assert torch.equal(rr.expert_combine_backward(dout, rows, slots, sources, need_rows=False)[1], want)
