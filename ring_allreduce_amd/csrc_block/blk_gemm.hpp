@@ -100,7 +100,8 @@ __device__ __forceinline__ int lanes_upto(int n) {
     return n;
 }
 
-// Called by whole waves.
+// Called by whole waves.  Offsets that descend make ranges that overlap, and of them more tiles
+// than the host counted, up to 2^34: those beyond its count are left out.
 __device__ __forceinline__ RowTiles count_tiles(const GemmArgs& a, int height) {
     RowTiles t = {};
     if (a.groups == 1 && !a.offsets) {
@@ -111,7 +112,7 @@ __device__ __forceinline__ RowTiles count_tiles(const GemmArgs& a, int height) {
         const Range r = range_of(a, r0 + (int)(threadIdx.x & 63));
         const int n = (r.hi - r.lo + height - 1) / height, upto = lanes_upto(n);
         if (r0 == 0) t.first = r, t.n = n, t.upto = upto;
-        t.total += __shfl(upto, 63);
+        t.total = min(t.total + __shfl(upto, 63), a.tiles_i);
     }
     t.total = __builtin_amdgcn_readfirstlane(t.total);
     return t;

@@ -168,3 +168,21 @@ def test_combine_backward_of_many_tokens(rr):
     want[at, 0] = (dout[at].float() * rows[:len(at)].float()).sum(1)
     assert torch.equal(dweights, want)
     assert torch.equal(rr.expert_combine_backward(dout, rows, slots, sources, need_rows=False)[1], want)
+
+
+def test_overlapping_groups_of_many_rows(rr):
+    """Offsets that descend, over so many rows that the tiles of all ranges are more than 2^31.
+    The first group has every row and all groups have the same weights, so that the result is
+    known; nothing around it is written."""
+    rows, groups, guard = 1 << 28, 1024, 512
+    value = (torch.arange(rows, dtype=torch.int32, device="cuda") % 7).bfloat16()
+    x = value[:, None].expand(rows, 8).contiguous()
+    w = torch.ones(groups, 8, 8, dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(groups + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = rows
+    store = torch.full((rows + 2 * guard, 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out = rr.block_linear(x, w, offsets=off, out=store[guard:-guard])
+    torch.cuda.synchronize()
+    del x
+    assert bool(store[:guard].isnan().all()) and bool(store[-guard:].isnan().all())
+    assert bool((out == (8 * value)[:, None]).all())           # 8 products of up to 6: exact
