@@ -186,3 +186,71 @@ def test_overlapping_groups_of_many_rows(rr):
     del x
     assert bool(store[:guard].isnan().all()) and bool(store[-guard:].isnan().all())
     assert bool((out == (8 * value)[:, None]).all())           # 8 products of up to 6: exact
+
+
+class Guarded:
+    """Tensors in one allocation, with 4 KiB of a pattern before, between and behind them."""
+    GAP, PATTERN = 4096, 0xA5
+
+    def __init__(self, size):
+        self.store = torch.full((size,), self.PATTERN, dtype=torch.uint8, device="cuda")
+        self.at, self.spans = self.GAP, []
+
+    def make(self, *shape, dtype):
+        n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+        lo, self.at = self.at, -(-(self.at + n) // 256) * 256 + self.GAP
+        assert self.at <= self.store.numel()
+        self.spans.append((lo, lo + n))
+        return self.store[lo:lo + n].view(dtype).view(shape)
+
+    def whole(self):
+        """Whether nothing around the tensors was written."""
+        left = self.store == self.PATTERN
+        for lo, hi in self.spans:
+            left[lo:hi] = True
+        return bool(left.all())
+
+
+def bad_offsets(rows, groups):
+    g = torch.Generator().manual_seed(rows)
+    wild = torch.randint(-rows, 2 * rows, (groups + 1,), generator=g)
+    wild[groups // 2], wild[-1] = -(1 << 31), (1 << 31) - 1
+    full = torch.zeros(groups + 1, dtype=torch.int64)
+    full[1::2] = rows
+    return [torch.arange(groups, -1, -1) * rows // groups, full, wild]
+
+
+# rows, groups, n, k: one pass over rows of 16 (whole, and cut along k), 32 and 64; four parts in a
+# workgroup; parts joined by a second launch; a last round of tiles cut along k; copied operands
+@pytest.mark.parametrize("rows,groups,n,k", [
+    (48, 4, 264, 520), (40, 4, 40, 4096), (100, 4, 264, 264), (200, 4, 264, 264), (160, 4, 264, 4096),
+    (300, 3, 128, 8192), (4400, 3, 4096, 2048), (300, 5, 131, 77), (900, 70, 200, 136)])
+def test_bad_offsets_write_nothing_else(rr, rows, groups, n, k):
+    """Whatever the offsets hold, the calls end, and write nothing but their outputs and scratch."""
+    blk, dt = rr.block, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(k)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dt)  # noqa: E731
+    x, w, bias, res, dout = rnd(rows, k), rnd(groups, n, k), rnd(groups, n), rnd(rows, n), rnd(rows, n)
+    stream, size = torch.cuda.current_stream().cuda_stream, blk._sz()
+    for offsets in bad_offsets(rows, groups):
+        off = offsets.to(torch.int32).cuda()
+        a = blk._linear_args(x, w, off, "silu")
+        a.bias, a.residual = bias.data_ptr(), blk._Rows(res.data_ptr(), n)
+        assert blk._block_linear_workspace(a, size) == 0
+        room = Guarded(size.value + 8 * rows * n + (1 << 16))
+        out, z, work = room.make(rows, n, dtype=dt), room.make(rows, n, dtype=dt), room.make(size.value, dtype=torch.uint8)
+        a.out, a.z = blk._Rows(out.data_ptr(), n), blk._Rows(z.data_ptr(), n)
+        assert blk._block_linear(a, work.data_ptr(), size.value, stream) == 0
+        assert room.whole(), offsets
+        zs, grad = rnd(rows, n), blk._LinearGrad()
+        a.z = blk._Rows(zs.data_ptr(), n)
+        grad.dout, grad.dw_dt = blk._Rows(dout.data_ptr(), n), blk.FLOAT_DTYPES[torch.float32]
+        grad.dx, grad.dw, grad.db = blk._Rows(1 << 20, k), 1 << 20, 1 << 20      # wanted; where to, below
+        assert blk._block_linear_backward_workspace(a, grad, size) == 0
+        room = Guarded(size.value + 4 * rows * k + 4 * groups * n * (k + 1) + (1 << 17))
+        dx, dw = room.make(rows, k, dtype=dt), room.make(groups, n, k, dtype=torch.float32)
+        db, work = room.make(groups, n, dtype=torch.float32), room.make(size.value, dtype=torch.uint8)
+        grad.dx, grad.dw, grad.db = blk._Rows(dx.data_ptr(), k), dw.data_ptr(), db.data_ptr()
+        assert blk._block_linear_backward(a, grad, work.data_ptr(), size.value, stream) == 0
+        assert room.whole(), offsets
+        torch.cuda.synchronize()
