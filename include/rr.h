@@ -558,6 +558,9 @@ typedef enum {
     RR_ACT_SILU = 3,    /* z / (1 + exp(-z)) */
     RR_ACT_SIGMOID = 4  /* gates only */
 } rr_act_t;
+/* NaN stays NaN.  At infinities GELU and its slope take their limits (infinity and 1, 0
+   and 0); SiLU's infinity and, at minus infinity, NaN are what the formula gives in
+   floating point, and so is NaN for its slope at both.  ReLU's slope is 0 at 0 and NaN. */
 
 /* --- tokens sorted by expert, and back --- */
 

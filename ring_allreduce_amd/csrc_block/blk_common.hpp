@@ -102,7 +102,8 @@ __device__ __forceinline__ float normal_tail(float a, float* tail) {
     *tail = e * q;
     return e;
 }
-// |z|, at most 20, from where on the tail is 0 in 32 bits; NaN stays.
+// |z|, at most 20, from where on the tail is 0 in 32 bits; NaN stays.  Infinities end here too:
+// they get the limits, where z Phi(z) and z phi(z) themselves would be infinity times 0.
 __device__ __forceinline__ float magnitude(float z) {
     const float a = fabsf(z);
     return a > 20.0f ? 20.0f : a;

@@ -254,3 +254,20 @@ def test_bad_offsets_write_nothing_else(rr, rows, groups, n, k):
         assert blk._block_linear_backward(a, grad, work.data_ptr(), size.value, stream) == 0
         assert room.whole(), offsets
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("act,value,slope", [
+    ("none", [np.inf, -np.inf, np.nan], [1, 1, 1]), ("relu", [np.inf, 0, np.nan], [1, 0, 0]),
+    ("gelu", [np.inf, 0, np.nan], [1, 0, np.nan]), ("silu", [np.inf, np.nan, np.nan], [np.nan] * 3)])
+def test_activations_at_infinities(rr, dtype, act, value, slope):
+    """x w^T with k = 1 and w = 1 is x itself, so this is the activation and its slope alone."""
+    x = torch.tensor([[np.inf], [-np.inf], [np.nan]]).to(DTYPES[dtype]).cuda()
+    one = torch.ones(1, 1, dtype=x.dtype, device="cuda")
+    for rows in (1, 3, 40, 300):                   # a wave's dots, one pass, tiles
+        z = x.repeat(rows, 1)[:rows]
+        out = rr.block_linear(z, one, act=act)
+        d = rr.block_linear_backward(torch.ones_like(z), z, one, z, act=act, need_dw=False)
+        want = [torch.tensor(v, dtype=torch.float64).repeat(rows)[:rows, None] for v in (value, slope)]
+        torch.testing.assert_close(out.cpu().double(), want[0], rtol=0, atol=0, equal_nan=True)
+        torch.testing.assert_close(d.dx.cpu().double(), want[1], rtol=0, atol=0, equal_nan=True)
