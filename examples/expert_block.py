@@ -116,7 +116,7 @@ def errors(each, capacity):
     outs, leaf, shared = plain(each, capacity)
 
     def off(a, b):
-        return float((a.double() - b).norm() / b.norm())
+        return float((a.double() - b.detach()).norm() / b.detach().norm())
 
     far = {"out": max(off(r["out"], o) for r, o in zip(each, outs))}
     for name in ("x", "branch", "w1", "b1", "w2", "b2", "weights"):

@@ -10,8 +10,13 @@ was built with; what it does not take it leaves to the Python here, which also s
 is wrong with a call.
 
 Every call runs on ``stream`` (default: torch's current stream of the tensors'
-device); the outputs and scratch it allocates belong to that stream.  Matrices may
-have any row stride as long as the elements of a row are neighbours.
+device); the outputs and scratch it allocates belong to that stream, and inputs of
+another stream are the caller's to keep until it is done.  Matrices may have any row
+stride (of the products: up to 2^22 elements) as long as the elements of a row are
+neighbours.
+
+There is no autograd here: outputs have no history, whether or not an input requires a
+gradient, and each operator's gradients are a function of their own, ``*_backward``.
 """
 from __future__ import annotations
 
