@@ -307,9 +307,12 @@ __global__ void __launch_bounds__(64 * kOneWaves) sort_one_kernel(const SortArgs
 // All bound by HBM: a row is a few KiB, so the copies are made of 16-byte accesses
 // by a group of threads per token (a wave for short rows, a workgroup for long
 // ones), which reads a token's row once and writes all its copies, or reads all its
-// copies and writes the sum once.  16384 tokens of 4 rows of 4096 bf16: copies 109 us (6.1
-// TB/s), sums 132 (5.1), both gradients 207 with dropped rows (5.2); loads behind branches
-// made them 134, 176 and 402.
+// copies and writes the sum once.  16384 tokens of 4 rows of 4096 bf16, one kernel again and
+// again: copies 131 us (671 MB: 5.1 TB/s), sums 131 (5.1), both gradients 231 with dropped rows
+// (1136 MB: 4.9).  Between others the caches move time from one to the next: copies take 109
+// behind a kernel that wrote little, and leave what the caches hold of their 537 MB to be
+// written under the next one; sums take 165 right behind them, 126 with a read of 1 GiB between.
+// Loads behind branches made them 134, 176 and 402.
 
 struct MoveArgs {
     const void* in;      // x, rows or dout

@@ -208,7 +208,10 @@ static bool good_rows(const rr_rows_t& r, uint64_t group, uint64_t width) {
 // The kernel and the parts of the contraction for one product: the least of the times that
 // these figures give, fitted on an MI355X to 320 products of 32 to 6400 rows and 128 to 8192
 // columns and depths, each with every tile and 1 to 16 parts (microseconds; a step is 64
-// deep; what they choose is 0.4% slower on average than the best).
+// deep).  Over 354 such products of 16 to 6400 rows the choice takes 1.009 of the best on
+// average; 36 take more than 1.05 of it, 12 more than 1.1, the worst 1.36 (6400 x 768 x 768 by
+// w).  The figures are for the whole device: with fewer compute units (a partition of it) the
+// results are the same, and the choice is off.
 //   tile       start   a step, with 1 .. 4 workgroups on each compute unit
 //   256 x 256   11.3    1.63 (1.1 on an empty device)
 //   128 x 128    6.6    0.73 (0.47), 1.16

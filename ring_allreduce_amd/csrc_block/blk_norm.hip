@@ -29,9 +29,17 @@ norm_parts_kernel(const float* part, int parts, uint64_t stride, int hidden, flo
 // ------------------------------------------------------------------ host side --
 
 // Threads and vectors per row.  A row of few vectors goes to a part of a wave or one wave (no barrier); a longer
-// one to as many threads as keep it in registers.  The backward kernel holds five rows, the
-// next five and the sums over tokens, so it takes twice the threads (16384 x 4096 bf16 with an
-// element gate: 358 us with 256 threads of two vectors).
+// one to as many threads as keep it in registers.  The backward kernel holds five rows and the
+// sums over tokens, so it takes twice the threads (16384 x 4096 bf16 with an element gate: 358
+// us with 256 threads of two vectors, 226 to 233 with 512 of one).  1024 threads leave each 128
+// registers, which the longest rows do not fit: the build spills
+//   bf16, fp16   backward beyond 8192 elements 26 to 36 registers, beyond 16384 238 to 400;
+//                forward beyond 16384 30 to 60
+//   fp32         backward beyond 8192 elements 38 to 122, beyond 16384 516 to 821; forward
+//                beyond 8192 with a gate 6 to 10, beyond 16384 154 to 378
+// at 128 MiB a matrix, without a gate and with one for each element (TB/s, forward; backward):
+//   bf16 16384  4.8, 4.6; 3.0, 3.2     32768  3.3, 3.4; 1.0, 0.8
+//   fp32 16384  4.8, 4.3; 2.9, 2.3     32768  1.8, 0.9; 1.0, 0.9
 static Config pick(int hidden, int dt, bool back) {
     const int n = (int)(16 / type_bytes(dt));
     const int vecs = (int)ceil_div(hidden, n);

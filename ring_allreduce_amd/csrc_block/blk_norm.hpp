@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(Shape<G>::block) norm_kernel(const NormArgs a)
 // workgroup takes (of the longest rows in LDS, where they fit), and the workgroups' parts
 // are added by a second, short kernel in a fixed order.  Registers decide the rate: the
 // loads of the next row on their way beside this one took 295 us for 16384 x 4096 bf16
-// with an element gate, with spills, against 236 (1074 MB: 4.6 TB/s) without.
+// with an element gate, with spills, against 226 to 236 (1074 MB: 4.6 to 4.8 TB/s) without.
 template <typename T, int G, int NV, int GATE, bool TINY>
 __global__ void __launch_bounds__(Shape<G>::block, G <= 64 ? (NV == 1 ? 3 : 2) : 4)
 norm_backward_kernel(const NormArgs a) {
