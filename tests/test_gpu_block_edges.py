@@ -271,3 +271,25 @@ def test_activations_at_infinities(rr, dtype, act, value, slope):
         want = [torch.tensor(v, dtype=torch.float64).repeat(rows)[:rows, None] for v in (value, slope)]
         torch.testing.assert_close(out.cpu().double(), want[0], rtol=0, atol=0, equal_nan=True)
         torch.testing.assert_close(d.dx.cpu().double(), want[1], rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hidden", [515, 1025, 1027, 1543, 2049, 4099, 8193, 16385])
+def test_norm_in_place_at_odd_widths(rr, dtype, hidden):
+    """A row's last vector is read so that it ends with the row, over elements that other waves
+    own and, without a norm in between, may have written by then: those do not count."""
+    g, dt, tokens = torch.Generator(device="cuda").manual_seed(hidden), DTYPES[dtype], 300
+    x, u, z = (torch.randn(tokens, hidden, generator=g, device="cuda").to(dt) for _ in range(3))
+    args = dict(post_norm=False, pre_norm=False, gate=z, gate_act="sigmoid", residual_scale=1.5)
+    h, _ = rr.block_norm(x, u, **args)
+    in_place = x.clone()
+    rr.block_norm(in_place, u, **args, h=in_place)
+    assert torch.equal(in_place, h)
+    want = rr.block_norm_backward(x, None, None, u, **args)
+    blk, dh = rr.block, x.clone()
+    a = blk._norm_args(x, u, False, None, z, "sigmoid", 1.5, 1.0, False, None, 1e-6)
+    grad, du, dz = blk._NormGrad(), torch.empty_like(x), torch.empty_like(x)
+    grad.dh = grad.dx = blk._Rows(dh.data_ptr(), hidden)
+    grad.dbranch, grad.dgate = blk._Rows(du.data_ptr(), hidden), blk._Rows(dz.data_ptr(), hidden)
+    assert blk._block_norm_backward(a, grad, None, 0, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(dh, want.dx) and torch.equal(du, want.dbranch) and torch.equal(dz, want.dgate)
