@@ -316,7 +316,8 @@ def _run_plain(s):
     if not c.get("train", True):
         return got
     if c["op"] == "checkpoint":
-        z = _plain_back(_plain_quantize(z.to(dt)))
+        z = z.to(dt).reshape(-1, 2, n)               # each half of a row by itself
+        z = _plain_back(_plain_quantize(z)).reshape(-1, 2 * n)
     else:
         got["z"] = z.to(dt)
         z = s["z"].float()
@@ -456,7 +457,8 @@ def exact(case, seed):
             p = {"out": curve(z[:, :n]) * z[:, n:]}
             if train:
                 if c["op"] == "checkpoint":
-                    z = _exact_kept(z.to(dt))[0] if hi > lo else z
+                    if hi > lo:
+                        z = _exact_kept(z.to(dt).unflatten(1, (2, n)))[0].flatten(1)
                     p["again"] = curve(z[:, :n]) * z[:, n:]
                 else:
                     p["z"], z = z, s["z"][lo:hi].double()
