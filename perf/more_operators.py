@@ -168,7 +168,7 @@ def _two_power(a):
     """The least power of two p, from 2^-126, with a / p <= 448; 1 for a = 0."""
     m, e = torch.frexp(a)                           # a = m 2^e, 1/2 <= m < 1; 448 = 7/8 2^9
     p = torch.where(m > 0.875, e - 8, e - 9).clamp(min=-126)
-    return torch.where(a == 0, 1.0, torch.ldexp(torch.ones_like(a), p))
+    return torch.where(a == 0, 1.0, ((p + 127) << 23).view(torch.float32))
 
 
 def _plain_quantize(x, square=False, two_power=True):
@@ -375,6 +375,11 @@ def run(state):
 
 # ---------------------------------------------------------------- 64 bits --
 
+def _exact_power(p):
+    """2^p in 64 bits, to the bit (exp2 and pow may be a step off)."""
+    return ((p.long() + 1023) << 52).view(torch.float64)
+
+
 def _exact_scales(x, square):
     """The scale of each block, in 64 bits."""
     size = x.double().abs()
@@ -383,13 +388,13 @@ def _exact_scales(x, square):
     top = torch.nn.functional.max_pool2d(size.reshape(-1, 1, *size.shape[-2:]), area, ceil_mode=True)
     top = top.reshape(*size.shape[:-2], *top.shape[-2:])
     p = torch.ceil(torch.log2(top.clamp(min=LARGEST * 2.0 ** -126) / LARGEST))
-    p = torch.where(LARGEST * torch.exp2(p - 1) >= top, p - 1, p)       # where log2 was rounded up
-    return torch.where(top > 0, torch.exp2(p.clamp(min=-126.0)), 1.0)
+    p = torch.where(LARGEST * _exact_power(p - 1) >= top, p - 1, p)       # where log2 was rounded up
+    return torch.where(top > 0, _exact_power(p.clamp(min=-126.0)), 1.0)
 
 
 def _exact_e4m3(v):
     """v, up to 448 in size, at e4m3's steps: 2^-3 of its power of two, from 2^-9."""
-    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    step = _exact_power(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
     return torch.round(v / step) * step
 
 
