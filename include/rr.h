@@ -556,7 +556,7 @@ typedef enum {
     RR_ACT_RELU = 1,
     RR_ACT_GELU = 2,    /* z/2 (1 + erf(z / sqrt 2)) */
     RR_ACT_SILU = 3,    /* z / (1 + exp(-z)) */
-    RR_ACT_SIGMOID = 4  /* gates only */
+    RR_ACT_SIGMOID = 4  /* gates and gated projections only */
 } rr_act_t;
 /* NaN stays NaN.  At infinities GELU and its slope take their limits (infinity and 1, 0
    and 0); SiLU's infinity and, at minus infinity, NaN are what the formula gives in
@@ -712,6 +712,89 @@ rr_status_t block_linear_backward(const rr_linear_t *a, const rr_linear_grad_t *
                                   void *workspace, size_t workspace_bytes, rr_stream_t stream);
 rr_status_t block_linear_backward_workspace(const rr_linear_t *a, const rr_linear_grad_t *g,
                                             size_t *bytes);
+
+/* --- 8-bit values with a scale for each block of 128 --- */
+
+/* e4m3 (1 sign, 4 exponent and 3 mantissa bits, largest value 448, no infinities) in
+   bytes, and fp32 scales: an element stands for its value times its block's scale.
+   A block is 128 columns of a row or, `square`, 128 rows by 128 columns of a matrix; the
+   last ones of a row or matrix may be smaller.  The scales are contiguous, in the order
+   of the blocks: of `groups` matrices of `rows` rows, rows * B of each, or, square,
+   R * B, with B = ceil(width / 128) and R = ceil(rows / 128).
+   block_quantize: a = the largest finite magnitude in the block, scale = the least
+   power of two p with a / p <= 448, but at least 2^-126, and 1 for a = 0; value =
+   x / p rounded to the nearest, ties to even; NaN and infinities become NaN.
+   block_dequantize: value * scale, rounded to dt; a finite product beyond the largest
+   value of RR_FP16 becomes that.
+   Matrix g starts at element g * x_stride of x and byte g * q_stride of q (both not read
+   for one matrix).  Matrices that are written may not overlap.  Limits: width and
+   groups * rows < 2^31 - 1024, 2^34 blocks, of which block_quantize makes 2^24 square ones. */
+typedef struct {
+    size_t groups, rows, width;
+    int32_t dt;         /* of x: RR_FP32, RR_BF16 or RR_FP16 */
+    int32_t square;     /* 0 or 1 */
+    rr_rows_t x;        /* in; out of block_dequantize */
+    size_t x_stride;
+    rr_rows_t q;        /* out, ld in bytes; in of block_dequantize */
+    size_t q_stride;
+    float *scales;      /* out; in of block_dequantize */
+} rr_quantize_t;
+rr_status_t block_quantize(const rr_quantize_t *a, rr_stream_t stream);
+rr_status_t block_dequantize(const rr_quantize_t *a, rr_stream_t stream);
+
+/* A block's product of 8-bit operands, as rr_linear_t says, with l.x and l.w in e4m3:
+   l.x.ld, l.w_ld and l.w_stride are bytes, x has a scale for 128 columns of a row and w_e
+   square blocks, both as above (rows and n x k matrices); any fp32 scales will do.  l.dt is
+   the type of bias, residual, z and out.  The products of a block of 128 are summed in
+   the matrix instructions' 32 bits, the blocks on top of each other, times their scales, in
+   32 bits.  z_scales: NULL. */
+typedef struct {
+    rr_linear_t l;
+    const float *x_scales, *w_scales;
+    float *z_scales;
+} rr_linear8_t;
+rr_status_t block_linear8(const rr_linear8_t *a, void *workspace, size_t workspace_bytes,
+                          rr_stream_t stream);
+rr_status_t block_linear8_workspace(const rr_linear8_t *a, size_t *bytes);
+/* The gradients of block_linear or block_linear8, at what the 8 bits stand for: x and w are
+   each in e4m3 where they have scales, else in l.dt.  8-bit operands become dt on their way
+   into the products, which is exact with block_quantize's scales (but for values past the
+   ends of RR_FP16) and half a step off with others. */
+rr_status_t block_linear8_backward(const rr_linear8_t *a, const rr_linear_grad_t *g,
+                                   void *workspace, size_t workspace_bytes, rr_stream_t stream);
+rr_status_t block_linear8_backward_workspace(const rr_linear8_t *a, const rr_linear_grad_t *g,
+                                             size_t *bytes);
+
+/* --- a block's gated projections --- */
+
+/* [g | u] = x w_e^T + bias_e, out = act(g) * u: the gate's n rows of w_e and, n * w_ld
+   elements behind, the other projection's n rows; bias has groups * 2 * n elements, z rows
+   have the n columns of g and then those of u; l.n is n, and l.residual absent.  Sizes,
+   groups, offsets and types as rr_linear_t says, l.act also RR_ACT_SIGMOID.  x and w
+   both with scales: products of 8-bit operands, w_e's two halves being matrices of n rows
+   with blocks of their own.  z with z_scales: e4m3, z.ld in bytes, each half of a row
+   in blocks of its own (rows * 2 * ceil(n / 128) scales, g's of a row first):
+   block_quantize's of z in dt.  Limits: 2 * n <= 2^22. */
+typedef struct {
+    rr_rows_t dout;
+    rr_rows_t dx;
+    void *dw;           /* groups x 2 n x k, contiguous, in dt or fp32 (dw_dt) */
+    float *db;          /* groups x 2 n */
+    rr_rows_t out;      /* out once more, made from z: what the next product's dw needs */
+    int32_t dw_dt;
+    int32_t reserved;   /* 0 */
+} rr_gated_grad_t;
+rr_status_t block_gated(const rr_linear8_t *a, void *workspace, size_t workspace_bytes,
+                        rr_stream_t stream);
+rr_status_t block_gated_workspace(const rr_linear8_t *a, size_t *bytes);
+/* dg = dout * u * act'(g), du = dout * act(g); dx = [dg | du] w_e, dw_e = [dg | du]^T x_e, db_e =
+   their sums, as block_linear_backward gives them.  x, w and z are each in e4m3 where they
+   have scales, else in l.dt; z is always read.  Each output NULL or absent if not wanted; out
+   is zero in rows of no group. */
+rr_status_t block_gated_backward(const rr_linear8_t *a, const rr_gated_grad_t *g, void *workspace,
+                                 size_t workspace_bytes, rr_stream_t stream);
+rr_status_t block_gated_backward_workspace(const rr_linear8_t *a, const rr_gated_grad_t *g,
+                                           size_t *bytes);
 
 /* Human-readable name of a status. */
 const char *rr_status_string(rr_status_t s);

@@ -18,8 +18,10 @@ from dataclasses import dataclass
 import torch  # noqa: F401  (loads the HIP runtime librr.so must share)
 
 from . import block
-from .block import (ExpertOrder, LinearGrads, NormGrads, block_linear,  # noqa: F401
-                    block_linear_backward, block_norm, block_norm_backward, expert_combine,
+from .block import (ExpertOrder, GatedGrads, LinearGrads, NormGrads, Quantized,  # noqa: F401
+                    block_dequantize, block_gated, block_gated_backward, block_linear,
+                    block_linear8, block_linear8_backward, block_linear_backward, block_norm,
+                    block_norm_backward, block_quantize, expert_combine,
                     expert_combine_backward, expert_dispatch, expert_dispatch_backward,
                     expert_sort)
 

@@ -1,8 +1,8 @@
 """A block's operators between two collectives -- Python binding.
 
 Tokens sorted by expert and moved to the AlltoAll's blocks and back, the norms
-around a block, and a block's matrix products, with their gradients, as declared
-in ``include/rr.h``.  Like the rest of the binding this only marshals: it checks
+around a block, and a block's matrix products, plain and gated, in 16 and in 8 bits,
+with their gradients, as declared in ``include/rr.h``.  Like the rest of the binding this only marshals: it checks
 shapes and types, makes output and scratch tensors, and calls the library; there
 is no fallback.  Calls in their usual form (on the current device and stream, new
 outputs) are marshalled by the module ``_block``, in C++, which is bound to the torch it
@@ -69,6 +69,21 @@ class _LinearGrad(ctypes.Structure):
                 ("dw_dt", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class _Linear8(ctypes.Structure):
+    _fields_ = [("l", _Linear), ("x_scales", _vp), ("w_scales", _vp), ("z_scales", _vp)]
+
+
+class _GatedGrad(ctypes.Structure):
+    _fields_ = [("dout", _Rows), ("dx", _Rows), ("dw", _vp), ("db", _vp), ("out", _Rows),
+                ("dw_dt", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _Quantize(ctypes.Structure):
+    _fields_ = [("groups", _sz), ("rows", _sz), ("width", _sz), ("dt", ctypes.c_int32),
+                ("square", ctypes.c_int32), ("x", _Rows), ("x_stride", _sz), ("q", _Rows),
+                ("q_stride", _sz), ("scales", _vp)]
+
+
 class _Absent:
     """In the place of the module ``_block``: takes no call, so that all are marshalled here."""
 
@@ -108,12 +123,24 @@ def _bind(sig):
                                       _sz, _vp)
     g["_block_linear_backward_workspace"] = sig("block_linear_backward_workspace", _i, p(_Linear),
                                                 p(_LinearGrad), p(_sz))
+    g["_block_quantize"] = sig("block_quantize", _i, p(_Quantize), _vp)
+    g["_block_dequantize"] = sig("block_dequantize", _i, p(_Quantize), _vp)
+    for name, grad in (("linear8", _LinearGrad), ("gated", _GatedGrad)):
+        name = "block_" + name
+        g["_" + name] = sig(name, _i, p(_Linear8), _vp, _sz, _vp)
+        g[f"_{name}_workspace"] = sig(name + "_workspace", _i, p(_Linear8), p(_sz))
+        g[f"_{name}_backward"] = sig(name + "_backward", _i, p(_Linear8), p(grad), _vp, _sz, _vp)
+        g[f"_{name}_backward_workspace"] = sig(name + "_backward_workspace", _i, p(_Linear8), p(grad),
+                                               p(_sz))
 
 
 EXPORTED = ["expert_sort", "expert_sort_workspace", "expert_dispatch", "expert_combine",
             "expert_combine_backward", "block_norm", "block_norm_backward",
             "block_norm_backward_workspace", "block_linear", "block_linear_workspace",
-            "block_linear_backward", "block_linear_backward_workspace"]
+            "block_linear_backward", "block_linear_backward_workspace", "block_quantize",
+            "block_dequantize", "block_linear8", "block_linear8_workspace",
+            "block_linear8_backward", "block_linear8_backward_workspace", "block_gated",
+            "block_gated_workspace", "block_gated_backward", "block_gated_backward_workspace"]
 
 
 def _check(status, what):
@@ -297,7 +324,17 @@ def _pairs(slots, name="slots"):
 
 def expert_dispatch(x, slots, sources, *, out=None, stream=None):
     """Copies each token's row to the rows of its slots: [len(sources), hidden].  Rows
-    without a source become zero."""
+    without a source become zero.  A Quantized ``x`` (a scale for each 128 of a row, an even
+    number of columns) is dispatched as values and scales."""
+    if isinstance(x, Quantized):
+        _need(out is None, "out is for tensors only")
+        _quantized(x, "x", False)
+        v = x.values
+        _need(v.dim() == 2 and v.shape[1] % 2 == 0 and (v.shape[0] < 2 or v.stride(0) % 2 == 0) and
+              v.storage_offset() % 2 == 0, "x must be a matrix whose rows are whole pairs of values")
+        _scales(x, "x", v.device)
+        return Quantized(expert_dispatch(v.view(torch.bfloat16), slots, sources, stream=stream).view(E4M3),
+                         expert_dispatch(x.scales, slots, sources, stream=stream))
     if stream is None and out is None:
         done = _block.dispatch(x, slots, sources)
         if done is not None:
@@ -623,4 +660,384 @@ def block_linear_backward(dout, x, w, z=None, *, act="none", offsets=None, need_
         _check(_block_linear_backward_workspace(a, g, size), "block_linear_backward")
         work, wp = _scratch(size.value, dev)
         _check(_block_linear_backward(a, g, wp, size.value, s), "block_linear_backward")
+    return out
+
+
+# ------------------------------------- 8-bit values with a scale for each block of 128
+
+BLOCK = 128
+E4M3 = torch.float8_e4m3fn
+
+
+@dataclass
+class Quantized:
+    """8-bit values and the fp32 scales of their blocks: an element stands for its value times
+    its block's scale.  ``values`` [..., rows, k] (float8_e4m3fn); ``scales`` [..., rows,
+    ceil(k / 128)], one for 128 columns of a row, or, ``square``, [..., ceil(rows / 128),
+    ceil(k / 128)], one for 128 rows by 128 columns."""
+    values: torch.Tensor
+    scales: torch.Tensor
+    square: bool = False
+
+
+def _blocks(n):
+    return -(-n // BLOCK)
+
+
+def _scales_shape(shape, square):
+    return (*shape[:-2], _blocks(shape[-2]) if square else shape[-2], _blocks(shape[-1]))
+
+
+def _scales(q, name, device):
+    """The address of a Quantized's scales, their shape and place checked."""
+    shape, s = _scales_shape(q.values.shape, q.square), q.scales
+    if not isinstance(s, torch.Tensor) or s.device != device:
+        raise ValueError(f"{name}.scales must be on the same GPU")
+    if s.dtype != torch.float32:
+        raise TypeError(f"{name}.scales must be torch.float32, not {s.dtype}")
+    if tuple(s.shape) != shape or not s.is_contiguous():
+        raise ValueError(f"{name}.scales must be contiguous, of shape {list(shape)}")
+    return s.data_ptr()
+
+
+def _quantized(q, name, square):
+    if not isinstance(q.values, torch.Tensor) or q.values.dtype != E4M3:
+        raise TypeError(f"{name}.values must be {E4M3}")
+    _need(bool(q.square) == square, f"{name} must have " +
+          ("square blocks" if square else "a scale for each 128 of a row, not square blocks"))
+
+
+def _stack(t, name):
+    """``t`` [..., rows, width] as matrices a stride apart: (groups, _Rows, stride)."""
+    if not isinstance(t, torch.Tensor) or t.dim() < 2:
+        raise ValueError(f"{name} must be a matrix, or matrices")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the same GPU")
+    if t.dim() == 2:
+        return 1, _matrix(t, name), 0
+    try:
+        s = t.view(-1, *t.shape[-2:]) if t.numel() else t.new_empty((0, *t.shape[-2:]))
+    except RuntimeError:
+        raise ValueError(f"{name}: its matrices must be one stride apart") from None
+    if not s.shape[0]:
+        return 0, _Rows(), 0
+    return s.shape[0], _matrix(s[0], name), s.stride(0)
+
+
+def _quantize_args(wide, q, dt):
+    a = _Quantize()
+    groups, a.x, a.x_stride = _stack(wide, "x")
+    n, a.q, a.q_stride = _stack(q.values, "values")
+    a.groups, a.rows, a.width = groups, wide.shape[-2], wide.shape[-1]
+    a.dt, a.square = dt, int(q.square)
+    a.scales = q.scales.data_ptr()
+    return a
+
+
+def block_quantize(x, *, square=False, stream=None) -> Quantized:
+    """``x`` [..., rows, k] in e4m3 with a scale for each 128 columns of a row, or, ``square``,
+    128 x 128 of a matrix: the least power of two with which the block's largest finite value is
+    at most 448 (1 for zeros).  Values are rounded to the nearest, ties to even; NaN and
+    infinities become NaN."""
+    if stream is None:
+        done = _block.quantize(x, square)
+        if done is not None:
+            return Quantized(*done, bool(square))
+    dt = _float_type(x, "x")
+    _need(x.dim() >= 2, "x must be a matrix, or matrices")
+    _need(x.is_cuda, "x must be on a GPU")
+    _need(x.shape[-1] > 0, "x must have columns")
+    square = bool(square)
+    with _on(x.device, stream) as s:
+        q = Quantized(torch.empty(x.shape, dtype=E4M3, device=x.device),
+                      torch.empty(_scales_shape(x.shape, square), device=x.device), square)
+        if x.numel():
+            _check(_block_quantize(_quantize_args(x, q, dt), s), "block_quantize")
+    return q
+
+
+def block_dequantize(q, dtype=torch.bfloat16, *, out=None, stream=None):
+    """What ``q`` stands for, in ``dtype``; a finite value beyond float16's largest becomes that."""
+    if stream is None and out is None and isinstance(q, Quantized):
+        done = _block.dequantize(q.values, q.scales, q.square, FLOAT_DTYPES.get(dtype, -1))
+        if done is not None:
+            return done
+    if not isinstance(q, Quantized):
+        raise TypeError("q must be Quantized")
+    _quantized(q, "q", bool(q.square))
+    _need(q.values.dim() >= 2 and q.values.is_cuda, "q must be matrices on a GPU")
+    _need(q.values.shape[-1] > 0, "q must have columns")
+    dev = q.values.device
+    _scales(q, "q", dev)
+    if out is not None:
+        dtype = out.dtype
+        _need(out.device == dev and out.shape == q.values.shape, "out must have q's shape and GPU")
+    if dtype not in FLOAT_DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}; use float32, bfloat16 or float16")
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(q.values.shape, dtype=dtype, device=dev)
+        if q.values.numel():
+            _check(_block_dequantize(_quantize_args(out, q, FLOAT_DTYPES[dtype]), s), "block_dequantize")
+    return out
+
+
+_NOWHERE = 16       # in the place of an empty tensor's address: there, and read by nothing
+
+
+def _operand(t, name, dev, dtype, rows=None, width=None):
+    """The matrix x, in ``dtype`` or Quantized: (its _Rows, its scales' address or None)."""
+    if not isinstance(t, Quantized):
+        return _matrix(t, name, dev, dtype, rows, width), None
+    _quantized(t, name, False)
+    return _matrix(t.values, name, dev, E4M3, rows, width), \
+        _scales(t, name, t.values.device if dev is None else dev) or _NOWHERE
+
+
+def _wide_args(x, w, offsets, act, dtype, halves):
+    """The _Linear8 of x [rows, k] and w [n, k] or [groups, n, k], with ``halves`` 2 [2, n, k] or
+    [groups, 2, n, k], each in ``dtype`` or Quantized."""
+    a = _Linear8()
+    l = a.l
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"unsupported dtype {dtype}; use bfloat16 or float16")
+    xv, wv = (t.values if isinstance(t, Quantized) else t for t in (x, w))
+    if not isinstance(xv, torch.Tensor) or xv.dim() != 2:
+        raise ValueError("x must be a matrix")
+    dev = xv.device
+    l.x, a.x_scales = _operand(x, "x", None, dtype)
+    l.rows, l.k, l.dt = xv.shape[0], xv.shape[1], FLOAT_DTYPES[dtype]
+    d = 2 if halves == 1 else 3
+    _need(isinstance(wv, torch.Tensor) and wv.dim() in (d, d + 1),
+          "w must be [n, k] or [groups, n, k]" if halves == 1 else "w must be [2, n, k] or [groups, 2, n, k]")
+    _need(wv.device == dev, "w must be on the same GPU")
+    if isinstance(w, Quantized):
+        _quantized(w, "w", True)
+        a.w_scales = _scales(w, "w", dev)
+    elif wv.dtype != dtype:
+        raise TypeError(f"w must be {dtype}, not {wv.dtype}")
+    _need(wv.shape[-1] == l.k, f"w must have {l.k} columns, not {wv.shape[-1]}")
+    l.groups = wv.shape[0] if wv.dim() > d else 1
+    _need(l.groups >= 1, "w must have at least one group")
+    l.n = wv.shape[-2]
+    first = wv[0] if wv.dim() > d else wv
+    r = _matrix(first[0] if halves == 2 else first, "w")
+    l.w, l.w_ld = r.data, r.ld
+    if halves == 2:
+        _need(first.shape[0] == 2, "w must hold two matrices, the gate's and the other projection's")
+        if l.n == 1:
+            l.w_ld = first.stride(0)
+        _need(first.stride(0) == l.n * l.w_ld, "w: the second matrix must follow the first")
+    l.w_stride = wv.stride(0) if wv.dim() > d else 0
+    l.act = ACTS[act]
+    if offsets is not None:
+        l.offsets = _ints(offsets, "offsets", dev, l.groups + 1)
+    else:
+        _need(l.rows % l.groups == 0, "without offsets the groups must divide the rows")
+    return a, dev
+
+
+def _act_of(act, allowed):
+    _need(act in allowed, "act must be " + ", ".join(allowed[:-1]) + " or " + allowed[-1])
+
+
+_LINEAR_ACTS = ("none", "relu", "gelu", "silu")
+_GATED_ACTS = ("none", "relu", "gelu", "silu", "sigmoid")
+
+
+def block_linear8(x, w, bias=None, *, dtype=torch.bfloat16, act="none", residual=None, offsets=None,
+                  save_preact=False, out=None, stream=None):
+    """``block_linear`` of 8-bit operands: ``x`` Quantized [rows, k] with a scale for each 128 of a
+    row, ``w`` Quantized [n, k] or [groups, n, k] with square blocks (``block_quantize``'s, or any
+    others with fp32 scales).  ``dtype`` (bfloat16 or float16) is the type of bias, residual, z
+    and out."""
+    if stream is None and out is None and isinstance(x, Quantized) and isinstance(w, Quantized) and \
+            w.square and not x.square:
+        done = _block.linear8(x.values, x.scales, w.values, w.scales, bias, ACTS.get(act, -1),
+                              residual, offsets, save_preact, FLOAT_DTYPES.get(dtype, -1))
+        if done is not None:
+            return done
+    if not isinstance(x, Quantized) or not isinstance(w, Quantized):
+        raise TypeError("x and w must be Quantized")
+    _act_of(act, _LINEAR_ACTS)
+    a, dev = _wide_args(x, w, offsets, act, dtype, 1)
+    l, shape = a.l, (x.values.shape[0], a.l.n)
+    l.bias = _ordered(bias, "bias", dev, dtype, l.groups, l.n)
+    if residual is not None:
+        l.residual = _matrix(residual, "residual", dev, dtype, *shape)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        l.out = _matrix(out, "out", dev, dtype, *shape)
+        z = None
+        if save_preact:
+            z = torch.empty(shape, dtype=dtype, device=dev)
+            l.z = _matrix(z, "z", dev, dtype, *shape)
+        size = _sz()
+        _check(_block_linear8_workspace(a, size), "block_linear8")
+        work, wp = _scratch(size.value, dev)
+        _check(_block_linear8(a, wp, size.value, s), "block_linear8")
+    return (out, z) if save_preact else out
+
+
+def _dw_type(dw_dtype, dtype):
+    dw_dtype = dw_dtype or dtype
+    if dw_dtype not in (dtype, torch.float32):
+        raise TypeError(f"dw_dtype must be {dtype} or float32")
+    return dw_dtype
+
+
+def _values(t):
+    return t.values if isinstance(t, Quantized) else t
+
+
+def block_linear8_backward(dout, x, w, z=None, *, act="none", offsets=None, need_dx=True, need_dw=True,
+                           need_db=True, dw_dtype=None, stream=None) -> LinearGrads:
+    """Gradients of ``block_linear8`` or ``block_linear`` by x, w and bias, at what ``x`` and ``w``
+    stand for: each Quantized, as a forward pass used or kept it, or a tensor of ``dout``'s
+    dtype."""
+    if not isinstance(dout, torch.Tensor):
+        raise ValueError("dout must be a matrix")
+    dtype = dout.dtype
+    if stream is None and dw_dtype in (None, torch.float32):
+        done = _block.linear8_backward(
+            dout, *_pair(x, False), *_pair(w, True), z, ACTS.get(act, -1), offsets, need_dx, need_dw,
+            need_db, dw_dtype is not None)
+        if done is not None:
+            return LinearGrads(*done)
+    _act_of(act, _LINEAR_ACTS)
+    a, dev = _wide_args(x, w, offsets, act, dtype, 1)
+    l, g, out = a.l, _LinearGrad(), LinearGrads()
+    g.dout = _matrix(dout, "dout", dev, dtype, l.rows, l.n)
+    if act != "none":
+        _need(z is not None, "act needs the pre-activation z")
+        l.z = _matrix(z, "z", dev, dtype, l.rows, l.n)
+    dw_dtype = _dw_type(dw_dtype, dtype)
+    g.dw_dt = FLOAT_DTYPES[dw_dtype]
+    with _on(dev, stream) as s:
+        _make_grads(g, out, _values(x), _values(w), dtype, dw_dtype, dev, need_dx, need_dw, need_db)
+        size = _sz()
+        _check(_block_linear8_backward_workspace(a, g, size), "block_linear8_backward")
+        work, wp = _scratch(size.value, dev)
+        _check(_block_linear8_backward(a, g, wp, size.value, s), "block_linear8_backward")
+    return out
+
+
+def _pair(t, square):
+    """A Quantized's tensors, or a tensor and None, for the module ``_block``."""
+    if isinstance(t, Quantized):
+        return (t.values, t.scales) if bool(t.square) == square else (False, False)
+    return t, None
+
+
+def _make_grads(g, out, x, w, dtype, dw_dtype, dev, need_dx, need_dw, need_db):
+    if need_dx:
+        out.dx = torch.empty(x.shape, dtype=dtype, device=dev)
+        g.dx = _Rows(out.dx.data_ptr(), x.shape[1] or 1)
+    if need_dw:
+        out.dw = torch.empty(w.shape, dtype=dw_dtype, device=dev)
+        g.dw = out.dw.data_ptr()
+    if need_db:
+        out.db = torch.empty(w.shape[:-1], dtype=torch.float32, device=dev)
+        g.db = out.db.data_ptr()
+
+
+# ------------------------------------------------------- a block's gated projections
+
+def block_gated(x, w, bias=None, *, act="silu", offsets=None, save_preact=False, dtype=None, out=None,
+                stream=None):
+    """act(g) * u for [g | u] = x w^T + bias: x [rows, k], w [2, n, k] (the gate's matrix, then
+    the other projection's) and bias [2, n], or the rows of each group with its own w [groups, 2, n,
+    k] and bias [groups, 2, n]; ``offsets`` as ``block_linear`` takes them.  act: none, relu, gelu,
+    silu or sigmoid.  x and w are tensors of ``dtype``, or both Quantized (then ``dtype`` says the
+    type of bias, z and out: bfloat16 by default).  Returns out, or (out, z) if save_preact: z
+    [rows, 2 n] is g and u, and with save_preact="e4m3" a Quantized [rows, 2, n].  Rows of no group
+    become zero."""
+    eight = save_preact == "e4m3"
+    if stream is None and out is None:
+        kind = FLOAT_DTYPES.get(dtype, -1 if dtype is not None else 0)
+        done = _block.gated(*_pair(x, False), *_pair(w, True), bias, ACTS.get(act, -1), offsets,
+                            2 if eight else 1 if save_preact is True else 0 if save_preact is False else -1, kind)
+        if done is not None:
+            if eight:
+                return done[0], Quantized(done[1], done[2])
+            return done
+    _need(save_preact in (False, True, "e4m3"), 'save_preact must be False, True or "e4m3"')
+    _act_of(act, _GATED_ACTS)
+    if isinstance(x, Quantized) != isinstance(w, Quantized):
+        raise TypeError("x and w must both be Quantized, or neither")
+    if dtype is None:
+        dtype = torch.bfloat16 if isinstance(x, Quantized) else getattr(x, "dtype", None)
+    a, dev = _wide_args(x, w, offsets, act, dtype, 2)
+    l = a.l
+    l.bias = _ordered(bias, "bias", dev, dtype, l.groups, 2, l.n)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((l.rows, l.n), dtype=dtype, device=dev)
+        l.out = _matrix(out, "out", dev, dtype, l.rows, l.n)
+        z = None
+        if eight:
+            z = Quantized(torch.empty((l.rows, 2, l.n), dtype=E4M3, device=dev),
+                          torch.empty((l.rows, 2, _blocks(l.n)), device=dev))
+            l.z, a.z_scales = _Rows(z.values.data_ptr(), 2 * l.n), z.scales.data_ptr()
+        elif save_preact:
+            z = torch.empty((l.rows, 2 * l.n), dtype=dtype, device=dev)
+            l.z = _Rows(z.data_ptr(), 2 * l.n)
+        size = _sz()
+        _check(_block_gated_workspace(a, size), "block_gated")
+        work, wp = _scratch(size.value, dev)
+        _check(_block_gated(a, wp, size.value, s), "block_gated")
+    return (out, z) if save_preact else out
+
+
+@dataclass
+class GatedGrads:
+    """Gradients of ``block_gated``; what is not needed is None.  db is fp32.  ``out`` is the
+    forward pass's result, made again from z."""
+    dx: torch.Tensor | None = None
+    dw: torch.Tensor | None = None
+    db: torch.Tensor | None = None
+    out: torch.Tensor | None = None
+
+
+def block_gated_backward(dout, x, w, z, *, act="silu", offsets=None, need_dx=True, need_dw=True,
+                         need_db=True, need_out=False, dw_dtype=None, stream=None) -> GatedGrads:
+    """Gradients of ``block_gated`` by x, w and bias, of w's shape.  ``z`` is what save_preact
+    gave, in either form; x and w are tensors of ``dout``'s dtype or Quantized, each by itself: the
+    gradients are those at what they stand for.  ``need_out`` makes the forward pass's out
+    again, which the next product's backward pass reads, so that nobody has to keep it."""
+    if not isinstance(dout, torch.Tensor):
+        raise ValueError("dout must be a matrix")
+    dtype = dout.dtype
+    if stream is None and dw_dtype in (None, torch.float32):
+        done = _block.gated_backward(
+            dout, *_pair(x, False), *_pair(w, True), *_pair(z, False), ACTS.get(act, -1), offsets,
+            need_dx, need_dw, need_db, need_out, dw_dtype is not None)
+        if done is not None:
+            return GatedGrads(*done)
+    _act_of(act, _GATED_ACTS)
+    a, dev = _wide_args(x, w, offsets, act, dtype, 2)
+    l, g, out = a.l, _GatedGrad(), GatedGrads()
+    g.dout = _matrix(dout, "dout", dev, dtype, l.rows, l.n)
+    if isinstance(z, Quantized):
+        _quantized(z, "z", False)
+        v = z.values
+        _need(v.device == dev and tuple(v.shape) == (l.rows, 2, l.n), f"z must be [{l.rows}, 2, {l.n}]")
+        _need(not v.numel() or (v.stride(2) == 1 or l.n == 1) and v.stride(1) == l.n and
+              (l.rows == 1 or v.stride(0) >= 2 * l.n), "z: the halves of a row must be neighbours")
+        l.z = _Rows(v.data_ptr(), v.stride(0) if l.rows > 1 else 2 * l.n)
+        a.z_scales = _scales(z, "z", dev) or _NOWHERE
+    else:
+        l.z = _matrix(z, "z", dev, dtype, l.rows, 2 * l.n)
+    dw_dtype = _dw_type(dw_dtype, dtype)
+    g.dw_dt = FLOAT_DTYPES[dw_dtype]
+    with _on(dev, stream) as s:
+        _make_grads(g, out, _values(x), _values(w), dtype, dw_dtype, dev, need_dx, need_dw, need_db)
+        if need_out:
+            out.out = torch.empty((l.rows, l.n), dtype=dtype, device=dev)
+            g.out = _Rows(out.out.data_ptr(), l.n or 1)
+        size = _sz()
+        _check(_block_gated_backward_workspace(a, g, size), "block_gated_backward")
+        work, wp = _scratch(size.value, dev)
+        _check(_block_gated_backward(a, g, wp, size.value, s), "block_gated_backward")
     return out

@@ -383,6 +383,241 @@ PyObject* linear_backward(Args& a) {
     return tuple({dx, dw, db});
 }
 
+// ------------------------------------------------- 8-bit values and gated projections
+
+constexpr auto kE4M3 = at::kFloat8_e4m3fn;
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+
+// The shape of the scales of values of shape `s`.
+std::vector<int64_t> scales_shape(at::IntArrayRef s, bool square) {
+    std::vector<int64_t> v(s.begin(), s.end());
+    const size_t d = v.size();
+    v[d - 1] = blocks_of(v[d - 1]);
+    if (square) v[d - 2] = blocks_of(v[d - 2]);
+    return v;
+}
+bool scales_fit(const Call& c, const Tensor& values, const Tensor& scales, bool square) {
+    return c.here(scales) && scales.scalar_type() == at::kFloat && scales.is_contiguous() &&
+           scales.sizes().equals(scales_shape(values.sizes(), square));
+}
+
+// t [..., rows, width], not empty, as contiguous matrices or one of any row stride.
+bool stack(const Call& c, const Tensor& t, rr_rows_t& r, size_t& stride, rr_quantize_t& q) {
+    const int64_t d = t.dim();
+    if (d < 2 || t.numel() < 1 || !c.here(t)) return false;
+    q.rows = (size_t)t.size(d - 2);
+    q.width = (size_t)t.size(d - 1);
+    q.groups = (size_t)t.numel() / q.rows / q.width;
+    stride = q.rows * q.width;
+    r = {t.data_ptr(), q.width};
+    if (t.is_contiguous()) return true;
+    if (d != 2 || t.stride(1) != 1 || (t.size(0) > 1 && t.stride(0) < t.size(1))) return false;
+    if (t.size(0) > 1) r.ld = (size_t)t.stride(0);
+    return true;
+}
+
+// x, square
+PyObject* quantize(Args& a) {
+    const Tensor* x = a.needed(0);
+    const bool square = a.flag(1);
+    Call c;
+    rr_quantize_t q = {};
+    if (!a.good || !c.begin(*x) || !known(x->scalar_type()) || !stack(c, *x, q.x, q.x_stride, q)) return none();
+    Tensor values = c.make(x->sizes(), kE4M3), scales = c.make(scales_shape(x->sizes(), square), at::kFloat);
+    q.dt = type_of(x->scalar_type());
+    q.square = square;
+    q.q = {values.data_ptr(), q.width};
+    q.q_stride = q.rows * q.width;
+    q.scales = (float*)scales.data_ptr();
+    if (block_quantize(&q, c.stream) != RR_OK) return none();
+    return tuple({values, scales});
+}
+
+at::ScalarType type_named(long dt) {
+    return dt == RR_FP32 ? at::kFloat : dt == RR_BF16 ? at::kBFloat16 : dt == RR_FP16 ? at::kHalf : at::kByte;
+}
+
+// values, scales, square, dtype
+PyObject* dequantize(Args& a) {
+    const Tensor *values = a.needed(0), *scales = a.needed(1);
+    const bool square = a.flag(2);
+    const auto type = type_named(a.number(3));
+    Call c;
+    rr_quantize_t q = {};
+    if (!a.good || !known(type) || values->scalar_type() != kE4M3 || !c.begin(*values) ||
+        !stack(c, *values, q.q, q.q_stride, q) || !scales_fit(c, *values, *scales, square))
+        return none();
+    Tensor out = c.make(values->sizes(), type);
+    q.dt = type_of(type);
+    q.square = square;
+    q.x = {out.data_ptr(), q.width};
+    q.x_stride = q.rows * q.width;
+    q.scales = (float*)scales->data_ptr();
+    if (block_dequantize(&q, c.stream) != RR_OK) return none();
+    return wrap(out);
+}
+
+// x and w, each with its scales or none, of a product of `halves` matrices a group
+bool wide_args(const Call& c, const Tensor& x, const Tensor* xs, const Tensor& w, const Tensor* ws, const Tensor* offsets,
+               long act, at::ScalarType type, int halves, rr_linear8_t& a) {
+    rr_linear_t& l = a.l;
+    if (x.dim() != 2 || (type != at::kBFloat16 && type != at::kHalf)) return false;
+    const int64_t rows = x.size(0), k = x.size(1);
+    if (!c.matrix(x, xs ? kE4M3 : type, rows, k, l.x) || (xs && !scales_fit(c, x, *xs, false))) return false;
+    const int d = (int)w.dim(), one = halves == 1 ? 2 : 3;
+    if ((d != one && d != one + 1) || !c.here(w) || w.scalar_type() != (ws ? kE4M3 : type) || w.numel() == 0 ||
+        w.size(d - 1) != k || (halves == 2 && w.size(d - 3) != 2) || (ws && !scales_fit(c, w, *ws, true)))
+        return false;
+    const int64_t groups = d > one ? w.size(0) : 1, n = w.size(d - 2);
+    const int64_t ld = n > 1 ? w.stride(d - 2) : halves == 2 ? w.stride(d - 3) : k;
+    if (groups > RR_MAX_EXPERTS || (w.stride(d - 1) != 1 && k > 1) || ld < k) return false;
+    if (halves == 2 && w.stride(d - 3) != n * ld) return false;
+    if (act < RR_ACT_NONE || act > (halves == 2 ? RR_ACT_SIGMOID : RR_ACT_SILU)) return false;
+    if (offsets ? !c.vector(*offsets, at::kInt, groups + 1) : rows % groups != 0) return false;
+    l.rows = (size_t)rows;
+    l.n = (size_t)n;
+    l.k = (size_t)k;
+    l.groups = (int32_t)groups;
+    l.dt = type_of(type);
+    l.act = (int32_t)act;
+    l.offsets = offsets ? ints(*offsets) : nullptr;
+    l.w = w.data_ptr();
+    l.w_ld = (size_t)ld;
+    l.w_stride = d > one ? (size_t)w.stride(0) : 0;
+    a.x_scales = xs ? (const float*)xs->data_ptr() : nullptr;
+    a.w_scales = ws ? (const float*)ws->data_ptr() : nullptr;
+    return d == one || w.stride(0) >= 0;
+}
+
+// x, x's scales, w, w's scales, bias, act, residual, offsets, save_preact, dtype
+PyObject* linear8(Args& a) {
+    const Tensor *x = a.needed(0), *xs = a.needed(1), *w = a.needed(2), *ws = a.needed(3), *bias = a.tensor(4);
+    const Tensor *residual = a.tensor(6), *offsets = a.tensor(7);
+    const long act = a.number(5);
+    const bool save = a.flag(8);
+    const auto type = type_named(a.number(9));
+    Call c;
+    rr_linear8_t l = {};
+    if (!a.good || !c.begin(*x) || !wide_args(c, *x, xs, *w, ws, offsets, act, type, 1, l)) return none();
+    const int64_t rows = (int64_t)l.l.rows, n = (int64_t)l.l.n;
+    if (bias && !c.ordered(*bias, type, {l.l.groups, n})) return none();
+    l.l.bias = bias ? bias->data_ptr() : nullptr;
+    if (residual && !c.matrix(*residual, type, rows, n, l.l.residual)) return none();
+    Tensor out = c.make_rows(rows, n, type, l.l.out), z;
+    if (save) z = c.make_rows(rows, n, type, l.l.z);
+    size_t bytes = 0;
+    if (block_linear8_workspace(&l, &bytes) != RR_OK) return none();
+    void* at;
+    Tensor work = c.scratch(bytes, at);
+    if (block_linear8(&l, at, bytes, c.stream) != RR_OK) return none();
+    return save ? tuple({out, z}) : wrap(out);
+}
+
+// The gradients by x, w and bias that are wanted.
+template <typename G>
+void make_grads(const Call& c, const Tensor& x, const Tensor& w, at::ScalarType type, at::ScalarType wide, bool need_dx,
+                bool need_dw, bool need_db, G& g, Tensor& dx, Tensor& dw, Tensor& db) {
+    if (need_dx) dx = c.make_rows(x.size(0), x.size(1), type, g.dx);
+    if (need_dw) {
+        dw = c.make(w.sizes(), wide);
+        g.dw = dw.data_ptr();
+    }
+    if (need_db) {
+        db = c.make(w.sizes().slice(0, (size_t)w.dim() - 1), at::kFloat);
+        g.db = (float*)db.data_ptr();
+    }
+    g.dw_dt = type_of(wide);
+}
+
+// dout, x, x's scales, w, w's scales, z, act, offsets, need_dx, need_dw, need_db, dw in fp32
+PyObject* linear8_backward(Args& a) {
+    const Tensor *dout = a.needed(0), *x = a.needed(1), *xs = a.tensor(2), *w = a.needed(3), *ws = a.tensor(4);
+    const Tensor *z = a.tensor(5), *offsets = a.tensor(7);
+    const long act = a.number(6);
+    const bool need_dx = a.flag(8), need_dw = a.flag(9), need_db = a.flag(10), wide_dw = a.flag(11);
+    Call c;
+    rr_linear8_t l = {};
+    rr_linear_grad_t g = {};
+    if (!a.good || !c.begin(*x)) return none();
+    const auto type = dout->scalar_type(), wide = wide_dw ? at::kFloat : type;
+    if (!wide_args(c, *x, xs, *w, ws, offsets, act, type, 1, l)) return none();
+    const int64_t rows = (int64_t)l.l.rows, n = (int64_t)l.l.n;
+    if (!c.matrix(*dout, type, rows, n, g.dout)) return none();
+    if (act != RR_ACT_NONE && (!z || !c.matrix(*z, type, rows, n, l.l.z))) return none();
+    Tensor dx, dw, db;
+    make_grads(c, *x, *w, type, wide, need_dx, need_dw, need_db, g, dx, dw, db);
+    size_t bytes = 0;
+    if (block_linear8_backward_workspace(&l, &g, &bytes) != RR_OK) return none();
+    void* at;
+    Tensor work = c.scratch(bytes, at);
+    if (block_linear8_backward(&l, &g, at, bytes, c.stream) != RR_OK) return none();
+    return tuple({dx, dw, db});
+}
+
+// x, x's scales, w, w's scales, bias, act, offsets, z (0 none, 1 in 16 bits, 2 in 8), dtype (0: x's)
+PyObject* gated(Args& a) {
+    const Tensor *x = a.needed(0), *xs = a.tensor(1), *w = a.needed(2), *ws = a.tensor(3), *bias = a.tensor(4);
+    const Tensor* offsets = a.tensor(6);
+    const long act = a.number(5), save = a.number(7), named = a.number(8);
+    Call c;
+    rr_linear8_t l = {};
+    if (!a.good || !c.begin(*x) || save < 0 || save > 2 || !xs != !ws) return none();
+    const auto type = named ? type_named(named) : xs ? at::kBFloat16 : x->scalar_type();
+    if (!wide_args(c, *x, xs, *w, ws, offsets, act, type, 2, l)) return none();
+    const int64_t rows = (int64_t)l.l.rows, n = (int64_t)l.l.n;
+    if (bias && !c.ordered(*bias, type, {l.l.groups, 2, n})) return none();
+    l.l.bias = bias ? bias->data_ptr() : nullptr;
+    Tensor out = c.make_rows(rows, n, type, l.l.out), z, scales;
+    if (save == 1) z = c.make_rows(rows, 2 * n, type, l.l.z);
+    if (save == 2) {
+        z = c.make({rows, 2, n}, kE4M3);
+        scales = c.make({rows, 2, blocks_of(n)}, at::kFloat);
+        l.l.z = {z.data_ptr(), (size_t)(2 * n)};
+        l.z_scales = (float*)scales.data_ptr();
+    }
+    size_t bytes = 0;
+    if (block_gated_workspace(&l, &bytes) != RR_OK) return none();
+    void* at;
+    Tensor work = c.scratch(bytes, at);
+    if (block_gated(&l, at, bytes, c.stream) != RR_OK) return none();
+    return save == 2 ? tuple({out, z, scales}) : save ? tuple({out, z}) : wrap(out);
+}
+
+// dout, x, x's scales, w, w's scales, z, z's scales, act, offsets, need_dx, need_dw, need_db,
+// need_out, dw in fp32
+PyObject* gated_backward(Args& a) {
+    const Tensor *dout = a.needed(0), *x = a.needed(1), *xs = a.tensor(2), *w = a.needed(3), *ws = a.tensor(4);
+    const Tensor *z = a.needed(5), *zs = a.tensor(6), *offsets = a.tensor(8);
+    const long act = a.number(7);
+    const bool need_dx = a.flag(9), need_dw = a.flag(10), need_db = a.flag(11), need_out = a.flag(12), wide_dw = a.flag(13);
+    Call c;
+    rr_linear8_t l = {};
+    rr_gated_grad_t g = {};
+    if (!a.good || !c.begin(*x)) return none();
+    const auto type = dout->scalar_type(), wide = wide_dw ? at::kFloat : type;
+    if (!wide_args(c, *x, xs, *w, ws, offsets, act, type, 2, l)) return none();
+    const int64_t rows = (int64_t)l.l.rows, n = (int64_t)l.l.n;
+    if (!c.matrix(*dout, type, rows, n, g.dout)) return none();
+    if (!zs) {
+        if (!c.matrix(*z, type, rows, 2 * n, l.l.z)) return none();
+    } else {
+        if (!c.here(*z) || z->scalar_type() != kE4M3 || !z->sizes().equals({rows, 2, n}) || !z->is_contiguous() ||
+            !scales_fit(c, *z, *zs, false))
+            return none();
+        l.l.z = {z->data_ptr(), (size_t)(2 * n)};
+        l.z_scales = (float*)zs->data_ptr();
+    }
+    Tensor dx, dw, db, out;
+    make_grads(c, *x, *w, type, wide, need_dx, need_dw, need_db, g, dx, dw, db);
+    if (need_out) out = c.make_rows(rows, n, type, g.out);
+    size_t bytes = 0;
+    if (block_gated_backward_workspace(&l, &g, &bytes) != RR_OK) return none();
+    void* at;
+    Tensor work = c.scratch(bytes, at);
+    if (block_gated_backward(&l, &g, at, bytes, c.stream) != RR_OK) return none();
+    return tuple({dx, dw, db, out});
+}
+
 // No C++ exception leaves the module: what torch throws becomes the Python error it stands for.
 template <PyObject* (*F)(Args&), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -406,6 +641,12 @@ PyMethodDef methods[] = {BLK_ENTRY("sort", sort, 3),
                          BLK_ENTRY("norm_backward", norm_backward, 14),
                          BLK_ENTRY("linear", linear, 7),
                          BLK_ENTRY("linear_backward", linear_backward, 10),
+                         BLK_ENTRY("quantize", quantize, 2),
+                         BLK_ENTRY("dequantize", dequantize, 4),
+                         BLK_ENTRY("linear8", linear8, 10),
+                         BLK_ENTRY("linear8_backward", linear8_backward, 12),
+                         BLK_ENTRY("gated", gated, 9),
+                         BLK_ENTRY("gated_backward", gated_backward, 14),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

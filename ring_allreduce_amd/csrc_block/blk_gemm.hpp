@@ -6,6 +6,8 @@
 //   dw       i = n,   j = k, c = row:  P = dz, Q = x           both contiguous along i, j
 #pragma once
 
+#include <type_traits>
+
 #include "blk_common.hpp"
 
 namespace blk {
@@ -43,6 +45,12 @@ struct GemmArgs {
                                      // the last round
     uint64_t part_stride;            // elements of one part
     int32_t slots, steps;            // of the last round (slots 0: as it is), see last_round_parts
+    // of a gated product: j is the columns of out, z and the parts have 2 j
+    uint64_t q_half;                 // elements from the gate's Q to the other projection's
+    // of 8-bit operands: a scale for each 128 of a row of P, and for 128 x 128 of Q
+    const float *p_scale, *q_scale;
+    int32_t blocks;                  // along the contraction
+    int32_t q_rows;                  // blocks of 128 rows in Q, each half of a gated one
 };
 
 // What the host chose for one product; see blk_linear.hip.
@@ -56,6 +64,12 @@ struct GemmPlan {
 
 rr_status_t launch_gemm_bf16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
 rr_status_t launch_gemm_f16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
+rr_status_t launch_gated_bf16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
+rr_status_t launch_gated_f16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
+rr_status_t launch_gemm8_bf16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
+rr_status_t launch_gemm8_f16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
+rr_status_t launch_gated8_bf16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
+rr_status_t launch_gated8_f16(const GemmArgs& a, const GemmPlan& p, hipStream_t s);
 
 // ------------------------------------------------------------------- groups --
 
@@ -318,6 +332,25 @@ template <typename T, bool ACROSS, int ROWS, int THREADS, bool PART> struct Dire
 #pragma clang diagnostic pop
 };
 
+// The rows of both halves of a gated product's Q, one behind the other in a tile.
+template <typename T, bool ACROSS, int ROWS, int THREADS, bool PART> struct Twin {
+    typedef Direct<T, ACROSS, ROWS / 2, THREADS, PART> D;
+    static constexpr int kPieces = 2 * D::kPieces;
+    D one, two;
+    __device__ __forceinline__ void start(const T* b, uint64_t half, uint64_t ld, int r0, int r_end, int c0, int end) {
+        one.start(b, ld, r0, r_end, c0, end);
+        two.start(b + half, ld, r0, r_end, c0, end);
+    }
+    __device__ __forceinline__ void aim(uint32_t tile) {
+        one.aim(tile);
+        two.aim(tile + Tile<ACROSS, ROWS / 2>::kBytes);
+    }
+    __device__ __forceinline__ void piece(int k) const {
+        if (k < D::kPieces) one.piece(k);
+        else two.piece(k - D::kPieces);
+    }
+};
+
 // This wave's loads into LDS but the last LATER are there and its reads of LDS are done,
 // then every wave's.
 template <int LATER> __device__ __forceinline__ void arrived() {
@@ -409,6 +442,37 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int group, int i, int 
     const uint64_t at = (a.out_group ? (uint64_t)group * a.out_group : 0) + (uint64_t)i * a.out_ld + j;
     finish<T, N>(a, group, a.j - j, v, bias_of<T, N>(a, group, j), r,
                  (T*)a.z + (uint64_t)i * a.z_ld + j, (char*)a.out + at * (a.wide_out ? 4 : sizeof(T)));
+}
+
+// Both halves' sums of N neighbouring columns: z = sums + bias, out = act(z gate) times z of the
+// other; zeros for a row of no group.  z and out: of the first of the columns.
+template <typename T, int N>
+__device__ __forceinline__ void finish_gated(const GemmArgs& a, int group, int n, float (&g)[N], float (&u)[N],
+                                             const Some<T, N>& g_bias, const Some<T, N>& u_bias, T* z, T* out) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        g[e] = group < 0 ? 0.0f : g[e] + (float)g_bias.e[e];
+        u[e] = group < 0 ? 0.0f : u[e] + (float)u_bias.e[e];
+    }
+    if (a.z) {
+        store_some<T, N>(z, n, g);
+        store_some<T, N>(z + a.j, n, u);
+    }
+    act_values(a.act, g);
+#pragma unroll
+    for (int e = 0; e < N; ++e) g[e] *= u[e];
+    store_some<T, N>(out, n, g);
+}
+template <typename T, int N>
+__device__ __forceinline__ Some<T, N> gated_bias_of(const GemmArgs& a, int group, int half, int j) {
+    if (!a.bias || group < 0 || j >= a.j) return Some<T, N>{};
+    return load_some<T, N>((const T*)a.bias + ((uint64_t)group * 2 + half) * a.j + j, a.j - j);
+}
+template <typename T, int N>
+__device__ __forceinline__ void finish_gated(const GemmArgs& a, int group, int i, int j, float (&g)[N], float (&u)[N]) {
+    if (j >= a.j) return;
+    finish_gated<T, N>(a, group, a.j - j, g, u, gated_bias_of<T, N>(a, group, 0, j), gated_bias_of<T, N>(a, group, 1, j),
+                       (T*)a.z + (uint64_t)i * a.z_ld + j, (T*)a.out + (uint64_t)i * a.out_ld + j);
 }
 
 // ------------------------------------------------------------- where a tile is --
@@ -581,6 +645,58 @@ __device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, BLK_
     }
 }
 
+// The same of a gated product: the tile's columns are TJ / 2 of the gate and the other
+// projection's behind them, so a thread finds both sums of its 8 columns in LDS.
+template <typename T, int TI, int TJ, int WI, int WJ, int FI, int FJ>
+__device__ __forceinline__ void write_gated(const GemmArgs& a, const Spot& s, BLK_LDS char* room,
+                                            const f32x4 (&acc)[FI][FJ]) {
+    constexpr int THREADS = 64 * WI * WJ, LINE = TJ + 4, ROWS = 16 * WI, HALF = TJ / 2, GROUPS = HALF / 8;
+    constexpr int BUFFER = ROWS * LINE;
+    static_assert(ROWS * GROUPS <= THREADS, "a thread has one piece of 16 rows a wave");
+    BLK_LDS float* const store = (BLK_LDS float*)room;
+    const int thread = here(), lane = thread & 63, wave = thread >> 6;
+    const bool whole = a.splits == 1;
+    if (!whole && s.g.group < 0) return;        // join_gated_kernel knows
+    if (thread >= THREADS) {                    // of another part: there for the barriers
+        for (int x = 0; x < FI; ++x) __syncthreads();
+        return;
+    }
+    const int col = thread % GROUPS * 8, r = thread / GROUPS, j = s.j0 + col, n = a.j - j;
+    const int row = r / 16 * (TI / WI) + r % 16, i = s.i0 + row;
+    const int left = r < ROWS && n > 0 ? s.i_end - i : 0;
+    const Some<T, 8> g_bias = whole ? gated_bias_of<T, 8>(a, s.g.group, 0, j) : Some<T, 8>{};
+    const Some<T, 8> u_bias = whole ? gated_bias_of<T, 8>(a, s.g.group, 1, j) : Some<T, 8>{};
+    float* const part = whole ? nullptr : a.part + (uint64_t)s.split * a.part_stride + (uint64_t)i * 2 * a.j + j;
+    T* const z = (T*)a.z + (uint64_t)i * a.z_ld + j;
+    T* const out = (T*)a.out + (uint64_t)i * a.out_ld + j;
+    for (int x = 0; x < FI; ++x) {
+        BLK_LDS float* const buf = store + (x & 1) * BUFFER;
+        BLK_LDS float* const mine = buf + (wave / WJ * 16 + (lane & 15)) * LINE + wave % WJ * (TJ / WJ) + (lane >> 4) * 4;
+#pragma unroll
+        for (int u = 0; u < FI; ++u)
+            if (u == x)
+#pragma unroll
+                for (int y = 0; y < FJ; ++y) *(BLK_LDS f32x4*)(mine + y * 16) = acc[u][y];
+        __syncthreads();
+        if (x * 16 >= left) continue;
+        const BLK_LDS float* const from = buf + r * LINE + col;
+        float g[8], u[8];
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+            const f32x4 gv = *(const BLK_LDS f32x4*)(from + h), uv = *(const BLK_LDS f32x4*)(from + HALF + h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[h + e] = gv[e], u[h + e] = uv[e];
+        }
+        const uint64_t down = (uint64_t)(x * 16);
+        if (!whole) {
+            store_wide<8>(part + down * 2 * a.j, n, g);
+            store_wide<8>(part + down * 2 * a.j + a.j, n, u);
+        } else {
+            finish_gated<T, 8>(a, s.g.group, n, g, u, g_bias, u_bias, z + down * a.z_ld, out + down * a.out_ld);
+        }
+    }
+}
+
 template <int N> struct Int {
     static constexpr int value = N;
 };
@@ -603,7 +719,10 @@ template <int N> struct Int {
 //
 // PARTS parts of the contraction are multiplied by as many sets of waves, whose sums meet in
 // LDS, so that few rows fill the device without a second launch that adds them up.
-template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ, int STAGES, int PARTS = 1>
+//
+// GATED: Q's tile is TJ / 2 rows of each of two matrices, for TJ / 2 columns of out.
+template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ, int STAGES, int PARTS = 1,
+          bool GATED = false>
 __global__ void __launch_bounds__(64 * WI * WJ * PARTS, STAGES * (TI + TJ) * kDepth * 2 > 81920 && WI * WJ == 4 ? 1 : 2)
 gemm_kernel(const GemmArgs a) {
     typedef typename Mma<T>::V V;
@@ -616,7 +735,7 @@ gemm_kernel(const GemmArgs a) {
     RowTiles rows = {};
     if constexpr (BY_ROWS) rows = count_tiles(a, TI);
     Spot s;
-    if (!find_spot<BY_ROWS, TI, TJ>(a, rows, blockIdx.x, s)) return;
+    if (!find_spot<BY_ROWS, TI, GATED ? TJ / 2 : TJ>(a, rows, blockIdx.x, s)) return;
     const T* const p = (const T*)a.p;
     const T* const q = (const T*)a.q + (BY_ROWS && s.g.group > 0 ? (uint64_t)s.g.group * a.q_group : 0);
     int wave = threadIdx.x >> 6, part = 0, tiles = (s.c_end - s.c0 + kDepth - 1) / kDepth;
@@ -644,12 +763,13 @@ gemm_kernel(const GemmArgs a) {
     // of P that are STAGES tiles ahead follow into the place just read, those of Q, which has
     // one place more, in the next tile's first half.
     typedef Direct<T, PA, TI, THREADS, (PARTS > 1)> DP;
-    typedef Direct<T, QA, TJ, THREADS, (PARTS > 1)> DQ;
+    typedef std::conditional_t<GATED, Twin<T, QA, TJ, THREADS, (PARTS > 1)>, Direct<T, QA, TJ, THREADS, (PARTS > 1)>> DQ;
     constexpr int PIECES = DP::kPieces + DQ::kPieces;
     DP lp;
     DQ lq;
     lp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
-    lq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
+    if constexpr (GATED) lq.start(q, a.q_half, a.q_ld, s.j0, a.j, s.c0, s.c_end);
+    else lq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
     V fp[2][FI], fq[2][FJ];
     // reads of the other half in the first part of the block rows, so that they are done
     // when the last ones are
@@ -726,7 +846,8 @@ gemm_kernel(const GemmArgs a) {
                 for (int m = 0; m < PARTS - 1; ++m) acc[f / FJ][f % FJ] += sums[m * EACH + f * 64];
         __syncthreads();
     }
-    write_out<T, BY_ROWS, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
+    if constexpr (GATED) write_gated<T, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
+    else write_out<T, BY_ROWS, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
 }
 
 // ------------------------------------------------------------ few rows: one pass --
@@ -763,7 +884,8 @@ template <typename T, int R, bool DIRECT> struct Strip {
         const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            const int c = c0 + s * 32 + (lane >> 4) * 8;
+            constexpr int N = Vec<T>::N;
+            const int c = c0 + s * 4 * N + (lane >> 4) * N;
 #pragma unroll
             for (int f = 0; f < R; ++f) {
                 if constexpr (DIRECT) {
@@ -773,7 +895,7 @@ template <typename T, int R, bool DIRECT> struct Strip {
                 } else {
                     Vec<T> t;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) t.e[e] = (T)0.0f;
+                    for (int e = 0; e < N; ++e) t.e[e] = (T)0.0f;
                     const int y = row + f * 16 + (lane & 15);
                     if (y < row_end && c < c_end) t = load_vec(base + (uint64_t)y * ld, c, c_end);
                     v[s][f] = __builtin_bit_cast(u32x4, t);
@@ -783,65 +905,11 @@ template <typename T, int R, bool DIRECT> struct Strip {
     }
 };
 
-template <typename T, int FI, int FJ, bool DIRECT>
-__global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArgs a) {
-    typedef typename Mma<T>::V V;
-    __shared__ f32x4 sums[kStreamWaves][FI * FJ][64];
-    Range g;
-    if (!find_tile(a, count_tiles(a, 16 * FI), (int)blockIdx.y, 16 * FI, g)) return;
-    g.group = __builtin_amdgcn_readfirstlane(g.group);
-    const int i0 = __builtin_amdgcn_readfirstlane(g.lo), i_end = __builtin_amdgcn_readfirstlane(g.hi);
-    const int j0 = (int)blockIdx.x * (16 * FJ), lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    int c_lo = 0, c_end = g.group < 0 ? 0 : a.c;
-    if (a.splits > 1) {
-        const int each = ((a.c + kStreamDepth - 1) / kStreamDepth + a.splits - 1) / a.splits * kStreamDepth;
-        c_lo = (int)min((int64_t)blockIdx.z * each, (int64_t)c_end);
-        c_end = (int)min((int64_t)c_lo + each, (int64_t)c_end);
-    }
-    Strip<T, FI, DIRECT> sp;
-    Strip<T, FJ, DIRECT> sq;
-    sp.start((const T*)a.p, a.p_ld, i0, i_end, c_end);
-    sq.start((const T*)a.q + (g.group > 0 ? (uint64_t)g.group * a.q_group : 0), a.q_ld, j0, a.j, c_end);
-    f32x4 acc[FI][FJ];
-#pragma unroll
-    for (int x = 0; x < FI; ++x)
-#pragma unroll
-        for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    u32x4 vp[4][FI], vq[4][FJ];
-    int c = c_lo + wave * kStreamDepth;
-    if (c < c_end) {
-        sq.load(vq, c);
-        sp.load(vp, c);
-    }
-    while (c < c_end) {
-        c += kStreamWaves * kStreamDepth;
-        u32x4 np[4][FI], nq[4][FJ];
-        if (c < c_end) {
-            sq.load(nq, c);
-            sp.load(np, c);
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int x = 0; x < FI; ++x)
-#pragma unroll
-                for (int y = 0; y < FJ; ++y)
-                    acc[x][y] = Mma<T>::run(__builtin_bit_cast(V, vq[s][y]),
-                                            __builtin_bit_cast(V, vp[s][x]), acc[x][y]);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-#pragma unroll
-            for (int x = 0; x < FI; ++x) vp[s][x] = np[s][x];
-#pragma unroll
-            for (int y = 0; y < FJ; ++y) vq[s][y] = nq[s][y];
-        }
-    }
-#pragma unroll
-    for (int x = 0; x < FI; ++x)
-#pragma unroll
-        for (int y = 0; y < FJ; ++y) sums[wave][x * FJ + y][lane] = acc[x][y];
-    __syncthreads();
+// The waves' sums, added in the order of the waves.
+template <typename T, int FI, int FJ>
+__device__ __forceinline__ void finish_stream_plain(const GemmArgs& a, int group, int i0, int i_end, int j0, int wave,
+                                                    const f32x4 (&sums)[kStreamWaves][FI * FJ][64]) {
+    const int lane = threadIdx.x & 63;
     for (int f = wave; f < FI * FJ; f += kStreamWaves) {
         f32x4 v = sums[0][f][lane];
 #pragma unroll
@@ -851,10 +919,101 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArg
         float o[4] = {v[0], v[1], v[2], v[3]};
         if (i >= i_end || j >= a.j) continue;
         if (a.splits == 1)
-            finish<T, 4>(a, g.group, i, j, o);
-        else if (g.group >= 0)
+            finish<T, 4>(a, group, i, j, o);
+        else if (group >= 0)
             store_wide<4>(a.part + (uint64_t)blockIdx.z * a.part_stride + (uint64_t)i * a.j + j, a.j - j, o);
     }
+}
+
+// The same of a gated product: 16 columns of each projection.
+template <typename T, int FI>
+__device__ __forceinline__ void finish_stream(const GemmArgs& a, int group, int i0, int i_end, int j0, int wave,
+                                              const f32x4 (&sums)[kStreamWaves][FI * 2][64]) {
+    const int lane = threadIdx.x & 63;
+    for (int f = wave; f < FI; f += kStreamWaves) {
+        f32x4 g = sums[0][f * 2][lane], u = sums[0][f * 2 + 1][lane];
+#pragma unroll
+        for (int w = 1; w < kStreamWaves; ++w) {
+            g += sums[w][f * 2][lane];
+            u += sums[w][f * 2 + 1][lane];
+        }
+        const int i = i0 + f * 16 + (lane & 15), j = j0 + (lane >> 4) * 4;
+        if (i >= i_end || j >= a.j) continue;
+        float gv[4] = {g[0], g[1], g[2], g[3]}, uv[4] = {u[0], u[1], u[2], u[3]};
+        if (a.splits == 1) {
+            finish_gated<T, 4>(a, group, i, j, gv, uv);
+        } else if (group >= 0) {
+            float* const to = a.part + (uint64_t)blockIdx.z * a.part_stride + (uint64_t)i * 2 * a.j + j;
+            store_wide<4>(to, a.j - j, gv);
+            store_wide<4>(to + a.j, a.j - j, uv);
+        }
+    }
+}
+
+// GATED (FJ 2): 16 columns of the gate and the same 16 of the other projection.
+template <typename T, int FI, int FJ, bool DIRECT, bool GATED = false>
+__global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArgs a) {
+    typedef typename Mma<T>::V V;
+    __shared__ f32x4 sums[kStreamWaves][FI * FJ][64];
+    Range g;
+    if (!find_tile(a, count_tiles(a, 16 * FI), (int)blockIdx.y, 16 * FI, g)) return;
+    g.group = __builtin_amdgcn_readfirstlane(g.group);
+    const int i0 = __builtin_amdgcn_readfirstlane(g.lo), i_end = __builtin_amdgcn_readfirstlane(g.hi);
+    constexpr int HALVES = GATED ? 2 : 1, EACH = FJ / HALVES;
+    const int j0 = (int)blockIdx.x * (16 * EACH), lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    int c_lo = 0, c_end = g.group < 0 ? 0 : a.c;
+    if (a.splits > 1) {
+        const int each = ((a.c + kStreamDepth - 1) / kStreamDepth + a.splits - 1) / a.splits * kStreamDepth;
+        c_lo = (int)min((int64_t)blockIdx.z * each, (int64_t)c_end);
+        c_end = (int)min((int64_t)c_lo + each, (int64_t)c_end);
+    }
+    Strip<T, FI, DIRECT> sp;
+    Strip<T, EACH, DIRECT> sq[HALVES];
+    sp.start((const T*)a.p, a.p_ld, i0, i_end, c_end);
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h)
+        sq[h].start((const T*)a.q + (g.group > 0 ? (uint64_t)g.group * a.q_group : 0) + h * a.q_half, a.q_ld, j0, a.j, c_end);
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int x = 0; x < FI; ++x)
+#pragma unroll
+        for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 vp[4][FI], vq[HALVES][4][EACH];
+    const auto load = [&](u32x4 (&to_p)[4][FI], u32x4 (&to_q)[HALVES][4][EACH], int at) {
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) sq[h].load(to_q[h], at);
+        sp.load(to_p, at);
+    };
+    int c = c_lo + wave * kStreamDepth;
+    if (c < c_end) load(vp, vq, c);
+    while (c < c_end) {
+        c += kStreamWaves * kStreamDepth;
+        u32x4 np[4][FI], nq[HALVES][4][EACH];
+        if (c < c_end) load(np, nq, c);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int x = 0; x < FI; ++x)
+#pragma unroll
+                for (int y = 0; y < FJ; ++y)
+                    acc[x][y] = Mma<T>::run(__builtin_bit_cast(V, vq[y / EACH][s][y % EACH]),
+                                            __builtin_bit_cast(V, vp[s][x]), acc[x][y]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+#pragma unroll
+            for (int x = 0; x < FI; ++x) vp[s][x] = np[s][x];
+#pragma unroll
+            for (int y = 0; y < FJ; ++y) vq[y / EACH][s][y % EACH] = nq[y / EACH][s][y % EACH];
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < FI; ++x)
+#pragma unroll
+        for (int y = 0; y < FJ; ++y) sums[wave][x * FJ + y][lane] = acc[x][y];
+    __syncthreads();
+    if constexpr (GATED) finish_stream<T, FI>(a, g.group, i0, i_end, j0, wave, sums);
+    else finish_stream_plain<T, FI, FJ>(a, g.group, i0, i_end, j0, wave, sums);
 }
 
 // -------------------------------------------------------- one to four rows: dots --
@@ -868,14 +1027,16 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(const GemmArg
 // 4: 46 against 27).
 constexpr int kDotWaves = 4;
 
-template <typename T, int M, int R>
+// GATED (R 2): the wave's rows are one of each projection.
+template <typename T, int M, int R, bool GATED = false>
 __global__ void __launch_bounds__(64 * kDotWaves) dot_kernel(const GemmArgs a) {
     const int lane = threadIdx.x & 63;
-    const int j0 = ((int)blockIdx.x * kDotWaves + (int)(threadIdx.x >> 6)) * R;
+    const int j0 = ((int)blockIdx.x * kDotWaves + (int)(threadIdx.x >> 6)) * (GATED ? 1 : R);
     if (j0 >= a.j) return;
     const T *w[R], *x[M];
 #pragma unroll
-    for (int r = 0; r < R; ++r) w[r] = (const T*)a.q + (uint64_t)min(j0 + r, a.j - 1) * a.q_ld;
+    for (int r = 0; r < R; ++r)
+        w[r] = (const T*)a.q + (GATED ? r * a.q_half + (uint64_t)j0 * a.q_ld : (uint64_t)min(j0 + r, a.j - 1) * a.q_ld);
 #pragma unroll
     for (int m = 0; m < M; ++m) x[m] = (const T*)a.p + (uint64_t)m * a.p_ld;
     float sum[M][R];
@@ -927,6 +1088,17 @@ __global__ void __launch_bounds__(64 * kDotWaves) dot_kernel(const GemmArgs a) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 sum[m][r] = fmaf((float)x[m][whole + lane], (float)w[r][whole + lane], sum[m][r]);
+    if constexpr (GATED) {
+        float g[1] = {0.0f}, u[1] = {0.0f};
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const float gate = lane_sum<64>(sum[m][0]), other = lane_sum<64>(sum[m][1]);
+            g[0] = lane == m ? gate : g[0];
+            u[0] = lane == m ? other : u[0];
+        }
+        if (lane < M) finish_gated<T, 1>(a, 0, lane, j0, g, u);
+        return;
+    }
     float mine = 0.0f;
 #pragma unroll
     for (int m = 0; m < M; ++m)
@@ -940,11 +1112,24 @@ __global__ void __launch_bounds__(64 * kDotWaves) dot_kernel(const GemmArgs a) {
     if (m < M && j < a.j) finish<T, 1>(a, 0, m, j, v);
 }
 
-template <typename T, int M, int R> static void launch_dot(const GemmArgs& a, hipStream_t s) {
-    dot_kernel<T, M, R><<<(unsigned)ceil_div(a.j, (uint64_t)R * kDotWaves), 64 * kDotWaves, 0, s>>>(a);
+template <typename T, int M, int R, bool GATED = false> static void launch_dot(const GemmArgs& a, hipStream_t s) {
+    const unsigned grid = (unsigned)ceil_div(a.j, (uint64_t)(GATED ? 1 : R) * kDotWaves);
+    dot_kernel<T, M, R, GATED><<<grid, 64 * kDotWaves, 0, s>>>(a);
 }
 
 // ----------------------------------------------------- parts of the contraction --
+
+// The group of a row of the products by rows; -1: none.
+__device__ __forceinline__ int group_of(const GemmArgs& a, int row) {
+    if (!a.offsets) return a.groups > 1 ? row / (a.rows / a.groups) : 0;
+    int lo = 0, hi = a.groups + 1;           // the first of the offsets beyond the row
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (a.offsets[mid] <= row) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo > a.groups ? -1 : lo - 1;
+}
 
 // Adds the parts in their order and finishes the rows: four columns a thread.
 template <typename T> __global__ void __launch_bounds__(256) join_kernel(const GemmArgs a, int by_rows) {
@@ -954,20 +1139,7 @@ template <typename T> __global__ void __launch_bounds__(256) join_kernel(const G
     const int j = (int)(id % wide) * 4;
     const uint64_t rows = by_rows ? (uint64_t)a.rows : (uint64_t)a.groups * a.i;
     if (row >= rows) return;
-    int group = 0;
-    if (!by_rows) {
-        group = (int)(row / a.i);
-    } else if (a.offsets) {
-        int lo = 0, hi = a.groups + 1;       // the first of the offsets beyond the row
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (a.offsets[mid] <= (int)row) lo = mid + 1;
-            else hi = mid;
-        }
-        group = lo > a.groups ? -1 : lo - 1;
-    } else if (a.groups > 1) {
-        group = (int)row / (a.rows / a.groups);
-    }
+    const int group = by_rows ? group_of(a, (int)row) : (int)(row / a.i);
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (group >= 0)
 #pragma unroll 8
@@ -978,6 +1150,29 @@ template <typename T> __global__ void __launch_bounds__(256) join_kernel(const G
             for (int e = 0; e < 4; ++e) v[e] += p.e[e];
         }
     finish<T, 4>(a, group, by_rows ? (int)row : (int)(row % a.i), j, v);
+}
+
+// The same of a gated product: four columns of out a thread.
+template <typename T> __global__ void __launch_bounds__(256) join_gated_kernel(const GemmArgs a) {
+    const unsigned wide = (unsigned)(a.j + 3) / 4;
+    const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint64_t row = id / wide;
+    const int j = (int)(id % wide) * 4;
+    if (row >= (uint64_t)a.rows) return;
+    const int group = group_of(a, (int)row);
+    float g[4] = {}, u[4] = {};
+    if (group >= 0)
+#pragma unroll 4
+        for (int s = 0; s < a.splits; ++s) {
+            const float* from = a.part + (uint64_t)s * a.part_stride + row * 2 * a.j + j;
+            const Some<float, 4> gp = load_some<float, 4>(from, a.j - j), up = load_some<float, 4>(from + a.j, a.j - j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g[e] += gp.e[e];
+                u[e] += up.e[e];
+            }
+        }
+    finish_gated<T, 4>(a, group, (int)row, j, g, u);
 }
 
 // Adds the parts of the last round's tiles: 32 rows a workgroup.
@@ -1072,6 +1267,47 @@ template <typename T> static rr_status_t launch_gemm(const GemmArgs& a, const Ge
     const uint64_t blocks = ceil_div(rows * ceil_div(a.j, 4), 256);
     join_kernel<T><<<(unsigned)blocks, 256, 0, s>>>(a, by_rows);
     return launched();
+}
+
+// The gated forward product.
+template <typename T, int TI, int TJ, int WI, int WJ, int STAGES, int PARTS = 1>
+static void launch_gated_tile(const GemmArgs& a, hipStream_t s) {
+    const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits;
+    gemm_kernel<T, false, false, true, TI, TJ, WI, WJ, STAGES, PARTS, true><<<grid, 64 * WI * WJ * PARTS, 0, s>>>(a);
+}
+template <typename T, int FI> static void launch_gated_stream(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
+    const dim3 grid((unsigned)a.tiles_j, (unsigned)a.tiles_i, (unsigned)a.splits);
+    if (p.direct) stream_kernel<T, FI, 2, true, true><<<grid, 64 * kStreamWaves, 0, s>>>(a);
+    else stream_kernel<T, FI, 2, false, true><<<grid, 64 * kStreamWaves, 0, s>>>(a);
+}
+template <typename T> static rr_status_t join_gated(const GemmArgs& a, hipStream_t s) {
+    const rr_status_t st = launched();
+    if (st != RR_OK || a.splits == 1) return st;
+    join_gated_kernel<T><<<(unsigned)ceil_div((uint64_t)a.rows * ceil_div(a.j, 4), 256), 256, 0, s>>>(a);
+    return launched();
+}
+template <typename T> static rr_status_t launch_gated(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
+    switch (p.tile) {
+        case kDot:
+            if (a.rows == 1) launch_dot<T, 1, 2, true>(a, s);
+            else if (a.rows == 2) launch_dot<T, 2, 2, true>(a, s);
+            else if (a.rows == 3) launch_dot<T, 3, 2, true>(a, s);
+            else launch_dot<T, 4, 2, true>(a, s);
+            break;
+        case kStream16: launch_gated_stream<T, 1>(a, p, s); break;
+        case kStream32: launch_gated_stream<T, 2>(a, p, s); break;
+        case kStream64: launch_gated_stream<T, 4>(a, p, s); break;
+        case kInner64: launch_gated_tile<T, 64, 32, 2, 1, 3, 4>(a, s); break;
+        case kTile256: launch_gated_tile<T, 256, 256, 2, 4, 2>(a, s); break;
+        case kTile128:
+            if (p.deep) launch_gated_tile<T, 128, 128, 2, 2, 4>(a, s);
+            else launch_gated_tile<T, 128, 128, 2, 2, 2>(a, s);
+            break;
+        default:
+            if (p.deep) launch_gated_tile<T, 64, 64, 2, 2, 4>(a, s);
+            else launch_gated_tile<T, 64, 64, 2, 2, 2>(a, s);
+    }
+    return join_gated<T>(a, s);
 }
 
 }  // namespace blk

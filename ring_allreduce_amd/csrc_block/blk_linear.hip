@@ -1,7 +1,7 @@
 // blk_linear.hip -- the entry points of a block's matrix products (block_linear,
 // block_linear_backward): the choice of kernel for each product, the gradient of the
 // activation, and the checks.  The products themselves: blk_gemm.hpp.
-#include "blk_gemm.hpp"
+#include "blk_product.hpp"
 
 namespace blk {
 
@@ -141,37 +141,39 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
 
 // ------------------------------------------------------------------ host side --
 
-constexpr uint64_t kMaxSize = 0x7FFFFFFFull - 1024;
-constexpr uint64_t kMaxLd = 1ull << 22;
-
-static bool rows_ok(const rr_rows_t& r, uint64_t rows, uint64_t width, uint64_t bytes) {
-    return rows == 0 || (r.data && aligned_to(r.data, bytes) && r.ld >= width);
-}
-static bool rows_ok_if(const rr_rows_t& r, uint64_t rows, uint64_t width, uint64_t bytes) {
-    return !r.data || rows_ok(r, rows, width, bytes);
-}
-
-static rr_status_t check_linear(const rr_linear_t* a) {
+// All of it but the activation; the bytes of an element of x and of w.
+rr_status_t check_linear_sizes(const rr_linear_t* a, uint64_t x_bytes, uint64_t w_bytes) {
     if (!a || a->reserved) return RR_ERR_INVALID;
     if (a->dt != RR_BF16 && a->dt != RR_FP16)
         return a->dt == RR_FP32 ? RR_ERR_UNSUPPORTED : RR_ERR_INVALID;
     if (a->n < 1 || a->k < 1 || a->groups < 1) return RR_ERR_INVALID;
-    if (a->act < RR_ACT_NONE || a->act > RR_ACT_SILU) return RR_ERR_INVALID;
     if (a->rows > kMaxSize || a->n > kMaxSize || a->k > kMaxSize || a->groups > RR_MAX_EXPERTS)
         return RR_ERR_UNSUPPORTED;
     if (!a->offsets && a->rows % (uint64_t)a->groups) return RR_ERR_INVALID;
     if (!aligned_to(a->offsets, 4)) return RR_ERR_INVALID;
-    if (!a->w || !aligned_to(a->w, 2) || a->w_ld < a->k) return RR_ERR_INVALID;
+    if (!a->w || !aligned_to(a->w, w_bytes) || a->w_ld < a->k) return RR_ERR_INVALID;
     if (a->groups > 1 && a->w_stride < extent(a->n, a->w_ld, a->k, 1)) return RR_ERR_INVALID;
-    if (!rows_ok(a->x, a->rows, a->k, 2) || !rows_ok_if(a->z, a->rows, a->n, 2))
-        return RR_ERR_INVALID;
+    if (!rows_ok(a->x, a->rows, a->k, x_bytes)) return RR_ERR_INVALID;
     if (a->x.ld > kMaxLd || a->w_ld > kMaxLd) return RR_ERR_UNSUPPORTED;
     if (a->groups > 1 && a->w_stride > (1ull << 44)) return RR_ERR_UNSUPPORTED;
     return RR_OK;
 }
 
-static rr_status_t check_grad(const rr_linear_t* a, const rr_linear_grad_t* g) {
-    const rr_status_t st = check_linear(a);
+static rr_status_t check_linear(const rr_linear_t* a, uint64_t x_bytes = 2, uint64_t w_bytes = 2) {
+    const rr_status_t st = check_linear_sizes(a, x_bytes, w_bytes);
+    if (st == RR_ERR_INVALID) return st;
+    if (a->act < RR_ACT_NONE || a->act > RR_ACT_SILU) return RR_ERR_INVALID;
+    if (!rows_ok_if(a->z, a->rows, a->n, 2)) return RR_ERR_INVALID;
+    return st;
+}
+
+// The scales of 8-bit operands; none: 16 bits.
+struct Eight {
+    const float *x, *w;
+};
+
+static rr_status_t check_grad(const rr_linear_t* a, const rr_linear_grad_t* g, const Eight& e) {
+    const rr_status_t st = check_linear(a, e.x ? 1 : 2, e.w ? 1 : 2);
     if (st != RR_OK) return st;
     if (!g || g->reserved) return RR_ERR_INVALID;
     if (g->dw_dt != a->dt && g->dw_dt != RR_FP32) return RR_ERR_INVALID;
@@ -179,11 +181,12 @@ static rr_status_t check_grad(const rr_linear_t* a, const rr_linear_grad_t* g) {
         return RR_ERR_INVALID;
     if (a->act != RR_ACT_NONE && !rows_ok(a->z, a->rows, a->n, 2)) return RR_ERR_INVALID;
     if (!aligned_to(g->dw, type_bytes(g->dw_dt)) || !aligned_to(g->db, 4)) return RR_ERR_INVALID;
+    if (!aligned_to(e.x, 4) || !aligned_to(e.w, 4)) return RR_ERR_INVALID;
     if (g->dout.ld > kMaxLd || (g->dx.data && g->dx.ld > kMaxLd) || (a->act != RR_ACT_NONE && a->n > kMaxLd)) return RR_ERR_UNSUPPORTED;
     return RR_OK;
 }
 
-static GemmArgs groups_of(const rr_linear_t* a) {
+GemmArgs groups_of(const rr_linear_t* a) {
     GemmArgs k = {};
     k.rows = (int32_t)a->rows;
     k.groups = a->groups;
@@ -193,16 +196,10 @@ static GemmArgs groups_of(const rr_linear_t* a) {
 
 // Row tiles of all groups, at most: each that has rows can add one partly filled, and so can
 // the rows before the first and after the last one.
-static uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
+uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
     if (a->groups == 1 && !a->offsets) return ceil_div(a->rows, height);
     const uint64_t ranges = (uint64_t)a->groups + 2;
     return a->rows / height + (a->rows < ranges ? a->rows : ranges);
-}
-
-// An operand of 16-byte pieces: its rows start at them and, where the pieces lie along the
-// contraction, end at them too (past a row's end there may be anything).
-static bool good_rows(const rr_rows_t& r, uint64_t group, uint64_t width) {
-    return aligned_to(r.data, 16) && r.ld % 8 == 0 && group % 8 == 0 && width % 8 == 0;
 }
 
 // The kernel and the parts of the contraction for one product: the least of the times that
@@ -227,7 +224,7 @@ static bool good_rows(const rr_rows_t& r, uint64_t group, uint64_t width) {
 // against 25; the tiles only for whole 16-byte pieces, copies of the weights would cost more).
 constexpr unsigned kSlots = 256;      // 256 x 256 tiles that a device takes at once: one a compute unit
 
-static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) {
+GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) {
     const uint64_t groups = (uint64_t)a->groups, mean = ceil_div(a->rows, groups);
     const uint64_t i = form == kByW ? a->n : a->rows, j = form == kForward ? a->n : a->k;
     const uint64_t c = form == kForward ? a->k : form == kByX ? a->n : mean;
@@ -312,23 +309,7 @@ static GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) 
     return p;
 }
 
-struct Operand {
-    rr_rows_t rows;
-    uint64_t count, width, groups, group;  // rows of a group, row length, groups and their distance
-    bool good() const { return good_rows(rows, groups > 1 ? group : 0, width); }
-    uint64_t copy_bytes() const {
-        return ceil_div(groups * count * ceil_div(width, 8) * 16, 256) * 256;
-    }
-};
-
-// One product: `k` has the sizes and the epilogue.
-struct Product {
-    int form;
-    Operand p, q;
-    GemmArgs k;
-};
-
-static uint64_t product_bytes(const rr_linear_t* a, int form, const Operand& p, const Operand& q) {
+uint64_t product_bytes(const rr_linear_t* a, int form, const Operand& p, const Operand& q) {
     int splits, slots;
     const GemmPlan plan = choose(a, form, &splits, &slots);
     uint64_t bytes = (uint64_t)slots * 256 * 256 * sizeof(float);
@@ -341,12 +322,34 @@ static uint64_t product_bytes(const rr_linear_t* a, int form, const Operand& p, 
 }
 
 // Copies the operands that are not good into the scratch memory at `room`.
-static rr_status_t pack(Operand& p, Operand& q, char* room, hipStream_t s) {
+static rr_status_t pack(int dt, Operand& p, Operand& q, char* room, hipStream_t s) {
     PackArgs k = {};
     int n = 0;
     uint64_t blocks = 0;
     for (Operand* o : {&p, &q}) {
         if (o->good()) continue;
+        if (o->scales) {
+            BlockArgs b = {};
+            b.wide = room;
+            b.wide_ld = ceil_div(o->width, 8) * 8;
+            b.wide_group = o->count * b.wide_ld;
+            b.narrow = (uint8_t*)o->rows.data;
+            b.narrow_ld = o->rows.ld;
+            b.narrow_group = o->group;
+            b.scales = const_cast<float*>(o->scales);
+            b.rows = o->count;
+            b.groups = o->groups;
+            b.part = o->part;
+            b.width = (int32_t)o->width;
+            b.blocks = (int32_t)ceil_div(o->width, kBlock);
+            b.filled = (int32_t)b.wide_ld;
+            b.high = (int32_t)o->high;
+            const rr_status_t st = launch_back(b, dt, s);
+            if (st != RR_OK) return st;
+            room += o->copy_bytes();
+            *o = {{b.wide, b.wide_ld}, o->count, b.wide_ld, o->groups, b.wide_group};
+            continue;
+        }
         PackPart& m = k.part[n];
         m = {o->rows.data, room, o->rows.ld, o->group, 0, (int32_t)o->count, (int32_t)o->width,
              (int32_t)(ceil_div(o->width, 8) * 8)};
@@ -366,7 +369,7 @@ static rr_status_t pack(Operand& p, Operand& q, char* room, hipStream_t s) {
     return launched();
 }
 
-static rr_status_t run_product(const rr_linear_t* a, Product r, void* workspace, hipStream_t s) {
+rr_status_t run_product(const rr_linear_t* a, Product r, void* workspace, hipStream_t s) {
     GemmArgs& k = r.k;
     int splits, slots;
     GemmPlan plan = choose(a, r.form, &splits, &slots);
@@ -396,7 +399,7 @@ static rr_status_t run_product(const rr_linear_t* a, Product r, void* workspace,
         k.splits = 1;
     }
     if (plan.tile < kStream16) {
-        const rr_status_t st = pack(r.p, r.q, room, s);
+        const rr_status_t st = pack(a->dt, r.p, r.q, room, s);
         if (st != RR_OK) return st;
     }
     k.p = r.p.rows.data;
@@ -407,10 +410,10 @@ static rr_status_t run_product(const rr_linear_t* a, Product r, void* workspace,
     return a->dt == RR_BF16 ? launch_gemm_bf16(k, plan, s) : launch_gemm_f16(k, plan, s);
 }
 
-static Operand rows_of(const rr_linear_t* a, const rr_rows_t& r, uint64_t width) {
+Operand rows_of(const rr_linear_t* a, const rr_rows_t& r, uint64_t width) {
     return {r, a->rows, width, 1, 0};
 }
-static Operand weights_of(const rr_linear_t* a) {
+Operand weights_of(const rr_linear_t* a) {
     return {{const_cast<void*>(a->w), a->w_ld}, a->n, a->k, (uint64_t)a->groups, a->w_stride};
 }
 
@@ -432,7 +435,20 @@ static uint64_t splits_of(const rr_linear_t* a) {
 struct BackwardPlan {
     uint64_t dz, part, product;  // bytes of scratch
 };
-static BackwardPlan plan_of(const rr_linear_t* a, const rr_linear_grad_t* g) {
+static Operand x_of(const rr_linear_t* a, const Eight& e) {
+    Operand o = rows_of(a, a->x, a->k);
+    o.scales = e.x;
+    o.part = a->rows;
+    return o;
+}
+static Operand w_of(const rr_linear_t* a, const Eight& e) {
+    Operand o = weights_of(a);
+    o.scales = e.w;
+    o.high = kBlock;
+    o.part = a->n;
+    return o;
+}
+static BackwardPlan plan_of(const rr_linear_t* a, const rr_linear_grad_t* g, const Eight& e) {
     BackwardPlan p = {0, 0, 0};
     const Operand dout = rows_of(a, g->dout, a->n);
     if ((g->dx.data || g->dw) && (a->act != RR_ACT_NONE || !dout.good())) p.dz = dout.copy_bytes();
@@ -440,12 +456,102 @@ static BackwardPlan plan_of(const rr_linear_t* a, const rr_linear_grad_t* g) {
     Operand dz = dout;
     if (p.dz) dz.rows = {nullptr, ceil_div(a->n, 8) * 8};
     dz.width = ceil_div(a->n, 8) * 8;       // good rows, or a copy with zeros behind each
-    if (g->dx.data) p.product = product_bytes(a, kByX, dz, weights_of(a));
+    if (g->dx.data) p.product = product_bytes(a, kByX, dz, w_of(a, e));
     if (g->dw) {
-        const uint64_t bytes = product_bytes(a, kByW, dz, rows_of(a, a->x, a->k));
+        const uint64_t bytes = product_bytes(a, kByW, dz, x_of(a, e));
         if (bytes > p.product) p.product = bytes;
     }
     return p;
+}
+
+static rr_status_t backward_bytes(const rr_linear_t* a, const rr_linear_grad_t* g, const Eight& e, size_t* bytes) {
+    if (!bytes) return RR_ERR_INVALID;
+    const rr_status_t st = check_grad(a, g, e);
+    if (st != RR_OK) return st;
+    const BackwardPlan p = plan_of(a, g, e);
+    *bytes = p.dz + p.part + p.product;
+    return RR_OK;
+}
+
+static rr_status_t backward(const rr_linear_t* a, const rr_linear_grad_t* g, const Eight& e,
+                            void* workspace, size_t workspace_bytes, hipStream_t s) {
+    rr_status_t st = check_grad(a, g, e);
+    if (st != RR_OK) return st;
+    const BackwardPlan plan = plan_of(a, g, e);
+    const uint64_t need = plan.dz + plan.part + plan.product;
+    if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need))
+        return RR_ERR_INVALID;
+    const uint64_t blocks = ceil_div(a->k, kBlock);
+    const struct { const void* p; uint64_t n; } in[] = {
+        {g->dout.data, extent(a->rows, g->dout.ld, a->n, 2)},
+        {a->x.data, extent(a->rows, a->x.ld, a->k, e.x ? 1 : 2)}, {a->w, weights_extent(a, e.w ? 1 : 2)},
+        {e.x, a->rows * blocks * 4}, {e.w, (uint64_t)a->groups * ceil_div(a->n, kBlock) * blocks * 4},
+        {a->act != RR_ACT_NONE ? a->z.data : nullptr, extent(a->rows, a->z.ld, a->n, 2)},
+        {a->offsets, (uint64_t)(a->groups + 1) * 4}},
+    out[] = {
+        {g->dx.data, extent(a->rows, g->dx.ld, a->k, 2)},
+        {g->dw, (uint64_t)a->groups * a->n * a->k * type_bytes(g->dw_dt)},
+        {g->db, (uint64_t)a->groups * a->n * 4}, {workspace, need}};
+    for (int o = 0; o < 4; ++o) {
+        for (const auto& i : in)
+            if (overlap(out[o].p, out[o].n, i.p, i.n)) return RR_ERR_INVALID;
+        for (int q = o + 1; q < 4; ++q)
+            if (overlap(out[o].p, out[o].n, out[q].p, out[q].n)) return RR_ERR_INVALID;
+    }
+    rr_rows_t dz = g->dout;
+    void* const room = (char*)workspace + plan.dz + plan.part;
+    if (plan.dz || g->db) {
+        SlopeArgs k = {};
+        k.g = groups_of(a);
+        k.dout = g->dout.data;
+        k.dout_ld = g->dout.ld;
+        k.z = a->z.data;
+        k.z_ld = a->z.ld;
+        k.n = (int32_t)a->n;
+        k.act = a->act;
+        k.splits = (int32_t)splits_of(a);
+        k.threads = (int32_t)slope_threads(a);
+        if (plan.dz) {
+            dz = {workspace, ceil_div(a->n, 8) * 8};
+            k.dz = dz.data;
+            k.dz_ld = dz.ld;
+        }
+        k.part = plan.part ? (float*)((char*)workspace + plan.dz) : g->db;
+        const uint64_t cols = ceil_div(a->n, (uint64_t)k.threads * 8);
+        if (cols > (1u << 24) - 1) return RR_ERR_UNSUPPORTED;
+        const dim3 grid((unsigned)cols, (unsigned)k.splits, (unsigned)a->groups);
+        if (a->dt == RR_BF16)
+            slope_kernel<bf16><<<grid, 256, 0, s>>>(k);
+        else
+            slope_kernel<f16><<<grid, 256, 0, s>>>(k);
+        if ((st = launched()) != RR_OK) return st;
+        if (plan.part) {
+            const dim3 sums((unsigned)ceil_div(a->n, 16), (unsigned)a->groups);
+            slope_parts_kernel<<<sums, 256, 0, s>>>(k.part, k.splits, k.n, g->db);
+            if ((st = launched()) != RR_OK) return st;
+        }
+    }
+    Operand by = rows_of(a, dz, ceil_div(a->n, 8) * 8);     // zeros behind the columns, if any
+    if (g->dx.data && a->rows) {
+        Product r = {kByX, by, w_of(a, e), groups_of(a)};
+        r.k.i = (int32_t)a->rows;
+        r.k.j = (int32_t)a->k;
+        r.k.c = (int32_t)a->n;
+        r.k.out = g->dx.data;
+        r.k.out_ld = g->dx.ld;
+        if ((st = run_product(a, r, room, s)) != RR_OK) return st;
+    }
+    if (g->dw) {
+        Product r = {kByW, by, x_of(a, e), groups_of(a)};
+        r.k.i = (int32_t)a->n;
+        r.k.j = (int32_t)a->k;
+        r.k.out = g->dw;
+        r.k.out_ld = a->k;
+        r.k.out_group = (uint64_t)a->n * a->k;
+        r.k.wide_out = g->dw_dt == RR_FP32;
+        if ((st = run_product(a, r, room, s)) != RR_OK) return st;
+    }
+    return RR_OK;
 }
 
 }  // namespace blk
@@ -513,93 +619,24 @@ rr_status_t block_linear(const rr_linear_t* a, void* workspace, size_t workspace
 
 rr_status_t block_linear_backward_workspace(const rr_linear_t* a, const rr_linear_grad_t* g,
                                             size_t* bytes) {
-    if (!bytes) return RR_ERR_INVALID;
-    const rr_status_t st = check_grad(a, g);
-    if (st != RR_OK) return st;
-    const BackwardPlan p = plan_of(a, g);
-    *bytes = p.dz + p.part + p.product;
-    return RR_OK;
+    return backward_bytes(a, g, {nullptr, nullptr}, bytes);
 }
 
 rr_status_t block_linear_backward(const rr_linear_t* a, const rr_linear_grad_t* g,
                                   void* workspace, size_t workspace_bytes, rr_stream_t stream) {
-    rr_status_t st = check_grad(a, g);
-    if (st != RR_OK) return st;
-    const BackwardPlan plan = plan_of(a, g);
-    const uint64_t need = plan.dz + plan.part + plan.product;
-    if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need))
-        return RR_ERR_INVALID;
-    const uint64_t w_bytes = extent(a->groups, a->w_stride, extent(a->n, a->w_ld, a->k, 1), 2);
-    const struct { const void* p; uint64_t n; } in[] = {
-        {g->dout.data, extent(a->rows, g->dout.ld, a->n, 2)},
-        {a->x.data, extent(a->rows, a->x.ld, a->k, 2)}, {a->w, w_bytes},
-        {a->act != RR_ACT_NONE ? a->z.data : nullptr, extent(a->rows, a->z.ld, a->n, 2)},
-        {a->offsets, (uint64_t)(a->groups + 1) * 4}},
-    out[] = {
-        {g->dx.data, extent(a->rows, g->dx.ld, a->k, 2)},
-        {g->dw, (uint64_t)a->groups * a->n * a->k * type_bytes(g->dw_dt)},
-        {g->db, (uint64_t)a->groups * a->n * 4}, {workspace, need}};
-    for (int o = 0; o < 4; ++o) {
-        for (const auto& i : in)
-            if (overlap(out[o].p, out[o].n, i.p, i.n)) return RR_ERR_INVALID;
-        for (int q = o + 1; q < 4; ++q)
-            if (overlap(out[o].p, out[o].n, out[q].p, out[q].n)) return RR_ERR_INVALID;
-    }
-    hipStream_t s = (hipStream_t)stream;
-    rr_rows_t dz = g->dout;
-    void* const room = (char*)workspace + plan.dz + plan.part;
-    if (plan.dz || g->db) {
-        SlopeArgs k = {};
-        k.g = groups_of(a);
-        k.dout = g->dout.data;
-        k.dout_ld = g->dout.ld;
-        k.z = a->z.data;
-        k.z_ld = a->z.ld;
-        k.n = (int32_t)a->n;
-        k.act = a->act;
-        k.splits = (int32_t)splits_of(a);
-        k.threads = (int32_t)slope_threads(a);
-        if (plan.dz) {
-            dz = {workspace, ceil_div(a->n, 8) * 8};
-            k.dz = dz.data;
-            k.dz_ld = dz.ld;
-        }
-        k.part = plan.part ? (float*)((char*)workspace + plan.dz) : g->db;
-        const uint64_t cols = ceil_div(a->n, (uint64_t)k.threads * 8);
-        if (cols > (1u << 24) - 1) return RR_ERR_UNSUPPORTED;
-        const dim3 grid((unsigned)cols, (unsigned)k.splits, (unsigned)a->groups);
-        if (a->dt == RR_BF16)
-            slope_kernel<bf16><<<grid, 256, 0, s>>>(k);
-        else
-            slope_kernel<f16><<<grid, 256, 0, s>>>(k);
-        if ((st = launched()) != RR_OK) return st;
-        if (plan.part) {
-            const dim3 sums((unsigned)ceil_div(a->n, 16), (unsigned)a->groups);
-            slope_parts_kernel<<<sums, 256, 0, s>>>(k.part, k.splits, k.n, g->db);
-            if ((st = launched()) != RR_OK) return st;
-        }
-    }
-    Operand by = rows_of(a, dz, ceil_div(a->n, 8) * 8);     // zeros behind the columns, if any
-    if (g->dx.data && a->rows) {
-        Product r = {kByX, by, weights_of(a), groups_of(a)};
-        r.k.i = (int32_t)a->rows;
-        r.k.j = (int32_t)a->k;
-        r.k.c = (int32_t)a->n;
-        r.k.out = g->dx.data;
-        r.k.out_ld = g->dx.ld;
-        if ((st = run_product(a, r, room, s)) != RR_OK) return st;
-    }
-    if (g->dw) {
-        Product r = {kByW, by, rows_of(a, a->x, a->k), groups_of(a)};
-        r.k.i = (int32_t)a->n;
-        r.k.j = (int32_t)a->k;
-        r.k.out = g->dw;
-        r.k.out_ld = a->k;
-        r.k.out_group = (uint64_t)a->n * a->k;
-        r.k.wide_out = g->dw_dt == RR_FP32;
-        if ((st = run_product(a, r, room, s)) != RR_OK) return st;
-    }
-    return RR_OK;
+    return backward(a, g, {nullptr, nullptr}, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+rr_status_t block_linear8_backward_workspace(const rr_linear8_t* a, const rr_linear_grad_t* g,
+                                             size_t* bytes) {
+    if (!a || a->z_scales) return RR_ERR_INVALID;
+    return backward_bytes(&a->l, g, {a->x_scales, a->w_scales}, bytes);
+}
+
+rr_status_t block_linear8_backward(const rr_linear8_t* a, const rr_linear_grad_t* g,
+                                   void* workspace, size_t workspace_bytes, rr_stream_t stream) {
+    if (!a || a->z_scales) return RR_ERR_INVALID;
+    return backward(&a->l, g, {a->x_scales, a->w_scales}, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
 }  // extern "C"

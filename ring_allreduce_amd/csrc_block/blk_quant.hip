@@ -1,0 +1,296 @@
+// blk_quant.hip -- values to 8 bits with a scale for each block of 128, and back
+// (block_quantize, block_dequantize).
+//
+// Bound by memory: e bytes in and 1 + 4 / 128 out a value, or the other way round.
+#include "blk_product.hpp"
+
+namespace blk {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// 8 neighbouring columns in 32 bits.
+template <typename T> struct Eight {
+    static constexpr int RAWS = sizeof(T) / 2;
+    u32x4 raw[RAWS];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int r = 0; r < RAWS; ++r) raw[r] = load_raw(p + r * Vec<T>::N);
+    }
+    __device__ __forceinline__ void load_some(const T* row, int at, int len) {
+#pragma unroll
+        for (int r = 0; r < RAWS; ++r)
+            raw[r] = __builtin_bit_cast(u32x4, load_vec(row, at + r * Vec<T>::N, len));
+    }
+    __device__ __forceinline__ float value(int e) const {
+        return (float)vec_of<T>(raw[e / Vec<T>::N]).e[e % Vec<T>::N];
+    }
+    // the largest finite magnitude
+    __device__ __forceinline__ float size() const {
+        float a = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float v = fabsf(value(e));
+            a = fmaxf(a, v < INFINITY ? v : 0.0f);
+        }
+        return a;
+    }
+    // in e4m3, times 2^-p: exact but for the rounding to e4m3
+    __device__ __forceinline__ u32x2 narrow(float inverse) const {
+        u32x2 v;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[e] = value(h * 4 + e);
+                f[e] = fabsf(f[e]) < INFINITY ? f[e] * inverse : NAN;
+            }
+            int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+            w = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
+            v[h] = (uint32_t)w;
+        }
+        return v;
+    }
+};
+
+// The least power of two p with a / p <= 448 = 1.75 * 2^8, at least 2^-126; 1 for 0.  Its
+// exponent is a's less 8, or less 7 where a's mantissa is over 1.75.
+__device__ __forceinline__ float scale_of(float a) {
+    const uint32_t bits = __builtin_bit_cast(uint32_t, a);
+    const int e = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFF) > 0x600000);
+    return a == 0.0f ? 1.0f : __builtin_bit_cast(float, (uint32_t)max(e, 1) << 23);
+}
+// 1 / p: exponents 254 - e of e = 1 .. 247
+__device__ __forceinline__ float inverse_of(float scale) {
+    return __builtin_bit_cast(float, 0x7F000000u - __builtin_bit_cast(uint32_t, scale));
+}
+
+__device__ __forceinline__ void store_eight(uint8_t* row, int at, int len, u32x2 v) {
+    if (at + 8 <= len) {
+        ((LooseWords<uint8_t, 8>*)(row + at))->v = v;
+    } else {
+        for (int e = 0; at + e < len; ++e) row[at + e] = (uint8_t)(v[e >> 2] >> (e & 3) * 8);
+    }
+}
+
+__device__ __forceinline__ float largest_of_16_lanes(float a) {
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor(a, d));
+    return a;
+}
+
+// 16 lanes a block of a row.
+template <typename T> __global__ void __launch_bounds__(256) quantize_rows_kernel(const BlockArgs a) {
+    const int lane = threadIdx.x & 15;
+    const uint64_t all = a.groups * a.rows * (uint64_t)a.blocks;
+    for (uint64_t id = (uint64_t)blockIdx.x * 16 + (threadIdx.x >> 4); id < all; id += (uint64_t)gridDim.x * 16) {
+        const uint64_t line = id / (uint32_t)a.blocks;
+        const int col = (int)(id - line * (uint32_t)a.blocks) * 128 + lane * 8;
+        const uint64_t group = a.groups > 1 ? line / a.rows : 0, row = line - group * a.rows;
+        const T* from = (const T*)a.wide + group * a.wide_group + row * a.wide_ld;
+        Eight<T> v;
+        if (col + 8 <= a.width) v.load(from + col);
+        else v.load_some(from, col, a.width);
+        const float scale = scale_of(largest_of_16_lanes(v.size()));
+        if (col < a.width)
+            store_eight(a.narrow + group * a.narrow_group + row * a.narrow_ld, col, a.width, v.narrow(inverse_of(scale)));
+        if (lane == 0) a.scales[id] = scale;
+    }
+}
+
+// A workgroup a block of 128 x 128.
+template <typename T> __global__ void __launch_bounds__(256) quantize_square_kernel(const BlockArgs a) {
+    __shared__ float lds[4];
+    const int lane = threadIdx.x & 15, y = threadIdx.x >> 4, high = (int)((a.rows + 127) / 128);
+    const uint64_t line = blockIdx.x / (uint32_t)a.blocks, group = line / (uint32_t)high;
+    const int col = (int)(blockIdx.x % (uint32_t)a.blocks) * 128 + lane * 8;
+    const uint64_t row0 = (line - group * high) * 128;
+    Eight<T> v[8];
+    float size = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint64_t row = row0 + k * 16 + y;
+        const T* from = (const T*)a.wide + group * a.wide_group + min(row, a.rows - 1) * a.wide_ld;
+        if (col + 8 <= a.width) v[k].load(from + col);
+        else v[k].load_some(from, col, a.width);
+    }
+    // rows past the end are the last one again
+#pragma unroll
+    for (int k = 0; k < 8; ++k) size = fmaxf(size, v[k].size());
+    size = largest_of_16_lanes(size);
+    size = fmaxf(size, __shfl_xor(size, 16));
+    size = fmaxf(size, __shfl_xor(size, 32));
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = size;
+    __syncthreads();
+    size = fmaxf(fmaxf(lds[0], lds[1]), fmaxf(lds[2], lds[3]));
+    const float scale = scale_of(size);
+    if (threadIdx.x == 0) a.scales[blockIdx.x] = scale;
+    if (col >= a.width) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint64_t row = row0 + k * 16 + y;
+        if (row < a.rows)
+            store_eight(a.narrow + group * a.narrow_group + row * a.narrow_ld, col, a.width, v[k].narrow(inverse_of(scale)));
+    }
+}
+
+template <typename T> __device__ __forceinline__ T rounded(float v) { return (T)v; }
+// a finite value past the ends of fp16 is the end
+template <> __device__ __forceinline__ f16 rounded<f16>(float v) {
+    return (f16)(fabsf(v) < INFINITY ? fminf(fmaxf(v, -65504.0f), 65504.0f) : v);
+}
+
+// Eight columns a thread.
+template <typename T> __global__ void __launch_bounds__(256) back_kernel(const BlockArgs a) {
+    const uint32_t each = ((uint32_t)a.filled + 7) / 8;
+    const uint64_t all = a.groups * a.rows * each, per = a.rows / a.part;
+    for (uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x; id < all; id += (uint64_t)gridDim.x * 256) {
+        const uint64_t line = id / each;
+        const int col = (int)(id - line * each) * 8;
+        const uint64_t group = a.groups > 1 ? line / a.rows : 0, row = line - group * a.rows;
+        u32x2 q = {0, 0};
+        float scale = 0.0f;
+        if (col < a.width) {
+            const uint8_t* from = a.narrow + group * a.narrow_group + row * a.narrow_ld + col;
+            q = __builtin_bit_cast(u32x2, load_some<uint8_t, 8>(from, a.width - col));
+            uint64_t block = line;
+            if (a.high > 1) {
+                const uint64_t part = row / a.part;
+                block = (group * per + part) * ((a.part + 127) / 128) + (row - part * a.part) / 128;
+            }
+            scale = a.scales[block * (uint32_t)a.blocks + (uint32_t)col / 128];
+        }
+        float v[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[h], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[h], true);
+            v[h * 4] = lo[0] * scale, v[h * 4 + 1] = lo[1] * scale, v[h * 4 + 2] = hi[0] * scale, v[h * 4 + 3] = hi[1] * scale;
+        }
+        T* const to = (T*)a.wide + group * a.wide_group + row * a.wide_ld + col;
+        const int n = a.filled - col;
+        if (n >= 8) {
+#pragma unroll
+            for (int h = 0; h < 8; h += Vec<T>::N) {
+                Vec<T> o;
+#pragma unroll
+                for (int e = 0; e < Vec<T>::N; ++e) o.e[e] = rounded<T>(col + h + e < a.width ? v[h + e] : 0.0f);
+                ((Loose<T>*)(to + h))->v = __builtin_bit_cast(u32x4, o);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) to[e] = rounded<T>(v[e]);
+        }
+    }
+}
+
+// 16 bytes a thread; `narrow` -> `wide`.
+__global__ void __launch_bounds__(256) pack8_kernel(const BlockArgs a) {
+    const uint32_t each = (uint32_t)a.filled / 16;
+    const uint64_t all = a.groups * a.rows * each;
+    for (uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x; id < all; id += (uint64_t)gridDim.x * 256) {
+        const uint64_t line = id / each;
+        const int col = (int)(id - line * each) * 16;
+        const uint64_t group = a.groups > 1 ? line / a.rows : 0, row = line - group * a.rows;
+        const uint8_t* from = a.narrow + group * a.narrow_group + row * a.narrow_ld + col;
+        const Some<uint8_t, 16> v = load_some<uint8_t, 16>(from, a.width - col);
+        *(u32x4*)((char*)a.wide + line * a.wide_ld + col) = __builtin_bit_cast(u32x4, v);
+    }
+}
+
+// ------------------------------------------------------------------ host side --
+
+static unsigned grid_of(uint64_t items, uint64_t each) {
+    const uint64_t n = ceil_div(items, each);
+    return (unsigned)(n < 8192 ? n : 8192);
+}
+
+rr_status_t launch_back(const BlockArgs& a, int dt, hipStream_t s) {
+    const uint64_t all = a.groups * a.rows * ceil_div((uint64_t)a.filled, 8);
+    if (all == 0) return RR_OK;
+    const unsigned grid = grid_of(all, 256);
+    if (dt == RR_BF16) back_kernel<bf16><<<grid, 256, 0, s>>>(a);
+    else if (dt == RR_FP16) back_kernel<f16><<<grid, 256, 0, s>>>(a);
+    else back_kernel<float><<<grid, 256, 0, s>>>(a);
+    return launched();
+}
+
+rr_status_t launch_pack8(const BlockArgs& a, void* to, uint64_t to_ld, hipStream_t s) {
+    BlockArgs b = a;
+    b.wide = to;
+    b.wide_ld = to_ld;
+    b.filled = (int32_t)to_ld;
+    const uint64_t all = b.groups * b.rows * (to_ld / 16);
+    if (all == 0) return RR_OK;
+    pack8_kernel<<<grid_of(all, 256), 256, 0, s>>>(b);
+    return launched();
+}
+
+static rr_status_t check(const rr_quantize_t* a, bool back, BlockArgs& k) {
+    if (!a || (a->square != 0 && a->square != 1) || !is_float_type(a->dt) || a->width < 1 || a->groups < 1)
+        return RR_ERR_INVALID;
+    if (a->width > kMaxSize || a->rows > kMaxSize || a->groups > kMaxSize || a->groups * a->rows > kMaxSize)
+        return RR_ERR_UNSUPPORTED;
+    const uint64_t e = type_bytes(a->dt), blocks = ceil_div(a->width, kBlock), high = a->square ? ceil_div(a->rows, kBlock) : a->rows;
+    if (a->groups * high * blocks >= 1ull << 34) return RR_ERR_UNSUPPORTED;
+    if (a->square && !back && a->groups * high * blocks > (1ull << 24) - 1) return RR_ERR_UNSUPPORTED;
+    if (!rows_ok(a->x, a->rows, a->width, e) || !rows_ok(a->q, a->rows, a->width, 1)) return RR_ERR_INVALID;
+    if (a->rows && (!a->scales || !aligned_to(a->scales, 4))) return RR_ERR_INVALID;
+    if (a->x.ld > 1ull << 40 || a->q.ld > 1ull << 40 || a->x_stride > 1ull << 44 || a->q_stride > 1ull << 44)
+        return RR_ERR_UNSUPPORTED;
+    const uint64_t x_one = extent(a->rows, a->x.ld, a->width, 1), q_one = extent(a->rows, a->q.ld, a->width, 1);
+    if (a->groups > 1 && ((back && a->x_stride < x_one) || (!back && a->q_stride < q_one))) return RR_ERR_INVALID;
+    const uint64_t x_bytes = extent(a->groups, a->x_stride, x_one, e), q_bytes = extent(a->groups, a->q_stride, q_one, 1);
+    const uint64_t s_bytes = a->groups * high * blocks * 4;
+    if (overlap(a->x.data, x_bytes, a->q.data, q_bytes) || overlap(a->x.data, x_bytes, a->scales, s_bytes) ||
+        overlap(a->q.data, q_bytes, a->scales, s_bytes))
+        return RR_ERR_INVALID;
+    k = {};
+    k.wide = a->x.data;
+    k.narrow = (uint8_t*)a->q.data;
+    k.scales = a->scales;
+    k.wide_ld = a->x.ld;
+    k.wide_group = a->x_stride;
+    k.narrow_ld = a->q.ld;
+    k.narrow_group = a->q_stride;
+    k.rows = a->rows;
+    k.groups = a->groups;
+    k.part = a->rows ? a->rows : 1;
+    k.width = k.filled = (int32_t)a->width;
+    k.blocks = (int32_t)blocks;
+    k.high = a->square ? 128 : 1;
+    return RR_OK;
+}
+
+template <typename T> static void launch_quantize(const BlockArgs& k, hipStream_t s) {
+    if (k.high > 1)
+        quantize_square_kernel<T><<<(unsigned)(k.groups * ceil_div(k.rows, kBlock) * k.blocks), 256, 0, s>>>(k);
+    else
+        quantize_rows_kernel<T><<<grid_of(k.groups * k.rows * k.blocks, 16), 256, 0, s>>>(k);
+}
+
+}  // namespace blk
+
+using namespace blk;
+
+extern "C" {
+
+rr_status_t block_quantize(const rr_quantize_t* a, rr_stream_t stream) {
+    BlockArgs k;
+    const rr_status_t st = check(a, false, k);
+    if (st != RR_OK || a->rows == 0) return st;
+    if (a->dt == RR_BF16) launch_quantize<bf16>(k, (hipStream_t)stream);
+    else if (a->dt == RR_FP16) launch_quantize<f16>(k, (hipStream_t)stream);
+    else launch_quantize<float>(k, (hipStream_t)stream);
+    return launched();
+}
+
+rr_status_t block_dequantize(const rr_quantize_t* a, rr_stream_t stream) {
+    BlockArgs k;
+    const rr_status_t st = check(a, true, k);
+    if (st != RR_OK || a->rows == 0) return st;
+    return launch_back(k, a->dt, (hipStream_t)stream);
+}
+
+}  // extern "C"
