@@ -22,19 +22,68 @@ namespace blk {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// 16 rows of Q by 16 of P, 128 deep, from nothing.  A lane's 32 bytes are 32 of a row's 128, the
-// same ones of both operands; which ones does not matter to the sum.
-__device__ __forceinline__ f32x4 mma8(u32x4 q0, u32x4 q1, u32x4 p0, u32x4 p1) {
-    const i32x8 q = {(int)q0[0], (int)q0[1], (int)q0[2], (int)q0[3], (int)q1[0], (int)q1[1], (int)q1[2], (int)q1[3]};
-    const i32x8 p = {(int)p0[0], (int)p0[1], (int)p0[2], (int)p0[3], (int)p1[0], (int)p1[1], (int)p1[2], (int)p1[3]};
+// A lane's 32 bytes of a row's 128: the same ones of both operands; which ones does not matter to
+// the sum.
+typedef i32x8 Frag;
+__device__ __forceinline__ Frag frag_of(u32x4 lo, u32x4 hi) {
+    return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+// 16 rows of Q by 16 of P, 128 deep, from nothing.
+__device__ __forceinline__ f32x4 mma8(const Frag& q, const Frag& p) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q, p, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
 }
+// The same, times 2^(sq + sp - 254) of the lane's row of either operand, on top of c.
+__device__ __forceinline__ f32x4 mma8_scaled(const Frag& q, const Frag& p, f32x4 c, uint32_t sq, uint32_t sp) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q, p, c, 0, 0, 0, (int)sq, 0, (int)sp);
+}
+// Whether a scale is a power of two that the instruction takes: its exponent in 8 bits.  Of a
+// row past the end it is 0, and so is what it scales.
+__device__ __forceinline__ bool is_power(float scale) {
+    const uint32_t bits = __builtin_bit_cast(uint32_t, scale);
+    return (bits & 0x807FFFFF) == 0 && bits < 0x7F800000;
+}
+__device__ __forceinline__ uint32_t exponent_of(float scale) { return __builtin_bit_cast(uint32_t, scale) >> 23; }
 
 // ------------------------------------------------------------------- the tiles --
 //
 // The tiles of the 16-bit products, with two 8-bit values in the place of one of 16: a tile is
 // 128 bytes deep, one block.  The scales of four blocks at a time go to LDS beside the
 // operands: 16 bytes of a row for each of P's rows, and of up to two blocks of Q's.
+
+__device__ __forceinline__ u32x4 descriptor(const void* base, uint64_t bytes) {
+    const uint64_t p = (uint64_t)uniform((const char*)base);
+    return u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFF,
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(bytes < kReach ? (uint32_t)bytes : kReach)), 0x00027000};
+}
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t offset, uint32_t to) {
+    Direct<uint16_t, false, 64, 256, false>::issue(rsrc, offset, to);
+}
+
+// Rows of an operand into the places of tiles, as Direct does it, in fewer registers: what a
+// lane loads next is THREADS / 8 rows on, so one offset serves them all, and the descriptor ends
+// with the last row.  (Whether an offset is in its range goes by the lane's part alone, which is
+// why the steps are in it.)
+template <int ROWS, int THREADS> struct Load8 {
+    static constexpr int kPieces = ROWS * 8 / THREADS;
+    u32x4 rsrc;
+    uint32_t stride;
+    // r0, r_end: rows; end: bytes of a row, whole 16-byte pieces (part of one in range would come
+    // as zeros); ld: bytes
+    __device__ __forceinline__ void start(const char* b, uint64_t ld, int r0, int r_end, int end) {
+        const int rows = max(min(r_end - r0, ROWS), 0);
+        rsrc = descriptor(b + (uint64_t)r0 * ld, rows ? (uint64_t)(rows - 1) * ld + end : 0);
+        stride = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)ld * (THREADS / 8)));
+    }
+    __device__ __forceinline__ void piece(int k, uint32_t at, uint32_t tile) const {
+        load_to_lds(rsrc, at + k * stride, tile + k * THREADS * 16);
+    }
+};
+// A thread's first byte: of row thread / 8, the 16-byte pieces permuted by the row.
+__device__ __forceinline__ int piece_of() {
+    const int thread = here();
+    return (thread & 7) ^ (thread >> 3 & 7);
+}
+
 template <int TI> struct Scales {
     static constexpr int kBytes = (TI + 64) * 16;    // a wave's load for Q's
     u32x4 rsrc;
@@ -55,38 +104,40 @@ template <int TI> struct Scales {
             bytes = (uint64_t)(a.rows - s.i0) * line;
         } else {
             // of a gated product: of either half; of others the tile's columns have two at most
-            const int b = s.j0 / 128, r = GATED ? lane * a.q_rows + b : b + lane;
-            at = lane < 2 && (GATED ? b < a.q_rows : r < a.q_rows) ? (uint32_t)(GATED ? lane * a.q_rows : lane) * line : kReach;
+            const int b = s.j0 / 128;
+            at = lane < 2 && (GATED || b + lane < a.q_rows) ? (uint32_t)(GATED ? lane * a.q_rows : lane) * line : kReach;
             const uint64_t each = (uint64_t)a.q_rows * (GATED ? 2 : 1), group = s.g.group > 0 ? s.g.group : 0;
             base = a.q_scale + (group * each + b) * a.blocks;
             bytes = (each - b) * line;
         }
-        const uint64_t p = (uint64_t)uniform((const char*)base);
-        rsrc = u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFF,
-                     (uint32_t)__builtin_amdgcn_readfirstlane((int)(bytes < kReach ? (uint32_t)bytes : kReach)), 0x00027000};
+        rsrc = descriptor(base, bytes);
     }
     // blocks b .. b + 3 into place `which`
     __device__ __forceinline__ void load(int b, int which) const {
-        if (mine)
-            Direct<uint16_t, false, 64, 256, false>::issue(rsrc, at == kReach ? kReach : at + (uint32_t)b * 4, to + which * kBytes);
+        if (mine) load_to_lds(rsrc, at == kReach ? kReach : at + (uint32_t)b * 4, to + which * kBytes);
     }
 };
+
+// Nothing moves across: reads of LDS that are moved up take registers that there are none of.
+__device__ __forceinline__ void keep_order() {
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
 
 template <typename T, int TI, int TJ, int WI, int WJ, int STAGES, bool GATED>
 __global__ void __launch_bounds__(64 * WI * WJ, STAGES * (TI + TJ) * kDepth * 2 > 81920 && WI * WJ == 4 ? 1 : 2)
 gemm8_kernel(const GemmArgs a) {
-    constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16;
-    constexpr int PB = Tile<false, TI>::kBytes, QB = Tile<false, TJ>::kBytes;
+    constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16, HALVES = GATED ? 2 : 1;
+    constexpr int PB = TI * 128, QB = TJ * 128;
     constexpr uint32_t PLACES = STAGES * (PB + QB), ALL = PLACES + 2 * Scales<TI>::kBytes;
     constexpr uint32_t OUT = 2 * 16 * WI * (TJ + 4) * 4;   // write_out's place
     __shared__ __align__(PB) char lds[OUT > ALL ? OUT : ALL];
     BLK_LDS char* const room = (BLK_LDS char*)lds;
     const RowTiles rows = count_tiles(a, TI);
     Spot s;
-    if (!find_spot<true, TI, GATED ? TJ / 2 : TJ>(a, rows, blockIdx.x, s)) return;
-    const uint16_t* const p = (const uint16_t*)a.p;
-    const uint16_t* const q = (const uint16_t*)a.q + (s.g.group > 0 ? (uint64_t)s.g.group * a.q_group : 0);
-    const int wave = threadIdx.x >> 6, tiles = (s.c_end - s.c0 + kDepth - 1) / kDepth;
+    if (!find_spot<true, TI, TJ / HALVES>(a, rows, blockIdx.x, s)) return;
+    const int wave = threadIdx.x >> 6;
+    const int tiles = __builtin_amdgcn_readfirstlane((s.c_end - s.c0 + kDepth - 1) / kDepth);
     const int wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
     Reader<false, TI> rp;
     Reader<false, TJ> rq;
@@ -98,62 +149,141 @@ gemm8_kernel(const GemmArgs a) {
     for (int x = 0; x < FI; ++x)
 #pragma unroll
         for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    typedef Direct<uint16_t, false, TI, THREADS, false> DP;
-    typedef std::conditional_t<GATED, Twin<uint16_t, false, TJ, THREADS, false>, Direct<uint16_t, false, TJ, THREADS, false>> DQ;
-    constexpr int PIECES = DP::kPieces + DQ::kPieces;
+    // a, the sizes in it and the spot count pairs of values
+    typedef Load8<TI, THREADS> DP;
+    typedef Load8<TJ / HALVES, THREADS> DQ;
+    constexpr int PIECES = DP::kPieces + HALVES * DQ::kPieces;
     DP lp;
-    DQ lq;
+    DQ lq[HALVES];
     Scales<TI> ls;
-    lp.start(p, a.p_ld, s.i0, s.i_end, s.c0, s.c_end);
-    if constexpr (GATED) lq.start(q, a.q_half, a.q_ld, s.j0, a.j, s.c0, s.c_end);
-    else lq.start(q, a.q_ld, s.j0, a.j, s.c0, s.c_end);
+    const char* const q = (const char*)a.q + (s.g.group > 0 ? (uint64_t)s.g.group * a.q_group * 2 : 0);
+    const int end = (s.c_end * 2 + 15) / 16 * 16;
+    lp.start((const char*)a.p, a.p_ld * 2, s.i0, s.i_end, end);
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) lq[h].start(q + h * a.q_half * 2, a.q_ld * 2, s.j0, a.j, end);
     ls.template start<GATED>(a, s, s_at);
+    int left = (s.c_end - s.c0) * 2;         // bytes of a row
+    const int from = piece_of() * 16;        // of the 128
+    uint32_t at_p = (uint32_t)(here() >> 3) * (uint32_t)(a.p_ld * 2) + from + s.c0 * 2;
+    uint32_t at_q = (uint32_t)(here() >> 3) * (uint32_t)(a.q_ld * 2) + from + s.c0 * 2;
+    const uint32_t mine = (uint32_t)__builtin_amdgcn_readfirstlane(wave * 1024);
+    // the next tile: aim(), then all its pieces, then past()
+    const auto aim = [&]() {
+        const bool none = from >= left;
+        at_p = none ? kReach : at_p;
+        at_q = none ? kReach : at_q;
+    };
+    const auto past = [&]() {
+        left -= 128;
+        at_p += 128;
+        at_q += 128;
+    };
+    const auto load_p = [&](uint32_t place) {
+#pragma unroll
+        for (int k = 0; k < DP::kPieces; ++k) lp.piece(k, at_p, p_at + place * PB + mine);
+    };
+    const auto load_q = [&](uint32_t place) {
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+            for (int k = 0; k < DQ::kPieces; ++k) lq[h].piece(k, at_q, q_at + place * QB + h * (QB / 2) + mine);
+    };
     const int first = s.c0 / kDepth;         // block of the first tile
-    const auto fetch = [&](int place) {
-        lp.aim(p_at + place * PB);
-        lq.aim(q_at + place * QB);
+    // of this lane's rows, and of the wave's columns
+    const uint32_t sp_at = s_at + (wi + (threadIdx.x & 15)) * 16;
+    const uint32_t sq_at = s_at + TI * 16 + (GATED ? wj / (TJ / 2) : wj / 128) * 16;
+    // A tile's fragments of Q are in registers throughout, those of P one block row ahead.  The
+    // barrier is two block rows before the end, when the last of them are read: behind it the
+    // next tile has arrived, and the loads of the tile STAGES on go out, into the place just
+    // read.  The last two rows are multiplied column by column, and after each column the next
+    // tile's fragment of Q takes the place of this one's.
+    Frag fq[FJ], fp[FI > 4 ? 4 : FI * 2];
+    float sq, sp[FI];
+    const auto read_p = [&](int slot, int x) {
+        fp[slot] = frag_of(rp.template fragment<u32x4>(x, 0), rp.template fragment<u32x4>(x, 1));
+    };
+    const auto read_q = [&](int y) { fq[y] = frag_of(rq.template fragment<u32x4>(y, 0), rq.template fragment<u32x4>(y, 1)); };
+    const auto read_scales = [&](int t) {
+        const uint32_t at = (uint32_t)((t >> 2 & 1) * Scales<TI>::kBytes + (t & 3) * 4);
+        sq = *(const BLK_LDS float*)(uintptr_t)(sq_at + at);
 #pragma unroll
-        for (int k = 0; k < DP::kPieces; ++k) lp.piece(k);
+        for (int x = 0; x < FI; ++x) sp[x] = *(const BLK_LDS float*)(uintptr_t)(sp_at + at + x * 256);
+    };
+    constexpr int SLOTS = FI > 4 ? 4 : FI * 2;
+    int place = 0;
+    const auto tile = [&](auto power_, int t) {
+        constexpr bool POWER = decltype(power_)::value;
+        const auto multiply = [&](int x, int y, float s, float f) {
+            if constexpr (POWER) {
+                acc[x][y] = mma8_scaled(fq[y], fp[x % SLOTS], acc[x][y], exponent_of(sq), exponent_of(s));
+            } else {
+                acc[x][y] = __builtin_elementwise_fma(f32x4{f, f, f, f}, mma8(fq[y], fp[x % SLOTS]), acc[x][y]);
+            }
+        };
+        // (no branches between the products: they are moved down behind them, and what they read
+        // is held until then)
+        if ((t & 3) == 0) ls.load(first + t + 4, (t >> 2 & 1) ^ 1);
 #pragma unroll
-        for (int k = 0; k < DQ::kPieces; ++k) lq.piece(k);
+        for (int x = 0; x < FI - 2; ++x) {
+            read_p((x + 1) % SLOTS, x + 1);
+            if (x == FI - 3) read_p((x + 2) % SLOTS, x + 2);
+            const float f = sp[x] * sq;
+#pragma unroll
+            for (int y = 0; y < FJ; ++y) multiply(x, y, sp[x], f);
+            keep_order();
+        }
+        arrived<PIECES * (STAGES - 2)>();
+        const float s0 = sp[FI - 2], s1 = sp[FI - 1], f0 = s0 * sq, f1 = s1 * sq;
+        const int to = place;
+        const bool wrap = place == STAGES - 1;
+        rp.move(wrap ? -(STAGES - 1) * PB : PB);
+        rq.move(wrap ? -(STAGES - 1) * QB : QB);
+        place = wrap ? 0 : place + 1;
+        aim();
+        read_p(FI % SLOTS, 0);
+        if constexpr (FI == 2) read_p(3, 1);
+#pragma unroll
+        for (int y = 0; y < FJ; ++y) {
+            multiply(FI - 2, y, s0, f0);
+            multiply(FI - 1, y, s1, f1);
+            if (y == 0) load_p(to);
+            if (y == 1) load_q(to);
+            read_q(y);
+            keep_order();
+        }
+        past();
+        if constexpr (FI % SLOTS != 0) {
+            fp[0] = fp[FI % SLOTS];
+            if constexpr (FI == 2) fp[1] = fp[3];
+        }
+        read_scales(t + 1);
     };
     if (tiles > 0) {
         ls.load(first, 0);
 #pragma unroll
-        for (int t = 0; t < STAGES - 1; ++t) fetch(t);
-    }
-    // of this lane's rows, and of the wave's columns
-    const uint32_t sp_at = s_at + (wi + (threadIdx.x & 15)) * 16;
-    const uint32_t sq_at = s_at + TI * 16 + (GATED ? wj / (TJ / 2) : wj / 128) * 16;
-    int now = 0, next = STAGES - 1;
-    for (int t = 0; t < tiles; ++t) {
-        arrived<PIECES * (STAGES - 2)>();
-        if ((t & 3) == 0) ls.load(first + t + 4, (t >> 2 & 1) ^ 1);
-        fetch(next);
-        next = next == STAGES - 1 ? 0 : next + 1;
-        const uint32_t at = (t >> 2 & 1) * Scales<TI>::kBytes + (t & 3) * 4;
-        u32x4 fq[FJ][2];
-#pragma unroll
-        for (int y = 0; y < FJ; ++y)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fq[y][h] = rq.template fragment<u32x4>(y, h);
-        const float sq = *(const BLK_LDS float*)(uintptr_t)(sq_at + at);
-#pragma unroll
-        for (int x = 0; x < FI; ++x) {
-            const u32x4 p0 = rp.template fragment<u32x4>(x, 0), p1 = rp.template fragment<u32x4>(x, 1);
-            const float f = sq * *(const BLK_LDS float*)(uintptr_t)(sp_at + at + x * 256);
-#pragma unroll
-            for (int y = 0; y < FJ; ++y) {
-                const f32x4 sum = mma8(fq[y][0], fq[y][1], p0, p1);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[x][y][e] = fmaf(f, sum[e], acc[x][y][e]);
-            }
+        for (int t = 0; t < STAGES; ++t) {
+            aim();
+            load_p(t);
+            load_q(t);
+            past();
         }
-        const uint32_t by_p = now == STAGES - 1 ? -(STAGES - 1) * PB : PB, by_q = now == STAGES - 1 ? -(STAGES - 1) * QB : QB;
-        now = now == STAGES - 1 ? 0 : now + 1;
-        rp.move(by_p);
-        rq.move(by_q);
+        arrived<PIECES * (STAGES - 1)>();
+#pragma unroll
+        for (int y = 0; y < FJ; ++y) read_q(y);
+        read_p(0, 0);
+        if constexpr (FI == 2) read_p(1, 1);
+        read_scales(0);
     }
+    // as long as all scales are powers of two, and the rest
+    const auto powers = [&]() {
+        bool all = is_power(sq);
+#pragma unroll
+        for (int x = 0; x < FI; ++x) all = all && is_power(sp[x]);
+        return __all(all);
+    };
+    int t = 0;
+    for (; t < tiles && powers(); ++t) tile(std::true_type(), t);
+    for (; t < tiles; ++t) tile(std::false_type(), t);
     arrived<0>();                            // the loads past the end as well
     if constexpr (GATED) write_gated<T, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
     else write_out<T, true, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
@@ -228,7 +358,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream8_kernel(const GemmAr
 #pragma unroll
                 for (int y = 0; y < FJ; ++y) {
                     const u32x4 (&q)[4][EACH] = now.q[y / EACH];
-                    const f32x4 sum = mma8(q[b * 2][y % EACH], q[b * 2 + 1][y % EACH], now.p[b * 2][x], now.p[b * 2 + 1][x]);
+                    const f32x4 sum = mma8(frag_of(q[b * 2][y % EACH], q[b * 2 + 1][y % EACH]), frag_of(now.p[b * 2][x], now.p[b * 2 + 1][x]));
                     const float f = now.ps[b][x] * now.qs[b][y / EACH];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[x][y][e] = fmaf(f, sum[e], acc[x][y][e]);
