@@ -118,6 +118,9 @@ template <int TI> struct Scales {
     }
 };
 
+// Every wave's reads of LDS are done.
+__device__ __forceinline__ void all_read() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
+
 // Nothing moves across: reads of LDS that are moved up take registers that there are none of.
 __device__ __forceinline__ void keep_order() {
     asm volatile("" : : : "memory");
@@ -167,16 +170,12 @@ gemm8_kernel(const GemmArgs a) {
     uint32_t at_p = (uint32_t)(here() >> 3) * (uint32_t)(a.p_ld * 2) + from + s.c0 * 2;
     uint32_t at_q = (uint32_t)(here() >> 3) * (uint32_t)(a.q_ld * 2) + from + s.c0 * 2;
     const uint32_t mine = (uint32_t)__builtin_amdgcn_readfirstlane(wave * 1024);
-    // the next tile: aim(), then all its pieces, then past()
+    // before the loads of a tile: aim(); after its P's and Q's: 128 bytes on
     const auto aim = [&]() {
         const bool none = from >= left;
         at_p = none ? kReach : at_p;
         at_q = none ? kReach : at_q;
-    };
-    const auto past = [&]() {
         left -= 128;
-        at_p += 128;
-        at_q += 128;
     };
     const auto load_p = [&](uint32_t place) {
 #pragma unroll
@@ -192,11 +191,13 @@ gemm8_kernel(const GemmArgs a) {
     // of this lane's rows, and of the wave's columns
     const uint32_t sp_at = s_at + (wi + (threadIdx.x & 15)) * 16;
     const uint32_t sq_at = s_at + TI * 16 + (GATED ? wj / (TJ / 2) : wj / 128) * 16;
-    // A tile's fragments of Q are in registers throughout, those of P one block row ahead.  The
-    // barrier is two block rows before the end, when the last of them are read: behind it the
-    // next tile has arrived, and the loads of the tile STAGES on go out, into the place just
-    // read.  The last two rows are multiplied column by column, and after each column the next
-    // tile's fragment of Q takes the place of this one's.
+    // A tile's fragments of Q are in registers throughout, those of P one block row ahead.  So Q's
+    // place is free early on: behind a barrier at block row MID the loads of the tile STAGES on
+    // go into it, and P's behind one two block rows before the end, when the last of them are
+    // read and the next tile has arrived.  (Both at once, in the second place, wait for each
+    // other.)  The last two rows are multiplied column by column, and after each column the
+    // next tile's fragment of Q takes the place of this one's.
+    constexpr int MID = FI > 2 ? FI / 4 : 0;
     Frag fq[FJ], fp[FI > 4 ? 4 : FI * 2];
     float sq, sp[FI];
     const auto read_p = [&](int slot, int x) {
@@ -223,8 +224,14 @@ gemm8_kernel(const GemmArgs a) {
         // (no branches between the products: they are moved down behind them, and what they read
         // is held until then)
         if ((t & 3) == 0) ls.load(first + t + 4, (t >> 2 & 1) ^ 1);
+        aim();
 #pragma unroll
         for (int x = 0; x < FI - 2; ++x) {
+            if (x == MID) {
+                all_read();
+                load_q(place);
+                at_q += 128;
+            }
             read_p((x + 1) % SLOTS, x + 1);
             if (x == FI - 3) read_p((x + 2) % SLOTS, x + 2);
             const float f = sp[x] * sq;
@@ -232,14 +239,13 @@ gemm8_kernel(const GemmArgs a) {
             for (int y = 0; y < FJ; ++y) multiply(x, y, sp[x], f);
             keep_order();
         }
-        arrived<PIECES * (STAGES - 2)>();
+        arrived<PIECES * (STAGES - 2) + (MID > 0 ? HALVES * DQ::kPieces : 0)>();
         const float s0 = sp[FI - 2], s1 = sp[FI - 1], f0 = s0 * sq, f1 = s1 * sq;
         const int to = place;
         const bool wrap = place == STAGES - 1;
         rp.move(wrap ? -(STAGES - 1) * PB : PB);
         rq.move(wrap ? -(STAGES - 1) * QB : QB);
         place = wrap ? 0 : place + 1;
-        aim();
         read_p(FI % SLOTS, 0);
         if constexpr (FI == 2) read_p(3, 1);
 #pragma unroll
@@ -247,11 +253,12 @@ gemm8_kernel(const GemmArgs a) {
             multiply(FI - 2, y, s0, f0);
             multiply(FI - 1, y, s1, f1);
             if (y == 0) load_p(to);
-            if (y == 1) load_q(to);
+            if (MID == 0 && y == 1) load_q(to);
             read_q(y);
             keep_order();
         }
-        past();
+        at_p += 128;
+        if (MID == 0) at_q += 128;
         if constexpr (FI % SLOTS != 0) {
             fp[0] = fp[FI % SLOTS];
             if constexpr (FI == 2) fp[1] = fp[3];
@@ -265,7 +272,8 @@ gemm8_kernel(const GemmArgs a) {
             aim();
             load_p(t);
             load_q(t);
-            past();
+            at_p += 128;
+            at_q += 128;
         }
         arrived<PIECES * (STAGES - 1)>();
 #pragma unroll
