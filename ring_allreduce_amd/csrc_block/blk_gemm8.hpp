@@ -36,11 +36,13 @@ __device__ __forceinline__ f32x4 mma8(const Frag& q, const Frag& p) {
 __device__ __forceinline__ f32x4 mma8_scaled(const Frag& q, const Frag& p, f32x4 c, uint32_t sq, uint32_t sp) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q, p, c, 0, 0, 0, (int)sq, 0, (int)sp);
 }
-// Whether a scale is a power of two that the instruction takes: its exponent in 8 bits.  Of a
-// row past the end it is 0, and so is what it scales.
-__device__ __forceinline__ bool is_power(float scale) {
-    const uint32_t bits = __builtin_bit_cast(uint32_t, scale);
-    return (bits & 0x807FFFFF) == 0 && bits < 0x7F800000;
+// 0 if four scales are powers of two that the instruction takes: its exponent in 8 bits, 2^-127 and
+// NaN (0 and 255) not among them.
+__device__ __forceinline__ uint32_t not_power(u32x4 scales) {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bad |= (scales[k] & 0x807FFFFF) | (scales[k] - 0x00800000 < 0x7F000000 ? 0 : 1);
+    return bad;
 }
 __device__ __forceinline__ uint32_t exponent_of(float scale) { return __builtin_bit_cast(uint32_t, scale) >> 23; }
 
@@ -177,15 +179,11 @@ gemm8_kernel(const GemmArgs a) {
         at_q = none ? kReach : at_q;
         left -= 128;
     };
-    const auto load_p = [&](uint32_t place) {
-#pragma unroll
-        for (int k = 0; k < DP::kPieces; ++k) lp.piece(k, at_p, p_at + place * PB + mine);
-    };
-    const auto load_q = [&](uint32_t place) {
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-            for (int k = 0; k < DQ::kPieces; ++k) lq[h].piece(k, at_q, q_at + place * QB + h * (QB / 2) + mine);
+    constexpr int QS = HALVES * DQ::kPieces, PS = DP::kPieces;
+    const auto load_p = [&](uint32_t place, int k) { lp.piece(k, at_p, p_at + place * PB + mine); };
+    const auto load_q = [&](uint32_t place, int k) {
+        const int h = k / DQ::kPieces;
+        lq[h].piece(k % DQ::kPieces, at_q, q_at + place * QB + h * (QB / 2) + mine);
     };
     const int first = s.c0 / kDepth;         // block of the first tile
     // of this lane's rows, and of the wave's columns
@@ -197,18 +195,37 @@ gemm8_kernel(const GemmArgs a) {
     // read and the next tile has arrived.  (Both at once, in the second place, wait for each
     // other.)  The last two rows are multiplied column by column, and after each column the
     // next tile's fragment of Q takes the place of this one's.
-    constexpr int MID = FI > 2 ? FI / 4 : 0;
+    constexpr int MID = FI > 2 ? FI / 4 : 0, SPAN = FI > 2 ? FI - 2 - MID : 1;
     Frag fq[FJ], fp[FI > 4 ? 4 : FI * 2];
-    float sq, sp[FI];
+    float sq, sp[FI], sq_next, sp_next[FI];
     const auto read_p = [&](int slot, int x) {
         fp[slot] = frag_of(rp.template fragment<u32x4>(x, 0), rp.template fragment<u32x4>(x, 1));
     };
     const auto read_q = [&](int y) { fq[y] = frag_of(rq.template fragment<u32x4>(y, 0), rq.template fragment<u32x4>(y, 1)); };
     const auto read_scales = [&](int t) {
         const uint32_t at = (uint32_t)((t >> 2 & 1) * Scales<TI>::kBytes + (t & 3) * 4);
-        sq = *(const BLK_LDS float*)(uintptr_t)(sq_at + at);
+        sq_next = *(const BLK_LDS float*)(uintptr_t)(sq_at + at);
 #pragma unroll
-        for (int x = 0; x < FI; ++x) sp[x] = *(const BLK_LDS float*)(uintptr_t)(sp_at + at + x * 256);
+        for (int x = 0; x < FI; ++x) sp_next[x] = *(const BLK_LDS float*)(uintptr_t)(sp_at + at + x * 256);
+    };
+    const auto use_scales = [&]() {
+        sq = sq_next;
+#pragma unroll
+        for (int x = 0; x < FI; ++x) sp[x] = sp_next[x];
+    };
+    // Whether all scales of the four blocks from tile t on are powers of two: a lane looks at
+    // every fourth of its rows.
+    const auto powers = [&](int t) {
+        const uint32_t at = (uint32_t)((t >> 2 & 1) * Scales<TI>::kBytes);
+        const int lane = threadIdx.x & 63;
+        uint32_t bad = not_power(*(const BLK_LDS u32x4*)(uintptr_t)(sq_at + at));
+#pragma unroll
+        for (int x = 0; x < FI; x += 4) {
+            const int block = (x + (lane >> 4)) % FI;
+            const uint32_t not_this = not_power(*(const BLK_LDS u32x4*)(uintptr_t)(sp_at + at + block * 256));
+            bad |= s.i0 + wi + block * 16 + (lane & 15) < s.i_end ? not_this : 0;
+        }
+        return __all(bad == 0);
     };
     constexpr int SLOTS = FI > 4 ? 4 : FI * 2;
     int place = 0;
@@ -227,11 +244,10 @@ gemm8_kernel(const GemmArgs a) {
         aim();
 #pragma unroll
         for (int x = 0; x < FI - 2; ++x) {
-            if (x == MID) {
-                all_read();
-                load_q(place);
-                at_q += 128;
-            }
+            if (x == MID) all_read();
+            if (x >= MID)
+#pragma unroll
+                for (int k = (x - MID) * QS / SPAN; k < (x - MID + 1) * QS / SPAN; ++k) load_q(place, k);
             read_p((x + 1) % SLOTS, x + 1);
             if (x == FI - 3) read_p((x + 2) % SLOTS, x + 2);
             const float f = sp[x] * sq;
@@ -239,39 +255,45 @@ gemm8_kernel(const GemmArgs a) {
             for (int y = 0; y < FJ; ++y) multiply(x, y, sp[x], f);
             keep_order();
         }
-        arrived<PIECES * (STAGES - 2) + (MID > 0 ? HALVES * DQ::kPieces : 0)>();
+        arrived<PIECES * (STAGES - 2) + (FI > 2 ? QS : 0)>();
         const float s0 = sp[FI - 2], s1 = sp[FI - 1], f0 = s0 * sq, f1 = s1 * sq;
         const int to = place;
         const bool wrap = place == STAGES - 1;
         rp.move(wrap ? -(STAGES - 1) * PB : PB);
         rq.move(wrap ? -(STAGES - 1) * QB : QB);
         place = wrap ? 0 : place + 1;
+        read_scales(t + 1);
         read_p(FI % SLOTS, 0);
         if constexpr (FI == 2) read_p(3, 1);
 #pragma unroll
         for (int y = 0; y < FJ; ++y) {
             multiply(FI - 2, y, s0, f0);
             multiply(FI - 1, y, s1, f1);
-            if (y == 0) load_p(to);
-            if (MID == 0 && y == 1) load_q(to);
+#pragma unroll
+            for (int k = y * PS / FJ; k < (y + 1) * PS / FJ; ++k) load_p(to, k);
+            if (FI == 2)
+#pragma unroll
+                for (int k = y * QS / FJ; k < (y + 1) * QS / FJ; ++k) load_q(to, k);
             read_q(y);
             keep_order();
         }
         at_p += 128;
-        if (MID == 0) at_q += 128;
+        at_q += 128;
         if constexpr (FI % SLOTS != 0) {
             fp[0] = fp[FI % SLOTS];
             if constexpr (FI == 2) fp[1] = fp[3];
         }
-        read_scales(t + 1);
+        use_scales();
     };
     if (tiles > 0) {
         ls.load(first, 0);
 #pragma unroll
         for (int t = 0; t < STAGES; ++t) {
             aim();
-            load_p(t);
-            load_q(t);
+#pragma unroll
+            for (int k = 0; k < PS; ++k) load_p(t, k);
+#pragma unroll
+            for (int k = 0; k < QS; ++k) load_q(t, k);
             at_p += 128;
             at_q += 128;
         }
@@ -281,16 +303,11 @@ gemm8_kernel(const GemmArgs a) {
         read_p(0, 0);
         if constexpr (FI == 2) read_p(1, 1);
         read_scales(0);
+        use_scales();
     }
     // as long as all scales are powers of two, and the rest
-    const auto powers = [&]() {
-        bool all = is_power(sq);
-#pragma unroll
-        for (int x = 0; x < FI; ++x) all = all && is_power(sp[x]);
-        return __all(all);
-    };
     int t = 0;
-    for (; t < tiles && powers(); ++t) tile(std::true_type(), t);
+    for (; t < tiles && ((t & 3) != 0 || powers(t)); ++t) tile(std::true_type(), t);
     for (; t < tiles; ++t) tile(std::false_type(), t);
     arrived<0>();                            // the loads past the end as well
     if constexpr (GATED) write_gated<T, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
