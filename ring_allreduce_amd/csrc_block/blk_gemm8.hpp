@@ -86,6 +86,86 @@ __device__ __forceinline__ int piece_of() {
     return (thread & 7) ^ (thread >> 3 & 7);
 }
 
+// Which of Q's rows in the tile fragment y of a wave takes, so that a lane's results of two
+// fragments (16 rows of Q each, of which it gets four) are 8 neighbouring columns of out, and
+// those of the four lanes of a row 32: the results leave from the registers, in whole pieces of
+// 64 bytes a row.  Of a gated product the first half of the fragments are rows of the gate and the
+// second the same ones of the other projection.  Where a half is one fragment, a lane has four
+// columns.
+template <int TJ, int WJ, int FJ, bool GATED> struct Columns {
+    static constexpr int HALVES = GATED ? 2 : 1, N = FJ / HALVES > 1 ? 8 : 4, GROUPS = FJ * 4 / HALVES / N;
+    static constexpr int WIDE = TJ / WJ / HALVES;      // a wave's columns of out
+    // the first row of fragment y, and the one in it of lane r (0 .. 15)
+    static constexpr int row(int y) {
+        const int in = y % (FJ / HALVES);
+        return y / (FJ / HALVES) * (TJ / 2) + (N == 8 ? (in >> 1) * 32 + (in & 1) * 4 : 0);
+    }
+    __device__ __forceinline__ static int row_in(int r) { return N == 8 ? (r >> 2) * 8 + (r & 3) : r; }
+    // by which the 16-byte pieces of a row are permuted: another for each of 8 lanes
+    __device__ __forceinline__ static int mix(int row) { return N == 8 ? (row & 3) | (row >> 1 & 4) : row & 7; }
+};
+
+template <typename T, int TI, int TJ, int WI, int WJ, int FI, int FJ, bool GATED>
+__device__ __forceinline__ void write_direct(const GemmArgs& a, const Spot& s, const f32x4 (&acc)[FI][FJ]) {
+    typedef Columns<TJ, WJ, FJ, GATED> C;
+    constexpr int N = C::N, GROUPS = C::GROUPS, HALVES = C::HALVES;
+    const bool whole = a.splits == 1 && s.parts == 1, add = !GATED && whole && a.residual && s.g.group >= 0;
+    if (!whole && s.g.group < 0) return;        // the kernels that join the parts know
+    const int thread = here(), lane = thread & 63, wave = thread >> 6;
+    const int j0 = s.j0 + wave % WJ * C::WIDE + (lane >> 4) * N, i0 = s.i0 + wave / WJ * (TI / WI) + (lane & 15);
+    Some<T, N> bias[HALVES][GROUPS];
+#pragma unroll
+    for (int c = 0; c < GROUPS; ++c)
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+            if constexpr (GATED) bias[h][c] = whole ? gated_bias_of<T, N>(a, s.g.group, h, j0 + c * 32) : Some<T, N>{};
+            else bias[h][c] = whole ? bias_of<T, N>(a, s.g.group, j0 + c * 32) : Some<T, N>{};
+        }
+    const uint64_t part_ld = s.parts > 1 ? (uint64_t)TJ : (uint64_t)a.j * HALVES;
+    float* const part = whole ? nullptr
+                        : s.parts > 1 ? a.part + ((uint64_t)s.tile * s.parts + s.split) * (TI * TJ) + (uint64_t)(i0 - s.i0) * TJ + (j0 - s.j0)
+                                      : a.part + (uint64_t)s.split * a.part_stride + (uint64_t)i0 * part_ld + j0;
+    T* const out = (T*)a.out + (uint64_t)i0 * a.out_ld + j0;
+    T* const z = (T*)a.z + (uint64_t)i0 * a.z_ld + j0;
+    const T* const res = (const T*)a.residual + (uint64_t)i0 * a.residual_ld + j0;
+    Some<T, N> residual[GROUPS] = {}, later[GROUPS] = {};
+    const auto fetch = [&](Some<T, N> (&to)[GROUPS], int x) {
+#pragma unroll
+        for (int c = 0; c < GROUPS; ++c)
+            if (i0 + x * 16 < s.i_end && j0 + c * 32 < a.j)
+                to[c] = load_some<T, N>(res + (uint64_t)(x * 16) * a.residual_ld + c * 32, a.j - j0 - c * 32);
+    };
+    if (add) fetch(residual, 0);
+#pragma unroll
+    for (int x = 0; x < FI; ++x) {
+        if (add && x + 1 < FI) fetch(later, x + 1);
+        const uint64_t down = (uint64_t)(x * 16);
+        if (i0 + x * 16 < s.i_end)
+#pragma unroll
+            for (int c = 0; c < GROUPS; ++c) {
+                const int n = a.j - j0 - c * 32;
+                if (n <= 0) continue;
+                float v[HALVES][N];
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                    for (int e = 0; e < N; ++e) v[h][e] = acc[x][h * (FJ / 2) + c * (N / 4) + e / 4][e % 4];
+                if (!whole) {
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) store_wide<N>(part + down * part_ld + c * 32 + h * a.j, n, v[h]);
+                } else if constexpr (GATED) {
+                    finish_gated<T, N>(a, s.g.group, n, v[0], v[1], bias[0][c], bias[1][c], z + down * a.z_ld + c * 32,
+                                       out + down * a.out_ld + c * 32);
+                } else {
+                    finish<T, N>(a, s.g.group, n, v[0], bias[0][c], residual[c], z + down * a.z_ld + c * 32,
+                                 (char*)(out + down * a.out_ld + c * 32));
+                }
+            }
+#pragma unroll
+        for (int c = 0; c < GROUPS; ++c) residual[c] = later[c];
+    }
+}
+
 template <int TI> struct Scales {
     static constexpr int kBytes = (TI + 64) * 16;    // a wave's load for Q's
     u32x4 rsrc;
@@ -135,20 +215,24 @@ gemm8_kernel(const GemmArgs a) {
     constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16, HALVES = GATED ? 2 : 1;
     constexpr int PB = TI * 128, QB = TJ * 128;
     constexpr uint32_t PLACES = STAGES * (PB + QB), ALL = PLACES + 2 * Scales<TI>::kBytes;
-    constexpr uint32_t OUT = 2 * 16 * WI * (TJ + 4) * 4;   // write_out's place
-    __shared__ __align__(PB) char lds[OUT > ALL ? OUT : ALL];
+    typedef Columns<TJ, WJ, FJ, GATED> C;
+    __shared__ __align__(PB) char lds[ALL];
     BLK_LDS char* const room = (BLK_LDS char*)lds;
     const RowTiles rows = count_tiles(a, TI);
     Spot s;
     if (!find_spot<true, TI, TJ / HALVES>(a, rows, blockIdx.x, s)) return;
     const int wave = threadIdx.x >> 6;
     const int tiles = __builtin_amdgcn_readfirstlane((s.c_end - s.c0 + kDepth - 1) / kDepth);
-    const int wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
+    const int wi = wave / WJ * (TI / WI), wj = wave % WJ * C::WIDE;
     Reader<false, TI> rp;
-    Reader<false, TJ> rq;
     const uint32_t p_at = (uint32_t)(uintptr_t)room, q_at = p_at + STAGES * PB, s_at = p_at + PLACES;
     rp.start(p_at, wi);
-    rq.start(q_at, wj);
+    uint32_t rq[2];                          // the lane's row of fragment 0, both halves of its 128 bytes
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = wj + C::row_in(threadIdx.x & 15);
+        rq[h] = q_at + row * 128 + (((threadIdx.x >> 4 & 3) + h * 4) ^ C::mix(row)) * 16;
+    }
     f32x4 acc[FI][FJ];
 #pragma unroll
     for (int x = 0; x < FI; ++x)
@@ -169,14 +253,14 @@ gemm8_kernel(const GemmArgs a) {
     ls.template start<GATED>(a, s, s_at);
     int left = (s.c_end - s.c0) * 2;         // bytes of a row
     const int from = piece_of() * 16;        // of the 128
+    const int from_q = ((here() & 7) ^ C::mix(here() >> 3)) * 16;
     uint32_t at_p = (uint32_t)(here() >> 3) * (uint32_t)(a.p_ld * 2) + from + s.c0 * 2;
-    uint32_t at_q = (uint32_t)(here() >> 3) * (uint32_t)(a.q_ld * 2) + from + s.c0 * 2;
+    uint32_t at_q = (uint32_t)(here() >> 3) * (uint32_t)(a.q_ld * 2) + from_q + s.c0 * 2;
     const uint32_t mine = (uint32_t)__builtin_amdgcn_readfirstlane(wave * 1024);
     // before the loads of a tile: aim(); after its P's and Q's: 128 bytes on
     const auto aim = [&]() {
-        const bool none = from >= left;
-        at_p = none ? kReach : at_p;
-        at_q = none ? kReach : at_q;
+        at_p = from >= left ? kReach : at_p;
+        at_q = from_q >= left ? kReach : at_q;
         left -= 128;
     };
     constexpr int QS = HALVES * DQ::kPieces, PS = DP::kPieces;
@@ -188,7 +272,7 @@ gemm8_kernel(const GemmArgs a) {
     const int first = s.c0 / kDepth;         // block of the first tile
     // of this lane's rows, and of the wave's columns
     const uint32_t sp_at = s_at + (wi + (threadIdx.x & 15)) * 16;
-    const uint32_t sq_at = s_at + TI * 16 + (GATED ? wj / (TJ / 2) : wj / 128) * 16;
+    const uint32_t sq_at = s_at + TI * 16 + (GATED ? 0 : wj / 128) * 16;
     // A tile's fragments of Q are in registers throughout, those of P one block row ahead.  So Q's
     // place is free early on: behind a barrier at block row MID the loads of the tile STAGES on
     // go into it, and P's behind one two block rows before the end, when the last of them are
@@ -197,19 +281,26 @@ gemm8_kernel(const GemmArgs a) {
     // next tile's fragment of Q takes the place of this one's.
     constexpr int MID = FI > 2 ? FI / 4 : 0, SPAN = FI > 2 ? FI - 2 - MID : 1;
     Frag fq[FJ], fp[FI > 4 ? 4 : FI * 2];
-    float sq, sp[FI], sq_next, sp_next[FI];
+    float sq[HALVES], sp[FI], sq_next[HALVES], sp_next[FI];
     const auto read_p = [&](int slot, int x) {
         fp[slot] = frag_of(rp.template fragment<u32x4>(x, 0), rp.template fragment<u32x4>(x, 1));
     };
-    const auto read_q = [&](int y) { fq[y] = frag_of(rq.template fragment<u32x4>(y, 0), rq.template fragment<u32x4>(y, 1)); };
+    const auto read_q = [&](int y) {
+        u32x4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[h] = *(const BLK_LDS u32x4*)(uintptr_t)(rq[h] + C::row(y) * 128);
+        fq[y] = frag_of(v[0], v[1]);
+    };
     const auto read_scales = [&](int t) {
         const uint32_t at = (uint32_t)((t >> 2 & 1) * Scales<TI>::kBytes + (t & 3) * 4);
-        sq_next = *(const BLK_LDS float*)(uintptr_t)(sq_at + at);
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) sq_next[h] = *(const BLK_LDS float*)(uintptr_t)(sq_at + at + h * 16);
 #pragma unroll
         for (int x = 0; x < FI; ++x) sp_next[x] = *(const BLK_LDS float*)(uintptr_t)(sp_at + at + x * 256);
     };
     const auto use_scales = [&]() {
-        sq = sq_next;
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) sq[h] = sq_next[h];
 #pragma unroll
         for (int x = 0; x < FI; ++x) sp[x] = sp_next[x];
     };
@@ -218,7 +309,9 @@ gemm8_kernel(const GemmArgs a) {
     const auto powers = [&](int t) {
         const uint32_t at = (uint32_t)((t >> 2 & 1) * Scales<TI>::kBytes);
         const int lane = threadIdx.x & 63;
-        uint32_t bad = not_power(*(const BLK_LDS u32x4*)(uintptr_t)(sq_at + at));
+        uint32_t bad = 0;
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) bad |= not_power(*(const BLK_LDS u32x4*)(uintptr_t)(sq_at + at + h * 16));
 #pragma unroll
         for (int x = 0; x < FI; x += 4) {
             const int block = (x + (lane >> 4)) % FI;
@@ -231,10 +324,12 @@ gemm8_kernel(const GemmArgs a) {
     int place = 0;
     const auto tile = [&](auto power_, int t) {
         constexpr bool POWER = decltype(power_)::value;
-        const auto multiply = [&](int x, int y, float s, float f) {
+        const auto multiply = [&](int x, int y, float s) {
+            const int half = y / (FJ / HALVES);
             if constexpr (POWER) {
-                acc[x][y] = mma8_scaled(fq[y], fp[x % SLOTS], acc[x][y], exponent_of(sq), exponent_of(s));
+                acc[x][y] = mma8_scaled(fq[y], fp[x % SLOTS], acc[x][y], exponent_of(sq[half]), exponent_of(s));
             } else {
+                const float f = s * sq[half];
                 acc[x][y] = __builtin_elementwise_fma(f32x4{f, f, f, f}, mma8(fq[y], fp[x % SLOTS]), acc[x][y]);
             }
         };
@@ -250,25 +345,24 @@ gemm8_kernel(const GemmArgs a) {
                 for (int k = (x - MID) * QS / SPAN; k < (x - MID + 1) * QS / SPAN; ++k) load_q(place, k);
             read_p((x + 1) % SLOTS, x + 1);
             if (x == FI - 3) read_p((x + 2) % SLOTS, x + 2);
-            const float f = sp[x] * sq;
 #pragma unroll
-            for (int y = 0; y < FJ; ++y) multiply(x, y, sp[x], f);
+            for (int y = 0; y < FJ; ++y) multiply(x, y, sp[x]);
             keep_order();
         }
         arrived<PIECES * (STAGES - 2) + (FI > 2 ? QS : 0)>();
-        const float s0 = sp[FI - 2], s1 = sp[FI - 1], f0 = s0 * sq, f1 = s1 * sq;
         const int to = place;
         const bool wrap = place == STAGES - 1;
         rp.move(wrap ? -(STAGES - 1) * PB : PB);
-        rq.move(wrap ? -(STAGES - 1) * QB : QB);
+        rq[0] += wrap ? -(STAGES - 1) * QB : QB;
+        rq[1] += wrap ? -(STAGES - 1) * QB : QB;
         place = wrap ? 0 : place + 1;
         read_scales(t + 1);
         read_p(FI % SLOTS, 0);
         if constexpr (FI == 2) read_p(3, 1);
 #pragma unroll
         for (int y = 0; y < FJ; ++y) {
-            multiply(FI - 2, y, s0, f0);
-            multiply(FI - 1, y, s1, f1);
+            multiply(FI - 2, y, sp[FI - 2]);
+            multiply(FI - 1, y, sp[FI - 1]);
 #pragma unroll
             for (int k = y * PS / FJ; k < (y + 1) * PS / FJ; ++k) load_p(to, k);
             if (FI == 2)
@@ -310,8 +404,7 @@ gemm8_kernel(const GemmArgs a) {
     for (; t < tiles && ((t & 3) != 0 || powers(t)); ++t) tile(std::true_type(), t);
     for (; t < tiles; ++t) tile(std::false_type(), t);
     arrived<0>();                            // the loads past the end as well
-    if constexpr (GATED) write_gated<T, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
-    else write_out<T, true, TI, TJ, WI, WJ, FI, FJ>(a, s, room, acc);
+    write_direct<T, TI, TJ, WI, WJ, FI, FJ, GATED>(a, s, acc);
 }
 
 // ------------------------------------------------------------ few rows: one pass --
