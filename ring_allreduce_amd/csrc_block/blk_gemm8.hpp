@@ -209,12 +209,13 @@ __device__ __forceinline__ void keep_order() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <typename T, int TI, int TJ, int WI, int WJ, int STAGES, bool GATED>
+// EIGHT: operands in 8 bits, with scales; else in T.
+template <typename T, bool EIGHT, int TI, int TJ, int WI, int WJ, int STAGES, bool GATED>
 __global__ void __launch_bounds__(64 * WI * WJ, STAGES * (TI + TJ) * kDepth * 2 > 81920 && WI * WJ == 4 ? 1 : 2)
-gemm8_kernel(const GemmArgs a) {
+tile_kernel(const GemmArgs a) {
     constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16, HALVES = GATED ? 2 : 1;
     constexpr int PB = TI * 128, QB = TJ * 128;
-    constexpr uint32_t PLACES = STAGES * (PB + QB), ALL = PLACES + 2 * Scales<TI>::kBytes;
+    constexpr uint32_t PLACES = STAGES * (PB + QB), ALL = PLACES + (EIGHT ? 2 * Scales<TI>::kBytes : 0);
     typedef Columns<TJ, WJ, FJ, GATED> C;
     __shared__ __align__(PB) char lds[ALL];
     BLK_LDS char* const room = (BLK_LDS char*)lds;
@@ -250,7 +251,7 @@ gemm8_kernel(const GemmArgs a) {
     lp.start((const char*)a.p, a.p_ld * 2, s.i0, s.i_end, end);
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) lq[h].start(q + h * a.q_half * 2, a.q_ld * 2, s.j0, a.j, end);
-    ls.template start<GATED>(a, s, s_at);
+    if constexpr (EIGHT) ls.template start<GATED>(a, s, s_at);
     int left = (s.c_end - s.c0) * 2;         // bytes of a row
     const int from = piece_of() * 16;        // of the 128
     const int from_q = ((here() & 7) ^ C::mix(here() >> 3)) * 16;
@@ -326,7 +327,14 @@ gemm8_kernel(const GemmArgs a) {
         constexpr bool POWER = decltype(power_)::value;
         const auto multiply = [&](int x, int y, float s) {
             const int half = y / (FJ / HALVES);
-            if constexpr (POWER) {
+            if constexpr (!EIGHT) {
+                typedef typename Mma<T>::V V;
+                const Frag q = fq[y], p = fp[x % SLOTS];
+                acc[x][y] = Mma<T>::run(__builtin_bit_cast(V, __builtin_shufflevector(q, q, 0, 1, 2, 3)),
+                                        __builtin_bit_cast(V, __builtin_shufflevector(p, p, 0, 1, 2, 3)), acc[x][y]);
+                acc[x][y] = Mma<T>::run(__builtin_bit_cast(V, __builtin_shufflevector(q, q, 4, 5, 6, 7)),
+                                        __builtin_bit_cast(V, __builtin_shufflevector(p, p, 4, 5, 6, 7)), acc[x][y]);
+            } else if constexpr (POWER) {
                 acc[x][y] = mma8_scaled(fq[y], fp[x % SLOTS], acc[x][y], exponent_of(sq[half]), exponent_of(s));
             } else {
                 const float f = s * sq[half];
@@ -335,7 +343,7 @@ gemm8_kernel(const GemmArgs a) {
         };
         // (no branches between the products: they are moved down behind them, and what they read
         // is held until then)
-        if ((t & 3) == 0) ls.load(first + t + 4, (t >> 2 & 1) ^ 1);
+        if (EIGHT && (t & 3) == 0) ls.load(first + t + 4, (t >> 2 & 1) ^ 1);
         aim();
 #pragma unroll
         for (int x = 0; x < FI - 2; ++x) {
@@ -356,7 +364,7 @@ gemm8_kernel(const GemmArgs a) {
         rq[0] += wrap ? -(STAGES - 1) * QB : QB;
         rq[1] += wrap ? -(STAGES - 1) * QB : QB;
         place = wrap ? 0 : place + 1;
-        read_scales(t + 1);
+        if constexpr (EIGHT) read_scales(t + 1);
         read_p(FI % SLOTS, 0);
         if constexpr (FI == 2) read_p(3, 1);
 #pragma unroll
@@ -377,10 +385,10 @@ gemm8_kernel(const GemmArgs a) {
             fp[0] = fp[FI % SLOTS];
             if constexpr (FI == 2) fp[1] = fp[3];
         }
-        use_scales();
+        if constexpr (EIGHT) use_scales();
     };
     if (tiles > 0) {
-        ls.load(first, 0);
+        if constexpr (EIGHT) ls.load(first, 0);
 #pragma unroll
         for (int t = 0; t < STAGES; ++t) {
             aim();
@@ -396,12 +404,14 @@ gemm8_kernel(const GemmArgs a) {
         for (int y = 0; y < FJ; ++y) read_q(y);
         read_p(0, 0);
         if constexpr (FI == 2) read_p(1, 1);
-        read_scales(0);
-        use_scales();
+        if constexpr (EIGHT) {
+            read_scales(0);
+            use_scales();
+        }
     }
-    // as long as all scales are powers of two, and the rest
     int t = 0;
-    for (; t < tiles && ((t & 3) != 0 || powers(t)); ++t) tile(std::true_type(), t);
+    if constexpr (EIGHT)                     // as long as all scales are powers of two, and the rest
+        for (; t < tiles && ((t & 3) != 0 || powers(t)); ++t) tile(std::true_type(), t);
     for (; t < tiles; ++t) tile(std::false_type(), t);
     arrived<0>();                            // the loads past the end as well
     write_direct<T, TI, TJ, WI, WJ, FI, FJ, GATED>(a, s, acc);
@@ -497,7 +507,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream8_kernel(const GemmAr
 template <typename T, int TI, int TJ, int WI, int WJ, int STAGES, bool GATED>
 static void launch_tile8(const GemmArgs& a, hipStream_t s) {
     const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits;
-    gemm8_kernel<T, TI, TJ, WI, WJ, STAGES, GATED><<<grid + (unsigned)a.slots, 64 * WI * WJ, 0, s>>>(a);
+    tile_kernel<T, true, TI, TJ, WI, WJ, STAGES, GATED><<<grid + (unsigned)a.slots, 64 * WI * WJ, 0, s>>>(a);
 }
 template <typename T, int FI, bool GATED> static void launch_stream8(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
     const dim3 grid((unsigned)a.tiles_j, (unsigned)a.tiles_i, (unsigned)a.splits);
