@@ -29,6 +29,7 @@ SOURCES += [os.path.join(BLOCK, f) for f in ("blk_expert.hip", "blk_norm.hip", "
 HEADERS = [os.path.join(CSRC, "rr_device.hpp"), os.path.join(CSRC, "rr_kernels.hpp"),
            os.path.join(CSRC, "rr_ring_kernel.hpp"), os.path.join(BLOCK, "blk_common.hpp"),
            os.path.join(BLOCK, "blk_gemm.hpp"), os.path.join(BLOCK, "blk_gemm8.hpp"),
+           os.path.join(BLOCK, "blk_tile.hpp"), os.path.join(BLOCK, "blk_gated.hpp"),
            os.path.join(BLOCK, "blk_product.hpp"), os.path.join(BLOCK, "blk_norm.hpp"),
            os.path.join(ROOT, "include", "rr.h")]
 

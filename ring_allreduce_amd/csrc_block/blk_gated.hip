@@ -231,10 +231,7 @@ static Forward forward_of(const rr_linear8_t* a, uint64_t halves) {
     f.plan.form = kForward;
     if (eight && f.plan.tile == kDot) f.plan.tile = kStream16;
     if (eight && f.plan.tile == kInner64) f.plan.tile = kStream64, f.plan.narrow = 0;
-    if (halves == 2) {
-        f.plan.narrow = 0;
-        f.slots = 0;
-    }
+    if (halves == 2) f.plan.narrow = 0;
     f.plan.direct = good_x && good_w;
     if (f.plan.tile == kStream16 && !eight && !f.plan.direct && l.groups == 1 && !l.offsets && l.rows <= 4)
         f.plan.tile = kDot;

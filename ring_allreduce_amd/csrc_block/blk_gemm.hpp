@@ -1269,45 +1269,4 @@ template <typename T> static rr_status_t launch_gemm(const GemmArgs& a, const Ge
     return launched();
 }
 
-// The gated forward product.
-template <typename T, int TI, int TJ, int WI, int WJ, int STAGES, int PARTS = 1>
-static void launch_gated_tile(const GemmArgs& a, hipStream_t s) {
-    const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits;
-    gemm_kernel<T, false, false, true, TI, TJ, WI, WJ, STAGES, PARTS, true><<<grid, 64 * WI * WJ * PARTS, 0, s>>>(a);
-}
-template <typename T, int FI> static void launch_gated_stream(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
-    const dim3 grid((unsigned)a.tiles_j, (unsigned)a.tiles_i, (unsigned)a.splits);
-    if (p.direct) stream_kernel<T, FI, 2, true, true><<<grid, 64 * kStreamWaves, 0, s>>>(a);
-    else stream_kernel<T, FI, 2, false, true><<<grid, 64 * kStreamWaves, 0, s>>>(a);
-}
-template <typename T> static rr_status_t join_gated(const GemmArgs& a, hipStream_t s) {
-    const rr_status_t st = launched();
-    if (st != RR_OK || a.splits == 1) return st;
-    join_gated_kernel<T><<<(unsigned)ceil_div((uint64_t)a.rows * ceil_div(a.j, 4), 256), 256, 0, s>>>(a);
-    return launched();
-}
-template <typename T> static rr_status_t launch_gated(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
-    switch (p.tile) {
-        case kDot:
-            if (a.rows == 1) launch_dot<T, 1, 2, true>(a, s);
-            else if (a.rows == 2) launch_dot<T, 2, 2, true>(a, s);
-            else if (a.rows == 3) launch_dot<T, 3, 2, true>(a, s);
-            else launch_dot<T, 4, 2, true>(a, s);
-            break;
-        case kStream16: launch_gated_stream<T, 1>(a, p, s); break;
-        case kStream32: launch_gated_stream<T, 2>(a, p, s); break;
-        case kStream64: launch_gated_stream<T, 4>(a, p, s); break;
-        case kInner64: launch_gated_tile<T, 64, 32, 2, 1, 3, 4>(a, s); break;
-        case kTile256: launch_gated_tile<T, 256, 256, 2, 4, 2>(a, s); break;
-        case kTile128:
-            if (p.deep) launch_gated_tile<T, 128, 128, 2, 2, 4>(a, s);
-            else launch_gated_tile<T, 128, 128, 2, 2, 2>(a, s);
-            break;
-        default:
-            if (p.deep) launch_gated_tile<T, 64, 64, 2, 2, 4>(a, s);
-            else launch_gated_tile<T, 64, 64, 2, 2, 2>(a, s);
-    }
-    return join_gated<T>(a, s);
-}
-
 }  // namespace blk

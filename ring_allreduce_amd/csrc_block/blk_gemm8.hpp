@@ -16,406 +16,9 @@
 // bf16, at half the rate.
 #pragma once
 
-#include "blk_gemm.hpp"
+#include "blk_gated.hpp"
 
 namespace blk {
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-// A lane's 32 bytes of a row's 128: the same ones of both operands; which ones does not matter to
-// the sum.
-typedef i32x8 Frag;
-__device__ __forceinline__ Frag frag_of(u32x4 lo, u32x4 hi) {
-    return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-// 16 rows of Q by 16 of P, 128 deep, from nothing.
-__device__ __forceinline__ f32x4 mma8(const Frag& q, const Frag& p) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q, p, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
-}
-// The same, times 2^(sq + sp - 254) of the lane's row of either operand, on top of c.
-__device__ __forceinline__ f32x4 mma8_scaled(const Frag& q, const Frag& p, f32x4 c, uint32_t sq, uint32_t sp) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q, p, c, 0, 0, 0, (int)sq, 0, (int)sp);
-}
-// 0 if four scales are powers of two that the instruction takes: its exponent in 8 bits, 2^-127 and
-// NaN (0 and 255) not among them.
-__device__ __forceinline__ uint32_t not_power(u32x4 scales) {
-    uint32_t bad = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) bad |= (scales[k] & 0x807FFFFF) | (scales[k] - 0x00800000 < 0x7F000000 ? 0 : 1);
-    return bad;
-}
-__device__ __forceinline__ uint32_t exponent_of(float scale) { return __builtin_bit_cast(uint32_t, scale) >> 23; }
-
-// ------------------------------------------------------------------- the tiles --
-//
-// The tiles of the 16-bit products, with two 8-bit values in the place of one of 16: a tile is
-// 128 bytes deep, one block.  The scales of four blocks at a time go to LDS beside the
-// operands: 16 bytes of a row for each of P's rows, and of up to two blocks of Q's.
-
-__device__ __forceinline__ u32x4 descriptor(const void* base, uint64_t bytes) {
-    const uint64_t p = (uint64_t)uniform((const char*)base);
-    return u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFF,
-                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(bytes < kReach ? (uint32_t)bytes : kReach)), 0x00027000};
-}
-__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t offset, uint32_t to) {
-    Direct<uint16_t, false, 64, 256, false>::issue(rsrc, offset, to);
-}
-
-// Rows of an operand into the places of tiles, as Direct does it, in fewer registers: what a
-// lane loads next is THREADS / 8 rows on, so one offset serves them all, and the descriptor ends
-// with the last row.  (Whether an offset is in its range goes by the lane's part alone, which is
-// why the steps are in it.)
-template <int ROWS, int THREADS> struct Load8 {
-    static constexpr int kPieces = ROWS * 8 / THREADS;
-    u32x4 rsrc;
-    uint32_t stride;
-    // r0, r_end: rows; end: bytes of a row, whole 16-byte pieces (part of one in range would come
-    // as zeros); ld: bytes
-    __device__ __forceinline__ void start(const char* b, uint64_t ld, int r0, int r_end, int end) {
-        const int rows = max(min(r_end - r0, ROWS), 0);
-        rsrc = descriptor(b + (uint64_t)r0 * ld, rows ? (uint64_t)(rows - 1) * ld + end : 0);
-        stride = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)ld * (THREADS / 8)));
-    }
-    __device__ __forceinline__ void piece(int k, uint32_t at, uint32_t tile) const {
-        load_to_lds(rsrc, at + k * stride, tile + k * THREADS * 16);
-    }
-};
-// A thread's first byte: of row thread / 8, the 16-byte pieces permuted by the row.
-__device__ __forceinline__ int piece_of() {
-    const int thread = here();
-    return (thread & 7) ^ (thread >> 3 & 7);
-}
-
-// Which of Q's rows in the tile fragment y of a wave takes, so that a lane's results of two
-// fragments (16 rows of Q each, of which it gets four) are 8 neighbouring columns of out, and
-// those of the four lanes of a row 32: the results leave from the registers, in whole pieces of
-// 64 bytes a row.  Of a gated product the first half of the fragments are rows of the gate and the
-// second the same ones of the other projection.  Where a half is one fragment, a lane has four
-// columns.
-template <int TJ, int WJ, int FJ, bool GATED> struct Columns {
-    static constexpr int HALVES = GATED ? 2 : 1, N = FJ / HALVES > 1 ? 8 : 4, GROUPS = FJ * 4 / HALVES / N;
-    static constexpr int WIDE = TJ / WJ / HALVES;      // a wave's columns of out
-    // the first row of fragment y, and the one in it of lane r (0 .. 15)
-    static constexpr int row(int y) {
-        const int in = y % (FJ / HALVES);
-        return y / (FJ / HALVES) * (TJ / 2) + (N == 8 ? (in >> 1) * 32 + (in & 1) * 4 : 0);
-    }
-    __device__ __forceinline__ static int row_in(int r) { return N == 8 ? (r >> 2) * 8 + (r & 3) : r; }
-    // by which the 16-byte pieces of a row are permuted: another for each of 8 lanes
-    __device__ __forceinline__ static int mix(int row) { return N == 8 ? (row & 3) | (row >> 1 & 4) : row & 7; }
-};
-
-template <typename T, int TI, int TJ, int WI, int WJ, int FI, int FJ, bool GATED>
-__device__ __forceinline__ void write_direct(const GemmArgs& a, const Spot& s, const f32x4 (&acc)[FI][FJ]) {
-    typedef Columns<TJ, WJ, FJ, GATED> C;
-    constexpr int N = C::N, GROUPS = C::GROUPS, HALVES = C::HALVES;
-    const bool whole = a.splits == 1 && s.parts == 1, add = !GATED && whole && a.residual && s.g.group >= 0;
-    if (!whole && s.g.group < 0) return;        // the kernels that join the parts know
-    const int thread = here(), lane = thread & 63, wave = thread >> 6;
-    const int j0 = s.j0 + wave % WJ * C::WIDE + (lane >> 4) * N, i0 = s.i0 + wave / WJ * (TI / WI) + (lane & 15);
-    Some<T, N> bias[HALVES][GROUPS];
-#pragma unroll
-    for (int c = 0; c < GROUPS; ++c)
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-            if constexpr (GATED) bias[h][c] = whole ? gated_bias_of<T, N>(a, s.g.group, h, j0 + c * 32) : Some<T, N>{};
-            else bias[h][c] = whole ? bias_of<T, N>(a, s.g.group, j0 + c * 32) : Some<T, N>{};
-        }
-    const uint64_t part_ld = s.parts > 1 ? (uint64_t)TJ : (uint64_t)a.j * HALVES;
-    float* const part = whole ? nullptr
-                        : s.parts > 1 ? a.part + ((uint64_t)s.tile * s.parts + s.split) * (TI * TJ) + (uint64_t)(i0 - s.i0) * TJ + (j0 - s.j0)
-                                      : a.part + (uint64_t)s.split * a.part_stride + (uint64_t)i0 * part_ld + j0;
-    T* const out = (T*)a.out + (uint64_t)i0 * a.out_ld + j0;
-    T* const z = (T*)a.z + (uint64_t)i0 * a.z_ld + j0;
-    const T* const res = (const T*)a.residual + (uint64_t)i0 * a.residual_ld + j0;
-    Some<T, N> residual[GROUPS] = {}, later[GROUPS] = {};
-    const auto fetch = [&](Some<T, N> (&to)[GROUPS], int x) {
-#pragma unroll
-        for (int c = 0; c < GROUPS; ++c)
-            if (i0 + x * 16 < s.i_end && j0 + c * 32 < a.j)
-                to[c] = load_some<T, N>(res + (uint64_t)(x * 16) * a.residual_ld + c * 32, a.j - j0 - c * 32);
-    };
-    if (add) fetch(residual, 0);
-#pragma unroll
-    for (int x = 0; x < FI; ++x) {
-        if (add && x + 1 < FI) fetch(later, x + 1);
-        const uint64_t down = (uint64_t)(x * 16);
-        if (i0 + x * 16 < s.i_end)
-#pragma unroll
-            for (int c = 0; c < GROUPS; ++c) {
-                const int n = a.j - j0 - c * 32;
-                if (n <= 0) continue;
-                float v[HALVES][N];
-#pragma unroll
-                for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-                    for (int e = 0; e < N; ++e) v[h][e] = acc[x][h * (FJ / 2) + c * (N / 4) + e / 4][e % 4];
-                if (!whole) {
-#pragma unroll
-                    for (int h = 0; h < HALVES; ++h) store_wide<N>(part + down * part_ld + c * 32 + h * a.j, n, v[h]);
-                } else if constexpr (GATED) {
-                    finish_gated<T, N>(a, s.g.group, n, v[0], v[1], bias[0][c], bias[1][c], z + down * a.z_ld + c * 32,
-                                       out + down * a.out_ld + c * 32);
-                } else {
-                    finish<T, N>(a, s.g.group, n, v[0], bias[0][c], residual[c], z + down * a.z_ld + c * 32,
-                                 (char*)(out + down * a.out_ld + c * 32));
-                }
-            }
-#pragma unroll
-        for (int c = 0; c < GROUPS; ++c) residual[c] = later[c];
-    }
-}
-
-template <int TI> struct Scales {
-    static constexpr int kBytes = (TI + 64) * 16;    // a wave's load for Q's
-    u32x4 rsrc;
-    uint32_t at;                                     // this lane's row; kReach: none
-    bool mine;                                       // whether this wave loads any
-    uint32_t to;
-    template <bool GATED> __device__ __forceinline__ void start(const GemmArgs& a, const Spot& s, uint32_t room) {
-        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
-        mine = wave <= TI / 64;
-        to = room + wave * 1024;
-        const uint32_t line = (uint32_t)a.blocks * 4;
-        const float* base;
-        uint64_t bytes;
-        if (wave < TI / 64) {
-            const int r = wave * 64 + lane;
-            at = s.i0 + r < s.i_end ? (uint32_t)r * line : kReach;
-            base = a.p_scale + (uint64_t)s.i0 * a.blocks;
-            bytes = (uint64_t)(a.rows - s.i0) * line;
-        } else {
-            // of a gated product: of either half; of others the tile's columns have two at most
-            const int b = s.j0 / 128;
-            at = lane < 2 && (GATED || b + lane < a.q_rows) ? (uint32_t)(GATED ? lane * a.q_rows : lane) * line : kReach;
-            const uint64_t each = (uint64_t)a.q_rows * (GATED ? 2 : 1), group = s.g.group > 0 ? s.g.group : 0;
-            base = a.q_scale + (group * each + b) * a.blocks;
-            bytes = (each - b) * line;
-        }
-        rsrc = descriptor(base, bytes);
-    }
-    // blocks b .. b + 3 into place `which`
-    __device__ __forceinline__ void load(int b, int which) const {
-        if (mine) load_to_lds(rsrc, at == kReach ? kReach : at + (uint32_t)b * 4, to + which * kBytes);
-    }
-};
-
-// Every wave's reads of LDS are done.
-__device__ __forceinline__ void all_read() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
-
-// Nothing moves across: reads of LDS that are moved up take registers that there are none of.
-__device__ __forceinline__ void keep_order() {
-    asm volatile("" : : : "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-// EIGHT: operands in 8 bits, with scales; else in T.
-template <typename T, bool EIGHT, int TI, int TJ, int WI, int WJ, int STAGES, bool GATED>
-__global__ void __launch_bounds__(64 * WI * WJ, STAGES * (TI + TJ) * kDepth * 2 > 81920 && WI * WJ == 4 ? 1 : 2)
-tile_kernel(const GemmArgs a) {
-    constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16, HALVES = GATED ? 2 : 1;
-    constexpr int PB = TI * 128, QB = TJ * 128;
-    constexpr uint32_t PLACES = STAGES * (PB + QB), ALL = PLACES + (EIGHT ? 2 * Scales<TI>::kBytes : 0);
-    typedef Columns<TJ, WJ, FJ, GATED> C;
-    __shared__ __align__(PB) char lds[ALL];
-    BLK_LDS char* const room = (BLK_LDS char*)lds;
-    const RowTiles rows = count_tiles(a, TI);
-    Spot s;
-    if (!find_spot<true, TI, TJ / HALVES>(a, rows, blockIdx.x, s)) return;
-    const int wave = threadIdx.x >> 6;
-    const int tiles = __builtin_amdgcn_readfirstlane((s.c_end - s.c0 + kDepth - 1) / kDepth);
-    const int wi = wave / WJ * (TI / WI), wj = wave % WJ * C::WIDE;
-    Reader<false, TI> rp;
-    const uint32_t p_at = (uint32_t)(uintptr_t)room, q_at = p_at + STAGES * PB, s_at = p_at + PLACES;
-    rp.start(p_at, wi);
-    uint32_t rq[2];                          // the lane's row of fragment 0, both halves of its 128 bytes
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int row = wj + C::row_in(threadIdx.x & 15);
-        rq[h] = q_at + row * 128 + (((threadIdx.x >> 4 & 3) + h * 4) ^ C::mix(row)) * 16;
-    }
-    f32x4 acc[FI][FJ];
-#pragma unroll
-    for (int x = 0; x < FI; ++x)
-#pragma unroll
-        for (int y = 0; y < FJ; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // a, the sizes in it and the spot count pairs of values
-    typedef Load8<TI, THREADS> DP;
-    typedef Load8<TJ / HALVES, THREADS> DQ;
-    constexpr int PIECES = DP::kPieces + HALVES * DQ::kPieces;
-    DP lp;
-    DQ lq[HALVES];
-    Scales<TI> ls;
-    const char* const q = (const char*)a.q + (s.g.group > 0 ? (uint64_t)s.g.group * a.q_group * 2 : 0);
-    const int end = (s.c_end * 2 + 15) / 16 * 16;
-    lp.start((const char*)a.p, a.p_ld * 2, s.i0, s.i_end, end);
-#pragma unroll
-    for (int h = 0; h < HALVES; ++h) lq[h].start(q + h * a.q_half * 2, a.q_ld * 2, s.j0, a.j, end);
-    if constexpr (EIGHT) ls.template start<GATED>(a, s, s_at);
-    int left = (s.c_end - s.c0) * 2;         // bytes of a row
-    const int from = piece_of() * 16;        // of the 128
-    const int from_q = ((here() & 7) ^ C::mix(here() >> 3)) * 16;
-    uint32_t at_p = (uint32_t)(here() >> 3) * (uint32_t)(a.p_ld * 2) + from + s.c0 * 2;
-    uint32_t at_q = (uint32_t)(here() >> 3) * (uint32_t)(a.q_ld * 2) + from_q + s.c0 * 2;
-    const uint32_t mine = (uint32_t)__builtin_amdgcn_readfirstlane(wave * 1024);
-    // before the loads of a tile: aim(); after its P's and Q's: 128 bytes on
-    const auto aim = [&]() {
-        at_p = from >= left ? kReach : at_p;
-        at_q = from_q >= left ? kReach : at_q;
-        left -= 128;
-    };
-    constexpr int QS = HALVES * DQ::kPieces, PS = DP::kPieces;
-    const auto load_p = [&](uint32_t place, int k) { lp.piece(k, at_p, p_at + place * PB + mine); };
-    const auto load_q = [&](uint32_t place, int k) {
-        const int h = k / DQ::kPieces;
-        lq[h].piece(k % DQ::kPieces, at_q, q_at + place * QB + h * (QB / 2) + mine);
-    };
-    const int first = s.c0 / kDepth;         // block of the first tile
-    // of this lane's rows, and of the wave's columns
-    const uint32_t sp_at = s_at + (wi + (threadIdx.x & 15)) * 16;
-    const uint32_t sq_at = s_at + TI * 16 + (GATED ? 0 : wj / 128) * 16;
-    // A tile's fragments of Q are in registers throughout, those of P one block row ahead.  So Q's
-    // place is free early on: behind a barrier at block row MID the loads of the tile STAGES on
-    // go into it, and P's behind one two block rows before the end, when the last of them are
-    // read and the next tile has arrived.  (Both at once, in the second place, wait for each
-    // other.)  The last two rows are multiplied column by column, and after each column the
-    // next tile's fragment of Q takes the place of this one's.
-    constexpr int MID = FI > 2 ? FI / 4 : 0, SPAN = FI > 2 ? FI - 2 - MID : 1;
-    Frag fq[FJ], fp[FI > 4 ? 4 : FI * 2];
-    float sq[HALVES], sp[FI], sq_next[HALVES], sp_next[FI];
-    const auto read_p = [&](int slot, int x) {
-        fp[slot] = frag_of(rp.template fragment<u32x4>(x, 0), rp.template fragment<u32x4>(x, 1));
-    };
-    const auto read_q = [&](int y) {
-        u32x4 v[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) v[h] = *(const BLK_LDS u32x4*)(uintptr_t)(rq[h] + C::row(y) * 128);
-        fq[y] = frag_of(v[0], v[1]);
-    };
-    const auto read_scales = [&](int t) {
-        const uint32_t at = (uint32_t)((t >> 2 & 1) * Scales<TI>::kBytes + (t & 3) * 4);
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h) sq_next[h] = *(const BLK_LDS float*)(uintptr_t)(sq_at + at + h * 16);
-#pragma unroll
-        for (int x = 0; x < FI; ++x) sp_next[x] = *(const BLK_LDS float*)(uintptr_t)(sp_at + at + x * 256);
-    };
-    const auto use_scales = [&]() {
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h) sq[h] = sq_next[h];
-#pragma unroll
-        for (int x = 0; x < FI; ++x) sp[x] = sp_next[x];
-    };
-    // Whether all scales of the four blocks from tile t on are powers of two: a lane looks at
-    // every fourth of its rows.
-    const auto powers = [&](int t) {
-        const uint32_t at = (uint32_t)((t >> 2 & 1) * Scales<TI>::kBytes);
-        const int lane = threadIdx.x & 63;
-        uint32_t bad = 0;
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h) bad |= not_power(*(const BLK_LDS u32x4*)(uintptr_t)(sq_at + at + h * 16));
-#pragma unroll
-        for (int x = 0; x < FI; x += 4) {
-            const int block = (x + (lane >> 4)) % FI;
-            const uint32_t not_this = not_power(*(const BLK_LDS u32x4*)(uintptr_t)(sp_at + at + block * 256));
-            bad |= s.i0 + wi + block * 16 + (lane & 15) < s.i_end ? not_this : 0;
-        }
-        return __all(bad == 0);
-    };
-    constexpr int SLOTS = FI > 4 ? 4 : FI * 2;
-    int place = 0;
-    const auto tile = [&](auto power_, int t) {
-        constexpr bool POWER = decltype(power_)::value;
-        const auto multiply = [&](int x, int y, float s) {
-            const int half = y / (FJ / HALVES);
-            if constexpr (!EIGHT) {
-                typedef typename Mma<T>::V V;
-                const Frag q = fq[y], p = fp[x % SLOTS];
-                acc[x][y] = Mma<T>::run(__builtin_bit_cast(V, __builtin_shufflevector(q, q, 0, 1, 2, 3)),
-                                        __builtin_bit_cast(V, __builtin_shufflevector(p, p, 0, 1, 2, 3)), acc[x][y]);
-                acc[x][y] = Mma<T>::run(__builtin_bit_cast(V, __builtin_shufflevector(q, q, 4, 5, 6, 7)),
-                                        __builtin_bit_cast(V, __builtin_shufflevector(p, p, 4, 5, 6, 7)), acc[x][y]);
-            } else if constexpr (POWER) {
-                acc[x][y] = mma8_scaled(fq[y], fp[x % SLOTS], acc[x][y], exponent_of(sq[half]), exponent_of(s));
-            } else {
-                const float f = s * sq[half];
-                acc[x][y] = __builtin_elementwise_fma(f32x4{f, f, f, f}, mma8(fq[y], fp[x % SLOTS]), acc[x][y]);
-            }
-        };
-        // (no branches between the products: they are moved down behind them, and what they read
-        // is held until then)
-        if (EIGHT && (t & 3) == 0) ls.load(first + t + 4, (t >> 2 & 1) ^ 1);
-        aim();
-#pragma unroll
-        for (int x = 0; x < FI - 2; ++x) {
-            if (x == MID) all_read();
-            if (x >= MID)
-#pragma unroll
-                for (int k = (x - MID) * QS / SPAN; k < (x - MID + 1) * QS / SPAN; ++k) load_q(place, k);
-            read_p((x + 1) % SLOTS, x + 1);
-            if (x == FI - 3) read_p((x + 2) % SLOTS, x + 2);
-#pragma unroll
-            for (int y = 0; y < FJ; ++y) multiply(x, y, sp[x]);
-            keep_order();
-        }
-        arrived<PIECES * (STAGES - 2) + (FI > 2 ? QS : 0)>();
-        const int to = place;
-        const bool wrap = place == STAGES - 1;
-        rp.move(wrap ? -(STAGES - 1) * PB : PB);
-        rq[0] += wrap ? -(STAGES - 1) * QB : QB;
-        rq[1] += wrap ? -(STAGES - 1) * QB : QB;
-        place = wrap ? 0 : place + 1;
-        if constexpr (EIGHT) read_scales(t + 1);
-        read_p(FI % SLOTS, 0);
-        if constexpr (FI == 2) read_p(3, 1);
-#pragma unroll
-        for (int y = 0; y < FJ; ++y) {
-            multiply(FI - 2, y, sp[FI - 2]);
-            multiply(FI - 1, y, sp[FI - 1]);
-#pragma unroll
-            for (int k = y * PS / FJ; k < (y + 1) * PS / FJ; ++k) load_p(to, k);
-            if (FI == 2)
-#pragma unroll
-                for (int k = y * QS / FJ; k < (y + 1) * QS / FJ; ++k) load_q(to, k);
-            read_q(y);
-            keep_order();
-        }
-        at_p += 128;
-        at_q += 128;
-        if constexpr (FI % SLOTS != 0) {
-            fp[0] = fp[FI % SLOTS];
-            if constexpr (FI == 2) fp[1] = fp[3];
-        }
-        if constexpr (EIGHT) use_scales();
-    };
-    if (tiles > 0) {
-        if constexpr (EIGHT) ls.load(first, 0);
-#pragma unroll
-        for (int t = 0; t < STAGES; ++t) {
-            aim();
-#pragma unroll
-            for (int k = 0; k < PS; ++k) load_p(t, k);
-#pragma unroll
-            for (int k = 0; k < QS; ++k) load_q(t, k);
-            at_p += 128;
-            at_q += 128;
-        }
-        arrived<PIECES * (STAGES - 1)>();
-#pragma unroll
-        for (int y = 0; y < FJ; ++y) read_q(y);
-        read_p(0, 0);
-        if constexpr (FI == 2) read_p(1, 1);
-        if constexpr (EIGHT) {
-            read_scales(0);
-            use_scales();
-        }
-    }
-    int t = 0;
-    if constexpr (EIGHT)                     // as long as all scales are powers of two, and the rest
-        for (; t < tiles && ((t & 3) != 0 || powers(t)); ++t) tile(std::true_type(), t);
-    for (; t < tiles; ++t) tile(std::false_type(), t);
-    arrived<0>();                            // the loads past the end as well
-    write_direct<T, TI, TJ, WI, WJ, FI, FJ, GATED>(a, s, acc);
-}
 
 // ------------------------------------------------------------ few rows: one pass --
 //
@@ -504,11 +107,6 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream8_kernel(const GemmAr
 
 // -------------------------------------------------------------------- launching --
 
-template <typename T, int TI, int TJ, int WI, int WJ, int STAGES, bool GATED>
-static void launch_tile8(const GemmArgs& a, hipStream_t s) {
-    const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits;
-    tile_kernel<T, true, TI, TJ, WI, WJ, STAGES, GATED><<<grid + (unsigned)a.slots, 64 * WI * WJ, 0, s>>>(a);
-}
 template <typename T, int FI, bool GATED> static void launch_stream8(const GemmArgs& a, const GemmPlan& p, hipStream_t s) {
     const dim3 grid((unsigned)a.tiles_j, (unsigned)a.tiles_i, (unsigned)a.splits);
     const int threads = 64 * kStreamWaves;
@@ -528,17 +126,18 @@ template <typename T, bool GATED> static rr_status_t launch_gemm8(const GemmArgs
         case kStream32: launch_stream8<T, 2, GATED>(a, p, s); break;
         case kStream64: launch_stream8<T, 4, GATED>(a, p, s); break;
         case kTile256:
-            launch_tile8<T, 256, 256, 2, 4, 2, GATED>(a, s);
+            if constexpr (GATED) launch_gated_large<T, true>(a, s);
+            else launch_tile<T, true, 256, 256, 2, 4, 2, false>(a, s);
             if constexpr (!GATED)
                 if (a.slots) join_last_kernel<T, true, 256, 256><<<dim3((unsigned)a.slots / 2, 8), 256, 0, s>>>(a);
             break;
         case kTile128:
-            if (p.deep) launch_tile8<T, 128, 128, 2, 2, 4, GATED>(a, s);
-            else launch_tile8<T, 128, 128, 2, 2, 2, GATED>(a, s);
+            if (p.deep) launch_tile<T, true, 128, 128, 2, 2, 4, GATED>(a, s);
+            else launch_tile<T, true, 128, 128, 2, 2, 2, GATED>(a, s);
             break;
         default:
-            if (p.deep) launch_tile8<T, 64, 64, 2, 2, 4, GATED>(a, s);
-            else launch_tile8<T, 64, 64, 2, 2, 2, GATED>(a, s);
+            if (p.deep) launch_tile<T, true, 64, 64, 2, 2, 4, GATED>(a, s);
+            else launch_tile<T, true, 64, 64, 2, 2, 2, GATED>(a, s);
     }
     if constexpr (GATED) {
         return join_gated<T>(a, s);
