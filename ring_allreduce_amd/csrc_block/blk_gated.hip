@@ -22,37 +22,70 @@ struct GateArgs {
     int32_t n, act, splits, threads, blocks;
 };
 
-// 8 columns of one half of z.
-template <typename T, bool EIGHT> struct Half {
-    u32x4 raw;
-    float scale;
-    __device__ __forceinline__ void load(const GateArgs& a, int r, int half, int col) {
-        if constexpr (EIGHT) {
-            const uint8_t* from = (const uint8_t*)a.z + (uint64_t)r * a.z_ld + (uint64_t)half * a.n + col;
-            const auto v = __builtin_bit_cast(Words<8>::V, load_some<uint8_t, 8>(from, a.n - col));
-            raw = u32x4{v[0], v[1], 0, 0};
-            scale = a.z_scale[((uint64_t)r * 2 + half) * a.blocks + col / 128];
-        } else {
-            const T* from = (const T*)a.z + (uint64_t)r * a.z_ld + (uint64_t)half * a.n + col;
-            raw = __builtin_bit_cast(u32x4, load_some<T, 8>(from, a.n - col));
+// act(z) and its slope at once: the exponential is most of either.
+template <int ACT> __device__ __forceinline__ void gate_of(float z, float& value, float& slope) {
+    if constexpr (ACT == RR_ACT_GELU) {
+        const float a = magnitude(z);
+        float tail;
+        const float e = normal_tail(a, &tail);
+        value = fmaxf(z, 0.0f) - a * tail;
+        slope = (z > 0.0f ? 1.0f - tail : tail) + copysignf(a, z) * e * 0.39894228040143268f;
+    } else if constexpr (ACT == RR_ACT_SILU) {
+        const float q = logistic(z);
+        value = z * q;
+        slope = q * (1.0f + z * (1.0f - q));
+    } else if constexpr (ACT == RR_ACT_SIGMOID) {
+        value = logistic(z);
+        slope = value * (1.0f - value);
+    } else {
+        value = act_of<ACT>(z);
+        slope = slope_of<ACT>(z);
+    }
+}
+
+// 8 columns of both halves of z and of dout.
+template <typename T, bool EIGHT> struct GateRow {
+    u32x4 dout, z[2];
+    float scale[2];
+    // WHOLE: all of the 8 are there
+    template <bool WHOLE> __device__ __forceinline__ void load(const GateArgs& a, int r, int col) {
+        const T* d = (const T*)a.dout + (uint64_t)r * a.dout_ld + col;
+        if constexpr (WHOLE) dout = load_raw(d);
+        else dout = a.dout ? __builtin_bit_cast(u32x4, load_some<T, 8>(d, a.n - col)) : u32x4{};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (EIGHT) {
+                const uint8_t* from = (const uint8_t*)a.z + (uint64_t)r * a.z_ld + (uint64_t)h * a.n + col;
+                Words<8>::V v;
+                if constexpr (WHOLE) v = ((const LooseWords<uint8_t, 8>*)from)->v;
+                else v = __builtin_bit_cast(Words<8>::V, load_some<uint8_t, 8>(from, a.n - col));
+                z[h] = u32x4{v[0], v[1], 0, 0};
+                scale[h] = a.z_scale[((uint64_t)r * 2 + h) * a.blocks + col / 128];
+            } else {
+                const T* from = (const T*)a.z + (uint64_t)r * a.z_ld + (uint64_t)h * a.n + col;
+                if constexpr (WHOLE) z[h] = load_raw(from);
+                else z[h] = __builtin_bit_cast(u32x4, load_some<T, 8>(from, a.n - col));
+            }
         }
     }
-    __device__ __forceinline__ void values(float (&v)[8]) const {
+    __device__ __forceinline__ void values(int h, float (&v)[8]) const {
         if constexpr (EIGHT) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[h], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[h], true);
-                v[h * 4] = lo[0] * scale, v[h * 4 + 1] = lo[1] * scale, v[h * 4 + 2] = hi[0] * scale, v[h * 4 + 3] = hi[1] * scale;
+            for (int k = 0; k < 2; ++k) {
+                const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)z[h][k], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)z[h][k], true);
+                v[k * 4] = lo[0] * scale[h], v[k * 4 + 1] = lo[1] * scale[h], v[k * 4 + 2] = hi[0] * scale[h], v[k * 4 + 3] = hi[1] * scale[h];
             }
         } else {
-            const Vec<T> e = vec_of<T>(raw);
+            const Vec<T> e = vec_of<T>(z[h]);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = (float)e.e[k];
         }
     }
 };
 
-template <typename T, bool EIGHT> __global__ void __launch_bounds__(256) gate_kernel(const GateArgs a) {
+// Bound by memory: 16384 x 4096 in bf16, 671 MB in @TIME@ us (@RATE@ TB/s; one row's loads at a
+// time, behind a branch, 219).
+template <typename T, bool EIGHT, int ACT> __global__ void __launch_bounds__(256) gate_kernel(const GateArgs a) {
     __shared__ float lds[8][256];
     const int wide = a.threads, high = 256 / wide;      // threads across and along the rows
     const int x = (int)threadIdx.x % wide, y = (int)threadIdx.x / wide;
@@ -68,45 +101,59 @@ template <typename T, bool EIGHT> __global__ void __launch_bounds__(256) gate_ke
         return;
     }
     float sum[2][8] = {};
-    const auto row = [&](int r, const Half<T, EIGHT>& gate, const Half<T, EIGHT>& other, const Some<T, 8>& dout) {
-        float gv[8], uv[8], s[8], d[8];
-        gate.values(gv);
-        other.values(uv);
+    typedef GateRow<T, EIGHT> Row;
+    const auto row = [&](int r, const Row& in, auto whole_) {
+        const int n = decltype(whole_)::value ? 8 : left;
+        float g[8], u[8], s[8];
+        in.values(0, g);
+        in.values(1, u);
+        const Vec<T> d = vec_of<T>(in.dout);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] = gv[e], d[e] = (float)dout.e[e];
-        act_slopes(a.act, s);
-        act_values(a.act, gv);
+        for (int e = 0; e < 8; ++e) gate_of<ACT>(g[e], g[e], s[e]);
         if (a.out) {
             float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = gv[e] * uv[e];
-            store_some<T, 8>((T*)a.out + (uint64_t)r * a.out_ld + col, left, o);
+            for (int e = 0; e < 8; ++e) o[e] = g[e] * u[e];
+            store_some<T, 8>((T*)a.out + (uint64_t)r * a.out_ld + col, n, o);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            s[e] *= d[e] * uv[e];
-            gv[e] *= d[e];
+            s[e] *= (float)d.e[e] * u[e];
+            g[e] *= (float)d.e[e];
             sum[0][e] += s[e];
-            sum[1][e] += gv[e];
+            sum[1][e] += g[e];
         }
         if (a.dz) {
             T* const to = (T*)a.dz + (uint64_t)r * a.dz_ld;
-            store_some<T, 8>(to + col, left, s);
-            store_some<T, 8>(to + a.n + col, left, gv);
+            store_some<T, 8>(to + col, n, s);
+            store_some<T, 8>(to + a.n + col, n, g);
             // zeros behind the row's 2 n columns
             if (left <= 8)
                 for (uint64_t c = 2 * (uint64_t)a.n; c < a.dz_ld; ++c) to[c] = (T)0.0f;
         }
     };
-    if (left > 0)
-        for (int r = lo + y; r < hi; r += high) {
-            Half<T, EIGHT> gate, other;
-            gate.load(a, r, 0, col);
-            other.load(a, r, 1, col);
-            Some<T, 8> dout = {};
-            if (a.dout) dout = load_some<T, 8>((const T*)a.dout + (uint64_t)r * a.dout_ld + col, left);
-            row(r, gate, other, dout);
+    if (left >= 8 && a.dout) {
+        constexpr int U = 4;                            // rows on their way
+        int r = lo + y;
+        for (; r + (U - 1) * high < hi; r += U * high) {
+            Row in[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) in[u].template load<true>(a, r + u * high, col);
+#pragma unroll
+            for (int u = 0; u < U; ++u) row(r + u * high, in[u], std::true_type());
         }
+        for (; r < hi; r += high) {
+            Row in;
+            in.template load<true>(a, r, col);
+            row(r, in, std::true_type());
+        }
+    } else if (left > 0) {
+        for (int r = lo + y; r < hi; r += high) {
+            Row in;
+            in.template load<false>(a, r, col);
+            row(r, in, std::false_type());
+        }
+    }
     if (!a.part) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -125,6 +172,16 @@ template <typename T, bool EIGHT> __global__ void __launch_bounds__(256) gate_ke
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (e < left) to[col + e] = sum[h][e];
+    }
+}
+
+template <typename T, bool EIGHT> static void launch_gate(const GateArgs& k, const dim3& grid, hipStream_t s) {
+    switch (k.act) {
+        case RR_ACT_RELU: gate_kernel<T, EIGHT, RR_ACT_RELU><<<grid, 256, 0, s>>>(k); break;
+        case RR_ACT_GELU: gate_kernel<T, EIGHT, RR_ACT_GELU><<<grid, 256, 0, s>>>(k); break;
+        case RR_ACT_SILU: gate_kernel<T, EIGHT, RR_ACT_SILU><<<grid, 256, 0, s>>>(k); break;
+        case RR_ACT_SIGMOID: gate_kernel<T, EIGHT, RR_ACT_SIGMOID><<<grid, 256, 0, s>>>(k); break;
+        default: gate_kernel<T, EIGHT, RR_ACT_NONE><<<grid, 256, 0, s>>>(k);
     }
 }
 
@@ -512,14 +569,8 @@ static rr_status_t gated_backward(const rr_linear8_t* a, const rr_gated_grad_t* 
         const unsigned ranges = (unsigned)l.groups + (l.offsets && g->out.data ? 2 : 0);
         const dim3 grid((unsigned)ceil_div(l.n, (uint64_t)k.threads * 8), (unsigned)k.splits, ranges);
         const bool b16 = l.dt == RR_BF16;
-        if (a->z_scales) {
-            if (b16) gate_kernel<bf16, true><<<grid, 256, 0, s>>>(k);
-            else gate_kernel<f16, true><<<grid, 256, 0, s>>>(k);
-        } else if (b16) {
-            gate_kernel<bf16, false><<<grid, 256, 0, s>>>(k);
-        } else {
-            gate_kernel<f16, false><<<grid, 256, 0, s>>>(k);
-        }
+        if (a->z_scales) b16 ? launch_gate<bf16, true>(k, grid, s) : launch_gate<f16, true>(k, grid, s);
+        else b16 ? launch_gate<bf16, false>(k, grid, s) : launch_gate<f16, false>(k, grid, s);
         if ((st = launched()) != RR_OK) return st;
         if (plan.part) {
             const dim3 sums((unsigned)ceil_div(both.n, 16), (unsigned)l.groups);
