@@ -83,13 +83,17 @@ template <typename T, bool EIGHT> struct GateRow {
     }
 };
 
-// Bound by memory: 16384 x 4096 in bf16, 671 MB in @TIME@ us (@RATE@ TB/s; one row's loads at a
-// time, behind a branch, 219).
+// Bound by memory: 16384 x 4096 in bf16, 671 MB in 141 us (4.8 TB/s; one row's loads at a time,
+// behind a branch, 219).
 template <typename T, bool EIGHT, int ACT> __global__ void __launch_bounds__(256) gate_kernel(const GateArgs a) {
     __shared__ float lds[8][256];
     const int wide = a.threads, high = 256 / wide;      // threads across and along the rows
     const int x = (int)threadIdx.x % wide, y = (int)threadIdx.x / wide;
-    const int col = ((int)blockIdx.x * wide + x) * 8, left = a.n - col;
+    const int own = ((int)blockIdx.x * wide + x) * 8;
+    // The last columns' thread takes the last 8, some of them its neighbour's too, which get the
+    // same values twice; but not across the border of two scales.
+    const bool back = own < a.n && own + 8 > a.n && a.n >= 8 && !(EIGHT && (a.n & 127) < 8);
+    const int col = back ? a.n - 8 : own, left = a.n - col;
     const bool none = (int)blockIdx.z >= a.g.groups;    // the rows of no group
     const Range g = range_of(a.g, none ? ((int)blockIdx.z == a.g.groups ? 0 : a.g.groups + 1) : (int)blockIdx.z + 1);
     const int per = (g.hi - g.lo + a.splits - 1) / a.splits;
@@ -171,7 +175,7 @@ template <typename T, bool EIGHT, int ACT> __global__ void __launch_bounds__(256
         if (y == 0)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (e < left) to[col + e] = sum[h][e];
+                if (e < left && col + e >= own) to[col + e] = sum[h][e];
     }
 }
 
@@ -327,8 +331,14 @@ static rr_status_t run_forward(const rr_linear8_t* a, uint64_t halves, void* wor
     k.bias = l.bias;
     k.residual = l.residual.data;
     k.residual_ld = l.residual.ld;
-    k.z = l.z.data;
-    k.z_ld = l.z.ld;
+    if (a->z_scales) {
+        k.z8 = (uint8_t*)l.z.data;
+        k.z8_ld = l.z.ld;
+        k.z8_scale = a->z_scales;
+    } else {
+        k.z = l.z.data;
+        k.z_ld = l.z.ld;
+    }
     k.out = l.out.data;
     k.out_ld = l.out.ld;
     k.act = l.act;
@@ -388,16 +398,18 @@ static rr_status_t check_forward(const rr_linear8_t* a, uint64_t halves) {
     return x8 != w8 || (halves == 1 && !x8) ? RR_ERR_INVALID : RR_OK;
 }
 
-// z in 16 bits, where its 8-bit form is made from.
-static uint64_t z_room(const rr_linear8_t* a) {
-    return a->z_scales ? ceil_div(a->l.rows * a->l.n * 2 * 2, 256) * 256 : 0;
+// z in 16 bits, where its 8-bit form is made from: 256 x 256 tiles have whole blocks of it.
+static uint64_t z_room(const rr_linear8_t* a, const Forward& f) {
+    const bool apart = a->z_scales && (f.plan.tile != kTile256 || f.splits > 1);
+    return apart ? ceil_div(a->l.rows * a->l.n * 2 * 2, 256) * 256 : 0;
 }
 
 static rr_status_t forward(const rr_linear8_t* a, uint64_t halves, void* workspace, size_t workspace_bytes, hipStream_t s) {
     const rr_status_t st = check_forward(a, halves);
     if (st != RR_OK) return st;
     const rr_linear_t& l = a->l;
-    const uint64_t own = z_room(a), need = forward_of(a, halves).bytes() + own;
+    const Forward f = forward_of(a, halves);
+    const uint64_t own = z_room(a, f), need = f.bytes() + own;
     if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need)) return RR_ERR_INVALID;
     if (!rows_ok(l.out, l.rows, l.n, 2) || !rows_ok_if(l.residual, l.rows, l.n, 2) || !aligned_to(l.bias, 2))
         return RR_ERR_INVALID;
@@ -414,7 +426,7 @@ static rr_status_t forward(const rr_linear8_t* a, uint64_t halves, void* workspa
     for (int o = same ? 1 : 0; o < 4; ++o)
         if (overlap(l.residual.data, n_res, out[o].p, out[o].n)) return RR_ERR_INVALID;
     if (l.rows == 0) return RR_OK;
-    if (!a->z_scales) return run_forward(a, halves, workspace, s);
+    if (!own) return run_forward(a, halves, workspace, s);
     rr_linear8_t b = *a;
     b.l.z = {workspace, l.n * 2};
     b.z_scales = nullptr;
@@ -622,7 +634,8 @@ rr_status_t block_gated_workspace(const rr_linear8_t* a, size_t* bytes) {
     if (!bytes) return RR_ERR_INVALID;
     const rr_status_t st = check_forward(a, 2);
     if (st != RR_OK) return st;
-    *bytes = forward_of(a, 2).bytes() + z_room(a);
+    const Forward f = forward_of(a, 2);
+    *bytes = f.bytes() + z_room(a, f);
     return RR_OK;
 }
 

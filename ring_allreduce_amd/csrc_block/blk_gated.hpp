@@ -15,7 +15,7 @@ template <typename T, int TI, int TJ> __global__ void __launch_bounds__(256) joi
     if (!find_spot<true, TI, TJ / 2>(a, rows, whole + blockIdx.x, s)) return;
     constexpr int GROUPS = TJ / 16;
     const int col = (int)threadIdx.x % GROUPS * 8, j = s.j0 + col;
-    if (j >= a.j) return;
+    if (j >= a.j && !a.z8) return;           // with z in 8 bits the row's threads stay together
     const Some<T, 8> g_bias = gated_bias_of<T, 8>(a, s.g.group, 0, j), u_bias = gated_bias_of<T, 8>(a, s.g.group, 1, j);
     for (int row = (int)(blockIdx.y * 32 + threadIdx.x / GROUPS), k = 0; k < 32; k += 256 / GROUPS, row += 256 / GROUPS) {
         const int i = s.i0 + row;
@@ -34,6 +34,28 @@ template <typename T, int TI, int TJ> __global__ void __launch_bounds__(256) joi
                     }
                 }
             }
+        if (a.z8) {                          // 16 threads have the row's block
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float r[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[h][e] = s.g.group < 0 ? 0.0f : v[h][e] + (float)(h ? u_bias : g_bias).e[e];
+                    r[e] = j + e < a.j ? (float)(T)v[h][e] : 0.0f;
+                }
+                float size = largest_of(r);
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) size = fmaxf(size, __shfl_xor(size, d));
+                const float scale = scale_of(size);
+                if (col == 0) a.z8_scale[((uint64_t)i * 2 + h) * a.q_rows + s.j0 / 128] = scale;
+                if (j < a.j) store_eight(a.z8 + (uint64_t)i * a.z8_ld + (uint64_t)h * a.j + j, a.j - j, narrow(r, inverse_of(scale)));
+            }
+            act_values(a.act, v[0]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[0][e] *= v[1][e];
+            if (j < a.j) store_some<T, 8>((T*)a.out + (uint64_t)i * a.out_ld + j, a.j - j, v[0]);
+            continue;
+        }
         finish_gated<T, 8>(a, s.g.group, a.j - j, v[0], v[1], g_bias, u_bias, (T*)a.z + (uint64_t)i * a.z_ld + j,
                            (T*)a.out + (uint64_t)i * a.out_ld + j);
     }

@@ -51,6 +51,10 @@ struct GemmArgs {
     const float *p_scale, *q_scale;
     int32_t blocks;                  // along the contraction
     int32_t q_rows;                  // blocks of 128 rows in Q, each half of a gated one
+    // of a gated product whose z is kept in 8 bits (z is null then), by 256 x 256 tiles only
+    uint8_t* z8;
+    float* z8_scale;                 // [rows][2][q_rows]
+    uint64_t z8_ld;
 };
 
 // What the host chose for one product; see blk_linear.hip.
@@ -473,6 +477,50 @@ __device__ __forceinline__ void finish_gated(const GemmArgs& a, int group, int i
     if (j >= a.j) return;
     finish_gated<T, N>(a, group, a.j - j, g, u, gated_bias_of<T, N>(a, group, 0, j), gated_bias_of<T, N>(a, group, 1, j),
                        (T*)a.z + (uint64_t)i * a.z_ld + j, (T*)a.out + (uint64_t)i * a.out_ld + j);
+}
+
+// ------------------------------------------------------------------ 8-bit values --
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// The least power of two p with a / p <= 448 = 1.75 * 2^8, at least 2^-126; 1 for 0.  Its
+// exponent is a's less 8, or less 7 where a's mantissa is over 1.75.
+__device__ __forceinline__ float scale_of(float a) {
+    const uint32_t bits = __builtin_bit_cast(uint32_t, a);
+    const int e = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFF) > 0x600000);
+    return a == 0.0f ? 1.0f : __builtin_bit_cast(float, (uint32_t)max(e, 1) << 23);
+}
+// 1 / p: exponents 254 - e of e = 1 .. 247
+__device__ __forceinline__ float inverse_of(float scale) {
+    return __builtin_bit_cast(float, 0x7F000000u - __builtin_bit_cast(uint32_t, scale));
+}
+// The largest finite magnitude.
+__device__ __forceinline__ float largest_of(const float (&v)[8]) {
+    float a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(v[e]) < INFINITY ? fabsf(v[e]) : 0.0f);
+    return a;
+}
+// In e4m3, times 1 / p: exact but for the rounding to e4m3.
+__device__ __forceinline__ u32x2 narrow(const float (&v)[8], float inverse) {
+    u32x2 w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = fabsf(v[h * 4 + e]) < INFINITY ? v[h * 4 + e] * inverse : NAN;
+        int word = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+        word = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], word, true);
+        w[h] = (uint32_t)word;
+    }
+    return w;
+}
+__device__ __forceinline__ void store_eight(uint8_t* p, int n, u32x2 v) {
+    if (n >= 8) {
+        ((LooseWords<uint8_t, 8>*)p)->v = v;
+    } else {
+        for (int e = 0; e < n; ++e) p[e] = (uint8_t)(v[e >> 2] >> (e & 3) * 8);
+    }
 }
 
 // ------------------------------------------------------------- where a tile is --

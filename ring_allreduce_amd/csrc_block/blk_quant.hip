@@ -6,7 +6,6 @@
 
 namespace blk {
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // 8 neighbouring columns in 32 bits.
@@ -25,54 +24,21 @@ template <typename T> struct Eight {
     __device__ __forceinline__ float value(int e) const {
         return (float)vec_of<T>(raw[e / Vec<T>::N]).e[e % Vec<T>::N];
     }
-    // the largest finite magnitude
-    __device__ __forceinline__ float size() const {
-        float a = 0.0f;
+    __device__ __forceinline__ void values(float (&v)[8]) const {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float v = fabsf(value(e));
-            a = fmaxf(a, v < INFINITY ? v : 0.0f);
-        }
-        return a;
+        for (int e = 0; e < 8; ++e) v[e] = value(e);
     }
-    // in e4m3, times 2^-p: exact but for the rounding to e4m3
-    __device__ __forceinline__ u32x2 narrow(float inverse) const {
-        u32x2 v;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float f[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f[e] = value(h * 4 + e);
-                f[e] = fabsf(f[e]) < INFINITY ? f[e] * inverse : NAN;
-            }
-            int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-            w = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
-            v[h] = (uint32_t)w;
-        }
-        return v;
+    __device__ __forceinline__ float size() const {
+        float v[8];
+        values(v);
+        return largest_of(v);
+    }
+    __device__ __forceinline__ u32x2 e4m3(float inverse) const {
+        float v[8];
+        values(v);
+        return narrow(v, inverse);
     }
 };
-
-// The least power of two p with a / p <= 448 = 1.75 * 2^8, at least 2^-126; 1 for 0.  Its
-// exponent is a's less 8, or less 7 where a's mantissa is over 1.75.
-__device__ __forceinline__ float scale_of(float a) {
-    const uint32_t bits = __builtin_bit_cast(uint32_t, a);
-    const int e = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFF) > 0x600000);
-    return a == 0.0f ? 1.0f : __builtin_bit_cast(float, (uint32_t)max(e, 1) << 23);
-}
-// 1 / p: exponents 254 - e of e = 1 .. 247
-__device__ __forceinline__ float inverse_of(float scale) {
-    return __builtin_bit_cast(float, 0x7F000000u - __builtin_bit_cast(uint32_t, scale));
-}
-
-__device__ __forceinline__ void store_eight(uint8_t* row, int at, int len, u32x2 v) {
-    if (at + 8 <= len) {
-        ((LooseWords<uint8_t, 8>*)(row + at))->v = v;
-    } else {
-        for (int e = 0; at + e < len; ++e) row[at + e] = (uint8_t)(v[e >> 2] >> (e & 3) * 8);
-    }
-}
 
 __device__ __forceinline__ float largest_of_16_lanes(float a) {
 #pragma unroll
@@ -94,7 +60,7 @@ template <typename T> __global__ void __launch_bounds__(256) quantize_rows_kerne
         else v.load_some(from, col, a.width);
         const float scale = scale_of(largest_of_16_lanes(v.size()));
         if (col < a.width)
-            store_eight(a.narrow + group * a.narrow_group + row * a.narrow_ld, col, a.width, v.narrow(inverse_of(scale)));
+            store_eight(a.narrow + group * a.narrow_group + row * a.narrow_ld + col, a.width - col, v.e4m3(inverse_of(scale)));
         if (lane == 0) a.scales[id] = scale;
     }
 }
@@ -131,7 +97,7 @@ template <typename T> __global__ void __launch_bounds__(256) quantize_square_ker
     for (int k = 0; k < 8; ++k) {
         const uint64_t row = row0 + k * 16 + y;
         if (row < a.rows)
-            store_eight(a.narrow + group * a.narrow_group + row * a.narrow_ld, col, a.width, v[k].narrow(inverse_of(scale)));
+            store_eight(a.narrow + group * a.narrow_group + row * a.narrow_ld + col, a.width - col, v[k].e4m3(inverse_of(scale)));
     }
 }
 

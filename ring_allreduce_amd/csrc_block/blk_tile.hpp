@@ -91,10 +91,70 @@ template <int TJ, int WJ, int FJ, bool GATED> struct Columns {
     __device__ __forceinline__ static int mix(int row) { return N == 8 ? (row & 3) | (row >> 1 & 4) : row & 7; }
 };
 
+// Of a gated 256 x 256 tile, whose 128 columns of either half are a block of z: the largest
+// magnitudes of z, rounded to T, in the blocks' rows, by the waves and then all of them through
+// LDS; scales, z in 8 bits, and out.
+template <typename T, int TI, int WI, int WJ, int FI, int FJ>
+__device__ __forceinline__ void write_eight(const GemmArgs& a, const Spot& s, BLK_LDS char* room, const f32x4 (&acc)[FI][FJ]) {
+    static_assert(WJ * 32 == 128 && FJ == 4, "the columns of a block");
+    const int thread = here(), lane = thread & 63, wave = thread >> 6;
+    const int row = wave / WJ * (TI / WI) + (lane & 15), part = wave % WJ;
+    const int j = s.j0 + part * 32 + (lane >> 4) * 8, n = a.j - j, i0 = s.i0 + row;
+    const Some<T, 8> bias[2] = {gated_bias_of<T, 8>(a, s.g.group, 0, j), gated_bias_of<T, 8>(a, s.g.group, 1, j)};
+    BLK_LDS float* const sizes = (BLK_LDS float*)room;         // [half][part][row]
+    const auto z_of = [&](int x, int h, float (&v)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = s.g.group < 0 ? 0.0f : acc[x][h * 2 + e / 4][e % 4] + (float)bias[h].e[e];
+    };
+#pragma unroll
+    for (int x = 0; x < FI; ++x)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+            z_of(x, h, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (float)(T)v[e];
+            float size = largest_of(v);
+            size = fmaxf(size, __shfl_xor(size, 16));
+            size = fmaxf(size, __shfl_xor(size, 32));
+            if (lane < 16) sizes[(h * WJ + part) * TI + row + x * 16] = size;
+        }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < FI; ++x) {
+        const int i = i0 + x * 16;
+        if (i >= s.i_end) continue;
+        float v[2][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float size = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WJ; ++w) size = fmaxf(size, sizes[(h * WJ + w) * TI + row + x * 16]);
+            const float scale = scale_of(size);
+            if (part == 0 && lane < 16) a.z8_scale[((uint64_t)i * 2 + h) * a.q_rows + s.j0 / 128] = scale;
+            float r[8];
+            z_of(x, h, v[h]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[e] = (float)(T)v[h][e];
+            if (n > 0) store_eight(a.z8 + (uint64_t)i * a.z8_ld + (uint64_t)h * a.j + j, n, narrow(r, inverse_of(scale)));
+        }
+        act_values(a.act, v[0]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[0][e] *= v[1][e];
+        if (n > 0) store_some<T, 8>((T*)a.out + (uint64_t)i * a.out_ld + j, n, v[0]);
+    }
+}
+
 template <typename T, int TI, int TJ, int WI, int WJ, int FI, int FJ, bool GATED>
-__device__ __forceinline__ void write_direct(const GemmArgs& a, const Spot& s, const f32x4 (&acc)[FI][FJ]) {
+__device__ __forceinline__ void write_direct(const GemmArgs& a, const Spot& s, BLK_LDS char* room, const f32x4 (&acc)[FI][FJ]) {
     typedef Columns<TJ, WJ, FJ, GATED> C;
     constexpr int N = C::N, GROUPS = C::GROUPS, HALVES = C::HALVES;
+    if constexpr (GATED && TI == 256)
+        if (a.z8 && s.parts == 1) {
+            write_eight<T, TI, WI, WJ, FI, FJ>(a, s, room, acc);
+            return;
+        }
     const bool whole = a.splits == 1 && s.parts == 1, add = !GATED && whole && a.residual && s.g.group >= 0;
     if (!whole && s.g.group < 0) return;        // the kernels that join the parts know
     const int thread = here(), lane = thread & 63, wave = thread >> 6;
@@ -418,7 +478,7 @@ tile_kernel(const GemmArgs a) {
         for (; t < tiles && ((t & 3) != 0 || powers(t)); ++t) tile(std::true_type(), t);
     for (; t < tiles; ++t) tile(std::false_type(), t);
     arrived<0>();                            // the loads past the end as well
-    write_direct<T, TI, TJ, WI, WJ, FI, FJ, GATED>(a, s, acc);
+    write_direct<T, TI, TJ, WI, WJ, FI, FJ, GATED>(a, s, room, acc);
 }
 
 template <typename T, bool EIGHT, int TI, int TJ, int WI, int WJ, int STAGES, bool GATED>
