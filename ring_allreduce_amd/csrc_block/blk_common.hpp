@@ -53,7 +53,7 @@ __device__ __forceinline__ u32x4 zero_unless(bool keep, u32x4 v) {
     for (int i = 0; i < 4; ++i) v[i] = keep ? v[i] : 0u;
     return v;
 }
-// v without its first `skip` bytes (a multiple of 2, 0 .. 16), zeros behind.
+// v without its first `skip` bytes (0 .. 16), zeros behind.
 __device__ __forceinline__ u32x4 drop_first(u32x4 v, int skip) {
     const uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
     const int n = (skip & 7) * 8;

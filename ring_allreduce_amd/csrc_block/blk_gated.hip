@@ -290,11 +290,12 @@ static Forward forward_of(const rr_linear8_t* a, uint64_t halves) {
     Forward f = {};
     f.plan = choose(&l, kForward, &f.splits, &f.slots);
     f.plan.form = kForward;
-    if (eight && f.plan.tile == kDot) f.plan.tile = kStream16;
     if (eight && f.plan.tile == kInner64) f.plan.tile = kStream64, f.plan.narrow = 0;
     if (halves == 2) f.plan.narrow = 0;
     f.plan.direct = good_x && good_w;
-    if (f.plan.tile == kStream16 && !eight && !f.plan.direct && l.groups == 1 && !l.offsets && l.rows <= 4)
+    // the one-pass form takes 8-bit rows at any byte, but of no less than a piece
+    if (eight && !f.plan.direct && a->l.k < 16 && f.plan.tile >= kStream16) f.plan.tile = kTile64, f.splits = 1;
+    if (f.plan.tile == kStream16 && !f.plan.direct && l.groups == 1 && !l.offsets && l.rows <= 4)
         f.plan.tile = kDot;
     if (f.plan.tile == kDot) f.splits = 1;
     if (f.splits > 1) f.parts = ceil_div((uint64_t)f.splits * l.rows * l.n * sizeof(float), 256) * 256;

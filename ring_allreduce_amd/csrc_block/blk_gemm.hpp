@@ -940,6 +940,11 @@ template <typename T, int R, bool DIRECT> struct Strip {
                     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, kReach, 0x00027000);
                     v[s][f] = __builtin_amdgcn_raw_buffer_load_b128(
                         rsrc, c < c_end ? at[f] + (uint32_t)c * (uint32_t)sizeof(T) : kReach, 0, 0);
+                } else if constexpr (sizeof(T) == 1) {
+                    // rows of at least 16 bytes: whole pieces, the last one's without its first
+                    const int y = row + f * 16 + (lane & 15), from = min(c, c_end - 16);
+                    const u32x4 t = load_raw(base + (uint64_t)min(y, row_end - 1) * ld + from);
+                    v[s][f] = zero_unless(y < row_end, drop_first(t, min(c - from, 16)));
                 } else {
                     Vec<T> t;
 #pragma unroll
