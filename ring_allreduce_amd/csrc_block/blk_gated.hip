@@ -273,6 +273,46 @@ struct Forward {
     uint64_t bytes() const { return parts + tiles + x_bytes + w_bytes; }
 };
 
+// Few rows of 8-bit operands (of up to 64, `n` columns of both halves): microseconds on weights in
+// no cache.  One row goes as dots.  Up to 16 the one-pass form, 16 columns a workgroup where it
+// has them (3 x 8192 x 8192 17.2, 16 x 4096 x 4096 8.4), but of more than 8 by large weights 64 x
+// 64 tiles, deep, and parts of the contraction to fill the device (16 x 8192 x 8192 18.9 against
+// 21).  Up to 32 the one-pass form for weights under 48 MB (32 x 4096 x 4096 11.1, tiles 12.3; 32 x
+// 8192 x 8192 30 and 20.3), and tiles beyond (48 x 4096 x 4096 12.7, one pass 17; 64 x 8192 x 8192
+// 21 and 40).  Rows of many groups, where the weights' read is all, the same: to 16 a group the
+// one pass (256 over 32 groups of 2 x 2048 x 4096 124, tiles 126, 32 rows a pass 155), then deep
+// tiles (512 rows 126, 32 rows a pass 172, tiles with two stages 137).
+// `direct`: operands of whole 16-byte pieces; the tiles copy others first.
+static void choose_few(const rr_linear8_t* a, uint64_t halves, bool direct, Forward& f) {
+    const rr_linear_t& l = a->l;
+    const uint64_t n = l.n * halves, steps = ceil_div(l.k, kBlock), mean = ceil_div(l.rows, l.groups);
+    const bool one = l.groups == 1 && !l.offsets, large = direct && n * l.k >= 48u << 20;
+    GemmPlan& p = f.plan;
+    const auto parts = [&](uint64_t blocks, uint64_t most) {
+        uint64_t s = 1;
+        while (one && s < 16 && blocks * s * 2 <= kSlots && s * 2 <= most) s *= 2;
+        f.splits = (int)s;
+    };
+    p.narrow = p.deep = 0;
+    f.slots = 0;
+    if (one && l.rows == 1) {
+        p.tile = kDot;
+        f.splits = 1;
+    } else if (mean <= 16 && !(one && halves == 1 && mean > 8 && large)) {
+        p.tile = kStream16;
+        p.narrow = halves == 1 && one;
+        parts(ceil_div(n, p.narrow ? 16 : 32), ceil_div(n, 32) <= 32 && !p.narrow ? l.k / 512 : 1);
+    } else if (one && mean <= 32 && !large) {
+        p.tile = kStream32;
+        p.narrow = halves == 1 && n >= 4096 && n < 8192;
+        parts(ceil_div(n, p.narrow ? 16 : 32), l.k / 512);
+    } else {
+        p.tile = kTile64;
+        p.deep = 1;
+        parts(ceil_div(n, 64), steps >= 16 ? steps / 4 : 1);
+    }
+}
+
 static Forward forward_of(const rr_linear8_t* a, uint64_t halves) {
     const bool eight = a->x_scales != nullptr;
     rr_linear_t l = a->l;
@@ -290,12 +330,19 @@ static Forward forward_of(const rr_linear8_t* a, uint64_t halves) {
     Forward f = {};
     f.plan = choose(&l, kForward, &f.splits, &f.slots);
     f.plan.form = kForward;
-    if (eight && f.plan.tile == kInner64) f.plan.tile = kStream64, f.plan.narrow = 0;
-    if (halves == 2) f.plan.narrow = 0;
+    const uint64_t mean = ceil_div(l.rows, l.groups);
+    if (eight && mean <= 64) {
+        choose_few(a, halves, good_x && good_w, f);
+    } else if (halves == 2) {
+        f.plan.narrow = 0;
+        // as choose_few says of many groups (512 rows over 32 of 2 x 2048 x 4096 in 16 bits 213 us, 32
+        // rows a pass 255)
+        if (l.groups > 1 && mean > 16 && mean <= 64) f.plan.tile = kTile64, f.plan.deep = 1, f.splits = 1, f.slots = 0;
+    }
     f.plan.direct = good_x && good_w;
     // the one-pass form takes 8-bit rows at any byte, but of no less than a piece
     if (eight && !f.plan.direct && a->l.k < 16 && f.plan.tile >= kStream16) f.plan.tile = kTile64, f.splits = 1;
-    if (f.plan.tile == kStream16 && !f.plan.direct && l.groups == 1 && !l.offsets && l.rows <= 4)
+    if (f.plan.tile == kStream16 && !eight && !f.plan.direct && l.groups == 1 && !l.offsets && l.rows <= 4)
         f.plan.tile = kDot;
     if (f.plan.tile == kDot) f.splits = 1;
     if (f.splits > 1) f.parts = ceil_div((uint64_t)f.splits * l.rows * l.n * sizeof(float), 256) * 256;

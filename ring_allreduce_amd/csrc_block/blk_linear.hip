@@ -222,8 +222,6 @@ uint64_t row_tiles(const rr_linear_t* a, uint64_t height) {
 // to pay (48 x 8192 x 1024: 9.4 us against 10.2; 48 x 1024 x 8192: 40 against 16), and up to 16
 // where that is the better time (16 x 4096 x 4096 11.8 us against 12.9, 16 x 8192 x 8192 34
 // against 25; the tiles only for whole 16-byte pieces, copies of the weights would cost more).
-constexpr unsigned kSlots = 256;      // 256 x 256 tiles that a device takes at once: one a compute unit
-
 GemmPlan choose(const rr_linear_t* a, int form, int* splits, int* slots) {
     const uint64_t groups = (uint64_t)a->groups, mean = ceil_div(a->rows, groups);
     const uint64_t i = form == kByW ? a->n : a->rows, j = form == kForward ? a->n : a->k;

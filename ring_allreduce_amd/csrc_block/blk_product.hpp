@@ -9,6 +9,7 @@ namespace blk {
 
 constexpr uint64_t kMaxSize = 0x7FFFFFFFull - 1024;
 constexpr uint64_t kMaxLd = 1ull << 22;
+constexpr unsigned kSlots = 256;             // 256 x 256 tiles that a device takes at once: one a compute unit
 constexpr uint64_t kBlock = 128;             // elements of a row, or rows and elements, with one scale
 
 inline bool rows_ok(const rr_rows_t& r, uint64_t rows, uint64_t width, uint64_t bytes) {
