@@ -279,9 +279,10 @@ struct Forward {
 // 64 tiles, deep, and parts of the contraction to fill the device (16 x 8192 x 8192 18.9 against
 // 21).  Up to 32 the one-pass form for weights under 48 MB (32 x 4096 x 4096 11.1, tiles 12.3; 32 x
 // 8192 x 8192 30 and 20.3), and tiles beyond (48 x 4096 x 4096 12.7, one pass 17; 64 x 8192 x 8192
-// 21 and 40).  Rows of many groups, where the weights' read is all, the same: to 16 a group the
-// one pass (256 over 32 groups of 2 x 2048 x 4096 124, tiles 126, 32 rows a pass 155), then deep
-// tiles (512 rows 126, 32 rows a pass 172, tiles with two stages 137).
+// 21 and 40).  Rows of many groups, where the weights' read is all: to 16 a group, 8 of uneven
+// ones, of which some have more and read their weights twice, the one pass (32 groups of 2 x 2048
+// x 4096, 256 uneven rows 124, tiles 126; 512 uneven ones 174 and 126, equal ones 117 and 122), then
+// deep tiles (with two stages 137).
 // `direct`: operands of whole 16-byte pieces; the tiles copy others first.
 static void choose_few(const rr_linear8_t* a, uint64_t halves, bool direct, Forward& f) {
     const rr_linear_t& l = a->l;
@@ -298,7 +299,7 @@ static void choose_few(const rr_linear8_t* a, uint64_t halves, bool direct, Forw
     if (one && l.rows == 1) {
         p.tile = kDot;
         f.splits = 1;
-    } else if (mean <= 16 && !(one && halves == 1 && mean > 8 && large)) {
+    } else if (mean <= (one || !l.offsets ? 16 : 8) && !(one && halves == 1 && mean > 8 && large)) {
         p.tile = kStream16;
         p.narrow = halves == 1 && one;
         parts(ceil_div(n, p.narrow ? 16 : 32), ceil_div(n, 32) <= 32 && !p.narrow ? l.k / 512 : 1);
@@ -335,9 +336,9 @@ static Forward forward_of(const rr_linear8_t* a, uint64_t halves) {
         choose_few(a, halves, good_x && good_w, f);
     } else if (halves == 2) {
         f.plan.narrow = 0;
-        // as choose_few says of many groups (512 rows over 32 of 2 x 2048 x 4096 in 16 bits 213 us, 32
-        // rows a pass 255)
-        if (l.groups > 1 && mean > 16 && mean <= 64) f.plan.tile = kTile64, f.plan.deep = 1, f.splits = 1, f.slots = 0;
+        // as choose_few says of many groups (512 uneven rows over 32 of 2 x 2048 x 4096 in 16 bits 213 us,
+        // 32 rows a pass 255; 256 rows 229, the one pass 193)
+        if (l.groups > 1 && mean > (l.offsets ? 12 : 16) && mean <= 64) f.plan.tile = kTile64, f.plan.deep = 1, f.splits = 1, f.slots = 0;
     }
     f.plan.direct = good_x && good_w;
     // the one-pass form takes 8-bit rows at any byte, but of no less than a piece
@@ -398,18 +399,20 @@ static rr_status_t run_forward(const rr_linear8_t* a, uint64_t halves, void* wor
     k.q = l.w;
     k.q_ld = l.w_ld;
     k.q_group = l.groups > 1 ? l.w_stride : 0;
+    Pack8Args copies = {};
+    int n = 0;
     for (int o = 0; o < 2; ++o) {
         if (!(o ? f.pack_w : f.pack_x)) continue;
         // a 16-bit row is copied as the bytes it is
-        BlockArgs b = {};
+        BlockArgs& b = copies.part[n++];
         b.narrow = (uint8_t*)const_cast<void*>(o ? l.w : l.x.data);
         b.narrow_ld = (o ? l.w_ld : l.x.ld) * e;
         b.narrow_group = o && l.groups > 1 ? l.w_stride * e : 0;
         b.rows = o ? l.n * halves : l.rows;
         b.groups = o ? (uint64_t)l.groups : 1;
         b.width = (int32_t)(l.k * e);
-        const rr_status_t st = launch_pack8(b, room, row * e, s);
-        if (st != RR_OK) return st;
+        b.filled = (int32_t)(row * e);
+        b.wide = room;
         if (o) {
             k.q = room;
             k.q_ld = row;
@@ -419,6 +422,10 @@ static rr_status_t run_forward(const rr_linear8_t* a, uint64_t halves, void* wor
             k.p_ld = row;
         }
         room += o ? f.w_bytes : f.x_bytes;
+    }
+    if (n) {
+        const rr_status_t st = launch_pack8(copies, n, s);
+        if (st != RR_OK) return st;
     }
     k.q_half = k.q_ld * l.n;
     k.p_scale = a->x_scales;

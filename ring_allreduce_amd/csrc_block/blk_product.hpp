@@ -73,7 +73,11 @@ struct BlockArgs {
     int32_t high;
 };
 rr_status_t launch_back(const BlockArgs& a, int dt, hipStream_t s);   // narrow -> wide
-// Byte rows to rows of 16-byte pieces, with zeros behind.
-rr_status_t launch_pack8(const BlockArgs& a, void* to, uint64_t to_ld, hipStream_t s);
+// Byte rows of one or two operands to rows of `filled` bytes, whole 16-byte pieces, at `wide`, with
+// zeros behind.
+struct Pack8Args {
+    BlockArgs part[2];
+};
+rr_status_t launch_pack8(const Pack8Args& a, int parts, hipStream_t s);
 
 }  // namespace blk

@@ -151,8 +151,9 @@ template <typename T> __global__ void __launch_bounds__(256) back_kernel(const B
     }
 }
 
-// 16 bytes a thread; `narrow` -> `wide`.
-__global__ void __launch_bounds__(256) pack8_kernel(const BlockArgs a) {
+// 16 bytes a thread; both operands in one launch.
+__global__ void __launch_bounds__(256) pack8_kernel(const Pack8Args all_parts) {
+    const BlockArgs& a = all_parts.part[blockIdx.y];
     const uint32_t each = (uint32_t)a.filled / 16;
     const uint64_t all = a.groups * a.rows * each;
     for (uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x; id < all; id += (uint64_t)gridDim.x * 256) {
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(256) pack8_kernel(const BlockArgs a) {
         const uint64_t group = a.groups > 1 ? line / a.rows : 0, row = line - group * a.rows;
         const uint8_t* from = a.narrow + group * a.narrow_group + row * a.narrow_ld + col;
         const Some<uint8_t, 16> v = load_some<uint8_t, 16>(from, a.width - col);
-        *(u32x4*)((char*)a.wide + line * a.wide_ld + col) = __builtin_bit_cast(u32x4, v);
+        *(u32x4*)((char*)a.wide + line * (uint32_t)a.filled + col) = __builtin_bit_cast(u32x4, v);
     }
 }
 
@@ -182,14 +183,14 @@ rr_status_t launch_back(const BlockArgs& a, int dt, hipStream_t s) {
     return launched();
 }
 
-rr_status_t launch_pack8(const BlockArgs& a, void* to, uint64_t to_ld, hipStream_t s) {
-    BlockArgs b = a;
-    b.wide = to;
-    b.wide_ld = to_ld;
-    b.filled = (int32_t)to_ld;
-    const uint64_t all = b.groups * b.rows * (to_ld / 16);
-    if (all == 0) return RR_OK;
-    pack8_kernel<<<grid_of(all, 256), 256, 0, s>>>(b);
+rr_status_t launch_pack8(const Pack8Args& a, int parts, hipStream_t s) {
+    uint64_t most = 0;
+    for (int p = 0; p < parts; ++p) {
+        const uint64_t all = a.part[p].groups * a.part[p].rows * ((uint32_t)a.part[p].filled / 16);
+        most = all > most ? all : most;
+    }
+    if (most == 0) return RR_OK;
+    pack8_kernel<<<dim3(grid_of(most, 256), (unsigned)parts), 256, 0, s>>>(a);
     return launched();
 }
 
