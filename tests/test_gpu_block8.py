@@ -366,3 +366,83 @@ def test_two_tokens_of_large_weights(rr):
     assert bool((out[:, n - 1] == k).all()) and not bool(out[:, :n - 1].any())
     assert float(e4m3_64(torch.tensor([448.0], dtype=torch.float64))) == 448
     assert not bool(as_operand(x, torch.bfloat16)[1].any())
+
+
+def odd_scales(q, first):
+    """From block ``first`` of the contraction on, scales that are no powers of two."""
+    q.scales[..., first:] *= 1.0 + 0.5 * torch.rand(q.scales[..., first:].shape, generator=torch.Generator().manual_seed(1)).cuda()
+    return q
+
+
+FORMS = [  # rows, n, k: dots, one pass, deep tiles and their parts, at any byte and in whole pieces
+    (1, 8200, 4112), (1, 700, 4100), (2, 700, 1777), (5, 64, 9), (9, 513, 9000), (12, 8192, 6144), (14, 200, 8208),
+    (20, 300, 1001), (24, 1024, 4096), (30, 4112, 1040), (28, 8192, 6160), (40, 512, 2048), (50, 300, 1001), (64, 1000, 4112)]
+
+
+@pytest.mark.parametrize("rows,n,k", FORMS)
+def test_few_rows(rr, rows, n, k):
+    d = make(rr, rows, n, k, None, "fp16", True, True, foreign=rows % 2 == 1)
+    check_forward(rr, d, None, "silu", torch.float16)
+
+
+@pytest.mark.parametrize("first", [0, 5, 8, 100])
+@pytest.mark.parametrize("rows,n,k", [(130, 260, 1300), (1100, 1000, 1312)])
+def test_scales_of_both_kinds(rr, first, rows, n, k):
+    """Powers of two up to a block, which the instruction multiplies by, and others behind; in x and
+    in w, and for some of the rows only."""
+    for which in ("x", "w", "rows"):
+        d = make(rr, rows, n, k, None, "bf16", True, False)
+        if which == "rows":
+            d["x"].scales[rows // 2:rows // 2 + 3, first:first + 2] *= 3.0
+        else:
+            odd_scales(d[which], first)
+        check_forward(rr, d, None, "none", torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows,n,k", [(4500, 2200, 2064), (2560, 4608, 1040)])
+def test_large_tiles(rr, rows, n, k):
+    """Tiles of 256 x 256, ragged ones, and a last round cut along the contraction."""
+    d = make(rr, rows, n, k, None, "bf16", True, True)
+    odd_scales(d["w"], 9)
+    check_forward(rr, d, None, "gelu", torch.bfloat16)
+
+
+def test_large_groups(rr):
+    sizes = [2000, 0, 1, 1500, 900]
+    off = torch.from_numpy(7 + np.concatenate([[0], np.cumsum(sizes)])).to(torch.int32).cuda()
+    d = make(rr, sum(sizes) + 40, 2400, 2064, len(sizes), "bf16", True, False)
+    check_forward(rr, d, off, "silu", torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows", [1, 20, 300])
+def test_scales_of_zero(rr, rows):
+    """A scale of 0 makes its block 0, whatever its values and the other operand's scale; so do the
+    smallest ones there are, to what they are."""
+    d = make(rr, rows, 200, 384, None, "bf16", False, False)
+    d["x"].scales[:, 1] = 0.0
+    d["w"].scales[:, 1] = 2.0 ** 100
+    d["x"].scales[0, 0] = 2.0 ** -140
+    check_forward(rr, d, None, "none", torch.bfloat16)
+
+
+def test_many_rows_of_x(rr):
+    """Rows whose values are past 2^31 bytes behind the first, and whose results are."""
+    rows, k = 70000, 32768
+    x = torch.zeros(rows, k, dtype=torch.uint8, device="cuda").view(E4M3)
+    x.view(torch.uint8)[rows - 3:] = 0x38                     # 1.0
+    scales = torch.full((rows, k // 128), 0.5, device="cuda")
+    w = rr.block_quantize(torch.ones(40, k, device="cuda", dtype=torch.bfloat16), square=True)
+    out = torch.zeros(rows, 32800, device="cuda", dtype=torch.bfloat16)[:, :40]
+    rr.block_linear8(rr.Quantized(x, scales), w, out=out)
+    assert bool((out[rows - 3:] == k / 2).all()) and not bool(out[:rows - 3].any())
+
+
+def test_dispatch_of_8_bit_rows(rr):
+    x = rr.block_quantize(normal((50, 258), 2, torch.bfloat16))
+    order = rr.expert_sort(torch.randint(-1, 6, (50, 3), generator=torch.Generator().manual_seed(0)).cuda(), 6, 20)
+    got = rr.expert_dispatch(x, order.slots, order.sources)
+    want = rr.expert_dispatch(rr.block_dequantize(x, torch.float32), order.slots, order.sources)
+    assert torch.equal(rr.block_dequantize(got, torch.float32), want)
+    odd = rr.block_quantize(normal((50, 257), 2, torch.bfloat16))
+    with pytest.raises(ValueError):
+        rr.expert_dispatch(odd, order.slots, order.sources)

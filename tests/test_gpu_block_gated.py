@@ -292,3 +292,77 @@ def test_an_expert_layer(rr):
     assert_within(back.dx, dx, store_error(dx, torch.bfloat16) + edx * (1 + 2 ** -7), "dx")
     assert_within(back.dw, dw, store_error(dw, torch.bfloat16) + edw * (1 + 2 ** -7), "dw")
     assert per_element(z.scales, z.values.shape, False).shape == z.values.shape
+
+
+FORMS = [  # rows, n, k: dots, one pass, deep tiles and their parts, at any byte and in whole pieces
+    (1, 4100, 4112), (1, 350, 4100), (2, 350, 1777), (4, 64, 9), (9, 257, 9000), (12, 4096, 6144), (14, 100, 8208),
+    (20, 150, 1001), (24, 512, 4096), (28, 4096, 6160), (40, 256, 2048), (50, 150, 1001), (64, 500, 4112)]
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["16", "8"])
+@pytest.mark.parametrize("rows,n,k", FORMS)
+def test_few_rows(rr, rows, n, k, eight):
+    check_forward(rr, make(rr, rows, n, k, None, "fp16", True, eight), None, "silu", torch.float16)
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["16", "8"])
+@pytest.mark.parametrize("rows,n,k", [(4500, 2200, 2064), (4608, 2304, 2064), (2560, 2304, 1040)])
+def test_large_tiles(rr, rows, n, k, eight):
+    """Tiles of 256 x 256, ragged ones, and a last round cut along the contraction; z in 8 bits comes
+    from the tiles themselves."""
+    d = make(rr, rows, n, k, None, "bf16", True, eight)
+    if eight:
+        d["w"].scales[..., 9:] *= 1.25
+    check_forward(rr, d, None, "gelu", torch.bfloat16)
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["16", "8"])
+def test_large_groups(rr, eight):
+    sizes = [2000, 0, 1, 1500, 900]
+    off = torch.from_numpy(7 + np.concatenate([[0], np.cumsum(sizes)])).to(torch.int32).cuda()
+    d = make(rr, sum(sizes) + 40, 1200, 2064, len(sizes), "bf16", True, eight)
+    check_forward(rr, d, off, "silu", torch.bfloat16)
+    if not eight:
+        check_backward(rr, d, off, "silu", torch.bfloat16)
+
+
+def test_large_z_of_infinities(rr):
+    """In 8 bits z's NaN and infinities become NaN and leave their block's other values theirs, also
+    where fp16 makes infinities of finite sums."""
+    d = make(rr, 4500, 2200, 2064, None, "fp16", False)
+    d["x"][17] *= 30000.0
+    d["x"][4400, 5] = float("nan")
+    d["x"][18] = torch.where(d["x"][18] > 0, 20000.0, -20000.0)      # z of 20000, some 3.3 times that
+    check = rr.block_gated(d["x"], d["w"], save_preact=True)[1].view(4500, 2, 2200)
+    z = rr.block_gated(d["x"], d["w"], save_preact="e4m3")[1]
+    v, s = quantize64(check)
+    assert bool((z.scales.double() == s).all())
+    assert bool(((z.values.double() == v) | (v.isnan() & z.values.double().isnan())).all())
+    # row 17 is infinite itself (30000 times what is over 2.2), of both signs
+    assert bool(check[17].isnan().all())
+    assert bool(check[18].isinf().any()) and bool(check[18].isfinite().any())
+
+
+def test_strided_z_in_8_bits(rr):
+    """Through the library itself, which takes z's rows any distance apart."""
+    import ctypes
+    blk = rr.block
+    for rows in (5, 4500):
+        n, k = 256, 64
+        d = make(rr, rows, n, k, None, "bf16", False)
+        a = blk._Linear8()
+        a.l.rows, a.l.n, a.l.k, a.l.groups, a.l.dt, a.l.act = rows, n, k, 1, 2, 3
+        a.l.x, a.l.w, a.l.w_ld = blk._Rows(d["x"].data_ptr(), k), d["w"].data_ptr(), k
+        out = torch.zeros(rows, n, device="cuda", dtype=torch.bfloat16)
+        z = torch.full((rows, 2 * n + 40), 0x7F, dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(rows, 2, 2, device="cuda")
+        a.l.out, a.l.z, a.z_scales = blk._Rows(out.data_ptr(), n), blk._Rows(z.data_ptr(), 2 * n + 40), scales.data_ptr()
+        size = ctypes.c_size_t()
+        assert blk._block_gated_workspace(ctypes.byref(a), ctypes.byref(size)) == 0
+        work = torch.zeros(size.value or 1, dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.current_stream().cuda_stream
+        assert blk._block_gated(ctypes.byref(a), work.data_ptr() if size.value else None, size.value, stream) == 0
+        want_out, want = rr.block_gated(d["x"], d["w"], save_preact="e4m3")
+        assert torch.equal(out, want_out) and torch.equal(scales, want.scales)
+        assert torch.equal(z[:, :2 * n], want.values.view(torch.uint8).view(rows, 2 * n))
+        assert bool((z[:, 2 * n:] == 0x7F).all())
