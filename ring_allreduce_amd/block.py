@@ -330,7 +330,8 @@ def expert_dispatch(x, slots, sources, *, out=None, stream=None):
         _need(out is None, "out is for tensors only")
         _quantized(x, "x", False)
         v = x.values
-        _need(v.dim() == 2 and v.shape[1] % 2 == 0 and (v.shape[0] < 2 or v.stride(0) % 2 == 0) and
+        _need(v.dim() == 2 and v.shape[1] % 2 == 0 and v.stride(1) == 1 and
+              (v.shape[0] < 2 or v.stride(0) % 2 == 0) and
               v.storage_offset() % 2 == 0, "x must be a matrix whose rows are whole pairs of values")
         _scales(x, "x", v.device)
         return Quantized(expert_dispatch(v.view(torch.bfloat16), slots, sources, stream=stream).view(E4M3),
@@ -849,7 +850,7 @@ def block_linear8(x, w, bias=None, *, dtype=torch.bfloat16, act="none", residual
                   save_preact=False, out=None, stream=None):
     """``block_linear`` of 8-bit operands: ``x`` Quantized [rows, k] with a scale for each 128 of a
     row, ``w`` Quantized [n, k] or [groups, n, k] with square blocks (``block_quantize``'s, or any
-    others with fp32 scales).  ``dtype`` (bfloat16 or float16) is the type of bias, residual, z
+    others with finite fp32 scales).  ``dtype`` (bfloat16 or float16) is the type of bias, residual, z
     and out."""
     if stream is None and out is None and isinstance(x, Quantized) and isinstance(w, Quantized) and \
             w.square and not x.square:

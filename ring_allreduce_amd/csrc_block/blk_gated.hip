@@ -231,8 +231,11 @@ static rr_status_t check_operands(const rr_linear8_t* a, uint64_t halves) {
     if (halves == 1 ? a->z_scales != nullptr : l.residual.data != nullptr) return RR_ERR_INVALID;
     if (!rows_ok_if(l.z, l.rows, l.n, a->z_scales ? 1 : 2)) return RR_ERR_INVALID;
     if (a->z_scales && !l.z.data && l.rows) return RR_ERR_INVALID;
-    if (st == RR_OK && (l.n > kMaxLd || (l.z.data && l.z.ld > kMaxLd))) return RR_ERR_UNSUPPORTED;
-    return st;
+    if (st != RR_OK) return st;
+    if (l.n > kMaxLd || (l.z.data && l.z.ld > kMaxLd)) return RR_ERR_UNSUPPORTED;
+    // copies of operands count rows in 32 bits, and so do the halves of z in 8 bits
+    if ((uint64_t)l.groups * l.n > kMaxSize || (a->z_scales && l.rows * 2 > kMaxSize)) return RR_ERR_UNSUPPORTED;
+    return RR_OK;
 }
 
 struct Span {

@@ -694,7 +694,8 @@ __device__ __forceinline__ void write_out(const GemmArgs& a, const Spot& s, BLK_
 }
 
 // The same of a gated product: the tile's columns are TJ / 2 of the gate and the other
-// projection's behind them, so a thread finds both sums of its 8 columns in LDS.
+// projection's behind them, so a thread finds both sums of its 8 columns in LDS.  (Of tiles whose
+// contraction is in no parts but those of the workgroup.)
 template <typename T, int TI, int TJ, int WI, int WJ, int FI, int FJ>
 __device__ __forceinline__ void write_gated(const GemmArgs& a, const Spot& s, BLK_LDS char* room,
                                             const f32x4 (&acc)[FI][FJ]) {
@@ -703,8 +704,6 @@ __device__ __forceinline__ void write_gated(const GemmArgs& a, const Spot& s, BL
     static_assert(ROWS * GROUPS <= THREADS, "a thread has one piece of 16 rows a wave");
     BLK_LDS float* const store = (BLK_LDS float*)room;
     const int thread = here(), lane = thread & 63, wave = thread >> 6;
-    const bool whole = a.splits == 1;
-    if (!whole && s.g.group < 0) return;        // join_gated_kernel knows
     if (thread >= THREADS) {                    // of another part: there for the barriers
         for (int x = 0; x < FI; ++x) __syncthreads();
         return;
@@ -712,9 +711,7 @@ __device__ __forceinline__ void write_gated(const GemmArgs& a, const Spot& s, BL
     const int col = thread % GROUPS * 8, r = thread / GROUPS, j = s.j0 + col, n = a.j - j;
     const int row = r / 16 * (TI / WI) + r % 16, i = s.i0 + row;
     const int left = r < ROWS && n > 0 ? s.i_end - i : 0;
-    const Some<T, 8> g_bias = whole ? gated_bias_of<T, 8>(a, s.g.group, 0, j) : Some<T, 8>{};
-    const Some<T, 8> u_bias = whole ? gated_bias_of<T, 8>(a, s.g.group, 1, j) : Some<T, 8>{};
-    float* const part = whole ? nullptr : a.part + (uint64_t)s.split * a.part_stride + (uint64_t)i * 2 * a.j + j;
+    const Some<T, 8> g_bias = gated_bias_of<T, 8>(a, s.g.group, 0, j), u_bias = gated_bias_of<T, 8>(a, s.g.group, 1, j);
     T* const z = (T*)a.z + (uint64_t)i * a.z_ld + j;
     T* const out = (T*)a.out + (uint64_t)i * a.out_ld + j;
     for (int x = 0; x < FI; ++x) {
@@ -736,12 +733,7 @@ __device__ __forceinline__ void write_gated(const GemmArgs& a, const Spot& s, BL
             for (int e = 0; e < 4; ++e) g[h + e] = gv[e], u[h + e] = uv[e];
         }
         const uint64_t down = (uint64_t)(x * 16);
-        if (!whole) {
-            store_wide<8>(part + down * 2 * a.j, n, g);
-            store_wide<8>(part + down * 2 * a.j + a.j, n, u);
-        } else {
-            finish_gated<T, 8>(a, s.g.group, n, g, u, g_bias, u_bias, z + down * a.z_ld, out + down * a.out_ld);
-        }
+        finish_gated<T, 8>(a, s.g.group, n, g, u, g_bias, u_bias, z + down * a.z_ld, out + down * a.out_ld);
     }
 }
 
@@ -768,7 +760,8 @@ template <int N> struct Int {
 // PARTS parts of the contraction are multiplied by as many sets of waves, whose sums meet in
 // LDS, so that few rows fill the device without a second launch that adds them up.
 //
-// GATED: Q's tile is TJ / 2 rows of each of two matrices, for TJ / 2 columns of out.
+// GATED: Q's tile is TJ / 2 rows of each of two matrices, for TJ / 2 columns of out; of few rows
+// only, kInner64 (blk_tile.hpp has the others).
 template <typename T, bool PA, bool QA, bool BY_ROWS, int TI, int TJ, int WI, int WJ, int STAGES, int PARTS = 1,
           bool GATED = false>
 __global__ void __launch_bounds__(64 * WI * WJ * PARTS, STAGES * (TI + TJ) * kDepth * 2 > 81920 && WI * WJ == 4 ? 1 : 2)

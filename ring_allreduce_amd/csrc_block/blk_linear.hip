@@ -182,6 +182,8 @@ static rr_status_t check_grad(const rr_linear_t* a, const rr_linear_grad_t* g, c
     if (a->act != RR_ACT_NONE && !rows_ok(a->z, a->rows, a->n, 2)) return RR_ERR_INVALID;
     if (!aligned_to(g->dw, type_bytes(g->dw_dt)) || !aligned_to(g->db, 4)) return RR_ERR_INVALID;
     if (!aligned_to(e.x, 4) || !aligned_to(e.w, 4)) return RR_ERR_INVALID;
+    // copies of 8-bit operands count rows in 32 bits
+    if (e.w && (uint64_t)a->groups * a->n > kMaxSize) return RR_ERR_UNSUPPORTED;
     if (g->dout.ld > kMaxLd || (g->dx.data && g->dx.ld > kMaxLd) || (a->act != RR_ACT_NONE && a->n > kMaxLd)) return RR_ERR_UNSUPPORTED;
     return RR_OK;
 }

@@ -200,3 +200,25 @@ def test_binding(rr):
                  lambda: rr.block_gated_backward(None, b, w2, b), lambda: rr.expert_dispatch(x8, None, None, out=x)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("halves", [1, 2])
+def test_more_rows_of_weights_than_32_bits_count(blk, halves):
+    n, groups = (1 << 22) // halves, 1024
+    size = ctypes.c_size_t()
+    for g, status in ((groups, 2), (511, 0)):
+        a = wide(blk, halves, True, groups=g, n=n, k=16, x=(at(1), 32), w=1 << 40, w_ld=16, w_stride=n * halves * 16,
+                 z=(at(5), 1 << 22), out=(at(6), n), residual=(None, 0), bias=None, rows=g)
+        c = grad(blk, halves, dout=(at(10), n), dw=None, db=None)
+        if halves == 2:
+            c.out = blk._Rows(at(14), n)
+        calls_ = calls(blk, halves)
+        assert calls_[1](ctypes.byref(a), ctypes.byref(size)) == status
+        assert calls_[3](ctypes.byref(a), ctypes.byref(c), ctypes.byref(size)) == status
+
+
+def test_more_rows_of_8_bit_z_than_32_bits_count(blk):
+    size = ctypes.c_size_t()
+    for rows, status in ((1 << 30, 2), ((1 << 30) - 2048, 0)):
+        a = wide(blk, 2, False, groups=1, rows=rows, n=1, k=1, z_scales=at(9) << 4, z=(at(5), 2), out=(at(6), 1))
+        assert calls(blk, 2)[1](ctypes.byref(a), ctypes.byref(size)) == status

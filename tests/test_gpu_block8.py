@@ -446,3 +446,50 @@ def test_dispatch_of_8_bit_rows(rr):
     odd = rr.block_quantize(normal((50, 257), 2, torch.bfloat16))
     with pytest.raises(ValueError):
         rr.expert_dispatch(odd, order.slots, order.sources)
+
+
+def test_dispatch_of_every_byte(rr):
+    """The bits are moved, not the values: NaN of both signs stay as they are."""
+    v = torch.arange(256, dtype=torch.int64).repeat(2).view(2, 256).to(torch.uint8)
+    v[1] = v[0].roll(1)
+    x = rr.Quantized(v.cuda().view(E4M3), torch.tensor([[1.0, 2.0], [3.0, 4.0]]).cuda())
+    order = rr.expert_sort(torch.tensor([[1, 1], [0, 1]]).cuda(), 2)
+    got = rr.expert_dispatch(x, order.slots, order.sources)
+    rows = (order.sources // 2).long()
+    assert torch.equal(got.values.view(torch.uint8), x.values.view(torch.uint8)[rows])
+    assert torch.equal(got.scales, x.scales[rows])
+    across = rr.Quantized(v.cuda().t().contiguous().t().view(E4M3), x.scales)
+    with pytest.raises(ValueError):
+        rr.expert_dispatch(across, order.slots, order.sources)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 20, 60, 300])
+def test_scales_whose_product_is_past_the_end(rr, rows):
+    """The last of an odd number of blocks: infinity times a sum, not NaN."""
+    k = 384
+    one = lambda *s: torch.full(s, 0x38, dtype=torch.uint8, device="cuda").view(E4M3)  # noqa: E731
+    xs, ws = torch.ones(rows, 3, device="cuda"), torch.ones(2, 3, device="cuda")
+    xs[:, 2] = ws[0, 2] = 1.5 * 2.0 ** 100
+    out = rr.block_linear8(rr.Quantized(one(rows, k), xs), rr.Quantized(one(200, k), ws, True))
+    assert bool((out[:, :128] == float("inf")).all()) and bool((out[:, 128:] > 1e32).all())
+
+
+def test_two_streams_at_once(rr):
+    """Calls on two streams, whose scratch memory is each their own."""
+    d = [make(rr, 600, 768, 1040, 2, "bf16", True, True, seed=s) for s in (0, 1)]
+    e = [make(rr, 24, 1000, 4112, None, "bf16", True, True, seed=s) for s in (0, 1)]
+    off = torch.tensor([5, 200, 590], dtype=torch.int32, device="cuda")
+
+    def step(s, stream=None):
+        z = d[s]["z"]
+        g = rr.block_linear8_backward(d[s]["dout"], d[s]["x"], d[s]["w"], z, act="gelu", offsets=off, stream=stream)
+        return [rr.block_linear8(d[s]["x"], d[s]["w"], d[s]["bias"], act="gelu", offsets=off, stream=stream),
+                rr.block_linear8(e[s]["x"], e[s]["w"], e[s]["bias"], stream=stream), g.dx, g.dw, g.db]
+
+    want = [step(0), step(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [step(i % 2, streams[i % 2]) for i in range(8)]
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))

@@ -366,3 +366,23 @@ def test_strided_z_in_8_bits(rr):
         assert torch.equal(out, want_out) and torch.equal(scales, want.scales)
         assert torch.equal(z[:, :2 * n], want.values.view(torch.uint8).view(rows, 2 * n))
         assert bool((z[:, 2 * n:] == 0x7F).all())
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["16", "8"])
+def test_two_streams_at_once(rr, eight):
+    """Calls on two streams, whose scratch memory is each their own."""
+    d = [make(rr, 600, 384, 1040, 2, "bf16", True, eight, seed=s) for s in (0, 1)]
+    off = torch.tensor([5, 200, 590], dtype=torch.int32, device="cuda")
+
+    def step(s, stream=None):
+        out, z = rr.block_gated(d[s]["x"], d[s]["w"], d[s]["bias"], offsets=off, save_preact="e4m3", stream=stream)
+        g = rr.block_gated_backward(d[s]["dout"], d[s]["x"], d[s]["w"], z, offsets=off, need_out=True, stream=stream)
+        return [out, z.values.view(torch.uint8), z.scales, g.dx, g.dw, g.db, g.out]
+
+    want = [step(0), step(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [step(i % 2, streams[i % 2]) for i in range(8)]
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
