@@ -493,3 +493,17 @@ def test_two_streams_at_once(rr):
     torch.cuda.synchronize()
     for i, g in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
+
+
+@pytest.mark.parametrize("rows,n,k", [(2560, 4608, 1040), (4500, 2201, 2064)])
+def test_large_tiles_with_a_residual_anywhere(rr, rows, n, k):
+    """At any element, rows any distance apart, and as out itself."""
+    d = make(rr, rows, n, k, None, "bf16", True, True)
+    want = rr.block_linear8(d["x"], d["w"], d["bias"], act="silu", residual=d["residual"])
+    for ahead, ld in ((1, n), (3, n + 5), (8, n + 56)):
+        flat = torch.full((ahead + rows * ld,), float("nan"), device="cuda", dtype=torch.bfloat16)
+        r = flat[ahead:].view(rows, ld)[:, :n]
+        r.copy_(d["residual"])
+        assert torch.equal(rr.block_linear8(d["x"], d["w"], d["bias"], act="silu", residual=r), want)
+        assert torch.equal(rr.block_linear8(d["x"], d["w"], d["bias"], act="silu", residual=r, out=r), want)
+        assert bool(flat[:ahead].isnan().all()) and bool(flat[ahead:].view(rows, ld)[:, n:].isnan().all())
