@@ -286,7 +286,7 @@ struct Forward {
 // ones, of which some have more and read their weights twice, the one pass (32 groups of 2 x 2048
 // x 4096, 256 uneven rows 124, tiles 126; 512 uneven ones 174 and 126, equal ones 117 and 122), then
 // deep tiles (with two stages 137).
-// `direct`: operands of whole 16-byte pieces; the tiles copy others first.
+// `direct`: operands whose rows are whole words; the tiles copy others first.
 static void choose_few(const rr_linear8_t* a, uint64_t halves, bool direct, Forward& f) {
     const rr_linear_t& l = a->l;
     const uint64_t n = l.n * halves, steps = ceil_div(l.k, kBlock), mean = ceil_div(l.rows, l.groups);
@@ -323,8 +323,10 @@ static Forward forward_of(const rr_linear8_t* a, uint64_t halves) {
     l.n *= halves;
     // a byte's tiles are as deep as 16-bit ones of half as many values, and take as long
     const uint64_t piece = eight ? 16 : 8;
-    const bool good_x = good_rows(l.x, 0, l.k, piece);
-    const bool good_w = good_rows({const_cast<void*>(l.w), l.w_ld}, l.groups > 1 ? l.w_stride : 0, l.k, piece);
+    const rr_rows_t w = {const_cast<void*>(l.w), l.w_ld};
+    const uint64_t apart = l.groups > 1 ? l.w_stride : 0;
+    const bool good_x = good_rows(l.x, 0, l.k, piece), good_w = good_rows(w, apart, l.k, piece);
+    const bool word_x = word_rows(l.x, 0, l.k, eight ? 1 : 2), word_w = word_rows(w, apart, l.k, eight ? 1 : 2);
     if (eight) {
         l.k = ceil_div(l.k, 2);
         l.x.ld = l.w_ld = ceil_div(l.k, 8) * 8;
@@ -336,7 +338,7 @@ static Forward forward_of(const rr_linear8_t* a, uint64_t halves) {
     f.plan.form = kForward;
     const uint64_t mean = ceil_div(l.rows, l.groups);
     if (eight && mean <= 64) {
-        choose_few(a, halves, good_x && good_w, f);
+        choose_few(a, halves, word_x && word_w, f);
     } else if (halves == 2) {
         f.plan.narrow = 0;
         // as choose_few says of many groups (512 uneven rows over 32 of 2 x 2048 x 4096 in 16 bits 213 us,
@@ -353,8 +355,8 @@ static Forward forward_of(const rr_linear8_t* a, uint64_t halves) {
     f.tiles = (uint64_t)f.slots * 256 * 256 * sizeof(float);
     if (f.plan.tile < kStream16) {
         const uint64_t e = eight ? 1 : 2, row = ceil_div(a->l.k, piece) * piece * e;
-        f.pack_x = !good_x;
-        f.pack_w = !good_w;
+        f.pack_x = f.plan.tile == kInner64 ? !good_x : !word_x;
+        f.pack_w = f.plan.tile == kInner64 ? !good_w : !word_w;
         if (f.pack_x) f.x_bytes = ceil_div(l.rows * row, 256) * 256;
         if (f.pack_w) f.w_bytes = ceil_div((uint64_t)l.groups * l.n * row, 256) * 256;
     }
@@ -394,7 +396,7 @@ static rr_status_t run_forward(const rr_linear8_t* a, uint64_t halves, void* wor
     k.out = l.out.data;
     k.out_ld = l.out.ld;
     k.act = l.act;
-    // copies of operands whose rows are not made of 16-byte pieces
+    // copies of operands whose rows the tiles do not take
     const uint64_t e = eight ? 1 : 2, piece = 16 / e, row = ceil_div(l.k, piece) * piece;
     char* room = (char*)workspace + f.parts + f.tiles;
     k.p = l.x.data;

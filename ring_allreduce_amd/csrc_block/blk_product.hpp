@@ -25,6 +25,13 @@ inline bool good_rows(const rr_rows_t& r, uint64_t group, uint64_t width, uint64
     return aligned_to(r.data, 16) && r.ld % piece == 0 && group % piece == 0 && width % piece == 0;
 }
 
+// Rows that the tiles of blk_tile.hpp take as they are: whole words of 4 bytes, as the loads into
+// LDS need, and no less than a piece.
+inline bool word_rows(const rr_rows_t& r, uint64_t group, uint64_t width, uint64_t bytes) {
+    return aligned_to(r.data, 4) && r.ld * bytes % 4 == 0 && group * bytes % 4 == 0 && width * bytes % 4 == 0 &&
+           width * bytes >= 16;
+}
+
 struct Operand {
     rr_rows_t rows;
     uint64_t count, width, groups, group;  // rows of a group, row length, groups and their distance

@@ -63,8 +63,8 @@ template <int ROWS, int THREADS> struct Load8 {
     static constexpr int kPieces = ROWS * 8 / THREADS;
     u32x4 rsrc;
     uint32_t stride;
-    // r0, r_end: rows; end: bytes of a row, whole 16-byte pieces (part of one in range would come
-    // as zeros); ld: bytes
+    // r0, r_end: rows; end: bytes of a row, up to which all pieces are whole (part of one in range
+    // would come as zeros); ld: bytes
     __device__ __forceinline__ void start(const char* b, uint64_t ld, int r0, int r_end, int end) {
         const int rows = max(min(r_end - r0, ROWS), 0);
         rsrc = descriptor(b + (uint64_t)r0 * ld, rows ? (uint64_t)(rows - 1) * ld + end : 0);
@@ -358,12 +358,17 @@ tile_kernel(const GemmArgs a) {
     DQ lq[HALVES];
     Scales<TI> ls;
     const char* const q = (const char*)a.q + (s.g.group > 0 ? (uint64_t)s.g.group * a.q_group * 2 : 0);
-    const int end = (s.c_end * 2 + 15) / 16 * 16;
+    // Rows end with a whole piece or, of whole words, inside one, whose place takes the row's last
+    // 16 bytes: some of them twice, once too often, until `clean` has made them zeros.  Other rows
+    // are copies with zeros behind.
+    const int bytes = s.c_end * 2, end = (bytes & 3) || bytes < 16 ? (bytes + 15) / 16 * 16 : bytes;
+    const bool cut = tiles > 0 && (end & 15);
     lp.start((const char*)a.p, a.p_ld * 2, s.i0, s.i_end, end);
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) lq[h].start(q + h * a.q_half * 2, a.q_ld * 2, s.j0, a.j, end);
     if constexpr (EIGHT) ls.template start<GATED>(a, s, s_at);
-    int left = (s.c_end - s.c0) * 2;         // bytes of a row
+    int left = end - s.c0 * 2;               // bytes of a row
+    const int last = left - (tiles - 1) * 128;      // those of the last tile
     const int from = piece_of() * 16;        // of the 128
     const int from_q = ((here() & 7) ^ C::mix(here() >> 3)) * 16;
     uint32_t at_p = (uint32_t)(here() >> 3) * (uint32_t)(a.p_ld * 2) + from + s.c0 * 2;
@@ -371,8 +376,8 @@ tile_kernel(const GemmArgs a) {
     const uint32_t mine = (uint32_t)__builtin_amdgcn_readfirstlane(wave * 1024);
     // before the loads of a tile: aim(); after its P's and Q's: 128 bytes on
     const auto aim = [&]() {
-        at_p = from >= left ? kReach : at_p;
-        at_q = from_q >= left ? kReach : at_q;
+        at_p = from >= left ? kReach : at_p + min(left - from - 16, 0);
+        at_q = from_q >= left ? kReach : at_q + min(left - from_q - 16, 0);
         left -= 128;
     };
     constexpr int QS = HALVES * DQ::kPieces, PS = DP::kPieces;
@@ -434,8 +439,18 @@ tile_kernel(const GemmArgs a) {
     };
     constexpr int SLOTS = FI > 4 ? 4 : FI * 2;
     int place = 0;
-    const auto tile = [&](auto power_, int t) {
-        constexpr bool POWER = decltype(power_)::value;
+    // The last tile of rows that end inside a piece: the words of it that the piece before has too.
+    const auto clean = [&](Frag& f) {
+        const int piece = (int)(threadIdx.x >> 4 & 3);
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+            if (w % 4 < 3) f[w] = piece + w / 4 * 4 == last >> 4 && w % 4 * 4 < 16 - (last & 15) ? 0 : f[w];
+    };
+    const auto tile = [&](auto power_, auto cut_, int t) {
+        constexpr bool POWER = decltype(power_)::value, CUT = decltype(cut_)::value;
+        if constexpr (CUT)
+#pragma unroll
+            for (int y = 0; y < FJ; ++y) clean(fq[y]);
         const auto multiply = [&](int x, int y, float s) {
             const int half = y / (FJ / HALVES);
             if constexpr (!EIGHT) {
@@ -464,6 +479,7 @@ tile_kernel(const GemmArgs a) {
                 for (int k = (x - MID) * QS / SPAN; k < (x - MID + 1) * QS / SPAN; ++k) load_q(place, k);
             read_p((x + 1) % SLOTS, x + 1);
             if (x == FI - 3) read_p((x + 2) % SLOTS, x + 2);
+            if constexpr (CUT) clean(fp[x % SLOTS]);
 #pragma unroll
             for (int y = 0; y < FJ; ++y) multiply(x, y, sp[x]);
             keep_order();
@@ -478,6 +494,10 @@ tile_kernel(const GemmArgs a) {
         if constexpr (EIGHT) read_scales(t + 1);
         read_p(FI % SLOTS, 0);
         if constexpr (FI == 2) read_p(3, 1);
+        if constexpr (CUT) {
+            clean(fp[(FI - 2) % SLOTS]);
+            clean(fp[(FI - 1) % SLOTS]);
+        }
 #pragma unroll
         for (int y = 0; y < FJ; ++y) {
             multiply(FI - 2, y, sp[FI - 2]);
@@ -525,15 +545,20 @@ tile_kernel(const GemmArgs a) {
         if constexpr (TOUCH)
             if (t == touch) touch_residual<T, TI, TJ, THREADS>(a, s, s_at + SCALES);
     };
+    const int whole = cut ? tiles - 1 : tiles;
     int t = 0;
     if constexpr (EIGHT)                     // as long as all scales are powers of two, and the rest
-        for (; t < tiles && ((t & 3) != 0 || powers(t)); ++t) {
+        for (; t < whole && ((t & 3) != 0 || powers(t)); ++t) {
             ahead(t);
-            tile(std::true_type(), t);
+            tile(std::true_type(), std::false_type(), t);
         }
-    for (; t < tiles; ++t) {
+    for (; t < whole; ++t) {
         ahead(t);
-        tile(std::false_type(), t);
+        tile(std::false_type(), std::false_type(), t);
+    }
+    for (; t < tiles; ++t) {                 // once at most; as a loop nothing of it is moved down into the epilogue
+        ahead(t);
+        tile(std::false_type(), std::true_type(), t);
     }
     arrived<0>();                            // the loads past the end as well
     write_direct<T, TI, TJ, WI, WJ, FI, FJ, GATED>(a, s, room, acc);

@@ -507,3 +507,27 @@ def test_large_tiles_with_a_residual_anywhere(rr, rows, n, k):
         assert torch.equal(rr.block_linear8(d["x"], d["w"], d["bias"], act="silu", residual=r), want)
         assert torch.equal(rr.block_linear8(d["x"], d["w"], d["bias"], act="silu", residual=r, out=r), want)
         assert bool(flat[:ahead].isnan().all()) and bool(flat[ahead:].view(rows, ld)[:, n:].isnan().all())
+
+
+@pytest.mark.parametrize("rows,n", [(40, 6000), (70, 200), (600, 700), (2560, 4608)])
+@pytest.mark.parametrize("k", [16, 20, 300, 1032, 1292, 2060])
+def test_rows_of_words(rr, rows, n, k):
+    """Rows that end inside 16 bytes and begin at any word, NaN before, between and behind them, give
+    what copies in whole pieces give; and scales that are no powers of two."""
+    d = make(rr, rows, n, k, None, "bf16", True, False)
+    for foreign in (False, True):
+        if foreign:
+            odd_scales(d["w"], 0)
+        got = []
+        for ahead, ld in ((0, (k + 15) // 16 * 16 + 16), (4, k + 4), (12, k + 12), (0, k)):
+            ops = []
+            for q in (d["x"], d["w"]):
+                r = q.values.shape[0]
+                flat = torch.full((ahead + r * ld,), 0x7F, device="cuda", dtype=torch.uint8).view(E4M3)
+                v = flat[ahead:].view(r, ld)[:, :k]
+                v.copy_(q.values)
+                ops.append(rr.Quantized(v, q.scales, q.square))
+            got.append(rr.block_linear8(*ops, d["bias"]))
+        ro, _, eo, _ = linear64(d["x"], d["w"], d["bias"], None, "none", None)
+        assert_within(got[0], ro, store_error(ro, torch.bfloat16) + eo * (1 + 2 ** -7), "out")
+        assert all(torch.equal(g, got[0]) for g in got)

@@ -386,3 +386,24 @@ def test_two_streams_at_once(rr, eight):
     torch.cuda.synchronize()
     for i, g in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
+
+
+@pytest.mark.parametrize("rows,n", [(40, 2000), (70, 100), (600, 350), (2560, 2304)])
+@pytest.mark.parametrize("k", [8, 10, 150, 516, 1030])
+def test_rows_of_words(rr, rows, n, k):
+    """Rows that end inside 16 bytes and begin at any word, NaN before, between and behind them."""
+    d = make(rr, rows, n, k, None, "bf16", True)
+    ro, _, eo, _ = gated64(d["x"], d["w"], d["bias"], None, "silu")
+    got = []
+    for ahead, ld in ((0, (k + 7) // 8 * 8 + 8), (2, k + 2), (6, k + 6), (0, k)):
+        ops = []
+        for v in (d["x"], d["w"].view(2 * n, k)):
+            r = v.shape[0]
+            flat = torch.full((ahead + r * ld,), float("nan"), device="cuda", dtype=torch.bfloat16)
+            to = flat[ahead:].view(r, ld)[:, :k]
+            to.copy_(v)
+            ops.append(to)
+        got.append(rr.block_gated(ops[0], ops[1].view(2, n, k), d["bias"]))
+    assert_within(got[0], ro, store_error(ro, torch.bfloat16) + eo * (1 + 2 ** -7), "out")
+    for g in got[1:]:
+        assert_within(g, ro, store_error(ro, torch.bfloat16) + eo * (1 + 2 ** -7), "out")
