@@ -276,6 +276,13 @@ struct Forward {
     uint64_t bytes() const { return parts + tiles + x_bytes + w_bytes; }
 };
 
+// Parts of the contraction, `most` of them, that fill the device.
+static int parts_of(uint64_t blocks, uint64_t most) {
+    int s = 1;
+    while (s < 16 && blocks * s * 2 <= kSlots && (uint64_t)s * 2 <= most) s *= 2;
+    return s;
+}
+
 // Few rows of 8-bit operands (of up to 64, `n` columns of both halves): microseconds on weights in
 // no cache.  One row goes as dots.  Up to 16 the one-pass form, 16 columns a workgroup where it
 // has them (3 x 8192 x 8192 17.2, 16 x 4096 x 4096 8.4), but of more than 8 by large weights 64 x
@@ -285,24 +292,22 @@ struct Forward {
 // 21 and 40).  Rows of many groups, where the weights' read is all: to 16 a group, 8 of uneven
 // ones, of which some have more and read their weights twice, the one pass (32 groups of 2 x 2048
 // x 4096, 256 uneven rows 124, tiles 126; 512 uneven ones 174 and 126, equal ones 117 and 122), then
-// deep tiles (with two stages 137).
+// deep tiles (with two stages 137).  Of groups whose rows are whole words (`words`), which the one
+// pass takes without knowing where pieces begin, always the tiles (32 groups of 2 x 2048 x 4088,
+// 64, 128 and 256 uneven rows 86, 101 and 112, one pass 108, 127 and 155).
 // `direct`: operands whose rows are whole words; the tiles copy others first.
-static void choose_few(const rr_linear8_t* a, uint64_t halves, bool direct, Forward& f) {
+static void choose_few(const rr_linear8_t* a, uint64_t halves, bool direct, bool words, Forward& f) {
     const rr_linear_t& l = a->l;
     const uint64_t n = l.n * halves, steps = ceil_div(l.k, kBlock), mean = ceil_div(l.rows, l.groups);
     const bool one = l.groups == 1 && !l.offsets, large = direct && n * l.k >= 48u << 20;
     GemmPlan& p = f.plan;
-    const auto parts = [&](uint64_t blocks, uint64_t most) {
-        uint64_t s = 1;
-        while (one && s < 16 && blocks * s * 2 <= kSlots && s * 2 <= most) s *= 2;
-        f.splits = (int)s;
-    };
+    const auto parts = [&](uint64_t blocks, uint64_t most) { f.splits = one ? parts_of(blocks, most) : 1; };
     p.narrow = p.deep = 0;
     f.slots = 0;
     if (one && l.rows == 1) {
         p.tile = kDot;
         f.splits = 1;
-    } else if (mean <= (one || !l.offsets ? 16 : 8) && !(one && halves == 1 && mean > 8 && large)) {
+    } else if (!(words && !one) && mean <= (one || !l.offsets ? 16 : 8) && !(one && halves == 1 && mean > 8 && large)) {
         p.tile = kStream16;
         p.narrow = halves == 1 && one;
         parts(ceil_div(n, p.narrow ? 16 : 32), ceil_div(n, 32) <= 32 && !p.narrow ? l.k / 512 : 1);
@@ -337,13 +342,23 @@ static Forward forward_of(const rr_linear8_t* a, uint64_t halves) {
     f.plan = choose(&l, kForward, &f.splits, &f.slots);
     f.plan.form = kForward;
     const uint64_t mean = ceil_div(l.rows, l.groups);
+    const bool words = word_x && word_w && !(good_x && good_w);
     if (eight && mean <= 64) {
-        choose_few(a, halves, word_x && word_w, f);
+        choose_few(a, halves, word_x && word_w, words, f);
     } else if (halves == 2) {
         f.plan.narrow = 0;
         // as choose_few says of many groups (512 uneven rows over 32 of 2 x 2048 x 4096 in 16 bits 213 us,
-        // 32 rows a pass 255; 256 rows 229, the one pass 193)
-        if (l.groups > 1 && mean > (l.offsets ? 12 : 16) && mean <= 64) f.plan.tile = kTile64, f.plan.deep = 1, f.splits = 1, f.slots = 0;
+        // 32 rows a pass 255; 256 rows 229, the one pass 193), and of rows of whole words that the
+        // other forms take in single elements or from copies (5 .. 64 x 2 x 4000 x 7996 24 .. 28 us, so
+        // 60 .. 75; 2 x 500 x 996 8.2 .. 8.6 and 9.7 .. 20; 2 x 1000 x 3996 9.2 .. 11.6 and 9.8 .. 24; 64
+        // uneven rows over 32 groups of 2 x 2048 x 4094 168 and 378)
+        if (mean <= 64 && ((l.groups > 1 && mean > (l.offsets ? 12 : 16)) || (words && (mean > 4 || l.groups > 1)))) {
+            const uint64_t steps = ceil_div(l.k, (uint64_t)kDepth);
+            f.plan.tile = kTile64;
+            f.plan.deep = 1;
+            f.splits = l.groups == 1 && !l.offsets ? parts_of(ceil_div(l.n, 64), steps >= 16 ? steps / 4 : 1) : 1;
+            f.slots = 0;
+        }
     }
     f.plan.direct = good_x && good_w;
     // the one-pass form takes 8-bit rows at any byte, but of no less than a piece

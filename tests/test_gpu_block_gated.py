@@ -407,3 +407,11 @@ def test_rows_of_words(rr, rows, n, k):
     assert_within(got[0], ro, store_error(ro, torch.bfloat16) + eo * (1 + 2 ** -7), "out")
     for g in got[1:]:
         assert_within(g, ro, store_error(ro, torch.bfloat16) + eo * (1 + 2 ** -7), "out")
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["16", "8"])
+@pytest.mark.parametrize("sizes", [[2, 0, 3, 1], [9, 40, 0, 11], [30, 70, 33, 1], [130, 7, 300, 90]], ids=str)
+def test_groups_of_rows_of_words(rr, sizes, eight):
+    off = torch.from_numpy(3 + np.concatenate([[0], np.cumsum(sizes)])).to(torch.int32).cuda()
+    d = make(rr, sum(sizes) + 7, 200, 1036 if eight else 518, len(sizes), "bf16", True, eight)
+    check_forward(rr, d, off, "silu", torch.bfloat16)
