@@ -310,8 +310,8 @@ __device__ __forceinline__ void keep_order() {
 // Scales: where all of four blocks of a wave's rows and columns are powers of two, as
 // block_quantize makes them, the instruction itself takes their exponents (8192 x 8192 x 8192 431
 // us, 2550 TFLOP/s); others are multiplied in 32 bits and come on top of each block's sum by a
-// multiply-add a result on the vector units, beside the matrix cores but not without waiting
-// for them (540 us).
+// multiply-add a result on the vector units, beside the matrix cores (450 to 540 us, by the power
+// that is left).
 //
 // Bound, at 256 x 256: 8-bit products by the way from the L2s into LDS and by the epilogue, which no
 // product overlaps (one workgroup a compute unit, all 160 KB of LDS): a loop of 264 us of 8192
@@ -437,7 +437,7 @@ tile_kernel(const GemmArgs a) {
         }
         return __all(bad == 0);
     };
-    constexpr int SLOTS = FI > 4 ? 4 : FI * 2;
+    constexpr int SLOTS = FI > 4 ? 4 : FI * 2, HELD = 3;
     int place = 0;
     // The last tile of rows that end inside a piece: the words of it that the piece before has too.
     const auto clean = [&](Frag& f) {
@@ -451,6 +451,16 @@ tile_kernel(const GemmArgs a) {
         if constexpr (CUT)
 #pragma unroll
             for (int y = 0; y < FJ; ++y) clean(fq[y]);
+        // Sums that are to be multiplied wait for HELD more products: what follows a product at once
+        // would wait for it (1024 x 4096 x 4096 42 us instead of 45, 8192 x 8192 x 8192 450 instead of
+        // 462; with two or four of them less).
+        constexpr int LATER = FI * FJ > HELD ? HELD : 1;
+        f32x4 held[LATER];
+        const auto add_held = [&](int n) {          // of the tile's n-th product
+            const int late = n - (FI - 2) * FJ, x = late < 0 ? n / FJ : FI - 2 + (late & 1), y = late < 0 ? n % FJ : late >> 1;
+            const float f = sp[x] * sq[y / (FJ / HALVES)];
+            acc[x][y] = __builtin_elementwise_fma(f32x4{f, f, f, f}, held[n % LATER], acc[x][y]);
+        };
         const auto multiply = [&](int x, int y, float s) {
             const int half = y / (FJ / HALVES);
             if constexpr (!EIGHT) {
@@ -463,8 +473,10 @@ tile_kernel(const GemmArgs a) {
             } else if constexpr (POWER) {
                 acc[x][y] = mma8_scaled(fq[y], fp[x % SLOTS], acc[x][y], exponent_of(sq[half]), exponent_of(s));
             } else {
-                const float f = s * sq[half];
-                acc[x][y] = __builtin_elementwise_fma(f32x4{f, f, f, f}, mma8(fq[y], fp[x % SLOTS]), acc[x][y]);
+                const int n = x < FI - 2 ? x * FJ + y : (FI - 2) * FJ + y * 2 + x - (FI - 2);
+                const f32x4 sum = mma8(fq[y], fp[x % SLOTS]);
+                if (n >= LATER) add_held(n - LATER);
+                held[n % LATER] = sum;
             }
         };
         // (no branches between the products: they are moved down behind them, and what they read
@@ -516,6 +528,9 @@ tile_kernel(const GemmArgs a) {
             fp[0] = fp[FI % SLOTS];
             if constexpr (FI == 2) fp[1] = fp[3];
         }
+        if constexpr (EIGHT && !POWER)
+#pragma unroll
+            for (int n = FI * FJ - LATER; n < FI * FJ; ++n) add_held(n);
         if constexpr (EIGHT) use_scales();
     };
     if (tiles > 0) {
