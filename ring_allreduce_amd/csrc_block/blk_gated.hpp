@@ -94,7 +94,7 @@ template <typename T> static rr_status_t launch_gated(const GemmArgs& a, const G
             break;
         case kTile256: launch_gated_large<T, false>(a, s); break;
         case kTile128:
-            if (p.deep) launch_tile<T, false, 128, 128, 2, 2, 4, true>(a, s);
+            if (p.deep) launch_tile<T, false, 128, 128, 2, 4, 4, true>(a, s);
             else launch_tile<T, false, 128, 128, 2, 2, 2, true>(a, s);
             break;
         default:

@@ -226,7 +226,7 @@ template <typename T, bool GATED> static rr_status_t launch_gemm8(const GemmArgs
                 if (a.slots) join_last_kernel<T, true, 256, 256><<<dim3((unsigned)a.slots / 2, 8), 256, 0, s>>>(a);
             break;
         case kTile128:
-            if (p.deep) launch_tile<T, true, 128, 128, 2, 2, 4, GATED>(a, s);
+            if (p.deep) launch_tile<T, true, 128, 128, 2, 4, 4, GATED>(a, s);
             else launch_tile<T, true, 128, 128, 2, 2, 2, GATED>(a, s);
             break;
         default:

@@ -320,8 +320,7 @@ __device__ __forceinline__ void keep_order() {
 // instead of 192, and have no copy of Q's next tile (16384 x 8192 x 4096 gated with uneven
 // groups 548 us, gemm_kernel's tiles 621).
 template <typename T, bool EIGHT, int TI, int TJ, int WI, int WJ, int STAGES, bool GATED>
-__global__ void __launch_bounds__(64 * WI * WJ, STAGES * (TI + TJ) * kDepth * 2 > 81920 && WI * WJ == 4 ? 1 : 2)
-tile_kernel(const GemmArgs a) {
+__global__ void __launch_bounds__(64 * WI * WJ, 2) tile_kernel(const GemmArgs a) {
     constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16, HALVES = GATED ? 2 : 1;
     constexpr int PB = TI * 128, QB = TJ * 128;
     constexpr bool TOUCH = !GATED && TI == 256;
@@ -579,6 +578,10 @@ tile_kernel(const GemmArgs a) {
     write_direct<T, TI, TJ, WI, WJ, FI, FJ, GATED>(a, s, room, acc);
 }
 
+// 128 x 128 with four stages, one workgroup a compute unit, is launched with eight waves: with four, one
+// a SIMD, nothing hides a wave's waits, and the compiler keeps sums in registers that the vector
+// units cannot reach (1024 x 4096 x 4096, four waves: gated in 16 bits 48 us, in 8 bits at scales that
+// are no powers of two 42; so 36 and 29; at powers of two 26 and 27).
 template <typename T, bool EIGHT, int TI, int TJ, int WI, int WJ, int STAGES, bool GATED>
 static void launch_tile(const GemmArgs& a, hipStream_t s) {
     const unsigned grid = (unsigned)a.tiles_i * a.tiles_j * a.splits;
