@@ -531,3 +531,9 @@ def test_rows_of_words(rr, rows, n, k):
         ro, _, eo, _ = linear64(d["x"], d["w"], d["bias"], None, "none", None)
         assert_within(got[0], ro, store_error(ro, torch.bfloat16) + eo * (1 + 2 ** -7), "out")
         assert all(torch.equal(g, got[0]) for g in got)
+
+
+@pytest.mark.parametrize("rows,n,k", [(70, 200, 1003), (600, 700, 1011), (2560, 4608, 1007)])
+def test_odd_rows_that_end_a_byte_before_a_word(rr, rows, n, k):
+    d = make(rr, rows, n, k, None, "fp16", True, False, foreign=True)
+    check_forward(rr, d, None, "none", torch.float16)
