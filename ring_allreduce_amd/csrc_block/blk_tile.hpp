@@ -155,8 +155,8 @@ __device__ __forceinline__ void write_eight(const GemmArgs& a, const Spot& s, BL
 }
 
 // The results, from the registers: no LDS and no barrier, so that a wave that is done with its
-// products writes while others multiply (8192 x 8192 x 4096 through LDS 297 us, so 272).  Of parts
-// of the contraction, sums in 32 bits.
+// products writes while others multiply (8192 x 8192 x 2048 through LDS 169 us, so 159, before
+// other steps).  Of parts of the contraction, sums in 32 bits.
 template <typename T, int TI, int TJ, int WI, int WJ, int FI, int FJ, bool GATED>
 __device__ __forceinline__ void write_direct(const GemmArgs& a, const Spot& s, BLK_LDS char* room, const f32x4 (&acc)[FI][FJ]) {
     typedef Columns<TJ, WJ, FJ, GATED> C;
@@ -308,17 +308,17 @@ __device__ __forceinline__ void keep_order() {
 // EIGHT: operands in 8 bits, with scales; else in T.
 //
 // Scales: where all of four blocks of a wave's rows and columns are powers of two, as
-// block_quantize makes them, the instruction itself takes their exponents (8192 x 8192 x 8192 431
-// us, 2550 TFLOP/s); others are multiplied in 32 bits and come on top of each block's sum by a
-// multiply-add a result on the vector units, beside the matrix cores (450 to 540 us, by the power
-// that is left).
+// block_quantize makes them, the instruction itself takes their exponents (8192 x 8192 x 8192 395
+// us, 2780 TFLOP/s); others are multiplied in 32 bits and come on top of each block's sum by a
+// multiply-add a result on the vector units, beside the matrix cores (445
+// us).  Both once the clocks have settled; the first calls after a pause take up to 80 more.
 //
 // Bound, at 256 x 256: 8-bit products by the way from the L2s into LDS and by the epilogue, which no
-// product overlaps (one workgroup a compute unit, all 160 KB of LDS): a loop of 264 us of 8192
-// x 8192 x 4096 takes 272 with bias, GELU, residual and z.  16-bit ones by power, as gemm_kernel;
+// product overlaps (one workgroup a compute unit, nearly all of its LDS): 8192 x 8192 x 4096 takes
+// 215 us, with bias, SiLU and a residual from memory 271.  16-bit ones by power, as gemm_kernel;
 // beside it these tiles keep Q's fragments in registers, so that a step reads 128 KiB of LDS
-// instead of 192, and have no copy of Q's next tile (16384 x 8192 x 4096 gated with uneven
-// groups 548 us, gemm_kernel's tiles 621).
+// instead of 192, and have no copy of Q's next tile (16384 rows over 8 uneven groups of 2 x
+// 4096 x 2048 with z 548 us, gemm_kernel's tiles 591).
 template <typename T, bool EIGHT, int TI, int TJ, int WI, int WJ, int STAGES, bool GATED>
 __global__ void __launch_bounds__(64 * WI * WJ, 2) tile_kernel(const GemmArgs a) {
     constexpr int THREADS = 64 * WI * WJ, FI = TI / WI / 16, FJ = TJ / WJ / 16, HALVES = GATED ? 2 : 1;
