@@ -596,6 +596,14 @@ rr_status_t expert_dispatch(rr_rows_t x, size_t tokens, size_t hidden, int k, rr
                             const int32_t *slots, const int32_t *sources, size_t rows,
                             rr_rows_t out, rr_stream_t stream);
 
+/* The same for the scales of 8-bit rows (below; fp32, `blocks` of them a row), whose values
+   go by expert_dispatch as rows of half as many 16-bit elements: rows without a source get
+   scales of 1, as block_quantize gives rows of zeros.  (A scale of 0 is none that the matrix
+   instructions take, and the rows beside it would do without them too.) */
+rr_status_t expert_dispatch_scales(rr_rows_t scales, size_t tokens, size_t blocks, int k,
+                                   const int32_t *slots, const int32_t *sources, size_t rows,
+                                   rr_rows_t out, rr_stream_t stream);
+
 /* out[t] = sum over j of weights[t * k + j] * rows[slots[t * k + j]], in the order
    of j; pairs without a slot are left out (a token without any gets zeros).
    weights are fp32; NULL: all 1, which is the gradient of expert_dispatch. */

@@ -108,6 +108,8 @@ def _bind(sig):
     g["_expert_sort_workspace"] = sig("expert_sort_workspace", _i, _sz, _i, _i, p(_sz))
     g["_expert_dispatch"] = sig("expert_dispatch", _i, _Rows, _sz, _sz, _i, _i, _vp, _vp, _sz,
                                 _Rows, _vp)
+    g["_expert_dispatch_scales"] = sig("expert_dispatch_scales", _i, _Rows, _sz, _sz, _i, _vp, _vp, _sz,
+                                       _Rows, _vp)
     g["_expert_combine"] = sig("expert_combine", _i, _Rows, _sz, _sz, _i, _vp, _vp, _sz, _i, _Rows,
                                _vp)
     g["_expert_combine_backward"] = sig("expert_combine_backward", _i, _Rows, _Rows, _sz, _sz, _i,
@@ -134,7 +136,8 @@ def _bind(sig):
                                                p(_sz))
 
 
-EXPORTED = ["expert_sort", "expert_sort_workspace", "expert_dispatch", "expert_combine",
+EXPORTED = ["expert_sort", "expert_sort_workspace", "expert_dispatch",
+            "expert_dispatch_scales", "expert_combine",
             "expert_combine_backward", "block_norm", "block_norm_backward",
             "block_norm_backward_workspace", "block_linear", "block_linear_workspace",
             "block_linear_backward", "block_linear_backward_workspace", "block_quantize",
@@ -325,7 +328,8 @@ def _pairs(slots, name="slots"):
 def expert_dispatch(x, slots, sources, *, out=None, stream=None):
     """Copies each token's row to the rows of its slots: [len(sources), hidden].  Rows
     without a source become zero.  A Quantized ``x`` (a scale for each 128 of a row, an even
-    number of columns) is dispatched as values and scales."""
+    number of columns) is dispatched as values and scales; rows without a source are zeros with
+    scales of 1, as ``block_quantize`` gives them."""
     if isinstance(x, Quantized):
         _need(out is None, "out is for tensors only")
         _quantized(x, "x", False)
@@ -334,10 +338,14 @@ def expert_dispatch(x, slots, sources, *, out=None, stream=None):
               (v.shape[0] < 2 or v.stride(0) % 2 == 0) and
               v.storage_offset() % 2 == 0, "x must be a matrix whose rows are whole pairs of values")
         _scales(x, "x", v.device)
-        return Quantized(expert_dispatch(v.view(torch.bfloat16), slots, sources, stream=stream).view(E4M3),
-                         expert_dispatch(x.scales, slots, sources, stream=stream))
+        return Quantized(_dispatch(v.view(torch.bfloat16), slots, sources, None, stream).view(E4M3),
+                         _dispatch(x.scales, slots, sources, None, stream, True))
+    return _dispatch(x, slots, sources, out, stream)
+
+
+def _dispatch(x, slots, sources, out, stream, scales=False):
     if stream is None and out is None:
-        done = _block.dispatch(x, slots, sources)
+        done = _block.dispatch(x, slots, sources, scales)
         if done is not None:
             return done
     dt = _float_type(x, "x")
@@ -351,7 +359,10 @@ def expert_dispatch(x, slots, sources, *, out=None, stream=None):
             out, o = _new(rows, hidden, x)
         else:
             o = _matrix(out, "out", x.device, x.dtype, rows, hidden)
-        _check(_expert_dispatch(xr, tokens, hidden, k, dt, sp, so, rows, o, s), "expert_dispatch")
+        if scales:
+            _check(_expert_dispatch_scales(xr, tokens, hidden, k, sp, so, rows, o, s), "expert_dispatch")
+        else:
+            _check(_expert_dispatch(xr, tokens, hidden, k, dt, sp, so, rows, o, s), "expert_dispatch")
     return out
 
 

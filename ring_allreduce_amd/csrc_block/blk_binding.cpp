@@ -157,20 +157,25 @@ PyObject* sort(Args& a) {
     return tuple({slots, sources, counts, offsets});
 }
 
-// x, slots, sources
+// x, slots, sources, whether x is scales of 8-bit rows
 PyObject* dispatch(Args& a) {
     const Tensor *x = a.needed(0), *slots = a.needed(1), *sources = a.needed(2);
+    const bool scales = a.flag(3);
     Call c;
     if (!a.good || !c.begin(*x) || x->dim() != 2 || slots->dim() != 2 || !known(x->scalar_type())) return none();
+    if (scales && x->scalar_type() != at::kFloat) return none();
     const int64_t tokens = x->size(0), hidden = x->size(1), k = slots->size(1), rows = sources->numel();
     rr_rows_t in, to;
     if (!c.matrix(*x, x->scalar_type(), tokens, hidden, in) || slots->size(0) != tokens || rows < 1 || k < 1 ||
         !c.vector(*slots, at::kInt, tokens * k) || !c.vector(*sources, at::kInt, rows))
         return none();
     Tensor out = c.make_rows(rows, hidden, x->scalar_type(), to);
-    if (expert_dispatch(in, (size_t)tokens, (size_t)hidden, (int)k, type_of(x->scalar_type()), ints(*slots),
-                        ints(*sources), (size_t)rows, to, c.stream) != RR_OK)
-        return none();
+    const rr_status_t st =
+        scales ? expert_dispatch_scales(in, (size_t)tokens, (size_t)hidden, (int)k, ints(*slots), ints(*sources),
+                                        (size_t)rows, to, c.stream)
+               : expert_dispatch(in, (size_t)tokens, (size_t)hidden, (int)k, type_of(x->scalar_type()), ints(*slots),
+                                 ints(*sources), (size_t)rows, to, c.stream);
+    if (st != RR_OK) return none();
     return wrap(out);
 }
 
@@ -634,7 +639,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     {name, (PyCFunction)(void (*)(void))(entry<f, n>), METH_FASTCALL, nullptr}
 
 PyMethodDef methods[] = {BLK_ENTRY("sort", sort, 3),
-                         BLK_ENTRY("dispatch", dispatch, 3),
+                         BLK_ENTRY("dispatch", dispatch, 4),
                          BLK_ENTRY("combine", combine, 3),
                          BLK_ENTRY("combine_backward", combine_backward, 7),
                          BLK_ENTRY("norm", norm, 11),

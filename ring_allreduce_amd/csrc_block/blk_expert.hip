@@ -324,7 +324,8 @@ struct MoveArgs {
     const float* weights;
     float* dweights;
     int32_t tokens, k, rows, hidden;
-    int32_t token_blocks;  // workgroups that take tokens; later ones clear unused rows
+    int32_t token_blocks;  // workgroups that take tokens; later ones fill unused rows
+    float unused;          // with this
 };
 
 constexpr int kMoveBlock = 256;
@@ -335,7 +336,7 @@ __device__ __forceinline__ int slot_of(const MoveArgs& a, int t, int j) {
     return s >= 0 && s < a.rows ? s : -1;
 }
 
-// Zeros in the rows without a pair, of kClearRows rows from `first`, a wave its share of them.
+// a.unused in the rows without a pair, of kClearRows rows from `first`, a wave its share of them.
 template <typename T>
 __device__ __forceinline__ void clear_rows(const MoveArgs& a, int64_t first) {
     constexpr int EACH = kClearRows / (kMoveBlock / 64);
@@ -347,14 +348,14 @@ __device__ __forceinline__ void clear_rows(const MoveArgs& a, int64_t first) {
         clear = p < 0 || (int64_t)p >= (int64_t)a.tokens * a.k;
     }
     uint64_t left = __ballot(clear);
-    Vec<T> zero;
+    Vec<T> fill;
 #pragma unroll
-    for (int i = 0; i < Vec<T>::N; ++i) zero.e[i] = (T)0.0f;
+    for (int i = 0; i < Vec<T>::N; ++i) fill.e[i] = (T)a.unused;
     while (left) {
         const int b = __ffsll((unsigned long long)left) - 1;
         left &= left - 1;
         T* row = (T*)a.out + (uint64_t)(first + b) * a.out_ld;
-        for (int c = lane * Vec<T>::N; c < a.hidden; c += 64 * Vec<T>::N) store_vec(row, c, a.hidden, zero);
+        for (int c = lane * Vec<T>::N; c < a.hidden; c += 64 * Vec<T>::N) store_vec(row, c, a.hidden, fill);
     }
 }
 
@@ -668,6 +669,45 @@ template <typename T, int G> static void launch_backward(const MoveArgs& a, unsi
 
 using namespace blk;
 
+static rr_status_t dispatch(rr_rows_t x, size_t tokens, size_t hidden, int k, rr_dtype_t dt,
+                            const int32_t* slots, const int32_t* sources, size_t rows, float unused,
+                            rr_rows_t out, rr_stream_t stream) {
+    const rr_status_t st = check_move(tokens, hidden, k, rows, dt);
+    if (st != RR_OK) return st;
+    if (!good_rows(x, tokens, hidden, dt) || !good_rows(out, rows, hidden, dt))
+        return RR_ERR_INVALID;
+    const uint64_t pairs = (uint64_t)tokens * k;
+    if ((tokens && (!slots || !aligned_to(slots, 4))) || (rows && (!sources || !aligned_to(sources, 4))))
+        return RR_ERR_INVALID;
+    const uint64_t n_out = reach(out, rows, hidden, dt);
+    if (overlap(x.data, reach(x, tokens, hidden, dt), out.data, n_out) ||
+        overlap(slots, pairs * 4, out.data, n_out) || overlap(sources, rows * 4, out.data, n_out))
+        return RR_ERR_INVALID;
+    if (rows == 0) return RR_OK;
+    MoveArgs a = {};
+    a.in = x.data;
+    a.in_ld = x.ld;
+    a.out = out.data;
+    a.out_ld = out.ld;
+    a.slots = slots;
+    a.sources = sources;
+    a.tokens = (int32_t)tokens;
+    a.k = k;
+    a.rows = (int32_t)rows;
+    a.hidden = (int32_t)hidden;
+    const int g = group_for(hidden, dt);
+    if (!grid_fits(ceil_div(tokens, kMoveBlock / g) + ceil_div(rows, kClearRows)))
+        return RR_ERR_UNSUPPORTED;
+    a.token_blocks = (int32_t)ceil_div(tokens, kMoveBlock / g);
+    a.unused = unused;
+    const unsigned grid = (unsigned)(a.token_blocks + ceil_div(rows, kClearRows));
+    hipStream_t s = (hipStream_t)stream;
+#define CALL(T) BLK_BY_GROUP(g, T, dispatch_kernel, grid, s, a)
+    BLK_BY_TYPE(dt, CALL)
+#undef CALL
+    return launched();
+}
+
 extern "C" {
 
 rr_status_t expert_sort_workspace(size_t tokens, int k, int experts, size_t* bytes) {
@@ -726,39 +766,13 @@ rr_status_t expert_sort(const void* ids, int id_bytes, size_t id_ld, size_t toke
 rr_status_t expert_dispatch(rr_rows_t x, size_t tokens, size_t hidden, int k, rr_dtype_t dt,
                             const int32_t* slots, const int32_t* sources, size_t rows,
                             rr_rows_t out, rr_stream_t stream) {
-    const rr_status_t st = check_move(tokens, hidden, k, rows, dt);
-    if (st != RR_OK) return st;
-    if (!good_rows(x, tokens, hidden, dt) || !good_rows(out, rows, hidden, dt))
-        return RR_ERR_INVALID;
-    const uint64_t pairs = (uint64_t)tokens * k;
-    if ((tokens && (!slots || !aligned_to(slots, 4))) || (rows && (!sources || !aligned_to(sources, 4))))
-        return RR_ERR_INVALID;
-    const uint64_t n_out = reach(out, rows, hidden, dt);
-    if (overlap(x.data, reach(x, tokens, hidden, dt), out.data, n_out) ||
-        overlap(slots, pairs * 4, out.data, n_out) || overlap(sources, rows * 4, out.data, n_out))
-        return RR_ERR_INVALID;
-    if (rows == 0) return RR_OK;
-    MoveArgs a = {};
-    a.in = x.data;
-    a.in_ld = x.ld;
-    a.out = out.data;
-    a.out_ld = out.ld;
-    a.slots = slots;
-    a.sources = sources;
-    a.tokens = (int32_t)tokens;
-    a.k = k;
-    a.rows = (int32_t)rows;
-    a.hidden = (int32_t)hidden;
-    const int g = group_for(hidden, dt);
-    if (!grid_fits(ceil_div(tokens, kMoveBlock / g) + ceil_div(rows, kClearRows)))
-        return RR_ERR_UNSUPPORTED;
-    a.token_blocks = (int32_t)ceil_div(tokens, kMoveBlock / g);
-    const unsigned grid = (unsigned)(a.token_blocks + ceil_div(rows, kClearRows));
-    hipStream_t s = (hipStream_t)stream;
-#define CALL(T) BLK_BY_GROUP(g, T, dispatch_kernel, grid, s, a)
-    BLK_BY_TYPE(dt, CALL)
-#undef CALL
-    return launched();
+    return dispatch(x, tokens, hidden, k, dt, slots, sources, rows, 0.0f, out, stream);
+}
+
+rr_status_t expert_dispatch_scales(rr_rows_t scales, size_t tokens, size_t blocks, int k,
+                                   const int32_t* slots, const int32_t* sources, size_t rows,
+                                   rr_rows_t out, rr_stream_t stream) {
+    return dispatch(scales, tokens, blocks, k, RR_FP32, slots, sources, rows, 1.0f, out, stream);
 }
 
 rr_status_t expert_combine(rr_rows_t in, size_t rows, size_t hidden, rr_dtype_t dt,

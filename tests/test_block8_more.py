@@ -1,0 +1,27 @@
+"""More of what the operators of 8-bit rows refuse, on the host (no GPU needed; the addresses are
+never dereferenced)."""
+import pytest
+
+A = 0x7F0000000000
+
+
+@pytest.fixture(scope="module")
+def blk():
+    import ring_allreduce_amd.block as block
+    return block
+
+
+def at(n):
+    return A + (n << 30)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(x=None), 1), (dict(out=None), 1), (dict(x=at(0) + 2), 1), (dict(out=at(1) + 2), 1), (dict(x_ld=31), 1),
+    (dict(out_ld=31), 1), (dict(blocks=0), 1), (dict(k=0), 1), (dict(slots=None), 1), (dict(sources=None), 1),
+    (dict(sources=at(3) + 2), 1), (dict(tokens=1 << 31), 2), (dict(rows=1 << 31), 2), (dict(out=at(0) + 128), 1),
+    (dict(sources=at(1) + 4), 1), (dict(rows=0, tokens=0, x=None, out=None), 0)])
+def test_dispatch_of_scales(blk, change, status):
+    c = dict(dict(x=at(0), x_ld=32, tokens=8, blocks=32, k=2, slots=at(2), sources=at(3), rows=16, out=at(1),
+                  out_ld=32), **change)
+    assert blk._expert_dispatch_scales(blk._Rows(c["x"], c["x_ld"]), c["tokens"], c["blocks"], c["k"], c["slots"],
+                                       c["sources"], c["rows"], blk._Rows(c["out"], c["out_ld"]), None) == status

@@ -1,0 +1,65 @@
+"""8-bit rows on their way between experts."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def rr():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import ring_allreduce_amd
+    ring_allreduce_amd.init()
+    return ring_allreduce_amd
+
+
+def normal(shape, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).bfloat16()
+
+
+def sorted_rows(rr, tokens, experts, capacity, seed=0):
+    """Two experts a token, a few masked out, with room for more rows than there are."""
+    ids = torch.randint(-1, experts, (tokens, 2), generator=torch.Generator().manual_seed(seed)).cuda()
+    return rr.expert_sort(ids, experts, capacity)
+
+
+# ------------------------------------------- rows without a source, and their products --
+
+@pytest.mark.parametrize("rows_of", [(200, 6, 90), (5, 3, 16), (0, 2, 8), (3000, 4, 2048)], ids=str)
+def test_rows_without_a_source_have_scale_one(rr, rows_of):
+    """As block_quantize gives rows of zeros: a scale of 0 would cost the products of the rows beside
+    them the instruction's own scales."""
+    tokens, experts, capacity = rows_of
+    order = sorted_rows(rr, tokens, experts, capacity)
+    x = rr.block_quantize(normal((tokens, 264), 1))
+    for stream in (None, torch.cuda.current_stream()):
+        got = rr.expert_dispatch(x, order.slots, order.sources, stream=stream)
+        none = order.sources < 0
+        assert bool(none.any())
+        assert bool((got.scales[none] == 1).all()) and not bool(got.values.view(torch.uint8)[none].any())
+        there = (order.sources[~none] // 2).long()
+        assert torch.equal(got.scales[~none], x.scales[there])
+        assert torch.equal(got.values.view(torch.uint8)[~none], x.values.view(torch.uint8)[there])
+
+
+@pytest.mark.parametrize("tokens,capacity,n", [(40, 16, 200), (300, 130, 320), (3000, 2048, 1152)])
+def test_products_beside_rows_without_a_source(rr, tokens, capacity, n):
+    """Are to the bit what they are beside rows that all have one."""
+    experts, k = 4, 1024
+    order = sorted_rows(rr, tokens, experts, capacity)
+    rows = rr.expert_dispatch(rr.block_quantize(normal((tokens, k), 2)), order.slots, order.sources)
+    there = order.sources >= 0
+    assert not bool(there.all())
+    filled = rr.Quantized(rows.values.clone(), rows.scales.clone())
+    other = int(torch.nonzero(there)[0])
+    filled.values.view(torch.uint8)[~there] = rows.values.view(torch.uint8)[other]
+    filled.scales[~there] = rows.scales[other]
+    w = rr.block_quantize(normal((experts, 2, n, k), 3, k ** -0.5), square=True)
+    first = rr.Quantized(w.values[:, 0].contiguous(), w.scales[:, 0].contiguous(), True)
+    for offsets in (None, order.offsets):
+        a, b = (rr.block_gated(r, w, offsets=offsets) for r in (rows, filled))
+        assert torch.equal(a[there], b[there]) and not bool(a[~there].any())
+        a, b = (rr.block_linear8(r, first, offsets=offsets) for r in (rows, filled))
+        assert torch.equal(a[there], b[there]) and not bool(a[~there].any())
