@@ -338,6 +338,8 @@ def expert_dispatch(x, slots, sources, *, out=None, stream=None):
               (v.shape[0] < 2 or v.stride(0) % 2 == 0) and
               v.storage_offset() % 2 == 0, "x must be a matrix whose rows are whole pairs of values")
         _scales(x, "x", v.device)
+        if v.shape[0] < 2:              # no distance between rows to speak of, odd or not
+            v = v.as_strided(v.shape, (v.shape[1], 1))
         return Quantized(_dispatch(v.view(torch.bfloat16), slots, sources, None, stream).view(E4M3),
                          _dispatch(x.scales, slots, sources, None, stream, True))
     return _dispatch(x, slots, sources, out, stream)

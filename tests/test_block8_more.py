@@ -1,8 +1,15 @@
 """More of what the operators of 8-bit rows refuse, on the host (no GPU needed; the addresses are
 never dereferenced)."""
 import pytest
+import torch
 
 A = 0x7F0000000000
+
+
+@pytest.fixture(scope="module")
+def rr():
+    import ring_allreduce_amd
+    return ring_allreduce_amd
 
 
 @pytest.fixture(scope="module")
@@ -25,3 +32,13 @@ def test_dispatch_of_scales(blk, change, status):
                   out_ld=32), **change)
     assert blk._expert_dispatch_scales(blk._Rows(c["x"], c["x_ld"]), c["tokens"], c["blocks"], c["k"], c["slots"],
                                        c["sources"], c["rows"], blk._Rows(c["out"], c["out_ld"]), None) == status
+
+
+@pytest.mark.parametrize("rows", [0, 1])
+def test_dispatch_of_one_row_of_a_buffer_of_odd_rows(rr, rows):
+    """Its distance to the next row is no reason to refuse it: that it is on no GPU is."""
+    flat = torch.zeros(64, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    x = rr.Quantized(flat.as_strided((rows, 6), (7, 1), 2), torch.ones(rows, 1))
+    slots = torch.zeros(rows, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        rr.expert_dispatch(x, slots, slots.reshape(-1))

@@ -63,3 +63,16 @@ def test_products_beside_rows_without_a_source(rr, tokens, capacity, n):
         assert torch.equal(a[there], b[there]) and not bool(a[~there].any())
         a, b = (rr.block_linear8(r, first, offsets=offsets) for r in (rows, filled))
         assert torch.equal(a[there], b[there]) and not bool(a[~there].any())
+
+
+def test_dispatch_of_one_row_of_a_buffer_of_odd_rows(rr):
+    x = rr.block_quantize(normal((3, 258), 4))
+    wide = torch.zeros(3, 261, dtype=torch.uint8, device="cuda")
+    wide[:, 2:260] = x.values.view(torch.uint8)
+    order = rr.expert_sort(torch.tensor([[1, 0]], device="cuda"), 2, 2)
+    for r in range(0, 3, 2):
+        one = rr.Quantized(wide.view(x.values.dtype)[r:r + 1, 2:260], x.scales[r:r + 1])
+        got = rr.expert_dispatch(one, order.slots, order.sources)
+        there = order.sources >= 0
+        assert torch.equal(got.values.view(torch.uint8)[there], x.values.view(torch.uint8)[[r, r]])
+        assert torch.equal(got.scales[there], x.scales[[r, r]])
