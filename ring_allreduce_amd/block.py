@@ -835,10 +835,11 @@ def _wide_args(x, w, offsets, act, dtype, halves):
     _need(l.groups >= 1, "w must have at least one group")
     l.n = wv.shape[-2]
     first = wv[0] if wv.dim() > d else wv
+    if halves == 2:
+        _need(first.shape[0] == 2, "w must hold two matrices, the gate's and the other projection's")
     r = _matrix(first[0] if halves == 2 else first, "w")
     l.w, l.w_ld = r.data, r.ld
     if halves == 2:
-        _need(first.shape[0] == 2, "w must hold two matrices, the gate's and the other projection's")
         if l.n == 1:
             l.w_ld = first.stride(0)
         _need(first.stride(0) == l.n * l.w_ld, "w: the second matrix must follow the first")

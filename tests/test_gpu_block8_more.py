@@ -76,3 +76,15 @@ def test_dispatch_of_one_row_of_a_buffer_of_odd_rows(rr):
         there = order.sources >= 0
         assert torch.equal(got.values.view(torch.uint8)[there], x.values.view(torch.uint8)[[r, r]])
         assert torch.equal(got.scales[there], x.scales[[r, r]])
+
+
+# ------------------------------------------------------------------- refusals --
+
+def test_weights_of_no_matrices(rr):
+    x = normal((4, 8), 5)
+    for lead in ((0,), (1,), (3,), (2, 0), (2, 1), (2, 3)):
+        w = torch.zeros(*lead, 6, 8, device="cuda", dtype=torch.bfloat16)
+        with pytest.raises(ValueError, match="two matrices"):
+            rr.block_gated(x, w)
+        with pytest.raises(ValueError, match="two matrices"):
+            rr.block_gated_backward(x[:, :6], x, w, torch.zeros(4, 12, device="cuda", dtype=torch.bfloat16))
