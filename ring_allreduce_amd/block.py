@@ -757,6 +757,7 @@ def block_quantize(x, *, square=False, stream=None) -> Quantized:
         done = _block.quantize(x, square)
         if done is not None:
             return Quantized(*done, bool(square))
+    _need(isinstance(x, torch.Tensor), "x must be a matrix, or matrices")
     dt = _float_type(x, "x")
     _need(x.dim() >= 2, "x must be a matrix, or matrices")
     _need(x.is_cuda, "x must be on a GPU")
@@ -771,7 +772,7 @@ def block_quantize(x, *, square=False, stream=None) -> Quantized:
 
 
 def block_dequantize(q, dtype=torch.bfloat16, *, out=None, stream=None):
-    """What ``q`` stands for, in ``dtype``; a finite value beyond float16's largest becomes that."""
+    """What ``q`` stands for, in ``dtype``, or in ``out``'s; a finite value beyond float16's largest becomes that."""
     if stream is None and out is None and isinstance(q, Quantized):
         done = _block.dequantize(q.values, q.scales, q.square, FLOAT_DTYPES.get(dtype, -1))
         if done is not None:
@@ -784,6 +785,7 @@ def block_dequantize(q, dtype=torch.bfloat16, *, out=None, stream=None):
     dev = q.values.device
     _scales(q, "q", dev)
     if out is not None:
+        _need(isinstance(out, torch.Tensor), "out must be a tensor")
         dtype = out.dtype
         _need(out.device == dev and out.shape == q.values.shape, "out must have q's shape and GPU")
     if dtype not in FLOAT_DTYPES:

@@ -88,3 +88,11 @@ def test_weights_of_no_matrices(rr):
             rr.block_gated(x, w)
         with pytest.raises(ValueError, match="two matrices"):
             rr.block_gated_backward(x[:, :6], x, w, torch.zeros(4, 12, device="cuda", dtype=torch.bfloat16))
+
+
+def test_what_is_no_tensor(rr):
+    q = rr.block_quantize(normal((4, 8), 6))
+    for call in (lambda: rr.block_quantize(None), lambda: rr.block_quantize([1.0]),
+                 lambda: rr.block_dequantize(q, out=5)):
+        with pytest.raises(ValueError):
+            call()
