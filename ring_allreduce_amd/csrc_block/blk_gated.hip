@@ -285,16 +285,21 @@ static int parts_of(uint64_t blocks, uint64_t most) {
 
 // Few rows of 8-bit operands (of up to 64, `n` columns of both halves): microseconds on weights in
 // no cache.  One row goes as dots.  Up to 16 the one-pass form, 16 columns a workgroup where it
-// has them (3 x 8192 x 8192 17.2, 16 x 4096 x 4096 8.4), but of more than 8 by large weights 64 x
+// has them (4 x 8192 x 8192 17.6, with 32 columns 21.0; 16 x 4096 x 4096 8.8 and 10.4; 2 x 4096 x
+// 8191 24 and 42; but 16 x 4112 x 8192 21.4 and 18.0), but of more than 8 by large weights 64 x
 // 64 tiles, deep, and parts of the contraction to fill the device (16 x 8192 x 8192 18.9 against
 // 21).  Up to 32 the one-pass form for weights under 48 MB (32 x 4096 x 4096 11.1, tiles 12.3; 32 x
-// 8192 x 8192 30 and 20.3), and tiles beyond (48 x 4096 x 4096 12.7, one pass 17; 64 x 8192 x 8192
-// 21 and 40).  Rows of many groups, where the weights' read is all: to 16 a group, 8 of uneven
-// ones, of which some have more and read their weights twice, the one pass (32 groups of 2 x 2048
-// x 4096, 256 uneven rows 124, tiles 126; 512 uneven ones 174 and 126, equal ones 117 and 122), then
-// deep tiles (with two stages 137).  Of groups whose rows are whole words (`words`), which the one
-// pass takes without knowing where pieces begin, always the tiles (32 groups of 2 x 2048 x 4088,
-// 64, 128 and 256 uneven rows 86, 101 and 112, one pass 108, 127 and 155).
+// 8192 x 8192 30 and 20.3), 16 columns a workgroup where that gives no compute unit a second one
+// (32 x 4096 x 4096 11.0, with 32 columns 12.7, 17 x 2064 x 2048 5.7 and 9.2; but 32 x 4112 x 2048
+// 9.8 and 8.1, 32 x 6144 x 4096 18.2 and 13.3) and rows are short (17 and 32 x 4096 x 8192 14.5 and
+// 15.7, 18.5 and 17.8; at any byte 32 x 4096 x 1023 8.7 and 10.7, x 4095 26.5 and 22.5); and tiles
+// beyond (48 x 4096 x 4096 12.7, one pass 17; 64 x 8192 x 8192 21 and 40).  Rows of many groups,
+// where the weights' read is all: to 16 a group, 8 of uneven ones, of which some have more and read
+// their weights twice, the one pass (32 groups of 2 x 2048 x 4096, 256 uneven rows 124, tiles 126;
+// 512 uneven ones 174 and 126, equal ones 117 and 122), then deep tiles (with two stages 137).  Of
+// groups whose rows are whole words (`words`), which the one pass takes without knowing where pieces
+// begin, always the tiles (32 groups of 2 x 2048 x 4088, 64, 128 and 256 uneven rows 86, 101 and 112,
+// one pass 108, 127 and 155).
 // `direct`: operands whose rows are whole words; the tiles copy others first.
 static void choose_few(const rr_linear8_t* a, uint64_t halves, bool direct, bool words, Forward& f) {
     const rr_linear_t& l = a->l;
@@ -313,7 +318,7 @@ static void choose_few(const rr_linear8_t* a, uint64_t halves, bool direct, bool
         parts(ceil_div(n, p.narrow ? 16 : 32), ceil_div(n, 32) <= 32 && !p.narrow ? l.k / 512 : 1);
     } else if (one && mean <= 32 && !large) {
         p.tile = kStream32;
-        p.narrow = halves == 1 && n >= 4096 && n < 8192;
+        p.narrow = halves == 1 && ceil_div(n, 16) <= kSlots && l.k <= (direct && !words ? 4096 : 1024);
         parts(ceil_div(n, p.narrow ? 16 : 32), l.k / 512);
     } else {
         p.tile = kTile64;

@@ -2,6 +2,9 @@
 import pytest
 import torch
 
+from tests.block8_util import linear64
+from tests.block_util import assert_within, store_error
+
 pytestmark = pytest.mark.gpu
 
 
@@ -76,6 +79,20 @@ def test_dispatch_of_one_row_of_a_buffer_of_odd_rows(rr):
         there = order.sources >= 0
         assert torch.equal(got.values.view(torch.uint8)[there], x.values.view(torch.uint8)[[r, r]])
         assert torch.equal(got.scales[there], x.scales[[r, r]])
+
+
+# ------------------------------------------------------------------ few rows --
+
+@pytest.mark.parametrize("rows", [17, 32])
+@pytest.mark.parametrize("n,k", [(130, 1024), (130, 1025), (2100, 1009), (4096, 512), (4097, 512), (4100, 4096),
+                                 (3000, 4112)])
+def test_17_to_32_rows(rr, rows, n, k):
+    """Both widths of a workgroup of the one-pass form, on either side of where one takes over."""
+    x = rr.block_quantize(normal((rows, k), 8))
+    w = rr.block_quantize(normal((n, k), 9, k ** -0.5), square=True)
+    got = rr.block_linear8(x, w)
+    want, _, error, _ = linear64(x, w, None, None, "none", None)
+    assert_within(got, want, store_error(want, torch.bfloat16) + error * (1 + 2 ** -7), "out")
 
 
 # ------------------------------------------------------------------- refusals --
