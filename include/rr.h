@@ -753,10 +753,15 @@ rr_status_t block_dequantize(const rr_quantize_t *a, rr_stream_t stream);
 /* A block's product of 8-bit operands, as rr_linear_t says, with l.x and l.w in e4m3:
    l.x.ld, l.w_ld and l.w_stride are bytes, x has a scale for 128 columns of a row and w_e
    square blocks, both as above (rows and n x k matrices); any finite fp32 scales will do.  l.dt is
-   the type of bias, residual, z and out.  The products of a block of 128 are summed in
-   the matrix instructions' 32 bits, the blocks on top of each other, times their scales, in
-   32 bits; a scale of x times one of w is rounded to fp32 too.  z_scales: NULL.  Limits:
-   groups * n < 2^31 - 1024. */
+   the type of bias, residual, z and out.  The products of a block of 128 are summed by
+   the matrix instructions: in 32 bits, but before eight neighbours are added each is cut at
+   2^-13 of the power of two of the largest (with E the largest sum of the exponents of a
+   value of x and its one of w, at least -6 each, at multiples of 2^(E - 13)), so that up
+   to 7 * 2^(E - 13) of their sum may be missing.  The blocks are added in 32 bits, times
+   their scales; a scale of x times one of w is rounded to fp32 too.  One row alone (of at
+   least 16 columns, without offsets) is summed in 32 bits throughout, so that the same row
+   among others may come out different by what is cut.  z_scales: NULL.  Limits: groups * n
+   < 2^31 - 1024. */
 typedef struct {
     rr_linear_t l;
     const float *x_scales, *w_scales;
@@ -780,8 +785,8 @@ rr_status_t block_linear8_backward_workspace(const rr_linear8_t *a, const rr_lin
    elements behind, the other projection's n rows; bias has groups * 2 * n elements, z rows
    have the n columns of g and then those of u; l.n is n, and l.residual absent.  Sizes,
    groups, offsets and types as rr_linear_t says, l.act also RR_ACT_SIGMOID.  x and w
-   both with scales: products of 8-bit operands, w_e's two halves being matrices of n rows
-   with blocks of their own.  z with z_scales: e4m3, z.ld in bytes, each half of a row
+   both with scales: products of 8-bit operands, summed as block_linear8 says, w_e's two
+   halves being matrices of n rows with blocks of their own.  z with z_scales: e4m3, z.ld in bytes, each half of a row
    in blocks of its own (rows * 2 * ceil(n / 128) scales, g's of a row first):
    block_quantize's of z in dt.  Limits: 2 * n <= 2^22, groups * 2 * n and, with z_scales,
    2 * rows < 2^31 - 1024. */

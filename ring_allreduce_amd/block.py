@@ -867,7 +867,9 @@ def block_linear8(x, w, bias=None, *, dtype=torch.bfloat16, act="none", residual
     """``block_linear`` of 8-bit operands: ``x`` Quantized [rows, k] with a scale for each 128 of a
     row, ``w`` Quantized [n, k] or [groups, n, k] with square blocks (``block_quantize``'s, or any
     others with finite fp32 scales).  ``dtype`` (bfloat16 or float16) is the type of bias, residual, z
-    and out."""
+    and out.  Sums are held in 32 bits, but for more rows than one the matrix instructions cut each
+    of eight neighbouring products at 2^-13 of the power of two of the largest before they add them
+    (``include/rr.h`` has the bound)."""
     if stream is None and out is None and isinstance(x, Quantized) and isinstance(w, Quantized) and \
             w.square and not x.square:
         done = _block.linear8(x.values, x.scales, w.values, w.scales, bias, ACTS.get(act, -1),
@@ -967,9 +969,9 @@ def block_gated(x, w, bias=None, *, act="silu", offsets=None, save_preact=False,
     the other projection's) and bias [2, n], or the rows of each group with its own w [groups, 2, n,
     k] and bias [groups, 2, n]; ``offsets`` as ``block_linear`` takes them.  act: none, relu, gelu,
     silu or sigmoid.  x and w are tensors of ``dtype``, or both Quantized (then ``dtype`` says the
-    type of bias, z and out: bfloat16 by default).  Returns out, or (out, z) if save_preact: z
-    [rows, 2 n] is g and u, and with save_preact="e4m3" a Quantized [rows, 2, n].  Rows of no group
-    become zero."""
+    type of bias, z and out: bfloat16 by default; sums as ``block_linear8`` says).  Returns out, or
+    (out, z) if save_preact: z [rows, 2 n] is g and u, and with save_preact="e4m3" a Quantized [rows,
+    2, n].  Rows of no group become zero."""
     eight = save_preact == "e4m3"
     if stream is None and out is None:
         kind = FLOAT_DTYPES.get(dtype, -1 if dtype is not None else 0)

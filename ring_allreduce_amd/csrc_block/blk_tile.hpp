@@ -16,8 +16,8 @@ namespace blk {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// A lane's 32 bytes of a row's 128: the same ones of both operands; which ones does not matter to
-// the sum.
+// A lane's 32 bytes of a row's 128: the same ones of both operands; which ones matters to the sum
+// only by the eights that are neighbours.
 typedef i32x8 Frag;
 __device__ __forceinline__ Frag frag_of(u32x4 lo, u32x4 hi) {
     return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));

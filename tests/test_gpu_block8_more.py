@@ -1,8 +1,8 @@
-"""8-bit rows on their way between experts."""
+"""8-bit rows on their way between experts, and what sums of 8-bit products keep."""
 import pytest
 import torch
 
-from tests.block8_util import linear64
+from tests.block8_util import E4M3, linear64
 from tests.block_util import assert_within, store_error
 
 pytestmark = pytest.mark.gpu
@@ -93,6 +93,58 @@ def test_17_to_32_rows(rr, rows, n, k):
     got = rr.block_linear8(x, w)
     want, _, error, _ = linear64(x, w, None, None, "none", None)
     assert_within(got, want, store_error(want, torch.bfloat16) + error * (1 + 2 ** -7), "out")
+
+
+# --------------------------------------------------------- what the sums keep --
+
+SIZES = [(1, 14), (1, 2800), (5, 70), (20, 210), (40, 700), (200, 140), (600, 700), (1024, 4200), (2560, 4620)]
+
+
+@pytest.mark.parametrize("foreign", [False, True])
+@pytest.mark.parametrize("rows,n", SIZES)
+def test_a_small_product_beside_a_large_one(rr, rows, n, foreign):
+    """Beside a product of 2^16 among the same eight neighbours, which another eight cancel, one of
+    2^0 to 2^6 is there to the bit or, below 2^3, cut away; among other eight it is always there.  Of one row
+    all are.  Scales by the instruction (four blocks of powers of two) and on top of its sums."""
+    k = 512
+    x = torch.zeros(rows, k, device="cuda")
+    x[:, 0] = x[:, 64] = 256.0
+    x[:, 1] = x[:, 72] = 2.0
+    w = torch.zeros(14, k, device="cuda")
+    w[:, 0], w[:, 64] = 256.0, -256.0
+    for j in range(14):
+        w[j, 1 if j < 7 else 72] = 2.0 ** (j % 7 - 1)
+    w = w.repeat(n // 14, 1)
+    xs, ws = torch.ones(rows, 4, device="cuda"), torch.ones(-(-n // 128), 4, device="cuda")
+    if foreign:
+        xs *= 3.0
+    out = rr.block_linear8(rr.Quantized(x.to(E4M3), xs), rr.Quantized(w.to(E4M3), ws, True)).float()
+    exact = torch.tensor([2.0 ** (j % 7) for j in range(14)], device="cuda").repeat(n // 14) * (3 if foreign else 1)
+    keep = torch.tensor([j >= 3 or rows == 1 for j in range(14)], device="cuda").repeat(n // 14)
+    assert torch.equal(out[:, keep], exact[keep].expand(rows, -1))
+    assert bool(((out == exact) | (out == 0)).all())
+
+
+@pytest.mark.parametrize("foreign", [False, True])
+@pytest.mark.parametrize("rows,n", SIZES)
+def test_sums_of_blocks_are_kept_in_32_bits(rr, rows, n, foreign):
+    """2^23 from one block of 128, a small sum from a later one and -2^23 from another: what is left is
+    the small one but for a whole step of 32 bits at the large one for each of the three."""
+    k, f = 1024, 15.0 if foreign else 1.0
+    small = [4.0, 16.0, 64.0, 256.0, 448.0, 32.0, 8.0]
+    x = torch.ones(rows, k, device="cuda")
+    w = torch.zeros(7, k, device="cuda")
+    x[:, :128] = x[:, 768:896] = 256.0
+    w[:, :128], w[:, 768:896] = 256.0, -256.0
+    w[:, 400] = torch.tensor(small, device="cuda")
+    w = w.repeat(n // 7, 1)
+    xs, ws = torch.ones(rows, 8, device="cuda"), torch.ones(-(-n // 128), 8, device="cuda")
+    if foreign:
+        xs, ws = xs * 3.0, ws * 5.0
+    out = rr.block_linear8(rr.Quantized(x.to(E4M3), xs), rr.Quantized(w.to(E4M3), ws, True)).float()
+    exact = torch.tensor(small, device="cuda").repeat(n // 7) * f
+    bound = 3 * 2.0 ** -23 * 2.0 ** 23 * f
+    assert bool(((out - exact).abs() <= bound + 2.0 ** -8 * (exact + bound)).all())
 
 
 # ------------------------------------------------------------------- refusals --
