@@ -772,8 +772,11 @@ rr_status_t block_linear8(const rr_linear8_t *a, void *workspace, size_t workspa
 rr_status_t block_linear8_workspace(const rr_linear8_t *a, size_t *bytes);
 /* The gradients of block_linear or block_linear8, at what the 8 bits stand for: x and w are
    each in e4m3 where they have scales, else in l.dt.  8-bit operands become dt on their way
-   into the products, which is exact with block_quantize's scales (but for values past the
-   ends of RR_FP16) and half a step off with others. */
+   into the products.  That is exact with scales that are powers of two, for RR_BF16 from
+   2^-117 on, for RR_FP16 from 2^-15 to 2^7 or where block_quantize made them of RR_FP16 values
+   (65536 becomes 65504).  Else it is up to half a step of dt off, which for RR_FP16 is 2^-25 at
+   least, and what is past RR_FP16's ends becomes 65504 of its sign: such gradients are at
+   other values than the forward pass, which takes any scale, has seen. */
 rr_status_t block_linear8_backward(const rr_linear8_t *a, const rr_linear_grad_t *g,
                                    void *workspace, size_t workspace_bytes, rr_stream_t stream);
 rr_status_t block_linear8_backward_workspace(const rr_linear8_t *a, const rr_linear_grad_t *g,

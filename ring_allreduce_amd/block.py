@@ -914,7 +914,8 @@ def block_linear8_backward(dout, x, w, z=None, *, act="none", offsets=None, need
                            need_db=True, dw_dtype=None, stream=None) -> LinearGrads:
     """Gradients of ``block_linear8`` or ``block_linear`` by x, w and bias, at what ``x`` and ``w``
     stand for: each Quantized, as a forward pass used or kept it, or a tensor of ``dout``'s
-    dtype."""
+    dtype.  A Quantized becomes that dtype on its way into the products: float16 has multiples of 2^-24
+    up to 65504, and what is smaller or larger than its values becomes the nearest one."""
     if not isinstance(dout, torch.Tensor):
         raise ValueError("dout must be a matrix")
     dtype = dout.dtype
@@ -1023,7 +1024,7 @@ def block_gated_backward(dout, x, w, z, *, act="silu", offsets=None, need_dx=Tru
                          need_db=True, need_out=False, dw_dtype=None, stream=None) -> GatedGrads:
     """Gradients of ``block_gated`` by x, w and bias, of w's shape.  ``z`` is what save_preact
     gave, in either form; x and w are tensors of ``dout``'s dtype or Quantized, each by itself: the
-    gradients are those at what they stand for.  ``need_out`` makes the forward pass's out
+    gradients are those at what they stand for, in that dtype as ``block_linear8_backward`` says.  ``need_out`` makes the forward pass's out
     again, which the next product's backward pass reads, so that nobody has to keep it."""
     if not isinstance(dout, torch.Tensor):
         raise ValueError("dout must be a matrix")

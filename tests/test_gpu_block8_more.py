@@ -2,8 +2,8 @@
 import pytest
 import torch
 
-from tests.block8_util import E4M3, linear64
-from tests.block_util import assert_within, store_error
+from tests.block8_util import E4M3, gated_dz64, gradients64, linear64, wide
+from tests.block_util import U, assert_within, store_error
 
 pytestmark = pytest.mark.gpu
 
@@ -145,6 +145,41 @@ def test_sums_of_blocks_are_kept_in_32_bits(rr, rows, n, foreign):
     exact = torch.tensor(small, device="cuda").repeat(n // 7) * f
     bound = 3 * 2.0 ** -23 * 2.0 ** 23 * f
     assert bool(((out - exact).abs() <= bound + 2.0 ** -8 * (exact + bound)).all())
+
+
+# ------------------------------------------- gradients at the ends of 16-bit types --
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("size", [3e4, 1e-2, 1e-4, 1e-5, 1e-7])
+@pytest.mark.parametrize("which", ["x", "w"])
+def test_gradients_of_large_and_small_operands(rr, dtype, size, which):
+    """8-bit operands become dtype on their way: in bf16 exactly, in fp16 where it has what they stand
+    for, else the multiple of 2^-24 next to it or, past the end, 65504.  The forward pass takes any."""
+    rows, n, k = 150, 70, 200
+    x = torch.randn(rows, k, generator=torch.Generator().manual_seed(1)).cuda() * (size if which == "x" else 1.0)
+    w = torch.randn(2, n, k, generator=torch.Generator().manual_seed(2)).cuda() * (size if which == "w" else 1.0)
+    x, w = rr.block_quantize(x), rr.block_quantize(w, square=True)
+    first = rr.Quantized(w.values[0].contiguous(), w.scales[0].contiguous(), True)
+    dout = normal((rows, n), 3).to(dtype)
+    end = torch.finfo(dtype).max
+
+    def check(got, dz, edz, e32, *operands):
+        # as_operand's bound is for what is within the type's ends: past them the end itself is meant
+        xv, wv = (q if bool((wide(q).abs() <= end).all()) else wide(q).clamp(-end, end) for q in operands)
+        (dx, edx), (dw, edw), _ = gradients64(dz, edz, xv, wv, None, dtype, e32)
+        assert_within(got.dw, dw, edw + U * dw.abs(), "dw")
+        inside = dx.abs() + edx < end                  # fp16 results past the end are infinite
+        assert_within(torch.where(inside, got.dx.double(), 0.0), torch.where(inside, dx, 0.0),
+                      store_error(dx, dtype) + edx * (1 + 2 ** -7), "dx")
+
+    zero = torch.zeros(rows, n, dtype=torch.float64, device="cuda")
+    check(rr.block_linear8_backward(dout, x, first, dw_dtype=torch.float32), dout.double(), zero, zero, x, first)
+    z = normal((rows, 2 * n), 4).to(dtype)
+    dz, e32, edz = gated_dz64(dout, z.double(), "silu", dtype)
+    check(rr.block_gated_backward(dout, x, w, z, dw_dtype=torch.float32), dz, edz, e32, x, w)
+    out = rr.block_linear8(x, first, dtype=torch.bfloat16)
+    want, _, error, _ = linear64(x, first, None, None, "none", None)
+    assert_within(out, want, store_error(want, torch.bfloat16) + (error + 8 * U) * (1 + 2 ** -7), "out")
 
 
 # ------------------------------------------------------------------- refusals --
