@@ -1024,8 +1024,9 @@ def block_gated_backward(dout, x, w, z, *, act="silu", offsets=None, need_dx=Tru
                          need_db=True, need_out=False, dw_dtype=None, stream=None) -> GatedGrads:
     """Gradients of ``block_gated`` by x, w and bias, of w's shape.  ``z`` is what save_preact
     gave, in either form; x and w are tensors of ``dout``'s dtype or Quantized, each by itself: the
-    gradients are those at what they stand for, in that dtype as ``block_linear8_backward`` says.  ``need_out`` makes the forward pass's out
-    again, which the next product's backward pass reads, so that nobody has to keep it."""
+    gradients are those at what they stand for, in that dtype as ``block_linear8_backward`` says.
+    ``need_out`` makes the forward pass's out again, which the next product's backward pass reads, so
+    that nobody has to keep it."""
     if not isinstance(dout, torch.Tensor):
         raise ValueError("dout must be a matrix")
     dtype = dout.dtype

@@ -81,6 +81,39 @@ def test_dispatch_of_one_row_of_a_buffer_of_odd_rows(rr):
         assert torch.equal(got.scales[there], x.scales[[r, r]])
 
 
+@pytest.mark.parametrize("ranks,tokens,k", [(2, 30, 258), (4, 200, 1024), (8, 60, 264)])
+def test_rows_through_the_alltoall(rr, ranks, tokens, k):
+    """Values as pairs and scales go to the ranks of their experts, of which each makes the products that
+    one rank with all rows would, and the results come back to their tokens."""
+    n, capacity = 96, (2 * tokens // ranks + 8) // 8 * 8
+    ids = [torch.rand(tokens, ranks, generator=torch.Generator().manual_seed(r)).topk(2).indices.cuda()
+           for r in range(ranks)]
+    orders = [rr.expert_sort(i, ranks, capacity) for i in ids]
+    sent = [rr.expert_dispatch(rr.block_quantize(normal((tokens, k), 20 + r)), o.slots, o.sources)
+            for r, o in enumerate(orders)]
+    w = rr.block_quantize(normal((ranks, 2, n, k), 40, k ** -0.5), square=True)
+    values = rr.alltoall([s.values.view(torch.bfloat16) for s in sent])
+    scales = rr.alltoall([s.scales for s in sent])
+    made = []
+    for e in range(ranks):
+        rows = rr.Quantized(values[e].view(E4M3), scales[e])
+        block = slice(e * capacity, (e + 1) * capacity)
+        want = rr.Quantized(torch.cat([s.values.view(torch.uint8)[block] for s in sent]).view(E4M3),
+                            torch.cat([s.scales[block] for s in sent]))
+        assert torch.equal(rows.values.view(torch.uint8), want.values.view(torch.uint8))
+        assert torch.equal(rows.scales, want.scales)
+        one = rr.Quantized(w.values[e], w.scales[e], True)
+        made.append(rr.block_gated(rows, one))
+        assert torch.equal(made[-1], rr.block_gated(want, one))
+    for r, back in enumerate(rr.alltoall(made)):
+        rr.check_kernel_error()
+        out = rr.expert_combine(back, orders[r].slots)
+        slots = orders[r].slots.long()
+        terms = torch.where((slots >= 0)[..., None], back.double()[slots.clamp(min=0)], 0.0)
+        want, error = terms.sum(1), 2 * U * terms.abs().sum(1)
+        assert_within(out, want, store_error(want, torch.bfloat16) + error * (1 + 2 ** -7), "out")
+
+
 # ------------------------------------------------------------------ few rows --
 
 @pytest.mark.parametrize("rows", [17, 32])
