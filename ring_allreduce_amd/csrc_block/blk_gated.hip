@@ -189,24 +189,6 @@ template <typename T, bool EIGHT> static void launch_gate(const GateArgs& k, con
     }
 }
 
-// 16 columns a workgroup, 16 threads each.
-__global__ void __launch_bounds__(256) gate_parts_kernel(const float* part, int splits, int n, float* db) {
-    __shared__ float lds[16][17];
-    const int c = threadIdx.x & 15, s = threadIdx.x >> 4, col = (int)blockIdx.x * 16 + c;
-    const float* from = part + (uint64_t)blockIdx.y * splits * n;
-    float sum = 0.0f;
-    if (col < n)
-#pragma unroll 4
-        for (int p = s; p < splits; p += 16) sum += from[(uint64_t)p * n + col];
-    lds[s][c] = sum;
-    __syncthreads();
-    if (s == 0 && col < n) {
-        float all = 0.0f;
-        for (int q = 0; q < 16; ++q) all += lds[q][c];
-        db[(uint64_t)blockIdx.y * n + col] = all;
-    }
-}
-
 // ------------------------------------------------------------------ host side --
 
 // The same block with the columns of both halves for `n`, as its products see it.
@@ -558,21 +540,6 @@ struct Wanted {
     int32_t dw_dt;
 };
 
-// Threads of a workgroup across the columns of the gate's gradient, and parts of a group's rows:
-// enough workgroups to fill the device, and four rows a thread.
-static uint64_t gate_threads(const rr_linear_t& l) {
-    uint64_t t = 1;
-    while (t < 256 && t * 8 < l.n) t *= 2;
-    return t;
-}
-static uint64_t gate_splits(const rr_linear_t& l) {
-    const uint64_t t = gate_threads(l), cols = ceil_div(l.n, t * 8) * l.groups;
-    const uint64_t each = ceil_div(l.rows, l.groups);
-    const uint64_t want = ceil_div(2048, cols), most = ceil_div(each, 256 / t * 4);
-    const uint64_t n = want < most ? want : most;
-    return n < 1 ? 1 : n > 1024 ? 1024 : n;
-}
-
 struct GradPlan {
     uint64_t dz, part, product;
     uint64_t bytes() const { return dz + part + product; }
@@ -586,7 +553,7 @@ static GradPlan grad_plan(const rr_linear8_t* a, const Wanted& g) {
     const rr_linear_t both = both_halves(a);
     const Operand dz = dz_of(both, nullptr);
     if (g.dx.data || g.dw) p.dz = dz.copy_bytes();
-    const uint64_t splits = gate_splits(a->l);
+    const uint64_t splits = sum_splits(&a->l);
     if (g.db && splits > 1) p.part = ceil_div((uint64_t)a->l.groups * splits * both.n * sizeof(float), 256) * 256;
     if (g.dx.data) p.product = product_bytes(&both, kByX, dz, w_of(a, 2));
     if (g.dw) {
@@ -654,8 +621,8 @@ static rr_status_t gated_backward(const rr_linear8_t* a, const rr_gated_grad_t* 
         k.out_ld = g->out.ld;
         k.n = (int32_t)l.n;
         k.act = l.act;
-        k.splits = (int32_t)gate_splits(l);
-        k.threads = (int32_t)gate_threads(l);
+        k.splits = (int32_t)sum_splits(&l);
+        k.threads = (int32_t)sum_threads(&l);
         if (g->db) k.part = plan.part ? (float*)((char*)workspace + plan.dz) : g->db;
         // of the rows of no group, out is cleared
         const unsigned ranges = (unsigned)l.groups + (l.offsets && g->out.data ? 2 : 0);
@@ -664,11 +631,7 @@ static rr_status_t gated_backward(const rr_linear8_t* a, const rr_gated_grad_t* 
         if (a->z_scales) b16 ? launch_gate<bf16, true>(k, grid, s) : launch_gate<f16, true>(k, grid, s);
         else b16 ? launch_gate<bf16, false>(k, grid, s) : launch_gate<f16, false>(k, grid, s);
         if ((st = launched()) != RR_OK) return st;
-        if (plan.part) {
-            const dim3 sums((unsigned)ceil_div(both.n, 16), (unsigned)l.groups);
-            gate_parts_kernel<<<sums, 256, 0, s>>>(k.part, k.splits, (int)both.n, g->db);
-            if ((st = launched()) != RR_OK) return st;
-        }
+        if (plan.part && (st = launch_sums(k.part, k.splits, both.n, l.groups, g->db, s)) != RR_OK) return st;
     }
     if (g->dx.data && l.rows) {
         Product r = {kByX, dz, w_of(a, 2), groups_of(&both)};

@@ -90,9 +90,9 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a) {
         if (col + e < a.n) to[col + e] = sum[e];
 }
 
-// 16 columns a workgroup, 16 threads each.
+// Adds the parts of column sums: 16 columns a workgroup, 16 threads each.
 __global__ void __launch_bounds__(256)
-slope_parts_kernel(const float* part, int splits, int n, float* db) {
+sum_parts_kernel(const float* part, int splits, int n, float* db) {
     __shared__ float lds[16][17];
     const int c = threadIdx.x & 15, s = threadIdx.x >> 4, col = (int)blockIdx.x * 16 + c;
     const float* from = part + (uint64_t)blockIdx.y * splits * n;
@@ -107,6 +107,11 @@ slope_parts_kernel(const float* part, int splits, int n, float* db) {
         for (int q = 0; q < 16; ++q) all += lds[q][c];
         db[(uint64_t)blockIdx.y * n + col] = all;
     }
+}
+
+rr_status_t launch_sums(const float* part, int splits, uint64_t n, int groups, float* db, hipStream_t s) {
+    sum_parts_kernel<<<dim3((unsigned)ceil_div(n, 16), (unsigned)groups), 256, 0, s>>>(part, splits, (int)n, db);
+    return launched();
 }
 
 // ------------------------------------------------------------------- alignment --
@@ -417,15 +422,13 @@ Operand weights_of(const rr_linear_t* a) {
     return {{const_cast<void*>(a->w), a->w_ld}, a->n, a->k, (uint64_t)a->groups, a->w_stride};
 }
 
-// Threads of a workgroup across the columns in the gradient of the activation.
-static uint64_t slope_threads(const rr_linear_t* a) {
+uint64_t sum_threads(const rr_linear_t* a) {
     uint64_t t = 1;
     while (t < 256 && t * 8 < a->n) t *= 2;
     return t;
 }
-// Parts of a group's rows there: enough workgroups to fill the device, and four rows a thread.
-static uint64_t splits_of(const rr_linear_t* a) {
-    const uint64_t t = slope_threads(a), cols = ceil_div(a->n, t * 8) * a->groups;
+uint64_t sum_splits(const rr_linear_t* a) {
+    const uint64_t t = sum_threads(a), cols = ceil_div(a->n, t * 8) * a->groups;
     const uint64_t each = ceil_div(a->rows, a->groups);
     const uint64_t want = ceil_div(2048, cols), most = ceil_div(each, 256 / t * 4);
     const uint64_t n = want < most ? want : most;
@@ -452,7 +455,7 @@ static BackwardPlan plan_of(const rr_linear_t* a, const rr_linear_grad_t* g, con
     BackwardPlan p = {0, 0, 0};
     const Operand dout = rows_of(a, g->dout, a->n);
     if ((g->dx.data || g->dw) && (a->act != RR_ACT_NONE || !dout.good())) p.dz = dout.copy_bytes();
-    if (g->db && splits_of(a) > 1) p.part = ceil_div((uint64_t)a->groups * splits_of(a) * a->n * sizeof(float), 256) * 256;
+    if (g->db && sum_splits(a) > 1) p.part = ceil_div((uint64_t)a->groups * sum_splits(a) * a->n * sizeof(float), 256) * 256;
     Operand dz = dout;
     if (p.dz) dz.rows = {nullptr, ceil_div(a->n, 8) * 8};
     dz.width = ceil_div(a->n, 8) * 8;       // good rows, or a copy with zeros behind each
@@ -509,8 +512,8 @@ static rr_status_t backward(const rr_linear_t* a, const rr_linear_grad_t* g, con
         k.z_ld = a->z.ld;
         k.n = (int32_t)a->n;
         k.act = a->act;
-        k.splits = (int32_t)splits_of(a);
-        k.threads = (int32_t)slope_threads(a);
+        k.splits = (int32_t)sum_splits(a);
+        k.threads = (int32_t)sum_threads(a);
         if (plan.dz) {
             dz = {workspace, ceil_div(a->n, 8) * 8};
             k.dz = dz.data;
@@ -525,11 +528,7 @@ static rr_status_t backward(const rr_linear_t* a, const rr_linear_grad_t* g, con
         else
             slope_kernel<f16><<<grid, 256, 0, s>>>(k);
         if ((st = launched()) != RR_OK) return st;
-        if (plan.part) {
-            const dim3 sums((unsigned)ceil_div(a->n, 16), (unsigned)a->groups);
-            slope_parts_kernel<<<sums, 256, 0, s>>>(k.part, k.splits, k.n, g->db);
-            if ((st = launched()) != RR_OK) return st;
-        }
+        if (plan.part && (st = launch_sums(k.part, k.splits, a->n, a->groups, g->db, s)) != RR_OK) return st;
     }
     Operand by = rows_of(a, dz, ceil_div(a->n, 8) * 8);     // zeros behind the columns, if any
     if (g->dx.data && a->rows) {

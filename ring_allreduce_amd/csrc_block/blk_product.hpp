@@ -59,6 +59,13 @@ rr_status_t run_product(const rr_linear_t* a, Product r, void* workspace, hipStr
 Operand rows_of(const rr_linear_t* a, const rr_rows_t& r, uint64_t width);
 Operand weights_of(const rr_linear_t* a);
 
+// Column sums of the rows of each group, in the gradients of the activation and of the gate:
+// threads of a workgroup across the columns (8 each); parts of a group's rows, enough workgroups to
+// fill the device and four rows a thread; and the sum of the parts, [groups][splits][n].
+uint64_t sum_threads(const rr_linear_t* a);
+uint64_t sum_splits(const rr_linear_t* a);
+rr_status_t launch_sums(const float* part, int splits, uint64_t n, int groups, float* db, hipStream_t s);
+
 // Bytes that the weights reach over.
 inline uint64_t weights_extent(const rr_linear_t* a, uint64_t bytes) {
     return extent(a->groups, a->w_stride, extent(a->n, a->w_ld, a->k, 1), bytes);
