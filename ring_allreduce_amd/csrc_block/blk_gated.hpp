@@ -51,8 +51,7 @@ template <typename T, int TI, int TJ> __global__ void __launch_bounds__(256) joi
                 if (j < a.j) store_eight(a.z8 + (uint64_t)i * a.z8_ld + (uint64_t)h * a.j + j, a.j - j, narrow(r, inverse_of(scale)));
             }
             act_values(a.act, v[0]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[0][e] *= v[1][e];
+            times(v[0], v[1]);
             if (j < a.j) store_some<T, 8>((T*)a.out + (uint64_t)i * a.out_ld + j, a.j - j, v[0]);
             continue;
         }

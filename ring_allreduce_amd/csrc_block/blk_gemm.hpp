@@ -448,6 +448,16 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int group, int i, int 
                  (T*)a.z + (uint64_t)i * a.z_ld + j, (char*)a.out + at * (a.wide_out ? 4 : sizeof(T)));
 }
 
+// g u, rounded to 32 bits: where a rounding to fp16 follows in the same block of code, the compiler
+// makes both one instruction with one rounding, and out would depend on whether z is kept in 8 bits.
+template <int N> __device__ __forceinline__ void times(float (&g)[N], const float (&u)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        g[e] *= u[e];
+        asm("" : "+v"(g[e]));
+    }
+}
+
 // Both halves' sums of N neighbouring columns: z = sums + bias, out = act(z gate) times z of the
 // other; zeros for a row of no group.  z and out: of the first of the columns.
 template <typename T, int N>
@@ -463,8 +473,7 @@ __device__ __forceinline__ void finish_gated(const GemmArgs& a, int group, int n
         store_some<T, N>(z + a.j, n, u);
     }
     act_values(a.act, g);
-#pragma unroll
-    for (int e = 0; e < N; ++e) g[e] *= u[e];
+    times(g, u);
     store_some<T, N>(out, n, g);
 }
 template <typename T, int N>

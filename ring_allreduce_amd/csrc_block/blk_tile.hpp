@@ -148,8 +148,7 @@ __device__ __forceinline__ void write_eight(const GemmArgs& a, const Spot& s, BL
             if (n > 0) store_eight(a.z8 + (uint64_t)i * a.z8_ld + (uint64_t)h * a.j + j, n, narrow(r, inverse_of(scale)));
         }
         act_values(a.act, v[0]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[0][e] *= v[1][e];
+        times(v[0], v[1]);
         if (n > 0) store_some<T, 8>((T*)a.out + (uint64_t)i * a.out_ld + j, n, v[0]);
     }
 }

@@ -180,6 +180,23 @@ def test_sums_of_blocks_are_kept_in_32_bits(rr, rows, n, foreign):
     assert bool(((out - exact).abs() <= bound + 2.0 ** -8 * (exact + bound)).all())
 
 
+@pytest.mark.parametrize("eight", [False, True], ids=["16", "8"])
+@pytest.mark.parametrize("rows,n,k,groups", [(703, 9000, 3, 2), (2560, 2304, 40, 1), (4500, 2200, 2064, 1), (300, 300, 40, 3)])
+def test_the_product_does_not_depend_on_how_z_is_kept(rr, rows, n, k, groups, eight):
+    """In fp16, where the compiler may round a product and its 16-bit value in one step."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, k, generator=g, device="cuda").half()
+    w = (torch.randn(groups, 2, n, k, generator=g, device="cuda") * k ** -0.5).half()
+    offsets = torch.tensor([rows * (i + 1) // (groups + 2) for i in range(groups + 1)], dtype=torch.int32).cuda()
+    if eight:
+        x, w = rr.block_quantize(x), rr.block_quantize(w, square=True)
+    for act in ("none", "sigmoid", "gelu"):
+        args = dict(act=act, offsets=offsets, dtype=torch.float16)
+        want = rr.block_gated(x, w, **args)
+        for kept in (True, "e4m3"):
+            assert torch.equal(rr.block_gated(x, w, save_preact=kept, **args)[0], want), (act, kept)
+
+
 # ------------------------------------------- gradients at the ends of 16-bit types --
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
