@@ -1,6 +1,7 @@
 // blk_gated.hip -- the entry points of a block's gated projections and of the products of 8-bit
 // operands (block_gated, block_linear8 and their gradients): the checks, the operands, and the
-// gradient of the gate.  The products themselves: blk_gemm.hpp, blk_gemm8.hpp.
+// gradient of the gate.  The products themselves: blk_tile.hpp, for few rows blk_gemm.hpp and
+// blk_gemm8.hpp, and blk_gemm.hpp for the gradients.
 #include "blk_product.hpp"
 
 namespace blk {

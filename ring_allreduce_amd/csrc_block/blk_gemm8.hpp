@@ -18,7 +18,11 @@ namespace blk {
 // scales, any fp32 ones, come on top on the vector units.  Bound by the read of the weights
 // and, of few columns, by its start: 16 x 4096 x 4096 8.4 us (2.0 TB/s), 3 x 8192 x 8192 17.2
 // (3.9 TB/s), 32 x 4096 x 4096 11.1; 256 uneven rows over 32 groups of 2 x 2048 x 4096, gated, 124
-// (4.3 TB/s).
+// (4.3 TB/s).  Of up to 16 rows two workgroups a compute unit, which leaves a lane 128 registers:
+// rows at any byte with 32 columns (or 16 of each projection) keep 9 to 11 more in scratch memory.
+// With one workgroup and nothing there groups take longer and single products less (256 uneven rows
+// over 32 groups of 2 x 2048 x 4095 338 us instead of 325, plain 168 and 166; 16 x 2 x 4096 x 4095 25
+// instead of 27).
 constexpr int kStreamDepth8 = 256;
 
 template <typename T, int FI, int FJ, bool DIRECT, bool GATED>

@@ -2,7 +2,8 @@
 // (block_quantize, block_dequantize).
 //
 // Bound by memory: e bytes in and 1 + 4 / 128 out a value, or the other way round.  16384 x 8192 in
-// bf16, 407 MB: rows 80 us, 128 x 128 blocks 81 (5 TB/s; a copy of as many bytes takes 76).
+// bf16, 407 MB: rows 77 us, 128 x 128 blocks 78, and back 80 (5.1 .. 5.3 TB/s; a copy of as many
+// bytes takes 76).
 #include "blk_product.hpp"
 
 namespace blk {
@@ -114,7 +115,7 @@ template <> __device__ __forceinline__ f16 rounded<f16>(float v) {
 }
 
 // Eight columns a thread.  STREAM: what is written is not to stay in the caches, of which it would
-// leave nothing else: 134 million values to bf16 take 81 us so and 100 otherwise.
+// leave nothing else: 134 million values to bf16 take 80 us so and 100 otherwise.
 template <typename T, bool STREAM> __global__ void __launch_bounds__(256) back_kernel(const BlockArgs a) {
     const uint32_t each = ((uint32_t)a.filled + 7) / 8;
     const uint64_t all = a.groups * a.rows * each, per = a.rows / a.part;

@@ -242,8 +242,8 @@ __device__ __forceinline__ void write_direct(const GemmArgs& a, const Spot& s, B
 
 // Reads what the epilogue will want of the residual into the L2, by way of 1 KiB of LDS that nobody
 // looks at: one piece of each 128 bytes of the tile's rows, three steps before the end (8192 x
-// 8192 x 4096 with bias, SiLU and a residual that is in no cache 271 us, without this 280; 6 to 30
-// steps before the end are no better).  (A piece that begins before the
+// 8192 x 4096 with bias, SiLU and a residual that is in no cache 263 us, without this 269, at scales
+// that are no powers of two 286 and 297; 6 to 30 steps before the end are no better).  (A piece that begins before the
 // first element or ends behind the last one is one of theirs: 16 bytes at a boundary of 16.)
 template <typename T, int TI, int TJ, int THREADS>
 __device__ __forceinline__ void touch_residual(const GemmArgs& a, const Spot& s, uint32_t room) {
@@ -307,14 +307,14 @@ __device__ __forceinline__ void keep_order() {
 // EIGHT: operands in 8 bits, with scales; else in T.
 //
 // Scales: where all of four blocks of a wave's rows and columns are powers of two, as
-// block_quantize makes them, the instruction itself takes their exponents (8192 x 8192 x 8192 395
-// us, 2780 TFLOP/s); others are multiplied in 32 bits and come on top of each block's sum by a
-// multiply-add a result on the vector units, beside the matrix cores (445
-// us).  Both once the clocks have settled; the first calls after a pause take up to 80 more.
+// block_quantize makes them, the instruction itself takes their exponents (8192 x 8192 x 8192 403
+// us, 2730 TFLOP/s); others are multiplied in 32 bits and come on top of each block's sum by a
+// multiply-add a result on the vector units, beside the matrix cores (459 us).  Both once the
+// clocks have settled, after some 100 calls; the first ones after a pause take up to 100 more.
 //
 // Bound, at 256 x 256: 8-bit products by the way from the L2s into LDS and by the epilogue, which no
 // product overlaps (one workgroup a compute unit, nearly all of its LDS): 8192 x 8192 x 4096 takes
-// 215 us, with bias, SiLU and a residual from memory 271.  16-bit ones by power, as gemm_kernel;
+// 224 us, with bias, SiLU and a residual from memory 263.  16-bit ones by power, as gemm_kernel;
 // beside it these tiles keep Q's fragments in registers, so that a step reads 128 KiB of LDS
 // instead of 192, and have no copy of Q's next tile (16384 rows over 8 uneven groups of 2 x
 // 4096 x 2048 with z 548 us, gemm_kernel's tiles 591).
@@ -450,8 +450,8 @@ __global__ void __launch_bounds__(64 * WI * WJ, 2) tile_kernel(const GemmArgs a)
 #pragma unroll
             for (int y = 0; y < FJ; ++y) clean(fq[y]);
         // Sums that are to be multiplied wait for HELD more products: what follows a product at once
-        // would wait for it (1024 x 4096 x 4096 42 us instead of 45, 8192 x 8192 x 8192 450 instead of
-        // 462; with two or four of them less).
+        // would wait for it (8192 x 8192 x 8192 459 us instead of 473, 1024 x 4096 x 4096, where eight
+        // waves hide it too, 26 either way; with two or four of them less).
         constexpr int LATER = FI * FJ > HELD ? HELD : 1;
         f32x4 held[LATER];
         const auto add_held = [&](int n) {          // of the tile's n-th product
